@@ -9,7 +9,9 @@ The functions carry the C names:
   dflash_attn_dense, dflash_attn_anchored, dflash_attn_ragged,
   dflash_attn_dense_backward, dflash_attn_anchored_backward,
   dflash_attn_workspace_size, dflash_build_schedule_host, dflash_scan_mask,
-  dflash_last_device_error, dflash_status_string.
+  dflash_last_device_error, dflash_status_string,
+  dflash_qk_norm_rope, dflash_qk_norm_rope_backward, dflash_cache_append,
+  dflash_attn_paged, dflash_verify.
 """
 from __future__ import annotations
 
@@ -38,7 +40,9 @@ EXPORTS = ("dflash_attn_dense", "dflash_attn_anchored", "dflash_attn_ragged", "d
            "dflash_kernel_launches", "dflash_attn_dense_noalloc", "dflash_build_mask",
            "dflash_attn_anchored_backward", "dflash_attn_dense_backward", "dflash_test_inject_stall",
            "dflash_test_limit_tile_flags",
-           "dflash_attn_latent_ragged", "dflash_attn_latent_workspace_size")
+           "dflash_attn_latent_ragged", "dflash_attn_latent_workspace_size",
+           "dflash_qk_norm_rope", "dflash_qk_norm_rope_workspace_size", "dflash_qk_norm_rope_backward",
+           "dflash_cache_append", "dflash_attn_paged", "dflash_attn_paged_workspace_size", "dflash_verify")
 
 
 class DFlashError(RuntimeError):
@@ -51,6 +55,24 @@ class _Dims(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("S", ctypes.c_int), ("Q", ctypes.c_int),
                 ("d_nope", ctypes.c_int), ("d_rope", ctypes.c_int), ("d_v", ctypes.c_int),
                 ("scale", ctypes.c_float)]
+
+
+class _RopeDims(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int), ("H_q", ctypes.c_int), ("H_kv", ctypes.c_int), ("D", ctypes.c_int),
+                ("rot_dim", ctypes.c_int), ("max_pos", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("eps", ctypes.c_float), ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64)]
+
+
+class _PagedDims(ctypes.Structure):
+    _fields_ = [("R", ctypes.c_int), ("H_q", ctypes.c_int), ("H_kv", ctypes.c_int), ("D", ctypes.c_int),
+                ("total_q", ctypes.c_int), ("max_q_len", ctypes.c_int), ("num_pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("max_pages", ctypes.c_int), ("k_page_stride", ctypes.c_int64),
+                ("v_page_stride", ctypes.c_int64)]
+
+
+class _VerifyDims(ctypes.Structure):
+    _fields_ = [("R", ctypes.c_int), ("V", ctypes.c_int), ("total_draft", ctypes.c_int),
+                ("max_draft", ctypes.c_int), ("target_stride", ctypes.c_int64), ("draft_stride", ctypes.c_int64)]
 
 
 _lock = threading.Lock()
@@ -99,6 +121,20 @@ def load_library(path: str | None = None):
         lib.dflash_test_limit_tile_flags.restype = None
         lib.dflash_kernel_launches.argtypes = []
         lib.dflash_kernel_launches.restype = ctypes.c_uint64
+        RD, PD, VD, L = (ctypes.POINTER(_RopeDims), ctypes.POINTER(_PagedDims), ctypes.POINTER(_VerifyDims),
+                         ctypes.c_int64)
+        lib.dflash_qk_norm_rope.argtypes = [RD, I, P, P, P, P, P, P, P, P, P]
+        lib.dflash_qk_norm_rope_backward.argtypes = [RD, I, P, P, P, P, P, P, P, P, P, P, P, P, P, S, P]
+        lib.dflash_cache_append.argtypes = [PD, RD, I, P, P, P, L, P, P, P, P, P, P, P, P, P, P]
+        lib.dflash_attn_paged.argtypes = [PD, I, P, P, P, P, P, P, I, F, P, P, P, S, P]
+        lib.dflash_verify.argtypes = [VD, P, P, P, P, P, P, P, P, P]
+        for name in ("dflash_qk_norm_rope", "dflash_qk_norm_rope_backward", "dflash_cache_append",
+                     "dflash_attn_paged", "dflash_verify"):
+            getattr(lib, name).restype = ctypes.c_int
+        lib.dflash_qk_norm_rope_workspace_size.argtypes = [RD]
+        lib.dflash_qk_norm_rope_workspace_size.restype = S
+        lib.dflash_attn_paged_workspace_size.argtypes = [PD, I]
+        lib.dflash_attn_paged_workspace_size.restype = S
         for name in ("dflash_attn_dense", "dflash_attn_anchored", "dflash_attn_ragged",
                      "dflash_build_schedule_host", "dflash_scan_mask", "dflash_last_device_error"):
             getattr(lib, name).restype = ctypes.c_int
@@ -385,6 +421,283 @@ def dflash_attn_dense_backward(q, k_nope, k_rope, v, mask, out, lse, dout, grads
         _stream(stream))
     _check("dflash_attn_dense_backward", st)
     return dq, dkn, dkr, dvv
+
+
+# ---------------------------------------------------------------------------
+# the grouped-query draft's serving step
+# ---------------------------------------------------------------------------
+class _On:
+    """Launches on a tensor's device, whichever is current: the stream handle to
+    launch on, with the current device switched where it is another one."""
+
+    __slots__ = ("guard", "stream")
+
+    def __init__(self, device, stream):
+        torch = _torch()
+        cuda = torch.cuda
+        self.guard = cuda.device(device) if cuda.current_device() != device.index else None
+        if stream is None:
+            stream = cuda.current_stream(device)
+        self.stream = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self.stream
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _arg(t, name, device, dtype, shape=None):
+    """Data pointer of a contiguous CUDA tensor on `device`, checked; None for None."""
+    if t is None:
+        return None
+    if t.device != device or device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return t.data_ptr()
+
+
+def _token_arg(t, name, device, dtype, shape):
+    """Data pointer and token stride of [tokens, heads, D] whose tokens are each contiguous."""
+    if t.device != device or device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    T, H, D = shape
+    s = t.stride()
+    if (D > 1 and s[2] != 1) or (H > 1 and s[1] != D) or (T > 1 and s[0] < H * D):
+        raise ValueError(f"the heads of a token of {name} must be contiguous")
+    return t.data_ptr(), s[0] if T > 1 else 0
+
+
+def _cache_arg(t, name, device, dtype, shape):
+    """Data pointer and page stride of [pages, page_size, H_kv, D] whose pages are each contiguous."""
+    if t.device != device or device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    n, P, H, D = shape
+    s = t.stride()
+    if (D > 1 and s[3] != 1) or (H > 1 and s[2] != D) or (P > 1 and s[1] != H * D) or (n > 1 and s[0] < P * H * D):
+        raise ValueError(f"the pages of {name} must be contiguous")
+    return t.data_ptr(), s[0] if n > 1 else 0
+
+
+def _rope_args(q, k, positions, cos_sin):
+    torch = _torch()
+    one = q if q is not None else k
+    if one is None:
+        raise ValueError("q or k must be given")
+    if one.dim() != 3:
+        raise ValueError("q and k must be [tokens, heads, D]")
+    T, _, D = one.shape
+    dev = one.device
+    Hq, Hk = (0 if t is None else t.shape[1] for t in (q, k))
+    rot, max_pos = (0, 0) if cos_sin is None else (cos_sin.shape[1], cos_sin.shape[0])
+    cs = _arg(cos_sin, "cos_sin", dev, torch.float32)
+    ps = None if cos_sin is None else _arg(positions, "positions", dev, torch.int32, (T,))
+    return one.dtype, dev, T, Hq, Hk, D, rot, max_pos, cs, ps
+
+
+def dflash_qk_norm_rope(q, k, positions, cos_sin, q_norm=None, k_norm=None, eps=1e-6, interleaved=False, q_out=None,
+                        k_out=None, stream=None):
+    """Norm (where a weight [D] is given) and rotation of q [T,H_q,D] and k
+    [T,H_kv,D] at positions [T] int32.  Either of q and k may be None; their
+    tokens may be strided.  cos_sin [max_pos, rot_dim] fp32 (rot_dim/2 cosines,
+    then sines; None: no rotation).  Returns (q_out, k_out), contiguous."""
+    torch = _torch()
+    lib = load_library()
+    dt, dev, T, Hq, Hk, D, rot, max_pos, cs, ps = _rope_args(q, k, positions, cos_sin)
+    code = _dtype_code(q if q is not None else k)
+    qp, qs = (None, 0) if q is None else _token_arg(q, "q", dev, dt, (T, Hq, D))
+    kp, ks = (None, 0) if k is None else _token_arg(k, "k", dev, dt, (T, Hk, D))
+    if q_out is None and q is not None:
+        q_out = torch.empty((T, Hq, D), dtype=dt, device=dev)
+    if k_out is None and k is not None:
+        k_out = torch.empty((T, Hk, D), dtype=dt, device=dev)
+    d = _RopeDims(T, Hq, Hk, D, rot, max_pos, int(interleaved), eps, qs, ks)
+    with _On(dev, stream) as st:
+        rc = lib.dflash_qk_norm_rope(d, code, qp, kp, _arg(q_norm, "q_norm", dev, dt, (D,)),
+                                     _arg(k_norm, "k_norm", dev, dt, (D,)), cs, ps,
+                                     _arg(q_out, "q_out", dev, dt, (T, Hq, D)),
+                                     _arg(k_out, "k_out", dev, dt, (T, Hk, D)), st)
+    _check("dflash_qk_norm_rope", rc)
+    return q_out, k_out
+
+
+def dflash_qk_norm_rope_backward(q, k, positions, cos_sin, dq_out, dk_out, q_norm=None, k_norm=None, eps=1e-6,
+                                 interleaved=False, grads=None, workspace=None, stream=None):
+    """Gradients (dq, dk, dq_norm, dk_norm) of sum(dq_out * q_out) + sum(dk_out *
+    k_out); the norm gradients are fp32 [D], None without a weight.  grads:
+    optional preallocated (dq, dk, dq_norm, dk_norm)."""
+    torch = _torch()
+    lib = load_library()
+    dt, dev, T, Hq, Hk, D, rot, max_pos, cs, ps = _rope_args(q, k, positions, cos_sin)
+    code = _dtype_code(q if q is not None else k)
+    qp, qs = (None, 0) if q is None else _token_arg(q, "q", dev, dt, (T, Hq, D))
+    kp, ks = (None, 0) if k is None else _token_arg(k, "k", dev, dt, (T, Hk, D))
+    if grads is None:
+        grads = (None if q is None else torch.empty((T, Hq, D), dtype=dt, device=dev),
+                 None if k is None else torch.empty((T, Hk, D), dtype=dt, device=dev),
+                 None if q_norm is None else torch.empty(D, dtype=torch.float32, device=dev),
+                 None if k_norm is None else torch.empty(D, dtype=torch.float32, device=dev))
+    dq, dk, dwq, dwk = grads
+    d = _RopeDims(T, Hq, Hk, D, rot, max_pos, int(interleaved), eps, qs, ks)
+    nbytes = int(lib.dflash_qk_norm_rope_workspace_size(d))
+    ws = _workspace(nbytes, workspace, dev)
+    with _On(dev, stream) as st:
+        rc = lib.dflash_qk_norm_rope_backward(
+            d, code, qp, kp, _arg(q_norm, "q_norm", dev, dt, (D,)), _arg(k_norm, "k_norm", dev, dt, (D,)), cs, ps,
+            _arg(dq_out if q is not None else None, "dq_out", dev, dt, (T, Hq, D)),
+            _arg(dk_out if k is not None else None, "dk_out", dev, dt, (T, Hk, D)),
+            _arg(dq, "dq", dev, dt, (T, Hq, D)), _arg(dk, "dk", dev, dt, (T, Hk, D)),
+            _arg(dwq, "dq_norm", dev, torch.float32, (D,)), _arg(dwk, "dk_norm", dev, torch.float32, (D,)),
+            _arg(ws, "workspace", dev, ws.dtype), nbytes, st)
+    _check("dflash_qk_norm_rope_backward", rc)
+    return dq, dk, dwq, dwk
+
+
+def _paged_args(k_cache, v_cache, page_table, kv_lens, q_offsets, dt, dev):
+    torch = _torch()
+    shape = k_cache.shape
+    if len(shape) != 4:
+        raise ValueError("k_cache and v_cache must be [num_pages, page_size, H_kv, D]")
+    kp, ks = _cache_arg(k_cache, "k_cache", dev, dt, shape)
+    vp, vs = _cache_arg(v_cache, "v_cache", dev, dt, shape)
+    if page_table.dim() != 2 or q_offsets.dim() != 1:
+        raise ValueError("page_table must be [R, max_pages] and q_offsets [R + 1]")
+    R, max_pages = page_table.shape
+    tp = _arg(page_table, "page_table", dev, torch.int32)
+    lp = _arg(kv_lens, "kv_lens", dev, torch.int32, (R,))
+    op = _arg(q_offsets, "q_offsets", dev, torch.int32, (R + 1,))
+    return shape, R, max_pages, kp, ks, vp, vs, tp, lp, op
+
+
+def dflash_cache_append(k, v, k_cache, v_cache, page_table, kv_lens, q_offsets, q=None, cos_sin=None, q_norm=None,
+                        k_norm=None, eps=1e-6, interleaved=False, q_out=None, stream=None):
+    """Writes the new tokens' k (normed and rotated) and v [total_q,H_kv,D] into the
+    pages of k_cache and v_cache [num_pages,page_size,H_kv,D]: request r's tokens
+    [q_offsets[r], q_offsets[r+1]) are the last of its kv_lens[r] positions, and
+    position p lies in page page_table[r, p // page_size].  With q [total_q,H_q,D]
+    its heads are normed and rotated too; returns q_out (None without q)."""
+    torch = _torch()
+    lib = load_library()
+    dt, dev = k.dtype, k.device
+    code = _dtype_code(k)
+    (n, P, Hk, D), R, max_pages, kcp, kcs, vcp, vcs, tp, lp, op = _paged_args(k_cache, v_cache, page_table, kv_lens,
+                                                                              q_offsets, dt, dev)
+    T = k.shape[0]
+    kp, ks = _token_arg(k, "k", dev, dt, (T, Hk, D))
+    vp, vs = _token_arg(v, "v", dev, dt, (T, Hk, D))
+    Hq, qp, qs = Hk, None, 0
+    if q is not None:
+        if q.dim() != 3:
+            raise ValueError("q must be [total_q, H_q, D]")
+        Hq = q.shape[1]
+        qp, qs = _token_arg(q, "q", dev, dt, (T, Hq, D))
+        if q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=dt, device=dev)
+    else:
+        q_out = None
+    rot, max_pos = (0, 0) if cos_sin is None else (cos_sin.shape[1], cos_sin.shape[0])
+    pd = _PagedDims(R, Hq, Hk, D, T, 0, n, P, max_pages, kcs, vcs)
+    rd = _RopeDims(T, Hq, Hk, D, rot, max_pos, int(interleaved), eps, qs, ks)
+    with _On(dev, stream) as st:
+        rc = lib.dflash_cache_append(pd, rd, code, qp, kp, vp, vs, _arg(q_norm, "q_norm", dev, dt, (D,)),
+                                     _arg(k_norm, "k_norm", dev, dt, (D,)),
+                                     _arg(cos_sin, "cos_sin", dev, torch.float32), tp, lp, op,
+                                     _arg(q_out, "q_out", dev, dt, (T, Hq, D)), kcp, vcp, st)
+    _check("dflash_cache_append", rc)
+    return q_out
+
+
+def dflash_attn_paged_workspace_size(H_q, H_kv, D, max_q_len, page_size, dtype=DFLASH_BF16) -> int:
+    """Workspace bytes of dflash_attn_paged; they depend on neither the requests nor their lengths."""
+    d = _PagedDims(1, H_q, H_kv, D, 1, int(max_q_len), 1, page_size, 1, 0, 0)
+    return int(load_library().dflash_attn_paged_workspace_size(d, dtype))
+
+
+def dflash_attn_paged(q, k_cache, v_cache, page_table, kv_lens, q_offsets, max_q_len, causal=True, out=None, lse=None,
+                      scale=0.0, workspace=None, stream=None):
+    """Attention of the new tokens q [total_q,H_q,D] over their requests' pages (see
+    dflash_cache_append): all positions below kv_lens[r], or, causal, those up to
+    the token's own.  Returns out [total_q,H_q,D]; fills lse [H_q,total_q] fp32 if given."""
+    torch = _torch()
+    lib = load_library()
+    dt, dev = q.dtype, q.device
+    code = _dtype_code(q)
+    if q.dim() != 3:
+        raise ValueError("q must be [total_q, H_q, D]")
+    T, Hq, _ = q.shape
+    (n, P, Hk, D), R, max_pages, kcp, kcs, vcp, vcs, tp, lp, op = _paged_args(k_cache, v_cache, page_table, kv_lens,
+                                                                              q_offsets, dt, dev)
+    qp = _arg(q, "q", dev, dt, (T, Hq, D))
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=dt, device=dev)
+    d = _PagedDims(R, Hq, Hk, D, T, int(max_q_len), n, P, max_pages, kcs, vcs)
+    nbytes = int(lib.dflash_attn_paged_workspace_size(d, code))
+    ws = _workspace(nbytes, workspace, dev)
+    with _On(dev, stream) as st:
+        rc = lib.dflash_attn_paged(d, code, qp, kcp, vcp, tp, lp, op, int(causal), float(scale or 0.0),
+                                   _arg(out, "out", dev, dt, (T, Hq, D)),
+                                   _arg(lse, "lse", dev, torch.float32, (Hq, T)),
+                                   _arg(ws, "workspace", dev, ws.dtype), nbytes, st)
+    _check("dflash_attn_paged", rc)
+    return out
+
+
+def dflash_verify(target_probs, draft_probs, draft_tokens, draft_offsets, accept_u, sample_u, max_draft,
+                  out_tokens=None, num_accepted=None, stream=None):
+    """Accepts or replaces drafted tokens.  Request r drafted draft_tokens
+    [draft_offsets[r], draft_offsets[r+1]) (int32) from draft_probs
+    [total_draft, V] fp32 (None: it took its most likely token); target_probs fp32
+    has its n + 1 rows from draft_offsets[r] + r on.  accept_u [total_draft] and
+    sample_u [R] are fp32 in [0, 1).  Returns out_tokens [R, max_draft + 1] (the
+    accepted tokens, the drawn one, then -1) and num_accepted [R], int32."""
+    torch = _torch()
+    lib = load_library()
+    dev, f32, i32 = target_probs.device, torch.float32, torch.int32
+    if target_probs.dim() != 2 or target_probs.stride(1) != 1 or draft_offsets.dim() != 1:
+        raise ValueError("target_probs must be [rows, V] with contiguous rows, draft_offsets [R + 1]")
+    rows, V = target_probs.shape
+    T, R = draft_tokens.shape[0], draft_offsets.shape[0] - 1
+    if rows < T + R:
+        raise ValueError("target_probs needs a row for every drafted token and one more for every request")
+    if target_probs.device.type != "cuda" or target_probs.dtype != f32:
+        raise ValueError("target_probs must be a float32 CUDA tensor")
+    ps, qp, qs = target_probs.stride(0) if rows > 1 else 0, None, 0
+    if draft_probs is not None:
+        if draft_probs.shape != (T, V) or draft_probs.dtype != f32 or draft_probs.device != dev or (
+                V > 1 and draft_probs.stride(1) != 1):
+            raise ValueError("draft_probs must be a float32 [total_draft, V] tensor with contiguous rows on the "
+                             "device of target_probs")
+        if T > 0:
+            qp, qs = draft_probs.data_ptr(), draft_probs.stride(0) if T > 1 else 0
+    if out_tokens is None:
+        out_tokens = torch.empty((R, max_draft + 1), dtype=i32, device=dev)
+    if num_accepted is None:
+        num_accepted = torch.empty(R, dtype=i32, device=dev)
+    d = _VerifyDims(R, V, T, int(max_draft), ps, qs)
+    with _On(dev, stream) as st:
+        rc = lib.dflash_verify(d, target_probs.data_ptr(), qp, _arg(draft_tokens, "draft_tokens", dev, i32, (T,)),
+                               _arg(draft_offsets, "draft_offsets", dev, i32),
+                               _arg(accept_u, "accept_u", dev, f32, (T,)), _arg(sample_u, "sample_u", dev, f32, (R,)),
+                               _arg(out_tokens, "out_tokens", dev, i32, (R, max_draft + 1)),
+                               _arg(num_accepted, "num_accepted", dev, i32, (R,)), st)
+    _check("dflash_verify", rc)
+    return out_tokens, num_accepted
 
 
 def dflash_build_schedule_host(B, S, Q, anchors, block_size) -> np.ndarray:

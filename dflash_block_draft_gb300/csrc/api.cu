@@ -47,6 +47,17 @@ unsigned* error_word() {
   return p;
 }
 
+}  // namespace
+
+unsigned* device_error_word() { return error_word(); }
+unsigned long long wait_budget_ns() {
+  const unsigned long long w = g_wait_ns.load(std::memory_order_relaxed);
+  return w ? w : kDefaultWaitNs;
+}
+int stalled_cta() { return g_stall_cta.load(std::memory_order_relaxed); }
+
+namespace {
+
 bool env_flag(const char* name) {
   const char* v = getenv(name);
   return v && v[0] && strcmp(v, "0") != 0;
@@ -172,9 +183,8 @@ AttnParams base_params(int H, int dn, int dr, int dv, float scale, const void* q
   p.scale = resolve_scale(scale, dn, dr);
   p.scale_log2 = (float)((double)p.scale * 1.4426950408889634);
   p.err = error_word();
-  const unsigned long long w = g_wait_ns.load(std::memory_order_relaxed);
-  p.wait_ns = w ? w : kDefaultWaitNs;
-  p.stall_cta = g_stall_cta.load(std::memory_order_relaxed);
+  p.wait_ns = wait_budget_ns();
+  p.stall_cta = stalled_cta();
   const int nf = g_flag_tiles.load(std::memory_order_relaxed);
   p.flag_tiles = nf > 0 ? nf : INT_MAX;
   return p;

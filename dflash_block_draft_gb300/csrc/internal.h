@@ -99,6 +99,73 @@ size_t latent_absorbed_bytes(int R, int H, int total_q, int total_kv);
 cudaError_t launch_latent_absorbed(const AttnParams& p, const void* c_kv, const void* w, void* ws,
                                    cudaStream_t stream);
 
+// What every launcher takes from api.cu: the current device's error word, and the
+// bounded waits' settings (budget of one wait, stalled CTA of the timeout tests).
+unsigned* device_error_word();
+unsigned long long wait_budget_ns();
+int stalled_cta();
+
+// Norm and rotation of query and key heads (qk_norm_rope.cu), also on the way
+// into a paged cache: then kc/vc are written instead of ko and positions come
+// from the requests' lengths.  Strides in elements, from token to token.
+struct RopeArgs {
+  const void *q, *k, *v;
+  const void *wq, *wk;    // norm weights, nullable
+  const float* cs;        // [max_pos, rot]
+  const int32_t* pos;     // [T] (not paged)
+  void *qo, *ko;          // contiguous
+  long long qs, ks, vs;
+  int T, Hq, Hkv, D, rot, max_pos, interleaved;
+  float eps;
+  // paged
+  void *kc, *vc;
+  long long kps, vps;
+  const int32_t *table, *kv_lens, *q_off;
+  int R, P, max_pages, num_pages;
+  // backward
+  const void *dqo, *dko;
+  float* dw_part;         // [blocks, 2, D] partial norm gradients
+  unsigned* err;
+};
+cudaError_t launch_qk_norm_rope(const RopeArgs& a, bool bf16, bool paged, cudaStream_t stream);
+size_t rope_bwd_workspace_bytes(int D);
+// dq, dk go to a.qo, a.ko.
+cudaError_t launch_qk_norm_rope_bwd(const RopeArgs& a, bool bf16, float* dwq, float* dwk, cudaStream_t stream);
+
+// Attention over a paged cache (attn_paged.cu, attn_paged_tc.cu).
+struct PagedArgs {
+  const void *q, *kc, *vc;
+  const int32_t *table, *kv_lens, *q_off;
+  void* out;
+  float* lse;             // nullable
+  int R, Hq, Hkv, G, D, total_q, max_q, num_pages, P, max_pages;
+  long long kps, vps;     // elements from page to page
+  int causal;
+  float scale_log2;       // scale * log2(e)
+  int rows;               // rows (token, head of the group) of a row tile
+  // workspace: partial results of row tiles that several CTAs share
+  int4* meta;             // [grid]
+  float2* part_ml;        // [2 * grid, rows] running maximum (base 2) and sum
+  float* part_o;          // [2 * grid, rows, D] unnormalised
+  unsigned* err;
+  unsigned long long wait_ns;
+  int stall_cta;
+};
+size_t paged_workspace_bytes(bool bf16, int Hq, int Hkv, int D, int max_q, int P);
+cudaError_t launch_attn_paged(PagedArgs a, bool bf16, void* ws, cudaStream_t stream);
+
+// Verification of drafted tokens (verify.cu).
+struct VerifyArgs {
+  const float *p, *q;
+  const int32_t *tokens, *offsets;
+  const float *u, *s;
+  int32_t *out, *acc;
+  long long ps, qs;
+  int R, V, total, max_draft;
+  unsigned* err;
+};
+cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t stream);
+
 cudaError_t launch_build_mask(const int32_t* anchors, bool bf16, int B, int S, int Q, int nb, int bs, void* mask,
                               unsigned* err, cudaStream_t stream);
 cudaError_t launch_mask_scan(const void* mask, bool bf16, int B, int S, int Q, uint8_t* classes,

@@ -1,0 +1,215 @@
+// paged.cuh -- how the paged-attention kernels deal their work out (sm_103a).
+//
+// A row tile is `rows` consecutive rows (token, head of the group; token-major) of
+// one request and one key/value head; it needs the key tiles up to its last
+// token's limit.  All key tiles of all row tiles, in the order request, key/value
+// head, row tile, key tile, form one line of T tiles, and CTA c of G takes the
+// tiles [c T / G, (c+1) T / G) of it (G at most T, further CTAs have none): equal work whatever the lengths, one long
+// request or many short ones, without a host that knows the lengths.  A row tile
+// that one CTA holds whole is finished by it; of one that is cut, every CTA leaves
+// a partial result (running maximum, sum, unnormalised output) in the workspace:
+// slot 2c for the piece that continues a row tile begun by an earlier CTA, slot
+// 2c + 1 for the piece that begins one and is cut by the range's end.  The CTA
+// that begins a cut row tile writes down in meta[c] how many CTAs share it, and
+// the merge kernel adds the pieces up in that order.
+#pragma once
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace dflash {
+namespace paged {
+
+// One request as the kernels see it.
+struct Req {
+  int q0, n, kv;  // first packed row, new tokens, positions
+  int nrt;        // row tiles of one key/value head (0: nothing to do)
+};
+
+__device__ __forceinline__ Req load_request(const PagedArgs& a, int r, bool report) {
+  Req q;
+  q.q0 = a.q_off[r];
+  const int q1 = a.q_off[r + 1];
+  q.n = q1 - q.q0;
+  q.kv = a.kv_lens[r];
+  const bool bad = q.q0 < 0 || q.n < 0 || q1 > a.total_q || q.n > a.max_q || q.kv < 0 ||
+                   q.kv > (long long)a.max_pages * a.P;
+  if (bad && report) record_error(a.err, DFLASH_ERR_INVALID);
+  q.nrt = bad ? 0 : (int)(((long long)q.n * a.G + a.rows - 1) / a.rows);
+  return q;
+}
+
+// Positions that the last token of row tile rt sees; every row tile has one key
+// tile at least, so that rows that see nothing are written too.
+__device__ __forceinline__ int tile_limit(const PagedArgs& a, const Req& q, int rt) {
+  if (!a.causal) return q.kv;
+  const long long end = min((long long)(rt + 1) * a.rows, (long long)q.n * a.G);
+  return max(0, q.kv - q.n + (int)((end - 1) / a.G) + 1);
+}
+template <int BN>
+__device__ __forceinline__ int key_tiles(const PagedArgs& a, const Req& q, int rt) {
+  return max(1, (tile_limit(a, q, rt) + BN - 1) / BN);
+}
+// Key tiles of one key/value head of a request.
+template <int BN>
+__device__ __forceinline__ long long head_tiles(const PagedArgs& a, const Req& q) {
+  if (q.nrt == 0) return 0;
+  if (!a.causal) return (long long)q.nrt * key_tiles<BN>(a, q, 0);
+  long long s = 0;
+  for (int rt = 0; rt < q.nrt; ++rt) s += key_tiles<BN>(a, q, rt);
+  return s;
+}
+
+// A CTA's range, found once by the whole block and kept in shared memory.
+struct Range {
+  long long total;    // T
+  long long t0, t1;   // this CTA's tiles
+  long long before;   // tiles of the requests before r0
+  int r0;             // request that holds tile t0
+  int ctas;           // G, at most T: every CTA below it has a tile
+};
+
+// Whole block (kThreads threads): every thread adds up a strip of requests, a scan
+// over the strips gives T and finds the strip, and its thread the request, of t0.
+template <int BN, int kThreads>
+__device__ __forceinline__ void find_range(const PagedArgs& a, Range* out, long long* scratch /* [kThreads/32 + 1] */) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int strip = (a.R + kThreads - 1) / kThreads;
+  const int lo = min(a.R, tid * strip), hi = min(a.R, lo + strip);
+  long long mine = 0;
+  for (int r = lo; r < hi; ++r) mine += a.Hkv * head_tiles<BN>(a, load_request(a, r, blockIdx.x == 0));
+  long long c = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, c, o);
+    if (lane >= o) c += v;
+  }
+  if (lane == 31) scratch[warp] = c;
+  __syncthreads();
+  long long base = 0, total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    base += w < warp ? scratch[w] : 0;
+    total += scratch[w];
+  }
+  const long long before = base + c - mine;
+  const int ctas = (int)min((long long)gridDim.x, total), me = blockIdx.x;
+  const long long t0 = me < ctas ? total * me / ctas : total, t1 = me < ctas ? total * (me + 1) / ctas : total;
+  if (tid == 0) {
+    out->ctas = ctas;
+    out->total = total;
+    out->t0 = t0;
+    out->t1 = t1;
+    out->before = 0;
+    out->r0 = 0;
+  }
+  __syncthreads();
+  if (before <= t0 && t0 < before + mine) {  // one thread at most
+    long long s = before;
+    int r = lo;
+    for (; r + 1 < hi; ++r) {
+      const long long w = a.Hkv * head_tiles<BN>(a, load_request(a, r, false));
+      if (t0 < s + w) break;
+      s += w;
+    }
+    out->before = s;
+    out->r0 = r;
+  }
+  __syncthreads();
+}
+
+// A CTA's share of one row tile: key tiles [kt0, kt1) of nt.
+struct Piece {
+  int r, h, rt;
+  Req q;
+  int kt0, kt1, nt;
+  int limit;           // positions the row tile's last token sees
+  int slot;            // partial slot, -1: the row tile is whole
+  int shared;          // CTAs that share the row tile (set where this piece begins it)
+};
+
+// CTA that holds tile t.
+__device__ __forceinline__ int owner_of(long long t, long long total, int grid) {
+  int c = (int)((t * grid) / total);
+  while (c + 1 < grid && total * (c + 1) / grid <= t) ++c;
+  while (c > 0 && total * c / grid > t) --c;
+  return c;
+}
+
+// Walks the pieces of a CTA's range.  Every role of a kernel keeps its own.
+template <int BN>
+struct Walker {
+  const PagedArgs& a;
+  const Range& rg;
+  long long t;      // next tile
+  long long at;     // first tile of the current row tile
+  Req q;
+  int r, h, rt;
+
+  __device__ __forceinline__ Walker(const PagedArgs& a_, const Range& rg_) : a(a_), rg(rg_) {
+    t = rg.t0;
+    r = rg.r0;
+    h = rt = 0;
+    at = rg.before;
+    if (t >= rg.t1) return;
+    q = load_request(a, r, false);
+    const long long per = head_tiles<BN>(a, q);
+    h = (int)((t - at) / per);
+    at += h * per;
+    skip();
+  }
+  // Moves on to the row tile that holds tile t, within the current head.
+  __device__ __forceinline__ void skip() {
+    if (!a.causal) {
+      const int nt = key_tiles<BN>(a, q, 0);
+      const int k = (int)((t - at) / nt);
+      rt += k;
+      at += (long long)k * nt;
+      return;
+    }
+    for (;;) {
+      const int nt = key_tiles<BN>(a, q, rt);
+      if (t < at + nt) return;
+      at += nt;
+      ++rt;
+    }
+  }
+  __device__ __forceinline__ bool next(Piece* p) {
+    if (t >= rg.t1) return false;
+    p->r = r;
+    p->h = h;
+    p->rt = rt;
+    p->q = q;
+    p->limit = tile_limit(a, q, rt);
+    p->nt = key_tiles<BN>(a, q, rt);
+    p->kt0 = (int)(t - at);
+    const long long end = min(at + p->nt, rg.t1);
+    p->kt1 = (int)(end - at);
+    p->shared = 0;
+    if (p->kt0 > 0) p->slot = 2 * blockIdx.x;
+    else if (p->kt1 < p->nt) {
+      p->slot = 2 * blockIdx.x + 1;
+      p->shared = owner_of(at + p->nt - 1, rg.total, rg.ctas) - (int)blockIdx.x + 1;
+    } else {
+      p->slot = -1;
+    }
+    t = end;
+    if (t < rg.t1) {  // the next row tile, head or request with work
+      at += p->nt;
+      if (++rt == q.nrt) {
+        rt = 0;
+        if (++h == a.Hkv) {
+          h = 0;
+          do q = load_request(a, ++r, false);
+          while (q.nrt == 0 && r + 1 < a.R);
+        }
+      }
+    }
+    return true;
+  }
+};
+
+// What the merge kernel needs about CTA c: the row tile that it begins and leaves cut.
+__device__ __forceinline__ int4 pack_meta(const Piece& p) { return make_int4(p.shared, p.r, p.h, p.rt); }
+
+}  // namespace paged
+}  // namespace dflash

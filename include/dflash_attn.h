@@ -285,6 +285,194 @@ DFLASH_API dflash_status_t dflash_attn_dense_backward(const dflash_dims_t* dims,
                                                       size_t ws_bytes, dflash_stream_t stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * The serving step of a grouped-query draft (max.pipelines.architectures.
+ * dflash_kimi_k25 page: DFlashKimiK25, whose draft has grouped key/value heads,
+ * rotary positions and optional query/key norms; materialize writes projected
+ * context into the draft's cache, forward_block attends one drafted block per
+ * request over it, ragged by input_row_offsets):
+ *   dflash_qk_norm_rope   norm and rotation of query and key heads (+ backward),
+ *   dflash_cache_append   the same on the way into a paged cache,
+ *   dflash_attn_paged     attention of the new tokens over the pages,
+ *   dflash_verify         acceptance of drafted tokens.
+ * Element types, ownership, streams and errors as above.
+ */
+
+/*
+ * Norm and rotation of query and key heads.  Per token t and head vector x of
+ * D components:
+ *   y = x * (mean_d x_d^2 + eps)^-1/2 * w          (w given; y = x when it is null)
+ *   out = y with its first rot_dim components rotated in rot_dim/2 planes by
+ *         the angles of position positions[t]; the others are passed on.
+ * Plane i joins components (i, i + rot_dim/2), or (2i, 2i+1) when interleaved:
+ *   a' = a cos_i - b sin_i,  b' = b cos_i + a sin_i.
+ * Everything is computed in fp32 and rounded once, to the element type.
+ *   q [T, H_q, D] and k [T, H_kv, D]: tokens q_stride / k_stride elements apart
+ *     (0: H * D), the heads of a token contiguous, so that slices of one
+ *     projection's output [T, (H_q + 2 H_kv) D] are taken as they are.
+ *   q_norm, k_norm [D], each nullable: the norm weights, element type = dtype.
+ *   cos_sin [max_pos, rot_dim] fp32: rot_dim/2 cosines, then rot_dim/2 sines of
+ *     each position; null when rot_dim = 0 (then positions is not read either).
+ *   positions [T] int32.  A position outside [0, max_pos) is recorded as
+ *     DFLASH_ERR_INVALID in the device error word and its token is skipped (its
+ *     output rows are left as they were; it adds nothing to the norm gradients).
+ *   q_out [T, H_q, D], k_out [T, H_kv, D]: contiguous; may be q and k themselves
+ *     where those are contiguous.  H_q or H_kv may be 0 (its pointers unused).
+ * D: a multiple of 8 up to DFLASH_PAGED_MAX_D; rot_dim even, at most D.
+ */
+#define DFLASH_PAGED_MAX_D 256
+typedef struct {
+  int T;           /* tokens */
+  int H_q, H_kv;   /* query and key heads */
+  int D;           /* head dimension */
+  int rot_dim;     /* rotated components of a head */
+  int max_pos;     /* rows of cos_sin */
+  int interleaved; /* 0: planes (i, i + rot_dim/2); 1: planes (2i, 2i + 1) */
+  float eps;       /* norm epsilon, >= 0 */
+  int64_t q_stride, k_stride; /* elements from token to token of q and k; 0: contiguous */
+} dflash_rope_dims_t;
+
+DFLASH_API dflash_status_t dflash_qk_norm_rope(const dflash_rope_dims_t* dims, dflash_dtype_t dtype, const void* q,
+                                               const void* k, const void* q_norm, const void* k_norm,
+                                               const float* cos_sin, const int32_t* positions, void* q_out,
+                                               void* k_out, dflash_stream_t stream);
+
+/*
+ * Gradients of sum(dq_out * q_out) + sum(dk_out * k_out).  With g the rotation's
+ * transpose applied to the output gradient, x^ = x r, r = (mean x^2 + eps)^-1/2:
+ *   dw = sum over tokens and heads of g x^,
+ *   dx = r (g w - x^ mean_d(g w x^))       (dx = g without a norm).
+ *   q, k: the forward's inputs (strides as there; unused, and nullable, where
+ *     the norm weight is null).  dq_out, dk_out, dq, dk: contiguous; dq and dk
+ *     may be dq_out and dk_out themselves.
+ *   dq_norm, dk_norm [D] fp32: written (0 for no tokens); required where the
+ *     weight is given, unused elsewhere.  Sums run in a fixed order: equal
+ *     inputs give equal bits on one device type.
+ *   workspace: >= dflash_qk_norm_rope_workspace_size(dims) bytes, 256-byte
+ *     aligned; needs no initialisation.
+ */
+DFLASH_API size_t dflash_qk_norm_rope_workspace_size(const dflash_rope_dims_t* dims);
+DFLASH_API dflash_status_t dflash_qk_norm_rope_backward(
+    const dflash_rope_dims_t* dims, dflash_dtype_t dtype, const void* q, const void* k, const void* q_norm,
+    const void* k_norm, const float* cos_sin, const int32_t* positions, const void* dq_out, const void* dk_out,
+    void* dq, void* dk, float* dq_norm, float* dk_norm, void* workspace, size_t ws_bytes, dflash_stream_t stream);
+
+/*
+ * A paged key/value cache.  Page g holds page_size consecutive positions of one
+ * request, each with H_kv heads of D values: k_cache and v_cache are
+ * [num_pages, page_size, H_kv, D], pages k_page_stride / v_page_stride elements
+ * apart (0: contiguous), so that both may be halves of one
+ * [num_pages, 2, page_size, H_kv, D] tensor.  Position p of request r lies in
+ * row p % page_size of page page_table[r, p / page_size].
+ *
+ * A step's batch: R requests, request r with the new tokens
+ * [q_offsets[r], q_offsets[r+1]) of the packed token axis (possibly none), which
+ * are the last ones of its kv_lens[r] positions.  Table entries behind
+ * ceil(kv_lens[r] / page_size) and what lies behind position kv_lens[r] in the
+ * last page are never used.  Packed rows behind q_offsets[R] are left as they
+ * were.  All int32, on the device.
+ */
+typedef struct {
+  int R;                /* requests */
+  int H_q, H_kv;        /* query and key/value heads; H_kv divides H_q */
+  int D;                /* head dimension */
+  int total_q;          /* rows of the packed token axis (>= q_offsets[R]) */
+  int max_q_len;        /* bound on every request's new tokens */
+  int num_pages;        /* pages of the cache */
+  int page_size;        /* positions of a page */
+  int max_pages;        /* columns of page_table [R, max_pages] */
+  int64_t k_page_stride, v_page_stride; /* elements from page to page; 0: contiguous */
+} dflash_paged_dims_t;
+
+/*
+ * Appends the new tokens' keys and values to their pages, keys (and, where q is
+ * given, queries) normed and rotated as by dflash_qk_norm_rope at the position
+ * they take in their request, kv_lens[r] - n + i.  kv_lens already counts the
+ * new tokens.  Values are copied.  (DFlashKimiK25.materialize: without q.)
+ *   rope: norm and rotation (T, H_q, H_kv and D are not read; q_stride and
+ *     k_stride are, v_stride is this call's).  rot_dim = 0 and null weights
+ *     append the keys as they are.
+ *   q, k, v: packed [total_q, heads, D] with token strides; q and q_out are
+ *     null where no queries are wanted; q_out [total_q, H_q, D] contiguous.
+ * A token whose position is negative, lies beyond the rotation table or beyond
+ * the page table, or whose page id is outside [0, num_pages), and every token
+ * of a request whose offsets are not ascending within [0, total_q], is recorded
+ * as DFLASH_ERR_INVALID and skipped (its cache and q_out rows stay as they
+ * were).  Two tokens must not be given one cache row: requests may share pages
+ * that only hold earlier positions.  max_q_len is not read.
+ */
+DFLASH_API dflash_status_t dflash_cache_append(const dflash_paged_dims_t* dims, const dflash_rope_dims_t* rope,
+                                               dflash_dtype_t dtype, const void* q, const void* k, const void* v,
+                                               int64_t v_stride, const void* q_norm, const void* k_norm,
+                                               const float* cos_sin, const int32_t* page_table,
+                                               const int32_t* kv_lens, const int32_t* q_offsets, void* q_out,
+                                               void* k_cache, void* v_cache, dflash_stream_t stream);
+
+/*
+ * Attention of the new tokens over their requests' pages.  Token i of a request
+ * with n new tokens and length L = kv_lens[r] sees positions p < L (causal = 0:
+ * the drafted block, which sees its context and all of itself) or
+ * p < L - n + i + 1 (causal = 1: prefill chunks, verification, single tokens).
+ * Query head h reads key/value head h / (H_q / H_kv).
+ *   out(i,h) = sum_p softmax_p(q(i,h) . k(p) scale) v(p),  scale <= 0: D^-0.5
+ *   q, out [total_q, H_q, D] contiguous; lse [H_q, total_q] fp32, optional.
+ * A row that sees nothing gets out = 0 and lse = -inf.  Keys and values of the
+ * positions p < L have to be finite; a page id outside [0, num_pages) is recorded
+ * as DFLASH_ERR_INVALID and read as zeros.  A request whose offsets or length
+ * are out of range (n < 0 or > max_q_len, L < 0 or > max_pages * page_size) is
+ * recorded as DFLASH_ERR_INVALID and skipped (rows left as they were).
+ * D: a multiple of 8 up to DFLASH_PAGED_MAX_D.  bf16 with D <= 128,
+ * H_q / H_kv <= 128 and page_size a multiple of 8 runs on the tensor cores;
+ * everything else, and all fp32, on the CUDA-core kernel.  Work is dealt in
+ * equal runs of key tiles to the SMs whatever the lengths, and the pieces of
+ * divided rows are merged by a second kernel, in a fixed order.
+ *   workspace: >= dflash_attn_paged_workspace_size(dims, dtype) bytes, 256-byte
+ *     aligned; its size does not depend on the lengths; needs no initialisation.
+ */
+DFLASH_API size_t dflash_attn_paged_workspace_size(const dflash_paged_dims_t* dims, dflash_dtype_t dtype);
+DFLASH_API dflash_status_t dflash_attn_paged(const dflash_paged_dims_t* dims, dflash_dtype_t dtype, const void* q,
+                                             const void* k_cache, const void* v_cache, const int32_t* page_table,
+                                             const int32_t* kv_lens, const int32_t* q_offsets, int causal, float scale,
+                                             void* out, float* lse, void* workspace, size_t ws_bytes,
+                                             dflash_stream_t stream);
+
+/*
+ * Verification of drafted tokens against the target's probabilities, with given
+ * random numbers.  Request r drafted n = draft_offsets[r+1] - draft_offsets[r]
+ * tokens x_0 .. x_{n-1} (possibly none).  With p_j the target's probabilities at
+ * drafted position j (p_n: behind the last one) and q_j the draft's:
+ *   a = first j with not (u_j q_j(x_j) < p_j(x_j)), or n where there is none;
+ *   w = max(p_a - q_a, 0) where a < n and that is not all zero, else p_a;
+ *   z = smallest i with w_0 + ... + w_i > s_r (w_0 + ... + w_{V-1}).
+ * out_tokens[r] = x_0 .. x_{a-1}, z, then -1; num_accepted[r] = a.  A token
+ * drawn from q_j is so turned into one that is distributed as p_j.
+ *   target_probs [rows, V] fp32, request r's rows from draft_offsets[r] + r on
+ *     (n + 1 of them); draft_probs [total_draft, V] fp32, or null for a draft
+ *     that took its most likely token (q_j is then 1 at x_j and 0 elsewhere).
+ *     Rows target_stride / draft_stride elements apart (0: V).
+ *   draft_tokens [total_draft], draft_offsets [R+1] int32; accept_u
+ *     [total_draft] and sample_u [R] fp32 in [0, 1).
+ *   out_tokens [R, max_draft + 1], num_accepted [R] int32: every element written.
+ * Comparisons are made in 64 bits and sums over V exactly, on probabilities
+ * held to 2^-50 (values outside [0, 1] are clamped, NaN counts as 0), so that the
+ * result does not depend on the order of the sum.  A drafted token outside [0, V)
+ * is recorded as DFLASH_ERR_INVALID and rejected; a request whose w is all zero
+ * is recorded and gets z = 0; one whose offsets are out of range is recorded and
+ * gets num_accepted = 0 and tokens -1.
+ */
+typedef struct {
+  int R;           /* requests */
+  int V;           /* vocabulary */
+  int total_draft; /* rows of the packed draft axis (>= draft_offsets[R]) */
+  int max_draft;   /* bound on every request's drafted tokens */
+  int64_t target_stride, draft_stride; /* elements from row to row; 0: V */
+} dflash_verify_dims_t;
+DFLASH_API dflash_status_t dflash_verify(const dflash_verify_dims_t* dims, const float* target_probs,
+                                         const float* draft_probs, const int32_t* draft_tokens,
+                                         const int32_t* draft_offsets, const float* accept_u, const float* sample_u,
+                                         int32_t* out_tokens, int32_t* num_accepted, dflash_stream_t stream);
+
+/*
  * Workspace bytes a call needs.  For DENSE/ANCHORED (and their _BACKWARD
  * modes) pass dims (dims->B, S, Q,
  * H, head dims) and ignore the ragged arguments; for RAGGED pass dims = NULL

@@ -1,0 +1,625 @@
+"""The serving operators on the GPU against the 64-bit oracle (oracle/serving.py).
+
+Tolerances count roundings.  u = 2^-24 is half a step of fp32; a result in bf16 is
+off by half a step of its own, 2^-8 of its value, on top.  Sums of n terms in
+fp32 are off by at most n u of the sum of their absolute values, whatever the
+order; the oracle returns those sums of absolute values ("size").
+"""
+import numpy as np
+import pytest
+
+from oracle import serving as osv
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+U = 2.0 ** -24
+HALF = {"bf16": 2.0 ** -8, "fp32": U}
+DT = {"bf16": torch.bfloat16, "fp32": torch.float32}
+INVALID = 1
+
+
+@pytest.fixture(scope="module")
+def dfl():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import dflash_block_draft_gb300 as m
+    m.load_library()
+    m.dflash_last_device_error()
+    return m
+
+
+def _rand(rng, shape, dtype, scale=1.0):
+    return torch.from_numpy((rng.standard_normal(shape) * scale).astype(np.float32)).to(DT[dtype]).cuda()
+
+
+def _np(t):
+    return t.detach().double().cpu().numpy()
+
+
+def _i32(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+
+
+def _within(got, want, tol, what=""):
+    got = _np(got) if torch.is_tensor(got) else got
+    assert got.shape == want.shape, what
+    bad = ~(np.abs(got - want) <= tol)
+    assert not bad.any(), (what, int(bad.sum()), float(np.abs(got - want)[bad].max()), np.argwhere(bad)[:3].tolist())
+
+
+def _table(max_pos, rot, base=1e4):
+    if rot == 0:
+        return None
+    a = np.arange(max_pos)[:, None] * base ** (-np.arange(0, rot, 2) / rot)[None]
+    return torch.from_numpy(np.concatenate([np.cos(a), np.sin(a)], 1).astype(np.float32)).cuda()
+
+
+# ------------------------------------------------------------------ norm and rotation
+# T, Hq, Hkv, D, rot, interleaved, weights, layout
+ROPE = [
+    (1, 1, 1, 8, 8, False, True, "own"),
+    (5, 4, 2, 64, 64, False, True, "qkv"),
+    (7, 28, 4, 128, 128, False, True, "qkv"),
+    (33, 8, 8, 128, 64, False, True, "own"),
+    (9, 3, 1, 128, 128, True, True, "qkv"),
+    (6, 5, 5, 80, 40, False, True, "own"),     # planes cut the 16-byte vectors
+    (6, 5, 5, 80, 80, True, False, "qkv"),
+    (11, 2, 2, 256, 256, False, True, "qkv"),
+    (11, 2, 2, 256, 128, True, True, "own"),
+    (4, 2, 1, 16, 2, False, True, "own"),      # one plane: the plain kernel
+    (4, 2, 1, 24, 6, True, True, "odd"),       # tensors that start 4 or 2 bytes off a vector
+    (5, 4, 2, 128, 128, False, True, "odd"),
+    (3, 2, 2, 64, 0, False, True, "own"),      # norm only
+    (3, 2, 2, 64, 64, False, False, "own"),    # rotation only
+    (3, 2, 2, 64, 0, False, False, "qkv"),     # a copy
+    (700, 16, 4, 128, 128, False, True, "qkv"),
+    (900, 32, 8, 128, 128, False, True, "own"),
+]
+
+
+def _rope_case(rng, T, Hq, Hkv, D, rot, weighted, layout, dtype):
+    if layout == "qkv":
+        x = _rand(rng, (T, (Hq + 2 * Hkv) * D), dtype)
+        q = x[:, :Hq * D].view(T, Hq, D)
+        k = x[:, Hq * D:(Hq + Hkv) * D].view(T, Hkv, D)
+    elif layout == "odd":
+        q = _rand(rng, (1 + T * Hq * D,), dtype)[1:].view(T, Hq, D)
+        k = _rand(rng, (1 + T * Hkv * D,), dtype)[1:].view(T, Hkv, D)
+    else:
+        q, k = _rand(rng, (T, Hq, D), dtype), _rand(rng, (T, Hkv, D), dtype)
+    w = (_rand(rng, (D,), dtype, 0.2) + 1, _rand(rng, (D,), dtype, 0.2) + 1) if weighted else (None, None)
+    cs = _table(64, rot)
+    pos = rng.integers(0, 64, T)
+    return q, k, w, cs, pos
+
+
+def _w(w):
+    return None if w is None else _np(w)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("T,Hq,Hkv,D,rot,inter,weighted,layout", ROPE)
+def test_qk_norm_rope(dfl, T, Hq, Hkv, D, rot, inter, weighted, layout, dtype):
+    rng = np.random.default_rng(T * 1000 + D + rot)
+    q, k, (wq, wk), cs, pos = _rope_case(rng, T, Hq, Hkv, D, rot, weighted, layout, dtype)
+    qo, ko = dfl.dflash_qk_norm_rope(q, k, _i32(pos), cs, q_norm=wq, k_norm=wk, eps=1e-5, interleaved=inter)
+    assert dfl.dflash_last_device_error() == 0
+    for x, w, got in ((q, wq, qo), (k, wk, ko)):
+        want, size = osv.norm_rope(_np(x), _w(w), pos, None if cs is None else _np(cs), 1e-5, inter)
+        # mean of D squares, root, two products, a plane's two products and their sum
+        _within(got, want, size * (D + 16) * U + HALF[dtype] * np.abs(want))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("T,Hq,Hkv,D,rot,inter,weighted,layout", ROPE)
+def test_qk_norm_rope_backward(dfl, T, Hq, Hkv, D, rot, inter, weighted, layout, dtype):
+    rng = np.random.default_rng(T * 1000 + D + rot + 1)
+    q, k, (wq, wk), cs, pos = _rope_case(rng, T, Hq, Hkv, D, rot, weighted, layout, dtype)
+    gq, gk = _rand(rng, (T, Hq, D), dtype), _rand(rng, (T, Hkv, D), dtype)
+    run = lambda: dfl.dflash_qk_norm_rope_backward(q, k, _i32(pos), cs, gq, gk, q_norm=wq, k_norm=wk, eps=1e-5,  # noqa: E731
+                                                   interleaved=inter)
+    dq, dk, dwq, dwk = run()
+    assert dfl.dflash_last_device_error() == 0
+    for x, w, g, dx, dw, H in ((q, wq, gq, dq, dwq, Hq), (k, wk, gk, dk, dwk, Hkv)):
+        want, size, ww, wsize = osv.norm_rope_backward(_np(x), _w(w), pos, None if cs is None else _np(cs), 1e-5,
+                                                       inter, _np(g))
+        _within(dx, want, size * (2 * D + 64) * U + HALF[dtype] * np.abs(want), "dx")
+        if w is None:
+            assert dw is None
+        else:
+            _within(dw, ww, wsize * (T * H + D + 32) * U, "dw")
+    again = run()
+    for a, b in zip((dq, dk, dwq, dwk), again):
+        assert (a is None and b is None) or torch.equal(a, b)
+
+
+def test_qk_norm_rope_one_side_only_and_in_place(dfl):
+    rng = np.random.default_rng(7)
+    q, k, (wq, wk), cs, pos = _rope_case(rng, 40, 8, 2, 128, 128, True, "own", "bf16")
+    p = _i32(pos)
+    qo, ko = dfl.dflash_qk_norm_rope(q, k, p, cs, q_norm=wq, k_norm=wk)
+    only_q, none = dfl.dflash_qk_norm_rope(q, None, p, cs, q_norm=wq)
+    none2, only_k = dfl.dflash_qk_norm_rope(None, k, p, cs, k_norm=wk)
+    assert none is None and none2 is None and torch.equal(only_q, qo) and torch.equal(only_k, ko)
+    q2, k2 = q.clone(), k.clone()
+    dfl.dflash_qk_norm_rope(q2, k2, p, cs, q_norm=wq, k_norm=wk, q_out=q2, k_out=k2)
+    assert torch.equal(q2, qo) and torch.equal(k2, ko)
+    gq, gk = _rand(rng, q.shape, "bf16"), _rand(rng, k.shape, "bf16")
+    want = dfl.dflash_qk_norm_rope_backward(q, k, p, cs, gq, gk, q_norm=wq, k_norm=wk)
+    dw = [torch.empty(128, device="cuda") for _ in range(2)]
+    got = dfl.dflash_qk_norm_rope_backward(q, k, p, cs, gq, gk, q_norm=wq, k_norm=wk, grads=(gq, gk, *dw))
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+def test_qk_norm_rope_no_tokens_and_rows_of_zeros(dfl):
+    cs, w = _table(8, 64), torch.ones(64, device="cuda")
+    e = lambda h: torch.empty((0, h, 64), device="cuda")  # noqa: E731
+    qo, ko = dfl.dflash_qk_norm_rope(e(4), e(2), _i32([]), cs, q_norm=w, k_norm=w)
+    assert qo.shape == (0, 4, 64) and ko.shape == (0, 2, 64)
+    out = dfl.dflash_qk_norm_rope_backward(e(4), e(2), _i32([]), cs, e(4), e(2), q_norm=w, k_norm=w)
+    assert (out[2] == 0).all() and (out[3] == 0).all()
+    z = torch.zeros((3, 2, 64), device="cuda")
+    qo, _ = dfl.dflash_qk_norm_rope(z, None, _i32([0, 1, 2]), cs, q_norm=w, eps=1e-6)
+    assert (qo == 0).all()
+
+
+@pytest.mark.parametrize("D,rot", [(128, 128), (24, 6)])
+def test_positions_outside_the_table_are_skipped_and_recorded(dfl, D, rot):
+    rng = np.random.default_rng(8)
+    q, k, (wq, wk), cs, pos = _rope_case(rng, 6, 4, 2, D, rot, True, "own", "fp32")
+    pos = np.array([3, -1, 5, 64, 2 ** 31 - 1, 0])
+    good = np.array([0, 2, 5])
+    p = _i32(pos)
+    qo, ko = torch.full_like(q, 7.0), torch.full_like(k, 7.0)
+    dfl.dflash_qk_norm_rope(q, k, p, cs, q_norm=wq, k_norm=wk, q_out=qo, k_out=ko)
+    assert dfl.dflash_last_device_error() == INVALID and dfl.dflash_last_device_error() == 0
+    rest = [1, 3, 4]
+    assert (qo[rest] == 7).all() and (ko[rest] == 7).all()
+    sel = lambda t: t[good].contiguous()  # noqa: E731
+    a, b = dfl.dflash_qk_norm_rope(sel(q), sel(k), _i32(pos[good]), cs, q_norm=wq, k_norm=wk)
+    assert torch.equal(qo[good], a) and torch.equal(ko[good], b)
+    g = dfl.dflash_qk_norm_rope_backward(q, k, p, cs, q, k, q_norm=wq, k_norm=wk)
+    assert dfl.dflash_last_device_error() == INVALID
+    want = osv.norm_rope_backward(_np(sel(q)), _w(wq), pos[good], _np(cs), 1e-6, False, _np(sel(q)))
+    _within(g[2], want[2], want[3] * (12 + D + 32) * U)
+
+
+# ------------------------------------------------------------------ paged batches
+def _batch(rng, kv, n, P, Hkv, D, dtype, layout="own", spare=3, pad=2, garbage=float("nan")):
+    """A cache with the batch's pages in random order; everything that must not be read is `garbage`."""
+    R = len(kv)
+    cnt = [-(-x // P) for x in kv]
+    num, width = sum(cnt) + spare, max(max(cnt, default=0), 1) + 1
+    order = rng.permutation(num)
+    table = np.full((R, width), 2 ** 31 - 1, np.int64)
+    used = 0
+    for r in range(R):
+        table[r, :cnt[r]] = order[used:used + cnt[r]]
+        used += cnt[r]
+    if layout == "halves":
+        both = torch.full((num, 2, P, Hkv, D), garbage, dtype=DT[dtype], device="cuda")
+        kc, vc = both[:, 0], both[:, 1]
+    else:
+        kc, vc = (torch.full((num, P, Hkv, D), garbage, dtype=DT[dtype], device="cuda") for _ in range(2))
+    for r in range(R):
+        for c in range(cnt[r]):
+            m = min(P, kv[r] - c * P)
+            kc[table[r, c], :m] = _rand(rng, (m, Hkv, D), dtype)
+            vc[table[r, c], :m] = _rand(rng, (m, Hkv, D), dtype)
+    off = np.concatenate([[0], np.cumsum(n)])
+    return kc, vc, table, off, int(off[-1]) + pad
+
+
+def _check_attn(dfl, rng, kv, n, P, Hq, Hkv, D, dtype, causal, layout="own", scale=0.0, max_q=None):
+    kc, vc, table, off, T = _batch(rng, kv, n, P, Hkv, D, dtype, layout)
+    q = _rand(rng, (T, Hq, D), dtype)
+    q[off[-1]:] = float("nan")
+    out = torch.full((T, Hq, D), 7.0, dtype=DT[dtype], device="cuda")
+    lse = torch.full((Hq, T), 7.0, device="cuda")
+    ws_bytes = dfl.dflash_attn_paged_workspace_size(Hq, Hkv, D, max_q or max(n), P, 0 if dtype == "bf16" else 1)
+    ws = torch.full((ws_bytes // 4,), float("nan"), device="cuda")  # a workspace needs no initialisation
+    run = lambda: dfl.dflash_attn_paged(q, kc, vc, _i32(table), _i32(kv), _i32(off), max_q or max(n), causal=causal,  # noqa: E731
+                                        out=out, lse=lse, scale=scale, workspace=ws)
+    run()
+    assert dfl.dflash_last_device_error() == 0
+    assert (out[off[-1]:] == 7).all() and (lse[:, off[-1]:] == 7).all()  # rows behind the last request
+    got_o, got_l = out[:off[-1]].clone(), lse[:, :off[-1]].clone()
+    want, wl, size, score = osv.attn_paged(_np(q)[:off[-1]], _np(kc), _np(vc), table, kv, off, causal, scale or None)
+    m = max(kv)
+    # scores: D terms and the scale, in the weight and in the sum; the sums over at most m positions; bf16 weights
+    sc = score[..., None]
+    tol = size * (2 * (D + 8) * U * sc + (m + 64) * U + 2.0 ** -21 + (HALF[dtype] if dtype == "bf16" else 0.0))
+    _within(got_o, want, tol + HALF[dtype] * np.abs(want), "out")
+    seen = np.isfinite(wl)
+    got_np = _np(got_l)
+    assert (np.isneginf(got_np) == ~seen).all() and (got_np[~seen] == -np.inf).all()
+    ltol = (D + 8) * U * score.T + (m + 64) * U + 8 * U * np.abs(np.where(seen, wl, 0)) + 2.0 ** -20
+    _within(got_np[seen], wl[seen], ltol[seen], "lse")
+    run()
+    assert torch.equal(out[:off[-1]], got_o) and torch.equal(lse[:, :off[-1]], got_l)  # a fixed order of sums
+
+
+# kv lengths, new tokens, page size, Hq, Hkv, D
+ATTN = [
+    ([1], [1], 8, 1, 1, 8),
+    ([5], [5], 16, 4, 2, 64),
+    ([128, 129, 127], [1, 1, 1], 64, 8, 2, 128),
+    ([300, 17, 64], [16, 16, 16], 64, 32, 8, 128),
+    ([200, 0, 40, 3], [4, 0, 0, 3], 16, 28, 4, 128),   # requests without tokens; without positions
+    ([0, 2, 50], [3, 5, 4], 16, 8, 2, 64),             # fewer positions than new tokens: rows that see nothing
+    ([1000], [1], 128, 8, 1, 128),                     # one head and long: cut among many CTAs
+    ([3000, 700], [2, 1], 256, 4, 4, 64),
+    ([260, 131], [130, 131], 16, 8, 2, 128),           # row tiles within one request
+    ([500], [300], 32, 5, 5, 96),
+    ([90, 400], [9, 2], 24, 6, 2, 80),                 # pages that end inside a tile
+    ([90, 400], [9, 2], 7, 6, 2, 128),                 # odd pages
+    ([70, 30], [8, 8], 1, 2, 1, 64),
+    ([333], [33], 48, 2, 2, 256),
+    ([150], [20], 40, 16, 1, 40),
+    ([64] * 37, [1] * 37, 16, 4, 1, 128),
+    ([40] * 10, [2] * 10, 8, 130, 1, 64),              # more heads in a group than a tile has rows
+    ([257, 1, 129], [16, 1, 7], 128, 64, 8, 128),
+]
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("kv,n,P,Hq,Hkv,D", ATTN)
+def test_attn_paged(dfl, kv, n, P, Hq, Hkv, D, dtype, causal):
+    _check_attn(dfl, np.random.default_rng(sum(kv) + D), kv, n, P, Hq, Hkv, D, dtype, causal)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_attn_paged_halves_of_one_cache_scale_and_loose_bound(dfl, dtype):
+    _check_attn(dfl, np.random.default_rng(5), [100, 333], [16, 3], 16, 8, 2, 128, dtype, True, layout="halves",
+                scale=0.31)
+    _check_attn(dfl, np.random.default_rng(6), [100, 333], [1, 1], 64, 8, 2, 128, dtype, True, max_q=700)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_attn_paged_large_scores_keep_their_maximum(dfl, dtype):
+    """Rising keys: the running maximum moves at every tile, by more than fp32's exponent range in total."""
+    P, D, kv = 16, 64, 400
+    kc = torch.zeros((25, P, 1, D), dtype=DT[dtype], device="cuda")
+    vc = _rand(np.random.default_rng(3), kc.shape, dtype)
+    kc[..., 0] = torch.arange(kv, device="cuda").view(25, P, 1).to(DT[dtype]) * 4
+    q = torch.zeros((1, 2, D), dtype=DT[dtype], device="cuda")
+    q[0, 0, 0], q[0, 1, 0] = 1.0, -1.0
+    table, off = np.arange(25)[None], np.array([0, 1])
+    out = dfl.dflash_attn_paged(q, kc, vc, _i32(table), _i32([kv]), _i32(off), 1, scale=1.0)
+    want, _, size, _ = osv.attn_paged(_np(q), _np(kc), _np(vc), table, [kv], off, True, 1.0)
+    # one product a score: exact; exponent differences are whole multiples of 4 (or of their bf16 steps)
+    _within(out, want, size * (2.0 ** -8 if dtype == "bf16" else 2.0 ** -20) + HALF[dtype] * np.abs(want))
+
+
+@pytest.mark.parametrize("dtype,P", [("bf16", 16), ("bf16", 7), ("fp32", 16)])
+def test_attn_paged_bad_pages_and_bad_requests(dfl, dtype, P):
+    rng = np.random.default_rng(9)
+    kv, n, Hq, Hkv, D = [60, 45, 30, 50], [2, 2, 2, 3], 4, 2, 64
+    kc, vc, table, off, T = _batch(rng, kv, n, P, Hkv, D, dtype, garbage=0.0)
+    q = _rand(rng, (T, Hq, D), dtype)
+    bad = table.copy()
+    bad[0, 1], bad[1, 0] = -3, kc.shape[0]
+    tbl = table.copy()
+    zero = kc.shape[0]  # the oracle reads such pages as zeros
+    tbl[0, 1] = tbl[1, 0] = zero
+    kz, vz = (np.concatenate([_np(c), np.zeros((1,) + c.shape[1:])]) for c in (kc, vc))
+    out = dfl.dflash_attn_paged(q, kc, vc, _i32(bad), _i32(kv), _i32(off), 3, causal=True)
+    assert dfl.dflash_last_device_error() == INVALID
+    want, _, size, _ = osv.attn_paged(_np(q)[:off[-1]], kz, vz, tbl, kv, off, True)
+    _within(out[:off[-1]], want, size * (2.0 ** -8 if dtype == "bf16" else 2.0 ** -18) + HALF[dtype] * np.abs(want))
+    # requests that break the rules are skipped, the others computed: too many new tokens (max_q_len = 2),
+    # a length beyond the table, a negative length
+    lens = np.array([60, table.shape[1] * P + 1, -1, 50])
+    out = torch.full((T, Hq, D), 7.0, dtype=DT[dtype], device="cuda")
+    dfl.dflash_attn_paged(q, kc, vc, _i32(table), _i32(lens), _i32(off), 2, causal=True, out=out)
+    assert dfl.dflash_last_device_error() == INVALID
+    assert (out[off[1]:] == 7).all()
+    want, _, size, _ = osv.attn_paged(_np(q)[:2], _np(kc), _np(vc), table, kv[:1], off[:2], True)
+    _within(out[:2], want, size * (2.0 ** -8 if dtype == "bf16" else 2.0 ** -18) + HALF[dtype] * np.abs(want))
+    out = torch.full((T, Hq, D), 7.0, dtype=DT[dtype], device="cuda")
+    dfl.dflash_attn_paged(q, kc, vc, _i32(table), _i32(kv), _i32([0, 2, 1, T + 5, 9]), 3, out=out)
+    assert dfl.dflash_last_device_error() == INVALID
+    assert (out[off[1]:] == 7).all() and not (out[:2] == 7).any()
+
+
+# ------------------------------------------------------------------ append
+# kv lengths (new tokens counted), new tokens, P, Hq, Hkv, D, rot, interleaved, weights
+APPEND = [
+    ([1], [1], 16, 4, 1, 64, 64, False, True),
+    ([30, 5, 64], [16, 5, 1], 16, 32, 8, 128, 128, False, True),
+    ([100, 9, 0, 33], [40, 0, 0, 33], 7, 6, 2, 80, 40, False, True),
+    ([50, 20], [7, 20], 24, 4, 4, 256, 128, True, True),
+    ([50, 20], [7, 20], 64, 4, 4, 64, 0, False, False),
+    ([17], [9], 8, 2, 1, 24, 6, True, True),
+    ([400, 380], [390, 300], 64, 16, 4, 128, 128, False, True),
+]
+
+
+@pytest.mark.parametrize("layout", ["own", "halves"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("kv,n,P,Hq,Hkv,D,rot,inter,weighted", APPEND)
+def test_cache_append(dfl, kv, n, P, Hq, Hkv, D, rot, inter, weighted, dtype, layout):
+    rng = np.random.default_rng(sum(kv) + D)
+    kc, vc, table, off, T = _batch(rng, kv, n, P, Hkv, D, dtype, layout, garbage=3.0)
+    x = _rand(rng, (T, (Hq + 2 * Hkv) * D), dtype)
+    q, k, v = (t.view(T, -1, D) for t in x.split([Hq * D, Hkv * D, Hkv * D], 1))
+    wq, wk = (_rand(rng, (D,), dtype, 0.2) + 1, _rand(rng, (D,), dtype, 0.2) + 1) if weighted else (None, None)
+    cs = _table(512, rot)
+    k0, v0 = kc.clone(), vc.clone()
+    qo = torch.full((T, Hq, D), 7.0, dtype=DT[dtype], device="cuda")
+    dfl.dflash_cache_append(k, v, kc, vc, _i32(table), _i32(kv), _i32(off), q=q, cos_sin=cs, q_norm=wq, k_norm=wk,
+                            eps=1e-5, interleaved=inter, q_out=qo)
+    assert dfl.dflash_last_device_error() == 0
+    place = osv.token_places(off, kv, table, P)
+    pos = [p[1] for p in place]
+    csn, m = None if cs is None else _np(cs), len(place)
+    wk_, sk = osv.norm_rope(_np(k)[:m], _w(wk), pos, csn, 1e-5, inter)
+    wq_, sq = osv.norm_rope(_np(q)[:m], _w(wq), pos, csn, 1e-5, inter)
+    tol = lambda want, size: size * (D + 16) * U + HALF[dtype] * np.abs(want)  # noqa: E731
+    _within(qo[:m], wq_, tol(wq_, sq), "q")
+    assert (qo[m:] == 7).all()
+    if m:
+        page, row = (torch.tensor([p[i] for p in place], device="cuda") for i in (2, 3))
+        _within(kc[page, row], wk_, tol(wk_, sk), "k")
+        assert torch.equal(vc[page, row], v[:m])
+        k0[page, row], v0[page, row] = kc[page, row], vc[page, row]
+    assert torch.equal(kc, k0) and torch.equal(vc, v0)  # nothing else was written
+    kc2, vc2 = k0.clone(), v0.clone()
+    assert dfl.dflash_cache_append(k, v, kc2, vc2, _i32(table), _i32(kv), _i32(off), cos_sin=cs, k_norm=wk, eps=1e-5,
+                                   interleaved=inter) is None
+    assert torch.equal(kc2, k0) and torch.equal(vc2, v0)  # without queries: the same keys and values
+
+
+@pytest.mark.parametrize("D,rot", [(64, 64), (24, 6)])
+def test_cache_append_skips_and_records_what_has_no_place(dfl, D, rot):
+    rng = np.random.default_rng(10)
+    P, Hq, Hkv, n, kv = 4, 2, 1, [4, 4, 4, 4, 4], [10, 10, 10, 10, 10]
+    kc, vc, table, off, T = _batch(rng, kv, n, P, Hkv, D, "fp32", garbage=3.0, pad=0)
+    k, v, q = _rand(rng, (T, Hkv, D), "fp32"), _rand(rng, (T, Hkv, D), "fp32"), _rand(rng, (T, Hq, D), "fp32")
+    cs = _table(40, rot)
+    table[0, 1] = -1                         # positions 6, 7 (page 1): skipped; 8, 9 written
+    table[1, 2] = kc.shape[0]                # positions 8, 9 skipped
+    lens = [10, 10, 2, table.shape[1] * P + 2, 10]  # two negative positions; two beyond the table
+    k0 = kc.clone()
+    qo = torch.full((T, Hq, D), 7.0, device="cuda")
+    table[3, :] = np.arange(table.shape[1])  # a table whose every entry is a page
+    dfl.dflash_cache_append(k, v, kc, vc, _i32(table), _i32(lens), _i32(off), q=q, cos_sin=cs, q_out=qo)
+    assert dfl.dflash_last_device_error() == INVALID
+    skipped = [0, 1, 6, 7, 8, 9, 14, 15]
+    kept = [t for t in range(T) if t not in skipped]
+    assert (qo[skipped] == 7).all() and not (qo[kept] == 7).any()
+    assert int((kc != k0).any(-1).any(-1).sum()) <= len(kept)
+    # offsets that are not ascending within the packed axis
+    kc2 = kc.clone()
+    dfl.dflash_cache_append(k, v, kc2, vc, _i32(table), _i32(kv), _i32([0, T + 4, T + 5, T + 6, T + 7, T + 8]),
+                            cos_sin=cs)
+    assert dfl.dflash_last_device_error() == INVALID and torch.equal(kc2, kc)
+
+
+# ------------------------------------------------------------------ verify
+def _verify_case(rng, n, V, one_hot, sharp=2.0):
+    off = np.concatenate([[0], np.cumsum(n)]).astype(np.int64)
+    T, R = int(off[-1]), len(n)
+    soft = lambda x: np.exp(x - x.max(-1, keepdims=True)) / np.exp(x - x.max(-1, keepdims=True)).sum(-1, keepdims=True)  # noqa: E731
+    logits = rng.standard_normal((T + R, V)) * sharp
+    p = soft(logits).astype(np.float32)
+    rows = np.concatenate([np.arange(off[r] + r, off[r + 1] + r) for r in range(R)]).astype(int) if T else []
+    q = soft(logits[rows] + rng.standard_normal((T, V)) * 0.5).astype(np.float32)
+    tok = q.argmax(1) if one_hot else np.array([rng.choice(V, p=x / x.sum()) for x in q.astype(np.float64)], int)
+    return p, None if one_hot else q, tok.reshape(-1).astype(np.int32), off, rng.random(T, np.float32), rng.random(R, np.float32)
+
+
+def _run_verify(dfl, p, q, tok, off, u, s, N):
+    dev = lambda a: None if a is None else torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
+    out = torch.full((len(off) - 1, N + 1), 99, dtype=torch.int32, device="cuda")
+    acc = torch.full((len(off) - 1,), 99, dtype=torch.int32, device="cuda")
+    dfl.dflash_verify(dev(p), dev(q), dev(tok), _i32(off), dev(u), dev(s), N, out_tokens=out, num_accepted=acc)
+    return out.cpu().numpy(), acc.cpu().numpy()
+
+
+@pytest.mark.parametrize("one_hot", [False, True])
+@pytest.mark.parametrize("n,V", [
+    ([1], 1), ([0, 2, 1], 2), ([3, 0, 7, 5], 3), ([4] * 9, 5), ([15, 1, 0, 8], 127), ([7] * 16, 128),
+    ([2, 3], 1000), ([15] * 5, 4096), ([40, 33, 70], 515), ([3, 6, 3], 32000), ([5, 5], 100003), ([1] * 70, 640),
+])
+def test_verify(dfl, n, V, one_hot):
+    rng = np.random.default_rng(V + len(n))
+    case = _verify_case(rng, n, V, one_hot)
+    N = max(n) + 1
+    out, acc = _run_verify(dfl, *case, N)
+    assert dfl.dflash_last_device_error() == 0
+    want, wacc = osv.verify(*case, N)
+    np.testing.assert_array_equal(acc, wacc)
+    np.testing.assert_array_equal(out, want)
+
+
+@pytest.mark.parametrize("V", [37, 4096])
+def test_verify_borders(dfl, V):
+    """Random numbers of 0 and just below 1, equal distributions, rows with a single entry, drafts of probability 0."""
+    rng = np.random.default_rng(V)
+    n = [2] * 8
+    p, q, tok, off, u, s = _verify_case(rng, n, V, False)
+    u[:] = 1 - 2.0 ** -24
+    u[0:4] = 0.0
+    s[0::2], s[1::2] = 0.0, 1 - 2.0 ** -24
+    tgt = [off[r] + r for r in range(8)]
+    q[4], q[5] = p[tgt[2]], p[tgt[2] + 1]              # equal distributions: always accepted
+    p[tgt[3]:tgt[3] + 3] = 0.0
+    p[tgt[3]:tgt[3] + 3, V - 1] = 1.0                  # all mass on the last entry
+    p[tgt[4]:tgt[4] + 3] = 0.0
+    p[tgt[4]:tgt[4] + 3, 0] = 1.0
+    q[10] = 0.0                                        # a draft that names a token it gives no mass
+    p[tgt[6], tok[12]] = 0.0                           # a token the target gives no mass
+    p[tgt[7]] = q[14]                                  # the rest is all zero where it is rejected for p = q = 0
+    p[tgt[7], tok[14]] = q[14, tok[14]] = 0.0
+    out, acc = _run_verify(dfl, p, q, tok, off, u, s, 2)
+    assert dfl.dflash_last_device_error() == 0
+    want, wacc = osv.verify(p, q, tok, off, u, s, 2)
+    np.testing.assert_array_equal(acc, wacc)
+    np.testing.assert_array_equal(out, want)
+
+
+def test_verify_bad_tokens_rows_and_offsets(dfl):
+    rng = np.random.default_rng(11)
+    n, V = [3, 3, 3], 50
+    p, q, tok, off, u, s = _verify_case(rng, n, V, False)
+    u[:] = 0.0
+    tok[1], tok[4] = V, -1
+    out, acc = _run_verify(dfl, p, q, tok, off, u, s, 3)
+    assert dfl.dflash_last_device_error() == INVALID
+    want, wacc = osv.verify(p, q, tok, off, u, s, 3)
+    np.testing.assert_array_equal(out, want)
+    np.testing.assert_array_equal(acc, wacc)
+    assert acc.tolist()[:2] == [1, 1]
+    p2 = p.copy()
+    p2[:] = 0.0
+    p2[0, 0] = np.nan
+    out, acc = _run_verify(dfl, p2, q, tok, off, u, s, 3)
+    assert dfl.dflash_last_device_error() == INVALID
+    assert acc.tolist() == [0, 0, 0] and (out[:, 0] == 0).all() and (out[:, 1:] == -1).all()
+    out, acc = _run_verify(dfl, p, q, tok, np.array([0, 9, 4, 9]), u, s, 3)  # too many, fewer than none, too many
+    assert dfl.dflash_last_device_error() == INVALID
+    assert acc.tolist() == [0, 0, 0] and (out == -1).all()
+
+
+def test_verify_strided_rows(dfl):
+    rng = np.random.default_rng(12)
+    p, q, tok, off, u, s = _verify_case(rng, [5, 2, 8], 1000, False)
+    want = osv.verify(p, q, tok, off, u, s, 8)
+    for width in (1024, 1003):
+        pp = torch.full((p.shape[0], width), float("nan"), device="cuda")
+        qq = torch.full((q.shape[0], width + 8), float("nan"), device="cuda")
+        pp[:, :1000], qq[:, :1000] = torch.from_numpy(p).cuda(), torch.from_numpy(q).cuda()
+        out, acc = dfl.dflash_verify(pp[:, :1000], qq[:, :1000], torch.from_numpy(tok).cuda(), _i32(off),
+                                     torch.from_numpy(u).cuda(), torch.from_numpy(s).cuda(), 8)
+        np.testing.assert_array_equal(out.cpu().numpy(), want[0])
+        np.testing.assert_array_equal(acc.cpu().numpy(), want[1])
+
+
+# ------------------------------------------------------------------ together
+class _Step:
+    """One serving step as it is used: a drafted block enters the cache, attends over it, and the drafted tokens
+    are verified; every buffer is the caller's."""
+
+    def __init__(self, dfl, seed, dtype="bf16", R=3, n=8, P=16, Hq=8, Hkv=2, D=128, V=640):
+        rng = np.random.default_rng(seed)
+        self.dfl, self.n, self.D, self.P = dfl, n, D, P
+        self.kv = [n + int(x) for x in rng.integers(0, 200, R)]
+        self.kc, self.vc, self.table, self.off, T = _batch(rng, self.kv, [n] * R, P, Hkv, D, dtype, pad=0)
+        x = _rand(rng, (T, (Hq + 2 * Hkv) * D), dtype)
+        self.q, self.k, self.v = (t.view(T, -1, D) for t in x.split([Hq * D, Hkv * D, Hkv * D], 1))
+        self.wq, self.wk, self.cs = _rand(rng, (D,), dtype, 0.2) + 1, _rand(rng, (D,), dtype, 0.2) + 1, _table(512, D)
+        self.i = [_i32(self.table), _i32(self.kv), _i32(self.off)]
+        self.qo, self.out = torch.empty_like(self.q.contiguous()), torch.empty((T, Hq, D), dtype=DT[dtype], device="cuda")
+        self.ws = torch.empty(dfl.dflash_attn_paged_workspace_size(Hq, Hkv, D, n, P, 0 if dtype == "bf16" else 1),
+                              dtype=torch.uint8, device="cuda")
+        self.vcase = _verify_case(rng, [n - 1] * R, V, False)
+        p, q, tok, voff, u, s = self.vcase
+        self.v_in = [torch.from_numpy(a).cuda() for a in (p, q, tok)] + [_i32(voff)] + [torch.from_numpy(a).cuda()
+                                                                                       for a in (u, s)]
+        self.tok = torch.empty((R, n), dtype=torch.int32, device="cuda")
+        self.acc = torch.empty(R, dtype=torch.int32, device="cuda")
+
+    def run(self, ws=None):
+        d = self.dfl
+        d.dflash_cache_append(self.k, self.v, self.kc, self.vc, *self.i, q=self.q, cos_sin=self.cs, q_norm=self.wq,
+                              k_norm=self.wk, q_out=self.qo)
+        d.dflash_attn_paged(self.qo, self.kc, self.vc, *self.i, self.n, causal=False, out=self.out,
+                            workspace=self.ws if ws is None else ws)
+        d.dflash_verify(*self.v_in, self.n - 1, out_tokens=self.tok, num_accepted=self.acc)
+
+    def check(self):
+        pos = [p[1] for p in osv.token_places(self.off, self.kv, self.table, self.P)]
+        wq, _ = osv.norm_rope(_np(self.q), _np(self.wq), pos, _np(self.cs), 1e-6, False)
+        # from the cache as it now stands, which test_cache_append checks by itself
+        want, _, size, score = osv.attn_paged(_np(self.qo), _np(self.kc), _np(self.vc), self.table, self.kv, self.off,
+                                              False)
+        assert np.abs(_np(self.qo) - wq).max() <= 2.0 ** -8 * np.abs(wq).max() + 1e-4
+        _within(self.out, want, size * (2.0 ** -8 + 2 * (self.D + 8) * U * score[..., None] + 1e-4) +
+                2.0 ** -8 * np.abs(want))
+        tok, acc = osv.verify(*self.vcase, self.n - 1)
+        np.testing.assert_array_equal(self.tok.cpu().numpy(), tok)
+        np.testing.assert_array_equal(self.acc.cpu().numpy(), acc)
+
+
+def test_a_serving_step(dfl):
+    s = _Step(dfl, 1)
+    s.run()
+    assert dfl.dflash_last_device_error() == 0
+    s.check()
+
+
+def test_two_captured_steps_share_a_workspace_and_replay_on_new_values(dfl):
+    a, b = _Step(dfl, 2), _Step(dfl, 3)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graphs = []
+    with torch.cuda.stream(side):
+        for s in (a, b):
+            s.run(a.ws)
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=side):
+                s.run(a.ws)
+            graphs.append(g)
+        for s in (a, b, a):
+            s.out.zero_()
+            s.tok.zero_()
+            s.qo.zero_()
+            s.q.copy_(_rand(np.random.default_rng(99), s.q.shape, "bf16"))
+            graphs[0 if s is a else 1].replay()
+    side.synchronize()
+    assert dfl.dflash_last_device_error() == 0
+    a.check()
+    b.check()
+    # lengths live on the device: the captured step follows them
+    with torch.cuda.stream(side):
+        a.kv = [x - 1 if x > a.n else x for x in a.kv]
+        a.i[1].copy_(_i32(a.kv))
+        graphs[0].replay()
+    side.synchronize()
+    assert dfl.dflash_last_device_error() == 0
+    a.check()
+
+
+def test_two_streams_at_once(dfl):
+    steps = [_Step(dfl, 20 + i, R=5) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in steps]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, st in zip(steps, streams):
+            with torch.cuda.stream(st):
+                s.run()
+    torch.cuda.synchronize()
+    for s in steps:
+        s.check()
+    explicit = _Step(dfl, 30)
+    torch.cuda.synchronize()
+    dfl.dflash_attn_paged(explicit.qo.copy_(explicit.q), explicit.kc.nan_to_num_(), explicit.vc.nan_to_num_(),
+                          *explicit.i, explicit.n, causal=False, out=explicit.out, stream=torch.cuda.current_stream())
+    torch.cuda.synchronize()
+
+
+def test_offsets_beyond_32_bits(dfl):
+    """A cache of more than 2^32 elements whose used pages lie at its end."""
+    P, Hkv, D = 64, 8, 128
+    num = (1 << 32) // (P * Hkv * D) + 5
+    kc = torch.empty((num, P, Hkv, D), dtype=torch.bfloat16, device="cuda")
+    vc = torch.empty_like(kc)
+    rng = np.random.default_rng(13)
+    pages = [num - 1, num - 3, 0]
+    for c in (kc, vc):
+        for p in pages:
+            c[p] = _rand(rng, (P, Hkv, D), "bf16")
+    k, v = _rand(rng, (4, Hkv, D), "bf16"), _rand(rng, (4, Hkv, D), "bf16")
+    table, kv, off = np.array([pages]), [2 * P + 30], np.array([0, 4])
+    dfl.dflash_cache_append(k, v, kc, vc, _i32(table), _i32([P - 10]), _i32(off))
+    assert torch.equal(kc[num - 1, P - 14:P - 10], k) and torch.equal(vc[num - 1, P - 14:P - 10], v)
+    q = _rand(rng, (4, 16, D), "bf16")
+    out = dfl.dflash_attn_paged(q, kc, vc, _i32(table), _i32(kv), _i32(off), 4)
+    small = [c[pages] for c in (kc, vc)]
+    want, _, size, score = osv.attn_paged(_np(q), _np(small[0]), _np(small[1]), [[0, 1, 2]], kv, off, True)
+    _within(out, want, size * (2.0 ** -8 + 2 * (D + 8) * U * score[..., None] + 1e-4) + 2.0 ** -8 * np.abs(want))
