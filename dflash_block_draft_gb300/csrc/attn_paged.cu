@@ -17,6 +17,8 @@
 // 4 D multiply-adds for each row and 8 D bytes of a position, so it is bound by
 // the multiply-adds from about 10 rows on and by memory below.
 #include <math.h>
+#include <stdlib.h>
+#include <string.h>
 
 #include "paged.cuh"
 
@@ -345,8 +347,31 @@ cudaError_t pick_simt(const PagedArgs& a, int sms, int* grid, cudaStream_t s) {
 
 int simt_rows(int G, int max_q) { return (long long)G * max_q <= 16 ? 16 : 64; }
 
-constexpr size_t kPart = 256;
-size_t up(size_t x) { return (x + kPart - 1) / kPart * kPart; }
+// DFLASH_FORCE_SIMT=1 (tests) routes every call to the CUDA-core kernel.
+bool use_tensor_cores(bool bf16, int G, int D, int P) {
+  const char* v = getenv("DFLASH_FORCE_SIMT");
+  return bf16 && paged_tc_supported(G, D, P) && !(v && v[0] && strcmp(v, "0") != 0);
+}
+
+// Workspace: [meta | (m, l) | O], for the most CTAs a launch has.
+struct PagedPlan {
+  bool tc;
+  int rows, max_grid;
+  size_t ml, o, total;
+};
+PagedPlan plan_of(bool bf16, int Hq, int Hkv, int D, int max_q, int P) {
+  PagedPlan p;
+  const int G = Hq / Hkv;
+  p.tc = use_tensor_cores(bf16, G, D, P);
+  p.rows = p.tc ? paged_tc_rows(G, max_q) : simt_rows(G, max_q);
+  p.max_grid = p.tc ? kSms : kSimtMaxGrid;
+  const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  const size_t slots = 2 * (size_t)p.max_grid * p.rows;
+  p.ml = up(kSimtMaxGrid * sizeof(int4));
+  p.o = p.ml + up(slots * sizeof(float2));
+  p.total = p.o + up(slots * D * sizeof(float));
+  return p;
+}
 
 }  // namespace
 }  // namespace paged
@@ -354,31 +379,32 @@ size_t up(size_t x) { return (x + kPart - 1) / kPart * kPart; }
 using namespace paged;
 
 size_t paged_workspace_bytes(bool bf16, int Hq, int Hkv, int D, int max_q, int P) {
-  const int G = Hq / Hkv;
-  const size_t slots = 2 * kSimtMaxGrid, rows = simt_rows(G, max_q);
-  (void)bf16;
-  (void)P;
-  return up(kSimtMaxGrid * sizeof(int4)) + up(slots * rows * sizeof(float2)) + up(slots * rows * D * sizeof(float));
+  return plan_of(bf16, Hq, Hkv, D, max_q, P).total;
 }
 
 cudaError_t launch_attn_paged(PagedArgs a, bool bf16, void* ws, cudaStream_t stream) {
   int sms = sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
   if (sms > kSms) sms = kSms;
-  a.rows = simt_rows(a.G, a.max_q);
-  const size_t slots = 2 * kSimtMaxGrid;
+  const PagedPlan p = plan_of(bf16, a.Hq, a.Hkv, a.D, a.max_q, a.P);
+  a.rows = p.rows;
   uint8_t* w = static_cast<uint8_t*>(ws);
   a.meta = reinterpret_cast<int4*>(w);
-  w += up(kSimtMaxGrid * sizeof(int4));
-  a.part_ml = reinterpret_cast<float2*>(w);
-  w += up(slots * a.rows * sizeof(float2));
-  a.part_o = reinterpret_cast<float*>(w);
-  int grid = 0;
+  a.part_ml = reinterpret_cast<float2*>(w + p.ml);
+  a.part_o = reinterpret_cast<float*>(w + p.o);
+  int grid = sms;
   cudaError_t e;
-  if (a.rows == 16)
-    e = bf16 ? pick_simt<__nv_bfloat16, 16>(a, sms, &grid, stream) : pick_simt<float, 16>(a, sms, &grid, stream);
-  else
-    e = bf16 ? pick_simt<__nv_bfloat16, 64>(a, sms, &grid, stream) : pick_simt<float, 64>(a, sms, &grid, stream);
+  // Without a page there is no tensor to describe to TMA: the CUDA-core kernel with
+  // its small row tiles (2 x 152 CTAs x 16 rows fit the 152 x 65 or more planned).
+  if (p.tc && a.num_pages > 0) {
+    e = launch_paged_tc(a, grid, stream);
+  } else {
+    if (p.tc) a.rows = 16;
+    if (a.rows == 16)
+      e = bf16 ? pick_simt<__nv_bfloat16, 16>(a, sms, &grid, stream) : pick_simt<float, 16>(a, sms, &grid, stream);
+    else
+      e = bf16 ? pick_simt<__nv_bfloat16, 64>(a, sms, &grid, stream) : pick_simt<float, 64>(a, sms, &grid, stream);
+  }
   if (e != cudaSuccess) return e;
   const dim3 mg(grid, (a.rows + 3) / 4);
   if (bf16) paged_merge_kernel<__nv_bfloat16><<<mg, 128, 0, stream>>>(a);

@@ -211,5 +211,11 @@ struct Walker {
 // What the merge kernel needs about CTA c: the row tile that it begins and leaves cut.
 __device__ __forceinline__ int4 pack_meta(const Piece& p) { return make_int4(p.shared, p.r, p.h, p.rt); }
 
+// The tensor-core kernel (attn_paged_tc.cu): which shapes it takes, the rows of its
+// row tiles, and its launch over `grid` CTAs.
+bool paged_tc_supported(int G, int D, int P);
+int paged_tc_rows(int G, int max_q);
+cudaError_t launch_paged_tc(const PagedArgs& a, int grid, cudaStream_t stream);
+
 }  // namespace paged
 }  // namespace dflash

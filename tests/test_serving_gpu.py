@@ -272,6 +272,17 @@ def test_attn_paged(dfl, kv, n, P, Hq, Hkv, D, dtype, causal):
     _check_attn(dfl, np.random.default_rng(sum(kv) + D), kv, n, P, Hq, Hkv, D, dtype, causal)
 
 
+@pytest.mark.parametrize("dtype,n,Hq,Hkv,D,P", [("bf16", 1, 8, 4, 128, 64), ("bf16", 3, 8, 4, 64, 16),
+                                                ("bf16", 40, 16, 4, 128, 16), ("bf16", 70, 4, 2, 64, 48),
+                                                ("fp32", 1, 4, 4, 64, 16)])
+def test_attn_paged_many_row_tiles_a_cta(dfl, dtype, n, Hq, Hkv, D, P):
+    """More row tiles than CTAs: a CTA goes through several, with odd and even numbers of key tiles."""
+    rng = np.random.default_rng(n + D)
+    R = 260 if n < 10 else 40
+    kv = [int(x) for x in n + rng.integers(0, 700 if n < 10 else 500, R)]
+    _check_attn(dfl, rng, kv, [n] * R, P, Hq, Hkv, D, dtype, True)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_attn_paged_halves_of_one_cache_scale_and_loose_bound(dfl, dtype):
     _check_attn(dfl, np.random.default_rng(5), [100, 333], [16, 3], 16, 8, 2, 128, dtype, True, layout="halves",
@@ -324,6 +335,26 @@ def test_attn_paged_bad_pages_and_bad_requests(dfl, dtype, P):
     dfl.dflash_attn_paged(q, kc, vc, _i32(table), _i32(kv), _i32([0, 2, 1, T + 5, 9]), 3, out=out)
     assert dfl.dflash_last_device_error() == INVALID
     assert (out[off[1]:] == 7).all() and not (out[:2] == 7).any()
+
+
+@pytest.mark.parametrize("kv,n,P,Hq,Hkv,D", ATTN[3:8])
+def test_attn_paged_bf16_on_the_cuda_cores(dfl, monkeypatch, kv, n, P, Hq, Hkv, D):
+    monkeypatch.setenv("DFLASH_FORCE_SIMT", "1")
+    _check_attn(dfl, np.random.default_rng(D), kv, n, P, Hq, Hkv, D, "bf16", True)
+
+
+def test_attn_paged_without_a_page(dfl):
+    """A cache of no pages: requests without positions get zeros; a table entry has nothing to name."""
+    cache = torch.empty((0, 16, 2, 64), dtype=torch.bfloat16, device="cuda")
+    q = torch.ones((3, 4, 64), dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty((4, 3), device="cuda")
+    out = dfl.dflash_attn_paged(q, cache, cache, _i32([[0], [0]]), _i32([0, 5]), _i32([0, 2, 3]), 2, causal=False,
+                                lse=lse)
+    assert dfl.dflash_last_device_error() == INVALID  # the second request's page
+    assert (out == 0).all() and torch.isneginf(lse[:, :2]).all()
+    # five keys of zeros: every score 0, so the sum is 5
+    assert torch.allclose(lse[:, 2].double(), torch.full((4,), np.log(5.0), dtype=torch.float64, device="cuda"),
+                          atol=2.0 ** -20)
 
 
 # ------------------------------------------------------------------ append
