@@ -82,6 +82,8 @@ _lib_handle = None
 def load_library(path: str | None = None):
     """Load libdflash_attn.so (built by ``__graft_entry__.build()``); raises if absent."""
     global _lib_handle
+    if _lib_handle is not None:
+        return _lib_handle
     with _lock:
         if _lib_handle is not None:
             return _lib_handle
@@ -426,73 +428,63 @@ def dflash_attn_dense_backward(q, k_nope, k_rope, v, mask, out, lse, dout, grads
 # ---------------------------------------------------------------------------
 # the grouped-query draft's serving step
 # ---------------------------------------------------------------------------
-class _On:
-    """Launches on a tensor's device, whichever is current: the stream handle to
-    launch on, with the current device switched where it is another one."""
-
-    __slots__ = ("guard", "stream")
-
-    def __init__(self, device, stream):
-        torch = _torch()
-        cuda = torch.cuda
-        self.guard = cuda.device(device) if cuda.current_device() != device.index else None
-        if stream is None:
-            stream = cuda.current_stream(device)
-        self.stream = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self.stream
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+# These calls are short (a few microseconds on the device), so what the binding
+# checks it checks with the cheapest tensor methods, and says what is wrong only
+# once something is.
+def _call(name, fn, index, stream, *args):
+    """fn(*args, stream handle) with device `index` current; raises on a status."""
+    torch = _torch()
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(index)
+    else:
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if torch._C._cuda_getDevice() == index:
+        rc = fn(*args, handle)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, handle)
+    if rc:
+        raise DFlashError(name, rc)
 
 
-def _arg(t, name, device, dtype, shape=None):
-    """Data pointer of a contiguous CUDA tensor on `device`, checked; None for None."""
-    if t is None:
-        return None
-    if t.device != device or device.type != "cuda":
-        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+def _refuse(t, name, index, dtype, shape, form):
+    if t.device.type != "cuda" or t.get_device() != index:
+        raise ValueError(f"{name} must be a CUDA tensor" + (f" on device {index}" if index >= 0 else ""))
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    raise ValueError(f"{name} must be contiguous" if form is None else form)
+
+
+def _arg(t, name, index, dtype, shape=None):
+    """Data pointer of a contiguous tensor on CUDA device `index`, checked; None for None."""
+    if t is None:
+        return None
+    if not (t.is_cuda and t.get_device() == index and t.dtype is dtype and t.is_contiguous() and
+            (shape is None or t.shape == shape)):
+        _refuse(t, name, index, dtype, shape, None)
     return t.data_ptr()
 
 
-def _token_arg(t, name, device, dtype, shape):
+def _token_arg(t, name, index, dtype, shape):
     """Data pointer and token stride of [tokens, heads, D] whose tokens are each contiguous."""
-    if t.device != device or device.type != "cuda":
-        raise ValueError(f"{name} must be a CUDA tensor on {device}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    T, H, D = shape
-    s = t.stride()
-    if (D > 1 and s[2] != 1) or (H > 1 and s[1] != D) or (T > 1 and s[0] < H * D):
-        raise ValueError(f"the heads of a token of {name} must be contiguous")
-    return t.data_ptr(), s[0] if T > 1 else 0
+    if t.is_cuda and t.get_device() == index and t.dtype is dtype and t.shape == shape:
+        T, H, D = shape
+        s0, s1, s2 = t.stride()
+        if (s2 == 1 or D <= 1) and (s1 == D or H <= 1) and (s0 >= H * D or T <= 1):
+            return t.data_ptr(), s0 if T > 1 else 0
+    _refuse(t, name, index, dtype, shape, f"the heads of a token of {name} must be contiguous")
 
 
-def _cache_arg(t, name, device, dtype, shape):
+def _cache_arg(t, name, index, dtype, shape):
     """Data pointer and page stride of [pages, page_size, H_kv, D] whose pages are each contiguous."""
-    if t.device != device or device.type != "cuda":
-        raise ValueError(f"{name} must be a CUDA tensor on {device}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    n, P, H, D = shape
-    s = t.stride()
-    if (D > 1 and s[3] != 1) or (H > 1 and s[2] != D) or (P > 1 and s[1] != H * D) or (n > 1 and s[0] < P * H * D):
-        raise ValueError(f"the pages of {name} must be contiguous")
-    return t.data_ptr(), s[0] if n > 1 else 0
+    if t.is_cuda and t.get_device() == index and t.dtype is dtype and t.shape == shape:
+        n, P, H, D = shape
+        s0, s1, s2, s3 = t.stride()
+        if (s3 == 1 or D <= 1) and (s2 == D or H <= 1) and (s1 == H * D or P <= 1) and (s0 >= P * H * D or n <= 1):
+            return t.data_ptr(), s0 if n > 1 else 0
+    _refuse(t, name, index, dtype, shape, f"the pages of {name} must be contiguous")
 
 
 def _rope_args(q, k, positions, cos_sin):
@@ -503,12 +495,15 @@ def _rope_args(q, k, positions, cos_sin):
     if one.dim() != 3:
         raise ValueError("q and k must be [tokens, heads, D]")
     T, _, D = one.shape
-    dev = one.device
-    Hq, Hk = (0 if t is None else t.shape[1] for t in (q, k))
-    rot, max_pos = (0, 0) if cos_sin is None else (cos_sin.shape[1], cos_sin.shape[0])
+    dev = one.get_device()
+    Hq, Hk = 0 if q is None else q.shape[1], 0 if k is None else k.shape[1]
+    if cos_sin is None:
+        return one.dtype, dev, T, Hq, Hk, D, 0, 0, None, None
+    if positions is None or cos_sin.dim() != 2:
+        raise ValueError("cos_sin must be [max_pos, rot_dim] and comes with positions")
+    max_pos, rot = cos_sin.shape
     cs = _arg(cos_sin, "cos_sin", dev, torch.float32)
-    ps = None if cos_sin is None else _arg(positions, "positions", dev, torch.int32, (T,))
-    return one.dtype, dev, T, Hq, Hk, D, rot, max_pos, cs, ps
+    return one.dtype, dev, T, Hq, Hk, D, rot, max_pos, cs, _arg(positions, "positions", dev, torch.int32, (T,))
 
 
 def dflash_qk_norm_rope(q, k, positions, cos_sin, q_norm=None, k_norm=None, eps=1e-6, interleaved=False, q_out=None,
@@ -523,17 +518,18 @@ def dflash_qk_norm_rope(q, k, positions, cos_sin, q_norm=None, k_norm=None, eps=
     code = _dtype_code(q if q is not None else k)
     qp, qs = (None, 0) if q is None else _token_arg(q, "q", dev, dt, (T, Hq, D))
     kp, ks = (None, 0) if k is None else _token_arg(k, "k", dev, dt, (T, Hk, D))
-    if q_out is None and q is not None:
-        q_out = torch.empty((T, Hq, D), dtype=dt, device=dev)
-    if k_out is None and k is not None:
-        k_out = torch.empty((T, Hk, D), dtype=dt, device=dev)
+    if q is None:
+        q_out = None
+    elif q_out is None:
+        q_out = torch.empty((T, Hq, D), dtype=dt, device=q.device)
+    if k is None:
+        k_out = None
+    elif k_out is None:
+        k_out = torch.empty((T, Hk, D), dtype=dt, device=k.device)
     d = _RopeDims(T, Hq, Hk, D, rot, max_pos, int(interleaved), eps, qs, ks)
-    with _On(dev, stream) as st:
-        rc = lib.dflash_qk_norm_rope(d, code, qp, kp, _arg(q_norm, "q_norm", dev, dt, (D,)),
-                                     _arg(k_norm, "k_norm", dev, dt, (D,)), cs, ps,
-                                     _arg(q_out, "q_out", dev, dt, (T, Hq, D)),
-                                     _arg(k_out, "k_out", dev, dt, (T, Hk, D)), st)
-    _check("dflash_qk_norm_rope", rc)
+    _call("dflash_qk_norm_rope", lib.dflash_qk_norm_rope, dev, stream, d, code, qp, kp,
+          _arg(q_norm, "q_norm", dev, dt, (D,)), _arg(k_norm, "k_norm", dev, dt, (D,)), cs, ps,
+          _arg(q_out, "q_out", dev, dt, (T, Hq, D)), _arg(k_out, "k_out", dev, dt, (T, Hk, D)))
     return q_out, k_out
 
 
@@ -548,24 +544,23 @@ def dflash_qk_norm_rope_backward(q, k, positions, cos_sin, dq_out, dk_out, q_nor
     code = _dtype_code(q if q is not None else k)
     qp, qs = (None, 0) if q is None else _token_arg(q, "q", dev, dt, (T, Hq, D))
     kp, ks = (None, 0) if k is None else _token_arg(k, "k", dev, dt, (T, Hk, D))
+    device = (q if q is not None else k).device
     if grads is None:
-        grads = (None if q is None else torch.empty((T, Hq, D), dtype=dt, device=dev),
-                 None if k is None else torch.empty((T, Hk, D), dtype=dt, device=dev),
-                 None if q_norm is None else torch.empty(D, dtype=torch.float32, device=dev),
-                 None if k_norm is None else torch.empty(D, dtype=torch.float32, device=dev))
+        grads = (None if q is None else torch.empty((T, Hq, D), dtype=dt, device=device),
+                 None if k is None else torch.empty((T, Hk, D), dtype=dt, device=device),
+                 None if q_norm is None else torch.empty(D, dtype=torch.float32, device=device),
+                 None if k_norm is None else torch.empty(D, dtype=torch.float32, device=device))
     dq, dk, dwq, dwk = grads
     d = _RopeDims(T, Hq, Hk, D, rot, max_pos, int(interleaved), eps, qs, ks)
     nbytes = int(lib.dflash_qk_norm_rope_workspace_size(d))
-    ws = _workspace(nbytes, workspace, dev)
-    with _On(dev, stream) as st:
-        rc = lib.dflash_qk_norm_rope_backward(
-            d, code, qp, kp, _arg(q_norm, "q_norm", dev, dt, (D,)), _arg(k_norm, "k_norm", dev, dt, (D,)), cs, ps,
-            _arg(dq_out if q is not None else None, "dq_out", dev, dt, (T, Hq, D)),
-            _arg(dk_out if k is not None else None, "dk_out", dev, dt, (T, Hk, D)),
-            _arg(dq, "dq", dev, dt, (T, Hq, D)), _arg(dk, "dk", dev, dt, (T, Hk, D)),
-            _arg(dwq, "dq_norm", dev, torch.float32, (D,)), _arg(dwk, "dk_norm", dev, torch.float32, (D,)),
-            _arg(ws, "workspace", dev, ws.dtype), nbytes, st)
-    _check("dflash_qk_norm_rope_backward", rc)
+    ws = _workspace(nbytes, workspace, device)
+    _call("dflash_qk_norm_rope_backward", lib.dflash_qk_norm_rope_backward, dev, stream, d, code, qp, kp,
+          _arg(q_norm, "q_norm", dev, dt, (D,)), _arg(k_norm, "k_norm", dev, dt, (D,)), cs, ps,
+          _arg(dq_out if q is not None else None, "dq_out", dev, dt, (T, Hq, D)),
+          _arg(dk_out if k is not None else None, "dk_out", dev, dt, (T, Hk, D)),
+          _arg(dq, "dq", dev, dt, (T, Hq, D)), _arg(dk, "dk", dev, dt, (T, Hk, D)),
+          _arg(dwq, "dq_norm", dev, torch.float32, (D,)), _arg(dwk, "dk_norm", dev, torch.float32, (D,)),
+          _arg(ws, "workspace", dev, ws.dtype), nbytes)
     return dq, dk, dwq, dwk
 
 
@@ -594,7 +589,7 @@ def dflash_cache_append(k, v, k_cache, v_cache, page_table, kv_lens, q_offsets, 
     its heads are normed and rotated too; returns q_out (None without q)."""
     torch = _torch()
     lib = load_library()
-    dt, dev = k.dtype, k.device
+    dt, dev = k.dtype, k.get_device()
     code = _dtype_code(k)
     (n, P, Hk, D), R, max_pages, kcp, kcs, vcp, vcs, tp, lp, op = _paged_args(k_cache, v_cache, page_table, kv_lens,
                                                                               q_offsets, dt, dev)
@@ -608,18 +603,16 @@ def dflash_cache_append(k, v, k_cache, v_cache, page_table, kv_lens, q_offsets, 
         Hq = q.shape[1]
         qp, qs = _token_arg(q, "q", dev, dt, (T, Hq, D))
         if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=dt, device=dev)
+            q_out = torch.empty((T, Hq, D), dtype=dt, device=q.device)
     else:
         q_out = None
-    rot, max_pos = (0, 0) if cos_sin is None else (cos_sin.shape[1], cos_sin.shape[0])
+    max_pos, rot = (0, 0) if cos_sin is None else cos_sin.shape
     pd = _PagedDims(R, Hq, Hk, D, T, 0, n, P, max_pages, kcs, vcs)
     rd = _RopeDims(T, Hq, Hk, D, rot, max_pos, int(interleaved), eps, qs, ks)
-    with _On(dev, stream) as st:
-        rc = lib.dflash_cache_append(pd, rd, code, qp, kp, vp, vs, _arg(q_norm, "q_norm", dev, dt, (D,)),
-                                     _arg(k_norm, "k_norm", dev, dt, (D,)),
-                                     _arg(cos_sin, "cos_sin", dev, torch.float32), tp, lp, op,
-                                     _arg(q_out, "q_out", dev, dt, (T, Hq, D)), kcp, vcp, st)
-    _check("dflash_cache_append", rc)
+    _call("dflash_cache_append", lib.dflash_cache_append, dev, stream, pd, rd, code, qp, kp, vp, vs,
+          _arg(q_norm, "q_norm", dev, dt, (D,)), _arg(k_norm, "k_norm", dev, dt, (D,)),
+          _arg(cos_sin, "cos_sin", dev, torch.float32), tp, lp, op, _arg(q_out, "q_out", dev, dt, (T, Hq, D)), kcp,
+          vcp)
     return q_out
 
 
@@ -636,7 +629,7 @@ def dflash_attn_paged(q, k_cache, v_cache, page_table, kv_lens, q_offsets, max_q
     the token's own.  Returns out [total_q,H_q,D]; fills lse [H_q,total_q] fp32 if given."""
     torch = _torch()
     lib = load_library()
-    dt, dev = q.dtype, q.device
+    dt, dev = q.dtype, q.get_device()
     code = _dtype_code(q)
     if q.dim() != 3:
         raise ValueError("q must be [total_q, H_q, D]")
@@ -645,16 +638,13 @@ def dflash_attn_paged(q, k_cache, v_cache, page_table, kv_lens, q_offsets, max_q
                                                                               q_offsets, dt, dev)
     qp = _arg(q, "q", dev, dt, (T, Hq, D))
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=dt, device=dev)
+        out = torch.empty((T, Hq, D), dtype=dt, device=q.device)
     d = _PagedDims(R, Hq, Hk, D, T, int(max_q_len), n, P, max_pages, kcs, vcs)
-    nbytes = int(lib.dflash_attn_paged_workspace_size(d, code))
-    ws = _workspace(nbytes, workspace, dev)
-    with _On(dev, stream) as st:
-        rc = lib.dflash_attn_paged(d, code, qp, kcp, vcp, tp, lp, op, int(causal), float(scale or 0.0),
-                                   _arg(out, "out", dev, dt, (T, Hq, D)),
-                                   _arg(lse, "lse", dev, torch.float32, (Hq, T)),
-                                   _arg(ws, "workspace", dev, ws.dtype), nbytes, st)
-    _check("dflash_attn_paged", rc)
+    nbytes = lib.dflash_attn_paged_workspace_size(d, code)
+    ws = _workspace(nbytes, workspace, q.device)
+    _call("dflash_attn_paged", lib.dflash_attn_paged, dev, stream, d, code, qp, kcp, vcp, tp, lp, op, int(causal),
+          float(scale or 0.0), _arg(out, "out", dev, dt, (T, Hq, D)),
+          _arg(lse, "lse", dev, torch.float32, (Hq, T)), _arg(ws, "workspace", dev, ws.dtype), nbytes)
     return out
 
 
@@ -668,35 +658,33 @@ def dflash_verify(target_probs, draft_probs, draft_tokens, draft_offsets, accept
     accepted tokens, the drawn one, then -1) and num_accepted [R], int32."""
     torch = _torch()
     lib = load_library()
-    dev, f32, i32 = target_probs.device, torch.float32, torch.int32
+    dev, f32, i32 = target_probs.get_device(), torch.float32, torch.int32
     if target_probs.dim() != 2 or target_probs.stride(1) != 1 or draft_offsets.dim() != 1:
         raise ValueError("target_probs must be [rows, V] with contiguous rows, draft_offsets [R + 1]")
     rows, V = target_probs.shape
     T, R = draft_tokens.shape[0], draft_offsets.shape[0] - 1
     if rows < T + R:
         raise ValueError("target_probs needs a row for every drafted token and one more for every request")
-    if target_probs.device.type != "cuda" or target_probs.dtype != f32:
+    if not target_probs.is_cuda or target_probs.dtype is not f32:
         raise ValueError("target_probs must be a float32 CUDA tensor")
     ps, qp, qs = target_probs.stride(0) if rows > 1 else 0, None, 0
     if draft_probs is not None:
-        if draft_probs.shape != (T, V) or draft_probs.dtype != f32 or draft_probs.device != dev or (
-                V > 1 and draft_probs.stride(1) != 1):
+        if (draft_probs.shape != (T, V) or draft_probs.dtype is not f32 or draft_probs.get_device() != dev or
+                (V > 1 and draft_probs.stride(1) != 1)):
             raise ValueError("draft_probs must be a float32 [total_draft, V] tensor with contiguous rows on the "
                              "device of target_probs")
         if T > 0:
             qp, qs = draft_probs.data_ptr(), draft_probs.stride(0) if T > 1 else 0
     if out_tokens is None:
-        out_tokens = torch.empty((R, max_draft + 1), dtype=i32, device=dev)
+        out_tokens = torch.empty((R, max_draft + 1), dtype=i32, device=target_probs.device)
     if num_accepted is None:
-        num_accepted = torch.empty(R, dtype=i32, device=dev)
+        num_accepted = torch.empty(R, dtype=i32, device=target_probs.device)
     d = _VerifyDims(R, V, T, int(max_draft), ps, qs)
-    with _On(dev, stream) as st:
-        rc = lib.dflash_verify(d, target_probs.data_ptr(), qp, _arg(draft_tokens, "draft_tokens", dev, i32, (T,)),
-                               _arg(draft_offsets, "draft_offsets", dev, i32),
-                               _arg(accept_u, "accept_u", dev, f32, (T,)), _arg(sample_u, "sample_u", dev, f32, (R,)),
-                               _arg(out_tokens, "out_tokens", dev, i32, (R, max_draft + 1)),
-                               _arg(num_accepted, "num_accepted", dev, i32, (R,)), st)
-    _check("dflash_verify", rc)
+    _call("dflash_verify", lib.dflash_verify, dev, stream, d, target_probs.data_ptr(), qp,
+          _arg(draft_tokens, "draft_tokens", dev, i32, (T,)), _arg(draft_offsets, "draft_offsets", dev, i32),
+          _arg(accept_u, "accept_u", dev, f32, (T,)), _arg(sample_u, "sample_u", dev, f32, (R,)),
+          _arg(out_tokens, "out_tokens", dev, i32, (R, max_draft + 1)),
+          _arg(num_accepted, "num_accepted", dev, i32, (R,)))
     return out_tokens, num_accepted
 
 

@@ -53,7 +53,7 @@ dflash_status_t check_rope(const dflash_rope_dims_t* d, dflash_dtype_t dtype, co
   TRY(check_dtype(dtype));
   if (!d) return DFLASH_ERR_INVALID;
   if (d->T < 0 || d->H_q < 0 || d->H_kv < 0) return DFLASH_ERR_SHAPE;
-  if (d->H_q > 65535 || d->H_kv > 65535) return DFLASH_ERR_UNSUPPORTED;
+  if (d->H_q > 65535 || d->H_kv > 65535 || d->T >= 1 << 30) return DFLASH_ERR_UNSUPPORTED;
   TRY(check_head(d->D));
   memset(a, 0, sizeof *a);
   a->T = d->T;

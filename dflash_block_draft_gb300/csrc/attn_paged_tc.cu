@@ -32,6 +32,8 @@
 // wait is bounded (DFLASH_ERR_TIMEOUT, CTA abort flag, wind-down).
 #include <math.h>
 
+#include <atomic>
+
 #include "paged.cuh"
 #include "ptx.cuh"
 #include "tc_common.cuh"
@@ -565,13 +567,22 @@ template <int NP, bool PAIR>
 cudaError_t run_tc(const TcPagedArgs& ta, int grid, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                    cudaStream_t s) {
   auto kernel = paged_tc_kernel<NP, PAIR>;
-  // The setmaxnreg split assumes the kernel launches with exactly kLaunchRegs
-  // registers a thread; any other count would make setmaxnreg.inc wait forever.
-  cudaFuncAttributes fa;
-  if (cudaFuncGetAttributes(&fa, kernel) != cudaSuccess || fa.numRegs != kLaunchRegs)
-    return cudaErrorInvalidConfiguration;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg<NP, PAIR>::kSmem);
+  // Once a device: the shared memory's size, and the registers.  The setmaxnreg
+  // split assumes the kernel launches with exactly kLaunchRegs registers a thread;
+  // any other count would make setmaxnreg.inc wait forever.
+  static std::atomic<uint64_t> ready{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev >= 64 || !(ready.load(std::memory_order_acquire) & bit)) {
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, kernel) != cudaSuccess || fa.numRegs != kLaunchRegs)
+      return cudaErrorInvalidConfiguration;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg<NP, PAIR>::kSmem);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit, std::memory_order_release);
+  }
   kernel<<<grid, kThreads, Cfg<NP, PAIR>::kSmem, s>>>(ta, q, k, v);
   count_launch();
   return cudaGetLastError();

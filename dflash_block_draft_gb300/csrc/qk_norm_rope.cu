@@ -4,16 +4,15 @@
 //   y = x (mean x^2 + eps)^-1/2 w,   out = Rot(pos) y
 //   backward: g = Rot(pos)^T dout, dw = sum g x^, dx = r (g w - x^ mean(g w x^))
 //
-// All of it is bound by memory: about ten operations a component against 4 (bf16,
-// in and out) to 12 bytes.  So a head is held in the registers of a group of 8,
-// 16 or 32 lanes, each with one or two 16-byte vectors of it: the mean is a
-// shuffle reduction inside the group, the partner component of a plane in the
-// other half of the head comes by one shuffle, and nothing goes through shared
-// memory.  A group takes several heads of ONE token, so that the token's cosines
-// and sines (as many bytes in fp32 as two bf16 heads) are read once and stay in
-// registers, and the heads' loads are in flight together.
-// Head shapes whose planes cut through the vectors, and misaligned tensors, run
-// on a plain kernel with a warp for each head and its row in shared memory.
+// All of it is bound by memory: ten to twenty operations a component against 4
+// (bf16, in and out) to 12 bytes.  A head lies in the registers of a group of 8, 16
+// or 32 lanes, 8 components a lane: with planes (i, i + rot/2) the 4 components
+// at 4 c and the 4 at rot/2 + 4 c, so that every plane is whole inside a lane and
+// its 4 cosines and sines serve both; with planes (2 i, 2 i + 1) eight in a row.
+// Only the mean goes through shuffles.  (A first form with 16-byte vectors and the
+// partner components by shuffle needed twice the cosines and 8 shuffles a head.)
+// Head shapes whose planes cut through these vectors (rot % 8 != 0), and
+// misaligned tensors, run on a plain kernel with a warp for each head.
 #include "common.cuh"
 #include "internal.h"
 
@@ -22,126 +21,86 @@ namespace {
 
 constexpr int kThreads = 256;
 
-template <typename T, int VEC>
-struct alignas(sizeof(T) * VEC) Vec {
-  T e[VEC];
-};
-
-template <typename T, int VEC>
-__device__ __forceinline__ void load_vec(const T* p, float* x) {
-  const Vec<T, VEC> v = *reinterpret_cast<const Vec<T, VEC>*>(p);
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) x[i] = to_f32(v.e[i]);
-}
-
-template <typename T, int VEC>
-__device__ __forceinline__ void store_vec(T* p, const float* x) {
-  Vec<T, VEC> v;
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) v.e[i] = from_f32<T>(x[i]);
-  *reinterpret_cast<Vec<T, VEC>*>(p) = v;
-}
-
-// Where a token goes: its position and, for a paged call, the element offsets of
-// its cache rows.  False: the token is skipped.
-struct Place {
-  int pos;
-  long long krow, vrow;
-};
-
-template <bool PAGED>
-__device__ __forceinline__ bool place_token(const RopeArgs& a, int t, Place* pl) {
-  if (!PAGED) {
-    pl->pos = a.rot > 0 ? a.pos[t] : 0;
-    if (a.rot > 0 && (pl->pos < 0 || pl->pos >= a.max_pos)) {
-      record_error(a.err, DFLASH_ERR_INVALID);
-      return false;
-    }
-    return true;
+// Four components as they lie in memory.
+template <typename T>
+struct Raw;
+template <>
+struct Raw<__nv_bfloat16> {
+  uint2 v;
+  __device__ __forceinline__ void unpack(float* x) const {
+    x[0] = __uint_as_float(v.x << 16);
+    x[1] = __uint_as_float(v.x & 0xFFFF0000u);
+    x[2] = __uint_as_float(v.y << 16);
+    x[3] = __uint_as_float(v.y & 0xFFFF0000u);
   }
-  if (t >= a.q_off[a.R]) return false;  // padding behind the last request
-  int lo = 0, hi = a.R;
-  while (hi - lo > 1) {  // the last request that begins at or before t
-    const int mid = (lo + hi) >> 1;
-    if (a.q_off[mid] <= t) lo = mid;
-    else hi = mid;
-  }
-  const int q0 = a.q_off[lo], q1 = a.q_off[lo + 1];
-  const long long p = (long long)a.kv_lens[lo] - (q1 - q0) + (t - q0);
-  if (q0 < 0 || q0 > t || q1 <= t || q1 > a.T || p < 0 || p >= (long long)a.max_pages * a.P ||
-      (a.rot > 0 && p >= a.max_pos)) {
-    record_error(a.err, DFLASH_ERR_INVALID);
-    return false;
-  }
-  const int page = a.table[(long long)lo * a.max_pages + p / a.P];
-  if (page < 0 || page >= a.num_pages) {
-    record_error(a.err, DFLASH_ERR_INVALID);
-    return false;
-  }
-  pl->pos = (int)p;
-  const long long row = (p % a.P) * (long long)a.Hkv * a.D;
-  pl->krow = page * a.kps + row;
-  pl->vrow = page * a.vps + row;
-  return true;
-}
-
-// A lane's components of a head: VPL vectors of VEC, vector j at chunk lane + LANES j.
-template <int VEC, int LANES, int VPL>
-struct Rotor {
-  float cos[VPL][VEC], sin[VPL][VEC];  // sin carries the sign of the component
-  int mate[VPL];                       // chunk that holds the partner components (half-split planes)
-  bool turned[VPL];
-
-  __device__ __forceinline__ void load(const RopeArgs& a, int pos, int lane, bool active) {
-    const int h = a.rot >> 1;
-    const float* row = a.cs + (long long)pos * a.rot;
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) {
-      const int d = (lane + LANES * j) * VEC;
-      turned[j] = active && d < a.rot;
-      const bool second = !a.interleaved && d >= h;
-      mate[j] = !turned[j] || a.interleaved ? lane + LANES * j : (second ? d - h : d + h) / VEC;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const int ang = a.interleaved ? (d + e) >> 1 : (second ? d - h : d) + e;
-        cos[j][e] = turned[j] ? row[ang] : 1.f;
-        const float sn = turned[j] ? row[h + ang] : 0.f;
-        const bool first = a.interleaved ? (e & 1) == 0 : !second;
-        sin[j][e] = first ? -sn : sn;
-      }
-    }
-  }
-
-  // x := x rotated (dir = 1) or rotated back (dir = -1).  Whole warp.
-  __device__ __forceinline__ void apply(float (&x)[VPL][VEC], int interleaved, float dir) const {
-    float y[VPL][VEC];
-    if (interleaved) {
-#pragma unroll
-      for (int j = 0; j < VPL; ++j)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) y[j][e] = x[j][e ^ 1];
-    } else {
-#pragma unroll
-      for (int j = 0; j < VPL; ++j)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          if (VPL == 1) {
-            y[j][e] = __shfl_sync(0xffffffffu, x[0][e], mate[0], LANES);
-          } else {
-            const float y0 = __shfl_sync(0xffffffffu, x[0][e], mate[j] % LANES, LANES);
-            const float y1 = __shfl_sync(0xffffffffu, x[VPL - 1][e], mate[j] % LANES, LANES);
-            y[j][e] = mate[j] < LANES ? y0 : y1;
-          }
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < VPL; ++j)
-      if (turned[j]) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) x[j][e] = fmaf(x[j][e], cos[j][e], dir * y[j][e] * sin[j][e]);
-      }
+  __device__ __forceinline__ void pack(const float* x) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
+    v.x = *reinterpret_cast<const uint32_t*>(&a);
+    v.y = *reinterpret_cast<const uint32_t*>(&b);
   }
 };
+template <>
+struct Raw<float> {
+  float4 v;
+  __device__ __forceinline__ void unpack(float* x) const { x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w; }
+  __device__ __forceinline__ void pack(const float* x) { v = make_float4(x[0], x[1], x[2], x[3]); }
+};
+
+// A lane's 8 components of a head: 4 at `a`, 4 at `b`; angles ang .. ang + 3.
+struct LanePart {
+  int a, b, ang;
+  bool in, turned;
+};
+__device__ __forceinline__ LanePart lane_part(const RopeArgs& r, int c) {
+  LanePart p;
+  p.in = 8 * c < r.D;
+  p.turned = 8 * c < r.rot;
+  p.ang = 4 * c;
+  const bool split = p.turned && !r.interleaved;
+  p.a = split ? 4 * c : 8 * c;
+  p.b = split ? 4 * c + (r.rot >> 1) : 8 * c + 4;
+  return p;
+}
+
+template <typename T>
+struct Part {
+  Raw<T> a, b;
+  __device__ __forceinline__ void load(const T* head, const LanePart& p) {
+    a = *reinterpret_cast<const Raw<T>*>(head + p.a);
+    b = *reinterpret_cast<const Raw<T>*>(head + p.b);
+  }
+  __device__ __forceinline__ void store(T* head, const LanePart& p) const {
+    *reinterpret_cast<Raw<T>*>(head + p.a) = a;
+    *reinterpret_cast<Raw<T>*>(head + p.b) = b;
+  }
+  __device__ __forceinline__ void unpack(float* x) const {
+    a.unpack(x);
+    b.unpack(x + 4);
+  }
+  __device__ __forceinline__ void pack(const float* x) {
+    a.pack(x);
+    b.pack(x + 4);
+  }
+};
+
+// x := x rotated; with the sines' signs turned, rotated back.
+__device__ __forceinline__ void rotate8(float* x, const float* cs, const float* sn, int interleaved) {
+  if (interleaved) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float u = x[2 * e], v = x[2 * e + 1];
+      x[2 * e] = u * cs[e] - v * sn[e];
+      x[2 * e + 1] = v * cs[e] + u * sn[e];
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float u = x[e], v = x[4 + e];
+      x[e] = u * cs[e] - v * sn[e];
+      x[4 + e] = v * cs[e] + u * sn[e];
+    }
+  }
+}
 
 template <int LANES>
 __device__ __forceinline__ float group_sum(float v) {
@@ -150,180 +109,262 @@ __device__ __forceinline__ float group_sum(float v) {
   return v;
 }
 
-// A group of LANES takes HPG heads of one token.  Heads count q, then k, then
-// (paged) v.  Work units are [token][head chunk].
-template <typename T, int VEC, int LANES, int VPL, int HPG, bool PAGED>
-__global__ void __launch_bounds__(kThreads) rope_fwd_kernel(const __grid_constant__ RopeArgs a, int nchunk) {
-  const int lane = threadIdx.x % LANES;
-  const long long unit = (long long)blockIdx.x * (kThreads / LANES) + threadIdx.x / LANES;
-  const int t = (int)min(unit / nchunk, (long long)a.T);
-  const int h0 = (int)(unit % nchunk) * HPG;
+// Where a token goes: its position and, for a paged call, the element offsets of
+// its cache rows.
+struct Place {
+  int ok, pos;
+  long long krow, vrow;
+};
+
+// Request lo of token t and the rest of its placement; records what has no place.
+__device__ __forceinline__ Place place_in(const RopeArgs& a, int t, int lo) {
+  Place pl = {0, 0, 0, 0};
+  const int q0 = a.q_off[lo], q1 = a.q_off[lo + 1];
+  const long long p = (long long)a.kv_lens[lo] - (q1 - q0) + (t - q0);
+  if (q0 < 0 || q0 > t || q1 <= t || q1 > a.T || p < 0 || p >= (long long)a.max_pages * a.P ||
+      (a.rot > 0 && p >= a.max_pos)) {
+    record_error(a.err, DFLASH_ERR_INVALID);
+    return pl;
+  }
+  const int page = a.table[(long long)lo * a.max_pages + p / a.P];
+  if (page < 0 || page >= a.num_pages) {
+    record_error(a.err, DFLASH_ERR_INVALID);
+    return pl;
+  }
+  const long long row = (p % a.P) * (long long)a.Hkv * a.D;
+  pl.ok = 1;
+  pl.pos = (int)p;
+  pl.krow = page * a.kps + row;
+  pl.vrow = page * a.vps + row;
+  return pl;
+}
+
+// Whole warp: the placement of token t (the same in every lane).  The request is
+// found 32 offsets at a time.
+template <bool PAGED>
+__device__ __forceinline__ Place place_token(const RopeArgs& a, int t) {
+  Place pl = {0, 0, 0, 0};
+  if (t >= a.T) return pl;
+  if (!PAGED) {
+    pl.pos = a.rot > 0 ? a.pos[t] : 0;
+    pl.ok = a.rot <= 0 || (pl.pos >= 0 && pl.pos < a.max_pos);
+    if (!pl.ok) record_error(a.err, DFLASH_ERR_INVALID);
+    return pl;
+  }
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = a.R;  // the last request that begins at or before t lies in [lo, lo + n)
+  const bool pad = t >= a.q_off[a.R];  // padding behind the last request
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const int at = lane * step;
+    const unsigned m = __ballot_sync(0xffffffffu, at < n && a.q_off[lo + at] <= t);
+    const int k = m ? 31 - __clz(m) : 0;
+    lo += k * step;
+    n = min(step, n - k * step);
+  }
+  return pad ? pl : place_in(a, t, lo);
+}
+
+// Forward.  A block takes TB tokens and all their heads (q, then k, then, paged,
+// v).  Warps place one token each, and the tokens' table rows go through shared
+// memory; the first heads' loads are on their way meanwhile.
+constexpr int kTokens = kThreads / 32;  // most tokens of a block
+template <typename T, int LANES, bool PAGED>
+__global__ void __launch_bounds__(kThreads) rope_fwd_kernel(const __grid_constant__ RopeArgs a, int tb) {
+  constexpr int kGroups = kThreads / LANES;
+  constexpr int kBatch = sizeof(T) == 2 ? 4 : 2;  // heads in flight a group
+  __shared__ Place s_place[kTokens];
+  __shared__ float4 s_cs[kTokens * DFLASH_PAGED_MAX_D / 4];
+  const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES, warp = threadIdx.x >> 5;
   const int heads = a.Hq + (PAGED ? 2 : 1) * a.Hkv;
-  Place pl = {0, 0, 0};
-  const bool ok = t < a.T && place_token<PAGED>(a, t, &pl);
-  bool in[VPL];
+  const long long t0 = (long long)blockIdx.x * tb;
+  const int units = (int)min((long long)tb, a.T - t0) * heads;
+  const LanePart lp = lane_part(a, lane);
+  Part<T> x[kBatch];
+  auto fetch = [&](int u0) {
 #pragma unroll
-  for (int j = 0; j < VPL; ++j) in[j] = ok && (lane + LANES * j) * VEC < a.D;
-  float x[HPG][VPL][VEC];
-#pragma unroll
-  for (int u = 0; u < HPG; ++u) {
-    const int h = h0 + u;
-    const T* src;
-    if (h < a.Hq) src = static_cast<const T*>(a.q) + t * a.qs + (long long)h * a.D;
-    else if (!PAGED || h < a.Hq + a.Hkv) src = static_cast<const T*>(a.k) + t * a.ks + (long long)(h - a.Hq) * a.D;
-    else src = static_cast<const T*>(a.v) + t * a.vs + (long long)(h - a.Hq - a.Hkv) * a.D;
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) x[u][j][e] = 0.f;
-      if (in[j] && h < heads) load_vec<T, VEC>(src + (lane + LANES * j) * VEC, x[u][j]);
+    for (int j = 0; j < kBatch; ++j) {
+      const int u = u0 + j * kGroups;
+      if (u < units && lp.in) {
+        const int h = u % heads;
+        const long long t = t0 + u / heads;
+        const T* src = h < a.Hq ? static_cast<const T*>(a.q) + t * a.qs + (long long)h * a.D
+                       : !PAGED || h < a.Hq + a.Hkv
+                           ? static_cast<const T*>(a.k) + t * a.ks + (long long)(h - a.Hq) * a.D
+                           : static_cast<const T*>(a.v) + t * a.vs + (long long)(h - a.Hq - a.Hkv) * a.D;
+        x[j].load(src, lp);
+      }
+    }
+  };
+  fetch(group);
+  Part<T> wq, wk;
+  if (lp.in && a.wq) wq.load(static_cast<const T*>(a.wq), lp);
+  if (lp.in && a.wk) wk.load(static_cast<const T*>(a.wk), lp);
+  if (warp < tb) {
+    const long long t = t0 + warp;
+    const Place pl = place_token<PAGED>(a, (int)min(t, (long long)a.T));
+    if ((threadIdx.x & 31) == 0) s_place[warp] = pl;
+    if (pl.ok) {
+      const float4* row = reinterpret_cast<const float4*>(a.cs + (long long)pl.pos * a.rot);
+      for (int i = threadIdx.x & 31; i < a.rot / 4; i += 32) s_cs[warp * (DFLASH_PAGED_MAX_D / 4) + i] = row[i];
     }
   }
-  Rotor<VEC, LANES, VPL> rot;
-  rot.load(a, pl.pos, lane, ok);
+  __syncthreads();
+  for (int u0 = group; u0 - group < units; u0 += kBatch * kGroups) {
+    if (u0 != group) fetch(u0);
 #pragma unroll
-  for (int u = 0; u < HPG; ++u) {
-    const int h = h0 + u;
-    const bool is_q = h < a.Hq, is_v = PAGED && h >= a.Hq + a.Hkv;
-    if (__any_sync(0xffffffffu, h < heads && !is_v)) {
-      const T* w = static_cast<const T*>(is_q ? a.wq : a.wk);
+    for (int j = 0; j < kBatch; ++j) {
+      const int u = u0 + j * kGroups;
+      const int h = u % heads, tk = u < units ? u / heads : 0;
+      const bool is_q = h < a.Hq, is_v = PAGED && h >= a.Hq + a.Hkv;
+      const bool ok = u < units && lp.in && s_place[tk].ok;
+      float y[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = 0.f;
+      if (ok && !is_v) x[j].unpack(y);
       float ss = 0.f;
 #pragma unroll
-      for (int j = 0; j < VPL; ++j)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) ss = fmaf(x[u][j][e], x[u][j][e], ss);
+      for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
       ss = group_sum<LANES>(ss);
-      const float r = rsqrtf(ss / (float)a.D + a.eps);
-      float y[VPL][VEC];
-#pragma unroll
-      for (int j = 0; j < VPL; ++j) {
-        float wv[VEC];
-        const bool normed = w != nullptr && in[j];
-        if (normed) load_vec<T, VEC>(w + (lane + LANES * j) * VEC, wv);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) y[j][e] = normed ? x[u][j][e] * r * wv[e] : x[u][j][e];
-      }
-      rot.apply(y, a.interleaved, 1.f);
+      if (!ok) continue;
       if (!is_v) {
+        if (is_q ? a.wq != nullptr : a.wk != nullptr) {
+          const float r = rsqrtf(ss / (float)a.D + a.eps);
+          float w[8];
+          if (is_q) wq.unpack(w);
+          else wk.unpack(w);
 #pragma unroll
-        for (int j = 0; j < VPL; ++j)
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) x[u][j][e] = y[j][e];
+          for (int e = 0; e < 8; ++e) y[e] *= r * w[e];
+        }
+        if (lp.turned) {
+          const float4* row = s_cs + tk * (DFLASH_PAGED_MAX_D / 4) + lane;
+          const float4 c = row[0], sn = row[a.rot / 8];
+          const float cv[4] = {c.x, c.y, c.z, c.w}, sv[4] = {sn.x, sn.y, sn.z, sn.w};
+          rotate8(y, cv, sv, a.interleaved);
+        }
+        x[j].pack(y);
       }
+      const long long t = t0 + tk;
+      T* dst;
+      if (is_q) dst = static_cast<T*>(a.qo) + (t * a.Hq + h) * a.D;
+      else if (!PAGED) dst = static_cast<T*>(a.ko) + (t * a.Hkv + (h - a.Hq)) * a.D;
+      else if (!is_v) dst = static_cast<T*>(a.kc) + s_place[tk].krow + (long long)(h - a.Hq) * a.D;
+      else dst = static_cast<T*>(a.vc) + s_place[tk].vrow + (long long)(h - a.Hq - a.Hkv) * a.D;
+      x[j].store(dst, lp);
     }
-    if (h >= heads) continue;
-    T* dst;
-    if (is_q) dst = static_cast<T*>(a.qo) + ((long long)t * a.Hq + h) * a.D;
-    else if (!PAGED) dst = static_cast<T*>(a.ko) + ((long long)t * a.Hkv + (h - a.Hq)) * a.D;
-    else if (!is_v) dst = static_cast<T*>(a.kc) + pl.krow + (long long)(h - a.Hq) * a.D;
-    else dst = static_cast<T*>(a.vc) + pl.vrow + (long long)(h - a.Hq - a.Hkv) * a.D;
-#pragma unroll
-    for (int j = 0; j < VPL; ++j)
-      if (in[j]) store_vec<T, VEC>(dst + (lane + LANES * j) * VEC, x[u][j]);
   }
 }
 
-// Backward: groups walk the units with the grid's stride and keep their share of
-// the norm gradients in registers; a block adds its groups up in shared memory
-// and writes one row of partial sums, so that the order of the sums is fixed.
-template <typename T, int VEC, int LANES, int VPL>
+// Backward.  A block keeps to one chunk of hpg query heads or hpg key heads and
+// walks the tokens, a group a token: the weight and this lane's share of its
+// gradient stay in registers all along.  The block adds its groups' shares up in
+// shared memory and writes one row of partial sums, so the order of the sums is
+// fixed.  Blocks count [row of blocks][chunk]; chunks below nq are query heads.
+template <typename T, int LANES>
 __global__ void __launch_bounds__(kThreads)
-    rope_bwd_kernel(const __grid_constant__ RopeArgs a, int nchunk, int hpg) {
+    rope_bwd_kernel(const __grid_constant__ RopeArgs a, int hpg, int nq, int nchunk) {
   constexpr int kGroups = kThreads / LANES;
-  __shared__ float red[kGroups][VPL * LANES * VEC];
+  constexpr int kBatch = sizeof(T) == 2 ? 4 : 2;
+  __shared__ float red[kGroups][LANES * 8];
   const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
-  const int heads = a.Hq + a.Hkv;
-  float dw[2][VPL][VEC];
+  const int chunk = blockIdx.x % nchunk, brow = blockIdx.x / nchunk, brows = gridDim.x / nchunk;
+  const bool is_q = chunk < nq;
+  const int H = is_q ? a.Hq : a.Hkv;
+  const int h0 = (is_q ? chunk : chunk - nq) * hpg, h1 = min(H, h0 + hpg);
+  const T* w = static_cast<const T*>(is_q ? a.wq : a.wk);
+  const T* src = static_cast<const T*>(is_q ? a.q : a.k);
+  const T* dsrc = static_cast<const T*>(is_q ? a.dqo : a.dko);
+  T* dst = static_cast<T*>(is_q ? a.qo : a.ko);
+  const long long stride = is_q ? a.qs : a.ks;
+  const bool normed = w != nullptr;
+  const LanePart lp = lane_part(a, lane);
+  float wv[8], dw[8];
 #pragma unroll
-  for (int w = 0; w < 2; ++w)
+  for (int e = 0; e < 8; ++e) wv[e] = dw[e] = 0.f;
+  if (normed && lp.in) {
+    Part<T> wr;
+    wr.load(w, lp);
+    wr.unpack(wv);
+  }
+  const float inv_d = 1.f / (float)a.D;
+  const int step = brows * kGroups;
+  int t = brow * kGroups + group;  // T + step fits: the host bounds T
+  int pos = a.rot > 0 && t < a.T ? a.pos[t] : 0;
+  for (int base = brow * kGroups; base < a.T; base += step, t += step) {
+    const bool ok = t < a.T && (a.rot <= 0 || (pos >= 0 && pos < a.max_pos));
+    if (t < a.T && !ok) record_error(a.err, DFLASH_ERR_INVALID);
+    float cs[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
+    if (ok && lp.turned) {
+      const float* row = a.cs + (long long)pos * a.rot + lp.ang;
+      const float4 c = *reinterpret_cast<const float4*>(row), s = *reinterpret_cast<const float4*>(row + (a.rot >> 1));
+      cs[0] = c.x; cs[1] = c.y; cs[2] = c.z; cs[3] = c.w;
+      sn[0] = -s.x; sn[1] = -s.y; sn[2] = -s.z; sn[3] = -s.w;
+    }
+    if (a.rot > 0 && t + step < a.T) pos = a.pos[t + step];
+    for (int hb = h0; hb < h1; hb += kBatch) {
+      Part<T> xr[kBatch], gr[kBatch];
 #pragma unroll
-    for (int j = 0; j < VPL; ++j)
+      for (int j = 0; j < kBatch; ++j)
+        if (ok && lp.in && hb + j < h1) {
+          gr[j].load(dsrc + ((long long)t * H + hb + j) * a.D, lp);
+          if (normed) xr[j].load(src + t * stride + (long long)(hb + j) * a.D, lp);
+        }
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) dw[w][j][e] = 0.f;
-  const long long units = (long long)a.T * nchunk;
-  for (long long base = (long long)blockIdx.x * kGroups; base < units; base += (long long)gridDim.x * kGroups) {
-    const long long unit = base + group;
-    const int t = (int)min(unit / nchunk, (long long)a.T);
-    const int h0 = (int)(unit % nchunk) * hpg;
-    Place pl = {0, 0, 0};
-    const bool ok = t < a.T && place_token<false>(a, t, &pl);
-    bool in[VPL];
+      for (int j = 0; j < kBatch; ++j) {
+        const bool have = ok && lp.in && hb + j < h1;
+        float g[8], x[8];
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) in[j] = ok && (lane + LANES * j) * VEC < a.D;
-    Rotor<VEC, LANES, VPL> rot;
-    rot.load(a, pl.pos, lane, ok);
-#pragma unroll 2
-    for (int u = 0; u < hpg; ++u) {
-      const int h = h0 + u;
-      const bool is_q = h < a.Hq, have = h < heads;
-      const long long at = is_q ? ((long long)t * a.Hq + h) * a.D : ((long long)t * a.Hkv + (h - a.Hq)) * a.D;
-      const T* w = static_cast<const T*>(is_q ? a.wq : a.wk);
-      const bool normed = w != nullptr;
-      const T* src = is_q ? static_cast<const T*>(a.q) + t * a.qs + (long long)h * a.D
-                          : static_cast<const T*>(a.k) + t * a.ks + (long long)(h - a.Hq) * a.D;
-      const T* dsrc = static_cast<const T*>(is_q ? a.dqo : a.dko) + at;
-      float x[VPL][VEC], g[VPL][VEC], wv[VPL][VEC];
+        for (int e = 0; e < 8; ++e) g[e] = x[e] = 0.f;
+        if (have) {
+          gr[j].unpack(g);
+          if (normed) xr[j].unpack(x);
+        }
+        if (lp.turned) rotate8(g, cs, sn, a.interleaved);
+        if (normed) {
+          float ss = 0.f, dot = 0.f, gw[8];
 #pragma unroll
-      for (int j = 0; j < VPL; ++j) {
+          for (int e = 0; e < 8; ++e) {
+            gw[e] = g[e] * wv[e];
+            ss = fmaf(x[e], x[e], ss);
+            dot = fmaf(gw[e], x[e], dot);
+          }
+          ss = group_sum<LANES>(ss);
+          dot = group_sum<LANES>(dot);
+          const float r = rsqrtf(ss * inv_d + a.eps);
+          const float c = dot * r * r * inv_d * r;  // r times mean(g w x^) r, the factor of x
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) x[j][e] = g[j][e] = wv[j][e] = 0.f;
-        if (in[j] && have) {
-          const int d = (lane + LANES * j) * VEC;
-          load_vec<T, VEC>(dsrc + d, g[j]);
-          if (normed) {
-            load_vec<T, VEC>(src + d, x[j]);
-            load_vec<T, VEC>(w + d, wv[j]);
+          for (int e = 0; e < 8; ++e) {
+            dw[e] = fmaf(g[e], x[e] * r, dw[e]);
+            g[e] = gw[e] * r - x[e] * c;
           }
         }
-      }
-      rot.apply(g, a.interleaved, -1.f);
-      float ss = 0.f, dot = 0.f;
-#pragma unroll
-      for (int j = 0; j < VPL; ++j)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          ss = fmaf(x[j][e], x[j][e], ss);
-          dot = fmaf(g[j][e] * wv[j][e], x[j][e], dot);
-        }
-      ss = group_sum<LANES>(ss);
-      dot = group_sum<LANES>(dot);
-      const float r = rsqrtf(ss / (float)a.D + a.eps);
-      const float c = dot * r * r / (float)a.D;  // mean(g w x^) r, the factor of x inside the bracket
-      if (have) {
-        T* dst = static_cast<T*>(is_q ? a.qo : a.ko) + at;
-#pragma unroll
-        for (int j = 0; j < VPL; ++j) {
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            const float gx = normed ? g[j][e] * x[j][e] * r : 0.f;
-            dw[0][j][e] += is_q ? gx : 0.f;
-            dw[1][j][e] += is_q ? 0.f : gx;
-            if (normed) g[j][e] = r * (g[j][e] * wv[j][e] - x[j][e] * c);
-          }
-          if (in[j]) store_vec<T, VEC>(dst + (lane + LANES * j) * VEC, g[j]);
+        if (have) {
+          gr[j].pack(g);
+          gr[j].store(dst + ((long long)t * H + hb + j) * a.D, lp);
         }
       }
     }
   }
+  if (lp.in) {
 #pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < VPL; ++j)
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) red[group][(lane + LANES * j) * VEC + e] = dw[w][j][e];
-    __syncthreads();
-    for (int d = threadIdx.x; d < a.D; d += kThreads) {
-      float s = 0.f;
-#pragma unroll
-      for (int i = 0; i < kGroups; ++i) s += red[i][d];
-      a.dw_part[((long long)blockIdx.x * 2 + w) * a.D + d] = s;
+    for (int e = 0; e < 4; ++e) {
+      red[group][lp.a + e] = dw[e];
+      red[group][lp.b + e] = dw[4 + e];
     }
+  }
+  __syncthreads();
+  for (int d = threadIdx.x; d < a.D; d += kThreads) {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) s += red[i][d];
+    a.dw_part[(long long)blockIdx.x * a.D + d] = s;
   }
 }
 
-// Sums the blocks' rows: 32 columns a block, 32 threads down each column.
-__global__ void __launch_bounds__(1024) rope_dw_kernel(const float* part, int blocks, int D, float* dwq, float* dwk) {
+// Sums the blocks' rows: 32 columns a block, 32 threads down each column.  Row b
+// belongs to the query weight where b % nchunk < nq, else to the key weight.
+__global__ void __launch_bounds__(1024)
+    rope_dw_kernel(const float* part, int blocks, int nq, int nchunk, int D, float* dwq, float* dwk) {
   __shared__ float red[32][33];
   const int c = threadIdx.x & 31, y = threadIdx.x >> 5;
   const int d = blockIdx.x * 32 + c, w = blockIdx.y;
@@ -331,7 +372,8 @@ __global__ void __launch_bounds__(1024) rope_dw_kernel(const float* part, int bl
   if (!dst) return;
   float s = 0.f;
   if (d < D)
-    for (int b = y; b < blocks; b += 32) s += part[((long long)b * 2 + w) * D + d];
+    for (int b = y; b < blocks; b += 32)
+      if ((b % nchunk >= nq) == (w == 1)) s += part[(long long)b * D + d];
   red[y][c] = s;
   __syncthreads();
   if (y == 0 && d < D) {
@@ -366,8 +408,8 @@ __global__ void __launch_bounds__(kThreads) rope_fwd_plain_kernel(const __grid_c
   const long long unit = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (unit >= (long long)a.T * heads) return;
   const int t = (int)(unit / heads), h = (int)(unit % heads);
-  Place pl = {0, 0, 0};
-  if (!place_token<PAGED>(a, t, &pl)) return;
+  const Place pl = place_token<PAGED>(a, t);
+  if (!pl.ok) return;
   const bool is_q = h < a.Hq, is_v = PAGED && h >= a.Hq + a.Hkv;
   const T* src;
   T* dst;
@@ -405,12 +447,12 @@ __global__ void __launch_bounds__(kThreads) rope_bwd_plain_kernel(const __grid_c
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float* y = rows[warp];
   const int heads = a.Hq + a.Hkv;
-  for (int d = lane; d < 2 * DFLASH_PAGED_MAX_D; d += 32) (&acc[warp][0][0])[d] = 0.f;
+  for (int d = lane; d < 2 * DFLASH_PAGED_MAX_D; d += 32) (&acc[warp][0][0])[d] = 0.f;  // queries, then keys
   const long long units = (long long)a.T * heads;
   for (long long unit = (long long)blockIdx.x * kWarps + warp; unit < units; unit += (long long)gridDim.x * kWarps) {
     const int t = (int)(unit / heads), h = (int)(unit % heads);
-    Place pl = {0, 0, 0};
-    if (!place_token<false>(a, t, &pl)) continue;
+    const Place pl = place_token<false>(a, t);
+    if (!pl.ok) continue;
     const bool is_q = h < a.Hq;
     const long long at = is_q ? ((long long)t * a.Hq + h) * a.D : ((long long)t * a.Hkv + (h - a.Hq)) * a.D;
     const T* src = is_q ? static_cast<const T*>(a.q) + t * a.qs + (long long)h * a.D
@@ -447,65 +489,48 @@ __global__ void __launch_bounds__(kThreads) rope_bwd_plain_kernel(const __grid_c
     const int w = i / a.D, d = i % a.D;
     float s = 0.f;
     for (int k = 0; k < kWarps; ++k) s += acc[k][w][d];
-    a.dw_part[((long long)blockIdx.x * 2 + w) * a.D + d] = s;
+    a.dw_part[((long long)blockIdx.x * 2 + w) * a.D + d] = s;  // even rows the query weight, odd rows the key weight
   }
 }
 
 // ---------------------------------------------------------------- host side
-constexpr int kBwdBlocks = 608;  // 152 SMs x 4 resident blocks
+constexpr int kBwdBlocks = 608;  // 152 SMs x 4 blocks of 256 threads
 
 bool on(const void* p, size_t bytes) { return ((uintptr_t)p % bytes) == 0; }
 
-// Widest vector (elements) that the shape and the addresses allow; 0: the plain kernels.
-int vector_width(const RopeArgs& a, bool bf16, bool paged, bool bwd) {
-  const size_t esz = bf16 ? 2 : 4;
-  for (int vec = bf16 ? 8 : 4; vec >= 4; vec -= 4) {
-    const size_t b = vec * esz;
-    const int plane = a.interleaved ? a.rot : a.rot / 2;
-    bool ok = a.D % vec == 0 && plane % vec == 0;
-    if (a.Hq > 0) ok = ok && (!a.q || (on(a.q, b) && a.qs % vec == 0)) && on(a.qo, b) && on(a.wq, b);
-    if (a.Hkv > 0) ok = ok && (!a.k || (on(a.k, b) && a.ks % vec == 0)) && on(a.ko, b) && on(a.wk, b);
-    if (paged) ok = ok && on(a.v, b) && a.vs % vec == 0 && on(a.kc, b) && on(a.vc, b) && a.kps % vec == 0 && a.vps % vec == 0;
-    if (bwd) ok = ok && on(a.dqo, b) && on(a.dko, b);
-    if (ok) return vec;
-  }
-  return 0;
+// Whether planes and addresses suit the four-component vectors.
+bool vectors(const RopeArgs& a, bool bf16, bool paged, bool bwd) {
+  const size_t b = bf16 ? 8 : 16;
+  bool ok = a.rot % 8 == 0 && (a.rot == 0 || on(a.cs, 16));
+  if (a.Hq > 0) ok = ok && on(a.q, b) && a.qs % 4 == 0 && on(a.qo, b) && on(a.wq, b);
+  if (a.Hkv > 0) ok = ok && on(a.k, b) && a.ks % 4 == 0 && on(a.ko, b) && on(a.wk, b);
+  if (paged) ok = ok && on(a.v, b) && a.vs % 4 == 0 && on(a.kc, b) && on(a.vc, b) && a.kps % 4 == 0 && a.vps % 4 == 0;
+  if (bwd) ok = ok && on(a.dqo, b) && on(a.dko, b);
+  return ok;
 }
 
-template <typename T, int VEC, int LANES, int VPL, int HPG, bool PAGED>
+template <typename T, int LANES, bool PAGED>
 cudaError_t run_fwd(const RopeArgs& a, cudaStream_t s) {
-  const int heads = a.Hq + (PAGED ? 2 : 1) * a.Hkv;
-  const int nchunk = (heads + HPG - 1) / HPG, groups = kThreads / LANES;
-  const long long blocks = ((long long)a.T * nchunk + groups - 1) / groups;
-  if (blocks >= (1ll << 31)) return cudaErrorInvalidConfiguration;
-  rope_fwd_kernel<T, VEC, LANES, VPL, HPG, PAGED><<<(unsigned)blocks, kThreads, 0, s>>>(a, nchunk);
+  const int heads = a.Hq + (PAGED ? 2 : 1) * a.Hkv, groups = kThreads / LANES;
+  // Tokens of a block: about eight heads a group, as long as the blocks still fill
+  // the machine; with few tokens one a block, which shortens the call.
+  int tb = 8 * groups / heads;
+  if (tb > kTokens) tb = kTokens;
+  const long long most = a.T / (152 * 4);
+  if (tb > most) tb = (int)most;
+  if (tb < 1) tb = 1;
+  rope_fwd_kernel<T, LANES, PAGED><<<(unsigned)(((long long)a.T + tb - 1) / tb), kThreads, 0, s>>>(a, tb);
   count_launch();
   return cudaGetLastError();
 }
 
-// Four heads a group once the groups still fill the machine (152 SMs x 2048
-// threads); with fewer tokens one head a group, which shortens the call.
-template <typename T, int VEC, int LANES, int VPL, bool PAGED>
-cudaError_t pick_fwd(const RopeArgs& a, cudaStream_t s) {
-  const long long lanes = (long long)a.T * (a.Hq + (PAGED ? 2 : 1) * a.Hkv) * LANES;
-  return lanes / 4 >= 152ll * 2048 ? run_fwd<T, VEC, LANES, VPL, 4, PAGED>(a, s)
-                                   : run_fwd<T, VEC, LANES, VPL, 1, PAGED>(a, s);
-}
-
-template <typename T, int VEC, bool PAGED>
-cudaError_t width_fwd(const RopeArgs& a, cudaStream_t s) {
-  const int chunks = a.D / VEC;
-  if (chunks <= 8) return pick_fwd<T, VEC, 8, 1, PAGED>(a, s);
-  if (chunks <= 16) return pick_fwd<T, VEC, 16, 1, PAGED>(a, s);
-  if (chunks <= 32) return pick_fwd<T, VEC, 32, 1, PAGED>(a, s);
-  return pick_fwd<T, VEC, 32, 2, PAGED>(a, s);
-}
-
 template <typename T, bool PAGED>
 cudaError_t type_fwd(const RopeArgs& a, cudaStream_t s) {
-  const int vec = vector_width(a, sizeof(T) == 2, PAGED, false);
-  if (vec == 8) return width_fwd<T, sizeof(T) == 2 ? 8 : 4, PAGED>(a, s);
-  if (vec == 4) return width_fwd<T, 4, PAGED>(a, s);
+  if (vectors(a, sizeof(T) == 2, PAGED, false)) {
+    if (a.D <= 64) return run_fwd<T, 8, PAGED>(a, s);
+    if (a.D <= 128) return run_fwd<T, 16, PAGED>(a, s);
+    return run_fwd<T, 32, PAGED>(a, s);
+  }
   const int heads = a.Hq + (PAGED ? 2 : 1) * a.Hkv;
   const long long blocks = ((long long)a.T * heads + kWarps - 1) / kWarps;
   if (blocks >= (1ll << 31)) return cudaErrorInvalidConfiguration;
@@ -514,45 +539,45 @@ cudaError_t type_fwd(const RopeArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-template <typename T, int VEC, int LANES, int VPL>
-void run_bwd(const RopeArgs& a, int* blocks, cudaStream_t s) {
-  constexpr int groups = kThreads / LANES;
-  const int heads = a.Hq + a.Hkv;
-  // heads a group: as many as leave every group of the full grid at least one unit
-  int hpg = 8;
-  while (hpg > 1 && (long long)a.T * ((heads + hpg - 1) / hpg) < (long long)kBwdBlocks * groups) hpg >>= 1;
-  const int nchunk = (heads + hpg - 1) / hpg;
-  const long long need = ((long long)a.T * nchunk + groups - 1) / groups;
-  *blocks = (int)(need < kBwdBlocks ? need : kBwdBlocks);
-  rope_bwd_kernel<T, VEC, LANES, VPL><<<*blocks, kThreads, 0, s>>>(a, nchunk, hpg);
-}
+// How the partial norm gradients lie in the workspace.
+struct DwRows {
+  int blocks, nq, nchunk;
+};
 
-template <typename T, int VEC>
-void width_bwd(const RopeArgs& a, int* blocks, cudaStream_t s) {
-  const int chunks = a.D / VEC;
-  if (chunks <= 8) run_bwd<T, VEC, 8, 1>(a, blocks, s);
-  else if (chunks <= 16) run_bwd<T, VEC, 16, 1>(a, blocks, s);
-  else if (chunks <= 32) run_bwd<T, VEC, 32, 1>(a, blocks, s);
-  else run_bwd<T, VEC, 32, 2>(a, blocks, s);
+template <typename T, int LANES>
+DwRows run_bwd(const RopeArgs& a, cudaStream_t s) {
+  constexpr int groups = kThreads / LANES;
+  // Heads a chunk: as many as still leave a full grid of blocks with work.
+  int hpg = 8;
+  auto chunks = [&](int h) { return (h + hpg - 1) / hpg; };
+  while (hpg > 1 &&
+         ((long long)a.T + groups - 1) / groups * (chunks(a.Hq) + chunks(a.Hkv)) < kBwdBlocks)
+    hpg >>= 1;
+  while (chunks(a.Hq) + chunks(a.Hkv) > kBwdBlocks) hpg *= 2;
+  DwRows d;
+  d.nq = chunks(a.Hq);
+  d.nchunk = d.nq + chunks(a.Hkv);
+  const long long need = ((long long)a.T + groups - 1) / groups, most = kBwdBlocks / d.nchunk;
+  d.blocks = (int)(need < most ? need : most) * d.nchunk;
+  rope_bwd_kernel<T, LANES><<<d.blocks, kThreads, 0, s>>>(a, hpg, d.nq, d.nchunk);
+  return d;
 }
 
 template <typename T>
 cudaError_t type_bwd(const RopeArgs& a, float* dwq, float* dwk, cudaStream_t s) {
-  const int vec = vector_width(a, sizeof(T) == 2, false, true);
-  int blocks = 0;
-  if (vec == 8) {
-    width_bwd<T, sizeof(T) == 2 ? 8 : 4>(a, &blocks, s);
-  } else if (vec == 4) {
-    width_bwd<T, 4>(a, &blocks, s);
+  DwRows d;
+  if (vectors(a, sizeof(T) == 2, false, true)) {
+    d = a.D <= 64 ? run_bwd<T, 8>(a, s) : a.D <= 128 ? run_bwd<T, 16>(a, s) : run_bwd<T, 32>(a, s);
   } else {
     const long long need = ((long long)a.T * (a.Hq + a.Hkv) + kWarps - 1) / kWarps;
-    blocks = (int)(need < kBwdBlocks ? need : kBwdBlocks);
+    const int blocks = (int)(need < kBwdBlocks / 2 ? need : kBwdBlocks / 2);
     rope_bwd_plain_kernel<T><<<blocks, kThreads, 0, s>>>(a);
+    d = {2 * blocks, 1, 2};
   }
   count_launch();
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || (!dwq && !dwk)) return e;
-  rope_dw_kernel<<<dim3((a.D + 31) / 32, 2), 1024, 0, s>>>(a.dw_part, blocks, a.D, dwq, dwk);
+  rope_dw_kernel<<<dim3((a.D + 31) / 32, 2), 1024, 0, s>>>(a.dw_part, d.blocks, d.nq, d.nchunk, a.D, dwq, dwk);
   count_launch();
   return cudaGetLastError();
 }
@@ -564,7 +589,7 @@ cudaError_t launch_qk_norm_rope(const RopeArgs& a, bool bf16, bool paged, cudaSt
   return bf16 ? type_fwd<__nv_bfloat16, false>(a, stream) : type_fwd<float, false>(a, stream);
 }
 
-size_t rope_bwd_workspace_bytes(int D) { return sizeof(float) * 2 * (size_t)kBwdBlocks * D; }
+size_t rope_bwd_workspace_bytes(int D) { return sizeof(float) * (size_t)kBwdBlocks * D; }
 
 cudaError_t launch_qk_norm_rope_bwd(const RopeArgs& a, bool bf16, float* dwq, float* dwk, cudaStream_t stream) {
   return bf16 ? type_bwd<__nv_bfloat16>(a, dwq, dwk, stream) : type_bwd<float>(a, dwq, dwk, stream);

@@ -223,12 +223,3 @@ def test_binding_refuses_what_is_not_on_a_gpu_or_has_another_form(lib):
         dfl.dflash_verify(z(4, 10), z(3, 10), z(3, **i32), z(2, **i32), z(3), z(1), 3)
     with pytest.raises(ValueError):  # too few target rows
         dfl.dflash_verify(z(3, 10), z(3, 10), z(3, **i32), z(2, **i32), z(3), z(1), 3)
-
-
-def test_token_and_page_strides_are_taken_from_the_tensors():
-    f, dev = torch.float32, torch.device("cpu")
-    cuda = torch.device("cuda")
-    t = torch.zeros(5, 8 * 64)[:, 64:64 * 5].view(5, 4, 64)
-    with pytest.raises(ValueError):  # on another device than asked for
-        dfl._token_arg(t, "q", cuda, f, (5, 4, 64))
-    assert t.stride() == (512, 64, 1) and dev.type == "cpu"
