@@ -7,15 +7,17 @@
 // in one pass over the keys, the output rescaled by 2^(m_old - m_new) where the
 // running maximum m rises.
 //
-// A CTA holds a row tile's queries in shared memory, walks its key tiles of 64
-// positions (K, then V through one buffer) and multiplies in fp32: each thread
-// has 4 rows of the scores and of the output in registers, so that one 16-byte
-// shared-memory read feeds 4 to 16 multiply-adds.  Tiles of 64 rows, or of 16
-// where no request has more rows than that (single tokens and short blocks with
-// few heads a group, where 64-row tiles would multiply mostly padding).
-// Rates: see the table of cases in the tests' companion benchmark; fp32 needs
-// 4 D multiply-adds for each row and 8 D bytes of a position, so it is bound by
-// the multiply-adds from about 10 rows on and by memory below.
+// A CTA holds a row tile's queries in shared memory and walks its key tiles of 32
+// positions, which arrive by 16-byte asynchronous copies two tiles deep; the rows'
+// offsets (page table and page row) are worked out one tile ahead of the copies.
+// Each thread has 4 rows of the scores and of the output in registers, and all
+// threads of a row lie in one warp, so that the softmax needs shuffles only and a
+// key tile two block barriers.  Row tiles of 64 rows with 256 threads, or of 16 with
+// 128 where no request has more rows (single tokens and short blocks with few
+// heads a group, where 64-row tiles would multiply mostly padding; the smaller
+// CTAs also put more copies in flight).  fp32 needs 4 D multiply-adds for each row
+// and 8 D bytes of a position, so it is bound by the multiply-adds from about 10
+// rows on and by memory below.
 #include <math.h>
 #include <stdlib.h>
 #include <string.h>
@@ -25,184 +27,189 @@
 namespace dflash {
 namespace paged {
 
-constexpr int kSimtBN = 64;
-constexpr int kSimtThreads = 256;
+constexpr int kSimtBN = 32;
 constexpr int kSms = 152;
-constexpr int kSimtMaxGrid = 2 * kSms;
+// CTAs of a launch at most: 4 an SM with 16-row tiles, 2 with 64-row tiles.
+constexpr int kSimtPerSm16 = 4, kSimtPerSm64 = 2;
+constexpr int kSimtMaxGrid = kSimtPerSm16 * kSms;
 
 namespace {
 
-template <typename T>
-struct alignas(16) Vec16 {
-  T e[16 / sizeof(T)];
-};
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool have) {  // zeros where !have
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                   static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+               "l"(src), "r"(have ? 16u : 0u)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
-template <int BM, int DMAX>
-struct SimtSmem {
-  static constexpr int kStride = DMAX + 4;      // floats from row to row of Q, K and V
-  static constexpr int kPStride = kSimtBN + 4;  // and of the scores
-  float q[BM * kStride];
-  float kv[kSimtBN * kStride];
-  float p[BM * kPStride];
-  float m[BM], l[BM], alpha[BM];
-  int lim[BM];
-  long long koff[kSimtBN], voff[kSimtBN];  // element offsets of the tile's rows; -1: zeros
-  Range range;
-  long long scratch[kSimtThreads / 32 + 1];
-};
-
-// Copies n rows of D elements to fp32 rows of shared memory (zeros where off < 0).
-template <typename T, int STRIDE>
-__device__ __forceinline__ void load_rows(float* dst, const T* base, const long long* off, int n, int D) {
-  constexpr int VEC = 16 / sizeof(T);
-  const int per = D / VEC;
-  for (int i = threadIdx.x; i < n * per; i += kSimtThreads) {
-    const int r = i / per, c = (i - r * per) * VEC;
-    float x[VEC];
-    const long long o = off[r];
-    if (o >= 0) {
-      const Vec16<T> v = *reinterpret_cast<const Vec16<T>*>(base + o + c);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) x[e] = to_f32(v.e[e]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) x[e] = 0.f;
-    }
-#pragma unroll
-    for (int e = 0; e < VEC; e += 4)
-      *reinterpret_cast<float4*>(dst + r * STRIDE + c + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
-  }
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+  const uint2 v = *reinterpret_cast<const uint2*>(p);
+  return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
+                     __uint_as_float(v.y & 0xFFFF0000u));
 }
 
 template <typename T, int BM, int DMAX>
-__global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const __grid_constant__ PagedArgs a) {
-  constexpr int BN = kSimtBN;
-  constexpr int TY = BM / 4, TX = kSimtThreads / TY;  // threads down the rows and across
-  constexpr int CT = BN / TX;                         // scores a thread and row
-  constexpr int NC = DMAX / TX;                       // output columns a thread and row
+struct Simt {
+  static constexpr int BN = kSimtBN;
+  static constexpr int kThreads = BM == 16 ? 128 : 256;
+  static constexpr int kVec = 16 / sizeof(T);
+  static constexpr int kStride = DMAX + kVec;  // elements from row to row of K and V
+  static constexpr int kQStride = DMAX + 4;
+  static constexpr int kPStride = BN + 4;
+  struct Smem {
+    T k[2][BN * kStride], v[2][BN * kStride];
+    float q[BM * kQStride];
+    float p[BM * kPStride];
+    long long koff[3][BN], voff[3][BN];  // element offsets of the rows of tiles kt, kt + 1, kt + 2; -1: zeros
+    Range range;
+    long long scratch[kThreads / 32 + 1];
+  };
+};
+
+template <typename T, int BM, int DMAX>
+__global__ void __launch_bounds__(Simt<T, BM, DMAX>::kThreads)
+    paged_simt_kernel(const __grid_constant__ PagedArgs a) {
+  using C = Simt<T, BM, DMAX>;
+  constexpr int BN = C::BN, kThreads = C::kThreads, VEC = C::kVec;
+  constexpr int TY = BM / 4, TX = kThreads / TY;  // threads down the rows and across
+  constexpr int CT = BN / TX;                     // scores a thread and row
+  constexpr int NC = DMAX / TX;                   // output columns a thread and row
   constexpr int VW = NC < 4 ? NC : 4, U = NC / VW;
-  static_assert(CT >= 1 && NC >= 1, "thread layout");
-  using S = SimtSmem<BM, DMAX>;
+  static_assert(CT >= 1 && NC >= 2 && TX <= 32, "thread layout");
   extern __shared__ __align__(16) uint8_t raw[];
-  S& s = *reinterpret_cast<S*>(raw);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  typename C::Smem& s = *reinterpret_cast<typename C::Smem*>(raw);
+  const int tid = threadIdx.x;
   const int ty = tid / TX, tx = tid % TX;
-  const int D = a.D;
-  find_range<BN, kSimtThreads>(a, &s.range, s.scratch);
+  const int D = a.D, per = D / VEC;  // 16-byte pieces of a row
+  find_range<BN, kThreads>(a, &s.range, s.scratch);
   Walker<BN> walk(a, s.range);
   Piece pc;
   int4 meta = make_int4(0, 0, 0, 0);
   while (walk.next(&pc)) {
     const int f0 = pc.rt * BM;  // first row of the tile within (request, key/value head)
     const int nrow = min(BM, pc.q.n * a.G - f0);
-    __syncthreads();  // the previous piece is done with shared memory
-    if (tid < BM) {
-      s.m[tid] = -INFINITY;
-      s.l[tid] = 0.f;
-      const int tok = (f0 + tid) / a.G;
-      s.lim[tid] = tid >= nrow ? 0 : a.causal ? max(0, pc.q.kv - pc.q.n + tok + 1) : pc.q.kv;
-      if (tid < BN) {  // BM <= BN: the queries' offsets use the keys' table once
-        const int g = (f0 + tid) % a.G;
-        s.koff[tid] = tid < nrow ? ((long long)(pc.q.q0 + tok) * a.Hq + pc.h * a.G + g) * D : -1;
+    // offsets of key tile kt's row `tid` (threads below BN); the page's load is left in flight
+    auto page_of = [&](int kt) {
+      const int p = kt * BN + tid;
+      return tid < BN && kt < pc.kt1 && p < pc.q.kv ? a.table[(long long)pc.r * a.max_pages + p / a.P] : -2;
+    };
+    auto put_offsets = [&](int kt, int page) {
+      if (tid >= BN) return;
+      long long ko = -1, vo = -1;
+      if (page >= 0 && page < a.num_pages) {
+        const long long row = ((long long)((kt * BN + tid) % a.P) * a.Hkv + pc.h) * D;
+        ko = page * a.kps + row;
+        vo = page * a.vps + row;
+      } else if (page != -2 || (kt < pc.kt1 && kt * BN + tid < pc.q.kv)) {
+        record_error(a.err, DFLASH_ERR_INVALID);
       }
+      s.koff[kt % 3][tid] = ko;
+      s.voff[kt % 3][tid] = vo;
+    };
+    auto fetch = [&](int kt) {  // its offsets are in place
+      if (kt < pc.kt1) {
+        for (int i = tid; i < BN * per; i += kThreads) {
+          const int r = i / per, c = (i - r * per) * VEC;
+          const long long ko = s.koff[kt % 3][r], vo = s.voff[kt % 3][r];
+          copy16(&s.k[kt & 1][r * C::kStride + c], static_cast<const T*>(a.kc) + max(ko, 0ll) + c, ko >= 0);
+          copy16(&s.v[kt & 1][r * C::kStride + c], static_cast<const T*>(a.vc) + max(vo, 0ll) + c, vo >= 0);
+        }
+      }
+      copy_commit();
+    };
+    put_offsets(pc.kt0, page_of(pc.kt0));
+    put_offsets(pc.kt0 + 1, page_of(pc.kt0 + 1));
+    for (int i = tid; i < BM * (D / 4); i += kThreads) {
+      const int r = i / (D / 4), c = (i - r * (D / 4)) * 4;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < nrow) {
+        const int f = f0 + r;
+        x = load4(static_cast<const T*>(a.q) + ((long long)(pc.q.q0 + f / a.G) * a.Hq + pc.h * a.G + f % a.G) * D + c);
+      }
+      *reinterpret_cast<float4*>(s.q + r * C::kQStride + c) = x;
     }
-    __syncthreads();
-    load_rows<T, S::kStride>(s.q, static_cast<const T*>(a.q), s.koff, BM, D);
-    float o[4][NC];
+    int lim[4];
+    float m[4], l[4], o[4][NC];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 4; ++i) {
+      const int row = 4 * ty + i;
+      lim[i] = row >= nrow ? 0 : a.causal ? max(0, pc.q.kv - pc.q.n + (f0 + row) / a.G + 1) : pc.q.kv;
+      m[i] = -INFINITY;
+      l[i] = 0.f;
 #pragma unroll
       for (int c = 0; c < NC; ++c) o[i][c] = 0.f;
+    }
+    __syncthreads();
+    fetch(pc.kt0);
     for (int kt = pc.kt0; kt < pc.kt1; ++kt) {
+      fetch(kt + 1);
+      const int page = page_of(kt + 2);
+      copy_wait<1>();
+      __syncthreads();  // tile kt has landed
+      const T* ks = s.k[kt & 1];
+      const T* vs = s.v[kt & 1];
       const int k0 = kt * BN;
-      __syncthreads();  // the queries' offsets, or the previous tile, are done with
-      if (tid < BN) {
-        const int p = k0 + tid;
-        long long ko = -1, vo = -1;
-        if (p < pc.q.kv) {
-          const int page = a.table[(long long)pc.r * a.max_pages + p / a.P];
-          if (page < 0 || page >= a.num_pages) {
-            record_error(a.err, DFLASH_ERR_INVALID);
-          } else {
-            const long long row = ((long long)(p % a.P) * a.Hkv + pc.h) * D;
-            ko = page * a.kps + row;
-            vo = page * a.vps + row;
-          }
-        }
-        s.koff[tid] = ko;
-        s.voff[tid] = vo;
-      }
-      __syncthreads();
-      load_rows<T, S::kStride>(s.kv, static_cast<const T*>(a.kc), s.koff, BN, D);
-      __syncthreads();
       // scores: rows 4 ty .., columns tx + TX j
       float x[4][CT];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < CT; ++j) x[i][j] = 0.f;
-#pragma unroll 2
+#pragma unroll 4
       for (int d = 0; d < D; d += 4) {
         float4 kk[CT];
 #pragma unroll
-        for (int j = 0; j < CT; ++j) kk[j] = *reinterpret_cast<const float4*>(s.kv + (tx + TX * j) * S::kStride + d);
+        for (int j = 0; j < CT; ++j) kk[j] = load4(ks + (tx + TX * j) * C::kStride + d);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float4 qq = *reinterpret_cast<const float4*>(s.q + (4 * ty + i) * S::kStride + d);
+          const float4 qq = load4(s.q + (4 * ty + i) * C::kQStride + d);
 #pragma unroll
           for (int j = 0; j < CT; ++j)
             x[i][j] = fmaf(qq.x, kk[j].x, fmaf(qq.y, kk[j].y, fmaf(qq.z, kk[j].z, fmaf(qq.w, kk[j].w, x[i][j]))));
         }
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < CT; ++j) s.p[(4 * ty + i) * S::kPStride + tx + TX * j] = x[i][j];
-      __syncthreads();
-      load_rows<T, S::kStride>(s.kv, static_cast<const T*>(a.vc), s.voff, BN, D);
-      // softmax: a warp takes whole rows, two columns a lane
-#pragma unroll
-      for (int i = 0; i < BM / 8; ++i) {
-        const int row = warp + 8 * i;
-        float* pr = s.p + row * S::kPStride;
-        const int lim = s.lim[row] - k0;
-        const float x0 = lane < lim ? pr[lane] : -INFINITY;
-        const float x1 = lane + 32 < lim ? pr[lane + 32] : -INFINITY;
-        float mx = fmaxf(x0, x1);
-#pragma unroll
-        for (int w = 16; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-        const float m0 = s.m[row];
-        const float m1 = fmaxf(m0, mx * a.scale_log2);
-        const float mm = m1 == -INFINITY ? 0.f : m1;
-        // scaled and moved in one rounding: of large scores only the difference is rounded
-        const float p0 = exp2f(fmaf(x0, a.scale_log2, -mm)), p1 = exp2f(fmaf(x1, a.scale_log2, -mm));
-        pr[lane] = p0;
-        pr[lane + 32] = p1;
-        float sum = p0 + p1;
-#pragma unroll
-        for (int w = 16; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-        if (lane == 0) {
-          const float al = exp2f(m0 - mm);
-          s.alpha[row] = al;
-          s.l[row] = s.l[row] * al + sum;
-          s.m[row] = m1;
-        }
-        __syncwarp();
-      }
-      __syncthreads();
-#pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float al = s.alpha[4 * ty + i];
+        float mx = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < CT; ++j) {
+          if (k0 + tx + TX * j >= lim[i]) x[i][j] = -INFINITY;
+          mx = fmaxf(mx, x[i][j]);
+        }
+#pragma unroll
+        for (int w = TX / 2; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w, TX));
+        const float m1 = fmaxf(m[i], mx * a.scale_log2);
+        const float mm = m1 == -INFINITY ? 0.f : m1;
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < CT; ++j) {
+          // scaled and moved in one rounding: of large scores only the difference is rounded
+          const float e = exp2f(fmaf(x[i][j], a.scale_log2, -mm));
+          s.p[(4 * ty + i) * C::kPStride + tx + TX * j] = e;
+          sum += e;
+        }
+#pragma unroll
+        for (int w = TX / 2; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w, TX);
+        const float al = exp2f(m[i] - mm);
+        l[i] = l[i] * al + sum;
+        m[i] = m1;
 #pragma unroll
         for (int c = 0; c < NC; ++c) o[i][c] *= al;
       }
+      __syncwarp();  // the rows' weights, written by this warp alone
 #pragma unroll 2
       for (int k = 0; k < BN; k += 4) {
         float pp[4][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float4 v = *reinterpret_cast<const float4*>(s.p + (4 * ty + i) * S::kPStride + k);
-          pp[i][0] = v.x; pp[i][1] = v.y; pp[i][2] = v.z; pp[i][3] = v.w;
+          const float4 w = load4(s.p + (4 * ty + i) * C::kPStride + k);
+          pp[i][0] = w.x; pp[i][1] = w.y; pp[i][2] = w.z; pp[i][3] = w.w;
         }
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
@@ -213,15 +220,13 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const __grid_c
 #pragma unroll
             for (int e = 0; e < VW; ++e) vv[e] = 0.f;
             if (c0 < D) {
-              const float* vp = s.kv + (k + kk) * S::kStride + c0;
+              const T* vp = vs + (k + kk) * C::kStride + c0;
               if constexpr (VW == 4) {
-                const float4 v = *reinterpret_cast<const float4*>(vp);
-                vv[0] = v.x; vv[1] = v.y; vv[2] = v.z; vv[3] = v.w;
-              } else if constexpr (VW == 2) {
-                const float2 v = *reinterpret_cast<const float2*>(vp);
-                vv[0] = v.x; vv[1] = v.y;
+                const float4 w = load4(vp);
+                vv[0] = w.x; vv[1] = w.y; vv[2] = w.z; vv[3] = w.w;
               } else {
-                vv[0] = *vp;
+#pragma unroll
+                for (int e = 0; e < VW; ++e) vv[e] = to_f32(vp[e]);
               }
             }
 #pragma unroll
@@ -230,16 +235,18 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const __grid_c
               for (int e = 0; e < VW; ++e) o[i][u * VW + e] = fmaf(pp[i][kk], vv[e], o[i][u * VW + e]);
           }
       }
+      put_offsets(kt + 2, page);
+      __syncthreads();  // this stage's buffers may be filled again; the offsets are in place
     }
+    copy_wait<0>();
     // the piece's rows: finished, or left for the merge
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int row = 4 * ty + i;
       if (row >= nrow) continue;
-      const float l = s.l[row];
       if (pc.slot < 0) {
         const int tok = (f0 + row) / a.G, head = pc.h * a.G + (f0 + row) % a.G;
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
         T* dst = static_cast<T*>(a.out) + ((long long)(pc.q.q0 + tok) * a.Hq + head) * D;
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -250,7 +257,7 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const __grid_c
           }
         if (a.lse && tx == 0)
           a.lse[(long long)head * a.total_q + pc.q.q0 + tok] =
-              l > 0.f ? (s.m[row] + log2f(l)) * 0.6931471805599453f : -INFINITY;
+              l[i] > 0.f ? (m[i] + log2f(l[i])) * 0.6931471805599453f : -INFINITY;
       } else {
         const long long at = (long long)pc.slot * a.rows + row;
 #pragma unroll
@@ -260,7 +267,7 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const __grid_c
             const int c = (tx + TX * u) * VW + e;
             if (c < D) a.part_o[at * D + c] = o[i][u * VW + e];
           }
-        if (tx == 0) a.part_ml[at] = make_float2(s.m[row], l);
+        if (tx == 0) a.part_ml[at] = make_float2(m[i], l[i]);
       }
     }
     if (pc.slot >= 0 && pc.shared) meta = pack_meta(pc);
@@ -326,23 +333,27 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const __grid_constant_
 }
 
 template <typename T, int BM, int DMAX>
-cudaError_t run_simt(const PagedArgs& a, int sms, int* grid, cudaStream_t s) {
-  const size_t smem = sizeof(SimtSmem<BM, DMAX>);
+cudaError_t run_simt(const PagedArgs& a, int sms, int most, int* grid, cudaStream_t s) {
+  using C = Simt<T, BM, DMAX>;
+  const size_t smem = sizeof(typename C::Smem);
+  static_assert(sizeof(typename C::Smem) <= 232448, "shared memory budget");
   auto kernel = paged_simt_kernel<T, BM, DMAX>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  // two CTAs an SM where two fit, so that one loads while the other multiplies
-  *grid = sms * (2 * (smem + 1024) <= 228 * 1024 ? 2 : 1);
-  kernel<<<*grid, kSimtThreads, smem, s>>>(a);
+  // as many CTAs an SM as fit, so that some copy while others multiply
+  int per_sm = (int)(228 * 1024 / (smem + 1024));
+  if (per_sm > (BM == 16 ? kSimtPerSm16 : kSimtPerSm64)) per_sm = BM == 16 ? kSimtPerSm16 : kSimtPerSm64;
+  *grid = sms * per_sm < most ? sms * per_sm : most;
+  kernel<<<*grid, C::kThreads, smem, s>>>(a);
   count_launch();
   return cudaGetLastError();
 }
 
 template <typename T, int BM>
-cudaError_t pick_simt(const PagedArgs& a, int sms, int* grid, cudaStream_t s) {
-  if (a.D <= 64) return run_simt<T, BM, 64>(a, sms, grid, s);
-  if (a.D <= 128) return run_simt<T, BM, 128>(a, sms, grid, s);
-  return run_simt<T, BM, 256>(a, sms, grid, s);
+cudaError_t pick_simt(const PagedArgs& a, int sms, int most, int* grid, cudaStream_t s) {
+  if (a.D <= 64) return run_simt<T, BM, 64>(a, sms, most, grid, s);
+  if (a.D <= 128) return run_simt<T, BM, 128>(a, sms, most, grid, s);
+  return run_simt<T, BM, 256>(a, sms, most, grid, s);
 }
 
 int simt_rows(int G, int max_q) { return (long long)G * max_q <= 16 ? 16 : 64; }
@@ -364,7 +375,7 @@ PagedPlan plan_of(bool bf16, int Hq, int Hkv, int D, int max_q, int P) {
   const int G = Hq / Hkv;
   p.tc = use_tensor_cores(bf16, G, D, P);
   p.rows = p.tc ? paged_tc_rows(G, max_q) : simt_rows(G, max_q);
-  p.max_grid = p.tc ? kSms : kSimtMaxGrid;
+  p.max_grid = p.tc ? kSms : p.rows == 16 ? kSimtMaxGrid : kSimtPerSm64 * kSms;
   const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   const size_t slots = 2 * (size_t)p.max_grid * p.rows;
   p.ml = up(kSimtMaxGrid * sizeof(int4));
@@ -395,15 +406,19 @@ cudaError_t launch_attn_paged(PagedArgs a, bool bf16, void* ws, cudaStream_t str
   int grid = sms;
   cudaError_t e;
   // Without a page there is no tensor to describe to TMA: the CUDA-core kernel with
-  // its small row tiles (2 x 152 CTAs x 16 rows fit the 152 x 65 or more planned).
+  // its small row tiles (2 x 304 slots of 16 rows fit the planned 2 x 152 of 65 or more).
   if (p.tc && a.num_pages > 0) {
     e = launch_paged_tc(a, grid, stream);
   } else {
+    const int most = p.tc ? 2 * kSms : p.max_grid;
     if (p.tc) a.rows = 16;
+    if (a.num_pages == 0) a.kc = a.vc = a.q;  // every copy is one of no bytes, from an address that exists
     if (a.rows == 16)
-      e = bf16 ? pick_simt<__nv_bfloat16, 16>(a, sms, &grid, stream) : pick_simt<float, 16>(a, sms, &grid, stream);
+      e = bf16 ? pick_simt<__nv_bfloat16, 16>(a, sms, most, &grid, stream)
+               : pick_simt<float, 16>(a, sms, most, &grid, stream);
     else
-      e = bf16 ? pick_simt<__nv_bfloat16, 64>(a, sms, &grid, stream) : pick_simt<float, 64>(a, sms, &grid, stream);
+      e = bf16 ? pick_simt<__nv_bfloat16, 64>(a, sms, most, &grid, stream)
+               : pick_simt<float, 64>(a, sms, most, &grid, stream);
   }
   if (e != cudaSuccess) return e;
   const dim3 mg(grid, (a.rows + 3) / 4);

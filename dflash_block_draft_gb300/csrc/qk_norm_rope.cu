@@ -21,20 +21,19 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Four components as they lie in memory.
+// Four components as they lie in memory; in registers they are pairs, for the
+// packed fp32 instructions (these kernels issue about as long as they load).
 template <typename T>
 struct Raw;
 template <>
 struct Raw<__nv_bfloat16> {
   uint2 v;
-  __device__ __forceinline__ void unpack(float* x) const {
-    x[0] = __uint_as_float(v.x << 16);
-    x[1] = __uint_as_float(v.x & 0xFFFF0000u);
-    x[2] = __uint_as_float(v.y << 16);
-    x[3] = __uint_as_float(v.y & 0xFFFF0000u);
+  __device__ __forceinline__ void unpack(float2* x) const {
+    x[0] = make_float2(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u));
+    x[1] = make_float2(__uint_as_float(v.y << 16), __uint_as_float(v.y & 0xFFFF0000u));
   }
-  __device__ __forceinline__ void pack(const float* x) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
+  __device__ __forceinline__ void pack(const float2* x) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(x[0].x, x[0].y), b = __floats2bfloat162_rn(x[1].x, x[1].y);
     v.x = *reinterpret_cast<const uint32_t*>(&a);
     v.y = *reinterpret_cast<const uint32_t*>(&b);
   }
@@ -42,8 +41,11 @@ struct Raw<__nv_bfloat16> {
 template <>
 struct Raw<float> {
   float4 v;
-  __device__ __forceinline__ void unpack(float* x) const { x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w; }
-  __device__ __forceinline__ void pack(const float* x) { v = make_float4(x[0], x[1], x[2], x[3]); }
+  __device__ __forceinline__ void unpack(float2* x) const {
+    x[0] = make_float2(v.x, v.y);
+    x[1] = make_float2(v.z, v.w);
+  }
+  __device__ __forceinline__ void pack(const float2* x) { v = make_float4(x[0].x, x[0].y, x[1].x, x[1].y); }
 };
 
 // A lane's 8 components of a head: 4 at `a`, 4 at `b`; angles ang .. ang + 3.
@@ -73,31 +75,32 @@ struct Part {
     *reinterpret_cast<Raw<T>*>(head + p.a) = a;
     *reinterpret_cast<Raw<T>*>(head + p.b) = b;
   }
-  __device__ __forceinline__ void unpack(float* x) const {
+  __device__ __forceinline__ void unpack(float2* x) const {
     a.unpack(x);
-    b.unpack(x + 4);
+    b.unpack(x + 2);
   }
-  __device__ __forceinline__ void pack(const float* x) {
+  __device__ __forceinline__ void pack(const float2* x) {
     a.pack(x);
-    b.pack(x + 4);
+    b.pack(x + 2);
   }
 };
 
-// x := x rotated; with the sines' signs turned, rotated back.
-__device__ __forceinline__ void rotate8(float* x, const float* cs, const float* sn, int interleaved) {
+// x := x rotated; with the sines' signs turned, rotated back.  cs, sn: the lane's
+// four angles in pairs.
+__device__ __forceinline__ void rotate8(float2* x, const float2* cs, const float2* sn, int interleaved) {
   if (interleaved) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float u = x[2 * e], v = x[2 * e + 1];
-      x[2 * e] = u * cs[e] - v * sn[e];
-      x[2 * e + 1] = v * cs[e] + u * sn[e];
+      const float c = e & 1 ? cs[e / 2].y : cs[e / 2].x, s = e & 1 ? sn[e / 2].y : sn[e / 2].x;
+      const float2 u = x[e];
+      x[e] = __ffma2_rn(make_float2(u.y, u.x), make_float2(-s, s), __fmul2_rn(u, make_float2(c, c)));
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float u = x[e], v = x[4 + e];
-      x[e] = u * cs[e] - v * sn[e];
-      x[4 + e] = v * cs[e] + u * sn[e];
+    for (int e = 0; e < 2; ++e) {
+      const float2 u = x[e], v = x[2 + e], neg = make_float2(-sn[e].x, -sn[e].y);
+      x[e] = __ffma2_rn(v, neg, __fmul2_rn(u, cs[e]));
+      x[2 + e] = __ffma2_rn(u, sn[e], __fmul2_rn(v, cs[e]));
     }
   }
 }
@@ -116,31 +119,10 @@ struct Place {
   long long krow, vrow;
 };
 
-// Request lo of token t and the rest of its placement; records what has no place.
-__device__ __forceinline__ Place place_in(const RopeArgs& a, int t, int lo) {
-  Place pl = {0, 0, 0, 0};
-  const int q0 = a.q_off[lo], q1 = a.q_off[lo + 1];
-  const long long p = (long long)a.kv_lens[lo] - (q1 - q0) + (t - q0);
-  if (q0 < 0 || q0 > t || q1 <= t || q1 > a.T || p < 0 || p >= (long long)a.max_pages * a.P ||
-      (a.rot > 0 && p >= a.max_pos)) {
-    record_error(a.err, DFLASH_ERR_INVALID);
-    return pl;
-  }
-  const int page = a.table[(long long)lo * a.max_pages + p / a.P];
-  if (page < 0 || page >= a.num_pages) {
-    record_error(a.err, DFLASH_ERR_INVALID);
-    return pl;
-  }
-  const long long row = (p % a.P) * (long long)a.Hkv * a.D;
-  pl.ok = 1;
-  pl.pos = (int)p;
-  pl.krow = page * a.kps + row;
-  pl.vrow = page * a.vps + row;
-  return pl;
-}
-
-// Whole warp: the placement of token t (the same in every lane).  The request is
-// found 32 offsets at a time.
+// Whole warp: the placement of token t (the same in every lane); what has no place
+// is recorded.  The request is found 32 offsets at a time, and what the last 32
+// candidates need is loaded together, so that the chain of dependent loads is short:
+// offsets and lengths, the page, (the caller's) table row.
 template <bool PAGED>
 __device__ __forceinline__ Place place_token(const RopeArgs& a, int t) {
   Place pl = {0, 0, 0, 0};
@@ -152,9 +134,9 @@ __device__ __forceinline__ Place place_token(const RopeArgs& a, int t) {
     return pl;
   }
   const int lane = threadIdx.x & 31;
+  const int end = a.q_off[a.R];
   int lo = 0, n = a.R;  // the last request that begins at or before t lies in [lo, lo + n)
-  const bool pad = t >= a.q_off[a.R];  // padding behind the last request
-  while (n > 1) {
+  while (n > 32) {
     const int step = (n + 31) / 32;
     const int at = lane * step;
     const unsigned m = __ballot_sync(0xffffffffu, at < n && a.q_off[lo + at] <= t);
@@ -162,7 +144,35 @@ __device__ __forceinline__ Place place_token(const RopeArgs& a, int t) {
     lo += k * step;
     n = min(step, n - k * step);
   }
-  return pad ? pl : place_in(a, t, lo);
+  int q0 = 0, q1 = 0, len = 0;
+  if (lane < n) {
+    q0 = a.q_off[lo + lane];
+    q1 = a.q_off[lo + lane + 1];
+    len = a.kv_lens[lo + lane];
+  }
+  const unsigned m = __ballot_sync(0xffffffffu, lane < n && q0 <= t);
+  const int k = m ? 31 - __clz(m) : 0;
+  q0 = __shfl_sync(0xffffffffu, q0, k);
+  q1 = __shfl_sync(0xffffffffu, q1, k);
+  len = __shfl_sync(0xffffffffu, len, k);
+  if (t >= end) return pl;  // padding behind the last request
+  const long long p = (long long)len - (q1 - q0) + (t - q0);
+  if (q0 < 0 || q0 > t || q1 <= t || q1 > a.T || p < 0 || p >= (long long)a.max_pages * a.P ||
+      (a.rot > 0 && p >= a.max_pos)) {
+    record_error(a.err, DFLASH_ERR_INVALID);
+    return pl;
+  }
+  const int pp = (int)p, page = a.table[(long long)(lo + k) * a.max_pages + pp / a.P];
+  if (page < 0 || page >= a.num_pages) {
+    record_error(a.err, DFLASH_ERR_INVALID);
+    return pl;
+  }
+  const long long row = (long long)(pp % a.P) * a.Hkv * a.D;
+  pl.ok = 1;
+  pl.pos = pp;
+  pl.krow = page * a.kps + row;
+  pl.vrow = page * a.vps + row;
+  return pl;
 }
 
 // Forward.  A block takes TB tokens and all their heads (q, then k, then, paged,
@@ -181,25 +191,38 @@ __global__ void __launch_bounds__(kThreads) rope_fwd_kernel(const __grid_constan
   const int units = (int)min((long long)tb, a.T - t0) * heads;
   const LanePart lp = lane_part(a, lane);
   Part<T> x[kBatch];
-  auto fetch = [&](int u0) {
+  // Unit u is head u % heads of token u / heads; a group's units are kGroups apart.
+  int hf = group, tf = 0;  // of the next unit to fetch
+  auto fetch = [&]() {
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
-      const int u = u0 + j * kGroups;
-      if (u < units && lp.in) {
-        const int h = u % heads;
-        const long long t = t0 + u / heads;
-        const T* src = h < a.Hq ? static_cast<const T*>(a.q) + t * a.qs + (long long)h * a.D
-                       : !PAGED || h < a.Hq + a.Hkv
-                           ? static_cast<const T*>(a.k) + t * a.ks + (long long)(h - a.Hq) * a.D
-                           : static_cast<const T*>(a.v) + t * a.vs + (long long)(h - a.Hq - a.Hkv) * a.D;
-        x[j].load(src, lp);
+      while (hf >= heads) {
+        hf -= heads;
+        ++tf;
       }
+      if (tf * heads + hf < units && lp.in) {
+        const bool is_q = hf < a.Hq, is_v = PAGED && hf >= a.Hq + a.Hkv;
+        const T* base = static_cast<const T*>(is_q ? a.q : is_v ? a.v : a.k);
+        const long long stride = is_q ? a.qs : is_v ? a.vs : a.ks;
+        const int h = is_q ? hf : is_v ? hf - a.Hq - a.Hkv : hf - a.Hq;
+        x[j].load(base + (t0 + tf) * stride + h * a.D, lp);
+      }
+      hf += kGroups;
     }
   };
-  fetch(group);
-  Part<T> wq, wk;
-  if (lp.in && a.wq) wq.load(static_cast<const T*>(a.wq), lp);
-  if (lp.in && a.wk) wk.load(static_cast<const T*>(a.wk), lp);
+  fetch();
+  float2 wq[4], wk[4];
+  {
+    Part<T> w;
+    if (lp.in && a.wq) {
+      w.load(static_cast<const T*>(a.wq), lp);
+      w.unpack(wq);
+    }
+    if (lp.in && a.wk) {
+      w.load(static_cast<const T*>(a.wk), lp);
+      w.unpack(wk);
+    }
+  }
   if (warp < tb) {
     const long long t = t0 + warp;
     const Place pl = place_token<PAGED>(a, (int)min(t, (long long)a.T));
@@ -210,47 +233,54 @@ __global__ void __launch_bounds__(kThreads) rope_fwd_kernel(const __grid_constan
     }
   }
   __syncthreads();
-  for (int u0 = group; u0 - group < units; u0 += kBatch * kGroups) {
-    if (u0 != group) fetch(u0);
+  const float inv_d = 1.f / (float)a.D;
+  int h = group, tk = 0;
+  for (int u0 = 0; u0 < units; u0 += kBatch * kGroups) {
+    if (u0) fetch();
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
-      const int u = u0 + j * kGroups;
-      const int h = u % heads, tk = u < units ? u / heads : 0;
+      if (u0 + j * kGroups >= units) break;  // the whole block is done
+      while (h >= heads) {
+        h -= heads;
+        ++tk;
+      }
       const bool is_q = h < a.Hq, is_v = PAGED && h >= a.Hq + a.Hkv;
-      const bool ok = u < units && lp.in && s_place[tk].ok;
-      float y[8];
+      const bool ok = tk * heads + h < units && lp.in && s_place[tk < tb ? tk : 0].ok;
+      if (__any_sync(0xffffffffu, ok && !is_v)) {  // values are copied as they are
+        float2 y[4];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = 0.f;
-      if (ok && !is_v) x[j].unpack(y);
-      float ss = 0.f;
+        for (int e = 0; e < 4; ++e) y[e] = make_float2(0.f, 0.f);
+        if (ok) x[j].unpack(y);
+        if (a.wq || a.wk) {  // the sum takes the whole warp, whose groups may hold both kinds
+          float2 s2 = __fmul2_rn(y[0], y[0]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
-      ss = group_sum<LANES>(ss);
-      if (!ok) continue;
-      if (!is_v) {
-        if (is_q ? a.wq != nullptr : a.wk != nullptr) {
-          const float r = rsqrtf(ss / (float)a.D + a.eps);
-          float w[8];
-          if (is_q) wq.unpack(w);
-          else wk.unpack(w);
+          for (int e = 1; e < 4; ++e) s2 = __ffma2_rn(y[e], y[e], s2);
+          const float r = rsqrtf(group_sum<LANES>(s2.x + s2.y) * inv_d + a.eps);
+          if (is_q ? a.wq != nullptr : a.wk != nullptr) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] *= r * w[e];
+            for (int e = 0; e < 4; ++e)
+              y[e] = __fmul2_rn(__fmul2_rn(y[e], make_float2(r, r)), is_q ? wq[e] : wk[e]);
+          }
         }
         if (lp.turned) {
-          const float4* row = s_cs + tk * (DFLASH_PAGED_MAX_D / 4) + lane;
+          const float4* row = s_cs + (tk < tb ? tk : 0) * (DFLASH_PAGED_MAX_D / 4) + lane;
           const float4 c = row[0], sn = row[a.rot / 8];
-          const float cv[4] = {c.x, c.y, c.z, c.w}, sv[4] = {sn.x, sn.y, sn.z, sn.w};
+          const float2 cv[2] = {make_float2(c.x, c.y), make_float2(c.z, c.w)};
+          const float2 sv[2] = {make_float2(sn.x, sn.y), make_float2(sn.z, sn.w)};
           rotate8(y, cv, sv, a.interleaved);
         }
-        x[j].pack(y);
+        if (!is_v) x[j].pack(y);
       }
-      const long long t = t0 + tk;
-      T* dst;
-      if (is_q) dst = static_cast<T*>(a.qo) + (t * a.Hq + h) * a.D;
-      else if (!PAGED) dst = static_cast<T*>(a.ko) + (t * a.Hkv + (h - a.Hq)) * a.D;
-      else if (!is_v) dst = static_cast<T*>(a.kc) + s_place[tk].krow + (long long)(h - a.Hq) * a.D;
-      else dst = static_cast<T*>(a.vc) + s_place[tk].vrow + (long long)(h - a.Hq - a.Hkv) * a.D;
-      x[j].store(dst, lp);
+      if (ok) {
+        const long long t = t0 + tk;
+        T* dst;
+        if (is_q) dst = static_cast<T*>(a.qo) + t * a.Hq * a.D + h * a.D;
+        else if (!PAGED) dst = static_cast<T*>(a.ko) + t * a.Hkv * a.D + (h - a.Hq) * a.D;
+        else if (!is_v) dst = static_cast<T*>(a.kc) + s_place[tk].krow + (h - a.Hq) * a.D;
+        else dst = static_cast<T*>(a.vc) + s_place[tk].vrow + (h - a.Hq - a.Hkv) * a.D;
+        x[j].store(dst, lp);
+      }
+      h += kGroups;
     }
   }
 }
@@ -278,9 +308,9 @@ __global__ void __launch_bounds__(kThreads)
   const long long stride = is_q ? a.qs : a.ks;
   const bool normed = w != nullptr;
   const LanePart lp = lane_part(a, lane);
-  float wv[8], dw[8];
+  float2 wv[4], dw[4];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) wv[e] = dw[e] = 0.f;
+  for (int e = 0; e < 4; ++e) wv[e] = dw[e] = make_float2(0.f, 0.f);
   if (normed && lp.in) {
     Part<T> wr;
     wr.load(w, lp);
@@ -293,54 +323,60 @@ __global__ void __launch_bounds__(kThreads)
   for (int base = brow * kGroups; base < a.T; base += step, t += step) {
     const bool ok = t < a.T && (a.rot <= 0 || (pos >= 0 && pos < a.max_pos));
     if (t < a.T && !ok) record_error(a.err, DFLASH_ERR_INVALID);
-    float cs[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
+    const bool have = ok && lp.in;
+    float2 cs[2] = {make_float2(1.f, 1.f), make_float2(1.f, 1.f)}, sn[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
     if (ok && lp.turned) {
       const float* row = a.cs + (long long)pos * a.rot + lp.ang;
       const float4 c = *reinterpret_cast<const float4*>(row), s = *reinterpret_cast<const float4*>(row + (a.rot >> 1));
-      cs[0] = c.x; cs[1] = c.y; cs[2] = c.z; cs[3] = c.w;
-      sn[0] = -s.x; sn[1] = -s.y; sn[2] = -s.z; sn[3] = -s.w;
+      cs[0] = make_float2(c.x, c.y);
+      cs[1] = make_float2(c.z, c.w);
+      sn[0] = make_float2(-s.x, -s.y);
+      sn[1] = make_float2(-s.z, -s.w);
     }
     if (a.rot > 0 && t + step < a.T) pos = a.pos[t + step];
+    const long long row_in = t * stride, row_out = (long long)t * H * a.D;
     for (int hb = h0; hb < h1; hb += kBatch) {
       Part<T> xr[kBatch], gr[kBatch];
 #pragma unroll
       for (int j = 0; j < kBatch; ++j)
-        if (ok && lp.in && hb + j < h1) {
-          gr[j].load(dsrc + ((long long)t * H + hb + j) * a.D, lp);
-          if (normed) xr[j].load(src + t * stride + (long long)(hb + j) * a.D, lp);
+        if (have && hb + j < h1) {
+          gr[j].load(dsrc + row_out + (hb + j) * a.D, lp);
+          if (normed) xr[j].load(src + row_in + (hb + j) * a.D, lp);
         }
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
-        const bool have = ok && lp.in && hb + j < h1;
-        float g[8], x[8];
+        if (hb + j >= h1) break;  // the whole block's
+        float2 g[4], x[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) g[e] = x[e] = 0.f;
+        for (int e = 0; e < 4; ++e) g[e] = x[e] = make_float2(0.f, 0.f);
         if (have) {
           gr[j].unpack(g);
           if (normed) xr[j].unpack(x);
         }
         if (lp.turned) rotate8(g, cs, sn, a.interleaved);
         if (normed) {
-          float ss = 0.f, dot = 0.f, gw[8];
+          float2 gw[4], s2 = __fmul2_rn(x[0], x[0]), d2;
+          gw[0] = __fmul2_rn(g[0], wv[0]);
+          d2 = __fmul2_rn(gw[0], x[0]);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            gw[e] = g[e] * wv[e];
-            ss = fmaf(x[e], x[e], ss);
-            dot = fmaf(gw[e], x[e], dot);
+          for (int e = 1; e < 4; ++e) {
+            gw[e] = __fmul2_rn(g[e], wv[e]);
+            s2 = __ffma2_rn(x[e], x[e], s2);
+            d2 = __ffma2_rn(gw[e], x[e], d2);
           }
-          ss = group_sum<LANES>(ss);
-          dot = group_sum<LANES>(dot);
-          const float r = rsqrtf(ss * inv_d + a.eps);
-          const float c = dot * r * r * inv_d * r;  // r times mean(g w x^) r, the factor of x
+          const float r = rsqrtf(group_sum<LANES>(s2.x + s2.y) * inv_d + a.eps);
+          // r times mean(g w x^) r, the factor of x
+          const float c = -group_sum<LANES>(d2.x + d2.y) * r * r * inv_d * r;
+          const float2 r2 = make_float2(r, r), c2 = make_float2(c, c);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            dw[e] = fmaf(g[e], x[e] * r, dw[e]);
-            g[e] = gw[e] * r - x[e] * c;
+          for (int e = 0; e < 4; ++e) {
+            dw[e] = __ffma2_rn(g[e], __fmul2_rn(x[e], r2), dw[e]);
+            g[e] = __ffma2_rn(x[e], c2, __fmul2_rn(gw[e], r2));
           }
         }
         if (have) {
           gr[j].pack(g);
-          gr[j].store(dst + ((long long)t * H + hb + j) * a.D, lp);
+          gr[j].store(dst + row_out + (hb + j) * a.D, lp);
         }
       }
     }
@@ -348,8 +384,8 @@ __global__ void __launch_bounds__(kThreads)
   if (lp.in) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      red[group][lp.a + e] = dw[e];
-      red[group][lp.b + e] = dw[4 + e];
+      red[group][lp.a + e] = e & 1 ? dw[e / 2].y : dw[e / 2].x;
+      red[group][lp.b + e] = e & 1 ? dw[2 + e / 2].y : dw[2 + e / 2].x;
     }
   }
   __syncthreads();

@@ -7,19 +7,24 @@
 //
 // What has to be read is one row of p and one of q, 8 bytes for each entry of the
 // vocabulary, so large batches are bound by memory and small ones by the chain of
-// dependent steps.  A cluster of 8 CTAs takes a request: every CTA finds the
+// dependent steps.  A cluster of 1 to 8 CTAs takes a request: every CTA finds the
 // rejected position for itself (a few gathered values, cheaper than a round trip
-// through the cluster), adds up its eighth of the row, and one exchange of the 8
+// through the cluster), adds up its share of the row, and one exchange of the
 // sums through distributed shared memory tells all of them which CTA holds the
-// drawn entry.  That one narrows it down to a warp's run from the warps' sums,
-// and the warp walks its run (in L2 by now) once more.  One launch, no workspace.
+// drawn entry.  Its warps' sums, and the sums of the up to 32 segments of the
+// warp that holds it, narrow it down to one segment, which that warp walks once
+// more (in L2 by now).  One launch, no workspace.
 //
-// Sums are exact: every weight is an integer multiple of 2^-50, held in 64-bit
-// integers (a row of a distribution sums to about 2^50).  So neither the order of
-// the sum nor the number of CTAs changes the result, and an entry next to the
-// border is decided as in the real numbers up to 2^-50 a weight; fp32 sums
-// (2^-24) would draw another entry in every few hundredth row of a large
-// vocabulary, and fp64 adds run at a fraction of the integer rate.
+// Sums are exact: a weight is held in whole steps of 2^-45, and those are added up
+// as integers (a row of a distribution sums to about 2^45), so that neither the
+// order of the sum nor the number of CTAs changes the result, and an entry next
+// to the border is decided as in the real numbers up to 2^-46 a weight.  (fp32
+// sums would draw another entry in every few hundredth row of a large vocabulary;
+// fp64 adds run at a fraction of the integer rate.)  The steps come from the adder:
+// the bits of 1 + p count steps of 2^-23, what that addition lost is exact in fp32,
+// and the bits of its sum with 1.5 2^-22 count steps of 2^-45.  Eleven instructions
+// an entry; 64-bit conversions took 85 us for 128 rows of 131072, shifts of the
+// fraction 47 us, and the reads alone take 20.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -30,19 +35,27 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kCluster = 8;
-constexpr int kThreads = 512;
+constexpr int kMaxCluster = 8;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kStep = 128;  // entries a warp reads at once: a float4 a lane
+constexpr int kStep = 128;    // entries a warp reads at once: a float4 a lane
+constexpr int kUnroll = 4;    // such reads in flight; a segment is a multiple of kStep * kUnroll entries
+constexpr int kSegments = 32; // most segments of a warp's run
 
-// A probability in steps of 2^-50; outside [0, 1] clamped, NaN counts as 0.
-__device__ __forceinline__ unsigned long long fixed50(float p) {
-  return __float2ull_rn(fminf(fmaxf(p, 0.f), 1.f) * 0x1p50f);
+// Weight of one entry, max(p - q, 0), as steps of 2^-23 and of 2^-45 (signed) that
+// belong together.  No weight where p > q does not hold, NaN included.
+constexpr float kBias = 0x1.8p-22f;  // sums with it lie in [2^-22, 2^-21): their last bit is 2^-45
+__device__ __forceinline__ void add_weight(float p, float q, bool on, int& hi, int& lo) {
+  const float tp = 1.f + p, tq = 1.f + q;
+  const float rest = (p - (tp - 1.f)) - (q - (tq - 1.f));  // at most 2^-23; exact terms, one rounding
+  const float t = rest + kBias;
+  if (on && p > q) {
+    hi += __float_as_int(tp) - __float_as_int(tq);
+    lo += __float_as_int(t) - __float_as_int(kBias);
+  }
 }
-
-__device__ __forceinline__ unsigned long long weight(float p, float q) {
-  const unsigned long long a = fixed50(p), b = fixed50(q);
-  return a > b ? a - b : 0ull;
+__device__ __forceinline__ unsigned long long join(int hi, int lo) {
+  return (unsigned long long)(((long long)hi << 22) + lo);
 }
 
 __device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
@@ -57,50 +70,59 @@ struct Row {
   int skip;            // entry with weight 0 (-1: none)
 };
 
-// Weights of the four entries at i (i + 3 may lie beyond `end`: weight 0).
+// Four entries of p and q at i; those at and beyond `end` are 0.
+struct Four {
+  float p[4], q[4];
+};
 template <bool VEC>
-__device__ __forceinline__ void weights4(const Row& r, long long i, long long end, unsigned long long* w) {
-  float p[4], q[4] = {0.f, 0.f, 0.f, 0.f};
+__device__ __forceinline__ Four load4(const Row& r, long long i, long long end) {
+  Four f = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
   if (VEC) {
-    const float4 a = i < end ? *reinterpret_cast<const float4*>(r.p + i) : make_float4(0.f, 0.f, 0.f, 0.f);
-    p[0] = a.x; p[1] = a.y; p[2] = a.z; p[3] = a.w;
-    if (r.q && i < end) {
-      const float4 b = *reinterpret_cast<const float4*>(r.q + i);
-      q[0] = b.x; q[1] = b.y; q[2] = b.z; q[3] = b.w;
+    if (i < end) {
+      const float4 a = *reinterpret_cast<const float4*>(r.p + i);
+      f.p[0] = a.x; f.p[1] = a.y; f.p[2] = a.z; f.p[3] = a.w;
+      if (r.q) {
+        const float4 b = *reinterpret_cast<const float4*>(r.q + i);
+        f.q[0] = b.x; f.q[1] = b.y; f.q[2] = b.z; f.q[3] = b.w;
+      }
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      p[e] = i + e < end ? r.p[i + e] : 0.f;
-      if (r.q) q[e] = i + e < end ? r.q[i + e] : 0.f;
-    }
+    for (int e = 0; e < 4; ++e)
+      if (i + e < end) {
+        f.p[e] = r.p[i + e];
+        if (r.q) f.q[e] = r.q[i + e];
+      }
   }
-#pragma unroll
-  for (int e = 0; e < 4; ++e) w[e] = i + e == r.skip ? 0ull : weight(p[e], q[e]);
+  return f;
 }
 
-// Sum of the warp's run [lo, hi) (lo a multiple of 4).
+// Sum of [lo, hi) (lo a multiple of 4), over the whole warp.
 template <bool VEC>
-__device__ __forceinline__ unsigned long long run_sum(const Row& r, long long lo, long long hi, int lane) {
+__device__ __forceinline__ unsigned long long segment_sum(const Row& r, long long lo, long long hi, int lane) {
   unsigned long long s = 0;
-#pragma unroll 4
-  for (long long i = lo + 4 * lane; i < hi; i += kStep) {
-    unsigned long long w[4];
-    weights4<VEC>(r, i, hi, w);
-    s += w[0] + w[1] + w[2] + w[3];
+  for (long long i0 = lo + 4 * lane; i0 - 4 * lane < hi; i0 += kStep * kUnroll) {
+    Four f[kUnroll];
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) f[k] = load4<VEC>(r, i0 + k * kStep, hi);
+    int h = 0, l = 0;  // 16 entries: at most 2^27 and 2^26
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) add_weight(f[k].p[e], f[k].q[e], (int)(i0 + k * kStep) + e != r.skip, h, l);
+    s += join(h, l);
   }
   return warp_sum(s);
 }
 
 template <bool VEC>
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
-    verify_kernel(const __grid_constant__ VerifyArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_constant__ VerifyArgs a) {
   __shared__ int s_acc;
-  __shared__ unsigned long long s_warp[kWarps];
+  __shared__ unsigned long long s_warp[kWarps], s_seg[kWarps][kSegments];
   __shared__ unsigned long long s_total[2];  // this CTA's sums: weights, and p alone where those are all zero
   cg::cluster_group cluster = cg::this_cluster();
-  const int rank = (int)cluster.block_rank();
-  const int r = blockIdx.x / kCluster;
+  const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
+  const int r = blockIdx.x / ranks;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int t0 = a.offsets[r], t1 = a.offsets[r + 1];
   const int n = t1 - t0;
@@ -145,13 +167,20 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
   row.p = target + acc * a.ps;
   row.q = acc < n && a.q ? a.q + (t0 + acc) * a.qs : nullptr;
   row.skip = acc < n && !a.q ? a.tokens[t0 + acc] : -1;
-  // Runs: the vocabulary in kCluster * kWarps equal pieces, multiples of 4 entries.
-  const long long piece = ((long long)a.V + 4 * kCluster * kWarps - 1) / (4 * kCluster * kWarps) * 4;
+  // Runs: the vocabulary in equal pieces, one a warp, multiples of 4 entries; a run in
+  // up to kSegments segments.
+  const long long piece = ((long long)a.V + 4 * ranks * kWarps - 1) / (4 * ranks * kWarps) * 4;
+  const long long span = (piece + kSegments * kStep * kUnroll - 1) / (kSegments * kStep * kUnroll) * (kStep * kUnroll);
   const long long lo = min((long long)a.V, (rank * kWarps + warp) * piece), hi = min((long long)a.V, lo + piece);
 
   unsigned long long before = 0, total = 0, mine = 0;
   for (int pass = 0; pass < 2; ++pass) {
-    mine = run_sum<VEC>(row, lo, hi, lane);
+    mine = 0;
+    for (int g = 0; lo + g * span < hi; ++g) {
+      const unsigned long long s = segment_sum<VEC>(row, lo + g * span, min(hi, lo + (g + 1) * span), lane);
+      if (lane == 0) s_seg[warp][g] = s;
+      mine += s;
+    }
     if (lane == 0) s_warp[warp] = mine;
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -163,7 +192,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     }
     cluster.sync();
     before = total = 0;
-    for (int c = 0; c < kCluster; ++c) {
+    for (int c = 0; c < ranks; ++c) {
       const unsigned long long s = *cluster.map_shared_rank(&s_total[pass], c);
       before += c < rank ? s : 0ull;
       total += s;
@@ -181,10 +210,20 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     const unsigned long long bar = (unsigned long long)((double)u * (double)total);
     if (before <= bar && bar < before + mine) {  // one warp of the cluster
       unsigned long long at = before;
-      for (long long i0 = lo; i0 < hi; i0 += kStep) {
+      int g = 0;
+      while (lo + (g + 1) * span < hi && at + s_seg[warp][g] <= bar) at += s_seg[warp][g++];
+      const long long end = min(hi, lo + (g + 1) * span);
+#pragma unroll 4
+      for (long long i0 = lo + g * span; i0 < end; i0 += kStep) {
         const long long i = i0 + 4 * lane;
+        const Four f4 = load4<VEC>(row, i, end);
         unsigned long long w[4];
-        weights4<VEC>(row, i, hi, w);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          int h = 0, l = 0;
+          add_weight(f4.p[e], f4.q[e], (int)i + e != row.skip, h, l);
+          w[e] = join(h, l);
+        }
         const unsigned long long s = w[0] + w[1] + w[2] + w[3];
         unsigned long long c = s;  // inclusive scan over the lanes
 #pragma unroll
@@ -225,9 +264,23 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
 cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t stream) {
   const bool vec = a.V % 4 == 0 && a.ps % 4 == 0 && ((uintptr_t)a.p & 15u) == 0 &&
                    (!a.q || (a.qs % 4 == 0 && ((uintptr_t)a.q & 15u) == 0));
-  const unsigned grid = (unsigned)a.R * kCluster;
-  if (vec) verify_kernel<true><<<grid, kThreads, 0, stream>>>(a);
-  else verify_kernel<false><<<grid, kThreads, 0, stream>>>(a);
+  // As many CTAs a request as keep the launch within one wave of four CTAs an SM: a
+  // second wave repeats the chain of dependent steps, and fewer, larger shares
+  // read as fast.
+  int ranks = kMaxCluster;
+  while (ranks > 1 && (long long)a.R * ranks > 4 * 152) ranks >>= 1;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)ranks;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.gridDim = dim3((unsigned)a.R * ranks);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, vec ? verify_kernel<true> : verify_kernel<false>, a);
+  if (e != cudaSuccess) return e;
   count_launch();
   return cudaGetLastError();
 }

@@ -453,9 +453,11 @@ DFLASH_API dflash_status_t dflash_attn_paged(const dflash_paged_dims_t* dims, df
  *   draft_tokens [total_draft], draft_offsets [R+1] int32; accept_u
  *     [total_draft] and sample_u [R] fp32 in [0, 1).
  *   out_tokens [R, max_draft + 1], num_accepted [R] int32: every element written.
- * Comparisons are made in 64 bits and sums over V exactly, on probabilities
- * held to 2^-50 (values outside [0, 1] are clamped, NaN counts as 0), so that the
- * result does not depend on the order of the sum.  A drafted token outside [0, V)
+ * Comparisons are made in 64 bits, and weights are added up as whole steps of
+ * 2^-45, so that the result does not depend on the order of the sum (a w below
+ * 2^-46 counts as zero).  Probabilities lie in [0, 1]; an entry where one is NaN
+ * has no weight, and rows that are no distribution give some token of the
+ * vocabulary.  A drafted token outside [0, V)
  * is recorded as DFLASH_ERR_INVALID and rejected; a request whose w is all zero
  * is recorded and gets z = 0; one whose offsets are out of range is recorded and
  * gets num_accepted = 0 and tokens -1.
