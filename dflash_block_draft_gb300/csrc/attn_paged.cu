@@ -88,6 +88,7 @@ __global__ void __launch_bounds__(Simt<T, BM, DMAX>::kThreads)
   const int ty = tid / TX, tx = tid % TX;
   const int D = a.D, per = D / VEC;  // 16-byte pieces of a row
   find_range<BN, kThreads>(a, &s.range, s.scratch);
+  allow_merge();
   Walker<BN> walk(a, s.range);
   Piece pc;
   int4 meta = make_int4(0, 0, 0, 0);
@@ -279,6 +280,7 @@ __global__ void __launch_bounds__(Simt<T, BM, DMAX>::kThreads)
 // takes a row, its lanes the columns.
 template <typename T>
 __global__ void __launch_bounds__(128) paged_merge_kernel(const __grid_constant__ PagedArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the attention kernel has ended and its writes are visible
   const int4 m = a.meta[blockIdx.x];
   if (m.x == 0) return;
   const int lane = threadIdx.x & 31;
@@ -298,7 +300,7 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const __grid_constant_
   float o[DFLASH_PAGED_MAX_D / 32];
 #pragma unroll
   for (int c = 0; c < DFLASH_PAGED_MAX_D / 32; ++c) o[c] = 0.f;
-#pragma unroll 4
+#pragma unroll 8
   for (int i = 0; i < m.x; ++i) {
     const long long at = slot(i);
     const float2 ml = a.part_ml[at];
@@ -421,9 +423,20 @@ cudaError_t launch_attn_paged(PagedArgs a, bool bf16, void* ws, cudaStream_t str
                : pick_simt<float, 64>(a, sms, most, &grid, stream);
   }
   if (e != cudaSuccess) return e;
-  const dim3 mg(grid, (a.rows + 3) / 4);
-  if (bf16) paged_merge_kernel<__nv_bfloat16><<<mg, 128, 0, stream>>>(a);
-  else paged_merge_kernel<float><<<mg, 128, 0, stream>>>(a);
+  // The merge: four rows a block.  It is launched while the attention kernel runs and
+  // waits for its end (programmatic dependent launch), which hides its launch.
+  const long long most = (long long)a.max_q * a.G;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(grid, (unsigned)(((most < a.rows ? (int)most : a.rows) + 3) / 4));
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, bf16 ? paged_merge_kernel<__nv_bfloat16> : paged_merge_kernel<float>, a);
+  if (e != cudaSuccess) return e;
   count_launch();
   return cudaGetLastError();
 }

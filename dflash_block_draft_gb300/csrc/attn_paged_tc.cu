@@ -186,6 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tmem_relinquish();
   }
   find_range<kBN, kThreads>(a, &range, reinterpret_cast<long long*>(smem + C::kOffScratch));
+  allow_merge();
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();

@@ -3,9 +3,10 @@
 // A row tile is `rows` consecutive rows (token, head of the group; token-major) of
 // one request and one key/value head; it needs the key tiles up to its last
 // token's limit.  All key tiles of all row tiles, in the order request, key/value
-// head, row tile, key tile, form one line of T tiles, and CTA c of G takes the
-// tiles [c T / G, (c+1) T / G) of it (G at most T, further CTAs have none): equal work whatever the lengths, one long
-// request or many short ones, without a host that knows the lengths.  A row tile
+// head, row tile, key tile, form one line of T tiles, and every CTA takes the next
+// T / G of it, the first T mod G one more (G CTAs, at most T; further ones have
+// none): equal work whatever the lengths, one long request or many short ones,
+// without a host that knows the lengths.  A row tile
 // that one CTA holds whole is finished by it; of one that is cut, every CTA leaves
 // a partial result (running maximum, sum, unnormalised output) in the workspace:
 // slot 2c for the piece that continues a row tile begun by an earlier CTA, slot
@@ -60,6 +61,11 @@ __device__ __forceinline__ long long head_tiles(const PagedArgs& a, const Req& q
   return s;
 }
 
+// a / b for a >= 0, b > 0, in 32 bits where both fit (64-bit divisions are long).
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return (unsigned long long)(a | b) >> 32 ? a / b : (long long)((unsigned)a / (unsigned)b);
+}
+
 // A CTA's range, found once by the whole block and kept in shared memory.
 struct Range {
   long long total;    // T
@@ -67,6 +73,8 @@ struct Range {
   long long before;   // tiles of the requests before r0
   int r0;             // request that holds tile t0
   int ctas;           // G, at most T: every CTA below it has a tile
+  long long share;    // T / G
+  int more;           // T mod G: CTAs with one tile more
 };
 
 // Whole block (kThreads threads): every thread adds up a strip of requests, a scan
@@ -93,9 +101,14 @@ __device__ __forceinline__ void find_range(const PagedArgs& a, Range* out, long 
   }
   const long long before = base + c - mine;
   const int ctas = (int)min((long long)gridDim.x, total), me = blockIdx.x;
-  const long long t0 = me < ctas ? total * me / ctas : total, t1 = me < ctas ? total * (me + 1) / ctas : total;
+  const long long share = ctas > 0 ? quotient(total, ctas) : 0;
+  const int more = (int)(total - share * ctas);
+  const long long t0 = me < ctas ? share * me + min(me, more) : total;
+  const long long t1 = me < ctas ? t0 + share + (me < more) : total;
   if (tid == 0) {
     out->ctas = ctas;
+    out->share = share;
+    out->more = more;
     out->total = total;
     out->t0 = t0;
     out->t1 = t1;
@@ -128,11 +141,9 @@ struct Piece {
 };
 
 // CTA that holds tile t.
-__device__ __forceinline__ int owner_of(long long t, long long total, int grid) {
-  int c = (int)((t * grid) / total);
-  while (c + 1 < grid && total * (c + 1) / grid <= t) ++c;
-  while (c > 0 && total * c / grid > t) --c;
-  return c;
+__device__ __forceinline__ int owner_of(long long t, const Range& rg) {
+  const long long wide = (rg.share + 1) * rg.more;  // tiles of the CTAs with one more
+  return (int)(t < wide ? quotient(t, rg.share + 1) : rg.more + quotient(t - wide, rg.share));
 }
 
 // Walks the pieces of a CTA's range.  Every role of a kernel keeps its own.
@@ -153,7 +164,7 @@ struct Walker {
     if (t >= rg.t1) return;
     q = load_request(a, r, false);
     const long long per = head_tiles<BN>(a, q);
-    h = (int)((t - at) / per);
+    h = (int)quotient(t - at, per);
     at += h * per;
     skip();
   }
@@ -161,7 +172,7 @@ struct Walker {
   __device__ __forceinline__ void skip() {
     if (!a.causal) {
       const int nt = key_tiles<BN>(a, q, 0);
-      const int k = (int)((t - at) / nt);
+      const int k = (int)quotient(t - at, nt);
       rt += k;
       at += (long long)k * nt;
       return;
@@ -188,7 +199,7 @@ struct Walker {
     if (p->kt0 > 0) p->slot = 2 * blockIdx.x;
     else if (p->kt1 < p->nt) {
       p->slot = 2 * blockIdx.x + 1;
-      p->shared = owner_of(at + p->nt - 1, rg.total, rg.ctas) - (int)blockIdx.x + 1;
+      p->shared = owner_of(at + p->nt - 1, rg) - (int)blockIdx.x + 1;
     } else {
       p->slot = -1;
     }
@@ -216,6 +227,9 @@ __device__ __forceinline__ int4 pack_meta(const Piece& p) { return make_int4(p.s
 bool paged_tc_supported(int G, int D, int P);
 int paged_tc_rows(int G, int max_q);
 cudaError_t launch_paged_tc(const PagedArgs& a, int grid, cudaStream_t stream);
+
+// Lets the merge kernel launch (it waits for this kernel's end before it reads).
+__device__ __forceinline__ void allow_merge() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 }  // namespace paged
 }  // namespace dflash

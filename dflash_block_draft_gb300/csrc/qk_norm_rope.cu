@@ -175,113 +175,91 @@ __device__ __forceinline__ Place place_token(const RopeArgs& a, int t) {
   return pl;
 }
 
-// Forward.  A block takes TB tokens and all their heads (q, then k, then, paged,
-// v).  Warps place one token each, and the tokens' table rows go through shared
-// memory; the first heads' loads are on their way meanwhile.
-constexpr int kTokens = kThreads / 32;  // most tokens of a block
-template <typename T, int LANES, bool PAGED>
-__global__ void __launch_bounds__(kThreads) rope_fwd_kernel(const __grid_constant__ RopeArgs a, int tb) {
+// Forward.  A block takes HPG query heads, key heads or (paged) value heads of one
+// token a group: all loads of a group go out together, before the tokens' places
+// are found, and what differs between kinds of heads is the same in a whole block.
+// Blocks count [tokens][chunk]; chunks below nq are query heads, below nq + nk key
+// heads.  (A block that took all heads of its tokens, with the table rows in shared
+// memory, spent more instructions on which head is whose than on the heads: 205 an
+// two heads against 110, and 215 us against 125 for 32768 tokens of 40 heads.)
+template <typename T, int LANES, int HPG, bool PAGED>
+__global__ void __launch_bounds__(kThreads)
+    rope_fwd_kernel(const __grid_constant__ RopeArgs a, int nq, int nk, int nchunk) {
   constexpr int kGroups = kThreads / LANES;
-  constexpr int kBatch = sizeof(T) == 2 ? 4 : 2;  // heads in flight a group
-  __shared__ Place s_place[kTokens];
-  __shared__ float4 s_cs[kTokens * DFLASH_PAGED_MAX_D / 4];
-  const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES, warp = threadIdx.x >> 5;
-  const int heads = a.Hq + (PAGED ? 2 : 1) * a.Hkv;
-  const long long t0 = (long long)blockIdx.x * tb;
-  const int units = (int)min((long long)tb, a.T - t0) * heads;
+  __shared__ Place s_place[PAGED ? kGroups : 1];
+  const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
+  const int chunk = blockIdx.x % nchunk;
+  const long long t0 = (long long)(blockIdx.x / nchunk) * kGroups, t = t0 + group;
+  const bool is_q = chunk < nq, is_v = PAGED && chunk >= nq + nk;
+  const int H = is_q ? a.Hq : a.Hkv;
+  const int h0 = (chunk - (is_q ? 0 : is_v ? nq + nk : nq)) * HPG, nh = min(HPG, H - h0);
   const LanePart lp = lane_part(a, lane);
-  Part<T> x[kBatch];
-  // Unit u is head u % heads of token u / heads; a group's units are kGroups apart.
-  int hf = group, tf = 0;  // of the next unit to fetch
-  auto fetch = [&]() {
+  const bool mine = lp.in && t < a.T;
+  Part<T> x[HPG];
+  if (mine) {
+    const T* src = static_cast<const T*>(is_q ? a.q : is_v ? a.v : a.k) + t * (is_q ? a.qs : is_v ? a.vs : a.ks) +
+                   h0 * a.D;
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      while (hf >= heads) {
-        hf -= heads;
-        ++tf;
-      }
-      if (tf * heads + hf < units && lp.in) {
-        const bool is_q = hf < a.Hq, is_v = PAGED && hf >= a.Hq + a.Hkv;
-        const T* base = static_cast<const T*>(is_q ? a.q : is_v ? a.v : a.k);
-        const long long stride = is_q ? a.qs : is_v ? a.vs : a.ks;
-        const int h = is_q ? hf : is_v ? hf - a.Hq - a.Hkv : hf - a.Hq;
-        x[j].load(base + (t0 + tf) * stride + h * a.D, lp);
-      }
-      hf += kGroups;
+    for (int j = 0; j < HPG; ++j)
+      if (j < nh) x[j].load(src + j * a.D, lp);
+  }
+  const T* w = static_cast<const T*>(is_q ? a.wq : a.wk);
+  float2 wv[4];
+  if (w && lp.in && !is_v) {
+    Part<T> wr;
+    wr.load(w, lp);
+    wr.unpack(wv);
+  }
+  Place pl = {0, 0, 0, 0};
+  if (PAGED) {
+    for (int i = threadIdx.x >> 5; i < kGroups; i += kThreads / 32) {
+      const Place p = place_token<true>(a, (int)min(t0 + i, (long long)a.T));
+      if ((threadIdx.x & 31) == 0) s_place[i] = p;
     }
-  };
-  fetch();
-  float2 wq[4], wk[4];
-  {
-    Part<T> w;
-    if (lp.in && a.wq) {
-      w.load(static_cast<const T*>(a.wq), lp);
-      w.unpack(wq);
+    __syncthreads();
+    pl = s_place[group];
+  } else if (t < a.T) {
+    pl = place_token<false>(a, (int)t);
+  }
+  if (!is_v) {
+    float2 cs[2], sn[2];
+    if (pl.ok && lp.turned) {
+      const float* row = a.cs + (long long)pl.pos * a.rot + lp.ang;
+      const float4 c = *reinterpret_cast<const float4*>(row), s = *reinterpret_cast<const float4*>(row + (a.rot >> 1));
+      cs[0] = make_float2(c.x, c.y);
+      cs[1] = make_float2(c.z, c.w);
+      sn[0] = make_float2(s.x, s.y);
+      sn[1] = make_float2(s.z, s.w);
     }
-    if (lp.in && a.wk) {
-      w.load(static_cast<const T*>(a.wk), lp);
-      w.unpack(wk);
+    const float inv_d = 1.f / (float)a.D;
+#pragma unroll
+    for (int j = 0; j < HPG; ++j) {
+      if (j >= nh) break;  // the whole block's
+      float2 y[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] = make_float2(0.f, 0.f);
+      if (mine) x[j].unpack(y);
+      if (w) {
+        float2 s2 = __fmul2_rn(y[0], y[0]);
+#pragma unroll
+        for (int e = 1; e < 4; ++e) s2 = __ffma2_rn(y[e], y[e], s2);
+        const float r = rsqrtf(group_sum<LANES>(s2.x + s2.y) * inv_d + a.eps);
+        const float2 r2 = make_float2(r, r);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = __fmul2_rn(__fmul2_rn(y[e], r2), wv[e]);
+      }
+      if (lp.turned) rotate8(y, cs, sn, a.interleaved);
+      x[j].pack(y);
     }
   }
-  if (warp < tb) {
-    const long long t = t0 + warp;
-    const Place pl = place_token<PAGED>(a, (int)min(t, (long long)a.T));
-    if ((threadIdx.x & 31) == 0) s_place[warp] = pl;
-    if (pl.ok) {
-      const float4* row = reinterpret_cast<const float4*>(a.cs + (long long)pl.pos * a.rot);
-      for (int i = threadIdx.x & 31; i < a.rot / 4; i += 32) s_cs[warp * (DFLASH_PAGED_MAX_D / 4) + i] = row[i];
-    }
-  }
-  __syncthreads();
-  const float inv_d = 1.f / (float)a.D;
-  int h = group, tk = 0;
-  for (int u0 = 0; u0 < units; u0 += kBatch * kGroups) {
-    if (u0) fetch();
+  if (mine && pl.ok) {
+    T* dst = is_q     ? static_cast<T*>(a.qo) + (t * a.Hq + h0) * a.D
+             : !PAGED ? static_cast<T*>(a.ko) + (t * a.Hkv + h0) * a.D
+             : is_v   ? static_cast<T*>(a.vc) + pl.vrow + h0 * a.D
+                      : static_cast<T*>(a.kc) + pl.krow + h0 * a.D;
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      if (u0 + j * kGroups >= units) break;  // the whole block is done
-      while (h >= heads) {
-        h -= heads;
-        ++tk;
-      }
-      const bool is_q = h < a.Hq, is_v = PAGED && h >= a.Hq + a.Hkv;
-      const bool ok = tk * heads + h < units && lp.in && s_place[tk < tb ? tk : 0].ok;
-      if (__any_sync(0xffffffffu, ok && !is_v)) {  // values are copied as they are
-        float2 y[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = make_float2(0.f, 0.f);
-        if (ok) x[j].unpack(y);
-        if (a.wq || a.wk) {  // the sum takes the whole warp, whose groups may hold both kinds
-          float2 s2 = __fmul2_rn(y[0], y[0]);
-#pragma unroll
-          for (int e = 1; e < 4; ++e) s2 = __ffma2_rn(y[e], y[e], s2);
-          const float r = rsqrtf(group_sum<LANES>(s2.x + s2.y) * inv_d + a.eps);
-          if (is_q ? a.wq != nullptr : a.wk != nullptr) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              y[e] = __fmul2_rn(__fmul2_rn(y[e], make_float2(r, r)), is_q ? wq[e] : wk[e]);
-          }
-        }
-        if (lp.turned) {
-          const float4* row = s_cs + (tk < tb ? tk : 0) * (DFLASH_PAGED_MAX_D / 4) + lane;
-          const float4 c = row[0], sn = row[a.rot / 8];
-          const float2 cv[2] = {make_float2(c.x, c.y), make_float2(c.z, c.w)};
-          const float2 sv[2] = {make_float2(sn.x, sn.y), make_float2(sn.z, sn.w)};
-          rotate8(y, cv, sv, a.interleaved);
-        }
-        if (!is_v) x[j].pack(y);
-      }
-      if (ok) {
-        const long long t = t0 + tk;
-        T* dst;
-        if (is_q) dst = static_cast<T*>(a.qo) + t * a.Hq * a.D + h * a.D;
-        else if (!PAGED) dst = static_cast<T*>(a.ko) + t * a.Hkv * a.D + (h - a.Hq) * a.D;
-        else if (!is_v) dst = static_cast<T*>(a.kc) + s_place[tk].krow + (h - a.Hq) * a.D;
-        else dst = static_cast<T*>(a.vc) + s_place[tk].vrow + (h - a.Hq - a.Hkv) * a.D;
-        x[j].store(dst, lp);
-      }
-      h += kGroups;
-    }
+    for (int j = 0; j < HPG; ++j)
+      if (j < nh) x[j].store(dst + j * a.D, lp);
   }
 }
 
@@ -545,27 +523,35 @@ bool vectors(const RopeArgs& a, bool bf16, bool paged, bool bwd) {
   return ok;
 }
 
-template <typename T, int LANES, bool PAGED>
+template <typename T, int LANES, int HPG, bool PAGED>
 cudaError_t run_fwd(const RopeArgs& a, cudaStream_t s) {
-  const int heads = a.Hq + (PAGED ? 2 : 1) * a.Hkv, groups = kThreads / LANES;
-  // Tokens of a block: about eight heads a group, as long as the blocks still fill
-  // the machine; with few tokens one a block, which shortens the call.
-  int tb = 8 * groups / heads;
-  if (tb > kTokens) tb = kTokens;
-  const long long most = a.T / (152 * 4);
-  if (tb > most) tb = (int)most;
-  if (tb < 1) tb = 1;
-  rope_fwd_kernel<T, LANES, PAGED><<<(unsigned)(((long long)a.T + tb - 1) / tb), kThreads, 0, s>>>(a, tb);
+  constexpr int groups = kThreads / LANES;
+  const int nq = (a.Hq + HPG - 1) / HPG, nk = (a.Hkv + HPG - 1) / HPG, nchunk = nq + (PAGED ? 2 : 1) * nk;
+  const long long blocks = ((long long)a.T + groups - 1) / groups * nchunk;
+  if (blocks >= (1ll << 31)) return cudaErrorInvalidConfiguration;
+  rope_fwd_kernel<T, LANES, HPG, PAGED><<<(unsigned)blocks, kThreads, 0, s>>>(a, nq, nk, nchunk);
   count_launch();
   return cudaGetLastError();
+}
+
+// Heads a group: as many as still give every SM a few blocks.  The vectors of 8
+// (bf16) or 4 (fp32) heads are 128 bytes a lane in flight.
+template <typename T, int LANES, bool PAGED>
+cudaError_t pick_fwd(const RopeArgs& a, cudaStream_t s) {
+  constexpr int most = sizeof(T) == 2 ? 8 : 4;
+  const long long rows = ((long long)a.T + kThreads / LANES - 1) / (kThreads / LANES);
+  const long long want = 152 * 4, heads = a.Hq + (PAGED ? 2 : 1) * a.Hkv;
+  if (rows * heads / most >= want) return run_fwd<T, LANES, most, PAGED>(a, s);
+  if (rows * heads / 2 >= want) return run_fwd<T, LANES, 2, PAGED>(a, s);
+  return run_fwd<T, LANES, 1, PAGED>(a, s);
 }
 
 template <typename T, bool PAGED>
 cudaError_t type_fwd(const RopeArgs& a, cudaStream_t s) {
   if (vectors(a, sizeof(T) == 2, PAGED, false)) {
-    if (a.D <= 64) return run_fwd<T, 8, PAGED>(a, s);
-    if (a.D <= 128) return run_fwd<T, 16, PAGED>(a, s);
-    return run_fwd<T, 32, PAGED>(a, s);
+    if (a.D <= 64) return pick_fwd<T, 8, PAGED>(a, s);
+    if (a.D <= 128) return pick_fwd<T, 16, PAGED>(a, s);
+    return pick_fwd<T, 32, PAGED>(a, s);
   }
   const int heads = a.Hq + (PAGED ? 2 : 1) * a.Hkv;
   const long long blocks = ((long long)a.T * heads + kWarps - 1) / kWarps;
