@@ -26,8 +26,10 @@
 // not exist is loaded from behind the tensor's end, which TMA fills with zeros.
 // Head dimensions below 64 or 128 are padded with zeros the same way.
 //
-// Warp roles (384 threads): warp 0 loads, warps 1 and 2 issue the MMAs of halves 0
-// and 1, warps 4..7 and 8..11 are the softmax and epilogue of halves 0 and 1.
+// Warp roles (384 threads): warp 0 loads keys and values, warp 3 the queries (so that
+// the next row tile's keys do not wait for the queries' buffer), warps 1 and 2 issue
+// the MMAs of halves 0 and 1, warps 4..7 and 8..11 are the softmax and epilogue of
+// halves 0 and 1.
 // The grid is one CTA an SM; work is dealt as paged.cuh says.  Every mbarrier
 // wait is bounded (DFLASH_ERR_TIMEOUT, CTA abort flag, wind-down).
 #include <math.h>
@@ -139,7 +141,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const PagedArgs& a = ta.a;
   if (sbase & 1023u) {  // the swizzled tiles need it; dynamic shared memory starts there
     if (threadIdx.x == 0) {
-      a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
+      a.meta[blockIdx.x] = no_meta();
       record_error(a.err, DFLASH_ERR_CUDA);
     }
     return;
@@ -153,7 +155,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Range& range = *reinterpret_cast<Range*>(smem + C::kOffRange);
   float2* ml = reinterpret_cast<float2*>(smem + C::kOffMl);
 
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == kThreads - 1) {  // the first threads look at the requests meanwhile
     const uint32_t users = PAIR ? 2 : 1;  // MMA issuers that read a ring slot
     ptx::mbar_init(ctl.bar(C::Q_FULL), 1);
     ptx::mbar_init(ctl.bar(C::Q_EMPTY), 2);
@@ -176,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::fence_mbar_init();
     ptx::fence_proxy_async_smem();
   }
-  if (warp == 0 && lane == 0) {
+  if (warp == 3 && lane == 0) {
     ptx::prefetch_tmap(&tmQ);
     ptx::prefetch_tmap(&tmK);
     ptx::prefetch_tmap(&tmV);
@@ -186,7 +188,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tmem_relinquish();
   }
   find_range<kBN, kThreads>(a, &range, reinterpret_cast<long long*>(smem + C::kOffScratch));
-  allow_merge();
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
@@ -196,39 +197,33 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < 4) ptx::setmaxnreg_dec<kCtlRegs>();
 
   if (warp == 0) {
-    // ------------------------------------------------------------ TMA producer (whole warp)
+    // ------------------------------------------------------------ keys and values (whole warp)
     Walker<kBN> walk(a, range);
-    Piece pc;
-    uint32_t g = 0, n_q = 0;     // key tiles and row tiles loaded
+    Piece pc = {};
+    uint32_t g = 0;                 // key tiles loaded
     uint32_t load0 = 0, load1 = 0;  // of each ring
     bool stop = false;
     const int boxes = kBN / ta.box;                     // boxes of a panel
     const int my_box = lane % boxes, my_pn = lane / boxes;  // this lane's box
     const bool mine = lane < boxes * NP;
-    const uint32_t q_bytes = (uint32_t)tile_rows * 128u;  // bytes of a Q box
+    // Page id of this lane's box of key tile kt; the load is left in flight.
+    auto page_of = [&](int kt) {
+      const int p0 = kt * kBN + my_box * ta.box;
+      return mine && kt < pc.kt1 && p0 < pc.q.kv ? __ldg(a.table + (long long)pc.r * a.max_pages + p0 / a.P)
+                                                : a.num_pages;
+    };
     while (!stop && walk.next(&pc)) {
-      if (n_q > 0 && !__all_sync(0xffffffffu, ctl.wait(C::Q_EMPTY, (n_q - 1) & 1u))) break;
-      if (lane == 0) {
-        ptx::mbar_arrive_expect_tx(ctl.bar(C::Q_FULL), q_bytes * (PAIR ? 2 : 1) * NP);
-        for (int i = 0; i < (PAIR ? 2 : 1); ++i)
-          for (int pn = 0; pn < NP; ++pn)
-            ptx::tma_load_3d(sbase + C::kOffQ + (i * NP + pn) * kPanel, &tmQ, ctl.bar(C::Q_FULL), 64 * pn,
-                             pc.h * a.G, pc.q.q0 + (pc.rt * (PAIR ? 2 : 1) + i) * ta.tokens);
-      }
-      ++n_q;
+      int page_next = page_of(pc.kt0);
       if ((int)blockIdx.x == a.stall_cta) break;  // timeout test: this piece's key tiles never arrive
       for (int kt = pc.kt0; kt < pc.kt1 && !stop; ++kt, ++g) {
         // this lane's box: its page (one that does not exist lies behind the tensor's end) and row
-        const int p0 = kt * kBN + my_box * ta.box;
-        int page = a.num_pages;
-        if (mine && p0 < pc.q.kv) {
-          page = __ldg(a.table + (long long)pc.r * a.max_pages + p0 / a.P);
-          if (page < 0 || page >= a.num_pages) {
-            page = a.num_pages;
-            record_error(a.err, DFLASH_ERR_INVALID);
-          }
+        const int p0 = kt * kBN + my_box * ta.box, row = p0 % a.P;
+        int page = page_next;
+        page_next = page_of(kt + 1);
+        if (page < 0 || page >= a.num_pages) {
+          if (mine && p0 < pc.q.kv) record_error(a.err, DFLASH_ERR_INVALID);
+          page = a.num_pages;
         }
-        const int row = p0 % a.P;
         const uint32_t r = PAIR ? 0u : g & 1u;
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
@@ -254,7 +249,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (uint32_t i = c > C::kRing ? c - C::kRing : 0u; i < c; ++i)
         ctl.wait_landed(C::RING_FULL + C::slot(r, i), C::parity(i));
     }
-    if (n_q > 0) ctl.wait_landed(C::Q_FULL, (n_q - 1) & 1u);
+  } else if (warp == 3) {
+    // ------------------------------------------------------------ queries
+    if (lane == 0) {
+      Walker<kBN> walk(a, range);
+      Piece pc;
+      const uint32_t q_bytes = (uint32_t)tile_rows * 128u;  // bytes of a box
+      uint32_t n = 0;
+      while (walk.next(&pc)) {
+        if (n > 0 && !ctl.wait(C::Q_EMPTY, (n - 1) & 1u)) break;
+        ptx::mbar_arrive_expect_tx(ctl.bar(C::Q_FULL), q_bytes * (PAIR ? 2 : 1) * NP);
+        for (int i = 0; i < (PAIR ? 2 : 1); ++i)
+          for (int pn = 0; pn < NP; ++pn)
+            ptx::tma_load_3d(sbase + C::kOffQ + (i * NP + pn) * kPanel, &tmQ, ctl.bar(C::Q_FULL), 64 * pn,
+                             pc.h * a.G, pc.q.q0 + (pc.rt * (PAIR ? 2 : 1) + i) * ta.tokens);
+        ++n;
+      }
+      if (n > 0) ctl.wait_landed(C::Q_FULL, (n - 1) & 1u);
+    }
   } else if (warp == 1 || warp == 2) {
     // ------------------------------------------------------------ MMA issuers
     if (lane == 0) {
@@ -361,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float c2 = a.scale_log2;
     Walker<kBN> walk(a, range);
     Piece pc;
-    int4 meta = make_int4(0, 0, 0, 0);
+    Meta meta = no_meta();
     uint32_t g = 0, mine = 0, n_epi = 0;  // tiles of the CTA, tiles of this half, pieces finished
     uint32_t n_full[2] = {0, 0};          // accumulators finished, each half
     bool stop = false;
@@ -542,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tc_fence_after();
       }
       ++n_epi;
-      if (pc.slot >= 0 && pc.shared) meta = pack_meta(pc);
+      if (pc.slot >= 0 && pc.shared) meta = meta_of(a, pc);
     }
     if (warp == 4 && lane == 0) a.meta[blockIdx.x] = meta;
   }

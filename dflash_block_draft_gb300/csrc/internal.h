@@ -136,6 +136,9 @@ size_t rope_bwd_workspace_bytes(int D);
 cudaError_t launch_qk_norm_rope_bwd(const RopeArgs& a, bool bf16, float* dwq, float* dwk, cudaStream_t stream);
 
 // Attention over a paged cache (attn_paged.cu, attn_paged_tc.cu).
+namespace paged {
+struct Meta;
+}
 struct PagedArgs {
   const void *q, *kc, *vc;
   const int32_t *table, *kv_lens, *q_off;
@@ -147,7 +150,7 @@ struct PagedArgs {
   float scale_log2;       // scale * log2(e)
   int rows;               // rows (token, head of the group) of a row tile
   // workspace: partial results of row tiles that several CTAs share
-  int4* meta;             // [grid]
+  paged::Meta* meta;      // [grid]
   float2* part_ml;        // [2 * grid, rows] running maximum (base 2) and sum
   float* part_o;          // [2 * grid, rows, D] unnormalised
   unsigned* err;

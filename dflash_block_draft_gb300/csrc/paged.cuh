@@ -36,7 +36,8 @@ __device__ __forceinline__ Req load_request(const PagedArgs& a, int r, bool repo
   const bool bad = q.q0 < 0 || q.n < 0 || q1 > a.total_q || q.n > a.max_q || q.kv < 0 ||
                    q.kv > (long long)a.max_pages * a.P;
   if (bad && report) record_error(a.err, DFLASH_ERR_INVALID);
-  q.nrt = bad ? 0 : (int)(((long long)q.n * a.G + a.rows - 1) / a.rows);
+  // rows of a request fit 31 bits (the host bounds max_q * G)
+  q.nrt = bad ? 0 : (unsigned)(q.n * a.G + a.rows - 1) / (unsigned)a.rows;
   return q;
 }
 
@@ -44,21 +45,37 @@ __device__ __forceinline__ Req load_request(const PagedArgs& a, int r, bool repo
 // tile at least, so that rows that see nothing are written too.
 __device__ __forceinline__ int tile_limit(const PagedArgs& a, const Req& q, int rt) {
   if (!a.causal) return q.kv;
-  const long long end = min((long long)(rt + 1) * a.rows, (long long)q.n * a.G);
-  return max(0, q.kv - q.n + (int)((end - 1) / a.G) + 1);
+  const unsigned end = min((rt + 1) * a.rows, q.n * a.G);
+  return max(0, q.kv - q.n + (int)((end - 1) / (unsigned)a.G) + 1);
 }
 template <int BN>
 __device__ __forceinline__ int key_tiles(const PagedArgs& a, const Req& q, int rt) {
   return max(1, (tile_limit(a, q, rt) + BN - 1) / BN);
 }
-// Key tiles of one key/value head of a request.
+// Key tiles of the first m row tiles of one key/value head, m <= nrt.  In closed form
+// where the tokens of a row tile divide BN or BN divides them: with k = BN / tokens
+// a row tile ends one k-th of a key tile after the one before.
 template <int BN>
-__device__ __forceinline__ long long head_tiles(const PagedArgs& a, const Req& q) {
-  if (q.nrt == 0) return 0;
-  if (!a.causal) return (long long)q.nrt * key_tiles<BN>(a, q, 0);
+__device__ __forceinline__ long long tiles_before(const PagedArgs& a, const Req& q, int m) {
+  if (m == 0) return 0;
+  if (!a.causal) return (long long)m * key_tiles<BN>(a, q, 0);
+  const unsigned tokens = (unsigned)a.rows / (unsigned)a.G;
+  const int base = q.kv - q.n;
   long long s = 0;
-  for (int rt = 0; rt < q.nrt; ++rt) s += key_tiles<BN>(a, q, rt);
-  return s;
+  int full = min(m, q.nrt - 1);  // the last row tile may hold fewer tokens
+  if (base >= 0 && tokens * a.G == a.rows && BN % tokens == 0) {
+    const unsigned k = BN / tokens, first = (base + tokens - 1) / tokens;
+    auto sum = [&](unsigned x) {  // of ceil(j / k), j = 1 .. x
+      const unsigned c = x / k;
+      return (long long)k * c * (c + 1) / 2 + (long long)(x - c * k) * (c + 1);
+    };
+    s = sum(first + full) - sum(first);
+  } else if (base >= 0 && tokens * a.G == a.rows && tokens % BN == 0) {
+    s = full * (long long)((base + BN - 1) / BN) + (long long)(tokens / BN) * full * (full + 1) / 2;
+  } else {
+    for (int rt = 0; rt < full; ++rt) s += key_tiles<BN>(a, q, rt);
+  }
+  return m > full ? s + key_tiles<BN>(a, q, full) : s;
 }
 
 // a / b for a >= 0, b > 0, in 32 bits where both fit (64-bit divisions are long).
@@ -66,26 +83,32 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
   return (unsigned long long)(a | b) >> 32 ? a / b : (long long)((unsigned)a / (unsigned)b);
 }
 
-// A CTA's range, found once by the whole block and kept in shared memory.
+// A CTA's range, found once by the whole block and kept in shared memory, with the
+// row tile that holds its first tile.
 struct Range {
   long long total;    // T
   long long t0, t1;   // this CTA's tiles
-  long long before;   // tiles of the requests before r0
-  int r0;             // request that holds tile t0
-  int ctas;           // G, at most T: every CTA below it has a tile
   long long share;    // T / G
   int more;           // T mod G: CTAs with one tile more
+  int r, h, rt;       // first row tile
+  long long at;       // its first tile
+  Req q;
 };
 
 // Whole block (kThreads threads): every thread adds up a strip of requests, a scan
-// over the strips gives T and finds the strip, and its thread the request, of t0.
+// over the strips gives T and finds the strip, and its thread the row tile, of t0.
 template <int BN, int kThreads>
 __device__ __forceinline__ void find_range(const PagedArgs& a, Range* out, long long* scratch /* [kThreads/32 + 1] */) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int strip = (a.R + kThreads - 1) / kThreads;
   const int lo = min(a.R, tid * strip), hi = min(a.R, lo + strip);
-  long long mine = 0;
-  for (int r = lo; r < hi; ++r) mine += a.Hkv * head_tiles<BN>(a, load_request(a, r, blockIdx.x == 0));
+  long long mine = 0, last = 0;
+  Req q;
+  for (int r = lo; r < hi; ++r) {
+    q = load_request(a, r, blockIdx.x == 0);
+    last = a.Hkv * tiles_before<BN>(a, q, q.nrt);
+    mine += last;
+  }
   long long c = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -95,6 +118,7 @@ __device__ __forceinline__ void find_range(const PagedArgs& a, Range* out, long 
   if (lane == 31) scratch[warp] = c;
   __syncthreads();
   long long base = 0, total = 0;
+#pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
     base += w < warp ? scratch[w] : 0;
     total += scratch[w];
@@ -104,28 +128,44 @@ __device__ __forceinline__ void find_range(const PagedArgs& a, Range* out, long 
   const long long share = ctas > 0 ? quotient(total, ctas) : 0;
   const int more = (int)(total - share * ctas);
   const long long t0 = me < ctas ? share * me + min(me, more) : total;
-  const long long t1 = me < ctas ? t0 + share + (me < more) : total;
   if (tid == 0) {
-    out->ctas = ctas;
+    out->total = total;
     out->share = share;
     out->more = more;
-    out->total = total;
     out->t0 = t0;
-    out->t1 = t1;
-    out->before = 0;
-    out->r0 = 0;
+    out->t1 = me < ctas ? t0 + share + (me < more) : total;
   }
-  __syncthreads();
   if (before <= t0 && t0 < before + mine) {  // one thread at most
     long long s = before;
-    int r = lo;
-    for (; r + 1 < hi; ++r) {
-      const long long w = a.Hkv * head_tiles<BN>(a, load_request(a, r, false));
-      if (t0 < s + w) break;
-      s += w;
+    int r = hi - 1;
+    if (hi - lo > 1) {
+      for (r = lo; r < hi; ++r) {
+        q = load_request(a, r, false);
+        last = a.Hkv * tiles_before<BN>(a, q, q.nrt);
+        if (t0 < s + last) break;
+        s += last;
+      }
     }
-    out->before = s;
-    out->r0 = r;
+    const long long per = quotient(last, a.Hkv);
+    const int h = (int)quotient(t0 - s, per);
+    s += h * per;
+    // the last row tile that begins at or before t0
+    const long long want = t0 - s;
+    int x = 0, n = q.nrt;
+    while (n > 1) {
+      const int half = n >> 1;
+      if (tiles_before<BN>(a, q, x + half) <= want) {
+        x += half;
+        n -= half;
+      } else {
+        n = half;
+      }
+    }
+    out->r = r;
+    out->h = h;
+    out->rt = x;
+    out->at = s + tiles_before<BN>(a, q, x);
+    out->q = q;
   }
   __syncthreads();
 }
@@ -158,31 +198,11 @@ struct Walker {
 
   __device__ __forceinline__ Walker(const PagedArgs& a_, const Range& rg_) : a(a_), rg(rg_) {
     t = rg.t0;
-    r = rg.r0;
-    h = rt = 0;
-    at = rg.before;
-    if (t >= rg.t1) return;
-    q = load_request(a, r, false);
-    const long long per = head_tiles<BN>(a, q);
-    h = (int)quotient(t - at, per);
-    at += h * per;
-    skip();
-  }
-  // Moves on to the row tile that holds tile t, within the current head.
-  __device__ __forceinline__ void skip() {
-    if (!a.causal) {
-      const int nt = key_tiles<BN>(a, q, 0);
-      const int k = (int)quotient(t - at, nt);
-      rt += k;
-      at += (long long)k * nt;
-      return;
-    }
-    for (;;) {
-      const int nt = key_tiles<BN>(a, q, rt);
-      if (t < at + nt) return;
-      at += nt;
-      ++rt;
-    }
+    at = rg.at;
+    q = rg.q;
+    r = rg.r;
+    h = rg.h;
+    rt = rg.rt;
   }
   __device__ __forceinline__ bool next(Piece* p) {
     if (t >= rg.t1) return false;
@@ -220,16 +240,23 @@ struct Walker {
 };
 
 // What the merge kernel needs about CTA c: the row tile that it begins and leaves cut.
-__device__ __forceinline__ int4 pack_meta(const Piece& p) { return make_int4(p.shared, p.r, p.h, p.rt); }
+struct Meta {
+  int shared;     // CTAs that share it (0: none is cut)
+  int q0;         // its request's first packed row
+  int head;       // its group's first query head
+  int f0, rows;   // its first row within (request, key/value head), and rows
+};
+__device__ __forceinline__ Meta no_meta() { return Meta{0, 0, 0, 0, 0}; }
+__device__ __forceinline__ Meta meta_of(const PagedArgs& a, const Piece& p) {
+  const int f0 = p.rt * a.rows;
+  return Meta{p.shared, p.q.q0, p.h * a.G, f0, min(a.rows, p.q.n * a.G - f0)};
+}
 
 // The tensor-core kernel (attn_paged_tc.cu): which shapes it takes, the rows of its
 // row tiles, and its launch over `grid` CTAs.
 bool paged_tc_supported(int G, int D, int P);
 int paged_tc_rows(int G, int max_q);
 cudaError_t launch_paged_tc(const PagedArgs& a, int grid, cudaStream_t stream);
-
-// Lets the merge kernel launch (it waits for this kernel's end before it reads).
-__device__ __forceinline__ void allow_merge() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 }  // namespace paged
 }  // namespace dflash
