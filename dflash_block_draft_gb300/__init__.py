@@ -1,7 +1,9 @@
 """Python binding of the GB300 DFlash draft block-attention library.
 
 Argument marshalling only: every step of the computation runs in the CUDA
-kernels of ``libdflash_attn.so`` (C ABI in ``include/dflash_attn.h``).
+kernels of ``libdflash_attn.so`` (C ABI in ``include/dflash_attn.h``), called
+through ctypes or, for the short calls of the serving step, through a compiled
+module (``csrc/binding.cpp``).
 PyTorch supplies device memory and the current stream.  There is no CPU
 fallback: if the shared library has not been built, every call raises.
 
@@ -428,82 +430,25 @@ def dflash_attn_dense_backward(q, k_nope, k_rope, v, mask, out, lse, dout, grads
 # ---------------------------------------------------------------------------
 # the grouped-query draft's serving step
 # ---------------------------------------------------------------------------
-# These calls are short (a few microseconds on the device), so what the binding
-# checks it checks with the cheapest tensor methods, and says what is wrong only
-# once something is.
-def _call(name, fn, index, stream, *args):
-    """fn(*args, stream handle) with device `index` current; raises on a status."""
-    torch = _torch()
-    if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(index)
-    else:
-        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if torch._C._cuda_getDevice() == index:
-        rc = fn(*args, handle)
-    else:
-        with torch.cuda.device(index):
-            rc = fn(*args, handle)
-    if rc:
-        raise DFlashError(name, rc)
+_binding_handle = None
 
 
-def _refuse(t, name, index, dtype, shape, form):
-    if t.device.type != "cuda" or t.get_device() != index:
-        raise ValueError(f"{name} must be a CUDA tensor" + (f" on device {index}" if index >= 0 else ""))
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    raise ValueError(f"{name} must be contiguous" if form is None else form)
-
-
-def _arg(t, name, index, dtype, shape=None):
-    """Data pointer of a contiguous tensor on CUDA device `index`, checked; None for None."""
-    if t is None:
-        return None
-    if not (t.is_cuda and t.get_device() == index and t.dtype is dtype and t.is_contiguous() and
-            (shape is None or t.shape == shape)):
-        _refuse(t, name, index, dtype, shape, None)
-    return t.data_ptr()
-
-
-def _token_arg(t, name, index, dtype, shape):
-    """Data pointer and token stride of [tokens, heads, D] whose tokens are each contiguous."""
-    if t.is_cuda and t.get_device() == index and t.dtype is dtype and t.shape == shape:
-        T, H, D = shape
-        s0, s1, s2 = t.stride()
-        if (s2 == 1 or D <= 1) and (s1 == D or H <= 1) and (s0 >= H * D or T <= 1):
-            return t.data_ptr(), s0 if T > 1 else 0
-    _refuse(t, name, index, dtype, shape, f"the heads of a token of {name} must be contiguous")
-
-
-def _cache_arg(t, name, index, dtype, shape):
-    """Data pointer and page stride of [pages, page_size, H_kv, D] whose pages are each contiguous."""
-    if t.is_cuda and t.get_device() == index and t.dtype is dtype and t.shape == shape:
-        n, P, H, D = shape
-        s0, s1, s2, s3 = t.stride()
-        if (s3 == 1 or D <= 1) and (s2 == D or H <= 1) and (s1 == H * D or P <= 1) and (s0 >= P * H * D or n <= 1):
-            return t.data_ptr(), s0 if n > 1 else 0
-    _refuse(t, name, index, dtype, shape, f"the pages of {name} must be contiguous")
-
-
-def _rope_args(q, k, positions, cos_sin):
-    torch = _torch()
-    one = q if q is not None else k
-    if one is None:
-        raise ValueError("q or k must be given")
-    if one.dim() != 3:
-        raise ValueError("q and k must be [tokens, heads, D]")
-    T, _, D = one.shape
-    dev = one.get_device()
-    Hq, Hk = 0 if q is None else q.shape[1], 0 if k is None else k.shape[1]
-    if cos_sin is None:
-        return one.dtype, dev, T, Hq, Hk, D, 0, 0, None, None
-    if positions is None or cos_sin.dim() != 2:
-        raise ValueError("cos_sin must be [max_pos, rot_dim] and comes with positions")
-    max_pos, rot = cos_sin.shape
-    cs = _arg(cos_sin, "cos_sin", dev, torch.float32)
-    return one.dtype, dev, T, Hq, Hk, D, rot, max_pos, cs, _arg(positions, "positions", dev, torch.int32, (T,))
+def _binding():
+    """The compiled module of the serving step's calls (built with the library); raises if absent."""
+    global _binding_handle
+    if _binding_handle is None:
+        import importlib.util
+        _torch()
+        load_library()
+        path = _build.BINDING_PATH
+        if not os.path.exists(path):
+            raise RuntimeError(f"DFlash Python binding not built ({path} missing): run "
+                               "`python -c 'import __graft_entry__ as g; g.build()'`")
+        spec = importlib.util.spec_from_file_location("_dflash_binding", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _binding_handle = module
+    return _binding_handle
 
 
 def dflash_qk_norm_rope(q, k, positions, cos_sin, q_norm=None, k_norm=None, eps=1e-6, interleaved=False, q_out=None,
@@ -512,25 +457,11 @@ def dflash_qk_norm_rope(q, k, positions, cos_sin, q_norm=None, k_norm=None, eps=
     [T,H_kv,D] at positions [T] int32.  Either of q and k may be None; their
     tokens may be strided.  cos_sin [max_pos, rot_dim] fp32 (rot_dim/2 cosines,
     then sines; None: no rotation).  Returns (q_out, k_out), contiguous."""
-    torch = _torch()
-    lib = load_library()
-    dt, dev, T, Hq, Hk, D, rot, max_pos, cs, ps = _rope_args(q, k, positions, cos_sin)
-    code = _dtype_code(q if q is not None else k)
-    qp, qs = (None, 0) if q is None else _token_arg(q, "q", dev, dt, (T, Hq, D))
-    kp, ks = (None, 0) if k is None else _token_arg(k, "k", dev, dt, (T, Hk, D))
-    if q is None:
-        q_out = None
-    elif q_out is None:
-        q_out = torch.empty((T, Hq, D), dtype=dt, device=q.device)
-    if k is None:
-        k_out = None
-    elif k_out is None:
-        k_out = torch.empty((T, Hk, D), dtype=dt, device=k.device)
-    d = _RopeDims(T, Hq, Hk, D, rot, max_pos, int(interleaved), eps, qs, ks)
-    _call("dflash_qk_norm_rope", lib.dflash_qk_norm_rope, dev, stream, d, code, qp, kp,
-          _arg(q_norm, "q_norm", dev, dt, (D,)), _arg(k_norm, "k_norm", dev, dt, (D,)), cs, ps,
-          _arg(q_out, "q_out", dev, dt, (T, Hq, D)), _arg(k_out, "k_out", dev, dt, (T, Hk, D)))
-    return q_out, k_out
+    r = (_binding_handle or _binding()).qk_norm_rope(q, k, positions, cos_sin, q_norm, k_norm, eps, interleaved, q_out,
+                                                     k_out, stream)
+    if r.__class__ is int:
+        raise DFlashError("dflash_qk_norm_rope", r)
+    return r
 
 
 def dflash_qk_norm_rope_backward(q, k, positions, cos_sin, dq_out, dk_out, q_norm=None, k_norm=None, eps=1e-6,
@@ -538,46 +469,12 @@ def dflash_qk_norm_rope_backward(q, k, positions, cos_sin, dq_out, dk_out, q_nor
     """Gradients (dq, dk, dq_norm, dk_norm) of sum(dq_out * q_out) + sum(dk_out *
     k_out); the norm gradients are fp32 [D], None without a weight.  grads:
     optional preallocated (dq, dk, dq_norm, dk_norm)."""
-    torch = _torch()
-    lib = load_library()
-    dt, dev, T, Hq, Hk, D, rot, max_pos, cs, ps = _rope_args(q, k, positions, cos_sin)
-    code = _dtype_code(q if q is not None else k)
-    qp, qs = (None, 0) if q is None else _token_arg(q, "q", dev, dt, (T, Hq, D))
-    kp, ks = (None, 0) if k is None else _token_arg(k, "k", dev, dt, (T, Hk, D))
-    device = (q if q is not None else k).device
-    if grads is None:
-        grads = (None if q is None else torch.empty((T, Hq, D), dtype=dt, device=device),
-                 None if k is None else torch.empty((T, Hk, D), dtype=dt, device=device),
-                 None if q_norm is None else torch.empty(D, dtype=torch.float32, device=device),
-                 None if k_norm is None else torch.empty(D, dtype=torch.float32, device=device))
-    dq, dk, dwq, dwk = grads
-    d = _RopeDims(T, Hq, Hk, D, rot, max_pos, int(interleaved), eps, qs, ks)
-    nbytes = int(lib.dflash_qk_norm_rope_workspace_size(d))
-    ws = _workspace(nbytes, workspace, device)
-    _call("dflash_qk_norm_rope_backward", lib.dflash_qk_norm_rope_backward, dev, stream, d, code, qp, kp,
-          _arg(q_norm, "q_norm", dev, dt, (D,)), _arg(k_norm, "k_norm", dev, dt, (D,)), cs, ps,
-          _arg(dq_out if q is not None else None, "dq_out", dev, dt, (T, Hq, D)),
-          _arg(dk_out if k is not None else None, "dk_out", dev, dt, (T, Hk, D)),
-          _arg(dq, "dq", dev, dt, (T, Hq, D)), _arg(dk, "dk", dev, dt, (T, Hk, D)),
-          _arg(dwq, "dq_norm", dev, torch.float32, (D,)), _arg(dwk, "dk_norm", dev, torch.float32, (D,)),
-          _arg(ws, "workspace", dev, ws.dtype), nbytes)
-    return dq, dk, dwq, dwk
-
-
-def _paged_args(k_cache, v_cache, page_table, kv_lens, q_offsets, dt, dev):
-    torch = _torch()
-    shape = k_cache.shape
-    if len(shape) != 4:
-        raise ValueError("k_cache and v_cache must be [num_pages, page_size, H_kv, D]")
-    kp, ks = _cache_arg(k_cache, "k_cache", dev, dt, shape)
-    vp, vs = _cache_arg(v_cache, "v_cache", dev, dt, shape)
-    if page_table.dim() != 2 or q_offsets.dim() != 1:
-        raise ValueError("page_table must be [R, max_pages] and q_offsets [R + 1]")
-    R, max_pages = page_table.shape
-    tp = _arg(page_table, "page_table", dev, torch.int32)
-    lp = _arg(kv_lens, "kv_lens", dev, torch.int32, (R,))
-    op = _arg(q_offsets, "q_offsets", dev, torch.int32, (R + 1,))
-    return shape, R, max_pages, kp, ks, vp, vs, tp, lp, op
+    dq, dk, dwq, dwk = grads or (None, None, None, None)
+    r = (_binding_handle or _binding()).qk_norm_rope_backward(q, k, positions, cos_sin, dq_out, dk_out, q_norm, k_norm,
+                                                              eps, interleaved, dq, dk, dwq, dwk, workspace, stream)
+    if r.__class__ is int:
+        raise DFlashError("dflash_qk_norm_rope_backward", r)
+    return r
 
 
 def dflash_cache_append(k, v, k_cache, v_cache, page_table, kv_lens, q_offsets, q=None, cos_sin=None, q_norm=None,
@@ -587,33 +484,11 @@ def dflash_cache_append(k, v, k_cache, v_cache, page_table, kv_lens, q_offsets, 
     [q_offsets[r], q_offsets[r+1]) are the last of its kv_lens[r] positions, and
     position p lies in page page_table[r, p // page_size].  With q [total_q,H_q,D]
     its heads are normed and rotated too; returns q_out (None without q)."""
-    torch = _torch()
-    lib = load_library()
-    dt, dev = k.dtype, k.get_device()
-    code = _dtype_code(k)
-    (n, P, Hk, D), R, max_pages, kcp, kcs, vcp, vcs, tp, lp, op = _paged_args(k_cache, v_cache, page_table, kv_lens,
-                                                                              q_offsets, dt, dev)
-    T = k.shape[0]
-    kp, ks = _token_arg(k, "k", dev, dt, (T, Hk, D))
-    vp, vs = _token_arg(v, "v", dev, dt, (T, Hk, D))
-    Hq, qp, qs = Hk, None, 0
-    if q is not None:
-        if q.dim() != 3:
-            raise ValueError("q must be [total_q, H_q, D]")
-        Hq = q.shape[1]
-        qp, qs = _token_arg(q, "q", dev, dt, (T, Hq, D))
-        if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=dt, device=q.device)
-    else:
-        q_out = None
-    max_pos, rot = (0, 0) if cos_sin is None else cos_sin.shape
-    pd = _PagedDims(R, Hq, Hk, D, T, 0, n, P, max_pages, kcs, vcs)
-    rd = _RopeDims(T, Hq, Hk, D, rot, max_pos, int(interleaved), eps, qs, ks)
-    _call("dflash_cache_append", lib.dflash_cache_append, dev, stream, pd, rd, code, qp, kp, vp, vs,
-          _arg(q_norm, "q_norm", dev, dt, (D,)), _arg(k_norm, "k_norm", dev, dt, (D,)),
-          _arg(cos_sin, "cos_sin", dev, torch.float32), tp, lp, op, _arg(q_out, "q_out", dev, dt, (T, Hq, D)), kcp,
-          vcp)
-    return q_out
+    r = (_binding_handle or _binding()).cache_append(k, v, k_cache, v_cache, page_table, kv_lens, q_offsets, q,
+                                                     cos_sin, q_norm, k_norm, eps, interleaved, q_out, stream)
+    if r.__class__ is int:
+        raise DFlashError("dflash_cache_append", r)
+    return r
 
 
 def dflash_attn_paged_workspace_size(H_q, H_kv, D, max_q_len, page_size, dtype=DFLASH_BF16) -> int:
@@ -627,25 +502,11 @@ def dflash_attn_paged(q, k_cache, v_cache, page_table, kv_lens, q_offsets, max_q
     """Attention of the new tokens q [total_q,H_q,D] over their requests' pages (see
     dflash_cache_append): all positions below kv_lens[r], or, causal, those up to
     the token's own.  Returns out [total_q,H_q,D]; fills lse [H_q,total_q] fp32 if given."""
-    torch = _torch()
-    lib = load_library()
-    dt, dev = q.dtype, q.get_device()
-    code = _dtype_code(q)
-    if q.dim() != 3:
-        raise ValueError("q must be [total_q, H_q, D]")
-    T, Hq, _ = q.shape
-    (n, P, Hk, D), R, max_pages, kcp, kcs, vcp, vcs, tp, lp, op = _paged_args(k_cache, v_cache, page_table, kv_lens,
-                                                                              q_offsets, dt, dev)
-    qp = _arg(q, "q", dev, dt, (T, Hq, D))
-    if out is None:
-        out = torch.empty((T, Hq, D), dtype=dt, device=q.device)
-    d = _PagedDims(R, Hq, Hk, D, T, int(max_q_len), n, P, max_pages, kcs, vcs)
-    nbytes = lib.dflash_attn_paged_workspace_size(d, code)
-    ws = _workspace(nbytes, workspace, q.device)
-    _call("dflash_attn_paged", lib.dflash_attn_paged, dev, stream, d, code, qp, kcp, vcp, tp, lp, op, int(causal),
-          float(scale or 0.0), _arg(out, "out", dev, dt, (T, Hq, D)),
-          _arg(lse, "lse", dev, torch.float32, (Hq, T)), _arg(ws, "workspace", dev, ws.dtype), nbytes)
-    return out
+    r = (_binding_handle or _binding()).attn_paged(q, k_cache, v_cache, page_table, kv_lens, q_offsets, max_q_len,
+                                                   causal, out, lse, scale, workspace, stream)
+    if r.__class__ is int:
+        raise DFlashError("dflash_attn_paged", r)
+    return r
 
 
 def dflash_verify(target_probs, draft_probs, draft_tokens, draft_offsets, accept_u, sample_u, max_draft,
@@ -656,36 +517,11 @@ def dflash_verify(target_probs, draft_probs, draft_tokens, draft_offsets, accept
     has its n + 1 rows from draft_offsets[r] + r on.  accept_u [total_draft] and
     sample_u [R] are fp32 in [0, 1).  Returns out_tokens [R, max_draft + 1] (the
     accepted tokens, the drawn one, then -1) and num_accepted [R], int32."""
-    torch = _torch()
-    lib = load_library()
-    dev, f32, i32 = target_probs.get_device(), torch.float32, torch.int32
-    if target_probs.dim() != 2 or target_probs.stride(1) != 1 or draft_offsets.dim() != 1:
-        raise ValueError("target_probs must be [rows, V] with contiguous rows, draft_offsets [R + 1]")
-    rows, V = target_probs.shape
-    T, R = draft_tokens.shape[0], draft_offsets.shape[0] - 1
-    if rows < T + R:
-        raise ValueError("target_probs needs a row for every drafted token and one more for every request")
-    if not target_probs.is_cuda or target_probs.dtype is not f32:
-        raise ValueError("target_probs must be a float32 CUDA tensor")
-    ps, qp, qs = target_probs.stride(0) if rows > 1 else 0, None, 0
-    if draft_probs is not None:
-        if (draft_probs.shape != (T, V) or draft_probs.dtype is not f32 or draft_probs.get_device() != dev or
-                (V > 1 and draft_probs.stride(1) != 1)):
-            raise ValueError("draft_probs must be a float32 [total_draft, V] tensor with contiguous rows on the "
-                             "device of target_probs")
-        if T > 0:
-            qp, qs = draft_probs.data_ptr(), draft_probs.stride(0) if T > 1 else 0
-    if out_tokens is None:
-        out_tokens = torch.empty((R, max_draft + 1), dtype=i32, device=target_probs.device)
-    if num_accepted is None:
-        num_accepted = torch.empty(R, dtype=i32, device=target_probs.device)
-    d = _VerifyDims(R, V, T, int(max_draft), ps, qs)
-    _call("dflash_verify", lib.dflash_verify, dev, stream, d, target_probs.data_ptr(), qp,
-          _arg(draft_tokens, "draft_tokens", dev, i32, (T,)), _arg(draft_offsets, "draft_offsets", dev, i32),
-          _arg(accept_u, "accept_u", dev, f32, (T,)), _arg(sample_u, "sample_u", dev, f32, (R,)),
-          _arg(out_tokens, "out_tokens", dev, i32, (R, max_draft + 1)),
-          _arg(num_accepted, "num_accepted", dev, i32, (R,)))
-    return out_tokens, num_accepted
+    r = (_binding_handle or _binding()).verify(target_probs, draft_probs, draft_tokens, draft_offsets, accept_u,
+                                               sample_u, max_draft, out_tokens, num_accepted, stream)
+    if r.__class__ is int:
+        raise DFlashError("dflash_verify", r)
+    return r
 
 
 def dflash_build_schedule_host(B, S, Q, anchors, block_size) -> np.ndarray:

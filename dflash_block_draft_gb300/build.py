@@ -1,16 +1,21 @@
-"""Build the C-ABI shared library libdflash_attn.so in-tree with nvcc (sm_103a).
+"""Build the C-ABI shared library libdflash_attn.so in-tree with nvcc (sm_103a), and
+the Python entry of the serving operators (_dflash_binding.so) with g++ against
+the installed torch.
 
-Each translation unit compiles in parallel; the link step produces
-``dflash_block_draft_gb300/_lib/libdflash_attn.so``.  Object files go to
+Each translation unit compiles in parallel; the link steps produce
+``dflash_block_draft_gb300/_lib/libdflash_attn.so`` and, linked to it,
+``_lib/_dflash_binding.so``.  Object files go to
 ``dflash_block_draft_gb300/_build/``.  Both are git-ignored.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -19,6 +24,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OBJ_DIR = os.path.join(HERE, "_build")
 LIB_DIR = os.path.join(HERE, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libdflash_attn.so")
+BINDING_PATH = os.path.join(LIB_DIR, "_dflash_binding.so")
 
 SOURCES = ["api.cu", "attn_simt.cu", "attn_tc.cu", "mask_scan.cu", "dense_noalloc.cu",
            "attn_decode.cu", "attn_bwd.cu", "attn_bwd_tc.cu", "attn_latent.cu", "api_serving.cu", "qk_norm_rope.cu",
@@ -41,7 +47,41 @@ def _deps():
 
 
 def up_to_date() -> bool:
-    return os.path.exists(LIB_PATH) and os.path.getmtime(LIB_PATH) >= _deps()
+    newest = _deps()
+    return all(os.path.exists(p) and os.path.getmtime(p) >= newest for p in (LIB_PATH, BINDING_PATH))
+
+
+def _torch_dir() -> str:
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        raise RuntimeError("torch not found: the Python binding cannot be built")
+    return list(spec.submodule_search_locations)[0]
+
+
+def _run(cmd, what):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    return r
+
+
+def _compile_binding() -> str:
+    torch = _torch_dir()
+    obj = os.path.join(OBJ_DIR, "binding.o")
+    inc = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"), INCLUDE]
+    _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-w",
+          *[f"-I{d}" for d in inc], "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj], "g++ on binding.cpp")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    torch = os.path.join(_torch_dir(), "lib")
+    tmp = BINDING_PATH + f".{os.getpid()}.tmp"
+    _run([os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, f"-L{LIB_DIR}", "-ldflash_attn", f"-L{torch}",
+          "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{torch}"],
+         "link of the binding")
+    os.replace(tmp, BINDING_PATH)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
@@ -62,15 +102,16 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             sys.stderr.write(r.stdout + r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES), os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES) + 1, os.cpu_count() or 4)) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(compile_one, SOURCES))
+        binding = binding.result()
     tmp = LIB_PATH + f".{os.getpid()}.tmp"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs, "-ldl", "-lrt",
            "-lpthread"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    _run(cmd, "link")
     os.replace(tmp, LIB_PATH)
+    _link_binding(binding)
     return LIB_PATH
 
 
