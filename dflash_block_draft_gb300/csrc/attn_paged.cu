@@ -7,8 +7,8 @@
 // in one pass over the keys, the output rescaled by 2^(m_old - m_new) where the
 // running maximum m rises.
 //
-// A CTA holds a row tile's queries in shared memory and walks its key tiles of 32
-// positions, which arrive by 16-byte asynchronous copies two tiles deep; the rows'
+// A CTA holds a row tile's queries in shared memory and walks its key tiles of 64
+// positions (32 where rows are longer than 256 bytes), which arrive by 16-byte asynchronous copies two tiles deep; the rows'
 // offsets (page table and page row) are worked out one tile ahead of the copies.
 // Each thread has 4 rows of the scores and of the output in registers, and all
 // threads of a row lie in one warp, so that the softmax needs shuffles only and a
@@ -27,7 +27,6 @@
 namespace dflash {
 namespace paged {
 
-constexpr int kSimtBN = 32;
 constexpr int kSms = 152;
 // CTAs of a launch at most: 4 an SM with 16-row tiles, 2 with 64-row tiles.
 constexpr int kSimtPerSm16 = 4, kSimtPerSm64 = 2;
@@ -56,7 +55,7 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
 
 template <typename T, int BM, int DMAX>
 struct Simt {
-  static constexpr int BN = kSimtBN;
+  static constexpr int BN = DMAX * sizeof(T) <= 256 ? 64 : 32;  // two stages of K and V for several CTAs an SM
   static constexpr int kThreads = BM == 16 ? 128 : 256;
   static constexpr int kVec = 16 / sizeof(T);
   static constexpr int kStride = DMAX + kVec;  // elements from row to row of K and V
@@ -86,7 +85,10 @@ __global__ void __launch_bounds__(Simt<T, BM, DMAX>::kThreads)
   typename C::Smem& s = *reinterpret_cast<typename C::Smem*>(raw);
   const int tid = threadIdx.x;
   const int ty = tid / TX, tx = tid % TX;
-  const int D = a.D, per = D / VEC;  // 16-byte pieces of a row
+  const int D = a.D;
+  // copies: 16-byte piece tid % kPer of rows tid / kPer, + kRows, ...
+  constexpr int kPer = DMAX / VEC, kRows = kThreads / kPer;
+  static_assert(kRows >= 1 && BN % kRows == 0, "copy layout");
   find_range<BN, kThreads>(a, &s.range, s.scratch);
   Walker<BN> walk(a, s.range);
   Piece pc;
@@ -114,11 +116,15 @@ __global__ void __launch_bounds__(Simt<T, BM, DMAX>::kThreads)
     };
     auto fetch = [&](int kt) {  // its offsets are in place
       if (kt < pc.kt1) {
-        for (int i = tid; i < BN * per; i += kThreads) {
-          const int r = i / per, c = (i - r * per) * VEC;
-          const long long ko = s.koff[kt % 3][r], vo = s.voff[kt % 3][r];
-          copy16(&s.k[kt & 1][r * C::kStride + c], static_cast<const T*>(a.kc) + max(ko, 0ll) + c, ko >= 0);
-          copy16(&s.v[kt & 1][r * C::kStride + c], static_cast<const T*>(a.vc) + max(vo, 0ll) + c, vo >= 0);
+        const int c = tid % kPer * VEC;
+        if (c < D) {
+#pragma unroll
+          for (int i = 0; i < BN / kRows; ++i) {
+            const int r = tid / kPer + i * kRows;
+            const long long ko = s.koff[kt % 3][r], vo = s.voff[kt % 3][r];
+            copy16(&s.k[kt & 1][r * C::kStride + c], static_cast<const T*>(a.kc) + max(ko, 0ll) + c, ko >= 0);
+            copy16(&s.v[kt & 1][r * C::kStride + c], static_cast<const T*>(a.vc) + max(vo, 0ll) + c, vo >= 0);
+          }
         }
       }
       copy_commit();
@@ -145,6 +151,7 @@ __global__ void __launch_bounds__(Simt<T, BM, DMAX>::kThreads)
 #pragma unroll
       for (int c = 0; c < NC; ++c) o[i][c] = 0.f;
     }
+    const bool idle = 32 / TX * 4 * (tid / 32) >= nrow;  // none of the warp's rows exists: it only copies
     __syncthreads();
     fetch(pc.kt0);
     for (int kt = pc.kt0; kt < pc.kt1; ++kt) {
@@ -155,85 +162,87 @@ __global__ void __launch_bounds__(Simt<T, BM, DMAX>::kThreads)
       const T* ks = s.k[kt & 1];
       const T* vs = s.v[kt & 1];
       const int k0 = kt * BN;
-      // scores: rows 4 ty .., columns tx + TX j
-      float x[4][CT];
+      if (!idle) {
+        // scores: rows 4 ty .., columns tx + TX j
+        float x[4][CT];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < CT; ++j) x[i][j] = 0.f;
+          for (int j = 0; j < CT; ++j) x[i][j] = 0.f;
 #pragma unroll 4
-      for (int d = 0; d < D; d += 4) {
-        float4 kk[CT];
+        for (int d = 0; d < D; d += 4) {
+          float4 kk[CT];
 #pragma unroll
-        for (int j = 0; j < CT; ++j) kk[j] = load4(ks + (tx + TX * j) * C::kStride + d);
+          for (int j = 0; j < CT; ++j) kk[j] = load4(ks + (tx + TX * j) * C::kStride + d);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float4 qq = load4(s.q + (4 * ty + i) * C::kQStride + d);
+          for (int i = 0; i < 4; ++i) {
+            const float4 qq = load4(s.q + (4 * ty + i) * C::kQStride + d);
 #pragma unroll
-          for (int j = 0; j < CT; ++j)
-            x[i][j] = fmaf(qq.x, kk[j].x, fmaf(qq.y, kk[j].y, fmaf(qq.z, kk[j].z, fmaf(qq.w, kk[j].w, x[i][j]))));
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float mx = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < CT; ++j) {
-          if (k0 + tx + TX * j >= lim[i]) x[i][j] = -INFINITY;
-          mx = fmaxf(mx, x[i][j]);
-        }
-#pragma unroll
-        for (int w = TX / 2; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w, TX));
-        const float m1 = fmaxf(m[i], mx * a.scale_log2);
-        const float mm = m1 == -INFINITY ? 0.f : m1;
-        float sum = 0.f;
-#pragma unroll
-        for (int j = 0; j < CT; ++j) {
-          // scaled and moved in one rounding: of large scores only the difference is rounded
-          const float e = exp2f(fmaf(x[i][j], a.scale_log2, -mm));
-          s.p[(4 * ty + i) * C::kPStride + tx + TX * j] = e;
-          sum += e;
-        }
-#pragma unroll
-        for (int w = TX / 2; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w, TX);
-        const float al = exp2f(m[i] - mm);
-        l[i] = l[i] * al + sum;
-        m[i] = m1;
-#pragma unroll
-        for (int c = 0; c < NC; ++c) o[i][c] *= al;
-      }
-      __syncwarp();  // the rows' weights, written by this warp alone
-#pragma unroll 2
-      for (int k = 0; k < BN; k += 4) {
-        float pp[4][4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float4 w = load4(s.p + (4 * ty + i) * C::kPStride + k);
-          pp[i][0] = w.x; pp[i][1] = w.y; pp[i][2] = w.z; pp[i][3] = w.w;
-        }
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-          for (int u = 0; u < U; ++u) {
-            const int c0 = (tx + TX * u) * VW;
-            float vv[VW];
-#pragma unroll
-            for (int e = 0; e < VW; ++e) vv[e] = 0.f;
-            if (c0 < D) {
-              const T* vp = vs + (k + kk) * C::kStride + c0;
-              if constexpr (VW == 4) {
-                const float4 w = load4(vp);
-                vv[0] = w.x; vv[1] = w.y; vv[2] = w.z; vv[3] = w.w;
-              } else {
-#pragma unroll
-                for (int e = 0; e < VW; ++e) vv[e] = to_f32(vp[e]);
-              }
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-              for (int e = 0; e < VW; ++e) o[i][u * VW + e] = fmaf(pp[i][kk], vv[e], o[i][u * VW + e]);
+            for (int j = 0; j < CT; ++j)
+              x[i][j] = fmaf(qq.x, kk[j].x, fmaf(qq.y, kk[j].y, fmaf(qq.z, kk[j].z, fmaf(qq.w, kk[j].w, x[i][j]))));
           }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float mx = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < CT; ++j) {
+            if (k0 + tx + TX * j >= lim[i]) x[i][j] = -INFINITY;
+            mx = fmaxf(mx, x[i][j]);
+          }
+#pragma unroll
+          for (int w = TX / 2; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w, TX));
+          const float m1 = fmaxf(m[i], mx * a.scale_log2);
+          const float mm = m1 == -INFINITY ? 0.f : m1;
+          float sum = 0.f;
+#pragma unroll
+          for (int j = 0; j < CT; ++j) {
+            // scaled and moved in one rounding: of large scores only the difference is rounded
+            const float e = exp2f(fmaf(x[i][j], a.scale_log2, -mm));
+            s.p[(4 * ty + i) * C::kPStride + tx + TX * j] = e;
+            sum += e;
+          }
+#pragma unroll
+          for (int w = TX / 2; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w, TX);
+          const float al = exp2f(m[i] - mm);
+          l[i] = l[i] * al + sum;
+          m[i] = m1;
+#pragma unroll
+          for (int c = 0; c < NC; ++c) o[i][c] *= al;
+        }
+        __syncwarp();  // the rows' weights, written by this warp alone
+#pragma unroll 2
+        for (int k = 0; k < BN; k += 4) {
+          float pp[4][4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float4 w = load4(s.p + (4 * ty + i) * C::kPStride + k);
+            pp[i][0] = w.x; pp[i][1] = w.y; pp[i][2] = w.z; pp[i][3] = w.w;
+          }
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              const int c0 = (tx + TX * u) * VW;
+              float vv[VW];
+#pragma unroll
+              for (int e = 0; e < VW; ++e) vv[e] = 0.f;
+              if (c0 < D) {
+                const T* vp = vs + (k + kk) * C::kStride + c0;
+                if constexpr (VW == 4) {
+                  const float4 w = load4(vp);
+                  vv[0] = w.x; vv[1] = w.y; vv[2] = w.z; vv[3] = w.w;
+                } else {
+#pragma unroll
+                  for (int e = 0; e < VW; ++e) vv[e] = to_f32(vp[e]);
+                }
+              }
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int e = 0; e < VW; ++e) o[i][u * VW + e] = fmaf(pp[i][kk], vv[e], o[i][u * VW + e]);
+            }
+        }
       }
       put_offsets(kt + 2, page);
       __syncthreads();  // this stage's buffers may be filled again; the offsets are in place

@@ -13,6 +13,8 @@
 // partner components by shuffle needed twice the cosines and 8 shuffles a head.)
 // Head shapes whose planes cut through these vectors (rot % 8 != 0), and
 // misaligned tensors, run on a plain kernel with a warp for each head.
+#include <limits.h>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -20,6 +22,7 @@ namespace dflash {
 namespace {
 
 constexpr int kThreads = 256;
+
 
 // Four components as they lie in memory; in registers they are pairs, for the
 // packed fp32 instructions (these kernels issue about as long as they load).
@@ -119,50 +122,17 @@ struct Place {
   long long krow, vrow;
 };
 
-// Whole warp: the placement of token t (the same in every lane); what has no place
-// is recorded.  The request is found 32 offsets at a time, and what the last 32
-// candidates need is loaded together, so that the chain of dependent loads is short:
-// offsets and lengths, the page, (the caller's) table row.
-template <bool PAGED>
-__device__ __forceinline__ Place place_token(const RopeArgs& a, int t) {
+// The rest of token t's placement, request r found; what has no place is recorded.
+__device__ __forceinline__ Place place_in(const RopeArgs& a, int t, int r) {
   Place pl = {0, 0, 0, 0};
-  if (t >= a.T) return pl;
-  if (!PAGED) {
-    pl.pos = a.rot > 0 ? a.pos[t] : 0;
-    pl.ok = a.rot <= 0 || (pl.pos >= 0 && pl.pos < a.max_pos);
-    if (!pl.ok) record_error(a.err, DFLASH_ERR_INVALID);
-    return pl;
-  }
-  const int lane = threadIdx.x & 31;
-  const int end = a.q_off[a.R];
-  int lo = 0, n = a.R;  // the last request that begins at or before t lies in [lo, lo + n)
-  while (n > 32) {
-    const int step = (n + 31) / 32;
-    const int at = lane * step;
-    const unsigned m = __ballot_sync(0xffffffffu, at < n && a.q_off[lo + at] <= t);
-    const int k = m ? 31 - __clz(m) : 0;
-    lo += k * step;
-    n = min(step, n - k * step);
-  }
-  int q0 = 0, q1 = 0, len = 0;
-  if (lane < n) {
-    q0 = a.q_off[lo + lane];
-    q1 = a.q_off[lo + lane + 1];
-    len = a.kv_lens[lo + lane];
-  }
-  const unsigned m = __ballot_sync(0xffffffffu, lane < n && q0 <= t);
-  const int k = m ? 31 - __clz(m) : 0;
-  q0 = __shfl_sync(0xffffffffu, q0, k);
-  q1 = __shfl_sync(0xffffffffu, q1, k);
-  len = __shfl_sync(0xffffffffu, len, k);
-  if (t >= end) return pl;  // padding behind the last request
+  const int q0 = a.q_off[r], q1 = a.q_off[r + 1], len = a.kv_lens[r];
   const long long p = (long long)len - (q1 - q0) + (t - q0);
   if (q0 < 0 || q0 > t || q1 <= t || q1 > a.T || p < 0 || p >= (long long)a.max_pages * a.P ||
       (a.rot > 0 && p >= a.max_pos)) {
     record_error(a.err, DFLASH_ERR_INVALID);
     return pl;
   }
-  const int pp = (int)p, page = a.table[(long long)(lo + k) * a.max_pages + pp / a.P];
+  const int pp = (int)p, page = a.table[(long long)r * a.max_pages + pp / a.P];
   if (page < 0 || page >= a.num_pages) {
     record_error(a.err, DFLASH_ERR_INVALID);
     return pl;
@@ -175,19 +145,64 @@ __device__ __forceinline__ Place place_token(const RopeArgs& a, int t) {
   return pl;
 }
 
+// Whole warp: lane i < n places token t0 + i (ok = 0 elsewhere).  The request of t0,
+// the last one that begins at or before it, is found 32 offsets at a time; the
+// next tokens' requests follow from the 32 offsets behind it, or, where more
+// requests than that end among them (empty ones), by a search of the lane's own.
+__device__ __forceinline__ Place place_tokens(const RopeArgs& a, long long t0, int n) {
+  const int lane = threadIdx.x & 31;
+  const long long t = t0 + lane;
+  const int end = a.q_off[a.R];
+  int lo = 0, len = a.R;  // it lies in [lo, lo + len)
+  while (len > 1) {
+    const int step = (len + 31) / 32;
+    const int at = lane * step;
+    const unsigned m = __ballot_sync(0xffffffffu, at < len && a.q_off[lo + at] <= t0);
+    const int k = m ? 31 - __clz(m) : 0;
+    lo += k * step;
+    len = min(step, len - k * step);
+  }
+  const int next = lo + 1 + lane < a.R ? a.q_off[lo + 1 + lane] : INT_MAX;
+  int r = lo;
+  for (int i = 0; i < n; ++i) {
+    const int c = __popc(__ballot_sync(0xffffffffu, next <= t0 + i));
+    if (lane == i) r = lo + c;
+  }
+  if (lane < n && t < a.T && t < end) {
+    if (r - lo == 32) {
+      int hi = a.R;
+      while (hi - r > 1) {
+        const int mid = (r + hi) >> 1;
+        if (a.q_off[mid] <= t) r = mid;
+        else hi = mid;
+      }
+    }
+    return place_in(a, (int)t, r);
+  }
+  return Place{0, 0, 0, 0};
+}
+
+__device__ __forceinline__ Place place_position(const RopeArgs& a, int t) {
+  Place pl = {0, 0, 0, 0};
+  pl.pos = a.rot > 0 ? a.pos[t] : 0;
+  pl.ok = a.rot <= 0 || (pl.pos >= 0 && pl.pos < a.max_pos);
+  if (!pl.ok) record_error(a.err, DFLASH_ERR_INVALID);
+  return pl;
+}
+
 // Forward.  A block takes HPG query heads, key heads or (paged) value heads of one
 // token a group: all loads of a group go out together, before the tokens' places
 // are found, and what differs between kinds of heads is the same in a whole block.
 // Blocks count [tokens][chunk]; chunks below nq are query heads, below nq + nk key
 // heads.  (A block that took all heads of its tokens, with the table rows in shared
-// memory, spent more instructions on which head is whose than on the heads: 205 an
-// two heads against 110, and 215 us against 125 for 32768 tokens of 40 heads.)
+// memory, spent more instructions on which head is whose than on the heads: 205 for
+// every two heads, and 215 us against 117 for 32768 tokens of 40 heads.)
 template <typename T, int LANES, int HPG, bool PAGED>
 __global__ void __launch_bounds__(kThreads)
     rope_fwd_kernel(const __grid_constant__ RopeArgs a, int nq, int nk, int nchunk) {
   constexpr int kGroups = kThreads / LANES;
   __shared__ Place s_place[PAGED ? kGroups : 1];
-  const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
+  const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES, lane32 = threadIdx.x & 31;
   const int chunk = blockIdx.x % nchunk;
   const long long t0 = (long long)(blockIdx.x / nchunk) * kGroups, t = t0 + group;
   const bool is_q = chunk < nq, is_v = PAGED && chunk >= nq + nk;
@@ -212,14 +227,14 @@ __global__ void __launch_bounds__(kThreads)
   }
   Place pl = {0, 0, 0, 0};
   if (PAGED) {
-    for (int i = threadIdx.x >> 5; i < kGroups; i += kThreads / 32) {
-      const Place p = place_token<true>(a, (int)min(t0 + i, (long long)a.T));
-      if ((threadIdx.x & 31) == 0) s_place[i] = p;
+    if (threadIdx.x < 32) {
+      const Place p = place_tokens(a, t0, kGroups);
+      if (lane32 < kGroups) s_place[lane32] = p;
     }
     __syncthreads();
     pl = s_place[group];
   } else if (t < a.T) {
-    pl = place_token<false>(a, (int)t);
+    pl = place_position(a, (int)t);
   }
   if (!is_v) {
     float2 cs[2], sn[2];
@@ -269,10 +284,13 @@ __global__ void __launch_bounds__(kThreads)
 // shared memory and writes one row of partial sums, so the order of the sums is
 // fixed.  Blocks count [row of blocks][chunk]; chunks below nq are query heads.
 template <typename T, int LANES>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
     rope_bwd_kernel(const __grid_constant__ RopeArgs a, int hpg, int nq, int nchunk) {
   constexpr int kGroups = kThreads / LANES;
-  constexpr int kBatch = sizeof(T) == 2 ? 4 : 2;
+  // Heads in flight a group.  Two (one in fp32) with four blocks an SM: 184 us for 32768
+  // tokens of 40 heads; four with two blocks 191; the next heads' loads ahead of
+  // the arithmetic, with two blocks, 183.
+  constexpr int kBatch = sizeof(T) == 2 ? 2 : 1;
   __shared__ float red[kGroups][LANES * 8];
   const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
   const int chunk = blockIdx.x % nchunk, brow = blockIdx.x / nchunk, brows = gridDim.x / nchunk;
@@ -422,7 +440,16 @@ __global__ void __launch_bounds__(kThreads) rope_fwd_plain_kernel(const __grid_c
   const long long unit = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (unit >= (long long)a.T * heads) return;
   const int t = (int)(unit / heads), h = (int)(unit % heads);
-  const Place pl = place_token<PAGED>(a, t);
+  Place pl;
+  if (PAGED) {
+    pl = place_tokens(a, t, 1);  // in lane 0
+    pl.ok = __shfl_sync(0xffffffffu, pl.ok, 0);
+    pl.pos = __shfl_sync(0xffffffffu, pl.pos, 0);
+    pl.krow = __shfl_sync(0xffffffffu, pl.krow, 0);
+    pl.vrow = __shfl_sync(0xffffffffu, pl.vrow, 0);
+  } else {
+    pl = place_position(a, t);
+  }
   if (!pl.ok) return;
   const bool is_q = h < a.Hq, is_v = PAGED && h >= a.Hq + a.Hkv;
   const T* src;
@@ -465,7 +492,7 @@ __global__ void __launch_bounds__(kThreads) rope_bwd_plain_kernel(const __grid_c
   const long long units = (long long)a.T * heads;
   for (long long unit = (long long)blockIdx.x * kWarps + warp; unit < units; unit += (long long)gridDim.x * kWarps) {
     const int t = (int)(unit / heads), h = (int)(unit % heads);
-    const Place pl = place_token<false>(a, t);
+    const Place pl = place_position(a, t);
     if (!pl.ok) continue;
     const bool is_q = h < a.Hq;
     const long long at = is_q ? ((long long)t * a.Hq + h) * a.D : ((long long)t * a.Hkv + (h - a.Hq)) * a.D;
@@ -534,14 +561,16 @@ cudaError_t run_fwd(const RopeArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-// Heads a group: as many as still give every SM a few blocks.  The vectors of 8
-// (bf16) or 4 (fp32) heads are 128 bytes a lane in flight.
+// Heads a group: as many as still give every SM two blocks.  The vectors of 8 (bf16)
+// or 4 (fp32) heads are 128 bytes a lane in flight.  (Appending 1024 tokens of 48
+// heads: 6.6 us so, 7.4 us with four blocks an SM asked for.)
 template <typename T, int LANES, bool PAGED>
 cudaError_t pick_fwd(const RopeArgs& a, cudaStream_t s) {
   constexpr int most = sizeof(T) == 2 ? 8 : 4;
   const long long rows = ((long long)a.T + kThreads / LANES - 1) / (kThreads / LANES);
-  const long long want = 152 * 4, heads = a.Hq + (PAGED ? 2 : 1) * a.Hkv;
+  const long long want = 152 * 2, heads = a.Hq + (PAGED ? 2 : 1) * a.Hkv;
   if (rows * heads / most >= want) return run_fwd<T, LANES, most, PAGED>(a, s);
+  if (rows * heads / 4 >= want) return run_fwd<T, LANES, 4, PAGED>(a, s);
   if (rows * heads / 2 >= want) return run_fwd<T, LANES, 2, PAGED>(a, s);
   return run_fwd<T, LANES, 1, PAGED>(a, s);
 }
