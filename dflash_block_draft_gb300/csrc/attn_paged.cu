@@ -414,7 +414,9 @@ PagedPlan plan_of(bool bf16, int Hq, int Hkv, int D, int max_q, int P) {
   p.rows = p.tc ? paged_tc_rows(G, max_q) : simt_rows(G, max_q);
   p.max_grid = p.tc ? kSms : p.rows == 16 ? kSimtMaxGrid : kSimtPerSm64 * kSms;
   const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  const size_t slots = 2 * (size_t)p.max_grid * p.rows;
+  size_t slots = 2 * (size_t)p.max_grid * p.rows;
+  // a tensor-core call on a cache without pages runs on the CUDA cores
+  if (p.tc && slots < 2 * 2 * (size_t)kSms * 16) slots = 2 * 2 * (size_t)kSms * 16;
   p.ml = up(kSimtMaxGrid * sizeof(Meta));
   p.o = p.ml + up(slots * sizeof(float2));
   p.total = p.o + up(slots * D * sizeof(float));
@@ -443,7 +445,7 @@ cudaError_t launch_attn_paged(PagedArgs a, bool bf16, void* ws, cudaStream_t str
   int grid = sms;
   cudaError_t e;
   // Without a page there is no tensor to describe to TMA: the CUDA-core kernel with
-  // its small row tiles (2 x 304 slots of 16 rows fit the planned 2 x 152 of 65 or more).
+  // its small row tiles.
   if (p.tc && a.num_pages > 0) {
     e = launch_paged_tc(a, grid, stream);
   } else {

@@ -16,11 +16,15 @@
 //          chunks, bound by the tensor cores;
 //   SPLIT  the halves are the even and the odd key tiles of one row tile, and
 //          are added up at the end of a piece: single tokens and draft blocks,
-//          bound by memory, where a second row tile would be padding.
+//          bound by memory, where a second row tile would be padding.  Row tiles of
+//          up to 64 rows have two query buffers, so that the next one's queries are
+//          there in time.
 //
 // Pages: a 128-position tile arrives as 128 / b boxes of b = gcd(page_size, 128)
 // positions, one TMA load for each box and 64 components, lane by lane; a tile may
-// so begin and end anywhere in a page.  Positions behind the request's length are
+// so begin and end anywhere in a page.  Boxes of 8 positions of 128 components bring
+// both halves of the components at once (their 1 KB blocks then lie next to each
+// other): 64 loads a tile took 733 us where 32 take 472.  Positions behind the request's length are
 // masked in S; of V their rows are set to zero in shared memory before P V reads
 // them, since what an unfinished page holds there may be NaN.  A page that does
 // not exist is loaded from behind the tensor's end, which TMA fills with zeros.
@@ -77,9 +81,9 @@ struct Cfg {
   static constexpr uint32_t kOffRing = kQBytes;
   static constexpr uint32_t kOffBar = kOffRing + kSlots * kSlot;
   enum : int {
-    Q_FULL = 0,
-    Q_EMPTY = 1,
-    RING_FULL = 2,
+    Q_FULL = 0,   // 2 (one buffer each)
+    Q_EMPTY = 2,  // 2
+    RING_FULL = 4,
     RING_EMPTY = RING_FULL + (int)kSlots,
     S_FULL = RING_EMPTY + (int)kSlots,
     P_LO = S_FULL + 2,     // P of keys 0-63 written
@@ -103,8 +107,11 @@ struct Cfg {
 
 struct TcPagedArgs {
   PagedArgs a;
-  int tokens;  // tokens of a 128-row tile: 128 / G
+  int tokens;  // tokens of a tile of up to 128 rows: 128 / G, or all that a request can have
   int box;     // positions of a TMA box
+  int dual;    // boxes hold both panels
+  uint32_t panel, group;  // bytes from panel to panel and from 8 rows to the next 8 of a K or V tile
+  int q_bufs;  // 2: row tiles of up to 64 rows, the second buffer in the first one's rows 64 ..
   int out_v8;  // output rows may be written in 32-byte pieces
 };
 
@@ -114,6 +121,15 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* m, 
       "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
       "[%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1),
       "r"(c2), "r"(c3)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, int c2,
+                                            int c3, int c4) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+      "[%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1),
+      "r"(c2), "r"(c3), "r"(c4)
       : "memory");
 }
 
@@ -157,8 +173,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == kThreads - 1) {  // the first threads look at the requests meanwhile
     const uint32_t users = PAIR ? 2 : 1;  // MMA issuers that read a ring slot
-    ptx::mbar_init(ctl.bar(C::Q_FULL), 1);
-    ptx::mbar_init(ctl.bar(C::Q_EMPTY), 2);
+    for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(ctl.bar(C::Q_FULL + b), 1);
+      ptx::mbar_init(ctl.bar(C::Q_EMPTY + b), 2);
+    }
     for (uint32_t s = 0; s < C::kSlots; ++s) {
       ptx::mbar_init(ctl.bar(C::RING_FULL + s), 1);
       ptx::mbar_init(ctl.bar(C::RING_EMPTY + s), users);
@@ -194,6 +212,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const uint32_t ring = sbase + C::kOffRing;
   const int tile_rows = ta.tokens * a.G;  // rows of one half's tile
+  // Buffer and phase parity of the n-th row tile's queries.
+  const uint32_t q_two = ta.q_bufs == 2;
+  auto q_buf = [&](uint32_t n) { return n & q_two; };
+  auto q_parity = [&](uint32_t n) { return (n >> q_two) & 1u; };
   if (warp < 4) ptx::setmaxnreg_dec<kCtlRegs>();
 
   if (warp == 0) {
@@ -205,7 +227,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool stop = false;
     const int boxes = kBN / ta.box;                     // boxes of a panel
     const int my_box = lane % boxes, my_pn = lane / boxes;  // this lane's box
-    const bool mine = lane < boxes * NP;
+    const bool mine = lane < (ta.dual ? boxes : boxes * NP);
+    const uint32_t my_dst = ta.dual ? lane * 2048u : my_pn * kPanel + my_box * ta.box * 128u;
     // Page id of this lane's box of key tile kt; the load is left in flight.
     auto page_of = [&](int kt) {
       const int p0 = kt * kBN + my_box * ta.box;
@@ -237,9 +260,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           load1 += r;
           if (lane == 0) ptx::mbar_arrive_expect_tx(ctl.bar(C::RING_FULL + s), C::kSlot);
           __syncwarp();
-          if (mine)
-            tma_load_4d(ring + s * C::kSlot + my_pn * kPanel + my_box * ta.box * 128, kv ? &tmV : &tmK,
-                        ctl.bar(C::RING_FULL + s), 64 * my_pn, pc.h, row, page);
+          if (mine) {
+            const uint32_t dst = ring + s * C::kSlot + my_dst, full = ctl.bar(C::RING_FULL + s);
+            const CUtensorMap* map = kv ? &tmV : &tmK;
+            if (ta.dual) tma_load_5d(dst, map, full, 0, row, 0, pc.h, page);
+            else tma_load_4d(dst, map, full, 64 * my_pn, pc.h, row, page);
+          }
         }
       }
     }
@@ -257,15 +283,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t q_bytes = (uint32_t)tile_rows * 128u;  // bytes of a box
       uint32_t n = 0;
       while (walk.next(&pc)) {
-        if (n > 0 && !ctl.wait(C::Q_EMPTY, (n - 1) & 1u)) break;
-        ptx::mbar_arrive_expect_tx(ctl.bar(C::Q_FULL), q_bytes * (PAIR ? 2 : 1) * NP);
+        const uint32_t b = q_buf(n), full = ctl.bar(C::Q_FULL + b);
+        if (!ctl.wait(C::Q_EMPTY + b, q_parity(n) ^ 1u)) break;
+        ptx::mbar_arrive_expect_tx(full, q_bytes * (PAIR ? 2 : 1) * NP);
         for (int i = 0; i < (PAIR ? 2 : 1); ++i)
           for (int pn = 0; pn < NP; ++pn)
-            ptx::tma_load_3d(sbase + C::kOffQ + (i * NP + pn) * kPanel, &tmQ, ctl.bar(C::Q_FULL), 64 * pn,
+            ptx::tma_load_3d(sbase + C::kOffQ + (i * NP + pn) * kPanel + b * (kPanel / 2), &tmQ, full, 64 * pn,
                              pc.h * a.G, pc.q.q0 + (pc.rt * (PAIR ? 2 : 1) + i) * ta.tokens);
         ++n;
       }
-      if (n > 0) ctl.wait_landed(C::Q_FULL, (n - 1) & 1u);
+      // the last load of each buffer
+      for (uint32_t i = n > q_two ? n - 1 - q_two : 0u; i < n; ++i)
+        ctl.wait_landed(C::Q_FULL + q_buf(i), q_parity(i));
     }
   } else if (warp == 1 || warp == 2) {
     // ------------------------------------------------------------ MMA issuers
@@ -274,8 +303,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t kIdescQK = ptx::idesc_bf16_f32(kBM, kBN, 0, 0);  // Q, K both K-major
       const uint32_t kIdescPV = ptx::idesc_bf16_f32(kBM, DP, 0, 1);   // P from TMEM, V MN-major
       const uint64_t dq = ptx::smem_desc(sbase + C::kOffQ + (PAIR ? i * NP * kPanel : 0u), 16, 1024);
-      const uint64_t dK = ptx::smem_desc(ring, 16, 1024);
-      const uint64_t dV = ptx::smem_desc(ring, kPanel, 1024);
+      const uint64_t dK = ptx::smem_desc(ring, 16, ta.group);
+      const uint64_t dV = ptx::smem_desc(ring, ta.panel, ta.group);
       const uint32_t d_s = tmem + kColS + 128u * i;  // S_i; P_i aliases its head
       const uint32_t d_o = tmem + kColO + 128u * i;
       const uint32_t r = PAIR ? 0u : (uint32_t)i;  // this half's ring
@@ -283,12 +312,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto full = [&](uint32_t c) { return ctl.wait(C::RING_FULL + C::slot(r, c), C::parity(c)); };
       auto release = [&](uint32_t c) { ptx::tc_commit(ctl.bar(C::RING_EMPTY + C::slot(r, c))); };
       // m: this half's tile number
-      auto issue_qk = [&](uint32_t m) {
+      auto issue_qk = [&](uint32_t m, uint32_t buf) {
         const uint64_t k = dK + ((C::slot(r, 2 * m) * C::kSlot) >> 4);
+        const uint64_t q = dq + ((buf * (kPanel / 2)) >> 4);
 #pragma unroll
         for (int ks = 0; ks < 4 * NP; ++ks) {
-          const uint32_t off = (uint32_t)(ks >> 2) * kPanel + (uint32_t)(ks & 3) * 32u;
-          ptx::mma_ss(d_s, dq + (off >> 4), k + (off >> 4), kIdescQK, ks > 0);
+          const uint32_t sub = (uint32_t)(ks & 3) * 32u, pn = (uint32_t)(ks >> 2);
+          ptx::mma_ss(d_s, q + ((pn * kPanel + sub) >> 4), k + ((pn * ta.panel + sub) >> 4), kIdescQK, ks > 0);
         }
         ptx::tc_commit(ctl.bar(C::S_FULL + i));
         release(2 * m);
@@ -296,8 +326,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto issue_pv = [&](uint32_t m, bool first, int ks0) {
         const uint64_t v = dV + ((C::slot(r, 2 * m + 1) * C::kSlot) >> 4);
 #pragma unroll
-        for (int ks = ks0; ks < ks0 + 4; ++ks)  // 16 keys: 8 packed P columns, two 1024-byte groups of V rows
-          ptx::mma_ts(d_o, d_s + (uint32_t)ks * 8u, v + (((uint32_t)ks * 2048u) >> 4), kIdescPV, !(first && ks == 0));
+        for (int ks = ks0; ks < ks0 + 4; ++ks)  // 16 keys: 8 packed P columns, two groups of 8 V rows
+          ptx::mma_ts(d_o, d_s + (uint32_t)ks * 8u, v + (((uint32_t)ks * 2u * ta.group) >> 4), kIdescPV,
+                      !(first && ks == 0));
       };
       // PV: keys 0-63 once that half of P is written, then the rest.
       auto pv = [&](uint32_t m, bool first) -> bool {
@@ -315,7 +346,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       Piece pc;
       bool stop = false;
       while (!stop && walk.next(&pc)) {
-        if (!ctl.wait(C::Q_FULL, n_q & 1u)) break;
+        const uint32_t buf = q_buf(n_q);
+        if (!ctl.wait(C::Q_FULL + buf, q_parity(n_q))) break;
         ++n_q;
         bool any = false, first_pv = true;
         for (int kt = pc.kt0; kt < pc.kt1; ++kt, ++g) {
@@ -339,13 +371,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           ptx::tc_fence_after();
-          issue_qk(mine);
+          issue_qk(mine, buf);
           if (PAIR) ptx::mbar_arrive(ctl.bar(C::QK_TURN + i));
           any = true;
           ++mine;
         }
         if (stop) break;
-        ptx::tc_commit(ctl.bar(C::Q_EMPTY));  // every QK of this half has been issued
+        ptx::tc_commit(ctl.bar(C::Q_EMPTY + buf));  // every QK of this half has been issued
         if (any) {
           if (!pv(mine - 1, first_pv)) break;
           ptx::tc_commit(ctl.bar(C::O_FULL + i));
@@ -400,11 +432,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           if (k0 + row >= pc.q.kv) {
-            uint4* v = reinterpret_cast<uint4*>(smem + C::kOffRing + s * C::kSlot + row * 128);
+            uint8_t* at = smem + C::kOffRing + s * C::kSlot + (row >> 3) * ta.group + (row & 7) * 128;
 #pragma unroll
             for (int pn = 0; pn < NP; ++pn)
 #pragma unroll
-              for (int e = 0; e < 8; ++e) v[pn * (kPanel / 16) + e] = make_uint4(0u, 0u, 0u, 0u);
+              for (int e = 0; e < 8; ++e)
+                reinterpret_cast<uint4*>(at + pn * ta.panel)[e] = make_uint4(0u, 0u, 0u, 0u);
           }
           ptx::fence_proxy_async_smem();
         }
@@ -470,8 +503,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const long long part = pc.slot >= 0 ? (long long)pc.slot * a.rows + (PAIR ? half * tile_rows : 0) + row : 0;
       const int head = pc.h * a.G + (row_ok ? f % a.G : 0);
       const long long token = (long long)pc.q.q0 + tok;
-      float w0 = 1.f, w1 = 0.f, m = m_used;
-      if (!PAIR) {
+      // SPLIT: both halves' accumulators are added up, each half taking half of the
+      // columns, or one half alone had tiles and finishes them by itself, while the
+      // other goes on to the next piece.
+      const bool both = !PAIR && had[0] && had[1];
+      float w0 = 1.f, w1 = 1.f, m = m_used;
+      if (both) {
         ml[half * kBM + row] = make_float2(m_used, l);
         ptx::mbar_arrive(ctl.bar(C::ML));
         if (!__all_sync(0xffffffffu, ctl.wait(C::ML, n_epi & 1u))) break;
@@ -485,44 +522,40 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool landed = true;
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        if (had[i] && (!PAIR || i == half)) landed = ctl.wait(C::O_FULL + i, n_full[i] & 1u) && landed;
+        if (both || (had[i] && i == half)) landed = ctl.wait(C::O_FULL + i, n_full[i] & 1u) && landed;
       if (!__all_sync(0xffffffffu, landed)) break;
 #pragma unroll
       for (int i = 0; i < 2; ++i) n_full[i] += had[i];
       ptx::tc_fence_after();
       const float inv = pc.slot >= 0 ? 1.f : l > 0.f ? 1.f / l : 0.f;
-      if (warp_ok) {
-        // PAIR: all DP columns of this half's accumulator; SPLIT: this half's share of the columns of both
-        constexpr int kCols = PAIR ? DP : DP / 2;
-        const int c0 = PAIR ? 0 : half * kCols;
+      w0 *= inv;
+      w1 *= inv;
+      if (warp_ok && (half ? had[1] : had[0])) {
+        const int c0 = both ? half * (DP / 2) : 0, c1 = both ? c0 + DP / 2 : DP;
         __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + (token * a.Hq + head) * a.D;
         float* pdst = a.part_o + part * a.D;
-#pragma unroll
-        for (int cc = 0; cc < kCols; cc += 32) {
+#pragma unroll 1
+        for (int cc = c0; cc < c1; cc += 32) {
           uint32_t o[32];
           __syncwarp();  // the TMEM reads take the whole warp
-          if (PAIR) {
-            ptx::tmem_ld32(o_col + cc, o);
+          ptx::tmem_ld32(both ? o_base + cc : o_col + cc, o);
+          if (!PAIR && both) {
+            uint32_t o1[32];
+            ptx::tmem_ld32(o_base + 128u + cc, o1);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              o[e] = __float_as_uint(fmaf(__uint_as_float(o1[e]), w1, __uint_as_float(o[e]) * w0));
+          } else {
             ptx::tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
-          } else {
-            uint32_t o1[32];
-            if (had[0]) ptx::tmem_ld32(o_base + c0 + cc, o);
-            if (had[1]) ptx::tmem_ld32(o_base + 128u + c0 + cc, o1);
-            ptx::tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const float v0 = had[0] ? __uint_as_float(o[e]) * w0 : 0.f;
-              const float v1 = had[1] ? __uint_as_float(o1[e]) * w1 : 0.f;
-              o[e] = __float_as_uint((v0 + v1) * inv);
-            }
           }
           if (!row_ok) {
           } else if (pc.slot >= 0) {
 #pragma unroll
             for (int e = 0; e < 32; e += 8)
-              if (c0 + cc + e < a.D) ptx::st_global_v8(pdst + c0 + cc + e, o + e);
+              if (cc + e < a.D) ptx::st_global_v8(pdst + cc + e, o + e);
           } else {
 #pragma unroll
             for (int e = 0; e < 32; e += 16) {
@@ -530,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int u = 0; u < 8; ++u)
                 b[u] = ptx::pack_bf16x2(__uint_as_float(o[e + 2 * u]), __uint_as_float(o[e + 2 * u + 1]));
-              const int col = c0 + cc + e;
+              const int col = cc + e;
               if (ta.out_v8 && col + 16 <= a.D) {
                 ptx::st_global_v8(dst + col, b);
               } else {
@@ -540,20 +573,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if (row_ok && (PAIR || half == 0)) {
+        if (row_ok && !(both && half == 1)) {
           if (pc.slot >= 0) a.part_ml[part] = make_float2(m, l);
           else if (a.lse)
             a.lse[(long long)head * a.total_q + token] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
         }
       }
-      if (!PAIR) {
+      if (both) {
         // neither half's next PV may overwrite an accumulator that the other still reads
         ptx::tc_fence_before();
         ptx::mbar_arrive(ctl.bar(C::EPI));
         if (!__all_sync(0xffffffffu, ctl.wait(C::EPI, n_epi & 1u))) break;
         ptx::tc_fence_after();
+        ++n_epi;
       }
-      ++n_epi;
       if (pc.slot >= 0 && pc.shared) meta = meta_of(a, pc);
     }
     if (warp == 4 && lane == 0) a.meta[blockIdx.x] = meta;
@@ -608,26 +641,49 @@ bool paged_tc_supported(int G, int D, int P) { return D <= 128 && D % 8 == 0 && 
 // A second row tile where some request has more rows than one holds.
 static bool paired(int G, int max_q) { return max_q > kBM / G; }
 
-int paged_tc_rows(int G, int max_q) { return (kBM / G) * G * (paired(G, max_q) ? 2 : 1); }
+// Tokens of a tile of up to 128 rows.
+static int tile_tokens(int G, int max_q) { return max_q < kBM / G ? max_q : kBM / G; }
+
+int paged_tc_rows(int G, int max_q) { return tile_tokens(G, max_q) * G * (paired(G, max_q) ? 2 : 1); }
 
 cudaError_t launch_paged_tc(const PagedArgs& a, int grid, cudaStream_t stream) {
   TcPagedArgs ta;
   ta.a = a;
-  ta.tokens = kBM / a.G;
+  ta.tokens = tile_tokens(a.G, a.max_q);
   ta.box = gcd(a.P, kBN);
+  ta.dual = ta.box == 8 && a.D == 128;
+  ta.panel = ta.dual ? 1024 : kPanel;
+  ta.group = ta.dual ? 2048 : 1024;
+  const bool pair = paired(a.G, a.max_q);
+  ta.q_bufs = !pair && ta.tokens * a.G <= kBM / 2 ? 2 : 1;
   ta.out_v8 = ((uintptr_t)a.out & 31u) == 0 && a.D % 16 == 0;
+  typedef unsigned long long u64;
   CUtensorMap mq, mk, mv;
-  const unsigned long long dq[3] = {(unsigned long long)a.D, (unsigned long long)a.Hq, (unsigned long long)a.total_q};
-  const unsigned long long sq[2] = {2ull * a.D, 2ull * a.D * a.Hq};
+  const u64 dq[3] = {(u64)a.D, (u64)a.Hq, (u64)a.total_q};
+  const u64 sq[2] = {2ull * a.D, 2ull * a.D * a.Hq};
   const unsigned bq[3] = {64, (unsigned)a.G, (unsigned)ta.tokens};
   if (!make_map_3d_box(&mq, a.q, dq, sq, bq)) return cudaErrorInvalidValue;
-  const unsigned long long dk[4] = {(unsigned long long)a.D, (unsigned long long)a.Hkv, (unsigned long long)a.P,
-                                    (unsigned long long)a.num_pages};
-  const unsigned long long sk[3] = {2ull * a.D, 2ull * a.D * a.Hkv, 2ull * (unsigned long long)a.kps};
-  const unsigned long long sv[3] = {2ull * a.D, 2ull * a.D * a.Hkv, 2ull * (unsigned long long)a.vps};
-  const unsigned bk[4] = {64, 1, (unsigned)ta.box, 1};
-  if (!make_map_4d_box(&mk, a.kc, dk, sk, bk) || !make_map_4d_box(&mv, a.vc, dk, sv, bk)) return cudaErrorInvalidValue;
-  const bool pair = paired(a.G, a.max_q);
+  // A row of one head is 2 D bytes among the other heads' rows: L2 is not to fetch
+  // beyond it, since the neighbours' turn is another CTA's (rows of 128 bytes fetched
+  // in 256 took 369 us for the block step with D = 64).
+  const int l2 = 2 * a.D % 256 == 0 ? 256 : 2 * a.D % 128 == 0 ? 128 : 64;
+  const u64 head = 2ull * a.D, token = head * a.Hkv;
+  bool ok = true;
+  for (int v = 0; v < 2; ++v) {
+    CUtensorMap* m = v ? &mv : &mk;
+    const void* base = v ? a.vc : a.kc;
+    const u64 page = 2ull * (u64)(v ? a.vps : a.kps);
+    if (ta.dual) {
+      const u64 d[5] = {64, (u64)a.P, 2, (u64)a.Hkv, (u64)a.num_pages}, s[4] = {token, 128, head, page};
+      const unsigned b[5] = {64, 8, 2, 1, 1};
+      ok = ok && make_map_box(m, base, 5, d, s, b, l2);
+    } else {
+      const u64 d[4] = {(u64)a.D, (u64)a.Hkv, (u64)a.P, (u64)a.num_pages}, s[3] = {head, token, page};
+      const unsigned b[4] = {64, 1, (unsigned)ta.box, 1};
+      ok = ok && make_map_box(m, base, 4, d, s, b, l2);
+    }
+  }
+  if (!ok) return cudaErrorInvalidValue;
   if (a.D <= 64) return pair ? run_tc<1, true>(ta, grid, mq, mk, mv, stream) : run_tc<1, false>(ta, grid, mq, mk, mv, stream);
   return pair ? run_tc<2, true>(ta, grid, mq, mk, mv, stream) : run_tc<2, false>(ta, grid, mq, mk, mv, stream);
 }

@@ -717,17 +717,24 @@ bool make_map_3d_box(CUtensorMap* m, const void* base, const unsigned long long 
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool make_map_4d_box(CUtensorMap* m, const void* base, const unsigned long long dims[4],
-                     const unsigned long long strides_bytes[3], const unsigned box[4]) {
+bool make_map_box(CUtensorMap* m, const void* base, int rank, const unsigned long long* dims,
+                  const unsigned long long* strides_bytes, const unsigned* box, int l2_bytes) {
   EncodeTiledFn enc = encode_fn();
-  if (!enc) return false;
-  const cuuint64_t d[4] = {dims[0], dims[1], dims[2], dims[3]};
-  const cuuint64_t st[3] = {strides_bytes[0], strides_bytes[1], strides_bytes[2]};
-  const cuuint32_t bx[4] = {box[0], box[1], box[2], box[3]};
-  const cuuint32_t es[4] = {1, 1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), d, st, bx, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  if (!enc || rank < 2 || rank > 5) return false;
+  cuuint64_t d[5], st[4];
+  cuuint32_t bx[5], es[5];
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    bx[i] = box[i];
+    es[i] = 1;
+    if (i + 1 < rank) st[i] = strides_bytes[i];
+  }
+  const CUtensorMapL2promotion l2 = l2_bytes == 256   ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                                    : l2_bytes == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                                                      : CU_TENSOR_MAP_L2_PROMOTION_L2_64B;
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base), d, st, bx, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, l2, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
 }
 
 bool make_map_2d(CUtensorMap* m, const void* base, long long rows, int width, int box_rows) {

@@ -57,9 +57,9 @@ bool make_map_2d(CUtensorMap* m, const void* base, long long rows, int width, in
 // dims 1 and 2, box extents (box[0] * 2 bytes = 128).
 bool make_map_3d_box(CUtensorMap* m, const void* base, const unsigned long long dims[3],
                      const unsigned long long strides_bytes[2], const unsigned box[3]);
-// The same with four dimensions (three strides).
-bool make_map_4d_box(CUtensorMap* m, const void* base, const unsigned long long dims[4],
-                     const unsigned long long strides_bytes[3], const unsigned box[4]);
+// Any rank from 2 to 5, with the bytes L2 fetches at once (64, 128 or 256).
+bool make_map_box(CUtensorMap* m, const void* base, int rank, const unsigned long long* dims,
+                  const unsigned long long* strides_bytes, const unsigned* box, int l2_bytes);
 int sm_count();
 
 bool tc_supported(int dn, int dr, int dv);

@@ -260,6 +260,8 @@ ATTN = [
     ([333], [33], 48, 2, 2, 256),
     ([150], [20], 40, 16, 1, 40),
     ([64] * 37, [1] * 37, 16, 4, 1, 128),
+    ([333, 40], [3, 1], 8, 8, 2, 128),                 # pages of 8: both halves of the components in one box
+    ([129, 77], [20, 6], 24, 4, 1, 128),
     ([40] * 10, [2] * 10, 8, 130, 1, 64),              # more heads in a group than a tile has rows
     ([257, 1, 129], [16, 1, 7], 128, 64, 8, 128),
 ]
@@ -273,13 +275,14 @@ def test_attn_paged(dfl, kv, n, P, Hq, Hkv, D, dtype, causal):
 
 
 @pytest.mark.parametrize("dtype,n,Hq,Hkv,D,P", [("bf16", 1, 8, 4, 128, 64), ("bf16", 3, 8, 4, 64, 16),
+                                                ("bf16", 2, 4, 2, 128, 8), ("bf16", 16, 16, 2, 128, 32),
                                                 ("bf16", 40, 16, 4, 128, 16), ("bf16", 70, 4, 2, 64, 48),
                                                 ("fp32", 1, 4, 4, 64, 16)])
 def test_attn_paged_many_row_tiles_a_cta(dfl, dtype, n, Hq, Hkv, D, P):
     """More row tiles than CTAs: a CTA goes through several, with odd and even numbers of key tiles."""
     rng = np.random.default_rng(n + D)
-    R = 260 if n < 10 else 40
-    kv = [int(x) for x in n + rng.integers(0, 700 if n < 10 else 500, R)]
+    R = 260 if n < 20 else 40
+    kv = [int(x) for x in n + rng.integers(0, 700 if n < 20 else 500, R)]
     _check_attn(dfl, rng, kv, [n] * R, P, Hq, Hkv, D, dtype, True)
 
 
