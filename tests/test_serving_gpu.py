@@ -360,6 +360,28 @@ def test_attn_paged_without_a_page(dfl):
                           atol=2.0 ** -20)
 
 
+@pytest.mark.parametrize("n,stall_cta", [(1, 0), (1, 3), (70, 0)])
+def test_attn_paged_wait_runs_out_then_context_is_usable(dfl, n, stall_cta):
+    """One CTA's producer leaves its first key tiles unloaded under a 20 ms budget: the call ends, the error word
+    says so, and the next call on the same stream is right.  Both forms of the tensor-core kernel."""
+    rng = np.random.default_rng(21)
+    kv, P, Hq, Hkv, D = [20000, 9000 + n], 64, 8, 2, 128  # three units of work a CTA: each has a key tile
+    kc, vc, table, off, T = _batch(rng, kv, [n, n], P, Hkv, D, "bf16")
+    q = _rand(rng, (T, Hq, D), "bf16")
+    args = (q, kc, vc, _i32(table), _i32(kv), _i32(off), n)
+    dfl.dflash_test_inject_stall(20_000_000, stall_cta)
+    try:
+        dfl.dflash_attn_paged(*args)
+        assert dfl.dflash_last_device_error() == 8
+    finally:
+        dfl.dflash_test_inject_stall(0, -1)
+    out = dfl.dflash_attn_paged(*args)
+    assert dfl.dflash_last_device_error() == 0
+    want, _, size, score = osv.attn_paged(_np(q)[:off[-1]], _np(kc), _np(vc), table, kv, off, True)
+    _within(out[:off[-1]], want, size * (2.0 ** -8 + 2 * (D + 8) * U * score[..., None] + 20100 * U) +
+            2.0 ** -8 * np.abs(want))
+
+
 # ------------------------------------------------------------------ append
 # kv lengths (new tokens counted), new tokens, P, Hq, Hkv, D, rot, interleaved, weights
 APPEND = [
