@@ -15,6 +15,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <initializer_list>
+#include <optional>
 #include <string>
 
 #include "dflash_attn.h"
@@ -67,10 +68,10 @@ std::string list(at::IntArrayRef s) {
   return r + "]";
 }
 
-bool on(const at::Tensor& t, int dev) { return t.is_cuda() && t.get_device() == dev; }
+bool lies_on(const at::Tensor& t, int dev) { return t.is_cuda() && t.get_device() == dev; }
 
 void common(const at::Tensor& t, const char* name, int dev, at::ScalarType type) {
-  if (!on(t, dev))
+  if (!lies_on(t, dev))
     refuse(std::string(name) + " must be a CUDA tensor" + (dev >= 0 ? " on device " + std::to_string(dev) : ""));
   if (t.scalar_type() != type)
     throw Refusal{PyExc_TypeError, std::string(name) + " must be " + at::toString(type) + ", got " + at::toString(t.scalar_type())};
@@ -127,28 +128,36 @@ at::Tensor fresh(const at::Tensor& like, Shape shape, at::ScalarType type) {
   return at::empty(at::IntArrayRef(shape), like.options().dtype(type));
 }
 
-// The stream's handle: of a stream object, a plain handle, or the device's current one.
-dflash_stream_t handle(PyObject* stream, int dev) {
-  if (stream == Py_None) return (dflash_stream_t)c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream();
-  PyObject* h = PyObject_GetAttrString(stream, "cuda_stream");
-  if (!h) {
-    PyErr_Clear();
-    Py_INCREF(stream);
-    h = stream;
+// Makes the inputs' device and the call's stream (a stream object, a plain handle, or
+// None: the device's current one) current, before anything is allocated, so that
+// workspaces and results come from the memory of the stream that uses them.
+class On {
+ public:
+  On(int dev, PyObject* stream) {
+    if (c10::cuda::current_device() != dev) device_.emplace((c10::DeviceIndex)dev);
+    if (stream == Py_None) {
+      handle_ = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream();
+      return;
+    }
+    PyObject* h = PyObject_GetAttrString(stream, "cuda_stream");
+    if (!h) {
+      PyErr_Clear();
+      h = Py_NewRef(stream);
+    }
+    void* p = PyLong_AsVoidPtr(h);
+    Py_DECREF(h);
+    if (!p && PyErr_Occurred()) throw PythonError{};
+    handle_ = (cudaStream_t)p;
+    stream_.emplace(p ? c10::cuda::getStreamFromExternal(handle_, (c10::DeviceIndex)dev)
+                      : c10::cuda::getDefaultCUDAStream((c10::DeviceIndex)dev));
   }
-  void* p = PyLong_AsVoidPtr(h);
-  Py_DECREF(h);
-  if (!p && PyErr_Occurred()) throw PythonError{};
-  return (dflash_stream_t)p;
-}
+  dflash_stream_t stream() const { return (dflash_stream_t)handle_; }
 
-// f(stream handle) with device `dev` current.
-template <typename F>
-dflash_status_t launch(int dev, PyObject* stream, F f) {
-  if (c10::cuda::current_device() == dev) return f(handle(stream, dev));
-  c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
-  return f(handle(stream, dev));
-}
+ private:
+  std::optional<c10::cuda::CUDAGuard> device_;
+  std::optional<c10::cuda::CUDAStreamGuard> stream_;
+  cudaStream_t handle_;
+};
 
 struct Workspace {
   at::Tensor own;
@@ -157,7 +166,7 @@ struct Workspace {
 Workspace workspace(PyObject* given, size_t bytes, const at::Tensor& like) {
   Workspace w;
   if (const at::Tensor* t = tensor(given, "workspace")) {
-    if (!on(*t, like.get_device()) || !t->is_contiguous()) refuse("workspace must be a contiguous CUDA tensor on the inputs' device");
+    if (!lies_on(*t, like.get_device()) || !t->is_contiguous()) refuse("workspace must be a contiguous CUDA tensor on the inputs' device");
     if (t->nbytes() < bytes) refuse("workspace too small: need " + std::to_string(bytes) + " bytes");
     w.ptr = t->data_ptr();
   } else {
@@ -255,6 +264,7 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Rope r = rope(a[0], a[1], a[2], a[3], a[6], a[7]);
     const void* wq = flat(tensor(a[4], "q_norm"), "q_norm", r.dev, r.type, {r.D});
     const void* wk = flat(tensor(a[5], "k_norm"), "k_norm", r.dev, r.type, {r.D});
+    const On on(r.dev, a[10]);
     at::Tensor qo, ko;
     void *qop = nullptr, *kop = nullptr;
     if (r.q) {
@@ -265,9 +275,8 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
       ko = given_or(a[9], "k_out", *r.k, {r.T, r.Hk, r.D}, r.type);
       kop = flat(&ko, "k_out", r.dev, r.type, {r.T, r.Hk, r.D});
     }
-    const dflash_status_t st = launch(r.dev, a[10], [&](dflash_stream_t s) {
-      return dflash_qk_norm_rope(&r.d, code_of(r.type), r.qp, r.kp, wq, wk, r.cs, r.pos, qop, kop, s);
-    });
+    const dflash_status_t st = dflash_qk_norm_rope(&r.d, code_of(r.type), r.qp, r.kp, wq, wk, r.cs, r.pos, qop, kop,
+                                                   on.stream());
     return st ? status(st) : tuple(qo, ko);
   });
 }
@@ -278,6 +287,7 @@ PyObject* qk_norm_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Rope r = rope(a[0], a[1], a[2], a[3], a[8], a[9]);
     const void* wq = flat(tensor(a[6], "q_norm"), "q_norm", r.dev, r.type, {r.D});
     const void* wk = flat(tensor(a[7], "k_norm"), "k_norm", r.dev, r.type, {r.D});
+    const On on(r.dev, a[15]);
     const void *gq = nullptr, *gk = nullptr;
     at::Tensor dq, dk, dwq, dwk;
     void *dqp = nullptr, *dkp = nullptr, *dwqp = nullptr, *dwkp = nullptr;
@@ -301,10 +311,9 @@ PyObject* qk_norm_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     const size_t bytes = dflash_qk_norm_rope_workspace_size(&r.d);
     const Workspace ws = workspace(a[14], bytes, *r.one);
-    const dflash_status_t st = launch(r.dev, a[15], [&](dflash_stream_t s) {
-      return dflash_qk_norm_rope_backward(&r.d, code_of(r.type), r.qp, r.kp, wq, wk, r.cs, r.pos, gq, gk, dqp, dkp,
-                                          (float*)dwqp, (float*)dwkp, ws.ptr, bytes, s);
-    });
+    const dflash_status_t st =
+        dflash_qk_norm_rope_backward(&r.d, code_of(r.type), r.qp, r.kp, wq, wk, r.cs, r.pos, gq, gk, dqp, dkp,
+                                     (float*)dwqp, (float*)dwkp, ws.ptr, bytes, on.stream());
     return st ? status(st) : tuple(dq, dk, dwq, dwk);
   });
 }
@@ -354,6 +363,7 @@ PyObject* cache_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     int64_t vs = 0;
     const void* kp = tokens(k, "k", dev, type, T, p.Hk, p.D, &d.k_stride);
     const void* vp = tokens(v, "v", dev, type, T, p.Hk, p.D, &vs);
+    const On on(dev, a[14]);
     const at::Tensor* q = tensor(a[7], "q");
     int64_t Hq = p.Hk;
     const void* qp = nullptr;
@@ -379,9 +389,8 @@ PyObject* cache_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     d.interleaved = truth(a[12]);
     p.d.H_q = narrow(Hq);
     p.d.total_q = narrow(T);
-    const dflash_status_t st = launch(dev, a[14], [&](dflash_stream_t s) {
-      return dflash_cache_append(&p.d, &d, code, qp, kp, vp, vs, wq, wk, cs, p.table, p.lens, p.off, qop, p.kc, p.vc, s);
-    });
+    const dflash_status_t st = dflash_cache_append(&p.d, &d, code, qp, kp, vp, vs, wq, wk, cs, p.table, p.lens, p.off,
+                                                   qop, p.kc, p.vc, on.stream());
     return st ? status(st) : wrap(qo);
   });
 }
@@ -397,6 +406,7 @@ PyObject* attn_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Paged p = paged(a[1], a[2], a[3], a[4], a[5], dev, type);
     const int64_t T = q.size(0), Hq = q.size(1);
     const void* qp = flat(&q, "q", dev, type, {T, Hq, p.D});
+    const On on(dev, a[12]);
     const at::Tensor out = given_or(a[8], "out", q, {T, Hq, p.D}, type);
     void* op = flat(&out, "out", dev, type, {T, Hq, p.D});
     float* lse = (float*)flat(tensor(a[9], "lse"), "lse", dev, at::kFloat, {Hq, T});
@@ -407,10 +417,8 @@ PyObject* attn_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const float scale = a[10] == Py_None ? 0.f : real(a[10]);
     const size_t bytes = dflash_attn_paged_workspace_size(&p.d, code);
     const Workspace ws = workspace(a[11], bytes, q);
-    const dflash_status_t st = launch(dev, a[12], [&](dflash_stream_t s) {
-      return dflash_attn_paged(&p.d, code, qp, p.kc, p.vc, p.table, p.lens, p.off, causal, scale, op, lse, ws.ptr,
-                               bytes, s);
-    });
+    const dflash_status_t st = dflash_attn_paged(&p.d, code, qp, p.kc, p.vc, p.table, p.lens, p.off, causal, scale, op,
+                                                 lse, ws.ptr, bytes, on.stream());
     return st ? status(st) : wrap(out);
   });
 }
@@ -449,13 +457,13 @@ PyObject* verify(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int32_t* fp = (const int32_t*)flat(&off, "draft_offsets", dev, at::kInt);
     const float* u = (const float*)flat(&required(a[4], "accept_u"), "accept_u", dev, at::kFloat, {T});
     const float* su = (const float*)flat(&required(a[5], "sample_u"), "sample_u", dev, at::kFloat, {R});
+    const On on(dev, a[9]);
     const at::Tensor out = given_or(a[7], "out_tokens", p, {R, N}, at::kInt);
     const at::Tensor acc = given_or(a[8], "num_accepted", p, {R}, at::kInt);
     int32_t* op = (int32_t*)flat(&out, "out_tokens", dev, at::kInt, {R, N});
     int32_t* ap = (int32_t*)flat(&acc, "num_accepted", dev, at::kInt, {R});
-    const dflash_status_t st = launch(dev, a[9], [&](dflash_stream_t s) {
-      return dflash_verify(&d, (const float*)p.data_ptr(), (const float*)qp, tp, fp, u, su, op, ap, s);
-    });
+    const dflash_status_t st = dflash_verify(&d, (const float*)p.data_ptr(), (const float*)qp, tp, fp, u, su, op, ap,
+                                             on.stream());
     return st ? status(st) : tuple(out, acc);
   });
 }

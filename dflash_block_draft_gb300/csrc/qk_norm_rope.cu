@@ -166,7 +166,7 @@ __device__ __forceinline__ Place place_tokens(const RopeArgs& a, long long t0, i
   int r = lo;
   for (int i = 0; i < n; ++i) {
     const int c = __popc(__ballot_sync(0xffffffffu, next <= t0 + i));
-    if (lane == i) r = lo + c;
+    if (lane == i) r = min(lo + c, a.R - 1);
   }
   if (lane < n && t < a.T && t < end) {
     if (r - lo == 32) {

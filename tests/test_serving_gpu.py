@@ -287,6 +287,14 @@ def test_attn_paged_many_row_tiles_a_cta(dfl, dtype, n, Hq, Hkv, D, P):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_attn_paged_more_requests_than_threads(dfl, dtype):
+    rng = np.random.default_rng(17)
+    n = [int(x) for x in rng.integers(0, 3, 1000)]
+    kv = [int(x) if a else 0 for a, x in zip(n, rng.integers(1, 40, 1000))]
+    _check_attn(dfl, rng, kv, n, 16, 2, 1, 64, dtype, True)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_attn_paged_halves_of_one_cache_scale_and_loose_bound(dfl, dtype):
     _check_attn(dfl, np.random.default_rng(5), [100, 333], [16, 3], 16, 8, 2, 128, dtype, True, layout="halves",
                 scale=0.31)
@@ -392,6 +400,8 @@ APPEND = [
     ([50, 20], [7, 20], 64, 4, 4, 64, 0, False, False),
     ([17], [9], 8, 2, 1, 24, 6, True, True),
     ([400, 380], [390, 300], 64, 16, 4, 128, 128, False, True),
+    ([20, 3] + [0] * 45 + [9, 2, 70], [3, 2] + [0] * 45 + [9, 1, 40], 16, 4, 2, 64, 64, False, True),  # many empty ones
+    ([1 + i % 7 for i in range(90)], [1 - i % 2 for i in range(90)], 4, 2, 1, 128, 128, True, True),
 ]
 
 
@@ -657,6 +667,60 @@ def test_two_streams_at_once(dfl):
     dfl.dflash_attn_paged(explicit.qo.copy_(explicit.q), explicit.kc.nan_to_num_(), explicit.vc.nan_to_num_(),
                           *explicit.i, explicit.n, causal=False, out=explicit.out, stream=torch.cuda.current_stream())
     torch.cuda.synchronize()
+
+
+def test_a_call_on_a_given_stream_takes_its_memory_from_it(dfl):
+    """Workspace and results of a call on another stream than the current one belong to that stream: what the
+    current stream allocates meanwhile does not overlap them."""
+    s = _Step(dfl, 31, R=6)
+    side = torch.cuda.Stream()
+    s.run()
+    torch.cuda.synchronize()
+    want = s.out.clone()
+    for form in (side, side.cuda_stream):
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)  # the call waits in its stream while this one goes on
+        out = dfl.dflash_attn_paged(s.qo, s.kc, s.vc, *s.i, s.n, causal=False, stream=form)
+        junk = [torch.full((1 << 20,), float("nan"), device="cuda") for _ in range(30)]
+        side.synchronize()
+        assert torch.equal(out, want)
+        del junk
+    torch.cuda.synchronize()
+
+
+def test_first_calls_of_a_process_can_be_captured():
+    """A fresh process whose first call of each operator is made while its stream is captured."""
+    code = """
+import torch, dflash_block_draft_gb300 as dfl
+dfl.load_library()
+i32 = dict(dtype=torch.int32, device="cuda")
+q, k = torch.randn(2, 4, 64, device="cuda").bfloat16(), torch.randn(2, 2, 64, device="cuda").bfloat16()
+kc = torch.zeros(4, 16, 2, 64, device="cuda", dtype=torch.bfloat16); vc = kc.clone()
+cs = torch.cat([torch.ones(32, 32), torch.zeros(32, 32)], 1).cuda()
+tbl, lens, off, pos = (torch.tensor(x, **i32) for x in ([[0, 1]], [20], [0, 2], [1, 2]))
+p = torch.softmax(torch.randn(3, 100, device="cuda"), 1); tok = torch.zeros(2, **i32); u = torch.rand(2, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    a = dfl.dflash_qk_norm_rope(q, k, pos, cs)
+    b = dfl.dflash_qk_norm_rope_backward(q, k, pos, cs, q, k, q_norm=q[0, 0].contiguous(), k_norm=k[0, 0].contiguous())
+    dfl.dflash_cache_append(k, k, kc, vc, tbl, lens, off, cos_sin=cs)
+    o = dfl.dflash_attn_paged(q, kc, vc, tbl, lens, off, 2)
+    o2 = dfl.dflash_attn_paged(q.float(), kc.float(), vc.float(), tbl, lens, off, 2)
+    t = dfl.dflash_verify(p, None, tok, off, u, u[:1].contiguous(), 2)
+g.replay()
+torch.cuda.synchronize()
+assert dfl.dflash_last_device_error() == 0 and torch.equal(vc[1, 2:4], k) and bool((t[1] >= 0).all())
+assert torch.isfinite(o).all() and torch.allclose(o.float(), o2, atol=0.02)
+print("captured")
+"""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
 
 
 def test_offsets_beyond_32_bits(dfl):
