@@ -8,7 +8,7 @@
 // running maximum m rises.
 //
 // A CTA holds a row tile's queries in shared memory and walks its key tiles of 64
-// positions (32 where rows are longer than 256 bytes), which arrive by 16-byte asynchronous copies two tiles deep; the rows'
+// positions (fp32 up to D = 64) or 32, which arrive by 16-byte asynchronous copies two tiles deep; the rows'
 // offsets (page table and page row) are worked out one tile ahead of the copies.
 // Each thread has 4 rows of the scores and of the output in registers, and all
 // threads of a row lie in one warp, so that the softmax needs shuffles only and a
@@ -55,7 +55,9 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
 
 template <typename T, int BM, int DMAX>
 struct Simt {
-  static constexpr int BN = DMAX * sizeof(T) <= 256 ? 64 : 32;  // two stages of K and V for several CTAs an SM
+  // positions of a key tile: two stages of K and V for two CTAs an SM (bf16 with D = 128
+  // and 64-row tiles: 160 us with 32, 172 with 64)
+  static constexpr int BN = sizeof(T) == 4 && DMAX <= 64 ? 64 : 32;
   static constexpr int kThreads = BM == 16 ? 128 : 256;
   static constexpr int kVec = 16 / sizeof(T);
   static constexpr int kStride = DMAX + kVec;  // elements from row to row of K and V
@@ -72,7 +74,7 @@ struct Simt {
 };
 
 template <typename T, int BM, int DMAX>
-__global__ void __launch_bounds__(Simt<T, BM, DMAX>::kThreads)
+__global__ void __launch_bounds__(Simt<T, BM, DMAX>::kThreads, BM == 64 && DMAX <= 128 ? 2 : 1)
     paged_simt_kernel(const __grid_constant__ PagedArgs a) {
   using C = Simt<T, BM, DMAX>;
   constexpr int BN = C::BN, kThreads = C::kThreads, VEC = C::kVec;
