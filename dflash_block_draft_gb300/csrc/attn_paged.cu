@@ -167,10 +167,11 @@ __global__ void __launch_bounds__(Simt<T, BM, DMAX>::kThreads, BM == 64 && DMAX 
       if (!idle) {
         // scores: rows 4 ty .., columns tx + TX j
         float x[4][CT];
+        float2 x2[4][CT];  // sums over the even and the odd components, for the packed multiply-adds
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int j = 0; j < CT; ++j) x[i][j] = 0.f;
+          for (int j = 0; j < CT; ++j) x2[i][j] = make_float2(0.f, 0.f);
 #pragma unroll 4
         for (int d = 0; d < D; d += 4) {
           float4 kk[CT];
@@ -181,9 +182,14 @@ __global__ void __launch_bounds__(Simt<T, BM, DMAX>::kThreads, BM == 64 && DMAX 
             const float4 qq = load4(s.q + (4 * ty + i) * C::kQStride + d);
 #pragma unroll
             for (int j = 0; j < CT; ++j)
-              x[i][j] = fmaf(qq.x, kk[j].x, fmaf(qq.y, kk[j].y, fmaf(qq.z, kk[j].z, fmaf(qq.w, kk[j].w, x[i][j]))));
+              x2[i][j] = __ffma2_rn(make_float2(qq.x, qq.y), make_float2(kk[j].x, kk[j].y),
+                                    __ffma2_rn(make_float2(qq.z, qq.w), make_float2(kk[j].z, kk[j].w), x2[i][j]));
           }
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < CT; ++j) x[i][j] = x2[i][j].x + x2[i][j].y;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           float mx = -INFINITY;
