@@ -91,7 +91,8 @@ __global__ void __launch_bounds__(Simt<T, BM, DMAX>::kThreads, BM == 64 && DMAX 
   // copies: 16-byte piece tid % kPer of rows tid / kPer, + kRows, ...
   constexpr int kPer = DMAX / VEC, kRows = kThreads / kPer;
   static_assert(kRows >= 1 && BN % kRows == 0, "copy layout");
-  find_range<BN, kThreads>(a, &s.range, s.scratch);
+  find_range<BN, kThreads>(a, tid, &s.range, s.scratch, [] { __syncthreads(); });
+  __syncthreads();
   Walker<BN> walk(a, s.range);
   Piece pc;
   Meta meta = no_meta();
@@ -287,7 +288,7 @@ __global__ void __launch_bounds__(Simt<T, BM, DMAX>::kThreads, BM == 64 && DMAX 
         if (tx == 0) a.part_ml[at] = make_float2(m[i], l[i]);
       }
     }
-    if (pc.slot >= 0 && pc.shared) meta = meta_of(a, pc);
+    if (begins_cut(pc)) meta = meta_of(a, s.range, pc);
   }
   if (tid == 0) a.meta[blockIdx.x] = meta;
 }

@@ -100,7 +100,7 @@ struct Cfg {
   static constexpr uint32_t kOffAbort = kOffTmem + 4;
   static constexpr uint32_t kOffRange = (kOffAbort + 4 + 7) / 8 * 8;
   static constexpr uint32_t kOffScratch = kOffRange + (sizeof(Range) + 7) / 8 * 8;
-  static constexpr uint32_t kOffMl = kOffScratch + 8 * (kThreads / 32);
+  static constexpr uint32_t kOffMl = kOffScratch + 8 * 8;
   static constexpr uint32_t kSmem = kOffMl + (PAIR ? 0 : 2 * kBM * 8);
   static_assert(kSmem <= 232448, "shared memory budget");
 };
@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Range& range = *reinterpret_cast<Range*>(smem + C::kOffRange);
   float2* ml = reinterpret_cast<float2*>(smem + C::kOffMl);
 
-  if (threadIdx.x == kThreads - 1) {  // the first threads look at the requests meanwhile
+  if (threadIdx.x == 0) {
     const uint32_t users = PAIR ? 2 : 1;  // MMA issuers that read a ring slot
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(ctl.bar(C::Q_FULL + b), 1);
@@ -205,7 +205,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tmem_alloc(ptx::smem_u32(tmem_slot), kTmemCols);
     ptx::tmem_relinquish();
   }
-  find_range<kBN, kThreads>(a, &range, reinterpret_cast<long long*>(smem + C::kOffScratch));
+  // the softmax warps look at the requests, while the others set the barriers and TMEM up
+  if (warp >= 4)
+    find_range<kBN, 256>(a, threadIdx.x - 128, &range, reinterpret_cast<long long*>(smem + C::kOffScratch),
+                         [] { ptx::named_barrier(1, 256); });
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
@@ -589,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tc_fence_after();
         ++n_epi;
       }
-      if (pc.slot >= 0 && pc.shared) meta = meta_of(a, pc);
+      if (begins_cut(pc)) meta = meta_of(a, range, pc);
     }
     if (warp == 4 && lane == 0) a.meta[blockIdx.x] = meta;
   }

@@ -89,31 +89,106 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
   return (unsigned long long)(a | b) >> 32 ? a / b : (long long)((unsigned)a / (unsigned)b);
 }
 
-// A CTA's range, found once by the whole block and kept in shared memory, with the
-// row tile that holds its first tile.
-struct Range {
-  long long total;    // T
-  long long t0, t1;   // this CTA's part
-  long long share;    // T / G
-  int more;           // T mod G: CTAs with one more
-  int r, h, rt;       // first row tile
-  long long at;       // where it begins
+// A CTA's share of one row tile: key tiles [kt0, kt1) of nt.
+struct Piece {
+  int r, h, rt;
   Req q;
+  int kt0, kt1, nt;
+  int slot;            // partial slot, -1: the row tile is whole
+  long long end;       // where the row tile ends
 };
 
-// Whole block (kThreads threads): every thread adds up a strip of requests, a scan
-// over the strips gives T and finds the strip, and its thread the row tile, of t0.
-template <int BN, int kThreads>
-__device__ __forceinline__ void find_range(const PagedArgs& a, Range* out, long long* scratch /* [kThreads/32 + 1] */) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+// A CTA's range, found once by a block's threads and kept in shared memory: its part
+// of the line and its first piece.
+struct Range {
+  long long t1;       // end of its part
+  long long share;    // T / G
+  int more;           // T mod G: CTAs with one more
+  int any;            // whether there is a piece
+  long long t;        // place behind the first piece
+  Piece first;
+};
+
+// Walks the pieces of a CTA's range.  Every role of a kernel keeps its own; the
+// first piece is worked out once (the code is cold then, and it cost a microsecond).
+template <int BN>
+struct Walker {
+  const PagedArgs& a;
+  long long t, t1;  // next place, end
+  long long at;     // where the current row tile begins
+  Req q;
+  int r, h, rt;
+  int state;        // 0: the current row tile is next, 1: it is done with, 2: the first piece lies in `first`
+  const Piece* first;
+
+  __device__ __forceinline__ Walker(const PagedArgs& a_, const Range& rg) : a(a_) {
+    t = rg.t;
+    t1 = rg.t1;
+    state = rg.any ? 2 : 0;
+    if (!rg.any) t = t1;
+    first = &rg.first;
+  }
+  __device__ __forceinline__ Walker(const PagedArgs& a_, long long t_, long long t1_, long long at_, const Req& q_, int r_,
+                                    int h_, int rt_)
+      : a(a_), t(t_), t1(t1_), at(at_), q(q_), r(r_), h(h_), rt(rt_), state(0), first(nullptr) {}
+
+  __device__ __forceinline__ bool next(Piece* p) {
+    if (state == 2) {
+      *p = *first;
+      r = p->r;
+      h = p->h;
+      rt = p->rt;
+      q = p->q;
+      at = p->end;
+      state = 1;
+      return true;
+    }
+    while (t < t1) {
+      if (state == 1) {  // the next row tile, head or request with work
+        if (++rt == q.nrt) {
+          rt = 0;
+          if (++h == a.Hkv) {
+            h = 0;
+            do q = load_request(a, ++r, false);
+            while (q.nrt == 0 && r + 1 < a.R);
+          }
+        }
+      }
+      p->r = r;
+      p->h = h;
+      p->rt = rt;
+      p->q = q;
+      p->nt = key_tiles<BN>(a, q, rt);
+      p->end = at + kSetup + p->nt;
+      const long long end = min(p->end, t1);
+      p->kt0 = max(0, (int)(t - at) - kSetup);
+      p->kt1 = max(0, (int)(end - at) - kSetup);
+      const int me = blockIdx.x;
+      p->slot = p->kt0 > 0 ? 2 * me : p->kt1 < p->nt ? 2 * me + 1 : -1;
+      t = end;
+      at = p->end;
+      state = 1;
+      if (p->kt1 > p->kt0) return true;  // else the range ends in the row tile's set-up
+    }
+    return false;
+  }
+};
+
+// kThreads threads, numbered tid: every thread adds up a strip of requests, a scan over
+// the strips gives T and finds the strip, and its thread the first piece, of the CTA's
+// part.  sync() is a barrier among them; the result is there after one more.
+template <int BN, int kThreads, typename Sync>
+__device__ __forceinline__ void find_range(const PagedArgs& a, int tid, Range* out,
+                                           long long* scratch /* [kThreads/32] */, Sync sync) {
+  const int lane = tid & 31, warp = tid >> 5;
   const int strip = (a.R + kThreads - 1) / kThreads;
   const int lo = min(a.R, tid * strip), hi = min(a.R, lo + strip);
-  long long mine = 0, last = 0;
+  long long mine = 0, per = 0;
   Req q;
   for (int r = lo; r < hi; ++r) {
     q = load_request(a, r, blockIdx.x == 0);
-    last = a.Hkv * length_of<BN>(a, q, q.nrt);
-    mine += last;
+    per = length_of<BN>(a, q, q.nrt);  // of one head
+    mine += a.Hkv * per;
   }
   long long c = mine;
 #pragma unroll
@@ -122,7 +197,8 @@ __device__ __forceinline__ void find_range(const PagedArgs& a, Range* out, long 
     if (lane >= o) c += v;
   }
   if (lane == 31) scratch[warp] = c;
-  __syncthreads();
+  if (tid == 0) out->any = 0;
+  sync();
   long long base = 0, total = 0;
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
@@ -134,12 +210,11 @@ __device__ __forceinline__ void find_range(const PagedArgs& a, Range* out, long 
   const long long share = ctas > 0 ? quotient(total, ctas) : 0;
   const int more = (int)(total - share * ctas);
   const long long t0 = me < ctas ? share * me + min(me, more) : total;
+  const long long t1 = me < ctas ? t0 + share + (me < more) : total;
   if (tid == 0) {
-    out->total = total;
+    out->t1 = t1;
     out->share = share;
     out->more = more;
-    out->t0 = t0;
-    out->t1 = me < ctas ? t0 + share + (me < more) : total;
   }
   if (before <= t0 && t0 < before + mine) {  // one thread at most
     long long s = before;
@@ -147,12 +222,11 @@ __device__ __forceinline__ void find_range(const PagedArgs& a, Range* out, long 
     if (hi - lo > 1) {
       for (r = lo; r < hi; ++r) {
         q = load_request(a, r, false);
-        last = a.Hkv * length_of<BN>(a, q, q.nrt);
-        if (t0 < s + last) break;
-        s += last;
+        per = length_of<BN>(a, q, q.nrt);
+        if (t0 < s + a.Hkv * per) break;
+        s += a.Hkv * per;
       }
     }
-    const long long per = quotient(last, a.Hkv);
     const int h = (int)quotient(t0 - s, per);
     s += h * per;
     // the last row tile that begins at or before t0
@@ -167,85 +241,21 @@ __device__ __forceinline__ void find_range(const PagedArgs& a, Range* out, long 
         n = half;
       }
     }
-    out->r = r;
-    out->h = h;
-    out->rt = x;
-    out->at = s + length_of<BN>(a, q, x);
-    out->q = q;
+    Walker<BN> walk(a, t0, t1, s + length_of<BN>(a, q, x), q, r, h, x);
+    Piece pc;
+    if (walk.next(&pc)) {
+      out->first = pc;
+      out->t = walk.t;
+      out->any = 1;
+    }
   }
-  __syncthreads();
 }
-
-// A CTA's share of one row tile: key tiles [kt0, kt1) of nt.
-struct Piece {
-  int r, h, rt;
-  Req q;
-  int kt0, kt1, nt;
-  int limit;           // positions the row tile's last token sees
-  int slot;            // partial slot, -1: the row tile is whole
-  int shared;          // CTAs that share the row tile (set where this piece begins it)
-};
 
 // CTA that holds place t of the line.
 __device__ __forceinline__ int owner_of(long long t, const Range& rg) {
   const long long wide = (rg.share + 1) * rg.more;  // parts of the CTAs with one more
   return (int)(t < wide ? quotient(t, rg.share + 1) : rg.more + quotient(t - wide, rg.share));
 }
-
-// Walks the pieces of a CTA's range.  Every role of a kernel keeps its own.
-template <int BN>
-struct Walker {
-  const PagedArgs& a;
-  const Range& rg;
-  long long t;      // next place
-  long long at;     // where the current row tile begins
-  Req q;
-  int r, h, rt;
-
-  __device__ __forceinline__ Walker(const PagedArgs& a_, const Range& rg_) : a(a_), rg(rg_) {
-    t = rg.t0;
-    at = rg.at;
-    q = rg.q;
-    r = rg.r;
-    h = rg.h;
-    rt = rg.rt;
-  }
-  __device__ __forceinline__ bool next(Piece* p) {
-    while (t < rg.t1) {
-      p->r = r;
-      p->h = h;
-      p->rt = rt;
-      p->q = q;
-      p->limit = tile_limit(a, q, rt);
-      p->nt = key_tiles<BN>(a, q, rt);
-      const long long len = kSetup + p->nt, end = min(at + len, rg.t1);
-      p->kt0 = max(0, (int)(t - at) - kSetup);
-      p->kt1 = max(0, (int)(end - at) - kSetup);
-      p->shared = 0;
-      if (p->kt0 > 0) p->slot = 2 * blockIdx.x;
-      else if (p->kt1 < p->nt) {
-        p->slot = 2 * blockIdx.x + 1;
-        p->shared = owner_of(at + len - 1, rg) - (int)blockIdx.x + 1;
-      } else {
-        p->slot = -1;
-      }
-      t = end;
-      if (t < rg.t1) {  // the next row tile, head or request with work
-        at += len;
-        if (++rt == q.nrt) {
-          rt = 0;
-          if (++h == a.Hkv) {
-            h = 0;
-            do q = load_request(a, ++r, false);
-            while (q.nrt == 0 && r + 1 < a.R);
-          }
-        }
-      }
-      if (p->kt1 > p->kt0) return true;  // else the range ends in the row tile's set-up
-    }
-    return false;
-  }
-};
 
 // What the merge kernel needs about CTA c: the row tile that it begins and leaves cut.
 struct Meta {
@@ -255,9 +265,11 @@ struct Meta {
   int f0, rows;   // its first row within (request, key/value head), and rows
 };
 __device__ __forceinline__ Meta no_meta() { return Meta{0, 0, 0, 0, 0}; }
-__device__ __forceinline__ Meta meta_of(const PagedArgs& a, const Piece& p) {
+// Whether this piece begins a row tile that is cut.
+__device__ __forceinline__ bool begins_cut(const Piece& p) { return p.slot >= 0 && (p.slot & 1); }
+__device__ __forceinline__ Meta meta_of(const PagedArgs& a, const Range& rg, const Piece& p) {
   const int f0 = p.rt * a.rows;
-  return Meta{p.shared, p.q.q0, p.h * a.G, f0, min(a.rows, p.q.n * a.G - f0)};
+  return Meta{owner_of(p.end - 1, rg) - (int)blockIdx.x + 1, p.q.q0, p.h * a.G, f0, min(a.rows, p.q.n * a.G - f0)};
 }
 
 // The tensor-core kernel (attn_paged_tc.cu): which shapes it takes, the rows of its
