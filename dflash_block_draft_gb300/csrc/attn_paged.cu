@@ -293,9 +293,51 @@ __global__ void __launch_bounds__(Simt<T, BM, DMAX>::kThreads, BM == 64 && DMAX 
   if (tid == 0) a.meta[blockIdx.x] = meta;
 }
 
+// Adds pieces i0 .. i0 + N - 1 of one row to (mx, l, o): a lane has CD float4 of columns.
+template <int N, int CD, typename Slot>
+__device__ __forceinline__ void merge_pieces(const PagedArgs& a, int i0, int count, Slot slot, int lane, float& mx,
+                                             float& l, float4 (&o)[CD]) {
+  float2 ml[N];
+  float4 v[N][CD];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    ml[i] = make_float2(-INFINITY, 0.f);
+    if (i0 + i < count) {
+      const long long at = slot(i0 + i);
+      ml[i] = a.part_ml[at];
+#pragma unroll
+      for (int c = 0; c < CD; ++c)
+        if (4 * lane + 128 * c < a.D) v[i][c] = *reinterpret_cast<const float4*>(a.part_o + at * a.D + 4 * lane + 128 * c);
+    }
+  }
+  float top = mx;
+#pragma unroll
+  for (int i = 0; i < N; ++i) top = fmaxf(top, ml[i].x);
+  const float mm = top == -INFINITY ? 0.f : top;
+  const float al = exp2f(mx - mm);
+  mx = top;
+  l *= al;
+#pragma unroll
+  for (int c = 0; c < CD; ++c) o[c] = make_float4(o[c].x * al, o[c].y * al, o[c].z * al, o[c].w * al);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float w = exp2f(ml[i].x - mm);
+    if (w > 0.f) {  // not a piece that does not exist, nor one that saw nothing
+      l = fmaf(w, ml[i].y, l);
+#pragma unroll
+      for (int c = 0; c < CD; ++c) {
+        o[c].x = fmaf(w, v[i][c].x, o[c].x);
+        o[c].y = fmaf(w, v[i][c].y, o[c].y);
+        o[c].z = fmaf(w, v[i][c].z, o[c].z);
+        o[c].w = fmaf(w, v[i][c].w, o[c].w);
+      }
+    }
+  }
+}
+
 // Merges the pieces of the row tile that CTA blockIdx.x began and left cut.  A warp
-// takes a row, its lanes the columns (CD float4 each), eight pieces at a time: two
-// memory latencies, the meta data's and the pieces', whatever their number up to eight.
+// takes a row, two pieces at a time or, of more than four (long contexts, few rows),
+// eight: two memory latencies in all, the meta data's and the pieces'.
 template <typename T, int CD>
 __global__ void __launch_bounds__(128) paged_merge_kernel(const __grid_constant__ PagedArgs a) {
   const Meta m = a.meta[blockIdx.x];
@@ -303,48 +345,15 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const __grid_constant_
   if (m.shared == 0 || row >= m.rows) return;
   // piece 0 lies in slot 2c + 1, piece i > 0, which continues the tile in CTA c + i, in slot 2 (c + i)
   auto slot = [&](int i) { return (long long)(i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i)) * a.rows + row; };
-  constexpr int kBatch = CD == 1 ? 8 : 4;
   float mx = -INFINITY, l = 0.f;
   float4 o[CD];
 #pragma unroll
   for (int c = 0; c < CD; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i0 = 0; i0 < m.shared; i0 += kBatch) {
-    float2 ml[kBatch];
-    float4 v[kBatch][CD];
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      ml[i] = make_float2(-INFINITY, 0.f);
-      if (i0 + i < m.shared) {
-        const long long at = slot(i0 + i);
-        ml[i] = a.part_ml[at];
-#pragma unroll
-        for (int c = 0; c < CD; ++c)
-          if (4 * lane + 128 * c < a.D) v[i][c] = *reinterpret_cast<const float4*>(a.part_o + at * a.D + 4 * lane + 128 * c);
-      }
-    }
-    float top = mx;
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) top = fmaxf(top, ml[i].x);
-    const float mm = top == -INFINITY ? 0.f : top;
-    const float al = exp2f(mx - mm);
-    mx = top;
-    l *= al;
-#pragma unroll
-    for (int c = 0; c < CD; ++c) o[c] = make_float4(o[c].x * al, o[c].y * al, o[c].z * al, o[c].w * al);
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const float w = exp2f(ml[i].x - mm);
-      if (i0 + i < m.shared && w > 0.f) {
-        l = fmaf(w, ml[i].y, l);
-#pragma unroll
-        for (int c = 0; c < CD; ++c) {
-          o[c].x = fmaf(w, v[i][c].x, o[c].x);
-          o[c].y = fmaf(w, v[i][c].y, o[c].y);
-          o[c].z = fmaf(w, v[i][c].z, o[c].z);
-          o[c].w = fmaf(w, v[i][c].w, o[c].w);
-        }
-      }
-    }
+  if (m.shared <= 4) {
+    for (int i = 0; i < m.shared; i += 2) merge_pieces<2>(a, i, m.shared, slot, lane, mx, l, o);
+  } else {
+    constexpr int kBatch = CD == 1 ? 8 : 4;
+    for (int i = 0; i < m.shared; i += kBatch) merge_pieces<kBatch>(a, i, m.shared, slot, lane, mx, l, o);
   }
   const int f = m.f0 + row, tok = f / a.G, head = m.head + f % a.G;
   const float inv = l > 0.f ? 1.f / l : 0.f;

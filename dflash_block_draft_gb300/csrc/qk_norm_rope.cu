@@ -393,25 +393,31 @@ __global__ void __launch_bounds__(kThreads, 4)
   }
 }
 
-// Sums the blocks' rows: 32 columns a block, 32 threads down each column.  Row b
-// belongs to the query weight where b % nchunk < nq, else to the key weight.
-__global__ void __launch_bounds__(1024)
+// Sums the blocks' rows: 8 columns a block, 128 threads down each column, whose five
+// loads go out together (one thread a column of 32 took as long as a short call's
+// gradients).  Row b belongs to the query weight where b % nchunk < nq, else to
+// the key weight.
+constexpr int kDwCols = 8, kDwRows = 128;
+__global__ void __launch_bounds__(kDwCols* kDwRows)
     rope_dw_kernel(const float* part, int blocks, int nq, int nchunk, int D, float* dwq, float* dwk) {
-  __shared__ float red[32][33];
-  const int c = threadIdx.x & 31, y = threadIdx.x >> 5;
-  const int d = blockIdx.x * 32 + c, w = blockIdx.y;
+  __shared__ float red[kDwRows / 4][kDwCols];
+  const int c = threadIdx.x % kDwCols, y = threadIdx.x / kDwCols;
+  const int d = blockIdx.x * kDwCols + c, w = blockIdx.y;
   float* dst = w ? dwk : dwq;
   if (!dst) return;
+  const int first = w ? nq : 0, n = w ? nchunk - nq : nq;  // this weight's chunks of every row of blocks
+  const int rows = n > 0 ? blocks / nchunk * n : 0;
   float s = 0.f;
-  if (d < D)
-    for (int b = y; b < blocks; b += 32)
-      if ((b % nchunk >= nq) == (w == 1)) s += part[(long long)b * D + d];
-  red[y][c] = s;
+#pragma unroll 8
+  for (int i = y; i < rows; i += kDwRows) s += part[((long long)(i / n) * nchunk + first + i % n) * D + d];
+  s += __shfl_xor_sync(0xffffffffu, s, 8);  // a warp's four rows
+  s += __shfl_xor_sync(0xffffffffu, s, 16);
+  if (y % 4 == 0) red[y / 4][c] = s;
   __syncthreads();
-  if (y == 0 && d < D) {
+  if (y == 0) {
     float sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) sum += red[i][c];
+    for (int i = 0; i < kDwRows / 4; ++i) sum += red[i][c];
     dst[d] = sum;
   }
 }
@@ -628,7 +634,7 @@ cudaError_t type_bwd(const RopeArgs& a, float* dwq, float* dwk, cudaStream_t s) 
   count_launch();
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || (!dwq && !dwk)) return e;
-  rope_dw_kernel<<<dim3((a.D + 31) / 32, 2), 1024, 0, s>>>(a.dw_part, d.blocks, d.nq, d.nchunk, a.D, dwq, dwk);
+  rope_dw_kernel<<<dim3(a.D / kDwCols, 2), kDwCols * kDwRows, 0, s>>>(a.dw_part, d.blocks, d.nq, d.nchunk, a.D, dwq, dwk);
   count_launch();
   return cudaGetLastError();
 }
