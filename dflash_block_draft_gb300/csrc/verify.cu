@@ -22,9 +22,10 @@
 // sums would draw another entry in every few hundredth row of a large vocabulary;
 // fp64 adds run at a fraction of the integer rate.)  The steps come from the adder:
 // the bits of 1 + p count steps of 2^-23, what that addition lost is exact in fp32,
-// and the bits of its sum with 1.5 2^-22 count steps of 2^-45.  Eleven instructions
-// an entry; 64-bit conversions took 85 us for 128 rows of 131072, shifts of the
-// fraction 47 us, and the reads alone take 20.
+// and the bits of its sum with 1.5 2^-22 count steps of 2^-45.  Nine instructions an
+// entry in packed fp32; 64-bit conversions took 85 us for 128 rows of 131072,
+// shifts of the fraction 47 us; this takes 28, of which the reads are 20 and the
+// chain of dependent steps the rest.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -39,19 +40,25 @@ constexpr int kMaxCluster = 8;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kStep = 128;    // entries a warp reads at once: a float4 a lane
-constexpr int kUnroll = 4;    // such reads in flight; a segment is a multiple of kStep * kUnroll entries
+constexpr int kUnroll = 2;    // such reads in flight (28 us; 29 with four, 31 with eight); a segment is a multiple of kStep * kUnroll entries
 constexpr int kSegments = 32; // most segments of a warp's run
 
-// Weight of one entry, max(p - q, 0), as steps of 2^-23 and of 2^-45 (signed) that
+// Weights of two entries, max(p - q, 0), as steps of 2^-23 and of 2^-45 (signed) that
 // belong together.  No weight where p > q does not hold, NaN included.
 constexpr float kBias = 0x1.8p-22f;  // sums with it lie in [2^-22, 2^-21): their last bit is 2^-45
-__device__ __forceinline__ void add_weight(float p, float q, bool on, int& hi, int& lo) {
-  const float tp = 1.f + p, tq = 1.f + q;
-  const float rest = (p - (tp - 1.f)) - (q - (tq - 1.f));  // at most 2^-23; exact terms, one rounding
-  const float t = rest + kBias;
-  if (on && p > q) {
-    hi += __float_as_int(tp) - __float_as_int(tq);
-    lo += __float_as_int(t) - __float_as_int(kBias);
+__device__ __forceinline__ void add_weights(float2 p, float2 q, int& hi, int& lo) {
+  const float2 one = make_float2(1.f, 1.f), none = make_float2(-1.f, -1.f), neg = make_float2(-1.f, -1.f);
+  const float2 tp = __fadd2_rn(p, one), tq = __fadd2_rn(q, one);
+  // p - (tp - 1) and the same of q: exact; their difference, at most 2^-23, is rounded once
+  const float2 rp = __ffma2_rn(__fadd2_rn(tp, none), neg, p), rq = __ffma2_rn(__fadd2_rn(tq, none), neg, q);
+  const float2 t = __fadd2_rn(__ffma2_rn(rq, neg, rp), make_float2(kBias, kBias));
+  if (p.x > q.x) {
+    hi += __float_as_int(tp.x) - __float_as_int(tq.x);
+    lo += __float_as_int(t.x) - __float_as_int(kBias);
+  }
+  if (p.y > q.y) {
+    hi += __float_as_int(tp.y) - __float_as_int(tq.y);
+    lo += __float_as_int(t.y) - __float_as_int(kBias);
   }
 }
 __device__ __forceinline__ unsigned long long join(int hi, int lo) {
@@ -70,46 +77,55 @@ struct Row {
   int skip;            // entry with weight 0 (-1: none)
 };
 
-// Four entries of p and q at i; those at and beyond `end` are 0.
+// Four entries of p and q at i; those at and beyond `end`, and the one without
+// weight, are 0.
 struct Four {
-  float p[4], q[4];
+  float4 p, q;
 };
-template <bool VEC>
-__device__ __forceinline__ Four load4(const Row& r, long long i, long long end) {
-  Four f = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+template <bool VEC, bool Q>
+__device__ __forceinline__ Four load4(const Row& r, int i, int end) {
+  Four f;
+  f.p = f.q = make_float4(0.f, 0.f, 0.f, 0.f);
   if (VEC) {
     if (i < end) {
-      const float4 a = *reinterpret_cast<const float4*>(r.p + i);
-      f.p[0] = a.x; f.p[1] = a.y; f.p[2] = a.z; f.p[3] = a.w;
-      if (r.q) {
-        const float4 b = *reinterpret_cast<const float4*>(r.q + i);
-        f.q[0] = b.x; f.q[1] = b.y; f.q[2] = b.z; f.q[3] = b.w;
-      }
+      f.p = *reinterpret_cast<const float4*>(r.p + i);
+      if (Q) f.q = *reinterpret_cast<const float4*>(r.q + i);
     }
   } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (i + e < end) {
-        f.p[e] = r.p[i + e];
-        if (r.q) f.q[e] = r.q[i + e];
-      }
+    if (i < end) f.p.x = r.p[i];
+    if (i + 1 < end) f.p.y = r.p[i + 1];
+    if (i + 2 < end) f.p.z = r.p[i + 2];
+    if (i + 3 < end) f.p.w = r.p[i + 3];
+    if (Q) {
+      if (i < end) f.q.x = r.q[i];
+      if (i + 1 < end) f.q.y = r.q[i + 1];
+      if (i + 2 < end) f.q.z = r.q[i + 2];
+      if (i + 3 < end) f.q.w = r.q[i + 3];
+    }
+  }
+  if (!Q && (unsigned)r.skip - (unsigned)i < 4u) {
+    if (r.skip == i) f.p.x = 0.f;
+    if (r.skip == i + 1) f.p.y = 0.f;
+    if (r.skip == i + 2) f.p.z = 0.f;
+    if (r.skip == i + 3) f.p.w = 0.f;
   }
   return f;
 }
 
 // Sum of [lo, hi) (lo a multiple of 4), over the whole warp.
-template <bool VEC>
-__device__ __forceinline__ unsigned long long segment_sum(const Row& r, long long lo, long long hi, int lane) {
+template <bool VEC, bool Q>
+__device__ __forceinline__ unsigned long long segment_sum(const Row& r, int lo, int hi, int lane) {
   unsigned long long s = 0;
-  for (long long i0 = lo + 4 * lane; i0 - 4 * lane < hi; i0 += kStep * kUnroll) {
+  for (int i0 = lo + 4 * lane; i0 - 4 * lane < hi; i0 += kStep * kUnroll) {
     Four f[kUnroll];
 #pragma unroll
-    for (int k = 0; k < kUnroll; ++k) f[k] = load4<VEC>(r, i0 + k * kStep, hi);
-    int h = 0, l = 0;  // 16 entries: at most 2^27 and 2^26
+    for (int k = 0; k < kUnroll; ++k) f[k] = load4<VEC, Q>(r, i0 + k * kStep, hi);
+    int h = 0, l = 0;  // 8 entries: at most 2^26 and 2^25
 #pragma unroll
-    for (int k = 0; k < kUnroll; ++k)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) add_weight(f[k].p[e], f[k].q[e], (int)(i0 + k * kStep) + e != r.skip, h, l);
+    for (int k = 0; k < kUnroll; ++k) {
+      add_weights(make_float2(f[k].p.x, f[k].p.y), make_float2(f[k].q.x, f[k].q.y), h, l);
+      add_weights(make_float2(f[k].p.z, f[k].p.w), make_float2(f[k].q.z, f[k].q.w), h, l);
+    }
     s += join(h, l);
   }
   return warp_sum(s);
@@ -169,15 +185,17 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
   row.skip = acc < n && !a.q ? a.tokens[t0 + acc] : -1;
   // Runs: the vocabulary in equal pieces, one a warp, multiples of 4 entries; a run in
   // up to kSegments segments.
-  const long long piece = ((long long)a.V + 4 * ranks * kWarps - 1) / (4 * ranks * kWarps) * 4;
-  const long long span = (piece + kSegments * kStep * kUnroll - 1) / (kSegments * kStep * kUnroll) * (kStep * kUnroll);
-  const long long lo = min((long long)a.V, (rank * kWarps + warp) * piece), hi = min((long long)a.V, lo + piece);
+  const int piece = (a.V + 4 * ranks * kWarps - 1) / (4 * ranks * kWarps) * 4;
+  const int span = (piece + kSegments * kStep * kUnroll - 1) / (kSegments * kStep * kUnroll) * (kStep * kUnroll);
+  const int lo = (int)min((long long)a.V, (long long)(rank * kWarps + warp) * piece), hi = min(a.V, lo + piece);
 
   unsigned long long before = 0, total = 0, mine = 0;
   for (int pass = 0; pass < 2; ++pass) {
     mine = 0;
     for (int g = 0; lo + g * span < hi; ++g) {
-      const unsigned long long s = segment_sum<VEC>(row, lo + g * span, min(hi, lo + (g + 1) * span), lane);
+      const int i0 = lo + g * span, i1 = min(hi, i0 + span);
+      const unsigned long long s =
+          row.q ? segment_sum<VEC, true>(row, i0, i1, lane) : segment_sum<VEC, false>(row, i0, i1, lane);
       if (lane == 0) s_seg[warp][g] = s;
       mine += s;
     }
@@ -212,16 +230,17 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
       unsigned long long at = before;
       int g = 0;
       while (lo + (g + 1) * span < hi && at + s_seg[warp][g] <= bar) at += s_seg[warp][g++];
-      const long long end = min(hi, lo + (g + 1) * span);
+      const int end = min(hi, lo + (g + 1) * span);
 #pragma unroll 4
-      for (long long i0 = lo + g * span; i0 < end; i0 += kStep) {
-        const long long i = i0 + 4 * lane;
-        const Four f4 = load4<VEC>(row, i, end);
+      for (int i0 = lo + g * span; i0 < end; i0 += kStep) {
+        const int i = i0 + 4 * lane;
+        const Four f = row.q ? load4<VEC, true>(row, i, end) : load4<VEC, false>(row, i, end);
+        const float p4[4] = {f.p.x, f.p.y, f.p.z, f.p.w}, q4[4] = {f.q.x, f.q.y, f.q.z, f.q.w};
         unsigned long long w[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           int h = 0, l = 0;
-          add_weight(f4.p[e], f4.q[e], (int)i + e != row.skip, h, l);
+          add_weights(make_float2(p4[e], 0.f), make_float2(q4[e], 0.f), h, l);
           w[e] = join(h, l);
         }
         const unsigned long long s = w[0] + w[1] + w[2] + w[3];
@@ -241,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
               if (k <= bar) e = f;  // entries up to the one that passes the bar
               k += w[f];
             }
-            out[acc] = (int)(i + e);
+            out[acc] = i + e;
           }
           break;
         }
