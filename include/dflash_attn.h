@@ -295,7 +295,10 @@ DFLASH_API dflash_status_t dflash_attn_dense_backward(const dflash_dims_t* dims,
  *   dflash_cache_append   the same on the way into a paged cache,
  *   dflash_attn_paged     attention of the new tokens over the pages,
  *   dflash_verify         acceptance of drafted tokens.
- * Element types, ownership, streams and errors as above.
+ * Element types, ownership, streams and errors as above.  The device that holds
+ * the tensors has to be the current one.  Calls that may run at the same time
+ * (on two streams, or in graphs that are replayed side by side) need a workspace
+ * each.  Every call may be captured into a graph.
  */
 
 /*
