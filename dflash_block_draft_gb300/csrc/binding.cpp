@@ -433,6 +433,9 @@ PyObject* verify(PyObject*, PyObject* const* a, Py_ssize_t n) {
       refuse("target_probs must be [rows, V] with contiguous rows, draft_tokens [total_draft], draft_offsets [R + 1]");
     const int dev = p.get_device();
     const int64_t rows = p.size(0), V = p.size(1), T = tok.size(0), R = off.size(0) - 1;
+    // (a broadcast row, whose stride is 0, would read as contiguous ones)
+    if ((rows > 1 && p.stride(0) < V) || (q && q->dim() == 2 && T > 1 && q->stride(0) < V))
+      refuse("the rows of target_probs and draft_probs must not overlap");
     if (rows < T + R) refuse("target_probs needs a row for every drafted token and one more for every request");
     common(p, "target_probs", dev, at::kFloat);
     dflash_verify_dims_t d = {};

@@ -223,3 +223,17 @@ def test_binding_refuses_what_is_not_on_a_gpu_or_has_another_form(lib):
         dfl.dflash_verify(z(4, 10), z(3, 10), z(3, **i32), z(2, **i32), z(3), z(1), 3)
     with pytest.raises(ValueError):  # too few target rows
         dfl.dflash_verify(z(3, 10), z(3, 10), z(3, **i32), z(2, **i32), z(3), z(1), 3)
+
+
+@pytest.mark.parametrize("which", ["target", "draft"])
+def test_verify_refuses_rows_that_overlap(lib, which):
+    """A broadcast row has stride 0, which the library takes for contiguous rows."""
+    z = torch.zeros
+    i32 = dict(dtype=torch.int32)
+    p = z(1, 10).expand(4, 10) if which == "target" else z(4, 10)
+    q = z(1, 10).expand(3, 10) if which == "draft" else z(3, 10)
+    with pytest.raises(ValueError, match="overlap"):
+        dfl.dflash_verify(p, q, z(3, **i32), z(2, **i32), z(3), z(1), 3)
+    overlapping = torch.as_strided(z(64), (4, 10), (9, 1))
+    with pytest.raises(ValueError, match="overlap"):
+        dfl.dflash_verify(overlapping, z(3, 10), z(3, **i32), z(2, **i32), z(3), z(1), 3)
