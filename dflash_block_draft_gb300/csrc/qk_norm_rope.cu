@@ -365,14 +365,15 @@ __global__ void __launch_bounds__(kThreads, 4)
             s2 = __ffma2_rn(x[e], x[e], s2);
             d2 = __ffma2_rn(gw[e], x[e], d2);
           }
-          const float r = rsqrtf(group_sum<LANES>(s2.x + s2.y) * inv_d + a.eps);
-          // r times mean(g w x^) r, the factor of x
-          const float c = -group_sum<LANES>(d2.x + d2.y) * r * r * inv_d * r;
+          // (0 for a group without a token: with eps = 0 its r would be infinite, and 0 r in dw NaN)
+          const float ms = group_sum<LANES>(s2.x + s2.y) * inv_d, r = ok ? rsqrtf(ms + a.eps) : 0.f;
+          const float c = -group_sum<LANES>(d2.x + d2.y) * r * inv_d;  // -mean(g w x^)
           const float2 r2 = make_float2(r, r), c2 = make_float2(c, c);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            dw[e] = __ffma2_rn(g[e], __fmul2_rn(x[e], r2), dw[e]);
-            g[e] = __ffma2_rn(x[e], c2, __fmul2_rn(gw[e], r2));
+            const float2 xh = __fmul2_rn(x[e], r2);
+            dw[e] = __ffma2_rn(g[e], xh, dw[e]);
+            g[e] = __fmul2_rn(__ffma2_rn(xh, c2, gw[e]), r2);
           }
         }
         if (have) {

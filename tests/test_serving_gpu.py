@@ -166,6 +166,26 @@ def test_qk_norm_rope_no_tokens_and_rows_of_zeros(dfl):
     assert (qo == 0).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("T,Hq,Hkv,D,rot,inter", [(5, 4, 2, 128, 128, False), (33, 3, 1, 96, 64, True),
+                                                  (6, 5, 5, 80, 40, False), (4, 2, 1, 24, 6, True)])
+def test_backward_without_epsilon(dfl, T, Hq, Hkv, D, rot, inter, dtype):
+    """eps = 0: what has no token (the last groups of a block, a position outside the table) adds nothing."""
+    rng = np.random.default_rng(T + D)
+    q, k, (wq, wk), cs, pos = _rope_case(rng, T, Hq, Hkv, D, rot, True, "own", dtype)
+    gq, gk = _rand(rng, (T, Hq, D), dtype), _rand(rng, (T, Hkv, D), dtype)
+    pos[1] = 64
+    keep = np.array([t for t in range(T) if t != 1])
+    dq, dk, dwq, dwk = dfl.dflash_qk_norm_rope_backward(q, k, _i32(pos), cs, gq, gk, q_norm=wq, k_norm=wk, eps=0.0,
+                                                        interleaved=inter)
+    assert dfl.dflash_last_device_error() == INVALID
+    for x, w, g, dx, dw, H in ((q, wq, gq, dq, dwq, Hq), (k, wk, gk, dk, dwk, Hkv)):
+        want, size, ww, wsize = osv.norm_rope_backward(_np(x)[keep], _w(w), pos[keep], _np(cs), 0.0, inter,
+                                                       _np(g)[keep])
+        _within(_np(dx)[keep], want, size * (2 * D + 64) * U + HALF[dtype] * np.abs(want), "dx")
+        _within(dw, ww, wsize * (T * H + D + 32) * U, "dw")
+
+
 @pytest.mark.parametrize("D,rot", [(128, 128), (24, 6)])
 def test_positions_outside_the_table_are_skipped_and_recorded(dfl, D, rot):
     rng = np.random.default_rng(8)
