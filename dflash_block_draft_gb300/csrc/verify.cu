@@ -223,9 +223,9 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
   for (int i = 0; i < warp; ++i) before += s_warp[i];
   if (total > 0) {
     // z is the first entry whose running sum exceeds s * total; sums are whole
-    // numbers, so it exceeds floor(s * total).
+    // numbers, so it exceeds floor(s * total), which a product rounded down keeps.
     const float u = fminf(fmaxf(a.s[r], 0.f), 0x1.fffffep-1f);
-    const unsigned long long bar = (unsigned long long)((double)u * (double)total);
+    const unsigned long long bar = (unsigned long long)__dmul_rd((double)u, (double)total);
     if (before <= bar && bar < before + mine) {  // one warp of the cluster
       unsigned long long at = before;
       int g = 0;
