@@ -8,16 +8,17 @@
 // running maximum m rises.
 //
 // A CTA holds a row tile's queries in shared memory and walks its key tiles of 64
-// positions (fp32 up to D = 64) or 32, which arrive by 16-byte asynchronous copies two tiles deep; the rows'
-// offsets (page table and page row) are worked out one tile ahead of the copies.
+// positions (fp32 up to D = 64, 64-row tiles) or 32, which arrive by 16-byte
+// asynchronous copies two tiles deep; the rows' offsets (page table and page row) are
+// worked out one tile ahead of the copies.
 // Each thread has 4 rows of the scores and of the output in registers, and all
 // threads of a row lie in one warp, so that the softmax needs shuffles only and a
 // key tile two block barriers.  Row tiles of 64 rows with 256 threads, or of 16 with
 // 128 where no request has more rows (single tokens and short blocks with few
 // heads a group, where 64-row tiles would multiply mostly padding; the smaller
 // CTAs also put more copies in flight): 6 requests of up to 16 tokens with 16 fp32
-// heads of 64, behind 300 to 4000 positions, take 35 us, 42 with 64-row tiles; 16
-// single tokens of 16 heads of 128 take 108 us (3.7 TB/s), 156 with them.  fp32 needs
+// heads of 64, behind 300 to 4000 positions, take 29 us, 42 with 64-row tiles; 16
+// single tokens of 16 heads of 128 take 107 us (3.8 TB/s), 156 with them.  fp32 needs
 // 2 D multiply-adds for each row and 8 D bytes of a position, so it is bound by the
 // multiply-adds, and by the shared memory that feeds them, from a few rows on and
 // by memory below.
@@ -55,13 +56,22 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
   return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
                      __uint_as_float(v.y & 0xFFFF0000u));
 }
+__device__ __forceinline__ float2 load2(const float* p) { return *reinterpret_cast<const float2*>(p); }
+__device__ __forceinline__ float2 load2(const __nv_bfloat16* p) {
+  const uint32_t v = *reinterpret_cast<const uint32_t*>(p);
+  return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+}
 
 template <typename T, int BM, int DMAX>
 struct Simt {
-  // positions of a key tile: two stages of K and V for two CTAs an SM (bf16 with D = 128
-  // and 64-row tiles: 160 us with 32, 172 with 64)
-  static constexpr int BN = sizeof(T) == 4 && DMAX <= 64 ? 64 : 32;
+  // Positions of a key tile: two stages of K and V for two CTAs an SM, four of 16-row tiles
+  // (bf16 with D = 128 and 64-row tiles: 160 us with 32, 172 with 64; fp32 with D = 64:
+  // 64-row tiles 167 and 149, 16-row tiles 29 and 33).
+  static constexpr int BN = sizeof(T) == 4 && DMAX <= 64 && BM == 64 ? 64 : 32;
   static constexpr int kThreads = BM == 16 ? 128 : 256;
+  // CTAs an SM that the registers are kept to, where shared memory has room for them (bf16
+  // 16-row tiles with D = 128: 63 us so, 113 with three and a grid of four)
+  static constexpr int kPerSm = BM == 64 ? (DMAX <= 128 ? 2 : 1) : DMAX <= 64 || (sizeof(T) == 2 && DMAX <= 128) ? 4 : 1;
   static constexpr int kVec = 16 / sizeof(T);
   static constexpr int kStride = DMAX + kVec;  // elements from row to row of K and V
   static constexpr int kQStride = DMAX + 4;
@@ -77,7 +87,7 @@ struct Simt {
 };
 
 template <typename T, int BM, int DMAX>
-__global__ void __launch_bounds__(Simt<T, BM, DMAX>::kThreads, BM == 64 && DMAX <= 128 ? 2 : 1)
+__global__ void __launch_bounds__(Simt<T, BM, DMAX>::kThreads, Simt<T, BM, DMAX>::kPerSm)
     paged_simt_kernel(const __grid_constant__ PagedArgs a) {
   using C = Simt<T, BM, DMAX>;
   constexpr int BN = C::BN, kThreads = C::kThreads, VEC = C::kVec;
@@ -147,7 +157,8 @@ __global__ void __launch_bounds__(Simt<T, BM, DMAX>::kThreads, BM == 64 && DMAX 
       *reinterpret_cast<float4*>(s.q + r * C::kQStride + c) = x;
     }
     int lim[4];
-    float m[4], l[4], o[4][NC];
+    float m[4], l[4];
+    float2 o[4][NC / 2];  // in pairs of columns, for the packed multiply-adds
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int row = 4 * ty + i;
@@ -155,7 +166,7 @@ __global__ void __launch_bounds__(Simt<T, BM, DMAX>::kThreads, BM == 64 && DMAX 
       m[i] = -INFINITY;
       l[i] = 0.f;
 #pragma unroll
-      for (int c = 0; c < NC; ++c) o[i][c] = 0.f;
+      for (int c = 0; c < NC / 2; ++c) o[i][c] = make_float2(0.f, 0.f);
     }
     const bool idle = 32 / TX * 4 * (tid / 32) >= nrow;  // none of the warp's rows exists: it only copies
     __syncthreads();
@@ -220,7 +231,7 @@ __global__ void __launch_bounds__(Simt<T, BM, DMAX>::kThreads, BM == 64 && DMAX 
           l[i] = l[i] * al + sum;
           m[i] = m1;
 #pragma unroll
-          for (int c = 0; c < NC; ++c) o[i][c] *= al;
+          for (int c = 0; c < NC / 2; ++c) o[i][c] = __fmul2_rn(o[i][c], make_float2(al, al));
         }
         __syncwarp();  // the rows' weights, written by this warp alone
 #pragma unroll 2
@@ -236,23 +247,26 @@ __global__ void __launch_bounds__(Simt<T, BM, DMAX>::kThreads, BM == 64 && DMAX 
 #pragma unroll
             for (int u = 0; u < U; ++u) {
               const int c0 = (tx + TX * u) * VW;
-              float vv[VW];
+              float2 vv[VW / 2];
 #pragma unroll
-              for (int e = 0; e < VW; ++e) vv[e] = 0.f;
+              for (int e = 0; e < VW / 2; ++e) vv[e] = make_float2(0.f, 0.f);
               if (c0 < D) {
                 const T* vp = vs + (k + kk) * C::kStride + c0;
                 if constexpr (VW == 4) {
                   const float4 w = load4(vp);
-                  vv[0] = w.x; vv[1] = w.y; vv[2] = w.z; vv[3] = w.w;
+                  vv[0] = make_float2(w.x, w.y);
+                  vv[1] = make_float2(w.z, w.w);
                 } else {
-#pragma unroll
-                  for (int e = 0; e < VW; ++e) vv[e] = to_f32(vp[e]);
+                  vv[0] = load2(vp);
                 }
               }
 #pragma unroll
               for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int e = 0; e < VW; ++e) o[i][u * VW + e] = fmaf(pp[i][kk], vv[e], o[i][u * VW + e]);
+                for (int e = 0; e < VW / 2; ++e) {
+                  float2& at = o[i][u * (VW / 2) + e];
+                  at = __ffma2_rn(make_float2(pp[i][kk], pp[i][kk]), vv[e], at);
+                }
             }
         }
       }
@@ -274,7 +288,8 @@ __global__ void __launch_bounds__(Simt<T, BM, DMAX>::kThreads, BM == 64 && DMAX 
 #pragma unroll
           for (int e = 0; e < VW; ++e) {
             const int c = (tx + TX * u) * VW + e;
-            if (c < D) dst[c] = from_f32<T>(o[i][u * VW + e] * inv);
+            const float2 oo = o[i][(u * VW + e) / 2];
+            if (c < D) dst[c] = from_f32<T>((e & 1 ? oo.y : oo.x) * inv);
           }
         if (a.lse && tx == 0)
           a.lse[(long long)head * a.total_q + pc.q.q0 + tok] =
@@ -286,7 +301,8 @@ __global__ void __launch_bounds__(Simt<T, BM, DMAX>::kThreads, BM == 64 && DMAX 
 #pragma unroll
           for (int e = 0; e < VW; ++e) {
             const int c = (tx + TX * u) * VW + e;
-            if (c < D) a.part_o[at * D + c] = o[i][u * VW + e];
+            const float2 oo = o[i][(u * VW + e) / 2];
+            if (c < D) a.part_o[at * D + c] = e & 1 ? oo.y : oo.x;
           }
         if (tx == 0) a.part_ml[at] = make_float2(m[i], l[i]);
       }
