@@ -133,7 +133,7 @@ struct RopeArgs {
 cudaError_t launch_qk_norm_rope(const RopeArgs& a, bool bf16, bool paged, cudaStream_t stream);
 size_t rope_bwd_workspace_bytes(int D);
 // dq, dk go to a.qo, a.ko.
-cudaError_t launch_qk_norm_rope_bwd(const RopeArgs& a, bool bf16, float* dwq, float* dwk, cudaStream_t stream);
+cudaError_t launch_qk_norm_rope_bwd(RopeArgs a, bool bf16, float* dwq, float* dwk, cudaStream_t stream);
 
 // Attention over a paged cache (attn_paged.cu, attn_paged_tc.cu).
 namespace paged {
