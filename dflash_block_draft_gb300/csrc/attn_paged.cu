@@ -312,130 +312,105 @@ __global__ void __launch_bounds__(Simt<T, BM, DMAX>::kThreads, Simt<T, BM, DMAX>
   if (tid == 0) a.meta[blockIdx.x] = meta;
 }
 
-// A row of the merge: a lane has CD float4 of columns.
-template <int CD>
-struct Merged {
-  float mx, l;
-  float4 o[CD];
-};
-
-// Adds pieces i0 .. i0 + N - 1 to each of the rows; at(i, j) is the place of piece i's row j.
-template <int N, int ROWS, int CD, typename At>
-__device__ __forceinline__ void merge_pieces(const PagedArgs& a, int i0, int count, At at, int lane,
-                                             Merged<CD> (&rows)[ROWS]) {
-  float2 ml[ROWS][N];
-  float4 v[ROWS][N][CD];
+// Adds pieces i0 .. i0 + N - 1 of one row to (mx, l, o): a lane has CD float4 of columns, 4 LANES
+// columns apart.
+template <int N, int LANES, int CD, typename Slot>
+__device__ __forceinline__ void merge_pieces(const PagedArgs& a, int i0, int count, Slot slot, int lane, float& mx,
+                                             float& l, float4 (&o)[CD]) {
+  float2 ml[N];
+  float4 v[N][CD];
 #pragma unroll
-  for (int j = 0; j < ROWS; ++j)
+  for (int i = 0; i < N; ++i) {
+    ml[i] = make_float2(-INFINITY, 0.f);
+    if (i0 + i < count) {
+      const long long at = slot(i0 + i);
+      ml[i] = a.part_ml[at];
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      ml[j][i] = make_float2(-INFINITY, 0.f);
-      if (i0 + i < count) {
-        const long long x = at(i0 + i, j);
-        ml[j][i] = a.part_ml[x];
-#pragma unroll
-        for (int c = 0; c < CD; ++c)
-          if (4 * lane + 128 * c < a.D)
-            v[j][i][c] = *reinterpret_cast<const float4*>(a.part_o + x * a.D + 4 * lane + 128 * c);
-      }
+      for (int c = 0; c < CD; ++c)
+        if (4 * (lane + LANES * c) < a.D)
+          v[i][c] = *reinterpret_cast<const float4*>(a.part_o + at * a.D + 4 * (lane + LANES * c));
     }
+  }
+  float top = mx;
 #pragma unroll
-  for (int j = 0; j < ROWS; ++j) {
-    Merged<CD>& r = rows[j];
-    float top = r.mx;
+  for (int i = 0; i < N; ++i) top = fmaxf(top, ml[i].x);
+  const float mm = top == -INFINITY ? 0.f : top;
+  const float al = exp2f(mx - mm);
+  mx = top;
+  l *= al;
 #pragma unroll
-    for (int i = 0; i < N; ++i) top = fmaxf(top, ml[j][i].x);
-    const float mm = top == -INFINITY ? 0.f : top;
-    const float al = exp2f(r.mx - mm);
-    r.mx = top;
-    r.l *= al;
+  for (int c = 0; c < CD; ++c) o[c] = make_float4(o[c].x * al, o[c].y * al, o[c].z * al, o[c].w * al);
 #pragma unroll
-    for (int c = 0; c < CD; ++c) r.o[c] = make_float4(r.o[c].x * al, r.o[c].y * al, r.o[c].z * al, r.o[c].w * al);
+  for (int i = 0; i < N; ++i) {
+    const float w = exp2f(ml[i].x - mm);
+    if (w > 0.f) {  // not a piece that does not exist, nor one that saw nothing
+      l = fmaf(w, ml[i].y, l);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float w = exp2f(ml[j][i].x - mm);
-      if (w > 0.f) {  // not a piece that does not exist, nor one that saw nothing
-        r.l = fmaf(w, ml[j][i].y, r.l);
-#pragma unroll
-        for (int c = 0; c < CD; ++c) {
-          r.o[c].x = fmaf(w, v[j][i][c].x, r.o[c].x);
-          r.o[c].y = fmaf(w, v[j][i][c].y, r.o[c].y);
-          r.o[c].z = fmaf(w, v[j][i][c].z, r.o[c].z);
-          r.o[c].w = fmaf(w, v[j][i][c].w, r.o[c].w);
-        }
+      for (int c = 0; c < CD; ++c) {
+        o[c].x = fmaf(w, v[i][c].x, o[c].x);
+        o[c].y = fmaf(w, v[i][c].y, o[c].y);
+        o[c].z = fmaf(w, v[i][c].z, o[c].z);
+        o[c].w = fmaf(w, v[i][c].w, o[c].w);
       }
     }
   }
 }
 
-// Merges the pieces of the row tile that CTA blockIdx.x began and left cut.  A warp
-// takes ROWS rows, two pieces of each at a time or, of one row with more than four
-// pieces (long contexts, few rows), eight: two memory latencies in all, the meta
-// data's and the pieces'.
-template <typename T, int CD, int ROWS>
+// Merges the pieces of the row tile that CTA blockIdx.x began and left cut.  LANES lanes take
+// a row, two pieces at a time or, of more than four (long contexts, few rows; whole
+// warps), eight: two memory latencies in all, the meta data's and the pieces'.
+template <typename T, int LANES, int CD>
 __global__ void __launch_bounds__(128) paged_merge_kernel(const __grid_constant__ PagedArgs a) {
   const Meta m = a.meta[blockIdx.x];
-  const int lane = threadIdx.x & 31, row = blockIdx.y * 4 * ROWS + (threadIdx.x >> 5);  // and every fourth after it
+  const int lane = threadIdx.x % LANES, row = blockIdx.y * (128 / LANES) + threadIdx.x / LANES;
   if (m.shared == 0 || row >= m.rows) return;
-  // piece 0 lies in slot 2c + 1, piece i > 0, which continues the tile in CTA c + i, in slot 2 (c + i);
-  // a row that does not exist reads the last one
-  auto at = [&](int i, int j) {
-    return (long long)(i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i)) * a.rows + min(row + 4 * j, m.rows - 1);
-  };
-  Merged<CD> rows[ROWS];
+  // piece 0 lies in slot 2c + 1, piece i > 0, which continues the tile in CTA c + i, in slot 2 (c + i)
+  auto slot = [&](int i) { return (long long)(i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i)) * a.rows + row; };
+  float mx = -INFINITY, l = 0.f;
+  float4 o[CD];
 #pragma unroll
-  for (int j = 0; j < ROWS; ++j) {
-    rows[j].mx = -INFINITY;
-    rows[j].l = 0.f;
-#pragma unroll
-    for (int c = 0; c < CD; ++c) rows[j].o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-  }
-  if (ROWS > 1 || m.shared <= 4) {
-    for (int i = 0; i < m.shared; i += 2) merge_pieces<2>(a, i, m.shared, at, lane, rows);
+  for (int c = 0; c < CD; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (LANES < 32 || m.shared <= 4) {
+    for (int i = 0; i < m.shared; i += 2) merge_pieces<2, LANES>(a, i, m.shared, slot, lane, mx, l, o);
   } else {
-    constexpr int kBatch = ROWS > 1 ? 1 : CD == 1 ? 8 : 4;
-    for (int i = 0; i < m.shared; i += kBatch) merge_pieces<kBatch>(a, i, m.shared, at, lane, rows);
+    constexpr int kBatch = LANES < 32 ? 1 : CD == 1 ? 8 : 4;
+    for (int i = 0; i < m.shared; i += kBatch) merge_pieces<kBatch, LANES>(a, i, m.shared, slot, lane, mx, l, o);
   }
+  const int f = m.f0 + row, tok = f / a.G, head = m.head + f % a.G;
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  T* dst = static_cast<T*>(a.out) + ((long long)(m.q0 + tok) * a.Hq + head) * a.D;
 #pragma unroll
-  for (int j = 0; j < ROWS; ++j) {
-    if (row + 4 * j >= m.rows) break;
-    const float mx = rows[j].mx, l = rows[j].l;
-    const float4(&o)[CD] = rows[j].o;
-    const int f = m.f0 + row + 4 * j, tok = f / a.G, head = m.head + f % a.G;
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    T* dst = static_cast<T*>(a.out) + ((long long)(m.q0 + tok) * a.Hq + head) * a.D;
-#pragma unroll
-    for (int c = 0; c < CD; ++c) {
-      const int d = 4 * lane + 128 * c;
-      if (d < a.D) {  // D is a multiple of 8: all four columns exist
-        if constexpr (sizeof(T) == 4) {
-          *reinterpret_cast<float4*>(dst + d) = make_float4(o[c].x * inv, o[c].y * inv, o[c].z * inv, o[c].w * inv);
-        } else {
-          const __nv_bfloat162 b0 = __floats2bfloat162_rn(o[c].x * inv, o[c].y * inv);
-          const __nv_bfloat162 b1 = __floats2bfloat162_rn(o[c].z * inv, o[c].w * inv);
-          uint2 w;
-          w.x = *reinterpret_cast<const uint32_t*>(&b0);
-          w.y = *reinterpret_cast<const uint32_t*>(&b1);
-          *reinterpret_cast<uint2*>(dst + d) = w;
-        }
+  for (int c = 0; c < CD; ++c) {
+    const int d = 4 * (lane + LANES * c);
+    if (d < a.D) {  // D is a multiple of 8: all four columns exist
+      if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<float4*>(dst + d) = make_float4(o[c].x * inv, o[c].y * inv, o[c].z * inv, o[c].w * inv);
+      } else {
+        const __nv_bfloat162 b0 = __floats2bfloat162_rn(o[c].x * inv, o[c].y * inv);
+        const __nv_bfloat162 b1 = __floats2bfloat162_rn(o[c].z * inv, o[c].w * inv);
+        uint2 w;
+        w.x = *reinterpret_cast<const uint32_t*>(&b0);
+        w.y = *reinterpret_cast<const uint32_t*>(&b1);
+        *reinterpret_cast<uint2*>(dst + d) = w;
       }
     }
-    if (a.lse && lane == 0)
-      a.lse[(long long)head * a.total_q + m.q0 + tok] = l > 0.f ? (mx + log2f(l)) * 0.6931471805599453f : -INFINITY;
   }
+  if (a.lse && lane == 0)
+    a.lse[(long long)head * a.total_q + m.q0 + tok] = l > 0.f ? (mx + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
-// Two rows a warp for pairs of tensor-core row tiles (more than 128 rows), whose blocks
-// would take many waves: 16 requests of 33 to 48 tokens 47.5 us in all, 49.9 with one row,
-// 50.0 with four; 4 chunks of 512 tokens 91.0, 93.5 and 91.4.
+// Eight lanes a row for pairs of tensor-core row tiles (more than 128 rows): with a warp a
+// row, most of what it issues is the same in all lanes.  (Requests of 33 to 48 tokens 45.4 us in
+// all, 49.8 with whole warps, 45.7 with 16 lanes and 45.6 with 4; 4 chunks of 512 tokens 84
+// to 89, 96, 89 and 84 to 90.)
 template <typename T>
 void run_merge(const PagedArgs& a, int grid, cudaStream_t s) {
+  constexpr int kLanes = sizeof(T) == 2 ? 8 : 32;  // only bf16 has such row tiles
   const long long most = (long long)a.max_q * a.G;
-  const int rows = most < a.rows ? (int)most : a.rows;
-  constexpr int kMany = sizeof(T) == 2 ? 2 : 1;  // only bf16 has such row tiles
-  if (a.D > 128) paged_merge_kernel<T, 2, 1><<<dim3(grid, (rows + 3) / 4), 128, 0, s>>>(a);
-  else if (rows <= 128) paged_merge_kernel<T, 1, 1><<<dim3(grid, (rows + 3) / 4), 128, 0, s>>>(a);
-  else paged_merge_kernel<T, 1, kMany><<<dim3(grid, (rows + 4 * kMany - 1) / (4 * kMany)), 128, 0, s>>>(a);
+  const int rows = most < a.rows ? (int)most : a.rows, per = 128 / kLanes;
+  if (a.D > 128) paged_merge_kernel<T, 32, 2><<<dim3(grid, (rows + 3) / 4), 128, 0, s>>>(a);
+  else if (rows <= 128) paged_merge_kernel<T, 32, 1><<<dim3(grid, (rows + 3) / 4), 128, 0, s>>>(a);
+  else paged_merge_kernel<T, kLanes, 32 / kLanes><<<dim3(grid, (rows + per - 1) / per), 128, 0, s>>>(a);
   count_launch();
 }
 

@@ -49,8 +49,8 @@
 // both halves take 2110 and one half's chain QK, softmax, PV the rest (P lies over S,
 // so QK of the next tile waits for PV).  Scores issued 64 keys at a time into
 // what P leaves free shorten that to 2950, but N = 64 MMAs then fill the tensor pipe
-// and the clock falls with the power: 804 us, and 4 chunks of 512 tokens 101 us
-// where they take 90.
+// and the clock falls with the power: 804 us, and 4 chunks of 512 tokens took
+// 101 us against 90.
 #include <math.h>
 
 #include <atomic>
@@ -659,9 +659,8 @@ cudaError_t run_tc(const TcPagedArgs& ta, int grid, const CUtensorMap& q, const 
 bool paged_tc_supported(int G, int D, int P) { return D <= 128 && D % 8 == 0 && G <= kBM && P % 8 == 0; }
 
 // A second row tile where some request has more rows than one holds: 808 us against 881
-// for 2048 tokens behind 32768, 51 against 55 for 16 requests of 33 to 48 tokens (4
-// heads a group), though 24 against 21 where 4 requests of 30 to 100 tokens leave
-// few row tiles.
+// for 2048 tokens behind 32768, 45 against 55 for 16 requests of 33 to 48 tokens (4
+// heads a group), 21 and 21 where 4 requests of 30 to 100 tokens leave few row tiles.
 static bool paired(int G, int max_q) { return max_q > kBM / G; }
 
 // Tokens of a tile of up to 128 rows.
