@@ -422,6 +422,11 @@ APPEND = [
     ([400, 380], [390, 300], 64, 16, 4, 128, 128, False, True),
     ([20, 3] + [0] * 45 + [9, 2, 70], [3, 2] + [0] * 45 + [9, 1, 40], 16, 4, 2, 64, 64, False, True),  # many empty ones
     ([1 + i % 7 for i in range(90)], [1 - i % 2 for i in range(90)], 4, 2, 1, 128, 128, True, True),
+    # a thread for every request, and more requests than threads
+    ([2 + i % 5 for i in range(256)], [i % 3 for i in range(256)], 4, 2, 1, 128, 128, False, True),
+    ([3 + i % 5 for i in range(257)], [i * i % 4 for i in range(257)], 4, 2, 1, 64, 64, False, True),
+    ([20, 3] + [0] * 300 + [9, 2, 70], [3, 2] + [0] * 300 + [9, 1, 40], 16, 4, 2, 64, 64, False, True),
+    ([3 + i % 5 for i in range(700)], [1] * 700, 8, 2, 2, 24, 24, False, True),
 ]
 
 
