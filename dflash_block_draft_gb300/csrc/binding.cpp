@@ -100,9 +100,10 @@ void* tokens(const at::Tensor& t, const char* name, int dev, at::ScalarType type
              int64_t* stride) {
   common(t, name, dev, type);
   shaped(t, name, {T, H, D});
-  if ((D > 1 && t.stride(2) != 1) || (H > 1 && t.stride(1) != D) || (T > 1 && t.stride(0) < H * D))
+  // (the strides of a tensor without elements mean nothing)
+  if (t.numel() > 0 && ((D > 1 && t.stride(2) != 1) || (H > 1 && t.stride(1) != D) || (T > 1 && t.stride(0) < H * D)))
     refuse(std::string("the heads of a token of ") + name + " must be contiguous");
-  *stride = T > 1 ? t.stride(0) : 0;
+  *stride = T > 1 && t.numel() > 0 ? t.stride(0) : 0;
   return t.data_ptr();
 }
 // Of [pages, page_size, H_kv, D] whose pages are each contiguous.
@@ -111,10 +112,10 @@ void* pages(const at::Tensor& t, const char* name, int dev, at::ScalarType type,
   common(t, name, dev, type);
   if (t.sizes() != shape) refuse(std::string(name) + " must be " + list(shape) + ", got " + list(t.sizes()));
   const int64_t n = shape[0], P = shape[1], H = shape[2], D = shape[3];
-  if ((D > 1 && t.stride(3) != 1) || (H > 1 && t.stride(2) != D) || (P > 1 && t.stride(1) != H * D) ||
-      (n > 1 && t.stride(0) < P * H * D))
+  if (t.numel() > 0 && ((D > 1 && t.stride(3) != 1) || (H > 1 && t.stride(2) != D) ||
+                        (P > 1 && t.stride(1) != H * D) || (n > 1 && t.stride(0) < P * H * D)))
     refuse(std::string("the pages of ") + name + " must be contiguous");
-  *stride = n > 1 ? t.stride(0) : 0;
+  *stride = n > 1 && t.numel() > 0 ? t.stride(0) : 0;
   return t.data_ptr();
 }
 
@@ -443,8 +444,8 @@ PyObject* verify(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (q) {
       common(*q, "draft_probs", dev, at::kFloat);
       shaped(*q, "draft_probs", {T, V});
-      if (V > 1 && q->stride(1) != 1) refuse("draft_probs must have contiguous rows");
       if (T > 0) {
+        if (V > 1 && q->stride(1) != 1) refuse("draft_probs must have contiguous rows");
         qp = q->data_ptr();
         d.draft_stride = T > 1 ? q->stride(0) : 0;
       }

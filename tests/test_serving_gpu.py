@@ -591,6 +591,22 @@ def test_verify_strided_rows(dfl):
         np.testing.assert_array_equal(acc.cpu().numpy(), want[1])
 
 
+def test_tensors_without_elements_may_have_any_strides(dfl):
+    rng = np.random.default_rng(13)
+    p, _, tok, off, u, s = _verify_case(rng, [0, 0, 0], 640, False)
+    want = osv.verify(p, None, tok, off, u, s, 2)
+    args = [torch.from_numpy(p).cuda(), None, _i32(tok), _i32(off), torch.from_numpy(u).cuda(),
+            torch.from_numpy(s).cuda(), 2]
+    for q in (None, torch.empty_strided((0, 640), (0, 0), device="cuda")):
+        args[1] = q
+        out, acc = dfl.dflash_verify(*args)
+        np.testing.assert_array_equal(out.cpu().numpy(), want[0])
+        np.testing.assert_array_equal(acc.cpu().numpy(), want[1])
+    e = torch.empty_strided((0, 4, 64), (1, 1, 0), device="cuda")
+    qo, ko = dfl.dflash_qk_norm_rope(e, e, _i32([]), _table(8, 64))
+    assert qo.shape == ko.shape == (0, 4, 64)
+
+
 # ------------------------------------------------------------------ together
 class _Step:
     """One serving step as it is used: a drafted block enters the cache, attends over it, and the drafted tokens
