@@ -141,6 +141,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
   const int r = blockIdx.x / ranks;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int t0 = a.offsets[r], t1 = a.offsets[r + 1];
+  const float sample = a.s[r];  // needed last, read while the offsets are
   const int n = t1 - t0;
   int* out = a.out + (long long)r * (a.max_draft + 1);
   if (t0 < 0 || n < 0 || t1 > a.total || n > a.max_draft) {  // the same in every CTA of the cluster
@@ -224,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
   if (total > 0) {
     // z is the first entry whose running sum exceeds s * total; sums are whole
     // numbers, so it exceeds floor(s * total), which a product rounded down keeps.
-    const float u = fminf(fmaxf(a.s[r], 0.f), 0x1.fffffep-1f);
+    const float u = fminf(fmaxf(sample, 0.f), 0x1.fffffep-1f);
     const unsigned long long bar = (unsigned long long)__dmul_rd((double)u, (double)total);
     if (before <= bar && bar < before + mine) {  // one warp of the cluster
       unsigned long long at = before;
