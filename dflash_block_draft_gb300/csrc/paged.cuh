@@ -38,7 +38,8 @@ __device__ __forceinline__ Req load_request(const PagedArgs& a, int r, bool repo
   const int q1 = a.q_off[r + 1];
   q.n = q1 - q.q0;
   q.kv = a.kv_lens[r];
-  const bool bad = q.q0 < 0 || q.n < 0 || q1 > a.total_q || q.n > a.max_q || q.kv < 0 ||
+  // (q1 < q0 by itself: of offsets far apart the difference wraps)
+  const bool bad = q.q0 < 0 || q1 < q.q0 || q1 > a.total_q || q.n > a.max_q || q.kv < 0 ||
                    q.kv > (long long)a.max_pages * a.P;
   if (bad && report) record_error(a.err, DFLASH_ERR_INVALID);
   // rows of a request fit 31 bits (the host bounds max_q * G)

@@ -368,6 +368,23 @@ def test_attn_paged_bad_pages_and_bad_requests(dfl, dtype, P):
     assert (out[off[1]:] == 7).all() and not (out[:2] == 7).any()
 
 
+@pytest.mark.parametrize("max_q", [2, 200])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_attn_paged_offsets_whose_difference_wraps(dfl, dtype, max_q):
+    """-2^31 - (2^31 - 1) is 1 in 32 bits: such a request is recorded and skipped like every other bad one."""
+    rng = np.random.default_rng(14)
+    kc, vc, table, off, T = _batch(rng, [60, 45, 30], [2, 1, 1], 16, 2, 64, dtype)
+    q = _rand(rng, (T, 4, 64), dtype)
+    out = torch.full((T, 4, 64), 7.0, dtype=DT[dtype], device="cuda")
+    dfl.dflash_attn_paged(q, kc, vc, _i32(table), _i32([60, 45, 30]), _i32([0, 2, 2 ** 31 - 1, -2 ** 31]), max_q,
+                          out=out)
+    assert dfl.dflash_last_device_error() == INVALID
+    assert (out[2:] == 7).all()
+    want, _, size, _ = osv.attn_paged(_np(q)[:2], _np(kc), _np(vc), table, [60], off[:2], True)
+    # scores of 64 terms, the sums over 60 positions; bf16 weights
+    _within(out[:2], want, size * (2.0 ** -8 if dtype == "bf16" else 2.0 ** -18) + HALF[dtype] * np.abs(want))
+
+
 @pytest.mark.parametrize("kv,n,P,Hq,Hkv,D", ATTN[3:8])
 def test_attn_paged_bf16_on_the_cuda_cores(dfl, monkeypatch, kv, n, P, Hq, Hkv, D):
     monkeypatch.setenv("DFLASH_FORCE_SIMT", "1")
