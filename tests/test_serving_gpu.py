@@ -380,9 +380,11 @@ def test_attn_paged_offsets_whose_difference_wraps(dfl, dtype, max_q):
                           out=out)
     assert dfl.dflash_last_device_error() == INVALID
     assert (out[2:] == 7).all()
-    want, _, size, _ = osv.attn_paged(_np(q)[:2], _np(kc), _np(vc), table, [60], off[:2], True)
-    # scores of 64 terms, the sums over 60 positions; bf16 weights
-    _within(out[:2], want, size * (2.0 ** -8 if dtype == "bf16" else 2.0 ** -18) + HALF[dtype] * np.abs(want))
+    want, _, size, score = osv.attn_paged(_np(q)[:2], _np(kc), _np(vc), table, [60], off[:2], True)
+    # as in _check_attn: scores of 64 terms, sums over 60 positions, bf16 weights
+    tol = size * (2 * (64 + 8) * U * score[..., None] + (60 + 64) * U + 2.0 ** -21 +
+                  (HALF[dtype] if dtype == "bf16" else 0.0))
+    _within(out[:2], want, tol + HALF[dtype] * np.abs(want))
 
 
 @pytest.mark.parametrize("kv,n,P,Hq,Hkv,D", ATTN[3:8])
