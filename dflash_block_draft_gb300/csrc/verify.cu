@@ -144,7 +144,8 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
   const float sample = a.s[r];  // needed last, read while the offsets are
   const int n = t1 - t0;
   int* out = a.out + (long long)r * (a.max_draft + 1);
-  if (t0 < 0 || n < 0 || t1 > a.total || n > a.max_draft) {  // the same in every CTA of the cluster
+  // (t1 < t0 by itself: of offsets far apart the difference wraps); the same in every CTA of the cluster
+  if (t0 < 0 || t1 < t0 || t1 > a.total || n > a.max_draft) {
     if (rank == 0) {
       for (int j = threadIdx.x; j <= a.max_draft; j += kThreads) out[j] = -1;
       if (threadIdx.x == 0) {

@@ -596,6 +596,17 @@ def test_verify_bad_tokens_rows_and_offsets(dfl):
     assert acc.tolist() == [0, 0, 0] and (out == -1).all()
 
 
+def test_verify_offsets_whose_difference_wraps(dfl):
+    """-2^31 - (2^31 - 1) is 1 in 32 bits: such a request is recorded like every other bad one."""
+    rng = np.random.default_rng(15)
+    p, q, tok, off, u, s = _verify_case(rng, [3, 1, 1], 50, False)
+    out, acc = _run_verify(dfl, p, q, tok, np.array([0, 3, 2 ** 31 - 1, -2 ** 31]), u, s, 3)
+    assert dfl.dflash_last_device_error() == INVALID
+    want, wacc = osv.verify(p, q, tok, off[:2], u, s[:1], 3)
+    np.testing.assert_array_equal(out[0], want[0])
+    assert acc.tolist() == [wacc[0], 0, 0] and (out[1:] == -1).all()
+
+
 def test_verify_strided_rows(dfl):
     rng = np.random.default_rng(12)
     p, q, tok, off, u, s = _verify_case(rng, [5, 2, 8], 1000, False)
