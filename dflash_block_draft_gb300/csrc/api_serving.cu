@@ -304,7 +304,8 @@ dflash_status_t dflash_verify(const dflash_verify_dims_t* dims, const float* tar
                               dflash_stream_t stream) {
   if (!dims) return DFLASH_ERR_INVALID;
   if (dims->R < 0 || dims->V <= 0 || dims->total_draft < 0 || dims->max_draft < 0) return DFLASH_ERR_SHAPE;
-  if (dims->V > (1 << 30) || dims->R > (1 << 24)) return DFLASH_ERR_UNSUPPORTED;
+  // (the kernel's indexes along a row of out_tokens are 32 bits and go a block's width beyond it)
+  if (dims->V > (1 << 30) || dims->R > (1 << 24) || dims->max_draft > (1 << 30)) return DFLASH_ERR_UNSUPPORTED;
   VerifyArgs a;
   memset(&a, 0, sizeof a);
   a.ps = dims->target_stride ? dims->target_stride : dims->V;

@@ -469,7 +469,7 @@ typedef struct {
   int R;           /* requests */
   int V;           /* vocabulary */
   int total_draft; /* rows of the packed draft axis (>= draft_offsets[R]) */
-  int max_draft;   /* bound on every request's drafted tokens */
+  int max_draft;   /* bound on every request's drafted tokens, at most 2^30 */
   int64_t target_stride, draft_stride; /* elements from row to row; 0: V */
 } dflash_verify_dims_t;
 DFLASH_API dflash_status_t dflash_verify(const dflash_verify_dims_t* dims, const float* target_probs,

@@ -189,6 +189,12 @@ def test_verify_refusals(lib, dims, over, want):
     assert lib.dflash_verify(None, GOOD, GOOD, GOOD, GOOD, GOOD, GOOD, GOOD, GOOD, None) == INVALID
 
 
+@pytest.mark.parametrize("max_draft", [(1 << 30) + 1, 2 ** 31 - 256, 2 ** 31 - 1])
+def test_verify_refuses_bounds_that_32_bit_indexes_cannot_pass(lib, max_draft):
+    d = dfl._VerifyDims(2, 100, 4, max_draft, 0, 0)
+    assert lib.dflash_verify(d, GOOD, GOOD, GOOD, GOOD, GOOD, GOOD, GOOD, GOOD, None) == UNSUPPORTED
+
+
 def test_empty_calls_launch_nothing(lib):
     before = dfl.dflash_kernel_launches()
     assert lib.dflash_cache_append(_paged(R=0), _rope(), 0, *[None] * 3, 0, None, None, GOOD, *[None] * 6, None) == OK
