@@ -86,6 +86,8 @@ dflash_status_t check_paged(const dflash_paged_dims_t* d, dflash_dtype_t dtype) 
     return DFLASH_ERR_SHAPE;
   TRY(check_head(d->D));
   if (d->H_q > 65535) return DFLASH_ERR_UNSUPPORTED;
+  // the kernels' 32-bit indexes of requests go some strips beyond the last one
+  if (d->R > 1 << 30) return DFLASH_ERR_UNSUPPORTED;
   // positions and rows of a request have to fit the kernels' 32-bit row arithmetic
   if ((long long)d->max_pages * d->page_size >= (1ll << 31) - 1024) return DFLASH_ERR_UNSUPPORTED;
   if ((long long)d->max_q_len * (d->H_q / d->H_kv) >= (1ll << 31) - 1024) return DFLASH_ERR_UNSUPPORTED;

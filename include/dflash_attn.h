@@ -376,7 +376,7 @@ DFLASH_API dflash_status_t dflash_qk_norm_rope_backward(
  * were.  All int32, on the device.
  */
 typedef struct {
-  int R;                /* requests */
+  int R;                /* requests, at most 2^30 */
   int H_q, H_kv;        /* query and key/value heads; H_kv divides H_q */
   int D;                /* head dimension */
   int total_q;          /* rows of the packed token axis (>= q_offsets[R]) */

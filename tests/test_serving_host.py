@@ -195,6 +195,14 @@ def test_verify_refuses_bounds_that_32_bit_indexes_cannot_pass(lib, max_draft):
     assert lib.dflash_verify(d, GOOD, GOOD, GOOD, GOOD, GOOD, GOOD, GOOD, GOOD, None) == UNSUPPORTED
 
 
+@pytest.mark.parametrize("R", [(1 << 30) + 1, 2 ** 31 - 1])
+def test_paged_calls_refuse_requests_that_32_bit_indexes_cannot_pass(lib, R):
+    assert _attn(lib, _paged(R=R)) == UNSUPPORTED
+    assert lib.dflash_attn_paged_workspace_size(_paged(R=R), 0) == 0
+    assert lib.dflash_cache_append(_paged(R=R), _rope(), 0, GOOD, GOOD, GOOD, 0, GOOD, GOOD, GOOD, GOOD, GOOD, GOOD,
+                                   GOOD, GOOD, GOOD, None) == UNSUPPORTED
+
+
 def test_empty_calls_launch_nothing(lib):
     before = dfl.dflash_kernel_launches()
     assert lib.dflash_cache_append(_paged(R=0), _rope(), 0, *[None] * 3, 0, None, None, GOOD, *[None] * 6, None) == OK
