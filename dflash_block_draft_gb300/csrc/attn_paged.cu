@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(Simt<T, BM, DMAX>::kThreads, Simt<T, BM, DMAX>
       if (row >= nrow) continue;
       if (pc.slot < 0) {
         const int tok = (f0 + row) / a.G, head = pc.h * a.G + (f0 + row) % a.G;
-        const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
+        const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
         T* dst = static_cast<T*>(a.out) + ((long long)(pc.q.q0 + tok) * a.Hq + head) * D;
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(Simt<T, BM, DMAX>::kThreads, Simt<T, BM, DMAX>
           }
         if (a.lse && tx == 0)
           a.lse[(long long)head * a.total_q + pc.q.q0 + tok] =
-              l[i] > 0.f ? (m[i] + log2f(l[i])) * 0.6931471805599453f : -INFINITY;
+              l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * 0.6931471805599453f;
       } else {
         const long long at = (long long)pc.slot * a.rows + row;
 #pragma unroll
@@ -343,7 +343,9 @@ __device__ __forceinline__ void merge_pieces(const PagedArgs& a, int i0, int cou
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const float w = exp2f(ml[i].x - mm);
-    if (w > 0.f) {  // not a piece that does not exist, nor one that saw nothing
+    // not a piece that does not exist, saw nothing or vanishes beside the others; what is NaN (m
+    // infinite or l NaN, from scores that are no numbers) stays NaN
+    if (w != 0.f || ml[i].y != ml[i].y) {
       l = fmaf(w, ml[i].y, l);
 #pragma unroll
       for (int c = 0; c < CD; ++c) {
@@ -377,7 +379,7 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const __grid_constant_
     for (int i = 0; i < m.shared; i += kBatch) merge_pieces<kBatch, LANES>(a, i, m.shared, slot, lane, mx, l, o);
   }
   const int f = m.f0 + row, tok = f / a.G, head = m.head + f % a.G;
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
   T* dst = static_cast<T*>(a.out) + ((long long)(m.q0 + tok) * a.Hq + head) * a.D;
 #pragma unroll
   for (int c = 0; c < CD; ++c) {
@@ -396,7 +398,7 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const __grid_constant_
     }
   }
   if (a.lse && lane == 0)
-    a.lse[(long long)head * a.total_q + m.q0 + tok] = l > 0.f ? (mx + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    a.lse[(long long)head * a.total_q + m.q0 + tok] = l == 0.f ? -INFINITY : (mx + log2f(l)) * 0.6931471805599453f;
 }
 
 // Eight lanes a row for pairs of tensor-core row tiles (more than 128 rows): with a warp a

@@ -547,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int i = 0; i < 2; ++i) n_full[i] += had[i];
       ptx::tc_fence_after();
-      const float inv = pc.slot >= 0 ? 1.f : l > 0.f ? 1.f / l : 0.f;
+      const float inv = pc.slot >= 0 ? 1.f : l == 0.f ? 0.f : 1.f / l;
       w0 *= inv;
       w1 *= inv;
       if (warp_ok && (half ? had[1] : had[0])) {
@@ -596,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (row_ok && !(both && half == 1)) {
           if (pc.slot >= 0) a.part_ml[part] = make_float2(m, l);
           else if (a.lse)
-            a.lse[(long long)head * a.total_q + token] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+            a.lse[(long long)head * a.total_q + token] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
         }
       }
       if (both) {

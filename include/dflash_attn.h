@@ -419,7 +419,8 @@ DFLASH_API dflash_status_t dflash_cache_append(const dflash_paged_dims_t* dims, 
  * Query head h reads key/value head h / (H_q / H_kv).
  *   out(i,h) = sum_p softmax_p(q(i,h) . k(p) scale) v(p),  scale <= 0: D^-0.5
  *   q, out [total_q, H_q, D] contiguous; lse [H_q, total_q] fp32, optional.
- * A row that sees nothing gets out = 0 and lse = -inf.  Keys and values of the
+ * A row that sees nothing gets out = 0 and lse = -inf; one with a score that is
+ * NaN or +inf gets NaN in both, and no other row is touched by it.  Keys and values of the
  * positions p < L have to be finite; a page id outside [0, num_pages) is recorded
  * as DFLASH_ERR_INVALID and read as zeros.  A request whose offsets or length
  * are out of range (n < 0 or > max_q_len, L < 0 or > max_pages * page_size) is

@@ -387,6 +387,28 @@ def test_attn_paged_offsets_whose_difference_wraps(dfl, dtype, max_q):
     _within(out[:2], want, tol + HALF[dtype] * np.abs(want))
 
 
+@pytest.mark.parametrize("what", [float("nan"), float("inf")])
+@pytest.mark.parametrize("kv,n", [([20], [2]), ([20000], [2]), ([9000, 40], [70, 3])])
+@pytest.mark.parametrize("dtype,P", [("bf16", 16), ("bf16", 7), ("fp32", 16)])
+def test_attn_paged_a_query_that_is_no_number_shows(dfl, dtype, P, kv, n, what):
+    """Whether one CTA holds the row or several do: NaN in its results, and in no other row's.  (A component of
+    infinity meets keys of both signs, so its row has scores of both infinities.)"""
+    rng = np.random.default_rng(16)
+    kc, vc, table, off, T = _batch(rng, kv, n, P, 2, 64, dtype, pad=0)
+    q = _rand(rng, (T, 8, 64), dtype)
+    lse, bad_lse = (torch.empty((8, T), device="cuda") for _ in range(2))
+    args = (kc, vc, _i32(table), _i32(kv), _i32(off), max(n))
+    want = dfl.dflash_attn_paged(q, *args, lse=lse)
+    rows = torch.zeros((T, 8), dtype=torch.bool, device="cuda")
+    for t, h in ((1, 5), (T - 1, 0)):
+        q[t, h, 3] = what
+        rows[t, h] = True
+    out = dfl.dflash_attn_paged(q, *args, lse=bad_lse)
+    assert dfl.dflash_last_device_error() == 0
+    assert out[rows].isnan().all() and bad_lse[rows.t()].isnan().all()
+    assert torch.equal(out[~rows], want[~rows]) and torch.equal(bad_lse[~rows.t()], lse[~rows.t()])
+
+
 @pytest.mark.parametrize("kv,n,P,Hq,Hkv,D", ATTN[3:8])
 def test_attn_paged_bf16_on_the_cuda_cores(dfl, monkeypatch, kv, n, P, Hq, Hkv, D):
     monkeypatch.setenv("DFLASH_FORCE_SIMT", "1")
