@@ -128,14 +128,20 @@ struct Place {
   long long krow, vrow;
 };
 
-// The rest of token t's placement, request r and its length found; what has no place is recorded.
-__device__ __forceinline__ Place place_in(const RopeArgs& a, int t, int r, int len) {
+// The rest of token t's placement, where r is the last request to begin at or before it (negative:
+// none does) and len its length.  What has no place is recorded, but for tokens that no request
+// holds behind the last offset, `end`.
+__device__ __forceinline__ Place place_in(const RopeArgs& a, int t, int r, int len, int end) {
   Place pl = {0, 0, 0, 0};
+  if (r < 0) {
+    if (t < end) record_error(a.err, DFLASH_ERR_INVALID);
+    return pl;
+  }
   const int q0 = a.q_off[r], q1 = a.q_off[r + 1];
   const long long p = (long long)len - (q1 - q0) + (t - q0);
   if (q0 < 0 || q0 > t || q1 <= t || q1 > a.T || p < 0 || p >= (long long)a.max_pages * a.P ||
       (a.rot > 0 && p >= a.max_pos)) {
-    record_error(a.err, DFLASH_ERR_INVALID);
+    if (q1 > t || t < end) record_error(a.err, DFLASH_ERR_INVALID);
     return pl;
   }
   const int pp = (int)p, page = a.table[(long long)r * a.max_pages + pp / a.P];
@@ -149,6 +155,15 @@ __device__ __forceinline__ Place place_in(const RopeArgs& a, int t, int r, int l
   pl.krow = page * a.kps + row;
   pl.vrow = page * a.vps + row;
   return pl;
+}
+
+__device__ __forceinline__ bool disordered(const RopeArgs& a, int q0, int q1) { return q0 < 0 || q1 < q0 || q1 > a.T; }
+
+// Records offsets out of order, the grid's threads sharing the requests: where tokens are found
+// by search, nobody else looks at all of them.
+__device__ __forceinline__ void check_offsets(const RopeArgs& a) {
+  for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < a.R; i += (long long)gridDim.x * kThreads)
+    if (disordered(a, a.q_off[i], a.q_off[i + 1])) record_error(a.err, DFLASH_ERR_INVALID);
 }
 
 // Whole warp: lane i < n places token t0 + i (ok = 0 elsewhere).  The request of t0,
@@ -174,7 +189,7 @@ __device__ __forceinline__ Place place_tokens(const RopeArgs& a, long long t0, i
     const int c = __popc(__ballot_sync(0xffffffffu, next <= t0 + i));
     if (lane == i) r = min(lo + c, a.R - 1);
   }
-  if (lane < n && t < a.T && t < end) {
+  if (lane < n && t < a.T) {
     if (r - lo == 32) {
       int hi = a.R;
       while (hi - r > 1) {
@@ -183,7 +198,7 @@ __device__ __forceinline__ Place place_tokens(const RopeArgs& a, long long t0, i
         else hi = mid;
       }
     }
-    return place_in(a, (int)t, r, a.kv_lens[r]);
+    return place_in(a, (int)t, r, a.kv_lens[r], end);
   }
   return Place{0, 0, 0, 0};
 }
@@ -201,6 +216,7 @@ __device__ __forceinline__ Place place_claimed(const RopeArgs& a, long long t0, 
   __syncthreads();
   if (q1 > q0 && q1 > t0 && q0 < t0 + n)
     atomicMax(&claims[max((long long)q0, t0) - t0], (unsigned long long)(i + 1) << 32 | (unsigned)len);
+  if (have && disordered(a, q0, q1)) record_error(a.err, DFLASH_ERR_INVALID);
   __syncthreads();
   if (i >= 32) return Place{0, 0, 0, 0};
   unsigned long long c = i < n ? claims[i] : 0;
@@ -210,12 +226,8 @@ __device__ __forceinline__ Place place_claimed(const RopeArgs& a, long long t0, 
     if (i >= o) c = max(c, v);
   }
   const long long t = t0 + i;
-  if (i >= n || t >= a.T || t >= end) return Place{0, 0, 0, 0};
-  if (c == 0) {  // no request's
-    record_error(a.err, DFLASH_ERR_INVALID);
-    return Place{0, 0, 0, 0};
-  }
-  return place_in(a, (int)t, (int)(c >> 32) - 1, (int)(unsigned)c);
+  if (i >= n || t >= a.T) return Place{0, 0, 0, 0};
+  return place_in(a, (int)t, (int)(c >> 32) - 1, (int)(unsigned)c, end);
 }
 
 __device__ __forceinline__ Place place_position(const RopeArgs& a, int t) {
@@ -269,9 +281,12 @@ __global__ void __launch_bounds__(kThreads)
       __shared__ unsigned long long claims[PAGED ? kGroups : 1];
       const Place p = place_claimed(a, t0, kGroups, claims);
       if (threadIdx.x < kGroups) s_place[threadIdx.x] = p;
-    } else if (threadIdx.x < 32) {
-      const Place p = place_tokens(a, t0, kGroups);
-      if (lane32 < kGroups) s_place[lane32] = p;
+    } else {
+      if (threadIdx.x < 32) {
+        const Place p = place_tokens(a, t0, kGroups);
+        if (lane32 < kGroups) s_place[lane32] = p;
+      }
+      check_offsets(a);
     }
     __syncthreads();
     pl = s_place[group];
@@ -486,6 +501,7 @@ __global__ void __launch_bounds__(kThreads) rope_fwd_plain_kernel(const __grid_c
   float* y = rows[threadIdx.x >> 5];
   const int heads = a.Hq + (PAGED ? 2 : 1) * a.Hkv;
   const long long unit = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (PAGED) check_offsets(a);
   if (unit >= (long long)a.T * heads) return;
   const int t = (int)(unit / heads), h = (int)(unit % heads);
   Place pl;

@@ -401,7 +401,8 @@ typedef struct {
  * the page table, or whose page id is outside [0, num_pages), and every token
  * of a request whose offsets are not ascending within [0, total_q], is recorded
  * as DFLASH_ERR_INVALID and skipped (its cache and q_out rows stay as they
- * were).  Two tokens must not be given one cache row: requests may share pages
+ * were); where offsets descend, tokens of requests next to that may be skipped
+ * too.  Two tokens must not be given one cache row: requests may share pages
  * that only hold earlier positions.  max_q_len is not read.
  */
 DFLASH_API dflash_status_t dflash_cache_append(const dflash_paged_dims_t* dims, const dflash_rope_dims_t* rope,

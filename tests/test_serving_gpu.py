@@ -532,6 +532,28 @@ def test_cache_append_skips_and_records_what_has_no_place(dfl, D, rot):
     assert dfl.dflash_last_device_error() == INVALID and torch.equal(kc2, kc)
 
 
+@pytest.mark.parametrize("empty", [0, 300])
+@pytest.mark.parametrize("D,rot", [(64, 64), (24, 6)])
+def test_cache_append_last_request_out_of_order(dfl, D, rot, empty):
+    """The last offset lies below the one before it: that request is recorded, the others' tokens all enter the
+    cache.  With up to 256 requests, with more, and on the plain kernel."""
+    rng = np.random.default_rng(18)
+    n, kv = [0] * empty + [3, 6, 0], [0] * empty + [10, 10, 5]
+    kc, vc, table, off, T = _batch(rng, kv, n, 4, 1, D, "fp32", garbage=3.0, pad=2)
+    k, v, q = _rand(rng, (T, 1, D), "fp32"), _rand(rng, (T, 1, D), "fp32"), _rand(rng, (T, 2, D), "fp32")
+    got = []
+    for last in (9, 5):
+        c = kc.clone(), vc.clone(), torch.full((T, 2, D), 7.0, device="cuda")
+        off[-1] = last
+        dfl.dflash_cache_append(k, v, c[0], c[1], _i32(table), _i32(kv), _i32(off), q=q, cos_sin=_table(40, rot),
+                                q_out=c[2])
+        assert dfl.dflash_last_device_error() == (0 if last == 9 else INVALID)
+        got.append(c)
+    assert (got[0][2][9:] == 7).all() and not (got[0][2][:9] == 7).any()
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
 # ------------------------------------------------------------------ verify
 def _verify_case(rng, n, V, one_hot, sharp=2.0):
     off = np.concatenate([[0], np.cumsum(n)]).astype(np.int64)
