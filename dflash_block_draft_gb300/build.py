@@ -6,6 +6,10 @@ Each translation unit compiles in parallel; the link steps produce
 ``dflash_block_draft_gb300/_lib/libdflash_attn.so`` and, linked to it,
 ``_lib/_dflash_binding.so``.  Object files go to
 ``dflash_block_draft_gb300/_build/``.  Both are git-ignored.
+
+The library needs nvcc alone.  Where torch, Python's headers or the C++ compiler are
+missing, it is built without the binding, which is said on stderr; the serving
+operators' Python functions then raise, the C ABI is whole.
 """
 from __future__ import annotations
 
@@ -48,14 +52,28 @@ def _deps():
 
 def up_to_date() -> bool:
     newest = _deps()
-    return all(os.path.exists(p) and os.path.getmtime(p) >= newest for p in (LIB_PATH, BINDING_PATH))
+    need = [LIB_PATH] if binding_lacks() else [LIB_PATH, BINDING_PATH]
+    return all(os.path.exists(p) and os.path.getmtime(p) >= newest for p in need)
 
 
-def _torch_dir() -> str:
+def _torch_dir() -> str | None:
     spec = importlib.util.find_spec("torch")
-    if spec is None or not spec.submodule_search_locations:
-        raise RuntimeError("torch not found: the Python binding cannot be built")
-    return list(spec.submodule_search_locations)[0]
+    return list(spec.submodule_search_locations)[0] if spec and spec.submodule_search_locations else None
+
+
+def _cxx() -> str:
+    return os.environ.get("CXX", "g++")
+
+
+def binding_lacks() -> str | None:
+    """What the binding needs and this machine does not have, or None."""
+    if _torch_dir() is None:
+        return "torch"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "Python.h"
+    if shutil.which(_cxx().split()[0]) is None:
+        return f"the C++ compiler {_cxx()}"
+    return None
 
 
 def _run(cmd, what):
@@ -70,7 +88,7 @@ def _compile_binding() -> str:
     obj = os.path.join(OBJ_DIR, "binding.o")
     inc = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
            sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"), INCLUDE]
-    _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-w",
+    _run([*_cxx().split(), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-w",
           *[f"-I{d}" for d in inc], "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj], "g++ on binding.cpp")
     return obj
 
@@ -78,14 +96,14 @@ def _compile_binding() -> str:
 def _link_binding(obj: str) -> None:
     torch = os.path.join(_torch_dir(), "lib")
     tmp = BINDING_PATH + f".{os.getpid()}.tmp"
-    _run([os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, f"-L{LIB_DIR}", "-ldflash_attn", f"-L{torch}",
+    _run([*_cxx().split(), "-shared", "-o", tmp, obj, f"-L{LIB_DIR}", "-ldflash_attn", f"-L{torch}",
           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{torch}"],
          "link of the binding")
     os.replace(tmp, BINDING_PATH)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile and link the library if stale (or force).  Returns its path."""
+    """Compile and link the library and the binding if stale (or force).  Returns the library's path."""
     if not force and not extra_flags and up_to_date():
         return LIB_PATH
     os.makedirs(OBJ_DIR, exist_ok=True)
@@ -102,16 +120,25 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             sys.stderr.write(r.stdout + r.stderr)
         return obj
 
+    lacks = binding_lacks()
     with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES) + 1, os.cpu_count() or 4)) as ex:
-        binding = ex.submit(_compile_binding)
+        binding = None if lacks else ex.submit(_compile_binding)
         objs = list(ex.map(compile_one, SOURCES))
-        binding = binding.result()
     tmp = LIB_PATH + f".{os.getpid()}.tmp"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs, "-ldl", "-lrt",
            "-lpthread"]
     _run(cmd, "link")
     os.replace(tmp, LIB_PATH)
-    _link_binding(binding)
+    linked = False
+    try:
+        if lacks:
+            sys.stderr.write(f"{lacks} not found: built without the Python binding of the serving operators\n")
+        else:
+            _link_binding(binding.result())
+            linked = True
+    finally:
+        if not linked and os.path.exists(BINDING_PATH):
+            os.remove(BINDING_PATH)  # it speaks to an older library
     return LIB_PATH
 
 

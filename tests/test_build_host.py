@@ -1,0 +1,45 @@
+"""The build where parts of the machine are missing: the C library needs nvcc alone.
+A library of one small source stands in for the whole one."""
+import ctypes
+import os
+
+import pytest
+
+from dflash_block_draft_gb300 import build as dbuild
+
+
+@pytest.fixture
+def small(monkeypatch, tmp_path):
+    csrc = tmp_path / "csrc"
+    csrc.mkdir()
+    (csrc / "one.cu").write_text('extern "C" __attribute__((visibility("default"))) int one() { return 1; }\n')
+    (csrc / "binding.cpp").write_text("#error it does not compile\n")
+    lib = tmp_path / "lib"
+    lib.mkdir()
+    for name, value in dict(CSRC=str(csrc), SOURCES=["one.cu"], OBJ_DIR=str(tmp_path / "obj"), LIB_DIR=str(lib),
+                            LIB_PATH=str(lib / "libone.so"), BINDING_PATH=str(lib / "binding.so")).items():
+        monkeypatch.setattr(dbuild, name, value)
+    (lib / "binding.so").write_text("of an older build")
+    return dbuild
+
+
+@pytest.mark.parametrize("missing", ["torch", "headers", "compiler"])
+def test_the_library_builds_without_what_only_the_binding_needs(small, monkeypatch, capsys, tmp_path, missing):
+    if missing == "torch":
+        monkeypatch.setattr(small.importlib.util, "find_spec", lambda name: None)
+    elif missing == "headers":
+        monkeypatch.setattr(small.sysconfig, "get_paths", lambda: {"include": str(tmp_path)})
+    else:
+        monkeypatch.setenv("CXX", str(tmp_path / "no-such-compiler"))
+    assert not small.up_to_date() and small.build() == small.LIB_PATH
+    assert ctypes.CDLL(small.LIB_PATH).one() == 1
+    assert not os.path.exists(small.BINDING_PATH)  # the old one belongs to another library
+    assert "without the Python binding" in capsys.readouterr().err
+    assert small.up_to_date()
+
+
+def test_a_binding_that_does_not_compile_is_an_error_after_the_library(small):
+    with pytest.raises(RuntimeError, match="binding.cpp"):
+        small.build()
+    assert ctypes.CDLL(small.LIB_PATH).one() == 1
+    assert not os.path.exists(small.BINDING_PATH) and not small.up_to_date()
