@@ -50,10 +50,29 @@ def _deps():
     return max(os.path.getmtime(f) for f in files)
 
 
+def _compiled_against() -> str:
+    """The Python and torch that a binding compiled now fits (torch itself is not imported)."""
+    with open(os.path.join(_torch_dir(), "version.py")) as f:
+        return f"{sysconfig.get_config_var('SOABI')}\n{_torch_dir()}\n{f.read()}"
+
+
+def _stamp() -> str:
+    return os.path.join(OBJ_DIR, "binding.for")
+
+
+def _binding_fits() -> bool:
+    try:
+        with open(_stamp()) as f:
+            return f.read() == _compiled_against()
+    except OSError:
+        return False
+
+
 def up_to_date() -> bool:
     newest = _deps()
-    need = [LIB_PATH] if binding_lacks() else [LIB_PATH, BINDING_PATH]
-    return all(os.path.exists(p) and os.path.getmtime(p) >= newest for p in need)
+    lacks = binding_lacks()
+    need = [LIB_PATH] if lacks else [LIB_PATH, BINDING_PATH]
+    return all(os.path.exists(p) and os.path.getmtime(p) >= newest for p in need) and bool(lacks or _binding_fits())
 
 
 def _torch_dir() -> str | None:
@@ -100,6 +119,8 @@ def _link_binding(obj: str) -> None:
           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{torch}"],
          "link of the binding")
     os.replace(tmp, BINDING_PATH)
+    with open(_stamp(), "w") as f:
+        f.write(_compiled_against())
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:

@@ -43,3 +43,21 @@ def test_a_binding_that_does_not_compile_is_an_error_after_the_library(small):
         small.build()
     assert ctypes.CDLL(small.LIB_PATH).one() == 1
     assert not os.path.exists(small.BINDING_PATH) and not small.up_to_date()
+
+
+def test_a_binding_for_another_torch_is_stale(small, monkeypatch, tmp_path):
+    torch = tmp_path / "torch"
+    torch.mkdir()
+    (torch / "version.py").write_text("__version__ = '1'\n")
+    monkeypatch.setattr(small, "_torch_dir", lambda: str(torch))
+    monkeypatch.setattr(small, "_compile_binding", lambda: "binding.o")
+    run = small._run
+    monkeypatch.setattr(small, "_run", lambda cmd, what: (open(cmd[cmd.index("-o") + 1], "w").close()
+                                                          if what == "link of the binding" else run(cmd, what)))
+    assert not small.up_to_date()
+    small.build()
+    assert small.up_to_date()
+    (torch / "version.py").write_text("__version__ = '2'\n")
+    assert not small.up_to_date()
+    small.build()
+    assert small.up_to_date()
