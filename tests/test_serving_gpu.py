@@ -135,6 +135,45 @@ def test_qk_norm_rope_backward(dfl, T, Hq, Hkv, D, rot, inter, weighted, layout,
         assert (a is None and b is None) or torch.equal(a, b)
 
 
+# Calls large enough for the most heads a group (forward: 8 in bf16, 4 in fp32, for every two blocks an SM) and a
+# chunk (backward: 8 where the blocks still fill the grid, and more tokens than one walk of it), with head counts
+# that leave the last of them short.
+ROPE_LARGE = [
+    (2100, 28, 4, 128, 128, False, True, "qkv"),   # forward 8, backward 8 of 28 and of 4
+    (3300, 13, 5, 128, 64, True, True, "own"),     # forward 8 with 5 left, backward 8 with 5 left: an odd last pair
+    (4600, 13, 5, 64, 64, False, True, "qkv"),     # 8 lanes a head: forward 8, backward 4 with 1 left
+    (1700, 9, 3, 256, 256, False, True, "own"),    # 32 lanes a head: forward 8 with 1 left, backward 8
+    (1700, 9, 3, 128, 128, True, False, "qkv"),    # forward 4 with 1 left, without weights
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("T,Hq,Hkv,D,rot,inter,weighted,layout", ROPE_LARGE)
+def test_qk_norm_rope_large(dfl, T, Hq, Hkv, D, rot, inter, weighted, layout, dtype):
+    test_qk_norm_rope(dfl, T, Hq, Hkv, D, rot, inter, weighted, layout, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("T,Hq,Hkv,D,rot,inter,weighted,layout", ROPE_LARGE)
+def test_qk_norm_rope_backward_large(dfl, T, Hq, Hkv, D, rot, inter, weighted, layout, dtype):
+    test_qk_norm_rope_backward(dfl, T, Hq, Hkv, D, rot, inter, weighted, layout, dtype)
+
+
+@pytest.mark.parametrize("D,rot", [(128, 128), (24, 6)])
+def test_qk_norm_rope_backward_one_side_only(dfl, D, rot):
+    rng = np.random.default_rng(19)
+    q, k, (wq, wk), cs, pos = _rope_case(rng, 40, 8, 2, D, rot, True, "own", "bf16")
+    p, gq, gk = _i32(pos), _rand(rng, q.shape, "bf16"), _rand(rng, k.shape, "bf16")
+    both = dfl.dflash_qk_norm_rope_backward(q, k, p, cs, gq, gk, q_norm=wq, k_norm=wk)
+    only_q = dfl.dflash_qk_norm_rope_backward(q, None, p, cs, gq, None, q_norm=wq)
+    only_k = dfl.dflash_qk_norm_rope_backward(None, k, p, cs, None, gk, k_norm=wk)
+    assert only_q[1] is None and only_q[3] is None and only_k[0] is None and only_k[2] is None
+    assert torch.equal(only_q[0], both[0]) and torch.equal(only_k[1], both[1])
+    for x, w, g, dw, H in ((q, wq, gq, only_q[2], 8), (k, wk, gk, only_k[3], 2)):
+        _, _, ww, wsize = osv.norm_rope_backward(_np(x), _w(w), pos, _np(cs), 1e-6, False, _np(g))
+        _within(dw, ww, wsize * (40 * H + D + 32) * U, "dw")
+
+
 def test_qk_norm_rope_one_side_only_and_in_place(dfl):
     rng = np.random.default_rng(7)
     q, k, (wq, wk), cs, pos = _rope_case(rng, 40, 8, 2, 128, 128, True, "own", "bf16")
@@ -506,6 +545,18 @@ def test_cache_append(dfl, kv, n, P, Hq, Hkv, D, rot, inter, weighted, dtype, la
     assert torch.equal(kc2, k0) and torch.equal(vc2, v0)  # without queries: the same keys and values
 
 
+# As many heads a group as there are (bf16 8, fp32 4, for every two blocks an SM), the last group short.
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("kv,n,P,Hq,Hkv,D,rot,inter,weighted", [
+    ([460, 500, 3, 470, 500], [450, 500, 0, 440, 450], 16, 28, 4, 128, 128, False, True),
+    ([500] * 8, [445] * 8, 24, 15, 5, 64, 64, True, True),
+    ([9] * 300, [6] * 300, 8, 15, 5, 128, 64, False, True),       # more requests than threads
+    ([300, 400], [290, 390], 7, 9, 3, 256, 256, False, False),
+])
+def test_cache_append_large(dfl, kv, n, P, Hq, Hkv, D, rot, inter, weighted, dtype):
+    test_cache_append(dfl, kv, n, P, Hq, Hkv, D, rot, inter, weighted, dtype, "own")
+
+
 @pytest.mark.parametrize("D,rot", [(64, 64), (24, 6)])
 def test_cache_append_skips_and_records_what_has_no_place(dfl, D, rot):
     rng = np.random.default_rng(10)
@@ -638,6 +689,41 @@ def test_verify_bad_tokens_rows_and_offsets(dfl):
     out, acc = _run_verify(dfl, p, q, tok, np.array([0, 9, 4, 9]), u, s, 3)  # too many, fewer than none, too many
     assert dfl.dflash_last_device_error() == INVALID
     assert acc.tolist() == [0, 0, 0] and (out == -1).all()
+
+
+@pytest.mark.parametrize("one_hot", [False, True])
+@pytest.mark.parametrize("R,V", [(77, 5000), (77, 4099), (153, 2048), (153, 2047), (305, 1000), (305, 70000),
+                                 (305, 70003)])
+def test_verify_large_batches(dfl, R, V, one_hot):
+    """Clusters of 4, 2 and 1 CTAs (more than 76, 152 and 304 requests); above 65536 entries one CTA's warps hold
+    more than 32 times 256 and walk longer segments.  The tokens are those of every request by itself, with 8 CTAs."""
+    rng = np.random.default_rng(R + V)
+    n = [i % 2 if V > 10000 else i % 4 for i in range(R)]
+    off = np.concatenate([[0], np.cumsum(n)]).astype(np.int64)
+    T = int(off[-1])
+    p = rng.random((T + R, V), np.float32) ** 6
+    p /= p.sum(1, keepdims=True)
+    rows = np.concatenate([np.arange(off[r] + r, off[r + 1] + r) for r in range(R)]).astype(int)
+    q = p[rows] * (0.5 + rng.random((T, V), np.float32))
+    q /= q.sum(1, keepdims=True)
+    tok = q.argmax(1) if one_hot else (q.cumsum(1) < rng.random((T, 1), np.float32)).sum(1).clip(0, V - 1)
+    tok, q = tok.astype(np.int32), None if one_hot else q
+    u, s = rng.random(T, np.float32), rng.random(R, np.float32)
+    if one_hot:
+        u[::2] *= 2 / V  # the most likely token has about 7 / V: every other one is accepted
+    out, acc = _run_verify(dfl, p, q, tok, off, u, s, 4)
+    assert dfl.dflash_last_device_error() == 0
+    want, wacc = osv.verify(p, q, tok, off, u, s, 4)
+    np.testing.assert_array_equal(acc, wacc)
+    np.testing.assert_array_equal(out, want)
+    assert len(set(acc.tolist())) > 1
+    for r in range(0, R, 19):
+        d = slice(off[r], off[r + 1])
+        one, a = _run_verify(dfl, p[off[r] + r:off[r + 1] + r + 1], None if one_hot else q[d], tok[d],
+                             np.array([0, n[r]]), u[d], s[r:r + 1], 4)
+        np.testing.assert_array_equal(one[0], out[r])
+        assert a[0] == acc[r]
+    assert dfl.dflash_last_device_error() == 0
 
 
 def test_verify_offsets_whose_difference_wraps(dfl):
@@ -782,6 +868,27 @@ def test_two_streams_at_once(dfl):
     dfl.dflash_attn_paged(explicit.qo.copy_(explicit.q), explicit.kc.nan_to_num_(), explicit.vc.nan_to_num_(),
                           *explicit.i, explicit.n, causal=False, out=explicit.out, stream=torch.cuda.current_stream())
     torch.cuda.synchronize()
+
+
+def test_two_streams_at_once_record_nothing_and_a_given_stream_gives_the_same(dfl):
+    steps = [_Step(dfl, 40 + i, R=5) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in steps]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, st in zip(steps, streams):
+            with torch.cuda.stream(st):
+                s.run()
+    torch.cuda.synchronize()
+    assert dfl.dflash_last_device_error() == 0
+    for s, st in zip(steps, streams):
+        want = s.out.clone()
+        s.out.zero_()
+        torch.cuda.synchronize()
+        dfl.dflash_attn_paged(s.qo, s.kc, s.vc, *s.i, s.n, causal=False, out=s.out, workspace=s.ws, stream=st)
+        torch.cuda.synchronize()
+        assert torch.equal(s.out, want)
+        s.check()
+    assert dfl.dflash_last_device_error() == 0
 
 
 def test_a_call_on_a_given_stream_takes_its_memory_from_it(dfl):
