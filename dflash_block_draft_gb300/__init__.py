@@ -79,11 +79,12 @@ class _VerifyDims(ctypes.Structure):
 
 _lock = threading.Lock()
 _lib_handle = None
+_lib_path = None
 
 
 def load_library(path: str | None = None):
     """Load libdflash_attn.so (built by ``__graft_entry__.build()``); raises if absent."""
-    global _lib_handle
+    global _lib_handle, _lib_path
     if _lib_handle is not None:
         return _lib_handle
     with _lock:
@@ -142,7 +143,7 @@ def load_library(path: str | None = None):
         for name in ("dflash_attn_dense", "dflash_attn_anchored", "dflash_attn_ragged",
                      "dflash_build_schedule_host", "dflash_scan_mask", "dflash_last_device_error"):
             getattr(lib, name).restype = ctypes.c_int
-        _lib_handle = lib
+        _lib_handle, _lib_path = lib, os.path.realpath(p)
         return lib
 
 
@@ -434,13 +435,20 @@ _binding_handle = None
 
 
 def _binding():
-    """The compiled module of the serving step's calls (built with the library); raises if absent."""
+    """The compiled module of the serving step's calls (built with the library); raises if absent.
+
+    It is taken from the folder of the loaded library and links to the one there, so that all calls
+    share one library with one error word, wherever load_library() found it."""
     global _binding_handle
     if _binding_handle is None:
         import importlib.util
         _torch()
         load_library()
-        path = _build.BINDING_PATH
+        folder = os.path.dirname(_lib_path)
+        path = os.path.join(folder, os.path.basename(_build.BINDING_PATH))
+        beside = os.path.join(folder, os.path.basename(_build.LIB_PATH))
+        if os.path.exists(path) and not (os.path.exists(beside) and os.path.samefile(beside, _lib_path)):
+            raise RuntimeError(f"DFlash Python binding {path} belongs to {beside}, but {_lib_path} is loaded")
         if not os.path.exists(path):
             raise RuntimeError(f"DFlash Python binding not built ({path} missing): run "
                                "`python -c 'import __graft_entry__ as g; g.build()'`")

@@ -2,6 +2,9 @@
 A library of one small source stands in for the whole one."""
 import ctypes
 import os
+import shutil
+import subprocess
+import sys
 
 import pytest
 
@@ -61,3 +64,30 @@ def test_a_binding_for_another_torch_is_stale(small, monkeypatch, tmp_path):
     assert not small.up_to_date()
     small.build()
     assert small.up_to_date()
+
+
+@pytest.mark.parametrize("name,copied,want", [
+    ("libdflash_attn.so", True, "one library"),
+    ("libdflash_attn.so", False, "not built"),
+    ("other.so", True, "belongs to"),
+])
+def test_a_library_from_another_place_brings_its_own_binding(tmp_path, name, copied, want):
+    """load_library(path): the serving operators run in that library, not in a second one with an error word of
+    its own."""
+    pytest.importorskip("torch")
+    dbuild.build()
+    shutil.copy(dbuild.LIB_PATH, tmp_path / name)
+    if copied:
+        shutil.copy(dbuild.BINDING_PATH, tmp_path)
+    code = f"""
+import dflash_block_draft_gb300 as dfl
+dfl.load_library({str(tmp_path / name)!r})
+try:
+    dfl._binding()
+    maps = {{line.split()[-1] for line in open("/proc/self/maps") if "libdflash_attn" in line}}
+    print("one library" if maps == {{{str(tmp_path / name)!r}}} else maps)
+except RuntimeError as e:
+    print(e)
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=dbuild.ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and want in r.stdout, (r.stdout, r.stderr[-2000:])
