@@ -360,7 +360,7 @@ __device__ __forceinline__ void merge_pieces(const PagedArgs& a, int i0, int cou
 
 // Merges the pieces of the row tile that CTA blockIdx.x began and left cut.  LANES lanes take
 // a row, two pieces at a time or, of more than four (long contexts, few rows; whole
-// warps), eight: two memory latencies in all, the meta data's and the pieces'.
+// warps), eight, four where D > 128: two memory latencies in all, the meta data's and the pieces'.
 template <typename T, int LANES, int CD>
 __global__ void __launch_bounds__(128) paged_merge_kernel(const __grid_constant__ PagedArgs a) {
   const Meta m = a.meta[blockIdx.x];
@@ -372,11 +372,12 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const __grid_constant_
   float4 o[CD];
 #pragma unroll
   for (int c = 0; c < CD; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (LANES < 32 || m.shared <= 4) {
+  if (LANES < 32 || m.shared <= 4)
     for (int i = 0; i < m.shared; i += 2) merge_pieces<2, LANES>(a, i, m.shared, slot, lane, mx, l, o);
-  } else {
-    constexpr int kBatch = LANES < 32 ? 1 : CD == 1 ? 8 : 4;
-    for (int i = 0; i < m.shared; i += kBatch) merge_pieces<kBatch, LANES>(a, i, m.shared, slot, lane, mx, l, o);
+  if constexpr (LANES == 32) {
+    constexpr int kBatch = CD == 1 ? 8 : 4;
+    if (m.shared > 4)
+      for (int i = 0; i < m.shared; i += kBatch) merge_pieces<kBatch, LANES>(a, i, m.shared, slot, lane, mx, l, o);
   }
   const int f = m.f0 + row, tok = f / a.G, head = m.head + f % a.G;
   const float inv = l == 0.f ? 0.f : 1.f / l;
