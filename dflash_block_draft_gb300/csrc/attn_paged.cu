@@ -17,11 +17,14 @@
 // 128 where no request has more rows (single tokens and short blocks with few
 // heads a group, where 64-row tiles would multiply mostly padding; the smaller
 // CTAs also put more copies in flight): 6 requests of up to 16 tokens with 16 fp32
-// heads of 64, behind 300 to 4000 positions, take 29 us, 42 with 64-row tiles; 16
+// heads of 64, behind 300 to 4000 positions, take 30 us, 42 with 64-row tiles; 16
 // single tokens of 16 heads of 128 take 107 us (3.8 TB/s), 156 with them.  fp32 needs
 // 2 D multiply-adds for each row and 8 D bytes of a position, so it is bound by the
 // multiply-adds, and by the shared memory that feeds them, from a few rows on and
-// by memory below.
+// by memory below.  So are the bf16 shapes that come here: with D = 256 and 32 heads in 8
+// groups, 16 single tokens behind 1000 to 8000 positions take 176 us (68 to read the keys and
+// values), blocks of 16 tokens 766, and 512 tokens behind 8192 positions 3540, 40 TFLOP/s;
+// with D = 128 and pages of 7 the last two take 406 and 1850.
 #include <math.h>
 #include <stdlib.h>
 #include <string.h>

@@ -20,6 +20,11 @@
 //          up to 64 rows have two query buffers, so that the next one's queries are
 //          there in time.
 //
+// The form is the launch's, from the bound on the requests' tokens: beside a chunk, or
+// under a bound that is too loose, single tokens run as pairs whose second half is padding.
+// 63 single tokens behind 1000 to 8000 positions take 186 us, 233 with a bound of 2048; in one
+// call with 2048 tokens behind 8192 456 us, the two calls by themselves 186 and 238.
+//
 // Pages: a 128-position tile arrives as 128 / b boxes of b = gcd(page_size, 128)
 // positions, one TMA load for each box and 64 components, lane by lane; a tile may
 // so begin and end anywhere in a page.  Boxes of 8 positions of 128 components bring
@@ -40,7 +45,9 @@
 //
 // Roundings: S, the softmax's statistics and O are fp32; P is rounded to bf16, the type
 // that the MMA takes beside V, while its sum l is taken before that rounding; the
-// results are rounded once.
+// results are rounded once.  (Against 64 bits the results' error is 2.2e-3 to 2.4e-3 of their
+// size; rounding them alone makes 1.7e-3 of it.  With l from the rounded P it is 1.9e-3 where
+// few keys matter and no less elsewhere, and a chunk takes 946 us.)
 //
 // Measured with 32 query heads in 8 groups, D = 128 (a block of 16 tokens, 64 requests
 // of 1 to 33 thousand positions: 2.9 GB of keys and values): 432 to 443 us, 6.5 to

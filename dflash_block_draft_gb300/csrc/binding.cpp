@@ -2,8 +2,9 @@
 // calls the C ABI.
 //
 // These calls take a few microseconds on the device, and a checked call through
-// ctypes took 17 to 30 on the host (Grace); reading the tensors in C++ takes a
-// few.  Each function takes the arguments of its Python function in order, all of
+// ctypes took 17 to 34 on the host (Grace).  Reading the tensors in C++, rotation, append
+// and verification take 4 to 8; attention and the gradients, which allocate a workspace
+// besides their results, 16 to 24.  Each function takes the arguments of its Python function in order, all of
 // them, and returns the results, or the status as an int where it is not 0.
 #include <Python.h>
 

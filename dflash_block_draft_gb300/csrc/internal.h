@@ -127,7 +127,7 @@ struct RopeArgs {
   int R, P, max_pages, num_pages;
   // backward
   const void *dqo, *dko;
-  float* dw_part;         // [blocks, 2, D] partial norm gradients
+  float* dw_part;         // [blocks, D] partial norm gradients, each block's row one weight's
   unsigned* err;
 };
 cudaError_t launch_qk_norm_rope(const RopeArgs& a, bool bf16, bool paged, cudaStream_t stream);

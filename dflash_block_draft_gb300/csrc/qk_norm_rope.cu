@@ -16,8 +16,9 @@
 // 40 heads of 128: 518 us where the others take 116; backward 1949 and 183).
 //
 // Measured, bf16, heads of 128: forward of 32768 x 40 heads 116 us, 5.9 TB/s; backward
-// 183 us, 5.6 TB/s (a mix of reads and writes that a copy moves at 6.8); appending
-// 64 blocks of 16 tokens with their queries 6.5 us, 31000 tokens' keys and values
+// 183 us, 5.6 TB/s (a mix of reads and writes that a copy moves at 6.8); the same in
+// fp32 283 us, 4.8 TB/s, and 318, 6.4; appending
+// 64 blocks of 16 tokens with their queries 6.6 us, 31000 tokens' keys and values
 // 42 us, 6.0 TB/s.
 #include <float.h>
 #include <limits.h>
@@ -275,7 +276,7 @@ __global__ void __launch_bounds__(kThreads)
   }
   Place pl = {0, 0, 0, 0};
   if (PAGED) {
-    // (64 blocks of 16 tokens: 6.5 us, 6.8 by the search; 250 requests of 100 to 200 tokens 52.4
+    // (64 blocks of 16 tokens: 6.6 us, 6.8 by the search; 250 requests of 100 to 200 tokens 52.4
     // and 53.7)
     if (a.R <= kThreads) {
       __shared__ unsigned long long claims[PAGED ? kGroups : 1];
@@ -484,7 +485,7 @@ constexpr int kWarps = kThreads / 32;
 
 __device__ __forceinline__ float warp_sum(float v) { return group_sum<32>(v); }
 
-// Component d of the rotation of row y (shared memory), dir as in Rotor::apply.
+// Component d of row y (shared memory) rotated (dir = 1) or rotated back (dir = -1).
 __device__ __forceinline__ float turn_one(const RopeArgs& a, const float* y, const float* row, int d, float dir) {
   if (d >= a.rot) return y[d];
   const int h = a.rot >> 1;

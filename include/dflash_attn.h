@@ -331,7 +331,7 @@ typedef struct {
   int rot_dim;     /* rotated components of a head */
   int max_pos;     /* rows of cos_sin */
   int interleaved; /* 0: planes (i, i + rot_dim/2); 1: planes (2i, 2i + 1) */
-  float eps;       /* norm epsilon, >= 0 */
+  float eps;       /* norm epsilon, >= 0 (the gradients take one below 2^-126 for 2^-126) */
   int64_t q_stride, k_stride; /* elements from token to token of q and k; 0: contiguous */
 } dflash_rope_dims_t;
 
@@ -430,7 +430,10 @@ DFLASH_API dflash_status_t dflash_cache_append(const dflash_paged_dims_t* dims, 
  * H_q / H_kv <= 128 and page_size a multiple of 8 runs on the tensor cores;
  * everything else, and all fp32, on the CUDA-core kernel.  Work is dealt in
  * equal runs of key tiles to the SMs whatever the lengths, and the pieces of
- * divided rows are merged by a second kernel, in a fixed order.
+ * divided rows are merged by a second kernel, in a fixed order.  max_q_len also
+ * chooses the form of the tensor-core kernel: with a bound of more tokens than 128
+ * rows hold, single tokens take about a quarter longer, so that a batch of single
+ * tokens wants a bound of its own.
  *   workspace: >= dflash_attn_paged_workspace_size(dims, dtype) bytes, 256-byte
  *     aligned; its size does not depend on the lengths; needs no initialisation.
  */
