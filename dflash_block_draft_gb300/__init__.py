@@ -13,7 +13,9 @@ The functions carry the C names:
   dflash_attn_workspace_size, dflash_build_schedule_host, dflash_scan_mask,
   dflash_last_device_error, dflash_status_string,
   dflash_qk_norm_rope, dflash_qk_norm_rope_backward, dflash_cache_append,
-  dflash_attn_paged, dflash_verify.
+  dflash_attn_paged, dflash_verify, dflash_attn_tree, dflash_sample,
+  dflash_tree_accept, dflash_cache_compact, dflash_cache_copy,
+  dflash_pages_resize, dflash_pages_fork.
 """
 from __future__ import annotations
 
@@ -44,7 +46,9 @@ EXPORTS = ("dflash_attn_dense", "dflash_attn_anchored", "dflash_attn_ragged", "d
            "dflash_test_limit_tile_flags",
            "dflash_attn_latent_ragged", "dflash_attn_latent_workspace_size",
            "dflash_qk_norm_rope", "dflash_qk_norm_rope_workspace_size", "dflash_qk_norm_rope_backward",
-           "dflash_cache_append", "dflash_attn_paged", "dflash_attn_paged_workspace_size", "dflash_verify")
+           "dflash_cache_append", "dflash_attn_paged", "dflash_attn_paged_workspace_size", "dflash_verify",
+           "dflash_attn_tree", "dflash_sample", "dflash_tree_accept", "dflash_cache_compact", "dflash_cache_copy",
+           "dflash_pages_workspace_size", "dflash_pages_resize", "dflash_pages_fork")
 
 
 class DFlashError(RuntimeError):
@@ -75,6 +79,24 @@ class _PagedDims(ctypes.Structure):
 class _VerifyDims(ctypes.Structure):
     _fields_ = [("R", ctypes.c_int), ("V", ctypes.c_int), ("total_draft", ctypes.c_int),
                 ("max_draft", ctypes.c_int), ("target_stride", ctypes.c_int64), ("draft_stride", ctypes.c_int64)]
+
+
+class _SampleDims(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int), ("V", ctypes.c_int), ("logits_stride", ctypes.c_int64),
+                ("probs_stride", ctypes.c_int64)]
+
+
+class _AcceptDims(ctypes.Structure):
+    _fields_ = [("R", ctypes.c_int), ("total", ctypes.c_int), ("max_path", ctypes.c_int)]
+
+
+class _Layers(ctypes.Structure):
+    _fields_ = [("L", ctypes.c_int), ("k_layer_stride", ctypes.c_int64), ("v_layer_stride", ctypes.c_int64)]
+
+
+class _PoolDims(ctypes.Structure):
+    _fields_ = [("R", ctypes.c_int), ("max_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("num_pages", ctypes.c_int)]
 
 
 _lock = threading.Lock()
@@ -133,8 +155,20 @@ def load_library(path: str | None = None):
         lib.dflash_cache_append.argtypes = [PD, RD, I, P, P, P, L, P, P, P, P, P, P, P, P, P, P]
         lib.dflash_attn_paged.argtypes = [PD, I, P, P, P, P, P, P, I, F, P, P, P, S, P]
         lib.dflash_verify.argtypes = [VD, P, P, P, P, P, P, P, P, P]
+        SD, AD, LD, OD = (ctypes.POINTER(_SampleDims), ctypes.POINTER(_AcceptDims), ctypes.POINTER(_Layers),
+                          ctypes.POINTER(_PoolDims))
+        lib.dflash_attn_tree.argtypes = [PD, I, P, P, P, P, P, P, P, F, P, P, P, S, P]
+        lib.dflash_sample.argtypes = [SD, I, P, P, P, P, P, P, P, P, P]
+        lib.dflash_tree_accept.argtypes = [AD, P, P, P, P, P, P, P, P]
+        lib.dflash_cache_compact.argtypes = [PD, LD, I, P, P, P, P, I, P, P, P, P, P]
+        lib.dflash_cache_copy.argtypes = [PD, LD, I, I, P, P, P, P, P, P]
+        lib.dflash_pages_resize.argtypes = [OD, P, P, P, P, P, P, S, P]
+        lib.dflash_pages_fork.argtypes = [OD, P, P, I, P, P, P, P, P, P, P, P, S, P]
+        lib.dflash_pages_workspace_size.argtypes = [OD, I]
+        lib.dflash_pages_workspace_size.restype = S
         for name in ("dflash_qk_norm_rope", "dflash_qk_norm_rope_backward", "dflash_cache_append",
-                     "dflash_attn_paged", "dflash_verify"):
+                     "dflash_attn_paged", "dflash_verify", "dflash_attn_tree", "dflash_sample", "dflash_tree_accept",
+                     "dflash_cache_compact", "dflash_cache_copy", "dflash_pages_resize", "dflash_pages_fork"):
             getattr(lib, name).restype = ctypes.c_int
         lib.dflash_qk_norm_rope_workspace_size.argtypes = [RD]
         lib.dflash_qk_norm_rope_workspace_size.restype = S
@@ -529,6 +563,96 @@ def dflash_verify(target_probs, draft_probs, draft_tokens, draft_offsets, accept
                                                sample_u, max_draft, out_tokens, num_accepted, stream)
     if r.__class__ is int:
         raise DFlashError("dflash_verify", r)
+    return r
+
+
+def dflash_attn_tree(q, k_cache, v_cache, page_table, kv_lens, q_offsets, parents, max_q_len, out=None, lse=None,
+                     scale=0.0, workspace=None, stream=None):
+    """Attention of drafted trees: the new tokens of dflash_attn_paged are the nodes of a
+    tree, each behind its parent parents [total_q] int32 (index within the request; -1: a
+    root), and see the positions in front of the tree, themselves and their ancestors.
+    Workspace as dflash_attn_paged_workspace_size says."""
+    r = (_binding_handle or _binding()).attn_tree(q, k_cache, v_cache, page_table, kv_lens, q_offsets, parents,
+                                                  max_q_len, out, lse, scale, workspace, stream)
+    if r.__class__ is int:
+        raise DFlashError("dflash_attn_tree", r)
+    return r
+
+
+def dflash_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, probs=None, tokens=None,
+                  stream=None):
+    """A token [N] int32 of every row of logits [N,V] (bf16 or fp32, rows may be
+    strided) with given random numbers u [N] fp32 in [0, 1).  Per row, each optional:
+    temperature [N] fp32 (0: the most likely token), top_k [N] int32 (<= 0: all), top_p
+    [N] fp32 (>= 1: all), min_p [N] fp32 (<= 0: all), applied in this order.  Fills
+    probs [N,V] fp32 with the distributions drawn from, if given."""
+    r = (_binding_handle or _binding()).sample(logits, u, temperature, top_k, top_p, min_p, probs, tokens, stream)
+    if r.__class__ is int:
+        raise DFlashError("dflash_sample", r)
+    return r
+
+
+def dflash_tree_accept(sampled, tokens, parents, q_offsets, max_path, path=None, out_tokens=None, num_accepted=None,
+                       stream=None):
+    """Walks down every request's drafted tree (see dflash_attn_tree) from node 0 to the
+    first child whose tokens [total] entry is the node's sampled [total] one, and so on, over
+    at most max_path nodes.  Returns path [R,max_path] (the nodes, then -1),
+    out_tokens [R,max_path] (the sampled tokens along it, then -1) and num_accepted [R]."""
+    r = (_binding_handle or _binding()).tree_accept(sampled, tokens, parents, q_offsets, max_path, path, out_tokens,
+                                                    num_accepted, stream)
+    if r.__class__ is int:
+        raise DFlashError("dflash_tree_accept", r)
+    return r
+
+
+def dflash_cache_compact(k_cache, v_cache, page_table, kv_lens, q_offsets, path, num_accepted, new_lens=None,
+                         stream=None):
+    """Moves the accepted nodes' keys and values together: with b the position of request
+    r's first new token, position b + path[r, j] goes to b + j for j < num_accepted[r].
+    k_cache and v_cache [num_pages,page_size,H_kv,D], or with an axis of layers in front.
+    Returns the new lengths b + num_accepted."""
+    r = (_binding_handle or _binding()).cache_compact(k_cache, v_cache, page_table, kv_lens, q_offsets, path,
+                                                      num_accepted, new_lens, stream)
+    if r.__class__ is int:
+        raise DFlashError("dflash_cache_compact", r)
+    return r
+
+
+def dflash_cache_copy(k_cache, v_cache, src_pages, dst_pages, rows=None, stream=None):
+    """Copies the first rows [n] positions (None: all) of pages src_pages [n] to pages
+    dst_pages [n], int32; pairs with a -1 are left out.  Caches as for dflash_cache_compact."""
+    r = (_binding_handle or _binding()).cache_copy(k_cache, v_cache, src_pages, dst_pages, rows, stream)
+    if r is not None:
+        raise DFlashError("dflash_cache_copy", r)
+
+
+def dflash_pages_workspace_size(num_pages, items) -> int:
+    """Workspace bytes of dflash_pages_resize (items: rows of the page table) and dflash_pages_fork
+    (items: forks)."""
+    return int(load_library().dflash_pages_workspace_size(_PoolDims(0, 0, 1, int(num_pages)), int(items)))
+
+
+def dflash_pages_resize(page_table, old_lens, new_lens, refs, page_size, missing=None, workspace=None, stream=None):
+    """Gives back and takes pages so that row r of page_table [R,max_pages] holds
+    ceil(new_lens[r] / page_size) of them where it held ceil(old_lens[r] / page_size).
+    refs [num_pages] int32 counts the rows that hold a page, 0: free.  Returns
+    missing [1]: pages that could not be had (their entries are -1)."""
+    r = (_binding_handle or _binding()).pages_resize(page_table, old_lens, new_lens, refs, page_size, missing,
+                                                     workspace, stream)
+    if r.__class__ is int:
+        raise DFlashError("dflash_pages_resize", r)
+    return r
+
+
+def dflash_pages_fork(page_table, lens, src, dst, refs, page_size, copy_src=None, copy_dst=None, copy_rows=None,
+                      missing=None, workspace=None, stream=None):
+    """Forks rows src [n] of page_table into the empty rows dst [n]: whole pages are
+    shared, of the last one a page of its own is taken.  Updates lens [R]; returns
+    copy_src, copy_dst, copy_rows [n], for dflash_cache_copy, and missing [1]."""
+    r = (_binding_handle or _binding()).pages_fork(page_table, lens, src, dst, refs, page_size, copy_src, copy_dst,
+                                                   copy_rows, missing, workspace, stream)
+    if r.__class__ is int:
+        raise DFlashError("dflash_pages_fork", r)
     return r
 
 

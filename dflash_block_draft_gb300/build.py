@@ -32,7 +32,7 @@ BINDING_PATH = os.path.join(LIB_DIR, "_dflash_binding.so")
 
 SOURCES = ["api.cu", "attn_simt.cu", "attn_tc.cu", "mask_scan.cu", "dense_noalloc.cu",
            "attn_decode.cu", "attn_bwd.cu", "attn_bwd_tc.cu", "attn_latent.cu", "api_serving.cu", "qk_norm_rope.cu",
-           "attn_paged.cu", "attn_paged_tc.cu", "verify.cu"]
+           "attn_paged.cu", "attn_paged_tc.cu", "verify.cu", "sample.cu", "tree_accept.cu", "cache_move.cu", "pages.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
               "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]

@@ -1,6 +1,7 @@
 // api_serving.cu -- C ABI of the grouped-query draft's serving step: host
 // validation, workspace layout and dispatch of dflash_qk_norm_rope (+ backward),
-// dflash_cache_append, dflash_attn_paged and dflash_verify.
+// dflash_cache_append, dflash_attn_paged, dflash_attn_tree, dflash_verify, dflash_sample,
+// dflash_tree_accept, and of what moves and hands out the cache's pages.
 #include <math.h>
 #include <string.h>
 
@@ -110,6 +111,103 @@ dflash_status_t check_table(const dflash_paged_dims_t* d, const int32_t* table, 
 
 size_t paged_ws(const dflash_paged_dims_t* d, dflash_dtype_t dtype) {
   return paged_workspace_bytes(dtype == DFLASH_BF16, d->H_q, d->H_kv, d->D, d->max_q_len, d->page_size);
+}
+
+// Attention over the pages, of a tree where `tree` is set (parents is required then).
+dflash_status_t attend(const dflash_paged_dims_t* dims, dflash_dtype_t dtype, const void* q, const void* k_cache,
+                       const void* v_cache, const int32_t* page_table, const int32_t* kv_lens, const int32_t* q_offsets,
+                       bool tree, const int32_t* parents, int causal, float scale, void* out, float* lse,
+                       void* workspace, size_t ws_bytes, dflash_stream_t stream) {
+  TRY(check_paged(dims, dtype));
+  if (isnan(scale) || isinf(scale)) return DFLASH_ERR_INVALID;
+  if (dims->R == 0 || dims->total_q == 0) return DFLASH_OK;
+  if (dims->max_q_len == 0) return DFLASH_ERR_SHAPE;
+  if (!q || !out || (dims->num_pages > 0 && (!k_cache || !v_cache))) return DFLASH_ERR_INVALID;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(lse, 4))
+    return DFLASH_ERR_ALIGN;
+  TRY(check_table(dims, page_table, kv_lens, q_offsets));
+  if (tree) TRY(check_tensor(parents, 4));
+  TRY(check_ws(workspace, ws_bytes, paged_ws(dims, dtype)));
+  const long long page = (long long)dims->page_size * dims->H_kv * dims->D;
+  PagedArgs a;
+  memset(&a, 0, sizeof a);
+  a.q = q;
+  a.kc = k_cache;
+  a.vc = v_cache;
+  a.table = page_table;
+  a.kv_lens = kv_lens;
+  a.q_off = q_offsets;
+  a.out = out;
+  a.lse = lse;
+  a.R = dims->R;
+  a.Hq = dims->H_q;
+  a.Hkv = dims->H_kv;
+  a.G = dims->H_q / dims->H_kv;
+  a.D = dims->D;
+  a.total_q = dims->total_q;
+  a.max_q = dims->max_q_len;
+  a.num_pages = dims->num_pages;
+  a.P = dims->page_size;
+  a.max_pages = dims->max_pages;
+  a.kps = dims->k_page_stride ? dims->k_page_stride : page;
+  a.vps = dims->v_page_stride ? dims->v_page_stride : page;
+  a.causal = causal != 0;
+  a.parents = tree ? parents : nullptr;
+  a.scale_log2 = (float)((scale > 0.f ? (double)scale : 1.0 / sqrt((double)dims->D)) * 1.4426950408889634);
+  a.err = device_error_word();
+  a.wait_ns = wait_budget_ns();
+  a.stall_cta = stalled_cta();
+  return launched(launch_attn_paged(a, dtype == DFLASH_BF16, workspace, (cudaStream_t)stream));
+}
+
+// Layers of a cache: strides in 16-byte vectors, and the cache's pointers.
+struct Layers {
+  long long kps, vps, kls, vls;
+  int row;
+};
+dflash_status_t check_layers(const dflash_paged_dims_t* d, const dflash_layers_t* l, dflash_dtype_t dtype,
+                             const void* kc, const void* vc, Layers* out) {
+  if (!l) return DFLASH_ERR_INVALID;
+  if (l->L < 0) return DFLASH_ERR_SHAPE;
+  if (l->L > 32767) return DFLASH_ERR_UNSUPPORTED;
+  const long long vec = dtype == DFLASH_BF16 ? 8 : 4, row = (long long)d->H_kv * d->D, page = row * d->page_size;
+  const long long kps = d->k_page_stride ? d->k_page_stride : page, vps = d->v_page_stride ? d->v_page_stride : page;
+  if (row / vec >= 1 << 30 || (d->num_pages > 0 && page > (1ll << 60) / d->num_pages)) return DFLASH_ERR_UNSUPPORTED;
+  const long long k_all = d->num_pages > 0 ? (d->num_pages - 1) * kps + page : 0;
+  const long long v_all = d->num_pages > 0 ? (d->num_pages - 1) * vps + page : 0;
+  const long long kls = l->k_layer_stride ? l->k_layer_stride : d->num_pages * kps;
+  const long long vls = l->v_layer_stride ? l->v_layer_stride : d->num_pages * vps;
+  // layers may lie in one another's gaps between pages (one tensor's [pages, L, ...]), or one behind the other
+  const bool k_in = kls > 0 && kls >= page && (d->num_pages <= 1 || (l->L - 1) * kls + page <= kps);
+  const bool v_in = vls > 0 && vls >= page && (d->num_pages <= 1 || (l->L - 1) * vls + page <= vps);
+  if (kls < 0 || vls < 0 || (l->L > 1 && ((kls < k_all && !k_in) || (vls < v_all && !v_in)))) return DFLASH_ERR_SHAPE;
+  if (kls % vec != 0 || vls % vec != 0) return DFLASH_ERR_ALIGN;
+  if (l->L > 0 && (kls > (1ll << 60) / l->L || vls > (1ll << 60) / l->L)) return DFLASH_ERR_UNSUPPORTED;
+  if (d->num_pages > 0 && l->L > 0) {
+    if (!kc || !vc) return DFLASH_ERR_INVALID;
+    if (!aligned(kc, 16) || !aligned(vc, 16)) return DFLASH_ERR_ALIGN;
+  }
+  *out = Layers{kps / vec, vps / vec, kls / vec, vls / vec, (int)(row / vec)};
+  return DFLASH_OK;
+}
+
+dflash_status_t check_pool(const dflash_pool_dims_t* d, int items) {
+  if (!d) return DFLASH_ERR_INVALID;
+  if (d->R < 0 || d->max_pages < 0 || d->page_size <= 0 || d->num_pages < 0 || items < 0) return DFLASH_ERR_SHAPE;
+  if (d->R > DFLASH_POOL_MAX_ROWS || items > DFLASH_POOL_MAX_ROWS || d->num_pages > 1 << 30) return DFLASH_ERR_UNSUPPORTED;
+  if ((long long)d->R * d->max_pages >= 1ll << 31 || (long long)d->max_pages * d->page_size >= (1ll << 31) - 1024)
+    return DFLASH_ERR_UNSUPPORTED;
+  return DFLASH_OK;
+}
+dflash_status_t pool_args(const dflash_pool_dims_t* d, int items, int32_t* table, int32_t* refs, int32_t* missing,
+                          void* ws, size_t ws_bytes, PoolArgs* a) {
+  if (d->R > 0 && d->max_pages > 0) TRY(check_tensor(table, 4));
+  if (d->num_pages > 0) TRY(check_tensor(refs, 4));
+  TRY(check_tensor(missing, 4));
+  TRY(check_ws(ws, ws_bytes, pool_workspace_bytes(d->num_pages, items)));
+  *a = PoolArgs{table, refs, missing, static_cast<int32_t*>(ws), d->R, d->max_pages, d->page_size, d->num_pages,
+                aligned(refs, 16), device_error_word()};
+  return DFLASH_OK;
 }
 
 }  // namespace
@@ -260,44 +358,16 @@ dflash_status_t dflash_attn_paged(const dflash_paged_dims_t* dims, dflash_dtype_
                                   const void* k_cache, const void* v_cache, const int32_t* page_table,
                                   const int32_t* kv_lens, const int32_t* q_offsets, int causal, float scale, void* out,
                                   float* lse, void* workspace, size_t ws_bytes, dflash_stream_t stream) {
-  TRY(check_paged(dims, dtype));
-  if (isnan(scale) || isinf(scale)) return DFLASH_ERR_INVALID;
-  if (dims->R == 0 || dims->total_q == 0) return DFLASH_OK;
-  if (dims->max_q_len == 0) return DFLASH_ERR_SHAPE;
-  if (!q || !out || (dims->num_pages > 0 && (!k_cache || !v_cache))) return DFLASH_ERR_INVALID;
-  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(lse, 4))
-    return DFLASH_ERR_ALIGN;
-  TRY(check_table(dims, page_table, kv_lens, q_offsets));
-  TRY(check_ws(workspace, ws_bytes, paged_ws(dims, dtype)));
-  const long long page = (long long)dims->page_size * dims->H_kv * dims->D;
-  PagedArgs a;
-  memset(&a, 0, sizeof a);
-  a.q = q;
-  a.kc = k_cache;
-  a.vc = v_cache;
-  a.table = page_table;
-  a.kv_lens = kv_lens;
-  a.q_off = q_offsets;
-  a.out = out;
-  a.lse = lse;
-  a.R = dims->R;
-  a.Hq = dims->H_q;
-  a.Hkv = dims->H_kv;
-  a.G = dims->H_q / dims->H_kv;
-  a.D = dims->D;
-  a.total_q = dims->total_q;
-  a.max_q = dims->max_q_len;
-  a.num_pages = dims->num_pages;
-  a.P = dims->page_size;
-  a.max_pages = dims->max_pages;
-  a.kps = dims->k_page_stride ? dims->k_page_stride : page;
-  a.vps = dims->v_page_stride ? dims->v_page_stride : page;
-  a.causal = causal != 0;
-  a.scale_log2 = (float)((scale > 0.f ? (double)scale : 1.0 / sqrt((double)dims->D)) * 1.4426950408889634);
-  a.err = device_error_word();
-  a.wait_ns = wait_budget_ns();
-  a.stall_cta = stalled_cta();
-  return launched(launch_attn_paged(a, dtype == DFLASH_BF16, workspace, (cudaStream_t)stream));
+  return attend(dims, dtype, q, k_cache, v_cache, page_table, kv_lens, q_offsets, false, nullptr, causal, scale, out,
+                lse, workspace, ws_bytes, stream);
+}
+
+dflash_status_t dflash_attn_tree(const dflash_paged_dims_t* dims, dflash_dtype_t dtype, const void* q,
+                                 const void* k_cache, const void* v_cache, const int32_t* page_table,
+                                 const int32_t* kv_lens, const int32_t* q_offsets, const int32_t* parents, float scale,
+                                 void* out, float* lse, void* workspace, size_t ws_bytes, dflash_stream_t stream) {
+  return attend(dims, dtype, q, k_cache, v_cache, page_table, kv_lens, q_offsets, true, parents, 1, scale, out, lse,
+                workspace, ws_bytes, stream);
 }
 
 dflash_status_t dflash_verify(const dflash_verify_dims_t* dims, const float* target_probs, const float* draft_probs,
@@ -338,6 +408,131 @@ dflash_status_t dflash_verify(const dflash_verify_dims_t* dims, const float* tar
   a.max_draft = dims->max_draft;
   a.err = device_error_word();
   return launched(launch_verify(a, (cudaStream_t)stream));
+}
+
+dflash_status_t dflash_sample(const dflash_sample_dims_t* dims, dflash_dtype_t dtype, const void* logits,
+                              const float* u, const float* temperature, const int32_t* top_k, const float* top_p,
+                              const float* min_p, int32_t* tokens, float* probs, dflash_stream_t stream) {
+  TRY(check_dtype(dtype));
+  if (!dims) return DFLASH_ERR_INVALID;
+  if (dims->N < 0 || dims->V <= 0) return DFLASH_ERR_SHAPE;
+  if (dims->V > DFLASH_SAMPLE_MAX_V || dims->N > (1 << 24)) return DFLASH_ERR_UNSUPPORTED;
+  SampleArgs a;
+  memset(&a, 0, sizeof a);
+  a.xs = dims->logits_stride ? dims->logits_stride : dims->V;
+  a.ps = dims->probs_stride ? dims->probs_stride : dims->V;
+  if (a.xs < dims->V || a.ps < dims->V) return DFLASH_ERR_SHAPE;
+  if (dims->N == 0) return DFLASH_OK;
+  TRY(check_tensor(logits, dtype == DFLASH_BF16 ? 2 : 4));
+  TRY(check_tensor(u, 4));
+  TRY(check_tensor(tokens, 4));
+  if (!aligned(temperature, 4) || !aligned(top_k, 4) || !aligned(top_p, 4) || !aligned(min_p, 4) || !aligned(probs, 4))
+    return DFLASH_ERR_ALIGN;
+  a.x = logits;
+  a.u = u;
+  a.temp = temperature;
+  a.top_k = top_k;
+  a.top_p = top_p;
+  a.min_p = min_p;
+  a.tokens = tokens;
+  a.probs = probs;
+  a.N = dims->N;
+  a.V = dims->V;
+  a.err = device_error_word();
+  return launched(launch_sample(a, dtype == DFLASH_BF16, (cudaStream_t)stream));
+}
+
+dflash_status_t dflash_tree_accept(const dflash_accept_dims_t* dims, const int32_t* sampled, const int32_t* tokens,
+                                   const int32_t* parents, const int32_t* q_offsets, int32_t* path,
+                                   int32_t* out_tokens, int32_t* num_accepted, dflash_stream_t stream) {
+  if (!dims) return DFLASH_ERR_INVALID;
+  if (dims->R < 0 || dims->total < 0 || dims->max_path <= 0) return DFLASH_ERR_SHAPE;
+  if (dims->R > 1 << 30 || dims->max_path > 1 << 30) return DFLASH_ERR_UNSUPPORTED;
+  if (dims->R == 0) return DFLASH_OK;
+  if (dims->total > 0) {
+    TRY(check_tensor(sampled, 4));
+    TRY(check_tensor(tokens, 4));
+    TRY(check_tensor(parents, 4));
+  }
+  TRY(check_tensor(q_offsets, 4));
+  TRY(check_tensor(path, 4));
+  TRY(check_tensor(out_tokens, 4));
+  TRY(check_tensor(num_accepted, 4));
+  const AcceptArgs a = {sampled, tokens, parents, q_offsets, path, out_tokens, num_accepted,
+                        dims->R, dims->total, dims->max_path, device_error_word()};
+  return launched(launch_tree_accept(a, (cudaStream_t)stream));
+}
+
+dflash_status_t dflash_cache_compact(const dflash_paged_dims_t* dims, const dflash_layers_t* layers,
+                                     dflash_dtype_t dtype, const int32_t* page_table, const int32_t* kv_lens,
+                                     const int32_t* q_offsets, const int32_t* path, int max_path,
+                                     const int32_t* num_accepted, void* k_cache, void* v_cache, int32_t* new_lens,
+                                     dflash_stream_t stream) {
+  TRY(check_paged(dims, dtype));
+  Layers l;
+  TRY(check_layers(dims, layers, dtype, k_cache, v_cache, &l));
+  if (max_path <= 0) return DFLASH_ERR_SHAPE;
+  if (max_path > 1 << 30) return DFLASH_ERR_UNSUPPORTED;
+  if (dims->R == 0) return DFLASH_OK;
+  if (layers->L == 0) return DFLASH_ERR_SHAPE;  // the new lengths come from the layers' call
+  TRY(check_table(dims, page_table, kv_lens, q_offsets));
+  TRY(check_tensor(path, 4));
+  TRY(check_tensor(num_accepted, 4));
+  TRY(check_tensor(new_lens, 4));
+  if (new_lens == kv_lens) return DFLASH_ERR_INVALID;
+  const CompactArgs a = {k_cache, v_cache, page_table, kv_lens, q_offsets, path, num_accepted, new_lens,
+                         l.kps, l.vps, l.kls, l.vls, dims->R, dims->total_q, dims->page_size, dims->max_pages,
+                         dims->num_pages, max_path, layers->L, l.row, device_error_word()};
+  return launched(launch_cache_compact(a, (cudaStream_t)stream));
+}
+
+dflash_status_t dflash_cache_copy(const dflash_paged_dims_t* dims, const dflash_layers_t* layers,
+                                  dflash_dtype_t dtype, int n, const int32_t* src, const int32_t* dst,
+                                  const int32_t* rows, void* k_cache, void* v_cache, dflash_stream_t stream) {
+  TRY(check_paged(dims, dtype));
+  Layers l;
+  TRY(check_layers(dims, layers, dtype, k_cache, v_cache, &l));
+  if (n < 0) return DFLASH_ERR_SHAPE;
+  if (n > 1 << 30) return DFLASH_ERR_UNSUPPORTED;
+  if (n == 0 || layers->L == 0) return DFLASH_OK;
+  TRY(check_tensor(src, 4));
+  TRY(check_tensor(dst, 4));
+  if (!aligned(rows, 4)) return DFLASH_ERR_ALIGN;
+  const CopyArgs a = {k_cache, v_cache, src, dst, rows, l.kps, l.vps, l.kls, l.vls,
+                      n, dims->page_size, dims->num_pages, layers->L, l.row, device_error_word()};
+  return launched(launch_cache_copy(a, (cudaStream_t)stream));
+}
+
+size_t dflash_pages_workspace_size(const dflash_pool_dims_t* dims, int items) {
+  return check_pool(dims, items) == DFLASH_OK ? pool_workspace_bytes(dims->num_pages, items) : 0;
+}
+
+dflash_status_t dflash_pages_resize(const dflash_pool_dims_t* dims, int32_t* page_table, const int32_t* old_lens,
+                                    const int32_t* new_lens, int32_t* refs, int32_t* missing, void* workspace,
+                                    size_t ws_bytes, dflash_stream_t stream) {
+  TRY(check_pool(dims, 0));
+  PoolArgs a;
+  TRY(pool_args(dims, dims->R, page_table, refs, missing, workspace, ws_bytes, &a));
+  if (dims->R > 0) {
+    TRY(check_tensor(old_lens, 4));
+    TRY(check_tensor(new_lens, 4));
+  }
+  return launched(launch_pages_resize(a, old_lens, new_lens, (cudaStream_t)stream));
+}
+
+dflash_status_t dflash_pages_fork(const dflash_pool_dims_t* dims, int32_t* page_table, int32_t* lens, int n,
+                                  const int32_t* src, const int32_t* dst, int32_t* refs, int32_t* copy_src,
+                                  int32_t* copy_dst, int32_t* copy_rows, int32_t* missing, void* workspace,
+                                  size_t ws_bytes, dflash_stream_t stream) {
+  TRY(check_pool(dims, n));
+  PoolArgs a;
+  TRY(pool_args(dims, n, page_table, refs, missing, workspace, ws_bytes, &a));
+  if (dims->R > 0) TRY(check_tensor(lens, 4));
+  if (n > 0)
+    for (const int32_t* p : {src, dst, (const int32_t*)copy_src, (const int32_t*)copy_dst, (const int32_t*)copy_rows})
+      TRY(check_tensor(p, 4));
+  const ForkArgs f = {src, dst, lens, copy_src, copy_dst, copy_rows, n};
+  return launched(launch_pages_fork(a, f, (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -89,7 +89,7 @@ struct Simt {
   };
 };
 
-template <typename T, int BM, int DMAX>
+template <typename T, int BM, int DMAX, bool TREE>
 __global__ void __launch_bounds__(Simt<T, BM, DMAX>::kThreads, Simt<T, BM, DMAX>::kPerSm)
     paged_simt_kernel(const __grid_constant__ PagedArgs a) {
   using C = Simt<T, BM, DMAX>;
@@ -159,13 +159,14 @@ __global__ void __launch_bounds__(Simt<T, BM, DMAX>::kThreads, Simt<T, BM, DMAX>
       }
       *reinterpret_cast<float4*>(s.q + r * C::kQStride + c) = x;
     }
+    const int base = pc.q.kv - pc.q.n;  // position of the first new token
     int lim[4];
     float m[4], l[4];
     float2 o[4][NC / 2];  // in pairs of columns, for the packed multiply-adds
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int row = 4 * ty + i;
-      lim[i] = row >= nrow ? 0 : a.causal ? max(0, pc.q.kv - pc.q.n + (f0 + row) / a.G + 1) : pc.q.kv;
+      lim[i] = row >= nrow ? 0 : a.causal && !TREE ? max(0, base + (f0 + row) / a.G + 1) : pc.q.kv;
       m[i] = -INFINITY;
       l[i] = 0.f;
 #pragma unroll
@@ -211,9 +212,12 @@ __global__ void __launch_bounds__(Simt<T, BM, DMAX>::kThreads, Simt<T, BM, DMAX>
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           float mx = -INFINITY;
+          uint64_t vis[1] = {~0ull};
+          if (TREE && k0 + BN > base)  // new tokens lie in this tile
+            tree_bits<1>(a.parents + pc.q.q0, min((f0 + 4 * ty + i) / a.G, pc.q.n - 1), base - k0, vis);
 #pragma unroll
           for (int j = 0; j < CT; ++j) {
-            if (k0 + tx + TX * j >= lim[i]) x[i][j] = -INFINITY;
+            if (k0 + tx + TX * j >= lim[i] || (TREE && !((vis[0] >> (tx + TX * j)) & 1))) x[i][j] = -INFINITY;
             mx = fmaxf(mx, x[i][j]);
           }
 #pragma unroll
@@ -420,12 +424,12 @@ void run_merge(const PagedArgs& a, int grid, cudaStream_t s) {
   count_launch();
 }
 
-template <typename T, int BM, int DMAX>
+template <typename T, int BM, int DMAX, bool TREE>
 cudaError_t run_simt(const PagedArgs& a, int sms, int most, int* grid, cudaStream_t s) {
   using C = Simt<T, BM, DMAX>;
   const size_t smem = sizeof(typename C::Smem);
   static_assert(sizeof(typename C::Smem) <= 232448, "shared memory budget");
-  auto kernel = paged_simt_kernel<T, BM, DMAX>;
+  auto kernel = paged_simt_kernel<T, BM, DMAX, TREE>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   // as many CTAs an SM as fit, so that some copy while others multiply
@@ -437,11 +441,17 @@ cudaError_t run_simt(const PagedArgs& a, int sms, int most, int* grid, cudaStrea
   return cudaGetLastError();
 }
 
-template <typename T, int BM>
+template <typename T, int BM, bool TREE>
 cudaError_t pick_simt(const PagedArgs& a, int sms, int most, int* grid, cudaStream_t s) {
-  if (a.D <= 64) return run_simt<T, BM, 64>(a, sms, most, grid, s);
-  if (a.D <= 128) return run_simt<T, BM, 128>(a, sms, most, grid, s);
-  return run_simt<T, BM, 256>(a, sms, most, grid, s);
+  if (a.D <= 64) return run_simt<T, BM, 64, TREE>(a, sms, most, grid, s);
+  if (a.D <= 128) return run_simt<T, BM, 128, TREE>(a, sms, most, grid, s);
+  return run_simt<T, BM, 256, TREE>(a, sms, most, grid, s);
+}
+template <bool TREE>
+cudaError_t pick_simt(const PagedArgs& a, bool bf16, int sms, int most, int* grid, cudaStream_t s) {
+  if (a.rows == 16)
+    return bf16 ? pick_simt<__nv_bfloat16, 16, TREE>(a, sms, most, grid, s) : pick_simt<float, 16, TREE>(a, sms, most, grid, s);
+  return bf16 ? pick_simt<__nv_bfloat16, 64, TREE>(a, sms, most, grid, s) : pick_simt<float, 64, TREE>(a, sms, most, grid, s);
 }
 
 int simt_rows(int G, int max_q) { return (long long)G * max_q <= 16 ? 16 : 64; }
@@ -505,12 +515,7 @@ cudaError_t launch_attn_paged(PagedArgs a, bool bf16, void* ws, cudaStream_t str
     const int most = p.tc ? 2 * kSms : p.max_grid;
     if (p.tc) a.rows = 16;
     if (a.num_pages == 0) a.kc = a.vc = a.q;  // every copy is one of no bytes, from an address that exists
-    if (a.rows == 16)
-      e = bf16 ? pick_simt<__nv_bfloat16, 16>(a, sms, most, &grid, stream)
-               : pick_simt<float, 16>(a, sms, most, &grid, stream);
-    else
-      e = bf16 ? pick_simt<__nv_bfloat16, 64>(a, sms, most, &grid, stream)
-               : pick_simt<float, 64>(a, sms, most, &grid, stream);
+    e = a.parents ? pick_simt<true>(a, bf16, sms, most, &grid, stream) : pick_simt<false>(a, bf16, sms, most, &grid, stream);
   }
   if (e != cudaSuccess) return e;
   // (As a programmatic dependent launch the merge measured no faster, and 3 us slower with

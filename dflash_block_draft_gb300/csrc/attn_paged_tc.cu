@@ -167,7 +167,17 @@ __device__ __forceinline__ void hide64(float* x, int c0, int lim) {
   }
 }
 
-template <int NP, bool PAIR>
+// Hides the columns (64 from c0 on) whose bit of `vis` is not set.
+__device__ __forceinline__ void hide_bits(float* x, uint64_t vis) {
+  const uint32_t lo = (uint32_t)vis, hi = (uint32_t)(vis >> 32);
+#pragma unroll
+  for (int c = 0; c < 32; ++c) {
+    x[c] = (lo >> c) & 1u ? x[c] : -INFINITY;
+    x[32 + c] = (hi >> c) & 1u ? x[32 + c] : -INFINITY;
+  }
+}
+
+template <int NP, bool PAIR, bool TREE>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_tc_kernel(const __grid_constant__ TcPagedArgs ta, const __grid_constant__ CUtensorMap tmQ,
                     const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {
@@ -438,7 +448,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int f = pc.rt * a.rows + (PAIR ? half * tile_rows : 0) + row;  // row within (request, key/value head)
       const bool row_ok = row < tile_rows && f < pc.q.n * a.G;
       const int tok = f / a.G;
-      const int lim = !row_ok ? 0 : a.causal ? max(0, pc.q.kv - pc.q.n + tok + 1) : pc.q.kv;
+      const int base = pc.q.kv - pc.q.n;  // position of the first new token
+      const int lim = !row_ok ? 0 : a.causal && !TREE ? max(0, base + tok + 1) : pc.q.kv;
       const bool warp_ok = __any_sync(0xffffffffu, row_ok);
       float m_used = -INFINITY, l = 0.f;
       bool had[2] = {PAIR, PAIR};
@@ -466,6 +477,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           ptx::fence_proxy_async_smem();
         }
+        // TREE: what the row sees of a tile with new tokens in it, while S is on its way
+        const bool among_new = TREE && k0 + kBN > base;
+        uint64_t vis[2] = {0, 0};
+        if (among_new && row_ok) tree_bits<2>(a.parents + pc.q.q0, tok, base - k0, vis);
         if (!__all_sync(0xffffffffu, ctl.wait(C::S_FULL + half, mine & 1u))) {
           stop = true;
           break;
@@ -481,7 +496,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::tmem_ld32(s_col + 64u * hh, reinterpret_cast<uint32_t*>(x));
             ptx::tmem_ld32(s_col + 64u * hh + 32u, reinterpret_cast<uint32_t*>(x) + 32);
             ptx::tmem_wait_ld();
-            hide64(x, 64 * hh, lim - k0);
+            if (among_new) hide_bits(x, hh ? vis[1] : vis[0]);
+            else hide64(x, 64 * hh, lim - k0);
             const float mh = max64(x) * c2;
             const bool raise = mh > m_used + 8.0f;  // also when m is still -inf and this half sees a key
             const bool scale_o = raise && m_used != -INFINITY;
@@ -636,10 +652,10 @@ int gcd(int x, int y) {
   return x;
 }
 
-template <int NP, bool PAIR>
+template <int NP, bool PAIR, bool TREE>
 cudaError_t run_tc(const TcPagedArgs& ta, int grid, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                    cudaStream_t s) {
-  auto kernel = paged_tc_kernel<NP, PAIR>;
+  auto kernel = paged_tc_kernel<NP, PAIR, TREE>;
   // Once a device: the shared memory's size, and the registers.  The setmaxnreg
   // split assumes the kernel launches with exactly kLaunchRegs registers a thread;
   // any other count would make setmaxnreg.inc wait forever.
@@ -659,6 +675,13 @@ cudaError_t run_tc(const TcPagedArgs& ta, int grid, const CUtensorMap& q, const 
   kernel<<<grid, kThreads, Cfg<NP, PAIR>::kSmem, s>>>(ta, q, k, v);
   count_launch();
   return cudaGetLastError();
+}
+
+template <bool TREE>
+cudaError_t pick_tc(const TcPagedArgs& ta, bool pair, int grid, const CUtensorMap& q, const CUtensorMap& k,
+                    const CUtensorMap& v, cudaStream_t s) {
+  if (ta.a.D <= 64) return pair ? run_tc<1, true, TREE>(ta, grid, q, k, v, s) : run_tc<1, false, TREE>(ta, grid, q, k, v, s);
+  return pair ? run_tc<2, true, TREE>(ta, grid, q, k, v, s) : run_tc<2, false, TREE>(ta, grid, q, k, v, s);
 }
 
 }  // namespace
@@ -714,8 +737,7 @@ cudaError_t launch_paged_tc(const PagedArgs& a, int grid, cudaStream_t stream) {
     }
   }
   if (!ok) return cudaErrorInvalidValue;
-  if (a.D <= 64) return pair ? run_tc<1, true>(ta, grid, mq, mk, mv, stream) : run_tc<1, false>(ta, grid, mq, mk, mv, stream);
-  return pair ? run_tc<2, true>(ta, grid, mq, mk, mv, stream) : run_tc<2, false>(ta, grid, mq, mk, mv, stream);
+  return a.parents ? pick_tc<true>(ta, pair, grid, mq, mk, mv, stream) : pick_tc<false>(ta, pair, grid, mq, mk, mv, stream);
 }
 
 }  // namespace paged

@@ -397,32 +397,44 @@ PyObject* cache_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// Attention over the pages; parents is null for dflash_attn_paged.
+PyObject* attend(PyObject* const* a, PyObject* parents, PyObject* max_q_len, int causal, PyObject* const* rest) {
+  const at::Tensor& q = required(a[0], "q");
+  const at::ScalarType type = q.scalar_type();
+  const dflash_dtype_t code = code_of(type);
+  if (q.dim() != 3) refuse("q must be [total_q, H_q, D]");
+  const int dev = q.get_device();
+  Paged p = paged(a[1], a[2], a[3], a[4], a[5], dev, type);
+  const int64_t T = q.size(0), Hq = q.size(1);
+  const void* qp = flat(&q, "q", dev, type, {T, Hq, p.D});
+  const int32_t* up =
+      parents ? (const int32_t*)flat(&required(parents, "parents"), "parents", dev, at::kInt, {T}) : nullptr;
+  const On on(dev, rest[4]);
+  const at::Tensor out = given_or(rest[0], "out", q, {T, Hq, p.D}, type);
+  void* op = flat(&out, "out", dev, type, {T, Hq, p.D});
+  float* lse = (float*)flat(tensor(rest[1], "lse"), "lse", dev, at::kFloat, {Hq, T});
+  p.d.H_q = narrow(Hq);
+  p.d.total_q = narrow(T);
+  p.d.max_q_len = (int)integer(max_q_len);
+  const float scale = rest[2] == Py_None ? 0.f : real(rest[2]);
+  const size_t bytes = dflash_attn_paged_workspace_size(&p.d, code);
+  const Workspace ws = workspace(rest[3], bytes, q);
+  const dflash_status_t st =
+      parents ? dflash_attn_tree(&p.d, code, qp, p.kc, p.vc, p.table, p.lens, p.off, up, scale, op, lse, ws.ptr, bytes,
+                                 on.stream())
+              : dflash_attn_paged(&p.d, code, qp, p.kc, p.vc, p.table, p.lens, p.off, causal, scale, op, lse, ws.ptr,
+                                  bytes, on.stream());
+  return st ? status(st) : wrap(out);
+}
+
 // (q, k_cache, v_cache, page_table, kv_lens, q_offsets, max_q_len, causal, out, lse, scale, workspace, stream)
 PyObject* attn_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 13, [&]() -> PyObject* {
-    const at::Tensor& q = required(a[0], "q");
-    const at::ScalarType type = q.scalar_type();
-    const dflash_dtype_t code = code_of(type);
-    if (q.dim() != 3) refuse("q must be [total_q, H_q, D]");
-    const int dev = q.get_device();
-    Paged p = paged(a[1], a[2], a[3], a[4], a[5], dev, type);
-    const int64_t T = q.size(0), Hq = q.size(1);
-    const void* qp = flat(&q, "q", dev, type, {T, Hq, p.D});
-    const On on(dev, a[12]);
-    const at::Tensor out = given_or(a[8], "out", q, {T, Hq, p.D}, type);
-    void* op = flat(&out, "out", dev, type, {T, Hq, p.D});
-    float* lse = (float*)flat(tensor(a[9], "lse"), "lse", dev, at::kFloat, {Hq, T});
-    p.d.H_q = narrow(Hq);
-    p.d.total_q = narrow(T);
-    p.d.max_q_len = (int)integer(a[6]);
-    const int causal = truth(a[7]);
-    const float scale = a[10] == Py_None ? 0.f : real(a[10]);
-    const size_t bytes = dflash_attn_paged_workspace_size(&p.d, code);
-    const Workspace ws = workspace(a[11], bytes, q);
-    const dflash_status_t st = dflash_attn_paged(&p.d, code, qp, p.kc, p.vc, p.table, p.lens, p.off, causal, scale, op,
-                                                 lse, ws.ptr, bytes, on.stream());
-    return st ? status(st) : wrap(out);
-  });
+  return guarded(n, 13, [&]() -> PyObject* { return attend(a, nullptr, a[6], truth(a[7]), a + 8); });
+}
+
+// (q, k_cache, v_cache, page_table, kv_lens, q_offsets, parents, max_q_len, out, lse, scale, workspace, stream)
+PyObject* attn_tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 13, [&]() -> PyObject* { return attend(a, a[6], a[7], 1, a + 8); });
 }
 
 // (target_probs, draft_probs, draft_tokens, draft_offsets, accept_u, sample_u, max_draft, out_tokens, num_accepted, stream)
@@ -473,9 +485,228 @@ PyObject* verify(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// (logits, u, temperature, top_k, top_p, min_p, probs, tokens, stream)
+PyObject* sample(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 9, [&]() -> PyObject* {
+    const at::Tensor& x = required(a[0], "logits");
+    const at::ScalarType type = x.scalar_type();
+    const dflash_dtype_t code = code_of(type);
+    const int dev = x.get_device();
+    if (x.dim() != 2) refuse("logits must be [N, V]");
+    const int64_t N = x.size(0), V = x.size(1);
+    common(x, "logits", dev, type);
+    dflash_sample_dims_t d = {};
+    d.N = narrow(N);
+    d.V = narrow(V);
+    // rows of [N, V] that are each contiguous and do not overlap
+    auto rows = [&](const at::Tensor& t, const char* name) -> int64_t {
+      if (t.numel() > 0 && ((V > 1 && t.stride(1) != 1) || (N > 1 && t.stride(0) < V)))
+        refuse(std::string("the rows of ") + name + " must be contiguous and must not overlap");
+      return N > 1 && t.numel() > 0 ? t.stride(0) : 0;
+    };
+    d.logits_stride = rows(x, "logits");
+    const float* u = (const float*)flat(&required(a[1], "u"), "u", dev, at::kFloat, {N});
+    const float* t = (const float*)flat(tensor(a[2], "temperature"), "temperature", dev, at::kFloat, {N});
+    const int32_t* k = (const int32_t*)flat(tensor(a[3], "top_k"), "top_k", dev, at::kInt, {N});
+    const float* p = (const float*)flat(tensor(a[4], "top_p"), "top_p", dev, at::kFloat, {N});
+    const float* m = (const float*)flat(tensor(a[5], "min_p"), "min_p", dev, at::kFloat, {N});
+    float* probs = nullptr;
+    if (const at::Tensor* o = tensor(a[6], "probs")) {
+      common(*o, "probs", dev, at::kFloat);
+      shaped(*o, "probs", {N, V});
+      d.probs_stride = rows(*o, "probs");
+      probs = (float*)o->data_ptr();
+    }
+    const On on(dev, a[8]);
+    const at::Tensor tokens = given_or(a[7], "tokens", x, {N}, at::kInt);
+    int32_t* tp = (int32_t*)flat(&tokens, "tokens", dev, at::kInt, {N});
+    const dflash_status_t st = dflash_sample(&d, code, x.data_ptr(), u, t, k, p, m, tp, probs, on.stream());
+    return st ? status(st) : wrap(tokens);
+  });
+}
+
+// (sampled, tokens, parents, q_offsets, max_path, path, out_tokens, num_accepted, stream)
+PyObject* tree_accept(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 9, [&]() -> PyObject* {
+    const at::Tensor &smp = required(a[0], "sampled"), &off = required(a[3], "q_offsets");
+    if (smp.dim() != 1 || off.dim() != 1 || off.size(0) < 1) refuse("sampled must be [total] and q_offsets [R + 1]");
+    const int dev = smp.get_device();
+    const int64_t T = smp.size(0), R = off.size(0) - 1;
+    dflash_accept_dims_t d = {narrow(R), narrow(T), (int)integer(a[4])};
+    if (d.max_path <= 0) refuse("max_path must be positive");
+    const int64_t M = d.max_path;
+    const int32_t* sp = (const int32_t*)flat(&smp, "sampled", dev, at::kInt);
+    const int32_t* tp = (const int32_t*)flat(&required(a[1], "tokens"), "tokens", dev, at::kInt, {T});
+    const int32_t* up = (const int32_t*)flat(&required(a[2], "parents"), "parents", dev, at::kInt, {T});
+    const int32_t* fp = (const int32_t*)flat(&off, "q_offsets", dev, at::kInt);
+    const On on(dev, a[8]);
+    const at::Tensor path = given_or(a[5], "path", smp, {R, M}, at::kInt);
+    const at::Tensor out = given_or(a[6], "out_tokens", smp, {R, M}, at::kInt);
+    const at::Tensor count = given_or(a[7], "num_accepted", smp, {R}, at::kInt);
+    int32_t* pp = (int32_t*)flat(&path, "path", dev, at::kInt, {R, M});
+    int32_t* op = (int32_t*)flat(&out, "out_tokens", dev, at::kInt, {R, M});
+    int32_t* cp = (int32_t*)flat(&count, "num_accepted", dev, at::kInt, {R});
+    const dflash_status_t st = dflash_tree_accept(&d, sp, tp, up, fp, pp, op, cp, on.stream());
+    return st ? status(st) : tuple(path, out, count);
+  });
+}
+
+// A cache with or without an axis of layers in front.
+struct Cache {
+  void *kc, *vc;
+  int64_t R;
+  at::ScalarType type;
+  int dev;
+  dflash_paged_dims_t d;
+  dflash_layers_t l;
+};
+void* layered(const at::Tensor& t, const char* name, int dev, at::ScalarType type, at::IntArrayRef shape,
+              int64_t* page, int64_t* layer) {
+  if (t.sizes() != shape) refuse(std::string(name) + " must be " + list(shape) + ", got " + list(t.sizes()));
+  if (t.dim() == 4) {
+    *layer = 0;
+    return pages(t, name, dev, type, shape, page);
+  }
+  *layer = t.size(0) > 1 && t.numel() > 0 ? t.stride(0) : 0;
+  if (t.size(0) == 0) {
+    common(t, name, dev, type);
+    *page = 0;
+    return t.data_ptr();
+  }
+  if (t.size(0) > 1 && t.numel() > 0 && t.stride(0) <= 0) refuse(std::string("the layers of ") + name + " must not overlap");
+  return pages(t.select(0, 0), name, dev, type, shape.slice(1), page);
+}
+Cache cache(PyObject* k_cache, PyObject* v_cache) {
+  Cache c = {};
+  const at::Tensor& k = required(k_cache, "k_cache");
+  if (k.dim() != 4 && k.dim() != 5)
+    refuse("k_cache and v_cache must be [num_pages, page_size, H_kv, D] or [L, num_pages, page_size, H_kv, D]");
+  c.type = k.scalar_type();
+  code_of(c.type);
+  c.dev = k.get_device();
+  c.kc = layered(k, "k_cache", c.dev, c.type, k.sizes(), &c.d.k_page_stride, &c.l.k_layer_stride);
+  c.vc = layered(required(v_cache, "v_cache"), "v_cache", c.dev, c.type, k.sizes(), &c.d.v_page_stride,
+                 &c.l.v_layer_stride);
+  const at::IntArrayRef s = k.sizes().slice(k.dim() - 4);
+  c.l.L = k.dim() == 5 ? narrow(k.size(0)) : 1;
+  c.d.num_pages = narrow(s[0]);
+  c.d.page_size = narrow(s[1]);
+  c.d.H_q = c.d.H_kv = narrow(s[2]);
+  c.d.D = narrow(s[3]);
+  return c;
+}
+
+// (k_cache, v_cache, page_table, kv_lens, q_offsets, path, num_accepted, new_lens, stream)
+PyObject* cache_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 9, [&]() -> PyObject* {
+    Cache c = cache(a[0], a[1]);
+    const at::Tensor &t = required(a[2], "page_table"), &lens = required(a[3], "kv_lens"), &path = required(a[5], "path");
+    if (t.dim() != 2 || path.dim() != 2) refuse("page_table must be [R, max_pages] and path [R, max_path]");
+    const int64_t R = t.size(0);
+    const int32_t* tp = (const int32_t*)flat(&t, "page_table", c.dev, at::kInt);
+    const int32_t* lp = (const int32_t*)flat(&lens, "kv_lens", c.dev, at::kInt, {R});
+    const int32_t* fp = (const int32_t*)flat(&required(a[4], "q_offsets"), "q_offsets", c.dev, at::kInt, {R + 1});
+    const int32_t* pp = (const int32_t*)flat(&path, "path", c.dev, at::kInt, {R, path.size(1)});
+    const int32_t* np = (const int32_t*)flat(&required(a[6], "num_accepted"), "num_accepted", c.dev, at::kInt, {R});
+    const On on(c.dev, a[8]);
+    const at::Tensor out = given_or(a[7], "new_lens", lens, {R}, at::kInt);
+    int32_t* op = (int32_t*)flat(&out, "new_lens", c.dev, at::kInt, {R});
+    if (R > 0 && op == lp) refuse("new_lens must not be kv_lens");
+    c.d.R = narrow(R);
+    c.d.max_pages = narrow(t.size(1));
+    c.d.total_q = INT32_MAX;  // the packed axis itself is not read
+    const dflash_status_t st = dflash_cache_compact(&c.d, &c.l, code_of(c.type), tp, lp, fp, pp, narrow(path.size(1)), np,
+                                                    c.kc, c.vc, op, on.stream());
+    return st ? status(st) : wrap(out);
+  });
+}
+
+// (k_cache, v_cache, src_pages, dst_pages, rows, stream)
+PyObject* cache_copy(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 6, [&]() -> PyObject* {
+    const Cache c = cache(a[0], a[1]);
+    const at::Tensor& src = required(a[2], "src_pages");
+    if (src.dim() != 1) refuse("src_pages must be [n]");
+    const int64_t N = src.size(0);
+    const int32_t* sp = (const int32_t*)flat(&src, "src_pages", c.dev, at::kInt);
+    const int32_t* dp = (const int32_t*)flat(&required(a[3], "dst_pages"), "dst_pages", c.dev, at::kInt, {N});
+    const int32_t* rp = (const int32_t*)flat(tensor(a[4], "rows"), "rows", c.dev, at::kInt, {N});
+    const On on(c.dev, a[5]);
+    const dflash_status_t st =
+        dflash_cache_copy(&c.d, &c.l, code_of(c.type), narrow(N), sp, dp, rp, c.kc, c.vc, on.stream());
+    return st ? status(st) : Py_NewRef(Py_None);
+  });
+}
+
+// A pool: page table and the pages' counts.
+struct Pool {
+  int32_t *table, *refs;
+  int dev;
+  dflash_pool_dims_t d;
+};
+Pool pool(PyObject* page_table, PyObject* refs, PyObject* page_size) {
+  Pool p = {};
+  const at::Tensor &t = required(page_table, "page_table"), &c = required(refs, "refs");
+  if (t.dim() != 2 || c.dim() != 1) refuse("page_table must be [R, max_pages] and refs [num_pages]");
+  p.dev = t.get_device();
+  p.table = (int32_t*)flat(&t, "page_table", p.dev, at::kInt);
+  p.refs = (int32_t*)flat(&c, "refs", p.dev, at::kInt);
+  p.d.R = narrow(t.size(0));
+  p.d.max_pages = narrow(t.size(1));
+  p.d.num_pages = narrow(c.size(0));
+  p.d.page_size = (int)integer(page_size);
+  return p;
+}
+
+// (page_table, old_lens, new_lens, refs, page_size, missing, workspace, stream)
+PyObject* pages_resize(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 8, [&]() -> PyObject* {
+    const Pool p = pool(a[0], a[3], a[4]);
+    const at::Tensor& old = required(a[1], "old_lens");
+    const int32_t* op = (const int32_t*)flat(&old, "old_lens", p.dev, at::kInt, {p.d.R});
+    const int32_t* np = (const int32_t*)flat(&required(a[2], "new_lens"), "new_lens", p.dev, at::kInt, {p.d.R});
+    const On on(p.dev, a[7]);
+    const at::Tensor missing = given_or(a[5], "missing", old, {1}, at::kInt);
+    int32_t* mp = (int32_t*)flat(&missing, "missing", p.dev, at::kInt, {1});
+    const size_t bytes = dflash_pages_workspace_size(&p.d, p.d.R);
+    const Workspace ws = workspace(a[6], bytes, old);
+    const dflash_status_t st = dflash_pages_resize(&p.d, p.table, op, np, p.refs, mp, ws.ptr, bytes, on.stream());
+    return st ? status(st) : wrap(missing);
+  });
+}
+
+// (page_table, lens, src, dst, refs, page_size, copy_src, copy_dst, copy_rows, missing, workspace, stream)
+PyObject* pages_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 12, [&]() -> PyObject* {
+    const Pool p = pool(a[0], a[4], a[5]);
+    const at::Tensor& src = required(a[2], "src");
+    if (src.dim() != 1) refuse("src must be [n]");
+    const int64_t N = src.size(0);
+    int32_t* lp = (int32_t*)flat(&required(a[1], "lens"), "lens", p.dev, at::kInt, {p.d.R});
+    const int32_t* sp = (const int32_t*)flat(&src, "src", p.dev, at::kInt);
+    const int32_t* dp = (const int32_t*)flat(&required(a[3], "dst"), "dst", p.dev, at::kInt, {N});
+    const On on(p.dev, a[11]);
+    at::Tensor out[3];
+    int32_t* op[3];
+    const char* names[3] = {"copy_src", "copy_dst", "copy_rows"};
+    for (int i = 0; i < 3; ++i) {
+      out[i] = given_or(a[6 + i], names[i], src, {N}, at::kInt);
+      op[i] = (int32_t*)flat(&out[i], names[i], p.dev, at::kInt, {N});
+    }
+    const at::Tensor missing = given_or(a[9], "missing", src, {1}, at::kInt);
+    int32_t* mp = (int32_t*)flat(&missing, "missing", p.dev, at::kInt, {1});
+    const size_t bytes = dflash_pages_workspace_size(&p.d, narrow(N));
+    const Workspace ws = workspace(a[10], bytes, src);
+    const dflash_status_t st = dflash_pages_fork(&p.d, p.table, lp, narrow(N), sp, dp, p.refs, op[0], op[1], op[2], mp,
+                                                 ws.ptr, bytes, on.stream());
+    return st ? status(st) : tuple(out[0], out[1], out[2], missing);
+  });
+}
+
 #define METHOD(f) {#f, (PyCFunction)(void (*)(void))f, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {METHOD(qk_norm_rope), METHOD(qk_norm_rope_backward), METHOD(cache_append), METHOD(attn_paged),
-                         METHOD(verify), {nullptr, nullptr, 0, nullptr}};
+                         METHOD(attn_tree), METHOD(verify), METHOD(sample), METHOD(tree_accept), METHOD(cache_compact),
+                         METHOD(cache_copy), METHOD(pages_resize), METHOD(pages_fork), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_dflash_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

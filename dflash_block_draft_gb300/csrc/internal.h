@@ -147,6 +147,7 @@ struct PagedArgs {
   int R, Hq, Hkv, G, D, total_q, max_q, num_pages, P, max_pages;
   long long kps, vps;     // elements from page to page
   int causal;
+  const int32_t* parents; // [total_q], a drafted tree's (causal is set then); nullable
   float scale_log2;       // scale * log2(e)
   int rows;               // rows (token, head of the group) of a row tile
   // workspace: partial results of row tiles that several CTAs share
@@ -171,6 +172,68 @@ struct VerifyArgs {
   unsigned* err;
 };
 cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t stream);
+
+// Tokens by temperature, top-k, top-p and min-p (sample.cu).
+struct SampleArgs {
+  const void* x;          // [N, V] logits, rows xs elements apart
+  const float *u, *temp, *top_p, *min_p;  // [N]; all but u nullable
+  const int32_t* top_k;   // [N], nullable
+  int32_t* tokens;
+  float* probs;           // [N, V], rows ps elements apart; nullable
+  long long xs, ps;
+  int N, V;
+  int chunk;              // logits a CTA holds
+  int probs_vec;          // rows of probs may be written in 16-byte pieces
+  unsigned* err;
+};
+cudaError_t launch_sample(SampleArgs a, bool bf16, cudaStream_t stream);
+
+// The walk down a drafted tree (tree_accept.cu).
+struct AcceptArgs {
+  const int32_t *sampled, *tokens, *parents, *offsets;
+  int32_t *path, *out, *count;
+  int R, total, max_path;
+  unsigned* err;
+};
+cudaError_t launch_tree_accept(const AcceptArgs& a, cudaStream_t stream);
+
+// Rows and pages moved within a paged cache (cache_move.cu).  Strides, and the size of a
+// position's row, in 16-byte vectors; the cache has `layers` layers kls / vls apart.
+struct CompactArgs {
+  void *kc, *vc;
+  const int32_t *table, *kv_lens, *q_off, *path, *count;
+  int32_t* new_lens;
+  long long kps, vps, kls, vls;
+  int R, total_q, P, max_pages, num_pages, max_path, layers, row;
+  unsigned* err;
+};
+cudaError_t launch_cache_compact(const CompactArgs& a, cudaStream_t stream);
+struct CopyArgs {
+  void *kc, *vc;
+  const int32_t *src, *dst, *rows;  // [n]; rows nullable: whole pages
+  long long kps, vps, kls, vls;
+  int n, P, num_pages, layers, row;
+  unsigned* err;
+};
+cudaError_t launch_cache_copy(const CopyArgs& a, cudaStream_t stream);
+
+// Pages taken, shared and given back (pages.cu).
+struct PoolArgs {
+  int32_t *table, *refs, *missing;
+  int32_t* ws;            // [num_pages + 2 * items]
+  int R, max_pages, P, num_pages;
+  int refs_vec;           // refs may be read in 16-byte pieces
+  unsigned* err;
+};
+struct ForkArgs {
+  const int32_t *src, *dst;
+  int32_t *lens, *copy_src, *copy_dst, *copy_rows;
+  int n;
+};
+size_t pool_workspace_bytes(int num_pages, int items);
+cudaError_t launch_pages_resize(const PoolArgs& a, const int32_t* old_lens, const int32_t* new_lens,
+                                cudaStream_t stream);
+cudaError_t launch_pages_fork(const PoolArgs& a, const ForkArgs& f, cudaStream_t stream);
 
 cudaError_t launch_build_mask(const int32_t* anchors, bool bf16, int B, int S, int Q, int nb, int bs, void* mask,
                               unsigned* err, cudaStream_t stream);

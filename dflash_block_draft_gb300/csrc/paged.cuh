@@ -85,6 +85,27 @@ __device__ __forceinline__ long long length_of(const PagedArgs& a, const Req& q,
   return m > full ? s + key_tiles<BN>(a, q, full) : s;
 }
 
+// What node `tok` of a tree sees of the 64 W positions from k0 on, `first` = (position of
+// node 0) - k0: the context in front of the tree, itself, and its chain of parents,
+// which is followed as far as the tile's beginning.  A parent that does not lie in front of
+// its node ends the chain, so that every chain ends.
+template <int W>
+__device__ __forceinline__ void tree_bits(const int32_t* __restrict__ parents, int tok, int first, uint64_t (&vis)[W]) {
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    const int c = first - 64 * w;  // context positions among these 64
+    vis[w] = c <= 0 ? 0ull : c >= 64 ? ~0ull : (1ull << c) - 1ull;
+  }
+  for (int j = tok; j >= 0 && first + j >= 0;) {
+    const int c = first + j;
+#pragma unroll
+    for (int w = 0; w < W; ++w)
+      if (c >> 6 == w) vis[w] |= 1ull << (c & 63);
+    const int up = __ldg(parents + j);
+    j = up < j ? up : -1;
+  }
+}
+
 // a / b for a >= 0, b > 0, in 32 bits where both fit (64-bit divisions are long).
 __device__ __forceinline__ long long quotient(long long a, long long b) {
   return (unsigned long long)(a | b) >> 32 ? a / b : (long long)((unsigned)a / (unsigned)b);

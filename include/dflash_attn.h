@@ -294,7 +294,14 @@ DFLASH_API dflash_status_t dflash_attn_dense_backward(const dflash_dims_t* dims,
  *   dflash_qk_norm_rope   norm and rotation of query and key heads (+ backward),
  *   dflash_cache_append   the same on the way into a paged cache,
  *   dflash_attn_paged     attention of the new tokens over the pages,
- *   dflash_verify         acceptance of drafted tokens.
+ *   dflash_verify         acceptance of drafted tokens;
+ * and where trees of tokens are drafted, or requests share their beginnings:
+ *   dflash_attn_tree      attention of a tree's nodes over the pages,
+ *   dflash_sample         tokens, or distributions, from logits,
+ *   dflash_tree_accept    the walk down the tree along the sampled tokens,
+ *   dflash_cache_compact  the accepted nodes moved together,
+ *   dflash_pages_resize, dflash_pages_fork, dflash_cache_copy
+ *                         pages taken, given back, shared and copied.
  * Element types, ownership, streams and errors as above.  The device that holds
  * the tensors has to be the current one.  Calls that may run at the same time
  * (on two streams, or in graphs that are replayed side by side) need a workspace
@@ -445,6 +452,28 @@ DFLASH_API dflash_status_t dflash_attn_paged(const dflash_paged_dims_t* dims, df
                                              dflash_stream_t stream);
 
 /*
+ * Attention of drafted trees over the pages.  A request's new tokens are the nodes
+ * of a tree, in an order in which every node comes behind its parent; they lie in
+ * the last n of its L = kv_lens[r] positions, node i at position L - n + i
+ * (what is rotated, if it is, is the depth: dflash_qk_norm_rope with positions
+ * L - n + depth, dflash_cache_append then without a rotation).  Node i sees the
+ * context p < L - n, itself, its parent, that one's parent and so on, and no other
+ * node.
+ *   parents [total_q] int32: index of the parent among the request's nodes, -1
+ *     for a root (there may be several).  A value that is not smaller than the
+ *     node's own index, or negative, ends the chain like -1.
+ * A node's chain is followed on the device, once for every 128 (or fewer) positions
+ * of the tree: deep trees of thousands of nodes are slow.  Everything else, the
+ * workspace and its size too, is as for dflash_attn_paged, whose causal form this
+ * is where every node's parent is the node before it.
+ */
+DFLASH_API dflash_status_t dflash_attn_tree(const dflash_paged_dims_t* dims, dflash_dtype_t dtype, const void* q,
+                                            const void* k_cache, const void* v_cache, const int32_t* page_table,
+                                            const int32_t* kv_lens, const int32_t* q_offsets, const int32_t* parents,
+                                            float scale, void* out, float* lse, void* workspace, size_t ws_bytes,
+                                            dflash_stream_t stream);
+
+/*
  * Verification of drafted tokens against the target's probabilities, with given
  * random numbers.  Request r drafted n = draft_offsets[r+1] - draft_offsets[r]
  * tokens x_0 .. x_{n-1} (possibly none).  With p_j the target's probabilities at
@@ -481,6 +510,155 @@ DFLASH_API dflash_status_t dflash_verify(const dflash_verify_dims_t* dims, const
                                          const float* draft_probs, const int32_t* draft_tokens,
                                          const int32_t* draft_offsets, const float* accept_u, const float* sample_u,
                                          int32_t* out_tokens, int32_t* num_accepted, dflash_stream_t stream);
+
+/*
+ * Tokens drawn from logits with given random numbers, and the distributions they are
+ * drawn from.  Row r with logits l, T = temperature[r], m = max l, w_i = exp((l_i - m) / T):
+ *   in the order of falling logits, equal ones by rising i,
+ *   K = the first top_k[r] tokens (all where that is <= 0 or >= V),
+ *   P = the shortest beginning of K whose weights reach top_p[r] times the weight of K
+ *       (one token at least; all of K where top_p[r] >= 1),
+ *   S = the tokens of P with w_i >= min_p[r] (<= 0: all; above 1 it counts as 1);
+ *   tokens[r] = smallest i in S such that the weights of S up to i exceed u[r] times
+ *               the weight of S (by rising i);
+ *   probs[r, i] = w_i / weight of S in S, 0 elsewhere.
+ * T = 0 takes the first of the largest logits (probs 1 there).  With probs as target_probs
+ * or draft_probs of dflash_verify blocks are verified against the filtered distribution.
+ *   logits [N, V] of dtype, rows logits_stride elements apart (0: V); u [N] fp32 in
+ *   [0, 1); temperature, top_p, min_p [N] fp32 and top_k [N] int32, each nullable (1, 1, 0, 0);
+ *   tokens [N] int32; probs [N, V] fp32, nullable, rows probs_stride elements apart (0: V).
+ * -inf (a masked token) and NaN are no choice; +inf counts as the largest finite value.
+ * A row without a choice, and one whose temperature is negative, infinite or NaN, is
+ * recorded as DFLASH_ERR_INVALID and gets token 0 and probs 0.  NaN in top_p or min_p
+ * leaves the filter out; a temperature below 2^-100 counts as 2^-100.
+ * Weights are held in steps of 2^-44 of the largest and added up as whole numbers: the
+ * result does not depend on the order of the sums (a w below 2^-45 counts as zero; its
+ * probability is still written).  V up to DFLASH_SAMPLE_MAX_V.
+ */
+#define DFLASH_SAMPLE_MAX_V 393216
+typedef struct {
+  int N;  /* rows */
+  int V;  /* vocabulary */
+  int64_t logits_stride, probs_stride; /* elements from row to row; 0: V */
+} dflash_sample_dims_t;
+DFLASH_API dflash_status_t dflash_sample(const dflash_sample_dims_t* dims, dflash_dtype_t dtype, const void* logits,
+                                         const float* u, const float* temperature, const int32_t* top_k,
+                                         const float* top_p, const float* min_p, int32_t* tokens, float* probs,
+                                         dflash_stream_t stream);
+
+/*
+ * The walk down a drafted tree.  Request r's nodes [q_offsets[r], q_offsets[r+1]) (see
+ * dflash_attn_tree; node 0, the last token that was accepted before, is accepted) carry
+ * tokens, and sampled[t] is the token drawn from the target's logits behind node t.  From
+ * node 0 on: of the current node's children the first one with tokens[child] =
+ * sampled[current] is accepted and becomes the current one; where there is none the walk
+ * ends, as it does with max_path nodes.
+ *   path [R, max_path]: the accepted nodes' indexes in the request, 0 first, then -1;
+ *   out_tokens [R, max_path]: sampled[] along the path, then -1: the accepted children's
+ *     tokens and behind them the new one;
+ *   num_accepted [R]: nodes of the path (0 for a request without nodes).
+ * A child has to come behind its parent; other entries of parents name no parent.  A
+ * request whose offsets are out of range or which has more than DFLASH_TREE_MAX_NODES
+ * nodes is recorded as DFLASH_ERR_INVALID and gets num_accepted = 0.
+ */
+#define DFLASH_TREE_MAX_NODES 4096
+typedef struct {
+  int R;         /* requests */
+  int total;     /* rows of the packed node axis (>= q_offsets[R]) */
+  int max_path;  /* columns of path and out_tokens */
+} dflash_accept_dims_t;
+DFLASH_API dflash_status_t dflash_tree_accept(const dflash_accept_dims_t* dims, const int32_t* sampled,
+                                              const int32_t* tokens, const int32_t* parents,
+                                              const int32_t* q_offsets, int32_t* path, int32_t* out_tokens,
+                                              int32_t* num_accepted, dflash_stream_t stream);
+
+/*
+ * Moving keys and values within a paged cache, in all layers at once: k_cache and
+ * v_cache [L, num_pages, page_size, H_kv, D], layers k_layer_stride / v_layer_stride elements
+ * apart (0: contiguous), all of one page table.
+ */
+typedef struct {
+  int L;  /* layers */
+  int64_t k_layer_stride, v_layer_stride; /* elements from layer to layer; 0: contiguous */
+} dflash_layers_t;
+
+/*
+ * The accepted nodes of a step moved together: with a = num_accepted[r] and L - n the
+ * position of the request's first new token, the keys and values of position
+ * L - n + path[r, j] go to position L - n + j, j < a, and new_lens[r] = L - n + a.
+ * (new_lens is not kv_lens: other caches are still to be moved by the old lengths.)
+ *   path [R, max_path]: rising indexes below n, as dflash_tree_accept writes them.
+ * A request whose offsets, length, count or path are out of range is recorded as
+ * DFLASH_ERR_INVALID and left as it is (new_lens = kv_lens); a row whose page id is out
+ * of range is recorded and not moved.  The positions moved must not lie in pages that
+ * other requests share.  H_q and max_q_len are not read.
+ */
+DFLASH_API dflash_status_t dflash_cache_compact(const dflash_paged_dims_t* dims, const dflash_layers_t* layers,
+                                                dflash_dtype_t dtype, const int32_t* page_table,
+                                                const int32_t* kv_lens, const int32_t* q_offsets, const int32_t* path,
+                                                int max_path, const int32_t* num_accepted, void* k_cache,
+                                                void* v_cache, int32_t* new_lens, dflash_stream_t stream);
+
+/*
+ * Pages copied: the first rows[i] positions (null: all) of page src[i] to page dst[i],
+ * i < n, as dflash_pages_fork asks for.  A pair with -1 in it is left out; one with another
+ * id outside [0, num_pages), or rows outside [0, page_size], is recorded as
+ * DFLASH_ERR_INVALID and left out.  A page is the dst of one pair at most, and then the
+ * src of none.  Of dims H_kv, D, num_pages, page_size and the page strides are read.
+ */
+DFLASH_API dflash_status_t dflash_cache_copy(const dflash_paged_dims_t* dims, const dflash_layers_t* layers,
+                                             dflash_dtype_t dtype, int n, const int32_t* src, const int32_t* dst,
+                                             const int32_t* rows, void* k_cache, void* v_cache,
+                                             dflash_stream_t stream);
+
+/*
+ * The pages of a cache handed out on the device.  refs [num_pages] int32 counts for every
+ * page the rows of page_table [R, max_pages] that hold it; a page with 0 is free.  (All 0
+ * and all lengths 0 at the beginning.)  Free pages are taken lowest first.
+ *   missing [1] int32: written; how many pages could not be had.  The table entries that
+ *     would have held them are -1, which giving them back passes over.
+ *   workspace: >= dflash_pages_workspace_size(dims, items) bytes, 256-byte aligned, with
+ *     items = R for dflash_pages_resize and the number of forks for dflash_pages_fork;
+ *     needs no initialisation.
+ * Calls on one pool must not run at the same time.  R and the number of forks up to
+ * DFLASH_POOL_MAX_ROWS, R * max_pages below 2^31.
+ */
+#define DFLASH_POOL_MAX_ROWS 65536
+typedef struct {
+  int R;          /* rows of the page table */
+  int max_pages;  /* its columns */
+  int page_size;  /* positions of a page */
+  int num_pages;  /* pages of the cache */
+} dflash_pool_dims_t;
+DFLASH_API size_t dflash_pages_workspace_size(const dflash_pool_dims_t* dims, int items);
+
+/*
+ * Requests made shorter or longer: row r holds ceil(old_lens[r] / page_size) pages and is
+ * to hold ceil(new_lens[r] / page_size).  All rows' pages that are too many are given back
+ * first (their entries become -1), then rows that need more take them, by rising r.  Length 0
+ * frees a request.  A request with a length outside [0, max_pages * page_size] is recorded
+ * as DFLASH_ERR_INVALID and left as it is; an entry that is given back and is no page, or a
+ * page that was free, is recorded.
+ */
+DFLASH_API dflash_status_t dflash_pages_resize(const dflash_pool_dims_t* dims, int32_t* page_table,
+                                               const int32_t* old_lens, const int32_t* new_lens, int32_t* refs,
+                                               int32_t* missing, void* workspace, size_t ws_bytes,
+                                               dflash_stream_t stream);
+
+/*
+ * Requests forked: row dst[i], which has to be empty (lens 0), gets lens[src[i]] positions of
+ * row src[i], i < n.  Whole pages are shared (their counts rise), for the rest in the
+ * last page a page is taken, in the order of i; copy_src[i], copy_dst[i] and copy_rows[i]
+ * say what dflash_cache_copy has to copy for it (-1, -1, 0 where the last page is whole).
+ * lens [R] is updated.  A row may be the source of many forks.  A fork whose row or source
+ * is out of range, whose row is not empty, is another fork's too or is some fork's source,
+ * is recorded as DFLASH_ERR_INVALID and left out (-1, -1, 0).  Positions in shared pages
+ * must not be written; a row is not shortened into them and then appended to.
+ */
+DFLASH_API dflash_status_t dflash_pages_fork(const dflash_pool_dims_t* dims, int32_t* page_table, int32_t* lens, int n,
+                                             const int32_t* src, const int32_t* dst, int32_t* refs, int32_t* copy_src,
+                                             int32_t* copy_dst, int32_t* copy_rows, int32_t* missing, void* workspace,
+                                             size_t ws_bytes, dflash_stream_t stream);
 
 /*
  * Workspace bytes a call needs.  For DENSE/ANCHORED (and their _BACKWARD
