@@ -22,14 +22,15 @@
 //   the kept weights' sums by runs of tokens, one exchange, and the run that passes u times
 //     the whole once more, a few tokens a thread.
 //
-// Weights are whole steps of 2^-44 of the largest one, added up as 64-bit integers, so that
-// no sum depends on the order, the number of CTAs or the threads' timing, and the cut and the
-// token are those of the real numbers unless a border lies within about 2^-38 of the
-// sum (fp32 sums would draw another token in every fiftieth row of a vocabulary of
-// 131072).  A weight costs 23 packed fp32 instructions for two tokens and about 15 integer
-// ones for each: l - m as two floats, times log2(e) / T as two floats; 2^y from a table of
-// 2^(j / 128) and a polynomial of degree 4, in fixed point from there on.  64-bit
-// floating point runs at a hundredth of that rate here.
+// Weights are whole steps of 2^-44 of the largest one, added up as integers, so that no sum
+// depends on the order, the number of CTAs or the threads' timing, and the cut and the token are
+// those of the real numbers unless a border lies within about 2^-40 of the sum (fp32 sums would
+// draw another token in every fiftieth row of a vocabulary of 131072).  A weight costs some 20
+// packed fp32 instructions and 9 others: l - m as two floats, times log2(e) / T as two floats;
+// 2^y from a table of 2^(j / 128) in two floats and a polynomial of degree 4; the bits of sums with
+// 2.5 and 1.5 2^-21 count the steps, as in verify.cu.  (In fixed point from the table on, with
+// 64-bit shifts, a row took twice as long, bound by the integer pipe.  64-bit floating point
+// runs at a hundredth of fp32's rate.)
 #include <cooperative_groups.h>
 #include <limits.h>
 #include <math.h>
@@ -39,6 +40,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace dflash {
 namespace {
@@ -48,32 +50,41 @@ typedef unsigned long long u64;
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBins = 2048;       // of a histogram: 4 a thread
+constexpr int kBins = 2048;       // of the masses: 4 a thread
+constexpr int kParts = 512;       // of a range whose border is looked for: one a thread
+constexpr int kPartBits = 9;
 constexpr int kList = 256;        // tokens whose order is found by comparing all pairs
+constexpr int kDirect = 160;      // top-k up to here: the tokens above the k-th of 512 groups' maxima, some 190, fit the list
 constexpr int kMaxCluster = 8;
 constexpr int kIndexBits = 19;    // of a token's number
 constexpr uint32_t kIndexMask = (1u << kIndexBits) - 1;
 constexpr int kChunkMax = 49152;  // logits a CTA can hold
 static_assert(DFLASH_SAMPLE_MAX_V <= kMaxCluster * kChunkMax && DFLASH_SAMPLE_MAX_V <= (int)kIndexMask + 1, "vocabulary");
-static_assert(kBins == 4 * kThreads && kThreads >= 2 * kList, "thread layout");
-constexpr float kTop = 3.402823466e+38f;  // the largest finite logit; +inf counts as that
+static_assert(kBins == 4 * kThreads && kParts == kThreads && kThreads >= 2 * kList, "thread layout");
+constexpr float kTop = 0x1p126f;  // logits above count as it, those below -kTop are no choice: differences are finite
+// Margin of the masses of top-p's first look: they are off by less than 6e-5 (bins linear within:
+// 2.9e-5, masses rounded down: 1.6e-5, fp32 distances and sums: 1e-5),
+// on either side of the comparison.
+constexpr float kOver = 1.0002f;
 
 // ------------------------------------------------------------------ weights
-// 2^(j / 128) in steps of 2^-45.
+// 2^(j / 128) as a float and what it lacks.
 struct Powers {
-  u64 at[128];
+  float hi[128], lo[128];
 };
 constexpr Powers make_powers() {
   Powers p = {};
   for (int j = 0; j < 128; ++j) {
-    // the series of e^x: its terms fall below 2^-60 of the sum
-    const long double x = 0.693147180559945309417232121458L * j / 128;
-    long double t = 1, s = 1;
-    for (int k = 1; k < 30; ++k) {
+    // the series of e^x, x = j ln 2 / 128, whose terms fall below 2^-60 of the sum; the 24 bits
+    // of hi leave 29 of the sum's 53 for lo
+    const double x = 0.69314718055994530942 * j / 128;
+    double t = 1, s = 0;
+    for (int k = 1; k < 25; ++k) {
       t = t * x / k;
       s += t;
     }
-    p.at[j] = (u64)(s * 35184372088832.0L + 0.5L);
+    p.hi[j] = (float)(1 + s);
+    p.lo[j] = (float)(s - ((double)p.hi[j] - 1));
   }
   return p;
 }
@@ -85,50 +96,68 @@ struct Scale {
 
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
-// From the bits of the three sums below: 2^y in steps of 2^-44, rounded, y = raw / 128 + z.
-__device__ __forceinline__ u64 power(const u64* tab, int raw, int zi, int rest) {
-  const u64 t = tab[raw & 127];
-  const int n = -(raw >> 7);
-  // 2^z - 1 in steps of 2^-39: z ln 2 exactly enough, and the rest of the series
-  const int s = (int)(((long long)zi * 1488522236) >> 16) + rest;  // (ln 2 * 2^31)
-  const u64 w = t + (u64)(((long long)(int)(t >> 15) * s) >> 24);
-  return ((w >> (n & 63)) + 1) >> 1;
-}
+// A weight in steps: hi of 2^-22, lo (signed) of 2^-44, or sums of them.
+struct Steps44 {
+  int hi, lo;
+  __device__ __forceinline__ u64 joined() const { return (u64)(((long long)hi << 22) + lo); }
+};
+constexpr float kHi = 2.5f, kLo = 0x1.8p-21f;  // sums with these have their last bits at 2^-22 and 2^-44
 
-// Weights of two logits.  What lies more than 45 powers of two below m, or is no number,
-// gives anything: the caller looks at the logit.
-__device__ __forceinline__ void weights(const Scale& c, const u64* tab, float2 l, u64& w0, u64& w1) {
+// Weights of two logits that are at most 45 powers of two below the largest one; 0 where !in.
+__device__ __forceinline__ void weights(const Scale& c, const float2* tab, float2 l, bool in0, bool in1, Steps44& w0,
+                                        Steps44& w1) {
   const float2 neg = both(-1.f), nm = both(-c.m), ch = both(c.ch);
+  l = make_float2(in0 ? l.x : c.m, in1 ? l.y : c.m);
   // l - m = d + err exactly (the two-sum of Moller and Knuth)
   const float2 d = __fadd2_rn(l, nm), bb = __ffma2_rn(l, neg, d);
   const float2 err = __fadd2_rn(__ffma2_rn(__ffma2_rn(bb, neg, d), neg, l), __ffma2_rn(bb, neg, nm));
   // y = -np + e
   const float2 np = __fmul2_rn(d, both(-c.ch));
   const float2 e = __ffma2_rn(err, ch, __ffma2_rn(d, both(c.cl), __ffma2_rn(d, ch, np)));
-  // whole steps of 1/128 by the adder's bits, and what remains, r = -rn
+  // whole steps of 1/128 by the adder's bits; y = (raw + r) / 128 + e with r = -rn, z = r + e
   const float big = 0x1.8p16f;
   const float2 t1 = __ffma2_rn(np, neg, both(big));
   const float2 rn = __fadd2_rn(np, __fadd2_rn(t1, both(-big)));
   const float2 z = __ffma2_rn(rn, neg, e);
-  // r in steps of 2^-24, and the tail
-  const float half = 0.75f;
-  const float2 t2 = __ffma2_rn(rn, neg, both(half));
-  const float2 tail = __ffma2_rn(__fadd2_rn(rn, __fadd2_rn(t2, both(-half))), neg, e);
-  // 2^z - 1 - r ln 2: the tail's part and z^2 (c2 + z (c3 + z c4)), in steps of 2^-39
-  const float tiny = 0x1.8p-16f;
-  const float2 q = __ffma2_rn(__ffma2_rn(z, both(9.618129107e-3f), both(5.550410867e-2f)), z, both(2.402265070e-1f));
-  const float2 t3 = __ffma2_rn(q, __fmul2_rn(z, z), __ffma2_rn(tail, both(0.6931471806f), both(tiny)));
-  const int b1 = __float_as_int(big), b2 = __float_as_int(half), b3 = __float_as_int(tiny);
-  w0 = power(tab, __float_as_int(t1.x) - b1, __float_as_int(t2.x) - b2, __float_as_int(t3.x) - b3);
-  w1 = power(tab, __float_as_int(t1.y) - b1, __float_as_int(t2.y) - b2, __float_as_int(t3.y) - b3);
+  const int raw0 = __float_as_int(t1.x) - __float_as_int(big), raw1 = __float_as_int(t1.y) - __float_as_int(big);
+  // 2^(raw / 128) = p (th + tl)
+  const float2 f0 = tab[raw0 & 127], f1 = tab[raw1 & 127];
+  const float2 th = make_float2(f0.x, f1.x), tl = make_float2(f0.y, f1.y);
+  const float2 p = make_float2(in0 ? __int_as_float((raw0 & ~127) * 65536 + 0x3F800000) : 0.f,
+                               in1 ? __int_as_float((raw1 & ~127) * 65536 + 0x3F800000) : 0.f);
+  // 2^z - 1 = a + b: r ln 2 in two floats, e ln 2, z^2 (c2 + z (c3 + z c4))
+  const float2 na = __fmul2_rn(rn, both(0.693147182f)), a = __fmul2_rn(rn, both(-0.693147182f));
+  float2 b = __ffma2_rn(rn, both(-0.693147182f), na);
+  b = __ffma2_rn(rn, both(1.90465421e-9f), b);  // (ln 2 = 0.693147182 - 1.9e-9)
+  b = __ffma2_rn(e, both(0.693147182f), b);
+  const float2 q = __ffma2_rn(__ffma2_rn(z, both(9.61812911e-3f), both(5.55041087e-2f)), z, both(0.240226507f));
+  b = __ffma2_rn(q, __fmul2_rn(z, z), b);
+  // (th + tl) (1 + a + b) = hi + lo
+  const float2 u = __fmul2_rn(th, a), hi = __fadd2_rn(th, u);
+  const float2 nu = __fmul2_rn(th, na);
+  float2 lo = __ffma2_rn(th, b, __ffma2_rn(tl, a, tl));
+  lo = __fadd2_rn(lo, __ffma2_rn(th, a, nu));
+  lo = __fadd2_rn(lo, __ffma2_rn(__ffma2_rn(th, neg, hi), neg, u));
+  const float2 h2 = __fadd2_rn(hi, lo);
+  lo = __ffma2_rn(__ffma2_rn(hi, neg, h2), neg, lo);
+  // in steps
+  const float2 hp = __fmul2_rn(h2, p), x = __fadd2_rn(hp, both(kHi));
+  const float2 left = __ffma2_rn(__fadd2_rn(x, both(-kHi)), neg, hp);
+  const float2 y = __fadd2_rn(__ffma2_rn(lo, p, left), both(kLo));
+  w0 = Steps44{__float_as_int(x.x) - __float_as_int(kHi), __float_as_int(y.x) - __float_as_int(kLo)};
+  w1 = Steps44{__float_as_int(x.y) - __float_as_int(kHi), __float_as_int(y.y) - __float_as_int(kLo)};
+}
+__device__ __forceinline__ u64 weight(const Scale& c, const float2* tab, float l, bool in) {
+  Steps44 w0, w1;
+  weights(c, tab, both(l), in, in, w0, w1);
+  return w0.joined();
 }
 
-// The weight as a float, for the distribution: 2^(fraction) times the power of two.
+// The weight as a float, for the distribution.
 __device__ __forceinline__ float weight_f32(const Scale& c, float l) {
-  const float d = l - c.m, p = d * c.ch;
-  const float n = rintf(p);
+  const float d = l - c.m, n = rintf(d * c.ch);
   const float f = fmaf(d, c.cl, fmaf(d, c.ch, -n));
-  return n < -140.f ? 0.f : ldexpf(exp2f(f), (int)n);
+  return n < -126.f ? 0.f : ptx::ex2(f) * __int_as_float(((int)n + 127) << 23);
 }
 
 // ------------------------------------------------------------------ order
@@ -155,57 +184,45 @@ template <typename T>
 struct Vec {
   static constexpr int N = 16 / sizeof(T);
 };
-// The N logits of one 16-byte vector.
-__device__ __forceinline__ void unpack(const uint4& v, float (&x)[4]) {
-  x[0] = __uint_as_float(v.x);
-  x[1] = __uint_as_float(v.y);
-  x[2] = __uint_as_float(v.z);
-  x[3] = __uint_as_float(v.w);
+// The larger of two, number for number (NaN loses), of what a 32-bit word holds.
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b, float) {
+  return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
 }
-__device__ __forceinline__ void unpack(const uint4& v, float (&x)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b, __nv_bfloat16) {
+  const __nv_bfloat162 m = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&m);
 }
-// NaN becomes -inf, +inf the largest finite value of the type.
-__device__ __forceinline__ uint32_t tidy(uint32_t w, float) {
-  return __float_as_uint(fminf(fmaxf(__uint_as_float(w), -INFINITY), kTop));
+template <typename T>
+__device__ __forceinline__ uint32_t largest(const uint4& v) {
+  return larger(larger(v.x, v.y, T()), larger(v.z, v.w, T()), T());
 }
-__device__ __forceinline__ uint32_t tidy(uint32_t w, __nv_bfloat16) {
-  __nv_bfloat162 x = *reinterpret_cast<__nv_bfloat162*>(&w);
-  const __nv_bfloat16 lo = __ushort_as_bfloat16(0xFF80), hi = __ushort_as_bfloat16(0x7F7F);
-  x = __hmin2(__hmax2(x, __nv_bfloat162(lo, lo)), __nv_bfloat162(hi, hi));
-  return *reinterpret_cast<uint32_t*>(&x);
+__device__ __forceinline__ float value_of(uint32_t w, float) { return __uint_as_float(w); }
+__device__ __forceinline__ float value_of(uint32_t w, __nv_bfloat16) {
+  return fmaxf(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
 
 struct Row {
   // what a CTA tells the others
-  float max, low;     // largest logit; smallest of the threads' maxima
-  int groups;         // threads that have logits
-  int best;           // the first token with the row's largest logit (greedy)
-  int listed;         // tokens of the range
-  uint32_t key_lo, key_hi;  // their keys
-  u64 sum;            // kept weights
+  float top[kThreads];             // largest logit of 1 to 8 neighbouring threads, 512 in the cluster
+  alignas(8) float2 low;           // smallest of the threads' maxima; threads that have logits
+  alignas(16) int4 listed;         // tokens of the range; the smallest and the largest of their keys
+  alignas(16) ulonglong2 weight;   // weights in front of the bracket, and all; kept weights
+  int best;                        // the first token with the row's largest logit (greedy)
   u64 list[kList];
+  alignas(16) uint32_t lo[kBins];  // counts, masses, or the weights' lower
+  uint32_t hi[kParts];             // and upper halves
   // its own
-  alignas(16) uint32_t lo[kBins];  // counts, or the weights' lower
-  alignas(16) uint32_t hi[kBins];  // and upper halves
-  u64 tab[128];
+  float2 tab[128];
   u64 scan[kWarps];
+  float scan_f[kWarps];
   u64 all[kList], all_w[kList];
-  float f[kWarps], g[kWarps];
+  uint32_t keys[kWarps], key;
   u64 found_before;
-  int found;
-  u64 cut;
+  int found, b1, b2;
+  u64 cut, bar;
   Scale scale;
-  float ends, least;  // no weight below `ends`; min-p's bound
-  double bar;
+  float ends, least, inv;  // no weight below `ends`; min-p's bound; 1 / kept weights
 };
-
-static_assert(offsetof(Row, lo) % 16 == 0 && offsetof(Row, hi) % 16 == 0, "histograms are read in 16-byte pieces");
 
 template <typename V>
 __device__ __forceinline__ V warp_sum(V v) {
@@ -214,214 +231,365 @@ __device__ __forceinline__ V warp_sum(V v) {
   return v;
 }
 
-// Exclusive sum over the block's threads; *total is the whole.
-__device__ __forceinline__ u64 block_scan(u64 v, u64* scratch, u64* total) {
+// The smallest value of the block's threads.
+__device__ __noinline__ uint32_t block_least(Row& s, uint32_t v) {
+  v = __reduce_min_sync(0xffffffffu, v);
+  __syncthreads();  // the values of an earlier call have been read
+  if ((threadIdx.x & 31) == 0) s.keys[threadIdx.x >> 5] = v;
+  __syncthreads();
+  return __reduce_min_sync(0xffffffffu, s.keys[threadIdx.x % kWarps]);
+}
+
+// Exclusive sum over the block's threads; *total is the whole.  (The kernel runs through most
+// of its code once a row: its size is time, so what is used in several places is called.)
+template <typename V>
+__device__ __noinline__ V block_scan(V v, V* scratch, V* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  u64 c = v;
+  V c = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const u64 u = __shfl_up_sync(0xffffffffu, c, o);
+    const V u = __shfl_up_sync(0xffffffffu, c, o);
     if (lane >= o) c += u;
   }
   __syncthreads();  // scratch of an earlier call has been read
   if (lane == 31) scratch[warp] = c;
   __syncthreads();
-  u64 before = 0, all = 0;
+  V w = lane < kWarps ? scratch[lane] : 0;
+  const V own = w;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    before += w < warp ? scratch[w] : 0;
-    all += scratch[w];
+  for (int o = 1; o < kWarps; o <<= 1) {
+    const V u = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += u;
   }
-  *total = all;
-  return before + c - v;
+  *total = __shfl_sync(0xffffffffu, w, kWarps - 1);
+  return __shfl_sync(0xffffffffu, w - own, warp) + c - v;
 }
 
+// The CTA's logits, 4 at a time.
 template <typename T>
 struct Pass {
-  static constexpr int N = Vec<T>::N;
-  const uint4* chunk;
+  T* chunk;
   int run;    // logits of a warp's run
   int first;  // number of the chunk's first token
-  // body(x, i): N logits, the first of which is token i's, for the whole warp at a time
+  __device__ __forceinline__ void load(int at, float (&x)[4]) const {
+    if constexpr (sizeof(T) == 4) {
+      const float4 v = *reinterpret_cast<const float4*>(chunk + at);
+      x[0] = v.x;
+      x[1] = v.y;
+      x[2] = v.z;
+      x[3] = v.w;
+    } else {
+      const uint2 v = *reinterpret_cast<const uint2*>(chunk + at);
+      x[0] = __uint_as_float(v.x << 16);
+      x[1] = __uint_as_float(v.x & 0xFFFF0000u);
+      x[2] = __uint_as_float(v.y << 16);
+      x[3] = __uint_as_float(v.y & 0xFFFF0000u);
+    }
+  }
+  __device__ __forceinline__ float logit(int at) const { return to_f32(chunk[at]); }
+  // body(x, at): the logits at .. at + 3 of the chunk, the whole warp together
   template <typename Body>
   __device__ __forceinline__ void each(Body body) const {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int k = lane * N; k < run; k += 32 * N) {
-      float x[N];
-      unpack(chunk[(warp * run + k) / N], x);
-      body(x, first + warp * run + k);
+    const int at = (threadIdx.x >> 5) * run + (threadIdx.x & 31) * 4;
+#pragma unroll 1
+    for (int k = 0; k < run; k += 128) {
+      float x[4];
+      load(at + k, x);
+      body(x, at + k);
     }
+  }
+  // body(l, at) for every logit that is `bound` at least: few of them
+  template <typename Body>
+  __device__ __forceinline__ void some(float bound, Body body) const {
+    const uint4* v = reinterpret_cast<const uint4*>(chunk + (threadIdx.x >> 5) * run) + (threadIdx.x & 31);
+#pragma unroll 2
+    for (int k = 0; k < run; k += 32 * Vec<T>::N, v += 32) {
+      if (value_of(largest<T>(*v), T()) >= bound) {
+        const int at = (int)(reinterpret_cast<const T*>(v) - chunk);
+        const uint32_t w[4] = {v->x, v->y, v->z, v->w};
+        unsigned mask = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (sizeof(T) == 4) {
+            mask |= (unsigned)(__uint_as_float(w[e]) >= bound) << e;
+          } else {
+            mask |= (unsigned)(__uint_as_float(w[e] << 16) >= bound) << (2 * e);
+            mask |= (unsigned)(__uint_as_float(w[e] & 0xFFFF0000u) >= bound) << (2 * e + 1);
+          }
+        }
+#pragma unroll 1
+        for (; mask; mask &= mask - 1) {
+          const int e = at + __ffs(mask) - 1;
+          body(logit(e), e);
+        }
+      }
+    }
+  }
+  // body(l, at) for every logit for which mask bit k of test(x, k): few of them
+  template <typename Test, typename Body>
+  __device__ __forceinline__ void where(Test test, Body body) const {
+    each([&](const float (&x)[4], int at) {
+      unsigned mask = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) mask |= (unsigned)test(x[k]) << k;
+#pragma unroll 1
+      for (; mask; mask &= mask - 1) {
+        const int k = at + __ffs(mask) - 1;
+        body(logit(k), k);
+      }
+    });
   }
 };
 
-// The cut of top-k (WEIGHTS false; target: k) or top-p (true; target from `share` of the
-// whole): the token of `prior`'s in which the running count or weight reaches the target.
-// The first division is by equal steps of the logit from m down to `bound`; without a
-// bound it is by the bits.  Returns prior where there are fewer tokens than k.
+// A logit's distance from the largest one in 2048 * 1024 steps of a range, by the adder's
+// bits.  Never falls as the logit falls.
+struct Steps {
+  float m, mul;
+  __device__ __forceinline__ Steps(float m_, float range) : m(m_), mul(0x1p21f / range) {}
+  __device__ __forceinline__ int at(float l) const {
+    return __float_as_int(fmaf(m - l, mul, 0x1.8p23f)) - __float_as_int(0x1.8p23f);
+  }
+};
+constexpr int kStepBits = 10;  // steps of a bin of the masses
+
+__device__ __forceinline__ void clear_list(Row& s) {
+  if (threadIdx.x == 0) s.listed = make_int4(0, -1, 0, 0);
+}
+// Puts a token into the CTA's list, as far as there is room, and its key into the thread's range.
+__device__ __forceinline__ void enlist(Row& s, float l, int i, uint32_t& klo, uint32_t& khi) {
+  const uint32_t key = key_of(l);
+  klo = min(klo, key);
+  khi = max(khi, key);
+  const int at = atomicAdd(&s.listed.x, 1);
+  if (at < kList) s.list[at] = place_of(key, i);
+}
+__device__ __forceinline__ void tell_keys(Row& s, uint32_t klo, uint32_t khi) {
+  klo = __reduce_min_sync(0xffffffffu, klo);
+  khi = __reduce_max_sync(0xffffffffu, khi);
+  if ((threadIdx.x & 31) == 0 && khi) {
+    atomicMin(reinterpret_cast<uint32_t*>(&s.listed.y), klo);
+    atomicMax(reinterpret_cast<uint32_t*>(&s.listed.z), khi);
+  }
+}
+// What a CTA of the cluster has at the place of `p`.
+template <typename V>
+__device__ __forceinline__ const V* peer(const V* p, int rank, int ranks) {
+  return ranks == 1 ? p : cg::this_cluster().map_shared_rank(p, rank);
+}
+// All CTAs' lists into s.all and their weights into s.all_w, if they are kList at most, and the
+// range of their keys.  Returns their number.  (After a cluster.sync; a block barrier follows.)
+__device__ __noinline__ int join_lists(Row& s, uint32_t* klo, uint32_t* khi) {
+  const int tid = threadIdx.x, lane = tid & 31, ranks = (int)cg::this_cluster().num_blocks();
+  int4 v = make_int4(0, -1, 0, 0);
+  if (lane < ranks) v = *peer(&s.listed, lane, ranks);
+  *klo = __reduce_min_sync(0xffffffffu, (uint32_t)v.y);
+  *khi = __reduce_max_sync(0xffffffffu, (uint32_t)v.z);
+  int upto = v.x;
+#pragma unroll
+  for (int o = 1; o < kMaxCluster; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += u;
+  }
+  const int n = __shfl_sync(0xffffffffu, upto, kMaxCluster - 1);
+  if (n <= kList) {
+    int owner = 0, before = 0;  // of entry tid
+#pragma unroll
+    for (int c = 0; c < kMaxCluster - 1; ++c) {
+      const int u = __shfl_sync(0xffffffffu, upto, c);
+      if (tid >= u) {
+        owner = c + 1;
+        before = u;
+      }
+    }
+    if (tid < n) {
+      const u64 p = peer(s.list, owner, ranks)[tid - before];
+      s.all[tid] = p;
+      const float l = logit_of((uint32_t)(p >> kIndexBits));
+      s.all_w[tid] = weight(s.scale, s.tab, l, l >= s.ends);
+    }
+  }
+  __syncthreads();
+  return n;
+}
+// For token i = tid / g of the n listed ones, g threads each (a power of two up to 32): how many
+// places of the list lie in front of its own, and their weight.
+__device__ __forceinline__ int group_of(int n) { return n <= 16 ? 32 : n <= 32 ? 16 : n <= 64 ? 8 : n <= 128 ? 4 : 2; }
+__device__ __noinline__ u64 in_front(const Row& s, int n, int g, int i, int* rank) {
+  u64 sum = 0;
+  int count = 0;
+  if (i < n) {
+    const u64 p = s.all[i];
+#pragma unroll 2
+    for (int j = threadIdx.x & (g - 1); j < n; j += g)
+      if (s.all[j] > p) {
+        sum += s.all_w[j];
+        ++count;
+      }
+  }
+  for (int o = g >> 1; o > 0; o >>= 1) {
+    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    count += __shfl_xor_sync(0xffffffffu, count, o);
+  }
+  *rank = count;
+  return sum;
+}
+__device__ __forceinline__ Cut cut_at(u64 place) {
+  return Cut{logit_of((uint32_t)(place >> kIndexBits)), (int)(kIndexMask - (uint32_t)(place & kIndexMask))};
+}
+
+// A condition that is the same all along a loop, tested where it stands: a copy of the loop for
+// either value would be read from memory on its only way through.
+__device__ __forceinline__ bool here(bool x) {
+  int y = x;
+  asm volatile("" : "+r"(y));
+  return y != 0;
+}
+
+// The cut of top-k (WEIGHTS false; target: k) or top-p (true): the token, of those that
+// `prior` keeps and that lie at or above `bound`, in which the running count or weight, `before` in
+// front of the range, reaches the target.  `linear`: the range is the logits whose step
+// lies in [q0, q0 + (512 << shift)), divided into 512 equal parts; else, and where
+// that leaves too many tokens, it is divided by places, from the largest key to the smallest.
+// Top-k with all tokens of the row down to the cut's part in the list: *listed is their number.
+// Returns prior, and *listed -1, where there are fewer tokens than k.
 template <bool WEIGHTS, typename T>
-__device__ __forceinline__ Cut select(const Pass<T>& pass, Row& s, cg::cluster_group& cluster, const Cut& prior,
-                                      const Scale sc, float bound, float range, u64 target, double share) {
-  constexpr int N = Vec<T>::N;
-  const int tid = threadIdx.x, lane = tid & 31, ranks = (int)cluster.num_blocks();
-  const float m = sc.m;
-  u64 before = 0;             // count or weight in front of the range
-  int bin = -1;               // the step that the range is, -1: none (the places below say)
-  u64 lo = 0, hi = ~0ull;     // the range's places
-  bool linear = range > 0.f;
-  const float step = linear ? kBins / range : 0.f;
-  auto bin_of = [&](float l) { return min(kBins - 1, (int)((m - l) * step)); };
-  bool divide = WEIGHTS || linear;
-  int shift = 0;
+__device__ __forceinline__ Cut select(const Pass<T>& pass, Row& s, const Cut& prior, const Scale& sc, float bound,
+                                      bool linear, const Steps& steps, int q0, int shift, u64 before, u64 target,
+                                      int* listed) {
+  cg::cluster_group cluster = cg::this_cluster();
+  const int tid = threadIdx.x, ranks = (int)cluster.num_blocks();
+  u64 lo = (u64)key_of(-kTop) << kIndexBits, hi = place_of(key_of(sc.m), 0);  // the range's places
+  if (!linear) shift = 64 - __clzll((long long)(hi - lo)) - kPartBits;
+  bool room = here(!WEIGHTS);
+  auto part_of = [&](float l, int i) -> int {
+    if (!prior.keeps(l, i)) return -1;
+    if (here(linear)) {
+      const int part = (steps.at(l) - q0) >> shift;
+      return part < kParts ? part : -1;
+    }
+    const u64 p = place_of(key_of(l), i);
+    return p < lo || p > hi ? -1 : (int)((hi - p) >> shift);
+  };
+#pragma unroll 1
   for (;;) {
-    if (divide) {
-      // ---- a histogram of the range
-      *reinterpret_cast<uint4*>(&s.lo[4 * tid]) = make_uint4(0, 0, 0, 0);
-      if (WEIGHTS) *reinterpret_cast<uint4*>(&s.hi[4 * tid]) = make_uint4(0, 0, 0, 0);
-      __syncthreads();
-      pass.each([&](const float (&x)[N], int i) {
-        bool in[N];
-        bool any = false;
-#pragma unroll
-        for (int k = 0; k < N; ++k) {
-          in[k] = x[k] >= bound && prior.keeps(x[k], i + k);
-          if (!linear && in[k]) {
-            const u64 p = place_of(key_of(x[k]), i + k);
-            in[k] = p >= lo && p <= hi;
-          }
-          any |= in[k];
-        }
-        if (!any) return;
-#pragma unroll
-        for (int k = 0; k < N; k += 2) {
-          u64 w[2] = {0, 0};
-          if (WEIGHTS && (in[k] || in[k + 1])) weights(sc, s.tab, make_float2(x[k], x[k + 1]), w[0], w[1]);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            if (!in[k + e]) continue;
-            const int b = linear ? bin_of(x[k + e]) : (int)((hi - place_of(key_of(x[k + e]), i + k + e)) >> shift);
-            if (WEIGHTS) {
-              const uint32_t wl = (uint32_t)w[e];
-              const uint32_t wh = (uint32_t)(w[e] >> 32) + (atomicAdd(&s.lo[b], wl) + wl < wl);
-              if (wh) atomicAdd(&s.hi[b], wh);
-            } else {
-              atomicAdd(&s.lo[b], 1u);
-            }
-          }
-        }
-      });
-      cluster.sync();
-      // ---- merged, every CTA for itself
-      u64 v[4] = {0, 0, 0, 0};
-      for (int c = 0; c < ranks; ++c) {
-        const uint4 a = *reinterpret_cast<const uint4*>(cluster.map_shared_rank(&s.lo[4 * tid], c));
-        uint4 b = make_uint4(0, 0, 0, 0);
-        if (WEIGHTS) b = *reinterpret_cast<const uint4*>(cluster.map_shared_rank(&s.hi[4 * tid], c));
-        v[0] += ((u64)b.x << 32) + a.x;
-        v[1] += ((u64)b.y << 32) + a.y;
-        v[2] += ((u64)b.z << 32) + a.z;
-        v[3] += ((u64)b.w << 32) + a.w;
-      }
-      u64 total;
-      u64 at = before + block_scan(v[0] + v[1] + v[2] + v[3], s.scan, &total);
-      if (WEIGHTS && target == 0) target = max(1ull, min(total, (u64)__dmul_ru(share, (double)total)));
-      if (!WEIGHTS && before + total < target) return prior;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (at < target && target <= at + v[k]) {  // one thread
-          s.found = 4 * tid + k;
-          s.found_before = at;
-        }
-        at += v[k];
-      }
-      __syncthreads();
-      bin = s.found;
-      before = s.found_before;
-      if (!linear) {
-        hi -= (u64)bin << shift;
-        lo = max(lo, hi - ((1ull << shift) - 1));
-      }
-    }
-    // ---- the range's tokens, as far as there is room for them
-    if (tid == 0) {
-      s.listed = 0;
-      s.key_lo = ~0u;
-      s.key_hi = 0;
-    }
+    // ---- a histogram of the range
+    s.lo[tid] = 0;
+    if (WEIGHTS) s.hi[tid] = 0;
     __syncthreads();
-    uint32_t klo = ~0u, khi = 0;
-    pass.each([&](const float (&x)[N], int i) {
-#pragma unroll
-      for (int k = 0; k < N; ++k) {
-        if (!(x[k] >= bound && prior.keeps(x[k], i + k))) continue;
-        const uint32_t key = key_of(x[k]);
-        const u64 p = place_of(key, i + k);
-        if (linear && bin >= 0 ? bin_of(x[k]) != bin : p < lo || p > hi) continue;
-        klo = min(klo, key);
-        khi = max(khi, key);
-        const int at = atomicAdd(&s.listed, 1);
-        if (at < kList) s.list[at] = p;
+    // (a linear range's logits, else all)
+    const unsigned width = linear ? (unsigned)kParts << shift : 0u;
+    auto near = [&](float l) { return l >= bound && (width == 0 || (unsigned)(steps.at(l) - q0) < width); };
+    pass.where(near, [&](float l, int at) {
+      const int part = part_of(l, pass.first + at);
+      if (part < 0) return;
+      if (WEIGHTS) {
+        const u64 w = weight(sc, s.tab, l, true);
+        const uint32_t wl = (uint32_t)w;
+        const uint32_t wh = (uint32_t)(w >> 32) + (atomicAdd(&s.lo[part], wl) + wl < wl);
+        if (wh) atomicAdd(&s.hi[part], wh);
+      } else {
+        atomicAdd(&s.lo[part], 1u);
       }
     });
-    klo = __reduce_min_sync(0xffffffffu, klo);
-    khi = __reduce_max_sync(0xffffffffu, khi);
-    if (lane == 0 && khi) {
-      atomicMin(&s.key_lo, klo);
-      atomicMax(&s.key_hi, khi);
-    }
     cluster.sync();
-    int n = 0, owner = -1, slot = 0;
-    klo = ~0u;
-    khi = 0;
-    for (int c = 0; c < ranks; ++c) {
-      const int k = *cluster.map_shared_rank(&s.listed, c);
-      klo = min(klo, *cluster.map_shared_rank(&s.key_lo, c));
-      khi = max(khi, *cluster.map_shared_rank(&s.key_hi, c));
-      if (tid >= n && tid < n + k) {
-        owner = c;
-        slot = tid - n;
-      }
-      n += k;
+    clear_list(s);  // (every CTA has read the lists of an earlier range)
+    // ---- merged, every CTA for itself
+    u64 v = 0;
+    uint32_t part_lo[kMaxCluster], part_hi[kMaxCluster];  // (all reads in flight at once)
+#pragma unroll
+    for (int c = 0; c < kMaxCluster; ++c) {
+      part_lo[c] = *cluster.map_shared_rank(&s.lo[tid], c & (ranks - 1));
+      part_hi[c] = WEIGHTS ? *cluster.map_shared_rank(&s.hi[tid], c & (ranks - 1)) : 0;
     }
-    if (n == 0) return prior;  // (a row without weights, or with fewer tokens than k)
+#pragma unroll
+    for (int c = 0; c < kMaxCluster; ++c) v += c < ranks ? ((u64)part_hi[c] << 32) + part_lo[c] : 0;
+    u64 total;
+    const u64 at = before + block_scan(v, s.scan, &total);
+    if (!WEIGHTS && before + total < target) {
+      *listed = -1;
+      return prior;
+    }
+    if (at < target && target <= at + v) {  // one thread
+      s.found = tid;
+      s.found_before = at;
+      s.b1 = (int)min(at + v, (u64)kList + 1);  // tokens down to the end of this part
+    }
+    __syncthreads();
+    const int part = s.found;
+    // top-k: everything down to this part fits the list
+    const bool whole = !WEIGHTS && room && s.b1 <= kList;
+    if (!whole) before = s.found_before;
+    // ---- the part's tokens
+    uint32_t klo = ~0u, khi = 0;
+    pass.where(near, [&](float l, int at) {
+      const int p = part_of(l, pass.first + at);
+      if (p >= 0 && (here(whole) ? p <= part : p == part)) enlist(s, l, pass.first + at, klo, khi);
+    });
+    tell_keys(s, klo, khi);
+    cluster.sync();
+    const int n = join_lists(s, &klo, &khi);
+    if (whole) {
+      *listed = n;
+      return prior;
+    }
     if (n <= kList) {
-      u64 mine = 0;
-      if (tid < n) {
-        mine = cluster.map_shared_rank(s.list, owner)[slot];
-        s.all[tid] = mine;
-        if (WEIGHTS) {
-          u64 w0, w1;
-          const float l = logit_of((uint32_t)(mine >> kIndexBits));
-          weights(sc, s.tab, both(l), w0, w1);
-          s.all_w[tid] = w0;
-        }
-      }
-      __syncthreads();
-      // two threads a token
-      const int i = tid >> 1;
-      u64 sum = 0;
+      const int g = group_of(n), i = tid / g;
+      int rank;
+      const u64 sum = in_front(s, n, g, i, &rank);
       if (i < n) {
-        const u64 p = s.all[i];
-        for (int j = tid & 1; j < n; j += 2)
-          if (s.all[j] > p) sum += WEIGHTS ? s.all_w[j] : 1ull;
-      }
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      if (i < n) {
-        const u64 at = before + sum, w = WEIGHTS ? s.all_w[i] : 1ull;
+        const u64 at = before + (WEIGHTS ? sum : rank), w = WEIGHTS ? s.all_w[i] : 1;
         if (at < target && target <= at + w) s.cut = s.all[i];
-        // fewer than k tokens in all: down to the last one
-        if (!WEIGHTS && before + n < target && sum == n - 1ull) s.cut = s.all[i];
       }
       __syncthreads();
-      const u64 p = s.cut;
-      return Cut{logit_of((uint32_t)(p >> kIndexBits)), (int)(kIndexMask - (uint32_t)(p & kIndexMask))};
+      return cut_at(s.cut);  // (*listed stays 0)
     }
-    // ---- too many: the range between its keys is divided again
-    hi = min(hi, place_of(khi, 0));
-    lo = max(lo, (u64)klo << kIndexBits);
-    shift = max(0, 64 - __clzll((long long)(hi - lo)) - 11);
-    linear = false;
-    divide = true;
+    // ---- too many: what lies between the part's keys is divided
+    if (!linear) {
+      hi -= (u64)part << shift;
+      lo = max(lo, hi - ((1ull << shift) - 1));
+    }
+    hi = linear ? place_of(khi, 0) : min(hi, place_of(khi, 0));
+    lo = linear ? (u64)klo << kIndexBits : max(lo, (u64)klo << kIndexBits);
+    shift = max(0, 64 - __clzll((long long)(hi - lo)) - kPartBits);
+    linear = here(false);
+    room = here(false);
   }
+}
+
+// log2(e) / T in two floats (2^-47), and where weights end: 45 powers of two below m they are less
+// than half a step.
+__device__ __forceinline__ Scale scale_of(float m, float t, float* ends) {
+  const float e = 1.44269502f, c = e / t;                             // log2(e) = e + 1.9259630e-8
+  const float left = fmaf(-c, t, e) + 1.92596299e-8f;
+  *ends = fmaxf(__fmaf_ru(-31.1916f, t, m), -kTop);
+  return Scale{m, c, left / t};
+}
+// The smallest logit whose weight is min_p at least (64-bit floating point is slow here: one thread).
+__device__ __noinline__ float min_p_bound(float m, float t, float min_p) {
+  return __double2float_ru((double)m + log(min((double)min_p, 1.0)) * (double)t);
+}
+
+// floor(x * whole) for x in [0, 1), exactly, and whether that is less than the product.
+__device__ __forceinline__ u64 times(float x, u64 whole, bool* more) {
+  const uint32_t b = __float_as_uint(x);
+  const uint32_t e = b >> 23;
+  const u64 mantissa = e ? (b & 0x7FFFFFu) | 0x800000u : b;
+  const int shift = 150 - (int)max(e, 1u);  // x = mantissa 2^-shift, 24 <= shift <= 149
+  const u64 lo = mantissa * whole, hi = __umul64hi(mantissa, whole);
+  *more = shift >= 128 ? (lo | hi) != 0 : shift >= 64 ? lo != 0 || (hi & ((1ull << (shift - 64)) - 1)) != 0
+                                                      : (lo & ((1ull << shift) - 1)) != 0;
+  return shift >= 128 ? 0 : shift >= 64 ? hi >> (shift - 64) : hi << (64 - shift) | lo >> shift;
+}
+// The weight that a nucleus has to reach: at least one step.
+__device__ __forceinline__ u64 share_of(float top_p, u64 whole) {
+  bool more;
+  const u64 x = times(fmaxf(top_p, 0.f), whole, &more);
+  return max(1ull, x + more);
+}
+// The bar of the draw: sums are whole numbers, and one exceeds u * whole where it exceeds its floor.
+__device__ __forceinline__ u64 draw_bar(float u, u64 whole) {
+  bool more;
+  return times(fminf(fmaxf(u, 0.f), 0x1.fffffep-1f), whole, &more);
 }
 
 template <typename T, bool VEC>
@@ -435,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const T* row = static_cast<const T*>(a.x) + r * a.xs;
   Pass<T> pass;
-  pass.chunk = chunk;
+  pass.chunk = reinterpret_cast<T*>(chunk);
   pass.run = a.chunk / kWarps;
   pass.first = rank * a.chunk;
   const float temp = a.temp ? a.temp[r] : 1.f;
@@ -443,16 +611,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   const int top_k = a.top_k ? a.top_k[r] : 0;
 
   // ---- the row comes in
-  float mine = -INFINITY;
+  constexpr uint32_t kNone = sizeof(T) == 4 ? 0xFF800000u : 0xFF80FF80u;  // -inf
+  uint32_t best = kNone;
   bool have = false;
 #pragma unroll 4
   for (int k = lane * N; k < pass.run; k += 32 * N) {
     const int at = warp * pass.run + k, i = pass.first + at;
     uint4 v;
-    uint32_t* w = reinterpret_cast<uint32_t*>(&v);
     if (VEC) {
-      constexpr uint32_t none = sizeof(T) == 4 ? 0xFF800000u : 0xFF80FF80u;
-      v = make_uint4(none, none, none, none);
+      v = make_uint4(kNone, kNone, kNone, kNone);
       if (i < a.V) v = __ldcs(reinterpret_cast<const uint4*>(row + i));
     } else {
       alignas(16) T e[N];
@@ -461,48 +628,33 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       v = *reinterpret_cast<uint4*>(e);
     }
     have |= i < a.V;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = tidy(w[j], T());
+    best = larger(best, largest<T>(v), T());
     chunk[at / N] = v;
-    float x[N];
-    unpack(v, x);
-#pragma unroll
-    for (int j = 0; j < N; ++j) mine = fmaxf(mine, x[j]);
   }
-  if (tid < 128) s.tab[tid] = kPowers.at[tid];
+  const float mine = value_of(best, T());
+  // ---- the largest logit
+  if (tid < 128) s.tab[tid] = make_float2(kPowers.hi[tid], kPowers.lo[tid]);
+  clear_list(s);
   {
-    float hi = mine, lo = have ? mine : INFINITY;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+    float hi = mine;
+    for (int o = 1; o < ranks; o <<= 1) hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    if (tid % ranks == 0) s.top[tid / ranks] = hi;
+    if (top_k > kThreads) {
+      const uint32_t least = block_least(s, have ? key_of(mine) : ~0u);
+      const int threads = __syncthreads_count(have);
+      if (tid == 0) s.low = make_float2(logit_of(least), (float)threads);
     }
-    if (lane == 0) {
-      s.f[warp] = hi;
-      s.g[warp] = lo;
-    }
-  }
-  const int groups = __syncthreads_count(have);
-  if (tid == 0) {
-    float hi = s.f[0], lo = s.g[0];
-    for (int w = 1; w < kWarps; ++w) {
-      hi = fmaxf(hi, s.f[w]);
-      lo = fminf(lo, s.g[w]);
-    }
-    s.max = hi;
-    s.low = lo;
-    s.groups = groups;
   }
   cluster.sync();
-  float m = -INFINITY, low = INFINITY;
-  int threads = 0;
-  for (int c = 0; c < ranks; ++c) {
-    m = fmaxf(m, *cluster.map_shared_rank(&s.max, c));
-    low = fminf(low, *cluster.map_shared_rank(&s.low, c));
-    threads += *cluster.map_shared_rank(&s.groups, c);
+  const float top = peer(s.top, tid * ranks / kThreads, ranks)[tid % (kThreads / ranks)];
+  float m = logit_of(~block_least(s, ~key_of(top)));
+  if (m > kTop) {
+    m = kTop;
+    pass.some(kTop, [&](float, int at) { pass.chunk[at] = from_f32<T>(kTop); });
+    __syncthreads();
   }
   const bool bad = !(temp >= 0.f) || isinf(temp);
-  const bool none = bad || m == -INFINITY;  // nothing to choose from
+  const bool none = bad || !(m >= -kTop);  // nothing to choose from
   int token = -1;                           // known to one thread of the cluster
   Cut cut = {-kTop, (int)kIndexMask};
   u64 total = 0;
@@ -516,130 +668,331 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     // ---- the first of the largest
     if (tid == 0) s.best = INT_MAX;
     __syncthreads();
-    int best = INT_MAX;
-    pass.each([&](const float (&x)[N], int i) {
-#pragma unroll
-      for (int k = N - 1; k >= 0; --k)
-        if (x[k] == m) best = min(best, i + k);
-    });
-    best = (int)__reduce_min_sync(0xffffffffu, (unsigned)best);
-    if (lane == 0) atomicMin(&s.best, best);
+    pass.some(m, [&](float, int at) { atomicMin(&s.best, pass.first + at); });
     cluster.sync();
-    best = INT_MAX;
-    for (int c = 0; c < ranks; ++c) best = min(best, *cluster.map_shared_rank(&s.best, c));
-    if (rank == 0 && tid == 0) token = best;
+    const int best = lane < ranks ? *peer(&s.best, lane, ranks) : INT_MAX;
     cut.v = m;
-    cut.i = best;
+    cut.i = (int)__reduce_min_sync(0xffffffffu, (unsigned)best);
+    if (rank == 0 && tid == 0) token = cut.i;
   } else {
+    const float t = fmaxf(temp, 0x1p-100f);
+    float ends, least = -kTop;
+    const Scale sc = scale_of(m, t, &ends);
     if (tid == 0) {
-      const double t = fmax((double)temp, 0x1p-100), c = 1.4426950408889634074 / t;
-      s.scale.m = m;
-      s.scale.ch = (float)c;
-      s.scale.cl = (float)(c - (double)(float)c);
-      // 45 powers of two below m weights are less than half a step
-      s.ends = __double2float_ru((double)m - 31.191623125 * t);
-      s.least = min_p > 0.f ? __double2float_ru((double)m + log(min((double)min_p, 1.0)) * t) : -kTop;
+      s.scale = sc;
+      s.ends = ends;
+      if (min_p > 0.f) s.least = min_p_bound(m, t, min_p);
     }
     __syncthreads();
-    const Scale sc = s.scale;
-    const float ends = fmaxf(s.ends, -kTop), least = s.least;
-    if (top_k > 0 && top_k < a.V) {
-      const bool known = top_k <= threads && low > -INFINITY;
-      const float bound = known ? low : -kTop;
-      cut = select<false, T>(pass, s, cluster, cut, sc, bound, known ? fminf(fmaxf(m - low, 1e-30f), kTop) : 0.f, top_k, 0.);
-    }
-    if (top_p < 1.f) {
-      const float bound = fmaxf(ends, cut.v);
-      if (top_k > 0) cluster.sync();  // the other CTAs have read this one's list and histogram
-      cut = select<true, T>(pass, s, cluster, cut, sc, bound, fminf(fmaxf(m - bound, 1e-30f), kTop), 0,
-                            (double)top_p);
-    }
-    if (least > cut.v) {
-      cut.v = least;
-      cut.i = (int)kIndexMask;
-    }
-    // ---- the kept weights
-    u64 sum = 0;
-    pass.each([&](const float (&x)[N], int i) {
-      bool in[N];
-      bool any = false;
-#pragma unroll
-      for (int k = 0; k < N; ++k) any |= in[k] = x[k] >= ends && cut.keeps(x[k], i + k);
-      if (!any) return;
-#pragma unroll
-      for (int k = 0; k < N; k += 2) {
-        u64 w0, w1;
-        weights(sc, s.tab, make_float2(x[k], x[k + 1]), w0, w1);
-        sum += (in[k] ? w0 : 0) + (in[k + 1] ? w1 : 0);
-      }
-    });
-    sum = warp_sum(sum);
-    __syncthreads();  // scan of an earlier pass has been read
-    if (lane == 0) s.scan[warp] = sum;
-    __syncthreads();
-    u64 own = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) own += s.scan[w];
-    if (tid == 0) s.sum = own;
-    cluster.sync();
-    u64 before = 0;
-    for (int c = 0; c < ranks; ++c) {
-      const u64 x = *cluster.map_shared_rank(&s.sum, c);
-      before += c < rank ? x : 0;
-      total += x;
-    }
-    // sums are whole numbers: one exceeds u * total where it exceeds its floor
-    const u64 bar = (u64)__dmul_rd((double)fminf(fmaxf(u, 0.f), 0x1.fffffep-1f), (double)total);
-    if (before <= bar && bar < before + own) {  // one CTA
-      int w = 0;
-      while (before + s.scan[w] <= bar) before += s.scan[w++];
-      // the warp's run once more, a few tokens in a row a thread
-      const int per = (pass.run + kThreads - 1) / kThreads;
-      const T* logits = reinterpret_cast<const T*>(chunk) + w * pass.run;
-      const int at = tid * per, i = pass.first + w * pass.run + at;
-      auto weight = [&](int k) -> u64 {
-        if (at + k >= pass.run) return 0;
-        const float l = to_f32(logits[at + k]);
-        u64 w0, w1;
-        weights(sc, s.tab, both(l), w0, w1);
-        return l >= ends && cut.keeps(l, i + k) ? w0 : 0;
-      };
-      u64 sum = 0, all;
-      for (int k = 0; k < per; ++k) sum += weight(k);
-      u64 c = before + block_scan(sum, s.scan, &all);
-      if (c <= bar && bar < c + sum)  // one thread
-        for (int k = 0; token < 0; ++k) {
-          c += weight(k);
-          if (c > bar) token = i + k;
+    if (min_p > 0.f) least = s.least;
+    int n = 0;  // tokens of s.all, where those are all that top-k leaves
+    const bool limited = top_k > 0 && top_k < a.V;
+    if (limited) {
+      float bound, range;
+      bool linear = true;
+      if (top_k <= __syncthreads_count(top >= -kTop)) {
+        // ---- k groups reach this far: their maxima, halved towards the k-th
+        bound = logit_of(block_least(s, top >= -kTop ? key_of(top) : ~0u));
+        float over = m;
+#pragma unroll 1
+        for (int i = 0; i < 12 && over > bound; ++i) {
+          const float mid = 0.5f * bound + 0.5f * over;
+          const int reach = __syncthreads_count(top >= mid);
+          if (reach >= top_k) bound = mid;
+          else over = mid;
+          if (reach >= top_k && reach <= top_k + top_k / 8) break;
         }
+        range = 1.001f * (m - bound);
+        if (top_k <= kDirect) {
+          // ---- the tokens above: some more than k
+          uint32_t klo = ~0u, khi = 0;
+          pass.some(bound, [&](float l, int at) { enlist(s, l, pass.first + at, klo, khi); });
+          tell_keys(s, klo, khi);
+          cluster.sync();
+          n = join_lists(s, &klo, &khi);
+          if (n > kList) n = 0;
+        }
+      } else {
+        const float2 v = lane < ranks ? *peer(&s.low, lane, ranks) : make_float2(INFINITY, 0.f);
+        const float low = logit_of(__reduce_min_sync(0xffffffffu, key_of(v.x)));
+        // as many tokens as threads lie above the least of the threads' maxima; else down to where weights end
+        const bool known = top_k > kThreads && top_k <= (int)warp_sum(v.y) && low >= -kTop;
+        bound = known ? low : ends;
+        range = known ? 1.001f * (m - low) : 31.2f * t;
+      }
+#pragma unroll 1
+      while (n == 0) {
+        cut = select<false, T>(pass, s, cut, sc, bound, linear, Steps(m, fmaxf(range, 1e-30f)), 0, 21 - kPartBits, 0,
+                               top_k, &n);
+        if (n >= 0) break;
+        n = 0;
+        if (!linear) break;  // fewer than k in all
+        bound = -kTop;       // the k-th has no weight: among all tokens
+        linear = false;
+      }
+    }
+    if (n > 0) {
+      // ---- all from the list
+      const int g = group_of(n), i = tid / g;
+      int rank_of;
+      const u64 at = in_front(s, n, g, i, &rank_of);
+      const u64 place = i < n ? s.all[i] : 0, w = i < n ? s.all_w[i] : 0;
+      const bool lead = i < n && (tid & (g - 1)) == 0;
+      if (tid == 0) s.cut = ~0ull;
+      if (lead && rank_of == top_k - 1) s.bar = top_p < 1.f ? share_of(top_p, at + w) : ~0ull;  // of K's weight
+      __syncthreads();
+      const bool keep = rank_of < top_k && at < s.bar && logit_of((uint32_t)(place >> kIndexBits)) >= least;
+      if (keep && lead) atomicMin(&s.cut, place);
+      __syncthreads();
+      const u64 edge = s.cut;
+      cut = cut_at(edge);
+      // kept weights by rising numbers
+      const u64 turned = place & kIndexMask;
+      u64 upto = 0, whole = 0;
+#pragma unroll 2
+      for (int j = tid & (g - 1); j < n; j += g) {
+        const u64 x = s.all[j], y = x >= edge ? s.all_w[j] : 0;
+        whole += y;
+        if ((x & kIndexMask) >= turned) upto += y;
+      }
+      for (int o = g >> 1; o > 0; o >>= 1) {
+        upto += __shfl_xor_sync(0xffffffffu, upto, o);
+        whole += __shfl_xor_sync(0xffffffffu, whole, o);
+      }
+      if (tid == 0) {
+        s.weight.x = whole;
+        s.bar = draw_bar(u, whole);
+      }
+      __syncthreads();
+      total = s.weight.x;
+      if (rank == 0 && lead && place >= edge && upto - w <= s.bar && s.bar < upto)
+        token = (int)(kIndexMask - (uint32_t)turned);
+    } else {
+      if (limited) {
+        // tokens that top-k's cut divides from their equals: from here on the logit alone says who is left
+        pass.some(cut.v, [&](float l, int at) {
+          if (l == cut.v && pass.first + at > cut.i) pass.chunk[at] = from_f32<T>(-INFINITY);
+        });
+        cut.i = (int)kIndexMask;
+      }
+      bool nucleus = top_p < 1.f;
+      int q1 = 0, q2 = 0;  // steps of the bracket in which top-p's cut lies
+      const Steps steps(m, 31.2f * t);
+      float floor = fmaxf(ends, cut.v);
+      if (nucleus) {
+        // ---- where top-p's cut can lie: the weights' masses in 2048 steps
+        if (limited) cluster.sync();  // the other CTAs have read this one's histogram
+        *reinterpret_cast<uint4*>(&s.lo[4 * tid]) = make_uint4(0, 0, 0, 0);
+        if (tid == 0) {
+          s.b1 = kBins;
+          s.b2 = -1;
+        }
+        __syncthreads();
+        pass.each([&](const float (&x)[4], int) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int q = steps.at(x[k]);
+            // the weight within its bin, linear from 1 to e^(-31.2 / 2048), in 1 / 32768
+            const uint32_t mass = (uint32_t)((32768 << kStepBits) - 495 * (q & 1023)) >> kStepBits;
+            if (x[k] >= floor) atomicAdd(&s.lo[min(kBins - 1, q >> kStepBits)], mass);
+          }
+        });
+        cluster.sync();
+        clear_list(s);
+        // ---- merged, every CTA for itself
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        uint4 x[kMaxCluster];  // (all reads in flight at once)
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c)
+          x[c] = *reinterpret_cast<const uint4*>(cluster.map_shared_rank(&s.lo[4 * tid], c & (ranks - 1)));
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c)
+          if (c < ranks) {
+            v[0] += (float)x[c].x;
+            v[1] += (float)x[c].y;
+            v[2] += (float)x[c].z;
+            v[3] += (float)x[c].w;
+          }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] *= ptx::ex2(-0.02197855f * (float)(4 * tid + k));  // 31.2 / 2048 log2(e)
+        float all;
+        float c0 = block_scan(v[0] + v[1] + v[2] + v[3], s.scan_f, &all);
+        const float want = fmaxf(top_p, 1e-6f) * all;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float c1 = c0 + v[k];
+          // (rounding can show two threads the same border, or none: then the bracket is the wider one)
+          if (c1 * kOver >= want && !(c0 * kOver >= want)) atomicMin(&s.b1, 4 * tid + k);
+          if (c1 >= want * kOver && !(c0 >= want * kOver)) atomicMax(&s.b2, 4 * tid + k);
+          c0 = c1;
+        }
+        __syncthreads();
+        q1 = s.b1 == kBins ? 0 : s.b1 << kStepBits;
+        q2 = s.b2 < 0 || s.b2 == kBins - 1 ? INT_MAX : (s.b2 + 1) << kStepBits;
+        // min-p ends in front of the bracket: top-p takes nothing away
+        if (least >= ends && steps.at(least) < q1) nucleus = false;
+      }
+      if (!nucleus && least > cut.v) {
+        cut.v = least;
+        cut.i = (int)kIndexMask;
+        floor = fmaxf(ends, least);
+      }
+      // ---- the weights: those in front of the bracket are kept, and those in it come to the list
+      uint32_t klo = ~0u, khi = 0;
+      Steps44 kept = {0, 0}, rest = {0, 0};  // (96 tokens a thread at most)
+      pass.each([&](const float (&x)[4], int at) {
+        if (!__any_sync(0xffffffffu, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) >= floor)) return;
+        Steps44 w[4];
+        weights(sc, s.tab, make_float2(x[0], x[1]), x[0] >= floor, x[1] >= floor, w[0], w[1]);
+        weights(sc, s.tab, make_float2(x[2], x[3]), x[2] >= floor, x[3] >= floor, w[2], w[3]);
+        if (!nucleus) {
+          kept.hi += w[0].hi + w[1].hi + w[2].hi + w[3].hi;
+          kept.lo += w[0].lo + w[1].lo + w[2].lo + w[3].lo;
+          return;
+        }
+        unsigned mask = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int q = steps.at(x[k]);  // (of a logit below the floor any, and its weight is 0)
+          Steps44& to = q < q1 ? kept : rest;
+          to.hi += w[k].hi;
+          to.lo += w[k].lo;
+          mask |= (unsigned)(x[k] >= floor && q >= q1 && q < q2) << k;
+        }
+#pragma unroll 1
+        for (; mask; mask &= mask - 1) {
+          const int k = at + __ffs(mask) - 1;
+          enlist(s, pass.logit(k), pass.first + k, klo, khi);
+        }
+      });
+      u64 sum = kept.joined();
+      if (nucleus) {
+        // ---- top-p's cut
+        tell_keys(s, klo, khi);
+        u64 above, whole;
+        block_scan(sum, s.scan, &above);
+        block_scan(rest.joined(), s.scan, &whole);
+        if (tid == 0) s.weight = make_ulonglong2(above, above + whole);
+        cluster.sync();
+        ulonglong2 v = make_ulonglong2(0, 0);
+        if (lane < ranks) v = *peer(&s.weight, lane, ranks);
+        const u64 before = warp_sum((u64)v.x);
+        whole = warp_sum((u64)v.y);
+        if (tid == 0) s.bar = share_of(top_p, whole);
+        const int n = join_lists(s, &klo, &khi);
+        const u64 target = s.bar;
+        if (n <= kList) {
+          const int g = group_of(n), i = tid / g;
+          int unused;
+          const u64 at = before + in_front(s, n, g, i, &unused);
+          if (i < n && at < target && target <= at + s.all_w[i]) s.cut = s.all[i];
+          __syncthreads();
+          cut = cut_at(s.cut);
+          if (least > cut.v) cut = Cut{least, (int)kIndexMask};
+          // what is kept of the bracket joins the runs' sums
+          const int from = pass.first + warp * pass.run;
+#pragma unroll 1
+          for (int j = lane; j < n; j += 32) {
+            const u64 p = s.all[j];
+            const int k = (int)(kIndexMask - (uint32_t)(p & kIndexMask));
+            if (k >= from && k < from + pass.run && cut.keeps(logit_of((uint32_t)(p >> kIndexBits)), k)) sum += s.all_w[j];
+          }
+        } else {
+          const int width = min(q2, (kBins + 1) << kStepBits) - q1;
+          const int shift = max(0, 32 - __clz(width - 1) - kPartBits);
+          cut = select<true, T>(pass, s, cut, sc, ends, true, steps, q1, shift, before, target, nullptr);
+          if (least > cut.v) cut = Cut{least, (int)kIndexMask};
+          const float from = fmaxf(ends, cut.v);
+          pass.each([&](const float (&x)[4], int at) {
+            unsigned mask = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mask |= (unsigned)(x[k] >= from && steps.at(x[k]) >= q1) << k;
+#pragma unroll 1
+            for (; mask; mask &= mask - 1) {
+              const int k = at + __ffs(mask) - 1;
+              const float l = pass.logit(k);
+              sum += weight(sc, s.tab, l, cut.keeps(l, pass.first + k));
+            }
+          });
+        }
+      }
+      // ---- the token
+      sum = warp_sum(sum);
+      __syncthreads();  // scan of an earlier pass has been read
+      if (lane == 0) s.scan[warp] = sum;
+      __syncthreads();
+      const u64 own = warp_sum(lane < kWarps ? s.scan[lane] : 0);
+      if (tid == 0) s.weight.x = own;
+      cluster.sync();
+      u64 before = 0;
+      {
+        const u64 x = lane < ranks ? peer(&s.weight, lane, ranks)->x : 0;
+        total = warp_sum(x);
+        before = warp_sum(lane < rank ? x : 0);
+      }
+      if (tid == 0) s.bar = draw_bar(u, total);
+      __syncthreads();
+      const u64 bar = s.bar;
+      if (before <= bar && bar < before + own) {  // one CTA
+        // the first run whose end passes the bar
+        u64 upto = lane < kWarps ? s.scan[lane] : 0;
+#pragma unroll
+        for (int o = 1; o < kWarps; o <<= 1) {
+          const u64 x = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += x;
+        }
+        const int w = __ffs(__ballot_sync(0xffffffffu, before + upto > bar)) - 1;
+        if (w > 0) before += __shfl_sync(0xffffffffu, upto, w - 1);
+        // the warp's run once more, a few tokens in a row a thread
+        const int per = (pass.run + kThreads - 1) / kThreads;
+        const int at = tid * per, i = w * pass.run + at;
+        auto weight_at = [&](int k) -> u64 {
+          if (at + k >= pass.run) return 0;
+          const float l = pass.logit(i + k);
+          return weight(sc, s.tab, l, l >= ends && cut.keeps(l, pass.first + i + k));
+        };
+        u64 sum = 0, all;
+#pragma unroll 1
+        for (int k = 0; k < per; ++k) sum += weight_at(k);
+        u64 c = before + block_scan(sum, s.scan, &all);
+        if (c <= bar && bar < c + sum)  // one thread
+#pragma unroll 1
+          for (int k = 0; token < 0; ++k) {
+            c += weight_at(k);
+            if (c > bar) token = pass.first + i + k;
+          }
+      }
     }
   }
   if (token >= 0) a.tokens[r] = token;
   if (a.probs) {
+    // ---- the distribution
     float* out = a.probs + r * a.ps;
     const Scale sc = none || temp == 0.f ? Scale{0.f, 0.f, 0.f} : s.scale;
     float inv = 1.f;
     if (total) {
+      if (tid == 0) s.inv = (float)(0x1p44 / (double)total);
       __syncthreads();
-      if (tid == 0) s.bar = 0x1p44 / (double)total;
-      __syncthreads();
-      inv = (float)s.bar;
+      inv = s.inv;
     }
-    pass.each([&](const float (&x)[N], int i) {
-      float p[N];
+    pass.each([&](const float (&x)[4], int at) {
+      const int i = pass.first + at;
+      float p[4] = {0.f, 0.f, 0.f, 0.f};
+      if (__any_sync(0xffffffffu, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) >= cut.v)) {
 #pragma unroll
-      for (int k = 0; k < N; ++k) p[k] = cut.keeps(x[k], i + k) ? weight_f32(sc, x[k]) * inv : 0.f;
+        for (int k = 0; k < 4; ++k)
+          if (cut.keeps(x[k], i + k)) p[k] = weight_f32(sc, x[k]) * inv;
+      }
       if (a.probs_vec) {
-#pragma unroll
-        for (int k = 0; k < N; k += 4)
-          if (i + k < a.V) __stcs(reinterpret_cast<float4*>(out + i + k), make_float4(p[k], p[k + 1], p[k + 2], p[k + 3]));
+        if (i < a.V) __stcs(reinterpret_cast<float4*>(out + i), make_float4(p[0], p[1], p[2], p[3]));
       } else {
 #pragma unroll
-        for (int k = 0; k < N; ++k)
+        for (int k = 0; k < 4; ++k)
           if (i + k < a.V) out[i + k] = p[k];
       }
     });
   }
+  // ---- the end
   cluster.sync();  // no CTA leaves while another may still read what it tells
 }
 

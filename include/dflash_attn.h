@@ -527,7 +527,8 @@ DFLASH_API dflash_status_t dflash_verify(const dflash_verify_dims_t* dims, const
  *   logits [N, V] of dtype, rows logits_stride elements apart (0: V); u [N] fp32 in
  *   [0, 1); temperature, top_p, min_p [N] fp32 and top_k [N] int32, each nullable (1, 1, 0, 0);
  *   tokens [N] int32; probs [N, V] fp32, nullable, rows probs_stride elements apart (0: V).
- * -inf (a masked token) and NaN are no choice; +inf counts as the largest finite value.
+ * A logit below -2^126 (-inf, a type's lowest value: a masked token) and NaN are no
+ * choice; one above 2^126 counts as 2^126.
  * A row without a choice, and one whose temperature is negative, infinite or NaN, is
  * recorded as DFLASH_ERR_INVALID and gets token 0 and probs 0.  NaN in top_p or min_p
  * leaves the filter out; a temperature below 2^-100 counts as 2^-100.
