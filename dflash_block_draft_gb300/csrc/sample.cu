@@ -23,14 +23,13 @@
 //     the whole once more, a few tokens a thread.
 //
 // Weights are whole steps of 2^-44 of the largest one, added up as integers, so that no sum
-// depends on the order, the number of CTAs or the threads' timing, and the cut and the token are
-// those of the real numbers unless a border lies within about 2^-40 of the sum (fp32 sums would
-// draw another token in every fiftieth row of a vocabulary of 131072).  A weight costs some 20
-// packed fp32 instructions and 9 others: l - m as two floats, times log2(e) / T as two floats;
-// 2^y from a table of 2^(j / 128) in two floats and a polynomial of degree 4; the bits of sums with
-// 2.5 and 1.5 2^-21 count the steps, as in verify.cu.  (In fixed point from the table on, with
-// 64-bit shifts, a row took twice as long, bound by the integer pipe.  64-bit floating point
-// runs at a hundredth of fp32's rate.)
+// depends on the order, the number of CTAs or the threads' timing.  A weight costs 13 packed fp32
+// instructions for a pair in bf16's 10, and 9 others: l - m, times log2(e) / T as two floats; 2^y
+// from a table of 2^(j / 128) in two floats and a polynomial of degree 3; the bits of sums with 2.5
+// and 1.5 2^-21 count the steps, as in verify.cu.  The weights' errors, 2^-33.5 rms, are
+// each other's by chance and add up to a border's as their root: of a vocabulary of 131072 every
+// 10^7th row would draw another token than the real numbers (every 50th with fp32 sums of weights
+// that are off in one direction).  64-bit floating point runs at a hundredth of fp32's rate.
 #include <cooperative_groups.h>
 #include <limits.h>
 #include <math.h>
@@ -103,53 +102,55 @@ struct Steps44 {
 };
 constexpr float kHi = 2.5f, kLo = 0x1.8p-21f;  // sums with these have their last bits at 2^-22 and 2^-44
 
+// The powers' table in shared memory.
+struct Table {
+  float hi[128], lo[128];
+};
+
 // Weights of two logits that are at most 45 powers of two below the largest one; 0 where !in.
-__device__ __forceinline__ void weights(const Scale& c, const float2* tab, float2 l, bool in0, bool in1, Steps44& w0,
+// Off by at most 2^-31 of themselves (2^-33.5 rms), and by half a step.  In fp32 l - m is
+// taken as two floats; of two bf16 values it fits one, but where one of them is below
+// 2^-16 of the other.
+template <typename T>
+__device__ __forceinline__ void weights(const Scale& c, const Table& tab, float2 l, bool in0, bool in1, Steps44& w0,
                                         Steps44& w1) {
   const float2 neg = both(-1.f), nm = both(-c.m), ch = both(c.ch);
   l = make_float2(in0 ? l.x : c.m, in1 ? l.y : c.m);
-  // l - m = d + err exactly (the two-sum of Moller and Knuth)
-  const float2 d = __fadd2_rn(l, nm), bb = __ffma2_rn(l, neg, d);
-  const float2 err = __fadd2_rn(__ffma2_rn(__ffma2_rn(bb, neg, d), neg, l), __ffma2_rn(bb, neg, nm));
+  const float2 d = __fadd2_rn(l, nm);
   // y = -np + e
   const float2 np = __fmul2_rn(d, both(-c.ch));
-  const float2 e = __ffma2_rn(err, ch, __ffma2_rn(d, both(c.cl), __ffma2_rn(d, ch, np)));
-  // whole steps of 1/128 by the adder's bits; y = (raw + r) / 128 + e with r = -rn, z = r + e
-  const float big = 0x1.8p16f;
+  float2 e = __ffma2_rn(d, both(c.cl), __ffma2_rn(d, ch, np));
+  if (sizeof(T) == 4) {  // l - m = d + err exactly (the two-sum of Moller and Knuth)
+    const float2 bb = __ffma2_rn(l, neg, d);
+    const float2 err = __fadd2_rn(__ffma2_rn(__ffma2_rn(bb, neg, d), neg, l), __ffma2_rn(bb, neg, nm));
+    e = __ffma2_rn(err, ch, e);
+  }
+  // y = raw / 128 + z, the whole steps by the adder's bits, the rest r = -rn exactly and z = r + e
+  const float big = 0x1.8p16f;  // (its own bits are 0 in the lower half)
   const float2 t1 = __ffma2_rn(np, neg, both(big));
-  const float2 rn = __fadd2_rn(np, __fadd2_rn(t1, both(-big)));
-  const float2 z = __ffma2_rn(rn, neg, e);
-  const int raw0 = __float_as_int(t1.x) - __float_as_int(big), raw1 = __float_as_int(t1.y) - __float_as_int(big);
+  const float2 z = __ffma2_rn(__fadd2_rn(np, __fadd2_rn(t1, both(-big))), neg, e);
+  const int raw0 = __float_as_int(t1.x), raw1 = __float_as_int(t1.y);
   // 2^(raw / 128) = p (th + tl)
-  const float2 f0 = tab[raw0 & 127], f1 = tab[raw1 & 127];
-  const float2 th = make_float2(f0.x, f1.x), tl = make_float2(f0.y, f1.y);
-  const float2 p = make_float2(in0 ? __int_as_float((raw0 & ~127) * 65536 + 0x3F800000) : 0.f,
-                               in1 ? __int_as_float((raw1 & ~127) * 65536 + 0x3F800000) : 0.f);
-  // 2^z - 1 = a + b: r ln 2 in two floats, e ln 2, z^2 (c2 + z (c3 + z c4))
-  const float2 na = __fmul2_rn(rn, both(0.693147182f)), a = __fmul2_rn(rn, both(-0.693147182f));
-  float2 b = __ffma2_rn(rn, both(-0.693147182f), na);
-  b = __ffma2_rn(rn, both(1.90465421e-9f), b);  // (ln 2 = 0.693147182 - 1.9e-9)
-  b = __ffma2_rn(e, both(0.693147182f), b);
-  const float2 q = __ffma2_rn(__ffma2_rn(z, both(9.61812911e-3f), both(5.55041087e-2f)), z, both(0.240226507f));
-  b = __ffma2_rn(q, __fmul2_rn(z, z), b);
-  // (th + tl) (1 + a + b) = hi + lo
-  const float2 u = __fmul2_rn(th, a), hi = __fadd2_rn(th, u);
-  const float2 nu = __fmul2_rn(th, na);
-  float2 lo = __ffma2_rn(th, b, __ffma2_rn(tl, a, tl));
-  lo = __fadd2_rn(lo, __ffma2_rn(th, a, nu));
-  lo = __fadd2_rn(lo, __ffma2_rn(__ffma2_rn(th, neg, hi), neg, u));
-  const float2 h2 = __fadd2_rn(hi, lo);
-  lo = __ffma2_rn(__ffma2_rn(hi, neg, h2), neg, lo);
+  const float2 th = make_float2(tab.hi[raw0 & 127], tab.hi[raw1 & 127]);
+  const float2 tl = make_float2(tab.lo[raw0 & 127], tab.lo[raw1 & 127]);
+  const int p0 = (raw0 * 65536 + 0x3F800000) & 0xFF800000, p1 = (raw1 * 65536 + 0x3F800000) & 0xFF800000;
+  const float2 p = make_float2(in0 ? __int_as_float(p0) : 0.f, in1 ? __int_as_float(p1) : 0.f);
+  // s = 2^z - 1, and (th + tl) (1 + s) = hi + lo
+  const float2 q = __ffma2_rn(z, both(5.55041087e-2f), both(0.240226507f));
+  const float2 s = __fmul2_rn(z, __ffma2_rn(q, z, both(0.693147182f)));
+  const float2 hi = __ffma2_rn(th, s, th);
+  const float2 lo = __fadd2_rn(__ffma2_rn(th, s, __ffma2_rn(hi, neg, th)), tl);
   // in steps
-  const float2 hp = __fmul2_rn(h2, p), x = __fadd2_rn(hp, both(kHi));
-  const float2 left = __ffma2_rn(__fadd2_rn(x, both(-kHi)), neg, hp);
+  const float2 x = __ffma2_rn(hi, p, both(kHi));
+  const float2 left = __ffma2_rn(hi, p, __ffma2_rn(x, neg, both(kHi)));
   const float2 y = __fadd2_rn(__ffma2_rn(lo, p, left), both(kLo));
   w0 = Steps44{__float_as_int(x.x) - __float_as_int(kHi), __float_as_int(y.x) - __float_as_int(kLo)};
   w1 = Steps44{__float_as_int(x.y) - __float_as_int(kHi), __float_as_int(y.y) - __float_as_int(kLo)};
 }
-__device__ __forceinline__ u64 weight(const Scale& c, const float2* tab, float l, bool in) {
+template <typename T>
+__device__ __forceinline__ u64 weight(const Scale& c, const Table& tab, float l, bool in) {
   Steps44 w0, w1;
-  weights(c, tab, both(l), in, in, w0, w1);
+  weights<T>(c, tab, both(l), in, in, w0, w1);
   return w0.joined();
 }
 
@@ -206,16 +207,18 @@ struct Row {
   float top[kThreads];             // largest logit of 1 to 8 neighbouring threads, 512 in the cluster
   alignas(8) float2 low;           // smallest of the threads' maxima; threads that have logits
   alignas(16) int4 listed;         // tokens of the range; the smallest and the largest of their keys
-  alignas(16) ulonglong2 weight;   // weights in front of the bracket, and all; kept weights
+  alignas(16) ulonglong2 weight;   // weights in front of the bracket, and all
+  u64 sum;                         // kept weights
   int best;                        // the first token with the row's largest logit (greedy)
   u64 list[kList];
   alignas(16) uint32_t lo[kBins];  // counts, masses, or the weights' lower
   uint32_t hi[kParts];             // and upper halves
   // its own
-  float2 tab[128];
+  Table tab;
   u64 scan[kWarps];
   float scan_f[kWarps];
   u64 all[kList], all_w[kList];
+  u64 ranked[kMaxCluster];         // kept weights of the bracket, each CTA's
   uint32_t keys[kWarps], key;
   u64 found_before;
   int found, b1, b2;
@@ -223,6 +226,13 @@ struct Row {
   Scale scale;
   float ends, least, inv;  // no weight below `ends`; min-p's bound; 1 / kept weights
 };
+
+// Adds to a 64-bit sum in shared memory, the halves by themselves.
+__device__ __forceinline__ void add64(u64* to, u64 w) {
+  uint32_t* h = reinterpret_cast<uint32_t*>(to);
+  const uint32_t lo = (uint32_t)w, hi = (uint32_t)(w >> 32) + (atomicAdd(h, lo) + lo < lo);
+  if (hi) atomicAdd(h + 1, hi);
+}
 
 template <typename V>
 __device__ __forceinline__ V warp_sum(V v) {
@@ -378,6 +388,7 @@ __device__ __forceinline__ const V* peer(const V* p, int rank, int ranks) {
 }
 // All CTAs' lists into s.all and their weights into s.all_w, if they are kList at most, and the
 // range of their keys.  Returns their number.  (After a cluster.sync; a block barrier follows.)
+template <typename T>
 __device__ __noinline__ int join_lists(Row& s, uint32_t* klo, uint32_t* khi) {
   const int tid = threadIdx.x, lane = tid & 31, ranks = (int)cg::this_cluster().num_blocks();
   int4 v = make_int4(0, -1, 0, 0);
@@ -405,7 +416,7 @@ __device__ __noinline__ int join_lists(Row& s, uint32_t* klo, uint32_t* khi) {
       const u64 p = peer(s.list, owner, ranks)[tid - before];
       s.all[tid] = p;
       const float l = logit_of((uint32_t)(p >> kIndexBits));
-      s.all_w[tid] = weight(s.scale, s.tab, l, l >= s.ends);
+      s.all_w[tid] = weight<T>(s.scale, s.tab, l, l >= s.ends);
     }
   }
   __syncthreads();
@@ -483,7 +494,7 @@ __device__ __forceinline__ Cut select(const Pass<T>& pass, Row& s, const Cut& pr
       const int part = part_of(l, pass.first + at);
       if (part < 0) return;
       if (WEIGHTS) {
-        const u64 w = weight(sc, s.tab, l, true);
+        const u64 w = weight<T>(sc, s.tab, l, true);
         const uint32_t wl = (uint32_t)w;
         const uint32_t wh = (uint32_t)(w >> 32) + (atomicAdd(&s.lo[part], wl) + wl < wl);
         if (wh) atomicAdd(&s.hi[part], wh);
@@ -527,7 +538,7 @@ __device__ __forceinline__ Cut select(const Pass<T>& pass, Row& s, const Cut& pr
     });
     tell_keys(s, klo, khi);
     cluster.sync();
-    const int n = join_lists(s, &klo, &khi);
+    const int n = join_lists<T>(s, &klo, &khi);
     if (whole) {
       *listed = n;
       return prior;
@@ -580,10 +591,12 @@ __device__ __forceinline__ u64 times(float x, u64 whole, bool* more) {
                                                       : (lo & ((1ull << shift) - 1)) != 0;
   return shift >= 128 ? 0 : shift >= 64 ? hi >> (shift - 64) : hi << (64 - shift) | lo >> shift;
 }
-// The weight that a nucleus has to reach: at least one step.
-__device__ __forceinline__ u64 share_of(float top_p, u64 whole) {
+// The weight that a nucleus has to reach: at least one step.  *exact: a whole number of steps, which
+// weights of less than half a step, counted as none, put out of reach of those that meet it.
+__device__ __forceinline__ u64 share_of(float top_p, u64 whole, bool* exact) {
   bool more;
   const u64 x = times(fmaxf(top_p, 0.f), whole, &more);
+  *exact = !more && x > 0;
   return max(1ull, x + more);
 }
 // The bar of the draw: sums are whole numbers, and one exceeds u * whole where it exceeds its floor.
@@ -633,7 +646,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   }
   const float mine = value_of(best, T());
   // ---- the largest logit
-  if (tid < 128) s.tab[tid] = make_float2(kPowers.hi[tid], kPowers.lo[tid]);
+  if (tid < 128) {
+    s.tab.hi[tid] = kPowers.hi[tid];
+    s.tab.lo[tid] = kPowers.lo[tid];
+  }
   clear_list(s);
   {
     float hi = mine;
@@ -709,7 +725,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           pass.some(bound, [&](float l, int at) { enlist(s, l, pass.first + at, klo, khi); });
           tell_keys(s, klo, khi);
           cluster.sync();
-          n = join_lists(s, &klo, &khi);
+          n = join_lists<T>(s, &klo, &khi);
           if (n > kList) n = 0;
         }
       } else {
@@ -739,7 +755,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       const u64 place = i < n ? s.all[i] : 0, w = i < n ? s.all_w[i] : 0;
       const bool lead = i < n && (tid & (g - 1)) == 0;
       if (tid == 0) s.cut = ~0ull;
-      if (lead && rank_of == top_k - 1) s.bar = top_p < 1.f ? share_of(top_p, at + w) : ~0ull;  // of K's weight
+      const int lost = __syncthreads_or(lead && rank_of < top_k && w == 0);
+      if (lead && rank_of == top_k - 1) {
+        bool exact = false;
+        s.bar = top_p < 1.f ? share_of(top_p, at + w, &exact) : ~0ull;  // of K's weight
+        if (exact && lost) ++s.bar;
+      }
       __syncthreads();
       const bool keep = rank_of < top_k && at < s.bar && logit_of((uint32_t)(place >> kIndexBits)) >= least;
       if (keep && lead) atomicMin(&s.cut, place);
@@ -843,8 +864,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       pass.each([&](const float (&x)[4], int at) {
         if (!__any_sync(0xffffffffu, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) >= floor)) return;
         Steps44 w[4];
-        weights(sc, s.tab, make_float2(x[0], x[1]), x[0] >= floor, x[1] >= floor, w[0], w[1]);
-        weights(sc, s.tab, make_float2(x[2], x[3]), x[2] >= floor, x[3] >= floor, w[2], w[3]);
+        weights<T>(sc, s.tab, make_float2(x[0], x[1]), x[0] >= floor, x[1] >= floor, w[0], w[1]);
+        weights<T>(sc, s.tab, make_float2(x[2], x[3]), x[2] >= floor, x[3] >= floor, w[2], w[3]);
         if (!nucleus) {
           kept.hi += w[0].hi + w[1].hi + w[2].hi + w[3].hi;
           kept.lo += w[0].lo + w[1].lo + w[2].lo + w[3].lo;
@@ -866,21 +887,40 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         }
       });
       u64 sum = kept.joined();
+      u64 own_sums = 0;   // lane c: kept weights of CTA c
+      bool told = false;  // known already, the runs' in s.scan
       if (nucleus) {
         // ---- top-p's cut
         tell_keys(s, klo, khi);
-        u64 above, whole;
-        block_scan(sum, s.scan, &above);
-        block_scan(rest.joined(), s.scan, &whole);
-        if (tid == 0) s.weight = make_ulonglong2(above, above + whole);
+        sum = warp_sum(sum);
+        const u64 behind = warp_sum(rest.joined());
+        if (lane == 0) {
+          s.scan[warp] = sum;
+          s.all_w[warp] = behind;
+        }
+        if (lane > 0) sum = 0;  // (the warp's sum is one lane's from here on)
+        __syncthreads();
+        if (warp == 0) {
+          const u64 x = warp_sum(lane < kWarps ? s.scan[lane] : 0), y = warp_sum(lane < kWarps ? s.all_w[lane] : 0);
+          if (lane == 0) s.weight = make_ulonglong2(x, x + y);
+        }
+        if (tid < kMaxCluster) s.ranked[tid] = 0;
         cluster.sync();
         ulonglong2 v = make_ulonglong2(0, 0);
         if (lane < ranks) v = *peer(&s.weight, lane, ranks);
-        const u64 before = warp_sum((u64)v.x);
-        whole = warp_sum((u64)v.y);
-        if (tid == 0) s.bar = share_of(top_p, whole);
-        const int n = join_lists(s, &klo, &khi);
-        const u64 target = s.bar;
+        const u64 before = warp_sum((u64)v.x), whole = warp_sum((u64)v.y);
+        bool exact;
+        u64 target = share_of(top_p, whole, &exact);
+        const int n = join_lists<T>(s, &klo, &khi);
+        if (exact) {
+          // (a share of a half does it in every other row, others hardly ever)
+          bool lost = false;
+          pass.some(fmaxf(cut.v, -kTop), [&](float l, int) { lost |= l < ends; });
+          lost = __syncthreads_or(lost);
+          if (tid == 0) s.best = lost;
+          cluster.sync();
+          target += __any_sync(0xffffffffu, lane < ranks && *peer(&s.best, lane, ranks)) ? 1 : 0;
+        }
         if (n <= kList) {
           const int g = group_of(n), i = tid / g;
           int unused;
@@ -889,14 +929,20 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           __syncthreads();
           cut = cut_at(s.cut);
           if (least > cut.v) cut = Cut{least, (int)kIndexMask};
-          // what is kept of the bracket joins the runs' sums
-          const int from = pass.first + warp * pass.run;
-#pragma unroll 1
-          for (int j = lane; j < n; j += 32) {
-            const u64 p = s.all[j];
+          // what is kept of the bracket joins the CTAs' and the runs' sums
+          if (tid < n) {
+            const u64 p = s.all[tid];
             const int k = (int)(kIndexMask - (uint32_t)(p & kIndexMask));
-            if (k >= from && k < from + pass.run && cut.keeps(logit_of((uint32_t)(p >> kIndexBits)), k)) sum += s.all_w[j];
+            const u64 w = s.all_w[tid];
+            if (cut.keeps(logit_of((uint32_t)(p >> kIndexBits)), k)) {
+              const int c = k / a.chunk;
+              add64(s.ranked + c, w);
+              if (c == rank) add64(s.scan + (k - pass.first) / pass.run, w);
+            }
           }
+          __syncthreads();
+          told = true;
+          own_sums = (lane < ranks ? v.x + s.ranked[lane] : 0);
         } else {
           const int width = min(q2, (kBins + 1) << kStepBits) - q1;
           const int shift = max(0, 32 - __clz(width - 1) - kPartBits);
@@ -911,25 +957,25 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
             for (; mask; mask &= mask - 1) {
               const int k = at + __ffs(mask) - 1;
               const float l = pass.logit(k);
-              sum += weight(sc, s.tab, l, cut.keeps(l, pass.first + k));
+              sum += weight<T>(sc, s.tab, l, cut.keeps(l, pass.first + k));
             }
           });
         }
       }
       // ---- the token
-      sum = warp_sum(sum);
-      __syncthreads();  // scan of an earlier pass has been read
-      if (lane == 0) s.scan[warp] = sum;
-      __syncthreads();
-      const u64 own = warp_sum(lane < kWarps ? s.scan[lane] : 0);
-      if (tid == 0) s.weight.x = own;
-      cluster.sync();
-      u64 before = 0;
-      {
-        const u64 x = lane < ranks ? peer(&s.weight, lane, ranks)->x : 0;
-        total = warp_sum(x);
-        before = warp_sum(lane < rank ? x : 0);
+      if (!told) {
+        sum = warp_sum(sum);
+        __syncthreads();  // scan of an earlier pass has been read
+        if (lane == 0) s.scan[warp] = sum;
+        __syncthreads();
+        const u64 own = warp_sum(lane < kWarps ? s.scan[lane] : 0);
+        if (tid == 0) s.sum = own;
+        cluster.sync();
+        own_sums = lane < ranks ? *peer(&s.sum, lane, ranks) : 0;
       }
+      total = warp_sum(own_sums);
+      u64 before = warp_sum(lane < rank ? own_sums : 0);
+      const u64 own = __shfl_sync(0xffffffffu, own_sums, rank);
       if (tid == 0) s.bar = draw_bar(u, total);
       __syncthreads();
       const u64 bar = s.bar;
@@ -949,7 +995,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         auto weight_at = [&](int k) -> u64 {
           if (at + k >= pass.run) return 0;
           const float l = pass.logit(i + k);
-          return weight(sc, s.tab, l, l >= ends && cut.keeps(l, pass.first + i + k));
+          return weight<T>(sc, s.tab, l, l >= ends && cut.keeps(l, pass.first + i + k));
         };
         u64 sum = 0, all;
 #pragma unroll 1
@@ -975,13 +1021,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       __syncthreads();
       inv = s.inv;
     }
+    const bool sparse = cut.v > -kTop;  // few are kept: zeros first, then those
     pass.each([&](const float (&x)[4], int at) {
       const int i = pass.first + at;
       float p[4] = {0.f, 0.f, 0.f, 0.f};
-      if (__any_sync(0xffffffffu, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) >= cut.v)) {
+      unsigned mask = 0;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (cut.keeps(x[k], i + k)) p[k] = weight_f32(sc, x[k]) * inv;
+      for (int k = 0; k < 4; ++k) {
+        mask |= (unsigned)(x[k] >= cut.v) << k;
+        if (!sparse && x[k] >= cut.v) p[k] = weight_f32(sc, x[k]) * inv;
       }
       if (a.probs_vec) {
         if (i < a.V) __stcs(reinterpret_cast<float4*>(out + i), make_float4(p[0], p[1], p[2], p[3]));
@@ -990,6 +1038,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         for (int k = 0; k < 4; ++k)
           if (i + k < a.V) out[i + k] = p[k];
       }
+      if (sparse)
+#pragma unroll 1
+        for (; mask; mask &= mask - 1) {
+          const int k = __ffs(mask) - 1;
+          const float l = pass.logit(at + k);
+          if (cut.keeps(l, i + k)) out[i + k] = weight_f32(sc, l) * inv;
+        }
     });
   }
   // ---- the end

@@ -800,3 +800,24 @@ def test_offsets_beyond_32_bits(dfl):
     tok = dfl.dflash_sample(x, torch.full((9000,), 0.5, device="cuda"))
     # 262144 equal tokens: the first whose running count exceeds half; the last row's one token has all but 5e-4
     assert (tok[:-1] == 131072).all() and tok[-1] == 262143 and dfl.dflash_last_device_error() == 0
+
+
+@pytest.mark.parametrize("top_k", [0, 2, 3, 700])
+def test_sample_shares_that_are_met_exactly(dfl, top_k):
+    """Two equal tokens have half of the weight each, and one of them is half of it; where further tokens
+    follow, however little they weigh, it is less than half."""
+    x = torch.full((3, 3000), -1e30, device="cuda")
+    x[:, 1000], x[:, 2000] = 5.0, 5.0
+    x[1, 7] = 5.0 - 0.36      # e^-36: less than half a step beside the two
+    x[2] = float("-inf")
+    x[2, 1000], x[2, 2000] = 5.0, 5.0
+    s = dict(temperature=0.01, top_p=0.5, top_k=top_k)
+    tok, probs = _sample(dfl, x, 0.9, **s)
+    # (a sum in 64 bits holds e^-36 too; the tokens at -1e30 weigh nothing in 64 bits either, but are above 0)
+    one = [[1000], [1000] if top_k == 2 else [1000, 2000], [1000]]
+    if top_k != 2:
+        one[0] = [1000, 2000]
+    for r in range(3):
+        assert np.flatnonzero(probs[r]).tolist() == one[r]
+        assert tok[r] == one[r][-1]
+    assert dfl.dflash_last_device_error() == 0
