@@ -220,7 +220,7 @@ cudaError_t launch_cache_copy(const CopyArgs& a, cudaStream_t stream);
 // Pages taken, shared and given back (pages.cu).
 struct PoolArgs {
   int32_t *table, *refs, *missing;
-  int32_t* ws;            // [num_pages + 2 * items]
+  int32_t* ws;            // [num_pages + items]
   int R, max_pages, P, num_pages;
   int refs_vec;           // refs may be read in 16-byte pieces
   unsigned* err;

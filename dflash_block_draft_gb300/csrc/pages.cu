@@ -110,7 +110,7 @@ __device__ __forceinline__ int take(const PoolArgs& a, int items, Shared& s, cg:
     found += all;
     cluster.sync();  // s.free has been read; the list and the counts are written
   }
-  cluster.sync();  // first[] too, where no page was looked at
+  if (found == 0) cluster.sync();  // first[], where no round's barrier lay behind it
   for (int i = rank * kWarps + (tid >> 5); i < items; i += kCluster * kWarps) {
     const int want = need(i), from = want ? __ldcg(first + i) : 0;
     for (int j = lane; j < want; j += 32) put(i, j, from + j < found ? __ldcg(list + from + j) : -1);
@@ -190,34 +190,31 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     const int n = __ldcg(f.lens + x);
     return n < 0 || n > most ? -1 : n;
   };
-  // whether the fork's row still holds something, before any row gets its new length
-  for (int i = rank * kThreads + tid; i < f.n; i += kCluster * kThreads) {
+  // (No fork's row is a source or another fork's: what one fork reads no other one writes.)
+  for (int i = rank * kWarps + (tid >> 5); i < f.n; i += kCluster * kWarps) {
     const int n = length(i);
     const bool ok = n >= 0 && __ldcg(f.lens + f.dst[i]) == 0;
-    if (!ok) record_error(a.err, DFLASH_ERR_INVALID);
-    f.copy_rows[i] = ok ? n % a.P : 0;
-    f.copy_src[i] = ok && n % a.P ? __ldcg(a.table + (long long)f.src[i] * a.max_pages + n / a.P) : -1;
-    f.copy_dst[i] = -1;
-    a.ws[a.num_pages + f.n + i] = ok;
-  }
-  cluster.sync();
-  const int32_t* ok = a.ws + a.num_pages + f.n;
-  for (int i = rank * kWarps + (tid >> 5); i < f.n; i += kCluster * kWarps) {
-    if (!__ldcg(ok + i)) continue;
-    const int n = length(i), full = n / a.P;
-    const int32_t* from = a.table + (long long)f.src[i] * a.max_pages;
-    int32_t* to = a.table + (long long)f.dst[i] * a.max_pages;
+    __syncwarp();  // read by all lanes before one of them writes it
+    const int full = ok ? n / a.P : 0, rest = ok ? n % a.P : 0;
+    const int32_t* from = a.table + (long long)(ok ? f.src[i] : 0) * a.max_pages;
+    int32_t* to = a.table + (long long)(ok ? f.dst[i] : 0) * a.max_pages;
     for (int j = lane; j < full; j += 32) {
       const int page = from[j];
       to[j] = page;
       if (page >= 0 && page < a.num_pages) atomicAdd(a.refs + page, 1);
       else record_error(a.err, DFLASH_ERR_INVALID);
     }
-    if (lane == 0) f.lens[f.dst[i]] = n;
+    if (lane == 0) {
+      if (ok) f.lens[f.dst[i]] = n;
+      else record_error(a.err, DFLASH_ERR_INVALID);
+      f.copy_rows[i] = rest;
+      f.copy_src[i] = rest ? from[full] : -1;
+      f.copy_dst[i] = -1;
+    }
   }
   cluster.sync();
   const int missing = take(
-      a, f.n, s, cluster, [&](int i) { return __ldcg(ok + i) && __ldcg(f.copy_rows + i) > 0 ? 1 : 0; },
+      a, f.n, s, cluster, [&](int i) { return __ldcg(f.copy_rows + i) > 0 ? 1 : 0; },
       [&](int i, int, int page) {
         a.table[(long long)f.dst[i] * a.max_pages + length(i) / a.P] = page;
         f.copy_dst[i] = page;
@@ -227,7 +224,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
 
 }  // namespace
 
-size_t pool_workspace_bytes(int num_pages, int items) { return sizeof(int32_t) * ((size_t)num_pages + 2 * (size_t)items); }
+size_t pool_workspace_bytes(int num_pages, int items) { return sizeof(int32_t) * ((size_t)num_pages + (size_t)items); }
 
 cudaError_t launch_pages_resize(const PoolArgs& a, const int32_t* old_lens, const int32_t* new_lens,
                                 cudaStream_t stream) {
