@@ -212,12 +212,12 @@ __global__ void __launch_bounds__(Simt<T, BM, DMAX>::kThreads, Simt<T, BM, DMAX>
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           float mx = -INFINITY;
-          uint64_t vis[1] = {~0ull};
+          TreeBits<1> vis = {{~0ull}};
           if (TREE && k0 + BN > base)  // new tokens lie in this tile
-            tree_bits<1>(a.parents + pc.q.q0, min((f0 + 4 * ty + i) / a.G, pc.q.n - 1), base - k0, vis);
+            vis = tree_bits<1>(a.parents + pc.q.q0, min((f0 + 4 * ty + i) / a.G, pc.q.n - 1), base - k0);
 #pragma unroll
           for (int j = 0; j < CT; ++j) {
-            if (k0 + tx + TX * j >= lim[i] || (TREE && !((vis[0] >> (tx + TX * j)) & 1))) x[i][j] = -INFINITY;
+            if (k0 + tx + TX * j >= lim[i] || (TREE && !((vis.w[0] >> (tx + TX * j)) & 1))) x[i][j] = -INFINITY;
             mx = fmaxf(mx, x[i][j]);
           }
 #pragma unroll

@@ -449,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool row_ok = row < tile_rows && f < pc.q.n * a.G;
       const int tok = f / a.G;
       const int base = pc.q.kv - pc.q.n;  // position of the first new token
-      const int lim = !row_ok ? 0 : a.causal && !TREE ? max(0, base + tok + 1) : pc.q.kv;
+      const int lim = !row_ok ? 0 : a.causal ? max(0, base + tok + 1) : pc.q.kv;  // (not TREE)
       const bool warp_ok = __any_sync(0xffffffffu, row_ok);
       float m_used = -INFINITY, l = 0.f;
       bool had[2] = {PAIR, PAIR};
@@ -478,9 +478,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::fence_proxy_async_smem();
         }
         // TREE: what the row sees of a tile with new tokens in it, while S is on its way
-        const bool among_new = TREE && k0 + kBN > base;
-        uint64_t vis[2] = {0, 0};
-        if (among_new && row_ok) tree_bits<2>(a.parents + pc.q.q0, tok, base - k0, vis);
+        const bool hides = TREE && (k0 + kBN > base || !row_ok);
+        TreeBits<2> vis;
+        if (hides) vis = tree_bits<2>(a.parents + pc.q.q0, row_ok ? tok : -1, base - k0);
         if (!__all_sync(0xffffffffu, ctl.wait(C::S_FULL + half, mine & 1u))) {
           stop = true;
           break;
@@ -496,8 +496,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::tmem_ld32(s_col + 64u * hh, reinterpret_cast<uint32_t*>(x));
             ptx::tmem_ld32(s_col + 64u * hh + 32u, reinterpret_cast<uint32_t*>(x) + 32);
             ptx::tmem_wait_ld();
-            if (among_new) hide_bits(x, hh ? vis[1] : vis[0]);
-            else hide64(x, 64 * hh, lim - k0);
+            if (!TREE) hide64(x, 64 * hh, lim - k0);
+            else if (hides) hide_bits(x, hh ? vis.w[1] : vis.w[0]);
             const float mh = max64(x) * c2;
             const bool raise = mh > m_used + 8.0f;  // also when m is still -inf and this half sees a key
             const bool scale_o = raise && m_used != -INFINITY;

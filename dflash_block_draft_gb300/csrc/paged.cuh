@@ -88,22 +88,30 @@ __device__ __forceinline__ long long length_of(const PagedArgs& a, const Req& q,
 // What node `tok` of a tree sees of the 64 W positions from k0 on, `first` = (position of
 // node 0) - k0: the context in front of the tree, itself, and its chain of parents,
 // which is followed as far as the tile's beginning.  A parent that does not lie in front of
-// its node ends the chain, so that every chain ends.
+// its node ends the chain, so that every chain ends.  tok < 0: nothing at all.
 template <int W>
-__device__ __forceinline__ void tree_bits(const int32_t* __restrict__ parents, int tok, int first, uint64_t (&vis)[W]) {
+struct TreeBits {
+  uint64_t w[W];
+};
+template <int W>
+__device__ __forceinline__ TreeBits<W> tree_bits(const int32_t* __restrict__ parents, int tok, int first) {
+  TreeBits<W> vis;
 #pragma unroll
   for (int w = 0; w < W; ++w) {
     const int c = first - 64 * w;  // context positions among these 64
-    vis[w] = c <= 0 ? 0ull : c >= 64 ? ~0ull : (1ull << c) - 1ull;
+    vis.w[w] = c <= 0 || tok < 0 ? 0ull : c >= 64 ? ~0ull : (1ull << c) - 1ull;
   }
   for (int j = tok; j >= 0 && first + j >= 0;) {
     const int c = first + j;
+    if (c < 64 * W) {
+      const uint64_t bit = 1ull << (c & 63);
 #pragma unroll
-    for (int w = 0; w < W; ++w)
-      if (c >> 6 == w) vis[w] |= 1ull << (c & 63);
+      for (int w = 0; w < W; ++w) vis.w[w] |= c >> 6 == w ? bit : 0ull;
+    }
     const int up = __ldg(parents + j);
     j = up < j ? up : -1;
   }
+  return vis;
 }
 
 // a / b for a >= 0, b > 0, in 32 bits where both fit (64-bit divisions are long).
