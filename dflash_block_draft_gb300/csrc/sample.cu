@@ -49,7 +49,8 @@ typedef unsigned long long u64;
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBins = 2048;       // of the masses: 4 a thread
+constexpr int kBins = 4096;       // of the masses
+constexpr int kCoarse = kBins / kThreads;  // bins that a thread looks at together
 constexpr int kParts = 512;       // of a range whose border is looked for: one a thread
 constexpr int kPartBits = 9;
 constexpr int kList = 256;        // tokens whose order is found by comparing all pairs
@@ -59,12 +60,13 @@ constexpr int kIndexBits = 19;    // of a token's number
 constexpr uint32_t kIndexMask = (1u << kIndexBits) - 1;
 constexpr int kChunkMax = 49152;  // logits a CTA can hold
 static_assert(DFLASH_SAMPLE_MAX_V <= kMaxCluster * kChunkMax && DFLASH_SAMPLE_MAX_V <= (int)kIndexMask + 1, "vocabulary");
-static_assert(kBins == 4 * kThreads && kParts == kThreads && kThreads >= 2 * kList, "thread layout");
+static_assert(kCoarse == 8 && kParts == kThreads && kThreads >= 2 * kList, "thread layout");
 constexpr float kTop = 0x1p126f;  // logits above count as it, those below -kTop are no choice: differences are finite
-// Margin of the masses of top-p's first look: they are off by less than 6e-5 (bins linear within:
-// 2.9e-5, masses rounded down: 1.6e-5, fp32 distances and sums: 1e-5),
-// on either side of the comparison.
-constexpr float kOver = 1.0002f;
+// Margin of the masses of top-p's first look, on either side of the comparison: they are off by
+// less than 3.4e-5 (bins linear within 7.2e-6, masses rounded down 1.5e-5, their slope's rounding
+// 4.6e-6, fp32 distances, powers and sums 7e-6).
+constexpr float kOver = 1.00008f;
+constexpr float kBinRatio = 0.99241175f;  // e^(-31.2 / 4096)
 
 // ------------------------------------------------------------------ weights
 // 2^(j / 128) as a float and what it lacks.
@@ -204,6 +206,7 @@ __device__ __forceinline__ float value_of(uint32_t w, __nv_bfloat16) {
 
 struct Row {
   // what a CTA tells the others
+  float coarse[kThreads];          // masses of kCoarse bins each
   float top[kThreads];             // largest logit of 1 to 8 neighbouring threads, 512 in the cluster
   alignas(8) float2 low;           // smallest of the threads' maxima; threads that have logits
   alignas(16) int4 listed;         // tokens of the range; the smallest and the largest of their keys
@@ -216,13 +219,15 @@ struct Row {
   // its own
   Table tab;
   u64 scan[kWarps];
-  float scan_f[kWarps];
+  float scan_f[kWarps], coarse_before[kThreads];
   u64 all[kList], all_w[kList];
   u64 ranked[kMaxCluster];         // kept weights of the bracket, each CTA's
   uint32_t keys[kWarps], key;
   u64 found_before;
   int found, b1, b2;
   u64 cut, bar;
+  double log_min_p;
+  int first;          // the first token that is kept (a random number of 0)
   Scale scale;
   float ends, least, inv;  // no weight below `ends`; min-p's bound; 1 / kept weights
 };
@@ -351,7 +356,7 @@ struct Pass {
   }
 };
 
-// A logit's distance from the largest one in 2048 * 1024 steps of a range, by the adder's
+// A logit's distance from the largest one in 2^21 steps of a range, by the adder's
 // bits.  Never falls as the logit falls.
 struct Steps {
   float m, mul;
@@ -360,7 +365,8 @@ struct Steps {
     return __float_as_int(fmaf(m - l, mul, 0x1.8p23f)) - __float_as_int(0x1.8p23f);
   }
 };
-constexpr int kStepBits = 10;  // steps of a bin of the masses
+constexpr int kStepBits = 9;  // steps of a bin of the masses
+static_assert(kBins << kStepBits == 1 << 21, "steps");
 
 __device__ __forceinline__ void clear_list(Row& s) {
   if (threadIdx.x == 0) s.listed = make_int4(0, -1, 0, 0);
@@ -575,10 +581,8 @@ __device__ __forceinline__ Scale scale_of(float m, float t, float* ends) {
   *ends = fmaxf(__fmaf_ru(-31.1916f, t, m), -kTop);
   return Scale{m, c, left / t};
 }
-// The smallest logit whose weight is min_p at least (64-bit floating point is slow here: one thread).
-__device__ __noinline__ float min_p_bound(float m, float t, float min_p) {
-  return __double2float_ru((double)m + log(min((double)min_p, 1.0)) * (double)t);
-}
+// (64-bit floating point is slow here: one thread, while the others wait for the row.)
+__device__ __noinline__ double log_of(float min_p) { return log(min((double)min_p, 1.0)); }
 
 // floor(x * whole) for x in [0, 1), exactly, and whether that is less than the product.
 __device__ __forceinline__ u64 times(float x, u64 whole, bool* more) {
@@ -661,7 +665,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       if (tid == 0) s.low = make_float2(logit_of(least), (float)threads);
     }
   }
-  cluster.sync();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  if (tid == kThreads - 32 && min_p > 0.f) s.log_min_p = log_of(min_p);
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   const float top = peer(s.top, tid * ranks / kThreads, ranks)[tid % (kThreads / ranks)];
   float m = logit_of(~block_least(s, ~key_of(top)));
   if (m > kTop) {
@@ -697,7 +704,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     if (tid == 0) {
       s.scale = sc;
       s.ends = ends;
-      if (min_p > 0.f) s.least = min_p_bound(m, t, min_p);
+      // the smallest logit whose weight is min_p at least
+      if (min_p > 0.f) s.least = __double2float_ru((double)m + s.log_min_p * (double)t);
     }
     __syncthreads();
     if (min_p > 0.f) least = s.least;
@@ -770,15 +778,18 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       // kept weights by rising numbers
       const u64 turned = place & kIndexMask;
       u64 upto = 0, whole = 0;
+      int earlier = 0;
 #pragma unroll 2
       for (int j = tid & (g - 1); j < n; j += g) {
         const u64 x = s.all[j], y = x >= edge ? s.all_w[j] : 0;
         whole += y;
         if ((x & kIndexMask) >= turned) upto += y;
+        earlier += x >= edge && (x & kIndexMask) > turned;
       }
       for (int o = g >> 1; o > 0; o >>= 1) {
         upto += __shfl_xor_sync(0xffffffffu, upto, o);
         whole += __shfl_xor_sync(0xffffffffu, whole, o);
+        earlier += __shfl_xor_sync(0xffffffffu, earlier, o);
       }
       if (tid == 0) {
         s.weight.x = whole;
@@ -786,7 +797,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       }
       __syncthreads();
       total = s.weight.x;
-      if (rank == 0 && lead && place >= edge && upto - w <= s.bar && s.bar < upto)
+      // (0 draws the first token that is kept, however little it weighs)
+      if (rank == 0 && lead && place >= edge && (u > 0.f ? upto - w <= s.bar && s.bar < upto : earlier == 0))
         token = (int)(kIndexMask - (uint32_t)turned);
     } else {
       if (limited) {
@@ -803,9 +815,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       if (nucleus) {
         // ---- where top-p's cut can lie: the weights' masses in 2048 steps
         if (limited) cluster.sync();  // the other CTAs have read this one's histogram
-        *reinterpret_cast<uint4*>(&s.lo[4 * tid]) = make_uint4(0, 0, 0, 0);
+        uint4* bins = reinterpret_cast<uint4*>(&s.lo[kCoarse * tid]);
+        bins[0] = bins[1] = make_uint4(0, 0, 0, 0);
         if (tid == 0) {
-          s.b1 = kBins;
+          s.b1 = kThreads;
           s.b2 = -1;
         }
         __syncthreads();
@@ -813,43 +826,64 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const int q = steps.at(x[k]);
-            // the weight within its bin, linear from 1 to e^(-31.2 / 2048), in 1 / 32768
-            const uint32_t mass = (uint32_t)((32768 << kStepBits) - 495 * (q & 1023)) >> kStepBits;
+            // the weight within its bin, linear from 1 to e^(-31.2 / 4096), in 1 / 65536
+            const uint32_t mass = (uint32_t)((65536 << kStepBits) - 497 * (q & 511)) >> kStepBits;
             if (x[k] >= floor) atomicAdd(&s.lo[min(kBins - 1, q >> kStepBits)], mass);
           }
         });
+        __syncthreads();
+        const float first = ptx::ex2(-0.0879142291f * (float)tid);  // at the first bin's beginning: 31.2 / 512 log2(e)
+        {
+          const uint4 x = bins[0], y = bins[1];
+          const uint32_t v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+          float mass = 0.f;
+#pragma unroll
+          for (int k = 7; k >= 0; --k) mass = fmaf(mass, kBinRatio, (float)v[k]);
+          s.coarse[tid] = mass * first;
+        }
         cluster.sync();
         clear_list(s);
-        // ---- merged, every CTA for itself
-        float v[4] = {0.f, 0.f, 0.f, 0.f};
-        uint4 x[kMaxCluster];  // (all reads in flight at once)
+        // ---- merged: eight bins together, then those that the border lies in by themselves
+        float part[kMaxCluster];  // (all reads in flight at once)
 #pragma unroll
-        for (int c = 0; c < kMaxCluster; ++c)
-          x[c] = *reinterpret_cast<const uint4*>(cluster.map_shared_rank(&s.lo[4 * tid], c & (ranks - 1)));
+        for (int c = 0; c < kMaxCluster; ++c) part[c] = *cluster.map_shared_rank(&s.coarse[tid], c & (ranks - 1));
+        float v = 0.f;
 #pragma unroll
-        for (int c = 0; c < kMaxCluster; ++c)
-          if (c < ranks) {
-            v[0] += (float)x[c].x;
-            v[1] += (float)x[c].y;
-            v[2] += (float)x[c].z;
-            v[3] += (float)x[c].w;
-          }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] *= ptx::ex2(-0.02197855f * (float)(4 * tid + k));  // 31.2 / 2048 log2(e)
+        for (int c = 0; c < kMaxCluster; ++c) v += c < ranks ? part[c] : 0.f;
         float all;
-        float c0 = block_scan(v[0] + v[1] + v[2] + v[3], s.scan_f, &all);
+        const float c0 = block_scan(v, s.scan_f, &all), c1 = c0 + v;
         const float want = fmaxf(top_p, 1e-6f) * all;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float c1 = c0 + v[k];
-          // (rounding can show two threads the same border, or none: then the bracket is the wider one)
-          if (c1 * kOver >= want && !(c0 * kOver >= want)) atomicMin(&s.b1, 4 * tid + k);
-          if (c1 >= want * kOver && !(c0 >= want * kOver)) atomicMax(&s.b2, 4 * tid + k);
-          c0 = c1;
-        }
+        // (rounding can show two threads the same border, or none: then the bracket is the wider one)
+        s.coarse_before[tid] = c0;
+        if (c1 * kOver >= want && !(c0 * kOver >= want)) atomicMin(&s.b1, tid);
+        if (c1 >= want * kOver && !(c0 >= want * kOver)) atomicMax(&s.b2, tid);
         __syncthreads();
-        q1 = s.b1 == kBins ? 0 : s.b1 << kStepBits;
-        q2 = s.b2 < 0 || s.b2 == kBins - 1 ? INT_MAX : (s.b2 + 1) << kStepBits;
+        const int lo8 = s.b1 == kThreads ? 0 : s.b1, hi8 = s.b2 < 0 ? kThreads - 1 : s.b2;
+        q1 = lo8 * kCoarse << kStepBits;
+        q2 = hi8 == kThreads - 1 ? INT_MAX : (hi8 + 1) * kCoarse << kStepBits;
+        if (hi8 - lo8 < 4) {  // 32 bins at most: every warp for itself
+          const int bin = min(kBins - 1, lo8 * kCoarse + lane);
+          uint32_t w[kMaxCluster];
+#pragma unroll
+          for (int c = 0; c < kMaxCluster; ++c) w[c] = *cluster.map_shared_rank(&s.lo[bin], c & (ranks - 1));
+          float mass = 0.f;
+#pragma unroll
+          for (int c = 0; c < kMaxCluster; ++c) mass += c < ranks ? (float)w[c] : 0.f;
+          mass *= ptx::ex2(-0.0109892786f * (float)bin);  // 31.2 / 4096 log2(e)
+          float upto = mass;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const float u = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += u;
+          }
+          upto += s.coarse_before[lo8];
+          const unsigned may = __ballot_sync(0xffffffffu, upto * kOver >= want), must = __ballot_sync(0xffffffffu, upto >= want * kOver);
+          // (where none of these bins reaches it, rounding hid the border: the last one)
+          const int end = (hi8 - lo8 + 1) * kCoarse - 1;
+          const int b1 = may ? min(__ffs(may) - 1, end) : end, b2 = must ? min(__ffs(must) - 1, end) : end;
+          q1 = (lo8 * kCoarse + b1) << kStepBits;
+          q2 = lo8 * kCoarse + b2 >= kBins - 1 ? INT_MAX : (lo8 * kCoarse + b2 + 1) << kStepBits;
+        }
         // min-p ends in front of the bracket: top-p takes nothing away
         if (least >= ends && steps.at(least) < q1) nucleus = false;
       }
@@ -976,10 +1010,21 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       total = warp_sum(own_sums);
       u64 before = warp_sum(lane < rank ? own_sums : 0);
       const u64 own = __shfl_sync(0xffffffffu, own_sums, rank);
-      if (tid == 0) s.bar = draw_bar(u, total);
-      __syncthreads();
-      const u64 bar = s.bar;
-      if (before <= bar && bar < before + own) {  // one CTA
+      if (!(u > 0.f)) {  // the first token that is kept, however little it weighs
+        if (tid == 0) s.first = INT_MAX;
+        __syncthreads();
+        pass.some(cut.v, [&](float l, int at) {
+          if (cut.keeps(l, pass.first + at)) atomicMin(&s.first, pass.first + at);
+        });
+        cluster.sync();
+        const int first = lane < ranks ? *peer(&s.first, lane, ranks) : INT_MAX;
+        if (rank == 0) {
+          const int best = (int)__reduce_min_sync(0xffffffffu, (unsigned)first);
+          if (tid == 0) token = best;
+        }
+      }
+      const u64 bar = draw_bar(u, total);
+      if (u > 0.f && before <= bar && bar < before + own) {  // one CTA
         // the first run whose end passes the bar
         u64 upto = lane < kWarps ? s.scan[lane] : 0;
 #pragma unroll

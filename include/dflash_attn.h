@@ -534,7 +534,7 @@ DFLASH_API dflash_status_t dflash_verify(const dflash_verify_dims_t* dims, const
  * leaves the filter out; a temperature below 2^-100 counts as 2^-100.
  * Weights are held in steps of 2^-44 of the largest and added up as whole numbers: the
  * result does not depend on the order of the sums (a w below 2^-45 counts as zero; its
- * probability is still written).  V up to DFLASH_SAMPLE_MAX_V.
+ * probability is still written, and u = 0 draws the first token of S whatever it weighs).  V up to DFLASH_SAMPLE_MAX_V.
  */
 #define DFLASH_SAMPLE_MAX_V 393216
 typedef struct {
