@@ -8,28 +8,42 @@
 // "cut", a logit and a token's number), and the token is the first one, in the order of the
 // numbers, whose running sum of kept weights exceeds u times the whole.
 //
-// A cluster of 1 to 8 CTAs takes a row and holds it in shared memory: the logits are
-// read from memory once.  There
-//   the largest logit;
-//   top-k: a histogram of counts over 2048 equal steps of the logit, from the largest one
-//     down to the smallest of the threads' maxima (as many tokens as there are threads lie
-//     above it), merged through distributed shared memory; the tokens in the step where
-//     the count is reached go into a list (at most 256; else the step is divided again, by the
-//     bits of logit and number, so that ties divide too), whose order is found by comparing
-//     all pairs;
-//   top-p: the same with weights instead of counts, over the steps down to where weights
-//     end (31.2 T);
-//   the kept weights' sums by runs of tokens, one exchange, and the run that passes u times
+// A cluster of 1 to 8 CTAs takes a row and holds it in shared memory: the logits are read
+// from memory once, by 16 bytes a thread.  Then
+//   the largest logit, and the maxima of 512 groups of threads (one exchange);
+//   top-k up to 160: a bound that k of the groups reach, found by halving, so that at least k
+//     tokens lie above it and about k + k^2 / 1000 more; they go into a list of 256 whose order
+//     comes from comparing all pairs, and everything else is worked out from the list;
+//   larger k: the tokens above the bound in 512 equal steps of the logit, counted, the counts
+//     merged through distributed shared memory, and the step in which k is reached listed (or
+//     divided again, by the bits of logit and number, so that ties divide too);
+//   top-p: the weights' approximate masses in 4096 equal steps say between which logits the
+//     cut must lie; the exact pass over all tokens adds up what is in front of them and lists
+//     what is between, and the exact border falls in the list (or, where that holds too
+//     many, is looked for as top-k's);
+//   the sums of kept weights by runs of tokens, one exchange, and the run that passes u times
 //     the whole once more, a few tokens a thread.
 //
+// Bound by instructions: a weight costs some 25, a look at a logit 2 to 15, and what a row
+// costs besides (barriers, exchanges, the list) is as much as 8000 tokens of a CTA.  Two CTAs of
+// 512 threads an SM, one row's wait under the other's work.  Measured: 64 rows of 131072 bf16
+// logits with temperature alone 21.5 us; 1664 rows of 32000 with top-k 40 in most of them 93;
+// 128 rows of 131072 fp32 with top-p and the distributions written 131; 4 rows of 32000 9.5.
+// (With a histogram of all weights for top-p and a second exact pass, 128 rows took 251 us;
+// top-k by a histogram of everything above the least of the threads' maxima, 4 rows 17.)  The
+// kernel runs once through most of its code, which was 190 KB where loops were copied and
+// functions inlined: 4 rows then took 29 us.
+//
 // Weights are whole steps of 2^-44 of the largest one, added up as integers, so that no sum
-// depends on the order, the number of CTAs or the threads' timing.  A weight costs 13 packed fp32
-// instructions for a pair in bf16's 10, and 9 others: l - m, times log2(e) / T as two floats; 2^y
-// from a table of 2^(j / 128) in two floats and a polynomial of degree 3; the bits of sums with 2.5
-// and 1.5 2^-21 count the steps, as in verify.cu.  The weights' errors, 2^-33.5 rms, are
-// each other's by chance and add up to a border's as their root: of a vocabulary of 131072 every
-// 10^7th row would draw another token than the real numbers (every 50th with fp32 sums of weights
-// that are off in one direction).  64-bit floating point runs at a hundredth of fp32's rate.
+// depends on the order, the number of CTAs or the threads' timing.  A pair of weights takes 19
+// packed fp32 instructions in bf16 and 25 in fp32, and each some 9 others: l - m, times
+// log2(e) / T as two floats; 2^y from a table of 2^(j / 128) in two floats and a polynomial of
+// degree 3; the bits of sums with 2.5 and 1.5 2^-21 count the steps, as in verify.cu.  The
+// weights' errors, 2^-33.5 rms, are each other's by chance and add up to a border's as their
+// root: of a vocabulary of 131072 every 10^7th row would draw another token than the real numbers
+// (every 50th with fp32 sums of weights that are off in one direction).  Twice the instructions
+// for 2^-40 took 1.5 times as long, and neither differed from 64-bit sums in 25000 rows; 64-bit
+// floating point runs at a hundredth of fp32's rate.
 #include <cooperative_groups.h>
 #include <limits.h>
 #include <math.h>
@@ -813,7 +827,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       const Steps steps(m, 31.2f * t);
       float floor = fmaxf(ends, cut.v);
       if (nucleus) {
-        // ---- where top-p's cut can lie: the weights' masses in 2048 steps
+        // ---- where top-p's cut can lie: the weights' masses in 4096 steps
         if (limited) cluster.sync();  // the other CTAs have read this one's histogram
         uint4* bins = reinterpret_cast<uint4*>(&s.lo[kCoarse * tid]);
         bins[0] = bins[1] = make_uint4(0, 0, 0, 0);

@@ -526,7 +526,8 @@ DFLASH_API dflash_status_t dflash_verify(const dflash_verify_dims_t* dims, const
  * or draft_probs of dflash_verify blocks are verified against the filtered distribution.
  *   logits [N, V] of dtype, rows logits_stride elements apart (0: V); u [N] fp32 in
  *   [0, 1); temperature, top_p, min_p [N] fp32 and top_k [N] int32, each nullable (1, 1, 0, 0);
- *   tokens [N] int32; probs [N, V] fp32, nullable, rows probs_stride elements apart (0: V).
+ *   tokens [N] int32; probs [N, V] fp32, nullable, rows probs_stride elements apart (0: V);
+ *   probs may be the fp32 logits themselves.
  * A logit below -2^126 (-inf, a type's lowest value: a masked token) and NaN are no
  * choice; one above 2^126 counts as 2^126.
  * A row without a choice, and one whose temperature is negative, infinite or NaN, is

@@ -821,3 +821,26 @@ def test_sample_shares_that_are_met_exactly(dfl, top_k):
         assert np.flatnonzero(probs[r]).tolist() == one[r]
         assert tok[r] == one[r][-1]
     assert dfl.dflash_last_device_error() == 0
+
+
+def test_sample_a_random_number_of_0_draws_the_first_kept_token(dfl):
+    """Also where it weighs less than a step of the sums; with and without a list of the kept."""
+    x = torch.zeros((1, 3000), device="cuda")
+    x[0, 5:] = 40.0 + torch.arange(2995, device="cuda") * 1e-3
+    x[0, :5] = float("-inf")
+    x[0, 3] = 1.0
+    for s, want in ((dict(), 3), (dict(top_k=100), 2900), (dict(top_k=2996), 3), (dict(top_p=0.999), None),
+                    (dict(temperature=0.0), 2999), (dict(min_p=0.5), None)):
+        tok, probs = _sample(dfl, x, 0.0, **s)
+        assert tok[0] == (np.flatnonzero(probs[0])[0] if want is None else want)
+    assert dfl.dflash_last_device_error() == 0
+
+
+@pytest.mark.parametrize("V", [4096, 1001])
+def test_sample_distributions_in_place_of_the_logits(dfl, V):
+    rng = np.random.default_rng(17)
+    x, u = _rand(rng, (40, V), "fp32", 2.0), torch.from_numpy(rng.random(40, np.float32)).cuda()
+    k = _i32([0, 30] * 20)
+    probs = torch.empty_like(x)
+    tok = dfl.dflash_sample(x, u, top_k=k, probs=probs)
+    assert torch.equal(dfl.dflash_sample(x, u, top_k=k, probs=x), tok) and torch.equal(x, probs)
