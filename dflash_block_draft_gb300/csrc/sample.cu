@@ -1146,15 +1146,19 @@ cudaError_t launch_sample(SampleArgs a, bool bf16, cudaStream_t stream) {
   const int esz = bf16 ? 2 : 4, n = 16 / esz;
   const bool vec = a.V % n == 0 && ((uintptr_t)a.x & 15u) == 0 && (a.N == 1 || a.xs % n == 0);
   a.probs_vec = a.V % 4 == 0 && ((uintptr_t)a.probs & 15u) == 0 && (a.N == 1 || a.ps % 4 == 0);
-  // CTAs a row: as few as hold a share of 64 KB (two CTAs an SM, so that one row comes in
-  // while another is worked on), more while the launch stays within one wave.
+  // CTAs a row: as few as hold a share of 64 KB (two CTAs an SM, so that one row comes in while
+  // another is worked on), more while there is an SM for each.  What a row costs besides its
+  // tokens is every CTA's: 1664 rows of 32000 bf16 logits take 95 us with one CTA, 140 with two and
+  // 260 with four; 128 of 131072 fp32 134 with eight (64 KB) and 149 with four; 64 of 131072 bf16
+  // 25 with four and 32 with eight.  With few rows the share of the tokens counts: 16 rows of
+  // 32000 fp32 10.6, 12.6 and 16.8 us with eight, two and one, one row of 131072 12.5 with eight and 16.5 with four.
   auto chunk_of = [&](int ranks) {
     const int unit = kThreads * n;
     return ((a.V + ranks - 1) / ranks + unit - 1) / unit * unit;
   };
   int ranks = 1;
   while (ranks < kMaxCluster && chunk_of(ranks) * esz > 65536) ranks *= 2;
-  while (ranks < kMaxCluster && (long long)a.N * ranks * 2 <= 2 * 152 && chunk_of(ranks) > kThreads * n) ranks *= 2;
+  while (ranks < kMaxCluster && (long long)a.N * ranks * 2 <= 152 && chunk_of(ranks) > kThreads * n) ranks *= 2;
   a.chunk = chunk_of(ranks);
   const size_t smem = (size_t)a.chunk * esz;
   if (bf16) return vec ? run<__nv_bfloat16, true>(a, ranks, smem, stream) : run<__nv_bfloat16, false>(a, ranks, smem, stream);
