@@ -18,6 +18,8 @@
 #include <initializer_list>
 #include <optional>
 #include <string>
+#include <utility>
+#include <vector>
 
 #include "dflash_attn.h"
 
@@ -107,16 +109,17 @@ void* tokens(const at::Tensor& t, const char* name, int dev, at::ScalarType type
   *stride = T > 1 && t.numel() > 0 ? t.stride(0) : 0;
   return t.data_ptr();
 }
-// Of [pages, page_size, H_kv, D] whose pages are each contiguous.
+// Of [pages, page_size, H_kv, D] whose pages are each contiguous, the last four axes of t.
 void* pages(const at::Tensor& t, const char* name, int dev, at::ScalarType type, at::IntArrayRef shape,
             int64_t* stride) {
   common(t, name, dev, type);
   if (t.sizes() != shape) refuse(std::string(name) + " must be " + list(shape) + ", got " + list(t.sizes()));
-  const int64_t n = shape[0], P = shape[1], H = shape[2], D = shape[3];
-  if (t.numel() > 0 && ((D > 1 && t.stride(3) != 1) || (H > 1 && t.stride(2) != D) ||
-                        (P > 1 && t.stride(1) != H * D) || (n > 1 && t.stride(0) < P * H * D)))
+  const at::IntArrayRef s = shape.slice(shape.size() - 4), st = t.strides().slice(shape.size() - 4);
+  const int64_t n = s[0], P = s[1], H = s[2], D = s[3];
+  if (t.numel() > 0 && ((D > 1 && st[3] != 1) || (H > 1 && st[2] != D) || (P > 1 && st[1] != H * D) ||
+                        (n > 1 && st[0] < P * H * D)))
     refuse(std::string("the pages of ") + name + " must be contiguous");
-  *stride = n > 1 && t.numel() > 0 ? t.stride(0) : 0;
+  *stride = n > 1 && t.numel() > 0 ? st[0] : 0;
   return t.data_ptr();
 }
 
@@ -485,6 +488,52 @@ PyObject* verify(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// Several int32 results in one allocation (each costs 1.2 us of a call that takes 2 besides):
+// views of one buffer, 256 bytes apart.  Those that the caller gives are taken as they are.
+class Ints {
+ public:
+  explicit Ints(const at::Tensor& like) : like_(like) {}
+  // A result of this shape, which make() allocates: at(0) for the first, and so on.
+  void want(PyObject* given, const char* name, std::vector<int64_t> shape) {
+    const at::Tensor* t = tensor(given, name);
+    parts_.push_back({t ? *t : at::Tensor(), name, std::move(shape), used_});
+    if (t) return;
+    int64_t n = 1;
+    for (const int64_t d : parts_.back().shape) n *= d;
+    used_ += (n + 63) / 64 * 64;
+    any_ = true;
+  }
+  void make(int dev) {
+    at::Tensor block;
+    if (any_) block = fresh(like_, {used_}, at::kInt);
+    for (Part& p : parts_) {
+      if (!p.t.defined()) {
+        p.t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(block.storage()), block.key_set(), block.dtype());
+        p.t.unsafeGetTensorImpl()->set_sizes_contiguous(p.shape);
+        p.t.unsafeGetTensorImpl()->set_storage_offset(p.offset);
+      }
+      common(p.t, p.name, dev, at::kInt);
+      if (p.t.sizes() != at::IntArrayRef(p.shape))
+        refuse(std::string(p.name) + " must be " + list(p.shape) + ", got " + list(p.t.sizes()));
+      if (!p.t.is_contiguous()) refuse(std::string(p.name) + " must be contiguous");
+    }
+  }
+  const at::Tensor& at(int i) const { return parts_[i].t; }
+  int32_t* ptr(int i) const { return (int32_t*)parts_[i].t.data_ptr(); }
+
+ private:
+  struct Part {
+    at::Tensor t;
+    const char* name;
+    std::vector<int64_t> shape;
+    int64_t offset;
+  };
+  const at::Tensor& like_;
+  std::vector<Part> parts_;
+  int64_t used_ = 0;
+  bool any_ = false;
+};
+
 // (logits, u, temperature, top_k, top_p, min_p, probs, tokens, stream)
 PyObject* sample(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 9, [&]() -> PyObject* {
@@ -540,14 +589,13 @@ PyObject* tree_accept(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int32_t* up = (const int32_t*)flat(&required(a[2], "parents"), "parents", dev, at::kInt, {T});
     const int32_t* fp = (const int32_t*)flat(&off, "q_offsets", dev, at::kInt);
     const On on(dev, a[8]);
-    const at::Tensor path = given_or(a[5], "path", smp, {R, M}, at::kInt);
-    const at::Tensor out = given_or(a[6], "out_tokens", smp, {R, M}, at::kInt);
-    const at::Tensor count = given_or(a[7], "num_accepted", smp, {R}, at::kInt);
-    int32_t* pp = (int32_t*)flat(&path, "path", dev, at::kInt, {R, M});
-    int32_t* op = (int32_t*)flat(&out, "out_tokens", dev, at::kInt, {R, M});
-    int32_t* cp = (int32_t*)flat(&count, "num_accepted", dev, at::kInt, {R});
-    const dflash_status_t st = dflash_tree_accept(&d, sp, tp, up, fp, pp, op, cp, on.stream());
-    return st ? status(st) : tuple(path, out, count);
+    Ints r(smp);
+    r.want(a[5], "path", {R, M});
+    r.want(a[6], "out_tokens", {R, M});
+    r.want(a[7], "num_accepted", {R});
+    r.make(dev);
+    const dflash_status_t st = dflash_tree_accept(&d, sp, tp, up, fp, r.ptr(0), r.ptr(1), r.ptr(2), on.stream());
+    return st ? status(st) : tuple(r.at(0), r.at(1), r.at(2));
   });
 }
 
@@ -562,19 +610,11 @@ struct Cache {
 };
 void* layered(const at::Tensor& t, const char* name, int dev, at::ScalarType type, at::IntArrayRef shape,
               int64_t* page, int64_t* layer) {
-  if (t.sizes() != shape) refuse(std::string(name) + " must be " + list(shape) + ", got " + list(t.sizes()));
-  if (t.dim() == 4) {
-    *layer = 0;
-    return pages(t, name, dev, type, shape, page);
-  }
-  *layer = t.size(0) > 1 && t.numel() > 0 ? t.stride(0) : 0;
-  if (t.size(0) == 0) {
-    common(t, name, dev, type);
-    *page = 0;
-    return t.data_ptr();
-  }
-  if (t.size(0) > 1 && t.numel() > 0 && t.stride(0) <= 0) refuse(std::string("the layers of ") + name + " must not overlap");
-  return pages(t.select(0, 0), name, dev, type, shape.slice(1), page);
+  void* p = pages(t, name, dev, type, shape, page);
+  const bool many = t.dim() == 5 && t.size(0) > 1 && t.numel() > 0;
+  *layer = many ? t.stride(0) : 0;
+  if (many && *layer <= 0) refuse(std::string("the layers of ") + name + " must not overlap");
+  return p;
 }
 Cache cache(PyObject* k_cache, PyObject* v_cache) {
   Cache c = {};
@@ -686,20 +726,17 @@ PyObject* pages_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int32_t* sp = (const int32_t*)flat(&src, "src", p.dev, at::kInt);
     const int32_t* dp = (const int32_t*)flat(&required(a[3], "dst"), "dst", p.dev, at::kInt, {N});
     const On on(p.dev, a[11]);
-    at::Tensor out[3];
-    int32_t* op[3];
-    const char* names[3] = {"copy_src", "copy_dst", "copy_rows"};
-    for (int i = 0; i < 3; ++i) {
-      out[i] = given_or(a[6 + i], names[i], src, {N}, at::kInt);
-      op[i] = (int32_t*)flat(&out[i], names[i], p.dev, at::kInt, {N});
-    }
-    const at::Tensor missing = given_or(a[9], "missing", src, {1}, at::kInt);
-    int32_t* mp = (int32_t*)flat(&missing, "missing", p.dev, at::kInt, {1});
     const size_t bytes = dflash_pages_workspace_size(&p.d, narrow(N));
     const Workspace ws = workspace(a[10], bytes, src);
-    const dflash_status_t st = dflash_pages_fork(&p.d, p.table, lp, narrow(N), sp, dp, p.refs, op[0], op[1], op[2], mp,
-                                                 ws.ptr, bytes, on.stream());
-    return st ? status(st) : tuple(out[0], out[1], out[2], missing);
+    Ints r(src);
+    r.want(a[6], "copy_src", {N});
+    r.want(a[7], "copy_dst", {N});
+    r.want(a[8], "copy_rows", {N});
+    r.want(a[9], "missing", {1});
+    r.make(p.dev);
+    const dflash_status_t st = dflash_pages_fork(&p.d, p.table, lp, narrow(N), sp, dp, p.refs, r.ptr(0), r.ptr(1), r.ptr(2),
+                                                 r.ptr(3), ws.ptr, bytes, on.stream());
+    return st ? status(st) : tuple(r.at(0), r.at(1), r.at(2), r.at(3));
   });
 }
 

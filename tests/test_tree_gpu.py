@@ -844,3 +844,25 @@ def test_sample_distributions_in_place_of_the_logits(dfl, V):
     probs = torch.empty_like(x)
     tok = dfl.dflash_sample(x, u, top_k=k, probs=probs)
     assert torch.equal(dfl.dflash_sample(x, u, top_k=k, probs=x), tok) and torch.equal(x, probs)
+
+
+def test_results_that_are_given_and_results_that_are_not(dfl):
+    """Results of one call share an allocation; each is whole by itself, and given ones are filled."""
+    rng = np.random.default_rng(18)
+    par, tok, smp, off = _drafted(rng, [30, 5], 0.9)
+    args = [_i32(x) for x in (smp, tok, par, off)]
+    want = dfl.dflash_tree_accept(*args, 5)
+    for name, t in zip(("path", "out_tokens", "num_accepted"), want):
+        mine = torch.full_like(t, 99)
+        got = dfl.dflash_tree_accept(*args, 5, **{name: mine})
+        assert all(torch.equal(a, b) for a, b in zip(got, want)) and torch.equal(mine, t)
+        assert mine.data_ptr() == got[("path", "out_tokens", "num_accepted").index(name)].data_ptr()
+    assert all(t.is_contiguous() and t.clone().add_(1).sub_(1).equal(t) for t in want)
+    want[0].fill_(-7)
+    assert not (want[1] == -7).any() and not (want[2] == -7).any()
+    empty = dfl.dflash_tree_accept(*args[:3], _i32([0]), 4)
+    assert [tuple(t.shape) for t in empty] == [(0, 4), (0, 4), (0,)]
+    with pytest.raises(ValueError):
+        dfl.dflash_tree_accept(*args, 5, num_accepted=_i32([0]))
+    with pytest.raises(TypeError):
+        dfl.dflash_tree_accept(*args, 5, path=torch.empty((2, 5), device="cuda"))
