@@ -164,7 +164,7 @@ def load_library(path: str | None = None):
         lib.dflash_cache_copy.argtypes = [PD, LD, I, I, P, P, P, P, P, P]
         lib.dflash_pages_resize.argtypes = [OD, P, P, P, P, P, P, S, P]
         lib.dflash_pages_fork.argtypes = [OD, P, P, I, P, P, P, P, P, P, P, P, S, P]
-        lib.dflash_pages_workspace_size.argtypes = [OD, I]
+        lib.dflash_pages_workspace_size.argtypes = [OD]
         lib.dflash_pages_workspace_size.restype = S
         for name in ("dflash_qk_norm_rope", "dflash_qk_norm_rope_backward", "dflash_cache_append",
                      "dflash_attn_paged", "dflash_verify", "dflash_attn_tree", "dflash_sample", "dflash_tree_accept",
@@ -626,10 +626,9 @@ def dflash_cache_copy(k_cache, v_cache, src_pages, dst_pages, rows=None, stream=
         raise DFlashError("dflash_cache_copy", r)
 
 
-def dflash_pages_workspace_size(num_pages, items) -> int:
-    """Workspace bytes of dflash_pages_resize (items: rows of the page table) and dflash_pages_fork
-    (items: forks)."""
-    return int(load_library().dflash_pages_workspace_size(_PoolDims(0, 0, 1, int(num_pages)), int(items)))
+def dflash_pages_workspace_size(num_pages) -> int:
+    """Workspace bytes of dflash_pages_resize and dflash_pages_fork."""
+    return int(load_library().dflash_pages_workspace_size(_PoolDims(0, 0, 1, int(num_pages))))
 
 
 def dflash_pages_resize(page_table, old_lens, new_lens, refs, page_size, missing=None, workspace=None, stream=None):

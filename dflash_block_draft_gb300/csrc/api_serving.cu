@@ -199,12 +199,12 @@ dflash_status_t check_pool(const dflash_pool_dims_t* d, int items) {
     return DFLASH_ERR_UNSUPPORTED;
   return DFLASH_OK;
 }
-dflash_status_t pool_args(const dflash_pool_dims_t* d, int items, int32_t* table, int32_t* refs, int32_t* missing,
+dflash_status_t pool_args(const dflash_pool_dims_t* d, int32_t* table, int32_t* refs, int32_t* missing,
                           void* ws, size_t ws_bytes, PoolArgs* a) {
   if (d->R > 0 && d->max_pages > 0) TRY(check_tensor(table, 4));
   if (d->num_pages > 0) TRY(check_tensor(refs, 4));
   TRY(check_tensor(missing, 4));
-  TRY(check_ws(ws, ws_bytes, pool_workspace_bytes(d->num_pages, items)));
+  TRY(check_ws(ws, ws_bytes, pool_workspace_bytes(d->num_pages)));
   *a = PoolArgs{table, refs, missing, static_cast<int32_t*>(ws), d->R, d->max_pages, d->page_size, d->num_pages,
                 aligned(refs, 16), device_error_word()};
   return DFLASH_OK;
@@ -503,8 +503,8 @@ dflash_status_t dflash_cache_copy(const dflash_paged_dims_t* dims, const dflash_
   return launched(launch_cache_copy(a, (cudaStream_t)stream));
 }
 
-size_t dflash_pages_workspace_size(const dflash_pool_dims_t* dims, int items) {
-  return check_pool(dims, items) == DFLASH_OK ? pool_workspace_bytes(dims->num_pages, items) : 0;
+size_t dflash_pages_workspace_size(const dflash_pool_dims_t* dims) {
+  return check_pool(dims, 0) == DFLASH_OK ? pool_workspace_bytes(dims->num_pages) : 0;
 }
 
 dflash_status_t dflash_pages_resize(const dflash_pool_dims_t* dims, int32_t* page_table, const int32_t* old_lens,
@@ -512,7 +512,7 @@ dflash_status_t dflash_pages_resize(const dflash_pool_dims_t* dims, int32_t* pag
                                     size_t ws_bytes, dflash_stream_t stream) {
   TRY(check_pool(dims, 0));
   PoolArgs a;
-  TRY(pool_args(dims, dims->R, page_table, refs, missing, workspace, ws_bytes, &a));
+  TRY(pool_args(dims, page_table, refs, missing, workspace, ws_bytes, &a));
   if (dims->R > 0) {
     TRY(check_tensor(old_lens, 4));
     TRY(check_tensor(new_lens, 4));
@@ -526,7 +526,7 @@ dflash_status_t dflash_pages_fork(const dflash_pool_dims_t* dims, int32_t* page_
                                   size_t ws_bytes, dflash_stream_t stream) {
   TRY(check_pool(dims, n));
   PoolArgs a;
-  TRY(pool_args(dims, n, page_table, refs, missing, workspace, ws_bytes, &a));
+  TRY(pool_args(dims, page_table, refs, missing, workspace, ws_bytes, &a));
   if (dims->R > 0) TRY(check_tensor(lens, 4));
   if (n > 0)
     for (const int32_t* p : {src, dst, (const int32_t*)copy_src, (const int32_t*)copy_dst, (const int32_t*)copy_rows})

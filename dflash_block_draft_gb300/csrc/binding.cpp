@@ -708,7 +708,7 @@ PyObject* pages_resize(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const On on(p.dev, a[7]);
     const at::Tensor missing = given_or(a[5], "missing", old, {1}, at::kInt);
     int32_t* mp = (int32_t*)flat(&missing, "missing", p.dev, at::kInt, {1});
-    const size_t bytes = dflash_pages_workspace_size(&p.d, p.d.R);
+    const size_t bytes = dflash_pages_workspace_size(&p.d);
     const Workspace ws = workspace(a[6], bytes, old);
     const dflash_status_t st = dflash_pages_resize(&p.d, p.table, op, np, p.refs, mp, ws.ptr, bytes, on.stream());
     return st ? status(st) : wrap(missing);
@@ -726,7 +726,7 @@ PyObject* pages_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int32_t* sp = (const int32_t*)flat(&src, "src", p.dev, at::kInt);
     const int32_t* dp = (const int32_t*)flat(&required(a[3], "dst"), "dst", p.dev, at::kInt, {N});
     const On on(p.dev, a[11]);
-    const size_t bytes = dflash_pages_workspace_size(&p.d, narrow(N));
+    const size_t bytes = dflash_pages_workspace_size(&p.d);
     const Workspace ws = workspace(a[10], bytes, src);
     Ints r(src);
     r.want(a[6], "copy_src", {N});

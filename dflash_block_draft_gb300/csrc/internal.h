@@ -220,7 +220,7 @@ cudaError_t launch_cache_copy(const CopyArgs& a, cudaStream_t stream);
 // Pages taken, shared and given back (pages.cu).
 struct PoolArgs {
   int32_t *table, *refs, *missing;
-  int32_t* ws;            // [num_pages + items]
+  int32_t* ws;            // [num_pages]
   int R, max_pages, P, num_pages;
   int refs_vec;           // refs may be read in 16-byte pieces
   unsigned* err;
@@ -230,7 +230,7 @@ struct ForkArgs {
   int32_t *lens, *copy_src, *copy_dst, *copy_rows;
   int n;
 };
-size_t pool_workspace_bytes(int num_pages, int items);
+size_t pool_workspace_bytes(int num_pages);
 cudaError_t launch_pages_resize(const PoolArgs& a, const int32_t* old_lens, const int32_t* new_lens,
                                 cudaStream_t stream);
 cudaError_t launch_pages_fork(const PoolArgs& a, const ForkArgs& f, cudaStream_t stream);

@@ -5,13 +5,17 @@
 // and giving back what was taken restores the state exactly.
 //
 // One launch of one cluster of 8 CTAs.  Every CTA adds up all requests' needs for
-// itself (a strip a thread and a scan), reads the counts of an eighth of the pages, up
-// to 64 a thread as a bit mask, and learns from one exchange through distributed
-// shared memory how many free pages lie before its own.  The free pages go into a
-// list in the workspace by their rank; the requests read their run of it.  Pages
-// beyond 262144 are looked at in further rounds, while pages are still wanted.
+// itself (a strip a thread and a scan, while the cluster waits for what is given back), reads the
+// counts of an eighth of the pages, up to 64 a thread as a bit mask, and learns from one
+// exchange through distributed shared memory how many free pages lie before its own.  The free
+// pages go into a list in the workspace by their rank; the requests read their run of it.
+// Pages beyond 262144 are looked at in further rounds, while pages are still wanted.
 //
-// Bound by the chain of dependent steps (lengths, table, counts, list, table).
+// Bound by the chain of dependent steps: lengths, table, counts, exchange, list, table, and three
+// barriers of the cluster at some 2000 cycles each.  256 requests of up to 8000 positions that
+// grow or shrink by up to 64, 30705 pages of 16: 7.3 us (8.4 with a warp a request, the needs
+// added up behind the barrier and the counts written before it; a prompt of 125 pages given back
+// four times and forked four times 16.4, 25.7 with eight lanes a request whatever their number).
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -52,30 +56,46 @@ __device__ __forceinline__ int block_scan(int v, int* scratch /* [kWarps] */, in
 
 struct Shared {
   int scan[kWarps];
-  int free;  // free pages of this CTA in the round
+  int at[kThreads];  // where the pages of a strip's askers begin among all that are wanted
+  int free;          // free pages of this CTA in the round
 };
 
-// Takes pages for `items` askers in their order: need(i) pages each, put(i, j, page) is
-// called for the j-th of asker i by one lane, page -1 where none is left.  need(i) has to give
-// the same in every CTA and must not depend on anything that put writes.  Returns the
-// number of pages that were missing.
-template <typename Need, typename Put>
-__device__ __forceinline__ int take(const PoolArgs& a, int items, Shared& s, cg::cluster_group& cluster, Need need,
-                                    Put put) {
-  const int rank = (int)cluster.block_rank(), tid = threadIdx.x, lane = tid & 31;
-  int32_t* list = a.ws;                 // [num_pages] free pages by rank
-  int32_t* first = a.ws + a.num_pages;  // [items] where an asker's run begins
-  const int strip = (items + kThreads - 1) / kThreads;
-  const int lo = min(items, tid * strip), hi = min(items, lo + strip);
+// Items (rows of the table, or forks) in strips, of one where there are no more than 512: a strip
+// a thread in every CTA to add them up, and a strip a group of the cluster's threads, at least 8
+// and as many as there are for it, to work on their pages.
+struct Strips {
+  int len, items;
+  int mine, sub, width;  // this thread's strip as one of a group (below 512), its number in it, the group's size
+  __device__ __forceinline__ Strips(int n, int rank) : items(n) {
+    len = (n + kThreads - 1) / kThreads;
+    const int strips = len ? (n + len - 1) / len : 0;
+    width = 8;
+    while (2 * width * strips <= kCluster * kThreads && width < kThreads) width *= 2;
+    const int t = rank * kThreads + (int)threadIdx.x;
+    mine = t / width;
+    sub = t % width;
+  }
+  __device__ __forceinline__ int lo(int strip) const { return min((long long)items, (long long)strip * len); }
+  __device__ __forceinline__ int hi(int strip) const { return min((long long)items, (long long)(strip + 1) * len); }
+};
+
+// Adds up what the askers want, need(i) pages each, the same in every CTA.  Returns the whole.
+template <typename Need>
+__device__ __forceinline__ int plan(const Strips& st, Shared& s, Need need) {
   int mine = 0, wanted;
-  for (int i = lo; i < hi; ++i) mine += need(i);
-  int at = block_scan(mine, s.scan, &wanted);
-  if (rank == 0)
-    for (int i = lo; i < hi; ++i) {
-      first[i] = at;
-      at += need(i);
-    }
-  // the counts, as far as pages are wanted
+  for (int i = st.lo(threadIdx.x); i < st.hi(threadIdx.x); ++i) mine += need(i);
+  s.at[threadIdx.x] = block_scan(mine, s.scan, &wanted);
+  __syncthreads();
+  return wanted;
+}
+
+// Takes pages for the askers in their order: put(i, j, page) is called for the j-th of asker
+// i, page -1 where none is left.  Returns the number of pages that were missing.
+template <typename Need, typename Put>
+__device__ __forceinline__ int take(const PoolArgs& a, const Strips& st, int wanted, Shared& s,
+                                    cg::cluster_group& cluster, Need need, Put put) {
+  const int rank = (int)cluster.block_rank(), tid = threadIdx.x, lane = tid & 31;
+  // the counts, as far as pages are wanted; the free pages by rank go to the workspace
   int found = 0;
   const int per = min(kStrip, ((a.num_pages + kCluster * kThreads - 1) / (kCluster * kThreads) + 3) & ~3);
   for (long long p0 = 0; p0 < a.num_pages && found < wanted; p0 += (long long)per * kThreads * kCluster) {
@@ -95,25 +115,22 @@ __device__ __forceinline__ int take(const PoolArgs& a, int items, Shared& s, cg:
     int k = block_scan(__popcll(mask), s.scan, &here);
     if (tid == 0) s.free = here;
     cluster.sync();
-    int all = 0;
-    for (int c = 0; c < kCluster; ++c) {
-      const int v = *cluster.map_shared_rank(&s.free, c);
-      k += c < rank ? v : 0;
-      all += v;
-    }
-    k += found;
-    for (; mask && k < wanted; mask &= mask - 1, ++k) {
-      const int page = (int)b + __ffsll((long long)mask) - 1;
-      list[k] = page;
-      a.refs[page] = 1;
-    }
-    found += all;
-    cluster.sync();  // s.free has been read; the list and the counts are written
+    const int v = lane < kCluster ? *cluster.map_shared_rank(&s.free, lane & (kCluster - 1)) : 0;
+    k += found + __reduce_add_sync(0xffffffffu, lane < rank ? v : 0);
+    for (; mask && k < wanted; mask &= mask - 1, ++k) a.ws[k] = (int)b + __ffsll((long long)mask) - 1;
+    found += __reduce_add_sync(0xffffffffu, v);
+    cluster.sync();  // s.free has been read, the list is written
   }
-  if (found == 0) cluster.sync();  // first[], where no round's barrier lay behind it
-  for (int i = rank * kWarps + (tid >> 5); i < items; i += kCluster * kWarps) {
-    const int want = need(i), from = want ? __ldcg(first + i) : 0;
-    for (int j = lane; j < want; j += 32) put(i, j, from + j < found ? __ldcg(list + from + j) : -1);
+  int at = s.at[st.mine];
+  for (int i = st.lo(st.mine); i < st.hi(st.mine); ++i) {
+    const int want = need(i);
+#pragma unroll 4
+    for (int j = st.sub; j < want; j += st.width) {
+      const int page = at + j < found ? __ldcg(a.ws + at + j) : -1;
+      if (page >= 0) a.refs[page] = 1;
+      put(i, j, page);
+    }
+    at += want;
   }
   return max(0, wanted - found);
 }
@@ -125,7 +142,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
                   const int32_t* __restrict__ new_lens) {
   __shared__ Shared s;
   cg::cluster_group cluster = cg::this_cluster();
-  const int rank = (int)cluster.block_rank(), lane = threadIdx.x & 31;
+  const int rank = (int)cluster.block_rank();
   const long long most = (long long)a.max_pages * a.P;
   // pages that request r has and is to have; a request with a length out of range keeps its own
   auto load = [&](int r, int& had, int& want) {
@@ -135,11 +152,12 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     want = bad ? 0 : pages_of(y, a.P);
     return bad;
   };
-  for (int r = rank * kWarps + (threadIdx.x >> 5); r < a.R; r += kCluster * kWarps) {
+  const Strips st(a.R, rank);
+  for (int r = st.lo(st.mine); r < st.hi(st.mine); ++r) {
     int had, want;
-    if (load(r, had, want) && lane == 0) record_error(a.err, DFLASH_ERR_INVALID);
+    if (load(r, had, want) && st.sub == 0) record_error(a.err, DFLASH_ERR_INVALID);
     int32_t* row = a.table + (long long)r * a.max_pages;
-    for (int j = want + lane; j < had; j += 32) {
+    for (int j = want + st.sub; j < had; j += st.width) {
       const int page = row[j];
       row[j] = -1;
       if (page == -1) continue;  // none was left when the request grew
@@ -151,17 +169,19 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
       }
     }
   }
-  cluster.sync();  // the counts after everything that was given back
-  const int missing = take(
-      a, a.R, s, cluster,
-      [&](int r) {
-        int had, want;
-        load(r, had, want);
-        return max(0, want - had);
-      },
-      [&](int r, int j, int page) {
-        a.table[(long long)r * a.max_pages + pages_of(old_lens[r], a.P) + j] = page;
-      });
+  auto need = [&](int r) {
+    int had, want;
+    load(r, had, want);
+    return max(0, want - had);
+  };
+  // the counts after everything that was given back; what is wanted meanwhile
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  const int wanted = plan(st, s, need);
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  const int missing = take(a, st, wanted, s, cluster, need, [&](int r, int j, int page) {
+    a.table[(long long)r * a.max_pages + pages_of(old_lens[r], a.P) + j] = page;
+  });
   if (rank == 0 && threadIdx.x == 0) a.missing[0] = missing;
 }
 
@@ -213,18 +233,18 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     }
   }
   cluster.sync();
-  const int missing = take(
-      a, f.n, s, cluster, [&](int i) { return __ldcg(f.copy_rows + i) > 0 ? 1 : 0; },
-      [&](int i, int, int page) {
-        a.table[(long long)f.dst[i] * a.max_pages + length(i) / a.P] = page;
-        f.copy_dst[i] = page;
-      });
+  auto need = [&](int i) { return __ldcg(f.copy_rows + i) > 0 ? 1 : 0; };
+  const Strips st(f.n, rank);
+  const int missing = take(a, st, plan(st, s, need), s, cluster, need, [&](int i, int, int page) {
+    a.table[(long long)f.dst[i] * a.max_pages + length(i) / a.P] = page;
+    f.copy_dst[i] = page;
+  });
   if (rank == 0 && tid == 0) a.missing[0] = missing;
 }
 
 }  // namespace
 
-size_t pool_workspace_bytes(int num_pages, int items) { return sizeof(int32_t) * ((size_t)num_pages + (size_t)items); }
+size_t pool_workspace_bytes(int num_pages) { return sizeof(int32_t) * (size_t)num_pages; }
 
 cudaError_t launch_pages_resize(const PoolArgs& a, const int32_t* old_lens, const int32_t* new_lens,
                                 cudaStream_t stream) {

@@ -619,9 +619,8 @@ DFLASH_API dflash_status_t dflash_cache_copy(const dflash_paged_dims_t* dims, co
  * and all lengths 0 at the beginning.)  Free pages are taken lowest first.
  *   missing [1] int32: written; how many pages could not be had.  The table entries that
  *     would have held them are -1, which giving them back passes over.
- *   workspace: >= dflash_pages_workspace_size(dims, items) bytes, 256-byte aligned, with
- *     items = R for dflash_pages_resize and the number of forks for dflash_pages_fork;
- *     needs no initialisation.
+ *   workspace: >= dflash_pages_workspace_size(dims) bytes, 256-byte aligned; needs no
+ *     initialisation.
  * Calls on one pool must not run at the same time.  R and the number of forks up to
  * DFLASH_POOL_MAX_ROWS, R * max_pages below 2^31.
  */
@@ -632,7 +631,7 @@ typedef struct {
   int page_size;  /* positions of a page */
   int num_pages;  /* pages of the cache */
 } dflash_pool_dims_t;
-DFLASH_API size_t dflash_pages_workspace_size(const dflash_pool_dims_t* dims, int items);
+DFLASH_API size_t dflash_pages_workspace_size(const dflash_pool_dims_t* dims);
 
 /*
  * Requests made shorter or longer: row r holds ceil(old_lens[r] / page_size) pages and is
