@@ -236,7 +236,7 @@ struct Row {
   float scan_f[kWarps], coarse_before[kThreads];
   u64 all[kList], all_w[kList];
   u64 ranked[kMaxCluster];         // kept weights of the bracket, each CTA's
-  uint32_t keys[kWarps], key;
+  uint32_t keys[kWarps];
   u64 found_before;
   int found, b1, b2;
   u64 cut, bar;
@@ -245,6 +245,10 @@ struct Row {
   Scale scale;
   float ends, least, inv;  // no weight below `ends`; min-p's bound; 1 / kept weights
 };
+
+static_assert(offsetof(Row, lo) % 16 == 0 && offsetof(Row, listed) % 16 == 0 && offsetof(Row, weight) % 16 == 0 &&
+                  offsetof(Row, low) % 8 == 0, "read in pieces of 16 and 8 bytes");
+static_assert(sizeof(Row) + kChunkMax * sizeof(float) <= 232448, "shared memory budget");
 
 // Adds to a 64-bit sum in shared memory, the halves by themselves.
 __device__ __forceinline__ void add64(u64* to, u64 w) {
@@ -683,10 +687,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   if (tid == kThreads - 32 && min_p > 0.f) s.log_min_p = log_of(min_p);
   __syncwarp();
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  const float top = peer(s.top, tid * ranks / kThreads, ranks)[tid % (kThreads / ranks)];
+  float top = peer(s.top, tid * ranks / kThreads, ranks)[tid % (kThreads / ranks)];
   float m = logit_of(~block_least(s, ~key_of(top)));
   if (m > kTop) {
     m = kTop;
+    top = fminf(top, kTop);
     pass.some(kTop, [&](float, int at) { pass.chunk[at] = from_f32<T>(kTop); });
     __syncthreads();
   }
@@ -767,6 +772,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         if (!linear) break;  // fewer than k in all
         bound = -kTop;       // the k-th has no weight: among all tokens
         linear = false;
+        cluster.sync();      // the other CTAs have read this one's histogram
       }
     }
     if (n > 0) {
@@ -820,6 +826,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         pass.some(cut.v, [&](float l, int at) {
           if (l == cut.v && pass.first + at > cut.i) pass.chunk[at] = from_f32<T>(-INFINITY);
         });
+        __syncthreads();  // (other lanes read them next)
         cut.i = (int)kIndexMask;
       }
       bool nucleus = top_p < 1.f;
