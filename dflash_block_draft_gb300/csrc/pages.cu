@@ -228,7 +228,9 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
       if (ok) f.lens[f.dst[i]] = n;
       else record_error(a.err, DFLASH_ERR_INVALID);
       f.copy_rows[i] = rest;
-      f.copy_src[i] = rest ? from[full] : -1;
+      const int last = rest ? from[full] : -1;
+      if (rest && (last < 0 || last >= a.num_pages)) record_error(a.err, DFLASH_ERR_INVALID);
+      f.copy_src[i] = last;
       f.copy_dst[i] = -1;
     }
   }

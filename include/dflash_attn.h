@@ -653,7 +653,8 @@ DFLASH_API dflash_status_t dflash_pages_resize(const dflash_pool_dims_t* dims, i
  * say what dflash_cache_copy has to copy for it (-1, -1, 0 where the last page is whole).
  * lens [R] is updated.  A row may be the source of many forks.  A fork whose row or source
  * is out of range, whose row is not empty, is another fork's too or is some fork's source,
- * is recorded as DFLASH_ERR_INVALID and left out (-1, -1, 0).  Positions in shared pages
+ * is recorded as DFLASH_ERR_INVALID and left out (-1, -1, 0); an entry of the source that
+ * is no page is recorded, and the fork's is the same.  Positions in shared pages
  * must not be written; a row is not shortened into them and then appended to.
  */
 DFLASH_API dflash_status_t dflash_pages_fork(const dflash_pool_dims_t* dims, int32_t* page_table, int32_t* lens, int n,

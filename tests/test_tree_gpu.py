@@ -559,6 +559,15 @@ def test_pages_fork_leaves_out_what_is_wrong(dfl):
     assert [x.tolist()[i] for i in good for x in (a, b, n)] == [x for z in zip(*want[3:6]) for x in z]
     bad = [i for i in range(10) if i not in good]
     assert all(a.tolist()[i] == b.tolist()[i] == -1 and n.tolist()[i] == 0 for i in bad)
+    # a source that lacks pages (whole ones and its last): recorded, and cache_copy has nothing to read for it
+    t, c, ln = _i32([[0, -1, -1], [-1] * 3, [1, 9, -1], [-1] * 3]), _i32([1, 1, 0, 0]), _i32([10, 0, 7, 0])
+    for src, dst, row, refs, copy in ((0, 1, [0, -1, 2], [2, 1, 1, 0], (-1, 2, 2)), (2, 3, [1, 3, -1], [2, 2, 1, 1], (9, 3, 3))):
+        a, b, n, miss = dfl.dflash_pages_fork(t, ln, _i32([src]), _i32([dst]), c, P)
+        assert dfl.dflash_last_device_error() == INVALID and miss.item() == 0
+        assert t[dst].tolist() == row and c.tolist() == refs and (a.item(), b.item(), n.item()) == copy
+    t, c, ln = _i32([[0, -1], [-1, -1]]), _i32([1, 0]), _i32([6, 0])  # only the last page is missing
+    a, b, n, miss = dfl.dflash_pages_fork(t, ln, _i32([0]), _i32([1]), c, P)
+    assert dfl.dflash_last_device_error() == INVALID and (a.item(), b.item(), n.item()) == (-1, 1, 2)
     e = _i32([])
     a, b, n, miss = dfl.dflash_pages_fork(t, ln, e, e, c, P)
     assert a.shape == (0,) and miss.item() == 0 and dfl.dflash_last_device_error() == 0
