@@ -124,7 +124,7 @@ struct Table {
 };
 
 // Weights of two logits that are at most 45 powers of two below the largest one; 0 where !in.
-// Off by at most 2^-31 of themselves (2^-33.5 rms), and by half a step.  In fp32 l - m is
+// Off by at most 2^-31 of themselves (2^-33.5 rms), and by half a step (small ones by one).  In fp32 l - m is
 // taken as two floats; of two bf16 values it fits one, but where one of them is below
 // 2^-16 of the other.
 template <typename T>
@@ -133,18 +133,16 @@ __device__ __forceinline__ void weights(const Scale& c, const Table& tab, float2
   const float2 neg = both(-1.f), nm = both(-c.m), ch = both(c.ch);
   l = make_float2(in0 ? l.x : c.m, in1 ? l.y : c.m);
   const float2 d = __fadd2_rn(l, nm);
-  // y = -np + e
-  const float2 np = __fmul2_rn(d, both(-c.ch));
-  float2 e = __ffma2_rn(d, both(c.cl), __ffma2_rn(d, ch, np));
+  // y = log2(e) / T d = raw / 128 + z, the whole steps by the adder's bits
+  const float big = 0x1.8p16f;  // (its own bits are 0 in the lower half)
+  const float2 t1 = __ffma2_rn(d, ch, both(big));
+  float2 z = __ffma2_rn(d, ch, __ffma2_rn(t1, neg, both(big)));
   if (sizeof(T) == 4) {  // l - m = d + err exactly (the two-sum of Moller and Knuth)
     const float2 bb = __ffma2_rn(l, neg, d);
     const float2 err = __fadd2_rn(__ffma2_rn(__ffma2_rn(bb, neg, d), neg, l), __ffma2_rn(bb, neg, nm));
-    e = __ffma2_rn(err, ch, e);
+    z = __ffma2_rn(err, ch, z);
   }
-  // y = raw / 128 + z, the whole steps by the adder's bits, the rest r = -rn exactly and z = r + e
-  const float big = 0x1.8p16f;  // (its own bits are 0 in the lower half)
-  const float2 t1 = __ffma2_rn(np, neg, both(big));
-  const float2 z = __ffma2_rn(__fadd2_rn(np, __fadd2_rn(t1, both(-big))), neg, e);
+  z = __ffma2_rn(d, both(c.cl), z);
   const int raw0 = __float_as_int(t1.x), raw1 = __float_as_int(t1.y);
   // 2^(raw / 128) = p (th + tl)
   const float2 th = make_float2(tab.hi[raw0 & 127], tab.hi[raw1 & 127]);
@@ -158,8 +156,7 @@ __device__ __forceinline__ void weights(const Scale& c, const Table& tab, float2
   const float2 lo = __fadd2_rn(__ffma2_rn(th, s, __ffma2_rn(hi, neg, th)), tl);
   // in steps
   const float2 x = __ffma2_rn(hi, p, both(kHi));
-  const float2 left = __ffma2_rn(hi, p, __ffma2_rn(x, neg, both(kHi)));
-  const float2 y = __fadd2_rn(__ffma2_rn(lo, p, left), both(kLo));
+  const float2 y = __ffma2_rn(lo, p, __ffma2_rn(hi, p, __ffma2_rn(x, neg, both(kHi + kLo))));
   w0 = Steps44{__float_as_int(x.x) - __float_as_int(kHi), __float_as_int(y.x) - __float_as_int(kLo)};
   w1 = Steps44{__float_as_int(x.y) - __float_as_int(kHi), __float_as_int(y.y) - __float_as_int(kLo)};
 }
@@ -481,39 +478,44 @@ __device__ __forceinline__ bool here(bool x) {
 }
 
 // The cut of top-k (WEIGHTS false; target: k) or top-p (true): the token, of those that
-// `prior` keeps and that lie at or above `bound`, in which the running count or weight, `before` in
-// front of the range, reaches the target.  `linear`: the range is the logits whose step
-// lies in [q0, q0 + (512 << shift)), divided into 512 equal parts; else, and where
-// that leaves too many tokens, it is divided by places, from the largest key to the smallest.
+// `prior` keeps and whose keys lie in [klo, khi], in which the running count or weight, `before` in
+// front of the range, reaches the target.  `linear` (top-k): the range of `steps` is divided
+// into 512 equal parts; else, and where that leaves too many tokens, the range is divided
+// by places, from the largest key to the smallest.
 // Top-k with all tokens of the row down to the cut's part in the list: *listed is their number.
 // Returns prior, and *listed -1, where there are fewer tokens than k.
 template <bool WEIGHTS, typename T>
-__device__ __forceinline__ Cut select(const Pass<T>& pass, Row& s, const Cut& prior, const Scale& sc, float bound,
-                                      bool linear, const Steps& steps, int q0, int shift, u64 before, u64 target,
+__device__ __forceinline__ Cut select(const Pass<T>& pass, Row& s, const Cut& prior, const Scale& sc, uint32_t klo,
+                                      uint32_t khi, bool linear, const Steps& steps, u64 before, u64 target,
                                       int* listed) {
   cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, ranks = (int)cluster.num_blocks();
-  u64 lo = (u64)key_of(-kTop) << kIndexBits, hi = place_of(key_of(sc.m), 0);  // the range's places
-  if (!linear) shift = 64 - __clzll((long long)(hi - lo)) - kPartBits;
+  u64 lo = (u64)klo << kIndexBits, hi = place_of(khi, 0);  // the range's places
+  int shift;
+  float under, over;  // and its logits
+  auto divide = [&]() {
+    shift = max(0, 64 - __clzll((long long)(hi - lo)) - kPartBits);
+    under = logit_of((uint32_t)(lo >> kIndexBits));
+    over = logit_of((uint32_t)(hi >> kIndexBits));
+  };
+  divide();
   bool room = here(!WEIGHTS);
   auto part_of = [&](float l, int i) -> int {
     if (!prior.keeps(l, i)) return -1;
-    if (here(linear)) {
-      const int part = (steps.at(l) - q0) >> shift;
+    if (!WEIGHTS && here(linear)) {
+      const int part = steps.at(l) >> (21 - kPartBits);
       return part < kParts ? part : -1;
     }
     const u64 p = place_of(key_of(l), i);
     return p < lo || p > hi ? -1 : (int)((hi - p) >> shift);
   };
+  auto near = [&](float l) { return l >= under && l <= over; };
 #pragma unroll 1
   for (;;) {
     // ---- a histogram of the range
     s.lo[tid] = 0;
     if (WEIGHTS) s.hi[tid] = 0;
     __syncthreads();
-    // (a linear range's logits, else all)
-    const unsigned width = linear ? (unsigned)kParts << shift : 0u;
-    auto near = [&](float l) { return l >= bound && (width == 0 || (unsigned)(steps.at(l) - q0) < width); };
     pass.where(near, [&](float l, int at) {
       const int part = part_of(l, pass.first + at);
       if (part < 0) return;
@@ -555,7 +557,8 @@ __device__ __forceinline__ Cut select(const Pass<T>& pass, Row& s, const Cut& pr
     const bool whole = !WEIGHTS && room && s.b1 <= kList;
     if (!whole) before = s.found_before;
     // ---- the part's tokens
-    uint32_t klo = ~0u, khi = 0;
+    klo = ~0u;
+    khi = 0;
     pass.where(near, [&](float l, int at) {
       const int p = part_of(l, pass.first + at);
       if (p >= 0 && (here(whole) ? p <= part : p == part)) enlist(s, l, pass.first + at, klo, khi);
@@ -579,13 +582,16 @@ __device__ __forceinline__ Cut select(const Pass<T>& pass, Row& s, const Cut& pr
       return cut_at(s.cut);  // (*listed stays 0)
     }
     // ---- too many: what lies between the part's keys is divided
-    if (!linear) {
+    if (WEIGHTS || !linear) {
       hi -= (u64)part << shift;
       lo = max(lo, hi - ((1ull << shift) - 1));
+    } else {
+      hi = ~0ull;
+      lo = 0;
     }
-    hi = linear ? place_of(khi, 0) : min(hi, place_of(khi, 0));
-    lo = linear ? (u64)klo << kIndexBits : max(lo, (u64)klo << kIndexBits);
-    shift = max(0, 64 - __clzll((long long)(hi - lo)) - kPartBits);
+    hi = min(hi, place_of(khi, 0));
+    lo = max(lo, (u64)klo << kIndexBits);
+    divide();
     linear = here(false);
     room = here(false);
   }
@@ -765,7 +771,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       }
 #pragma unroll 1
       while (n == 0) {
-        cut = select<false, T>(pass, s, cut, sc, bound, linear, Steps(m, fmaxf(range, 1e-30f)), 0, 21 - kPartBits, 0,
+        cut = select<false, T>(pass, s, cut, sc, key_of(bound), key_of(m), linear, Steps(m, fmaxf(range, 1e-30f)), 0,
                                top_k, &n);
         if (n >= 0) break;
         n = 0;
@@ -830,7 +836,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         cut.i = (int)kIndexMask;
       }
       bool nucleus = top_p < 1.f;
-      int q1 = 0, q2 = 0;  // steps of the bracket in which top-p's cut lies
+      float first_in = INFINITY, last_in = -INFINITY;  // logits of the bracket in which top-p's cut lies
       const Steps steps(m, 31.2f * t);
       float floor = fmaxf(ends, cut.v);
       if (nucleus) {
@@ -880,8 +886,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         if (c1 >= want * kOver && !(c0 >= want * kOver)) atomicMax(&s.b2, tid);
         __syncthreads();
         const int lo8 = s.b1 == kThreads ? 0 : s.b1, hi8 = s.b2 < 0 ? kThreads - 1 : s.b2;
-        q1 = lo8 * kCoarse << kStepBits;
-        q2 = hi8 == kThreads - 1 ? INT_MAX : (hi8 + 1) * kCoarse << kStepBits;
+        int b1 = lo8 * kCoarse, b2 = hi8 * kCoarse + kCoarse - 1;
         if (hi8 - lo8 < 4) {  // 32 bins at most: every warp for itself
           const int bin = min(kBins - 1, lo8 * kCoarse + lane);
           uint32_t w[kMaxCluster];
@@ -901,12 +906,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           const unsigned may = __ballot_sync(0xffffffffu, upto * kOver >= want), must = __ballot_sync(0xffffffffu, upto >= want * kOver);
           // (where none of these bins reaches it, rounding hid the border: the last one)
           const int end = (hi8 - lo8 + 1) * kCoarse - 1;
-          const int b1 = may ? min(__ffs(may) - 1, end) : end, b2 = must ? min(__ffs(must) - 1, end) : end;
-          q1 = (lo8 * kCoarse + b1) << kStepBits;
-          q2 = lo8 * kCoarse + b2 >= kBins - 1 ? INT_MAX : (lo8 * kCoarse + b2 + 1) << kStepBits;
+          b2 = b1 + (must ? min(__ffs(must) - 1, end) : end);
+          b1 += may ? min(__ffs(may) - 1, end) : end;
         }
+        // as logits, which take one comparison each: what is above first_in lies in an earlier bin, what is
+        // below last_in in a later one (steps are rounded, and off by a quarter besides: two more)
+        const float step = 31.2f * t * 0x1p-21f;
+        first_in = __fmaf_ru(-(float)((b1 << kStepBits) - 2), step, m);
+        if (b2 < kBins - 1) last_in = __fmaf_rd(-(float)(((b2 + 1) << kStepBits) + 2), step, m);
         // min-p ends in front of the bracket: top-p takes nothing away
-        if (least >= ends && steps.at(least) < q1) nucleus = false;
+        if (least >= ends && least > first_in) nucleus = false;
       }
       if (!nucleus && least > cut.v) {
         cut.v = least;
@@ -929,11 +938,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         unsigned mask = 0;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const int q = steps.at(x[k]);  // (of a logit below the floor any, and its weight is 0)
-          Steps44& to = q < q1 ? kept : rest;
+          Steps44& to = x[k] > first_in ? kept : rest;
           to.hi += w[k].hi;
           to.lo += w[k].lo;
-          mask |= (unsigned)(x[k] >= floor && q >= q1 && q < q2) << k;
+          mask |= (unsigned)(x[k] <= first_in && x[k] >= fmaxf(floor, last_in)) << k;
         }
 #pragma unroll 1
         for (; mask; mask &= mask - 1) {
@@ -999,15 +1007,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           told = true;
           own_sums = (lane < ranks ? v.x + s.ranked[lane] : 0);
         } else {
-          const int width = min(q2, (kBins + 1) << kStepBits) - q1;
-          const int shift = max(0, 32 - __clz(width - 1) - kPartBits);
-          cut = select<true, T>(pass, s, cut, sc, ends, true, steps, q1, shift, before, target, nullptr);
+          const float over = logit_of(khi);
+          cut = select<true, T>(pass, s, cut, sc, klo, khi, false, steps, before, target, nullptr);
           if (least > cut.v) cut = Cut{least, (int)kIndexMask};
           const float from = fmaxf(ends, cut.v);
           pass.each([&](const float (&x)[4], int at) {
             unsigned mask = 0;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mask |= (unsigned)(x[k] >= from && steps.at(x[k]) >= q1) << k;
+            for (int k = 0; k < 4; ++k) mask |= (unsigned)(x[k] >= from && x[k] <= over) << k;
 #pragma unroll 1
             for (; mask; mask &= mask - 1) {
               const int k = at + __ffs(mask) - 1;
