@@ -50,6 +50,7 @@
 #include <stddef.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -402,31 +403,62 @@ __device__ __forceinline__ void tell_keys(Row& s, uint32_t klo, uint32_t khi) {
     atomicMax(reinterpret_cast<uint32_t*>(&s.listed.z), khi);
   }
 }
-// What a CTA of the cluster has at the place of `p`.
-template <typename V>
-__device__ __forceinline__ const V* peer(const V* p, int rank, int ranks) {
-  return ranks == 1 ? p : cg::this_cluster().map_shared_rank(p, rank);
-}
+// A row's CTAs.  ONE: a single one, and none of the cluster's barriers and reads (1664 rows of
+// 32000 took 91 us with them, 79 without).
+template <bool ONE>
+struct Team {
+  static constexpr int kMost = ONE ? 1 : kMaxCluster;
+  static __device__ __forceinline__ int size() { return ONE ? 1 : (int)cg::this_cluster().num_blocks(); }
+  static __device__ __forceinline__ int rank() { return ONE ? 0 : (int)cg::this_cluster().block_rank(); }
+  static __device__ __forceinline__ void sync() {
+    if constexpr (ONE) __syncthreads();
+    else cg::this_cluster().sync();
+  }
+  // sync() in two halves; whole warps come to the second one
+  static __device__ __forceinline__ void arrive() {
+    if constexpr (!ONE) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  }
+  static __device__ __forceinline__ void wait() {
+    if constexpr (ONE) __syncthreads();
+    else asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
+  // what a CTA has at the place of `p`
+  template <typename V>
+  static __device__ __forceinline__ const V* peer(const V* p, int rank) {
+    if constexpr (ONE) return p;
+    else return cg::this_cluster().map_shared_rank(p, rank);
+  }
+  // what all of them have there, 0 beyond the team (all reads in flight at once)
+  template <typename V>
+  static __device__ __forceinline__ void all(const V* p, V (&out)[kMost]) {
+    const int ranks = size();
+#pragma unroll
+    for (int c = 0; c < kMost; ++c) out[c] = *peer(p, c & (ranks - 1));
+#pragma unroll
+    for (int c = 0; c < kMost; ++c) out[c] = c < ranks ? out[c] : V(0);
+  }
+};
 // All CTAs' lists into s.all and their weights into s.all_w, if they are kList at most, and the
-// range of their keys.  Returns their number.  (After a cluster.sync; a block barrier follows.)
-template <typename T>
+// range of their keys.  Returns their number.  (After a sync; a block barrier follows.)
+template <typename T, bool ONE>
 __device__ __noinline__ int join_lists(Row& s, uint32_t* klo, uint32_t* khi) {
-  const int tid = threadIdx.x, lane = tid & 31, ranks = (int)cg::this_cluster().num_blocks();
+  using G = Team<ONE>;
+  const int tid = threadIdx.x, lane = tid & 31, ranks = G::size();
   int4 v = make_int4(0, -1, 0, 0);
-  if (lane < ranks) v = *peer(&s.listed, lane, ranks);
+  if (lane < ranks) v = *G::peer(&s.listed, lane);
   *klo = __reduce_min_sync(0xffffffffu, (uint32_t)v.y);
   *khi = __reduce_max_sync(0xffffffffu, (uint32_t)v.z);
   int upto = v.x;
 #pragma unroll
-  for (int o = 1; o < kMaxCluster; o <<= 1) {
+  for (int o = 1; o < G::kMost; o <<= 1) {
     const int u = __shfl_up_sync(0xffffffffu, upto, o);
     if (lane >= o) upto += u;
   }
-  const int n = __shfl_sync(0xffffffffu, upto, kMaxCluster - 1);
+  const int n = __shfl_sync(0xffffffffu, upto, G::kMost - 1);
   if (n <= kList) {
     int owner = 0, before = 0;  // of entry tid
 #pragma unroll
-    for (int c = 0; c < kMaxCluster - 1; ++c) {
+    for (int c = 0; c < G::kMost - 1; ++c) {
       const int u = __shfl_sync(0xffffffffu, upto, c);
       if (tid >= u) {
         owner = c + 1;
@@ -434,7 +466,7 @@ __device__ __noinline__ int join_lists(Row& s, uint32_t* klo, uint32_t* khi) {
       }
     }
     if (tid < n) {
-      const u64 p = peer(s.list, owner, ranks)[tid - before];
+      const u64 p = G::peer(s.list, owner)[tid - before];
       s.all[tid] = p;
       const float l = logit_of((uint32_t)(p >> kIndexBits));
       s.all_w[tid] = weight<T>(s.scale, s.tab, l, l >= s.ends);
@@ -484,12 +516,12 @@ __device__ __forceinline__ bool here(bool x) {
 // by places, from the largest key to the smallest.
 // Top-k with all tokens of the row down to the cut's part in the list: *listed is their number.
 // Returns prior, and *listed -1, where there are fewer tokens than k.
-template <bool WEIGHTS, typename T>
+template <bool WEIGHTS, bool ONE, typename T>
 __device__ __forceinline__ Cut select(const Pass<T>& pass, Row& s, const Cut& prior, const Scale& sc, uint32_t klo,
                                       uint32_t khi, bool linear, const Steps& steps, u64 before, u64 target,
                                       int* listed) {
-  cg::cluster_group cluster = cg::this_cluster();
-  const int tid = threadIdx.x, ranks = (int)cluster.num_blocks();
+  using G = Team<ONE>;
+  const int tid = threadIdx.x;
   u64 lo = (u64)klo << kIndexBits, hi = place_of(khi, 0);  // the range's places
   int shift;
   float under, over;  // and its logits
@@ -528,18 +560,15 @@ __device__ __forceinline__ Cut select(const Pass<T>& pass, Row& s, const Cut& pr
         atomicAdd(&s.lo[part], 1u);
       }
     });
-    cluster.sync();
+    G::sync();
     clear_list(s);  // (every CTA has read the lists of an earlier range)
     // ---- merged, every CTA for itself
     u64 v = 0;
-    uint32_t part_lo[kMaxCluster], part_hi[kMaxCluster];  // (all reads in flight at once)
+    uint32_t part_lo[G::kMost], part_hi[G::kMost] = {};
+    G::all(&s.lo[tid], part_lo);
+    if (WEIGHTS) G::all(&s.hi[tid], part_hi);
 #pragma unroll
-    for (int c = 0; c < kMaxCluster; ++c) {
-      part_lo[c] = *cluster.map_shared_rank(&s.lo[tid], c & (ranks - 1));
-      part_hi[c] = WEIGHTS ? *cluster.map_shared_rank(&s.hi[tid], c & (ranks - 1)) : 0;
-    }
-#pragma unroll
-    for (int c = 0; c < kMaxCluster; ++c) v += c < ranks ? ((u64)part_hi[c] << 32) + part_lo[c] : 0;
+    for (int c = 0; c < G::kMost; ++c) v += ((u64)part_hi[c] << 32) + part_lo[c];
     u64 total;
     const u64 at = before + block_scan(v, s.scan, &total);
     if (!WEIGHTS && before + total < target) {
@@ -564,8 +593,8 @@ __device__ __forceinline__ Cut select(const Pass<T>& pass, Row& s, const Cut& pr
       if (p >= 0 && (here(whole) ? p <= part : p == part)) enlist(s, l, pass.first + at, klo, khi);
     });
     tell_keys(s, klo, khi);
-    cluster.sync();
-    const int n = join_lists<T>(s, &klo, &khi);
+    G::sync();
+    const int n = join_lists<T, ONE>(s, &klo, &khi);
     if (whole) {
       *listed = n;
       return prior;
@@ -633,13 +662,13 @@ __device__ __forceinline__ u64 draw_bar(float u, u64 whole) {
   return times(fminf(fmaxf(u, 0.f), 0x1.fffffep-1f), whole, &more);
 }
 
-template <typename T, bool VEC>
+template <typename T, bool VEC, bool ONE>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ SampleArgs a) {
   constexpr int N = Vec<T>::N;
   extern __shared__ __align__(16) uint4 chunk[];
   __shared__ __align__(16) Row s;
-  cg::cluster_group cluster = cg::this_cluster();
-  const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
+  using G = Team<ONE>;
+  const int rank = G::rank(), ranks = G::size();
   const int r = blockIdx.x / ranks;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const T* row = static_cast<const T*>(a.x) + r * a.xs;
@@ -689,11 +718,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       if (tid == 0) s.low = make_float2(logit_of(least), (float)threads);
     }
   }
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  G::arrive();
   if (tid == kThreads - 32 && min_p > 0.f) s.log_min_p = log_of(min_p);
   __syncwarp();
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  float top = peer(s.top, tid * ranks / kThreads, ranks)[tid % (kThreads / ranks)];
+  G::wait();
+  float top = G::peer(s.top, tid * ranks / kThreads)[tid % (kThreads / ranks)];
   float m = logit_of(~block_least(s, ~key_of(top)));
   if (m > kTop) {
     m = kTop;
@@ -717,8 +746,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     if (tid == 0) s.best = INT_MAX;
     __syncthreads();
     pass.some(m, [&](float, int at) { atomicMin(&s.best, pass.first + at); });
-    cluster.sync();
-    const int best = lane < ranks ? *peer(&s.best, lane, ranks) : INT_MAX;
+    G::sync();
+    const int best = lane < ranks ? *G::peer(&s.best, lane) : INT_MAX;
     cut.v = m;
     cut.i = (int)__reduce_min_sync(0xffffffffu, (unsigned)best);
     if (rank == 0 && tid == 0) token = cut.i;
@@ -757,12 +786,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           uint32_t klo = ~0u, khi = 0;
           pass.some(bound, [&](float l, int at) { enlist(s, l, pass.first + at, klo, khi); });
           tell_keys(s, klo, khi);
-          cluster.sync();
-          n = join_lists<T>(s, &klo, &khi);
+          G::sync();
+          n = join_lists<T, ONE>(s, &klo, &khi);
           if (n > kList) n = 0;
         }
       } else {
-        const float2 v = lane < ranks ? *peer(&s.low, lane, ranks) : make_float2(INFINITY, 0.f);
+        const float2 v = lane < ranks ? *G::peer(&s.low, lane) : make_float2(INFINITY, 0.f);
         const float low = logit_of(__reduce_min_sync(0xffffffffu, key_of(v.x)));
         // as many tokens as threads lie above the least of the threads' maxima; else down to where weights end
         const bool known = top_k > kThreads && top_k <= (int)warp_sum(v.y) && low >= -kTop;
@@ -771,14 +800,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       }
 #pragma unroll 1
       while (n == 0) {
-        cut = select<false, T>(pass, s, cut, sc, key_of(bound), key_of(m), linear, Steps(m, fmaxf(range, 1e-30f)), 0,
+        cut = select<false, ONE, T>(pass, s, cut, sc, key_of(bound), key_of(m), linear, Steps(m, fmaxf(range, 1e-30f)), 0,
                                top_k, &n);
         if (n >= 0) break;
         n = 0;
         if (!linear) break;  // fewer than k in all
         bound = -kTop;       // the k-th has no weight: among all tokens
         linear = false;
-        cluster.sync();      // the other CTAs have read this one's histogram
+        G::sync();      // the other CTAs have read this one's histogram
       }
     }
     if (n > 0) {
@@ -788,16 +817,20 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       const u64 at = in_front(s, n, g, i, &rank_of);
       const u64 place = i < n ? s.all[i] : 0, w = i < n ? s.all_w[i] : 0;
       const bool lead = i < n && (tid & (g - 1)) == 0;
-      if (tid == 0) s.cut = ~0ull;
-      const int lost = __syncthreads_or(lead && rank_of < top_k && w == 0);
-      if (lead && rank_of == top_k - 1) {
-        bool exact = false;
-        s.bar = top_p < 1.f ? share_of(top_p, at + w, &exact) : ~0ull;  // of K's weight
-        if (exact && lost) ++s.bar;
+      if (top_p < 1.f || min_p > 0.f) {
+        if (tid == 0) s.cut = ~0ull;
+        const int lost = __syncthreads_or(lead && rank_of < top_k && w == 0);
+        if (lead && rank_of == top_k - 1) {
+          bool exact = false;
+          s.bar = top_p < 1.f ? share_of(top_p, at + w, &exact) : ~0ull;  // of K's weight
+          if (exact && lost) ++s.bar;
+        }
+        __syncthreads();
+        const bool keep = rank_of < top_k && at < s.bar && logit_of((uint32_t)(place >> kIndexBits)) >= least;
+        if (keep && lead) atomicMin(&s.cut, place);
+      } else if (lead && rank_of == top_k - 1) {
+        s.cut = place;
       }
-      __syncthreads();
-      const bool keep = rank_of < top_k && at < s.bar && logit_of((uint32_t)(place >> kIndexBits)) >= least;
-      if (keep && lead) atomicMin(&s.cut, place);
       __syncthreads();
       const u64 edge = s.cut;
       cut = cut_at(edge);
@@ -817,14 +850,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         whole += __shfl_xor_sync(0xffffffffu, whole, o);
         earlier += __shfl_xor_sync(0xffffffffu, earlier, o);
       }
-      if (tid == 0) {
-        s.weight.x = whole;
-        s.bar = draw_bar(u, whole);
-      }
-      __syncthreads();
-      total = s.weight.x;
+      total = whole;
+      const u64 bar = draw_bar(u, whole);
       // (0 draws the first token that is kept, however little it weighs)
-      if (rank == 0 && lead && place >= edge && (u > 0.f ? upto - w <= s.bar && s.bar < upto : earlier == 0))
+      if (rank == 0 && lead && place >= edge && (u > 0.f ? upto - w <= bar && bar < upto : earlier == 0))
         token = (int)(kIndexMask - (uint32_t)turned);
     } else {
       if (limited) {
@@ -841,7 +870,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       float floor = fmaxf(ends, cut.v);
       if (nucleus) {
         // ---- where top-p's cut can lie: the weights' masses in 4096 steps
-        if (limited) cluster.sync();  // the other CTAs have read this one's histogram
+        if (limited) G::sync();  // the other CTAs have read this one's histogram
         uint4* bins = reinterpret_cast<uint4*>(&s.lo[kCoarse * tid]);
         bins[0] = bins[1] = make_uint4(0, 0, 0, 0);
         if (tid == 0) {
@@ -868,15 +897,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           for (int k = 7; k >= 0; --k) mass = fmaf(mass, kBinRatio, (float)v[k]);
           s.coarse[tid] = mass * first;
         }
-        cluster.sync();
+        G::sync();
         clear_list(s);
         // ---- merged: eight bins together, then those that the border lies in by themselves
-        float part[kMaxCluster];  // (all reads in flight at once)
-#pragma unroll
-        for (int c = 0; c < kMaxCluster; ++c) part[c] = *cluster.map_shared_rank(&s.coarse[tid], c & (ranks - 1));
+        float part[G::kMost];
+        G::all(&s.coarse[tid], part);
         float v = 0.f;
 #pragma unroll
-        for (int c = 0; c < kMaxCluster; ++c) v += c < ranks ? part[c] : 0.f;
+        for (int c = 0; c < G::kMost; ++c) v += part[c];
         float all;
         const float c0 = block_scan(v, s.scan_f, &all), c1 = c0 + v;
         const float want = fmaxf(top_p, 1e-6f) * all;
@@ -889,12 +917,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         int b1 = lo8 * kCoarse, b2 = hi8 * kCoarse + kCoarse - 1;
         if (hi8 - lo8 < 4) {  // 32 bins at most: every warp for itself
           const int bin = min(kBins - 1, lo8 * kCoarse + lane);
-          uint32_t w[kMaxCluster];
-#pragma unroll
-          for (int c = 0; c < kMaxCluster; ++c) w[c] = *cluster.map_shared_rank(&s.lo[bin], c & (ranks - 1));
+          uint32_t w[G::kMost];
+          G::all(&s.lo[bin], w);
           float mass = 0.f;
 #pragma unroll
-          for (int c = 0; c < kMaxCluster; ++c) mass += c < ranks ? (float)w[c] : 0.f;
+          for (int c = 0; c < G::kMost; ++c) mass += (float)w[c];
           mass *= ptx::ex2(-0.0109892786f * (float)bin);  // 31.2 / 4096 log2(e)
           float upto = mass;
 #pragma unroll
@@ -968,21 +995,21 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           if (lane == 0) s.weight = make_ulonglong2(x, x + y);
         }
         if (tid < kMaxCluster) s.ranked[tid] = 0;
-        cluster.sync();
+        G::sync();
         ulonglong2 v = make_ulonglong2(0, 0);
-        if (lane < ranks) v = *peer(&s.weight, lane, ranks);
+        if (lane < ranks) v = *G::peer(&s.weight, lane);
         const u64 before = warp_sum((u64)v.x), whole = warp_sum((u64)v.y);
         bool exact;
         u64 target = share_of(top_p, whole, &exact);
-        const int n = join_lists<T>(s, &klo, &khi);
+        const int n = join_lists<T, ONE>(s, &klo, &khi);
         if (exact) {
           // (a share of a half does it in every other row, others hardly ever)
           bool lost = false;
           pass.some(fmaxf(cut.v, -kTop), [&](float l, int) { lost |= l < ends; });
           lost = __syncthreads_or(lost);
           if (tid == 0) s.best = lost;
-          cluster.sync();
-          target += __any_sync(0xffffffffu, lane < ranks && *peer(&s.best, lane, ranks)) ? 1 : 0;
+          G::sync();
+          target += __any_sync(0xffffffffu, lane < ranks && *G::peer(&s.best, lane)) ? 1 : 0;
         }
         if (n <= kList) {
           const int g = group_of(n), i = tid / g;
@@ -1008,7 +1035,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           own_sums = (lane < ranks ? v.x + s.ranked[lane] : 0);
         } else {
           const float over = logit_of(khi);
-          cut = select<true, T>(pass, s, cut, sc, klo, khi, false, steps, before, target, nullptr);
+          cut = select<true, ONE, T>(pass, s, cut, sc, klo, khi, false, steps, before, target, nullptr);
           if (least > cut.v) cut = Cut{least, (int)kIndexMask};
           const float from = fmaxf(ends, cut.v);
           pass.each([&](const float (&x)[4], int at) {
@@ -1032,8 +1059,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         __syncthreads();
         const u64 own = warp_sum(lane < kWarps ? s.scan[lane] : 0);
         if (tid == 0) s.sum = own;
-        cluster.sync();
-        own_sums = lane < ranks ? *peer(&s.sum, lane, ranks) : 0;
+        G::sync();
+        own_sums = lane < ranks ? *G::peer(&s.sum, lane) : 0;
       }
       total = warp_sum(own_sums);
       u64 before = warp_sum(lane < rank ? own_sums : 0);
@@ -1044,8 +1071,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         pass.some(cut.v, [&](float l, int at) {
           if (cut.keeps(l, pass.first + at)) atomicMin(&s.first, pass.first + at);
         });
-        cluster.sync();
-        const int first = lane < ranks ? *peer(&s.first, lane, ranks) : INT_MAX;
+        G::sync();
+        const int first = lane < ranks ? *G::peer(&s.first, lane) : INT_MAX;
         if (rank == 0) {
           const int best = (int)__reduce_min_sync(0xffffffffu, (unsigned)first);
           if (tid == 0) token = best;
@@ -1121,12 +1148,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     });
   }
   // ---- the end
-  cluster.sync();  // no CTA leaves while another may still read what it tells
+  G::sync();  // no CTA leaves while another may still read what it tells
 }
 
-template <typename T, bool VEC>
+template <typename T, bool VEC, bool ONE>
 cudaError_t run(const SampleArgs& a, int ranks, size_t smem, cudaStream_t stream) {
-  auto kernel = sample_kernel<T, VEC>;
+  auto kernel = sample_kernel<T, VEC, ONE>;
   static std::atomic<uint64_t> ready{0};  // devices whose kernel has its shared memory's size
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1147,7 +1174,7 @@ cudaError_t run(const SampleArgs& a, int ranks, size_t smem, cudaStream_t stream
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = ONE ? 0 : 1;
   e = cudaLaunchKernelEx(&cfg, kernel, a);
   if (e != cudaSuccess) return e;
   count_launch();
@@ -1175,8 +1202,13 @@ cudaError_t launch_sample(SampleArgs a, bool bf16, cudaStream_t stream) {
   while (ranks < kMaxCluster && (long long)a.N * ranks * 2 <= 152 && chunk_of(ranks) > kThreads * n) ranks *= 2;
   a.chunk = chunk_of(ranks);
   const size_t smem = (size_t)a.chunk * esz;
-  if (bf16) return vec ? run<__nv_bfloat16, true>(a, ranks, smem, stream) : run<__nv_bfloat16, false>(a, ranks, smem, stream);
-  return vec ? run<float, true>(a, ranks, smem, stream) : run<float, false>(a, ranks, smem, stream);
+  auto pick = [&](auto one) {
+    constexpr bool ONE = decltype(one)::value;
+    if (bf16)
+      return vec ? run<__nv_bfloat16, true, ONE>(a, ranks, smem, stream) : run<__nv_bfloat16, false, ONE>(a, ranks, smem, stream);
+    return vec ? run<float, true, ONE>(a, ranks, smem, stream) : run<float, false, ONE>(a, ranks, smem, stream);
+  };
+  return ranks == 1 ? pick(std::true_type()) : pick(std::false_type());
 }
 
 }  // namespace dflash
