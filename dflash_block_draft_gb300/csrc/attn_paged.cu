@@ -510,6 +510,7 @@ cudaError_t launch_attn_paged(PagedArgs a, bool bf16, void* ws, cudaStream_t str
   // Without a page there is no tensor to describe to TMA: the CUDA-core kernel with
   // its small row tiles.
   if (p.tc && a.num_pages > 0) {
+    if (a.parents) a.tiles = (float)a.R * a.Hkv * (((long long)a.max_q * a.G + a.rows - 1) / a.rows);
     e = launch_paged_tc(a, grid, stream);
   } else {
     const int most = p.tc ? 2 * kSms : p.max_grid;

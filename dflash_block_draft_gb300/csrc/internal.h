@@ -149,6 +149,7 @@ struct PagedArgs {
   int causal;
   const int32_t* parents; // [total_q], a drafted tree's (causal is set then); nullable
   float scale_log2;       // scale * log2(e)
+  float tiles;            // row tiles in all, at most, where fewer CTAs may share them; 0: never
   int rows;               // rows (token, head of the group) of a row tile
   // workspace: partial results of row tiles that several CTAs share
   paged::Meta* meta;      // [grid]

@@ -16,6 +16,12 @@
 // by an earlier CTA, slot 2c + 1 for the piece that begins one and is cut by the
 // range's end.  The CTA that begins a cut row tile writes down in meta[c] how many
 // CTAs share it, and the merge kernel adds the pieces up in that order.
+// Where `tiles` row tiles in all are given (trees on the tensor cores), fewer CTAs share a
+// short line: a piece costs the merge a fifth of what a key tile costs a CTA, so that the sum
+// is least with sqrt(5 tiles T) CTAs; up to 12 pieces a row tile are merged in two reads whatever
+// their number.  (One tree of 24 nodes, 8 key/value heads, behind 4096 positions 18.5 us
+// with 106 CTAs, 20.4 with 152; behind 1000, 15.8 with 45 CTAs and 13.9 with 88; behind 8192 and
+// more, and for several trees, all CTAs work as before.)
 #pragma once
 
 #include "common.cuh"
@@ -236,7 +242,9 @@ __device__ __forceinline__ void find_range(const PagedArgs& a, int tid, Range* o
     total += scratch[w];
   }
   const long long before = base + c - mine;
-  const int ctas = (int)min((long long)gridDim.x, total), me = blockIdx.x;
+  int ctas = (int)min((long long)gridDim.x, total);
+  if (a.tiles > 0.f) ctas = (int)fminf((float)ctas, fmaxf(12.f * a.tiles, sqrtf(5.f * a.tiles * (float)total)));
+  const int me = blockIdx.x;
   const long long share = ctas > 0 ? quotient(total, ctas) : 0;
   const int more = (int)(total - share * ctas);
   const long long t0 = me < ctas ? share * me + min(me, more) : total;
