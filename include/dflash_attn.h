@@ -534,8 +534,10 @@ DFLASH_API dflash_status_t dflash_verify(const dflash_verify_dims_t* dims, const
  * recorded as DFLASH_ERR_INVALID and gets token 0 and probs 0.  NaN in top_p or min_p
  * leaves the filter out; a temperature below 2^-100 counts as 2^-100.
  * Weights are held in steps of 2^-44 of the largest and added up as whole numbers: the
- * result does not depend on the order of the sums (a w below 2^-45 counts as zero; its
- * probability is still written, and u = 0 draws the first token of S whatever it weighs).  V up to DFLASH_SAMPLE_MAX_V.
+ * result does not depend on the order of the sums.  A w below 2^-45 counts as zero in them;
+ * its probability is still written, u = 0 draws the first token of S whatever it weighs, and a
+ * beginning that meets top_p exactly falls short of it where such tokens follow.  V up to
+ * DFLASH_SAMPLE_MAX_V.
  */
 #define DFLASH_SAMPLE_MAX_V 393216
 typedef struct {

@@ -5,6 +5,7 @@ binding.
 from __future__ import annotations
 
 import math
+from fractions import Fraction
 
 import numpy as np
 
@@ -66,8 +67,13 @@ def distribution(logits, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
         while end < len(order):
             run += e[end]
             end += 1
-            if run >= top_p * whole:
-                break
+            if abs(run - top_p * whole) > 1e-9 * whole:
+                if run > top_p * whole:
+                    break
+            else:  # too near for sums in 64 bits; a weight that 64 bits hold as 0 is above 0
+                exact = sum(map(Fraction, e[:end])) - Fraction(top_p) * sum(map(Fraction, e))
+                if exact > 0 or (exact == 0 and e[-1] > 0):
+                    break
         order, e = order[:end], e[:end]
     for i, y in zip(order, e):
         if not min_p > 0 or y >= min(min_p, 1.0):

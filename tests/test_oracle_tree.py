@@ -38,6 +38,14 @@ def test_distribution_is_the_only_set_that_meets_the_definition(top_k, top_p, mi
         np.testing.assert_allclose(w, np.where(np.isin(np.arange(7), kept), e, 0))
 
 
+def test_a_share_that_is_met_exactly():
+    """Half of two equal weights is one of them, but less than half where anything follows, however little."""
+    kept = lambda x, **s: np.flatnonzero(otr.distribution(x, 1.0, top_p=0.5, **s)).tolist()  # noqa: E731
+    assert kept([0.0, 3.0, 3.0]) == [1, 2] and kept([3.0, -np.inf, 3.0]) == [0]
+    for less in (40.0, 700.0, 2000.0):  # e^-40 is lost in a sum of 64 bits, e^-2000 by itself
+        assert kept([3.0, 3.0, 3.0 - less]) == [0, 1] and kept([3.0, 3.0, 3.0 - less], top_k=2) == [0]
+
+
 def test_sample_has_the_distribution():
     w = otr.distribution([1.0, -np.inf, 2.0, 0.5, np.nan], 1.0)
     assert w[1] == w[4] == 0
