@@ -73,8 +73,8 @@ constexpr int kDirect = 160;      // top-k up to here: the tokens above the k-th
 constexpr int kMaxCluster = 8;
 constexpr int kIndexBits = 19;    // of a token's number
 constexpr uint32_t kIndexMask = (1u << kIndexBits) - 1;
-constexpr int kChunkMax = 49152;  // logits a CTA can hold
-static_assert(DFLASH_SAMPLE_MAX_V <= kMaxCluster * kChunkMax && DFLASH_SAMPLE_MAX_V <= (int)kIndexMask + 1, "vocabulary");
+constexpr int kChunkBytes = 196608;  // of logits that a CTA can hold
+static_assert(DFLASH_SAMPLE_MAX_V <= kMaxCluster * kChunkBytes / 4 && DFLASH_SAMPLE_MAX_V <= (int)kIndexMask + 1, "vocabulary");
 static_assert(kCoarse == 8 && kParts == kThreads && kThreads >= 2 * kList, "thread layout");
 constexpr float kTop = 0x1p126f;  // logits above count as it, those below -kTop are no choice: differences are finite
 // Margin of the masses of top-p's first look, on either side of the comparison: they are off by
@@ -246,7 +246,7 @@ struct Row {
 
 static_assert(offsetof(Row, lo) % 16 == 0 && offsetof(Row, listed) % 16 == 0 && offsetof(Row, weight) % 16 == 0 &&
                   offsetof(Row, low) % 8 == 0, "read in pieces of 16 and 8 bytes");
-static_assert(sizeof(Row) + kChunkMax * sizeof(float) <= 232448, "shared memory budget");
+static_assert(sizeof(Row) + kChunkBytes <= 232448, "shared memory budget");
 
 // Adds to a 64-bit sum in shared memory, the halves by themselves.
 __device__ __forceinline__ void add64(u64* to, u64 w) {
@@ -951,7 +951,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       }
       // ---- the weights: those in front of the bracket are kept, and those in it come to the list
       uint32_t klo = ~0u, khi = 0;
-      Steps44 kept = {0, 0}, rest = {0, 0};  // (96 tokens a thread at most)
+      Steps44 kept = {0, 0}, rest = {0, 0};  // (192 tokens a thread at most)
       pass.each([&](const float (&x)[4], int at) {
         if (!__any_sync(0xffffffffu, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) >= floor)) return;
         Steps44 w[4];
@@ -1160,7 +1160,7 @@ cudaError_t run(const SampleArgs& a, int ranks, size_t smem, cudaStream_t stream
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (dev >= 64 || !(ready.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kChunkMax * sizeof(T)));
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kChunkBytes);
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_release);
   }
@@ -1187,19 +1187,23 @@ cudaError_t launch_sample(SampleArgs a, bool bf16, cudaStream_t stream) {
   const int esz = bf16 ? 2 : 4, n = 16 / esz;
   const bool vec = a.V % n == 0 && ((uintptr_t)a.x & 15u) == 0 && (a.N == 1 || a.xs % n == 0);
   a.probs_vec = a.V % 4 == 0 && ((uintptr_t)a.probs & 15u) == 0 && (a.N == 1 || a.ps % 4 == 0);
-  // CTAs a row: as few as hold a share of 64 KB (two CTAs an SM, so that one row comes in while
-  // another is worked on), more while there is an SM for each.  What a row costs besides its
-  // tokens is every CTA's: 1664 rows of 32000 bf16 logits take 95 us with one CTA, 140 with two and
-  // 260 with four; 128 of 131072 fp32 134 with eight (64 KB) and 149 with four; 64 of 131072 bf16
-  // 25 with four and 32 with eight.  With few rows the share of the tokens counts: 16 rows of
-  // 32000 fp32 10.6, 12.6 and 16.8 us with eight, two and one, one row of 131072 12.5 with eight and 16.5 with four.
+  // CTAs a row.  What a row costs besides its tokens is every CTA's, and a single one waits for no
+  // other: one where a row fits, else as many as bring two CTAs an SM (64 KB each, so that one row comes
+  // in while another is worked on).  600 rows of 98304 bf16 logits take 107 us with one CTA (temperature alone;
+  // top-k 40: 51; top-p 0.9: 248), 137 (100, 286) with four; 1000 of 32000 fp32 92 (66, 150), 98 (80, 168) with
+  // two; 128 of 131072 fp32 with top-p 128 with eight, 142 with four.  While there is an SM for each,
+  // more CTAs share a long row: 38 rows of 50257 bf16 17.3 (14.5, 30.9) with four and 20.7 (14.4, 51.3)
+  // with one, but 60 of 8192 fp32 10.3 (10.4, 14.5) with two and 8.3 (8.3, 12.5) with one; 16384 are
+  // the same either way.
   auto chunk_of = [&](int ranks) {
     const int unit = kThreads * n;
     return ((a.V + ranks - 1) / ranks + unit - 1) / unit * unit;
   };
   int ranks = 1;
-  while (ranks < kMaxCluster && chunk_of(ranks) * esz > 65536) ranks *= 2;
-  while (ranks < kMaxCluster && (long long)a.N * ranks * 2 <= 152 && chunk_of(ranks) > kThreads * n) ranks *= 2;
+  if (chunk_of(1) * esz > kChunkBytes)
+    while (ranks < kMaxCluster && chunk_of(ranks) * esz > 65536) ranks *= 2;
+  if (a.V > 16384)
+    while (ranks < kMaxCluster && (long long)a.N * ranks * 2 <= 152) ranks *= 2;
   a.chunk = chunk_of(ranks);
   const size_t smem = (size_t)a.chunk * esz;
   auto pick = [&](auto one) {

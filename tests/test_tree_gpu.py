@@ -212,10 +212,11 @@ def test_sample_large_vocabularies(dfl, V, dtype):
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("what", ["steps", "equal", "two", "one_high", "wide"])
-def test_sample_ties_and_peaks(dfl, what, dtype):
+@pytest.mark.parametrize("V", [9000, 20000])  # a row in one CTA, and in eight
+def test_sample_ties_and_peaks(dfl, V, what, dtype):
     """Equal logits are cut by their numbers; the ranges of the search hold hundreds of them."""
     rng = np.random.default_rng(8)
-    N, V = 4, 9000
+    N = 4
     x = {"steps": np.round(rng.standard_normal((N, V)) * 2), "equal": np.zeros((N, V)),
          "two": (rng.random((N, V)) < 0.5).astype(float), "one_high": rng.standard_normal((N, V)) * 0.01,
          "wide": rng.standard_normal((N, V)) * 10.0 ** rng.integers(-6, 7, (N, V))}[what]
@@ -233,10 +234,10 @@ def test_sample_ties_and_peaks(dfl, what, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
-def test_sample_masks_and_odd_values(dfl, dtype):
+@pytest.mark.parametrize("V", [5000, 20000])
+def test_sample_masks_and_odd_values(dfl, V, dtype):
     """-inf, the type's lowest value and NaN are no choice, +inf and what is too large are equal."""
     rng = np.random.default_rng(9)
-    V = 5000
     x = (rng.standard_normal((8, V)) * 2).astype(np.float32)
     hide = rng.random((8, V)) < 0.9
     x[0][hide[0]] = -np.inf
@@ -291,6 +292,26 @@ def test_sample_settings_of_each_row_and_rows_by_themselves(dfl):
         assert one[0][0] == tok[r]
         np.testing.assert_array_equal(one[1][0], probs[r])
     np.testing.assert_array_equal(_sample(dfl, x, u, probs=False, **s)[0], tok)
+    assert dfl.dflash_last_device_error() == 0
+
+
+@pytest.mark.parametrize("V,dtype", [(17001, "fp32"), (32000, "bf16"), (49152, "fp32"), (50257, "bf16"), (98304, "bf16"),
+                                     (49153, "fp32"), (98305, "bf16")])
+def test_sample_long_rows_of_large_batches(dfl, V, dtype):
+    """Rows of many are worked on by one CTA where it can hold them, a row by itself by eight: the same bits."""
+    rng = np.random.default_rng(V)
+    N = 90
+    x = _rand(rng, (N, V), dtype, 2.5)
+    s = dict(temperature=rng.choice([0.4, 1.0, 1.8], N), top_k=rng.choice([0, 0, 40, 300], N),
+             top_p=rng.choice([1.0, 0.9, 0.6], N), min_p=rng.choice([0.0, 0.01], N))
+    u = rng.random(N, np.float32)
+    tok, probs = _sample(dfl, x, u, **s)
+    for r in range(0, N, 4):
+        one = _sample(dfl, x[r:r + 1], u[r:r + 1], **{k: v[r:r + 1] for k, v in s.items()})
+        assert one[0][0] == tok[r]
+        np.testing.assert_array_equal(one[1][0], probs[r])
+    few = [0, 45, 89]
+    _check_sample(x[few], u[few], tok[few], probs[few], **{k: v[few] for k, v in s.items()})
     assert dfl.dflash_last_device_error() == 0
 
 
@@ -811,11 +832,12 @@ def test_offsets_beyond_32_bits(dfl):
     assert (tok[:-1] == 131072).all() and tok[-1] == 262143 and dfl.dflash_last_device_error() == 0
 
 
+@pytest.mark.parametrize("V", [3000, 20000])
 @pytest.mark.parametrize("top_k", [0, 2, 3, 700])
-def test_sample_shares_that_are_met_exactly(dfl, top_k):
+def test_sample_shares_that_are_met_exactly(dfl, top_k, V):
     """Two equal tokens have half of the weight each, and one of them is half of it; where further tokens
     follow, however little they weigh, it is less than half."""
-    x = torch.full((3, 3000), -1e30, device="cuda")
+    x = torch.full((3, V), -1e30, device="cuda")
     x[:, 1000], x[:, 2000] = 5.0, 5.0
     x[1, 7] = 5.0 - 0.36      # e^-36: less than half a step beside the two
     x[2] = float("-inf")
@@ -832,11 +854,11 @@ def test_sample_shares_that_are_met_exactly(dfl, top_k):
     assert dfl.dflash_last_device_error() == 0
 
 
-def test_sample_a_random_number_of_0_draws_the_first_kept_token(dfl):
+@pytest.mark.parametrize("V", [3000, 20000])
+def test_sample_a_random_number_of_0_draws_the_first_kept_token(dfl, V):
     """Also where it weighs less than a step of the sums; with and without a list of the kept."""
-    x = torch.zeros((1, 3000), device="cuda")
-    x[0, 5:] = 40.0 + torch.arange(2995, device="cuda") * 1e-3
-    x[0, :5] = float("-inf")
+    x = torch.full((1, V), float("-inf"), device="cuda")
+    x[0, 5:3000] = 40.0 + torch.arange(2995, device="cuda") * 1e-3
     x[0, 3] = 1.0
     for s, want in ((dict(), 3), (dict(top_k=100), 2900), (dict(top_k=2996), 3), (dict(top_p=0.999), None),
                     (dict(temperature=0.0), 2999), (dict(min_p=0.5), None)):
@@ -845,7 +867,7 @@ def test_sample_a_random_number_of_0_draws_the_first_kept_token(dfl):
     assert dfl.dflash_last_device_error() == 0
 
 
-@pytest.mark.parametrize("V", [4096, 1001])
+@pytest.mark.parametrize("V", [4096, 1001, 20000])
 def test_sample_distributions_in_place_of_the_logits(dfl, V):
     rng = np.random.default_rng(17)
     x, u = _rand(rng, (40, V), "fp32", 2.0), torch.from_numpy(rng.random(40, np.float32)).cuda()
