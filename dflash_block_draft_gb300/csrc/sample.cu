@@ -8,8 +8,8 @@
 // "cut", a logit and a token's number), and the token is the first one, in the order of the
 // numbers, whose running sum of kept weights exceeds u times the whole.
 //
-// A cluster of 1 to 8 CTAs takes a row and holds it in shared memory: the logits are read
-// from memory once, by 16 bytes a thread.  Then
+// One CTA, or a cluster of 2 to 8, takes a row and holds it in shared memory: the logits are
+// read from memory once, by 16 bytes a thread.  Then
 //   the largest logit, and the maxima of 512 groups of threads (one exchange);
 //   top-k up to 160: a bound that k of the groups reach, found by halving, so that at least k
 //     tokens lie above it and about k + k^2 / 1000 more; they go into a list of 256 whose order
@@ -20,25 +20,27 @@
 //   top-p: the weights' approximate masses in 4096 equal steps say between which logits the
 //     cut must lie; the exact pass over all tokens adds up what is in front of them and lists
 //     what is between, and the exact border falls in the list (or, where that holds too
-//     many, is looked for as top-k's);
+//     many, is looked for by the bits of logit and number);
 //   the sums of kept weights by runs of tokens, one exchange, and the run that passes u times
 //     the whole once more, a few tokens a thread.
 //
-// Bound by instructions: a weight costs some 25, a look at a logit 2 to 15, and what a row
+// Bound by instructions: a weight costs some 21, a look at a logit 2 to 15, and what a row
 // costs besides (barriers, exchanges, the list) is as much as 8000 tokens of a CTA.  Two CTAs of
 // 512 threads an SM, one row's wait under the other's work.  Measured: 64 rows of 131072 bf16
-// logits with temperature alone 21.5 us; 1664 rows of 32000 with top-k 40 in most of them 93;
-// 128 rows of 131072 fp32 with top-p and the distributions written 131; 4 rows of 32000 9.5.
+// logits with temperature alone 20 us; 1664 rows of 32000 with top-k 40 in most of them 77;
+// 128 rows of 131072 fp32 with top-p and the distributions written 126; 4 rows of 32000 9.2.
 // (With a histogram of all weights for top-p and a second exact pass, 128 rows took 251 us;
 // top-k by a histogram of everything above the least of the threads' maxima, 4 rows 17.)  The
 // kernel runs once through most of its code, which was 190 KB where loops were copied and
 // functions inlined: 4 rows then took 29 us.
 //
 // Weights are whole steps of 2^-44 of the largest one, added up as integers, so that no sum
-// depends on the order, the number of CTAs or the threads' timing.  A pair of weights takes 19
-// packed fp32 instructions in bf16 and 25 in fp32, and each some 9 others: l - m, times
+// depends on the order, the number of CTAs or the threads' timing.  A pair of weights takes 16
+// packed fp32 instructions in bf16 and 22 in fp32, and each some 13 others: l - m, times
 // log2(e) / T as two floats; 2^y from a table of 2^(j / 128) in two floats and a polynomial of
-// degree 3; the bits of sums with 2.5 and 1.5 2^-21 count the steps, as in verify.cu.  The
+// degree 3; the bits of sums with 2.5 and 1.5 2^-21 count the steps, as in verify.cu.  (The packed
+// instructions bound it: four fewer a pair took 64 rows from 24.6 us to 22.7 where eight copies of the
+// table without bank conflicts, or shuffles in its place, changed nothing.)  The
 // weights' errors, 2^-33.5 rms, are each other's by chance and add up to a border's as their
 // root: of a vocabulary of 131072 every 10^7th row would draw another token than the real numbers
 // (every 50th with fp32 sums of weights that are off in one direction).  Twice the instructions
@@ -404,7 +406,7 @@ __device__ __forceinline__ void tell_keys(Row& s, uint32_t klo, uint32_t khi) {
   }
 }
 // A row's CTAs.  ONE: a single one, and none of the cluster's barriers and reads (1664 rows of
-// 32000 took 91 us with them, 79 without).
+// 32000 took 92 us with them, 78 without).
 template <bool ONE>
 struct Team {
   static constexpr int kMost = ONE ? 1 : kMaxCluster;
