@@ -14,9 +14,9 @@
 //   top-k up to 160: a bound that k of the groups reach, found by halving, so that at least k
 //     tokens lie above it and about k + k^2 / 1000 more; they go into a list of 256 whose order
 //     comes from comparing all pairs, and everything else is worked out from the list;
-//   larger k: the tokens above the bound in 512 equal steps of the logit, counted, the counts
-//     merged through distributed shared memory, and the step in which k is reached listed (or
-//     divided again, by the bits of logit and number, so that ties divide too);
+//   larger k: the tokens above a bound counted in 4096 equal steps of the logit, the counts
+//     merged through distributed shared memory, and the step in which k is reached listed (or,
+//     where it holds too many, divided by the bits of logit and number, so that ties divide too);
 //   top-p: the weights' approximate masses in 4096 equal steps say between which logits the
 //     cut must lie; the exact pass over all tokens adds up what is in front of them and lists
 //     what is between, and the exact border falls in the list (or, where that holds too
@@ -218,6 +218,29 @@ __device__ __forceinline__ float value_of(uint32_t w, __nv_bfloat16) {
   return fmaxf(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
 
+// A bit for each logit of a 32-bit word that lies from lo to hi (bf16: two, by borders in bf16).
+template <typename T>
+struct Between;
+template <>
+struct Between<float> {
+  float lo, hi;
+  __device__ __forceinline__ Between(float lo_, float hi_) : lo(lo_), hi(hi_) {}
+  __device__ __forceinline__ unsigned operator()(uint32_t w) const {
+    return __uint_as_float(w) >= lo && __uint_as_float(w) <= hi;
+  }
+};
+template <>
+struct Between<__nv_bfloat16> {
+  __nv_bfloat162 lo, hi;
+  __device__ __forceinline__ Between(float lo_, float hi_)
+      : lo(__bfloat162bfloat162(__float2bfloat16_ru(lo_))), hi(__bfloat162bfloat162(__float2bfloat16_rd(hi_))) {}
+  __device__ __forceinline__ unsigned operator()(uint32_t w) const {
+    const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&w);
+    const unsigned both = __hge2_mask(x, lo) & __hle2_mask(x, hi);
+    return (both & 1u) | (both >> 15 & 2u);
+  }
+};
+
 struct Row {
   // what a CTA tells the others
   float coarse[kThreads];          // masses of kCoarse bins each
@@ -358,19 +381,22 @@ struct Pass {
       }
     }
   }
-  // body(l, at) for every logit for which mask bit k of test(x, k): few of them
-  template <typename Test, typename Body>
-  __device__ __forceinline__ void where(Test test, Body body) const {
-    each([&](const float (&x)[4], int at) {
-      unsigned mask = 0;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) mask |= (unsigned)test(x[k]) << k;
+  // body(l, at) for every logit from `lo` to `hi`: few of them
+  template <typename Body>
+  __device__ __forceinline__ void range(float lo, float hi, Body body) const {
+    constexpr int N = Vec<T>::N;
+    const uint4* v = reinterpret_cast<const uint4*>(chunk + (threadIdx.x >> 5) * run) + (threadIdx.x & 31);
+    const Between<T> in(lo, hi);
+#pragma unroll 2
+    for (int k = 0; k < run; k += 32 * N, v += 32) {
+      const uint4 w = *v;
+      unsigned mask = in(w.x) | in(w.y) << (N / 4) | in(w.z) << (N / 2) | in(w.w) << (3 * N / 4);
 #pragma unroll 1
-      for (; mask; mask &= mask - 1) {
-        const int k = at + __ffs(mask) - 1;
-        body(logit(k), k);
+      for (const int at = (int)(reinterpret_cast<const T*>(v) - chunk); mask; mask &= mask - 1) {
+        const int e = at + __ffs(mask) - 1;
+        body(logit(e), e);
       }
-    });
+    }
   }
 };
 
@@ -503,25 +529,114 @@ __device__ __forceinline__ Cut cut_at(u64 place) {
   return Cut{logit_of((uint32_t)(place >> kIndexBits)), (int)(kIndexMask - (uint32_t)(place & kIndexMask))};
 }
 
-// A condition that is the same all along a loop, tested where it stands: a copy of the loop for
-// either value would be read from memory on its only way through.
-__device__ __forceinline__ bool here(bool x) {
-  int y = x;
-  asm volatile("" : "+r"(y));
-  return y != 0;
+// The listed token in which the running count or weight, `before` in front of the list, reaches the target.
+template <bool WEIGHTS>
+__device__ __forceinline__ Cut cut_in_list(Row& s, int n, u64 before, u64 target) {
+  const int g = group_of(n), i = threadIdx.x / g;
+  int rank;
+  const u64 sum = in_front(s, n, g, i, &rank);
+  if (i < n) {
+    const u64 at = before + (WEIGHTS ? sum : rank), w = WEIGHTS ? s.all_w[i] : 1;
+    if (at < target && target <= at + w) s.cut = s.all[i];
+  }
+  __syncthreads();
+  return cut_at(s.cut);
+}
+
+// The bins of s.lo in which a running sum over all CTAs' bins passes a border.  A bin's sum is its
+// content times 2^(-slope b) (ratio: 2^-slope); b1: the first bin whose running sum times `over`
+// reaches share times the whole, or `least`; b2: the first one whose running sum reaches `over` times that.
+// b1 < 0: the whole is below `least`.  before: the sum in front of b1, where b1 = b2.
+struct Border {
+  int b1, b2;
+  float before;
+};
+template <bool ONE>
+__device__ __forceinline__ Border border(Row& s, float slope, float ratio, float over, float share, float least) {
+  using G = Team<ONE>;
+  const int tid = threadIdx.x, lane = tid & 31;
+  {
+    const uint4* bins = reinterpret_cast<const uint4*>(&s.lo[kCoarse * tid]);
+    const uint4 x = bins[0], y = bins[1];
+    const uint32_t v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+    float mass = 0.f;
+#pragma unroll
+    for (int k = 7; k >= 0; --k) mass = fmaf(mass, ratio, (float)v[k]);
+    s.coarse[tid] = mass * ptx::ex2(-slope * (float)(kCoarse * tid));  // (at the first bin's beginning)
+  }
+  if (tid == 0) {
+    s.b1 = kThreads;
+    s.b2 = -1;
+  }
+  G::sync();
+  clear_list(s);
+  // ---- merged: eight bins together, then those that the border lies in by themselves
+  float part[G::kMost];
+  G::all(&s.coarse[tid], part);
+  float v = 0.f;
+#pragma unroll
+  for (int c = 0; c < G::kMost; ++c) v += part[c];
+  float all;
+  const float c0 = block_scan(v, s.scan_f, &all), c1 = c0 + v;
+  const float want = fmaxf(share * all, least);
+  if (all < least) return Border{-1, -1, 0.f};
+  // (rounding can show two threads the same border, or none: then the bracket is the wider one)
+  s.coarse_before[tid] = c0;
+  if (c1 * over >= want && !(c0 * over >= want)) atomicMin(&s.b1, tid);
+  if (c1 >= want * over && !(c0 >= want * over)) atomicMax(&s.b2, tid);
+  __syncthreads();
+  const int lo8 = s.b1 == kThreads ? 0 : s.b1, hi8 = s.b2 < 0 ? kThreads - 1 : s.b2;
+  int b1 = lo8 * kCoarse, b2 = hi8 * kCoarse + kCoarse - 1;
+  float before = 0.f;
+  if (hi8 - lo8 < 4) {  // 32 bins at most: every warp for itself
+    const int bin = min(kBins - 1, b1 + lane);
+    uint32_t w[G::kMost];
+    G::all(&s.lo[bin], w);
+    float mass = 0.f;
+#pragma unroll
+    for (int c = 0; c < G::kMost; ++c) mass += (float)w[c];
+    mass *= ptx::ex2(-slope * (float)bin);
+    float upto = mass;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const float u = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += u;
+    }
+    upto += s.coarse_before[lo8];
+    const unsigned may = __ballot_sync(0xffffffffu, upto * over >= want), must = __ballot_sync(0xffffffffu, upto >= want * over);
+    // (where none of these bins reaches it, rounding hid the border: the last one)
+    const int end = (hi8 - lo8 + 1) * kCoarse - 1, e1 = may ? min(__ffs(may) - 1, end) : end;
+    b2 = b1 + (must ? min(__ffs(must) - 1, end) : end);
+    b1 += e1;
+    before = __shfl_sync(0xffffffffu, upto - mass, e1);
+  }
+  return Border{b1, b2, before};
+}
+
+// The border's bins as logits, which take one comparison each: what is above `first` lies in an
+// earlier bin, what is below `last` in a later one (steps are rounded, and off by a quarter besides:
+// two more).
+struct Bracket {
+  float first, last;
+};
+__device__ __forceinline__ Bracket logits_of(const Border& b, float m, float range) {
+  const float step = range * 0x1p-21f;
+  return Bracket{__fmaf_ru(-(float)((b.b1 << kStepBits) - 2), step, m),
+                 b.b2 < kBins - 1 ? __fmaf_rd(-(float)(((b.b2 + 1) << kStepBits) + 2), step, m) : -INFINITY};
+}
+__device__ __forceinline__ void clear_bins(Row& s) {
+  uint4* bins = reinterpret_cast<uint4*>(&s.lo[kCoarse * threadIdx.x]);
+  bins[0] = bins[1] = make_uint4(0, 0, 0, 0);
+  __syncthreads();
 }
 
 // The cut of top-k (WEIGHTS false; target: k) or top-p (true): the token, of those that
 // `prior` keeps and whose keys lie in [klo, khi], in which the running count or weight, `before` in
-// front of the range, reaches the target.  `linear` (top-k): the range of `steps` is divided
-// into 512 equal parts; else, and where that leaves too many tokens, the range is divided
-// by places, from the largest key to the smallest.
-// Top-k with all tokens of the row down to the cut's part in the list: *listed is their number.
-// Returns prior, and *listed -1, where there are fewer tokens than k.
+// front of the range, reaches the target.  The range is divided by places, from the largest
+// key to the smallest, into 512 parts.  Returns prior where there are fewer tokens than k.
 template <bool WEIGHTS, bool ONE, typename T>
 __device__ __forceinline__ Cut select(const Pass<T>& pass, Row& s, const Cut& prior, const Scale& sc, uint32_t klo,
-                                      uint32_t khi, bool linear, const Steps& steps, u64 before, u64 target,
-                                      int* listed) {
+                                      uint32_t khi, u64 before, u64 target) {
   using G = Team<ONE>;
   const int tid = threadIdx.x;
   u64 lo = (u64)klo << kIndexBits, hi = place_of(khi, 0);  // the range's places
@@ -533,24 +648,18 @@ __device__ __forceinline__ Cut select(const Pass<T>& pass, Row& s, const Cut& pr
     over = logit_of((uint32_t)(hi >> kIndexBits));
   };
   divide();
-  bool room = here(!WEIGHTS);
   auto part_of = [&](float l, int i) -> int {
     if (!prior.keeps(l, i)) return -1;
-    if (!WEIGHTS && here(linear)) {
-      const int part = steps.at(l) >> (21 - kPartBits);
-      return part < kParts ? part : -1;
-    }
     const u64 p = place_of(key_of(l), i);
     return p < lo || p > hi ? -1 : (int)((hi - p) >> shift);
   };
-  auto near = [&](float l) { return l >= under && l <= over; };
 #pragma unroll 1
   for (;;) {
     // ---- a histogram of the range
     s.lo[tid] = 0;
     if (WEIGHTS) s.hi[tid] = 0;
     __syncthreads();
-    pass.where(near, [&](float l, int at) {
+    pass.range(under, over, [&](float l, int at) {
       const int part = part_of(l, pass.first + at);
       if (part < 0) return;
       if (WEIGHTS) {
@@ -573,58 +682,30 @@ __device__ __forceinline__ Cut select(const Pass<T>& pass, Row& s, const Cut& pr
     for (int c = 0; c < G::kMost; ++c) v += ((u64)part_hi[c] << 32) + part_lo[c];
     u64 total;
     const u64 at = before + block_scan(v, s.scan, &total);
-    if (!WEIGHTS && before + total < target) {
-      *listed = -1;
-      return prior;
-    }
+    if (!WEIGHTS && before + total < target) return prior;
     if (at < target && target <= at + v) {  // one thread
       s.found = tid;
       s.found_before = at;
-      s.b1 = (int)min(at + v, (u64)kList + 1);  // tokens down to the end of this part
     }
     __syncthreads();
     const int part = s.found;
-    // top-k: everything down to this part fits the list
-    const bool whole = !WEIGHTS && room && s.b1 <= kList;
-    if (!whole) before = s.found_before;
+    before = s.found_before;
     // ---- the part's tokens
     klo = ~0u;
     khi = 0;
-    pass.where(near, [&](float l, int at) {
-      const int p = part_of(l, pass.first + at);
-      if (p >= 0 && (here(whole) ? p <= part : p == part)) enlist(s, l, pass.first + at, klo, khi);
+    pass.range(under, over, [&](float l, int at) {
+      if (part_of(l, pass.first + at) == part) enlist(s, l, pass.first + at, klo, khi);
     });
     tell_keys(s, klo, khi);
     G::sync();
     const int n = join_lists<T, ONE>(s, &klo, &khi);
-    if (whole) {
-      *listed = n;
-      return prior;
-    }
-    if (n <= kList) {
-      const int g = group_of(n), i = tid / g;
-      int rank;
-      const u64 sum = in_front(s, n, g, i, &rank);
-      if (i < n) {
-        const u64 at = before + (WEIGHTS ? sum : rank), w = WEIGHTS ? s.all_w[i] : 1;
-        if (at < target && target <= at + w) s.cut = s.all[i];
-      }
-      __syncthreads();
-      return cut_at(s.cut);  // (*listed stays 0)
-    }
+    if (n <= kList) return cut_in_list<WEIGHTS>(s, n, before, target);
     // ---- too many: what lies between the part's keys is divided
-    if (WEIGHTS || !linear) {
-      hi -= (u64)part << shift;
-      lo = max(lo, hi - ((1ull << shift) - 1));
-    } else {
-      hi = ~0ull;
-      lo = 0;
-    }
+    hi -= (u64)part << shift;
+    lo = max(lo, hi - ((1ull << shift) - 1));
     hi = min(hi, place_of(khi, 0));
     lo = max(lo, (u64)klo << kIndexBits);
     divide();
-    linear = here(false);
-    room = here(false);
   }
 }
 
@@ -769,7 +850,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     const bool limited = top_k > 0 && top_k < a.V;
     if (limited) {
       float bound, range;
-      bool linear = true;
+      bool tight = true;  // few tokens lie above the bound
       if (top_k <= __syncthreads_count(top >= -kTop)) {
         // ---- k groups reach this far: their maxima, halved towards the k-th
         bound = logit_of(block_least(s, top >= -kTop ? key_of(top) : ~0u));
@@ -799,17 +880,42 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         const bool known = top_k > kThreads && top_k <= (int)warp_sum(v.y) && low >= -kTop;
         bound = known ? low : ends;
         range = known ? 1.001f * (m - low) : 31.2f * t;
+        tight = false;
       }
-#pragma unroll 1
-      while (n == 0) {
-        cut = select<false, ONE, T>(pass, s, cut, sc, key_of(bound), key_of(m), linear, Steps(m, fmaxf(range, 1e-30f)), 0,
-                               top_k, &n);
-        if (n >= 0) break;
-        n = 0;
-        if (!linear) break;  // fewer than k in all
-        bound = -kTop;       // the k-th has no weight: among all tokens
-        linear = false;
-        G::sync();      // the other CTAs have read this one's histogram
+      if (n == 0) {
+        // ---- counts in 4096 steps from the largest logit to the bound, and the k-th's step's tokens
+        range = fmaxf(range, 1e-30f);
+        const Steps steps(m, range);
+        clear_bins(s);
+        auto bin_of = [&](float l) { return min(kBins - 1, steps.at(l) >> kStepBits); };
+        if (tight)
+          pass.some(bound, [&](float l, int) { atomicAdd(&s.lo[bin_of(l)], 1u); });
+        else
+          pass.each([&](const float (&x)[4], int) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (x[k] >= bound) atomicAdd(&s.lo[bin_of(x[k])], 1u);
+          });
+        __syncthreads();
+        const Border at = border<ONE>(s, 0.f, 1.f, 1.f, 0.f, (float)top_k);
+        uint32_t klo = ~0u, khi = 0;
+        u64 before = 0;
+        int listed = kList + 1;
+        if (at.b1 >= 0) {
+          const Bracket in = logits_of(at, m, range);
+          pass.range(fmaxf(in.last, bound), in.first, [&](float l, int i) {
+            if (bin_of(l) == at.b1) enlist(s, l, pass.first + i, klo, khi);
+          });
+          tell_keys(s, klo, khi);
+          before = (u64)at.before;
+        } else {  // the k-th has no weight: among all tokens
+          klo = key_of(-kTop);
+          khi = key_of(m);
+        }
+        G::sync();
+        if (at.b1 >= 0) listed = join_lists<T, ONE>(s, &klo, &khi);
+        if (listed <= kList) cut = cut_in_list<false>(s, listed, before, top_k);
+        else cut = select<false, ONE, T>(pass, s, cut, sc, klo, khi, before, top_k);
       }
     }
     if (n > 0) {
@@ -873,13 +979,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       if (nucleus) {
         // ---- where top-p's cut can lie: the weights' masses in 4096 steps
         if (limited) G::sync();  // the other CTAs have read this one's histogram
-        uint4* bins = reinterpret_cast<uint4*>(&s.lo[kCoarse * tid]);
-        bins[0] = bins[1] = make_uint4(0, 0, 0, 0);
-        if (tid == 0) {
-          s.b1 = kThreads;
-          s.b2 = -1;
-        }
-        __syncthreads();
+        clear_bins(s);
         pass.each([&](const float (&x)[4], int) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -890,59 +990,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           }
         });
         __syncthreads();
-        const float first = ptx::ex2(-0.0879142291f * (float)tid);  // at the first bin's beginning: 31.2 / 512 log2(e)
-        {
-          const uint4 x = bins[0], y = bins[1];
-          const uint32_t v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-          float mass = 0.f;
-#pragma unroll
-          for (int k = 7; k >= 0; --k) mass = fmaf(mass, kBinRatio, (float)v[k]);
-          s.coarse[tid] = mass * first;
-        }
-        G::sync();
-        clear_list(s);
-        // ---- merged: eight bins together, then those that the border lies in by themselves
-        float part[G::kMost];
-        G::all(&s.coarse[tid], part);
-        float v = 0.f;
-#pragma unroll
-        for (int c = 0; c < G::kMost; ++c) v += part[c];
-        float all;
-        const float c0 = block_scan(v, s.scan_f, &all), c1 = c0 + v;
-        const float want = fmaxf(top_p, 1e-6f) * all;
-        // (rounding can show two threads the same border, or none: then the bracket is the wider one)
-        s.coarse_before[tid] = c0;
-        if (c1 * kOver >= want && !(c0 * kOver >= want)) atomicMin(&s.b1, tid);
-        if (c1 >= want * kOver && !(c0 >= want * kOver)) atomicMax(&s.b2, tid);
-        __syncthreads();
-        const int lo8 = s.b1 == kThreads ? 0 : s.b1, hi8 = s.b2 < 0 ? kThreads - 1 : s.b2;
-        int b1 = lo8 * kCoarse, b2 = hi8 * kCoarse + kCoarse - 1;
-        if (hi8 - lo8 < 4) {  // 32 bins at most: every warp for itself
-          const int bin = min(kBins - 1, lo8 * kCoarse + lane);
-          uint32_t w[G::kMost];
-          G::all(&s.lo[bin], w);
-          float mass = 0.f;
-#pragma unroll
-          for (int c = 0; c < G::kMost; ++c) mass += (float)w[c];
-          mass *= ptx::ex2(-0.0109892786f * (float)bin);  // 31.2 / 4096 log2(e)
-          float upto = mass;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const float u = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += u;
-          }
-          upto += s.coarse_before[lo8];
-          const unsigned may = __ballot_sync(0xffffffffu, upto * kOver >= want), must = __ballot_sync(0xffffffffu, upto >= want * kOver);
-          // (where none of these bins reaches it, rounding hid the border: the last one)
-          const int end = (hi8 - lo8 + 1) * kCoarse - 1;
-          b2 = b1 + (must ? min(__ffs(must) - 1, end) : end);
-          b1 += may ? min(__ffs(may) - 1, end) : end;
-        }
-        // as logits, which take one comparison each: what is above first_in lies in an earlier bin, what is
-        // below last_in in a later one (steps are rounded, and off by a quarter besides: two more)
-        const float step = 31.2f * t * 0x1p-21f;
-        first_in = __fmaf_ru(-(float)((b1 << kStepBits) - 2), step, m);
-        if (b2 < kBins - 1) last_in = __fmaf_rd(-(float)(((b2 + 1) << kStepBits) + 2), step, m);
+        const Border at = border<ONE>(s, 0.0109892786f, kBinRatio, kOver, fmaxf(top_p, 1e-6f), 0.f);  // 31.2 / 4096 log2(e)
+        const Bracket in = logits_of(at, m, 31.2f * t);
+        first_in = in.first;
+        last_in = in.last;
         // min-p ends in front of the bracket: top-p takes nothing away
         if (least >= ends && least > first_in) nucleus = false;
       }
@@ -1037,19 +1088,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           own_sums = (lane < ranks ? v.x + s.ranked[lane] : 0);
         } else {
           const float over = logit_of(khi);
-          cut = select<true, ONE, T>(pass, s, cut, sc, klo, khi, false, steps, before, target, nullptr);
+          cut = select<true, ONE, T>(pass, s, cut, sc, klo, khi, before, target);
           if (least > cut.v) cut = Cut{least, (int)kIndexMask};
           const float from = fmaxf(ends, cut.v);
-          pass.each([&](const float (&x)[4], int at) {
-            unsigned mask = 0;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) mask |= (unsigned)(x[k] >= from && x[k] <= over) << k;
-#pragma unroll 1
-            for (; mask; mask &= mask - 1) {
-              const int k = at + __ffs(mask) - 1;
-              const float l = pass.logit(k);
-              sum += weight<T>(sc, s.tab, l, cut.keeps(l, pass.first + k));
-            }
+          pass.range(from, over, [&](float l, int at) {
+            sum += weight<T>(sc, s.tab, l, cut.keeps(l, pass.first + at));
           });
         }
       }
