@@ -130,6 +130,13 @@ def test_attn_tree_long_contexts_are_cut_and_many_requests(dfl):
     _check_tree(dfl, rng, [int(a + x) if a else 0 for a, x in zip(n, rng.integers(0, 40, 300))], n, 16, 2, 1, 64, "bf16")
 
 
+@pytest.mark.parametrize("kv", [1500, 2600, 4120, 6000])
+def test_attn_tree_one_tree_is_shared_by_fewer_ctas(dfl, kv):
+    """One tree of eight key/value heads behind some thousand positions: about 60 to 130 CTAs take it."""
+    _check_tree(dfl, np.random.default_rng(kv), [kv], [24], 64, 16, 8, 128, "bf16")
+    _check_tree(dfl, np.random.default_rng(kv), [kv], [70], 16, 12, 3, 64, "bf16")
+
+
 def test_attn_tree_bf16_on_the_cuda_cores(dfl, monkeypatch):
     monkeypatch.setenv("DFLASH_FORCE_SIMT", "1")
     for kv, n, P, Hq, Hkv, D in TREES[2:5]:
