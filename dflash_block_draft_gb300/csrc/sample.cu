@@ -79,11 +79,16 @@ constexpr int kChunkBytes = 196608;  // of logits that a CTA can hold
 static_assert(DFLASH_SAMPLE_MAX_V <= kMaxCluster * kChunkBytes / 4 && DFLASH_SAMPLE_MAX_V <= (int)kIndexMask + 1, "vocabulary");
 static_assert(kCoarse == 8 && kParts == kThreads && kThreads >= 2 * kList, "thread layout");
 constexpr float kTop = 0x1p126f;  // logits above count as it, those below -kTop are no choice: differences are finite
-// Margin of the masses of top-p's first look, on either side of the comparison: they are off by
-// less than 3.4e-5 (bins linear within 7.2e-6, masses rounded down 1.5e-5, their slope's rounding
-// 4.6e-6, fp32 distances, powers and sums 7e-6).
-constexpr float kOver = 1.00008f;
+// Masses of top-p's first look: a weight within its bin, linear from 1 to e^(-31.2 / 4096), in
+// 1 / kMass, the finest unit in which all tokens that a CTA can hold fit one 32-bit bin (equal
+// logits, or a high temperature).
 constexpr float kBinRatio = 0.99241175f;  // e^(-31.2 / 4096)
+constexpr uint32_t kMass = 43690;
+constexpr uint32_t kMassSlope = (uint32_t)(kMass * 128 * (1.0 - 0.99241175) + 0.5);  // a 512th of a bin, in 2^-16
+static_assert((u64)kMass * (kChunkBytes / 2) < 1ull << 32, "a bin holds every token of a CTA");
+// Margin of the masses, on either side of the comparison: they are off by less than 2.7e-5 (bins
+// linear within 7.2e-6, masses rounded 1.2e-5, fp32 distances, powers and sums 7e-6).
+constexpr float kOver = 1.00008f;
 
 // ------------------------------------------------------------------ weights
 // 2^(j / 128) as a float and what it lacks.
@@ -984,8 +989,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const int q = steps.at(x[k]);
-            // the weight within its bin, linear from 1 to e^(-31.2 / 4096), in 1 / 65536
-            const uint32_t mass = (uint32_t)((65536 << kStepBits) - 497 * (q & 511)) >> kStepBits;
+            const uint32_t mass = ((kMass << 16) + 32768u - kMassSlope * (q & 511)) >> 16;
             if (x[k] >= floor) atomicAdd(&s.lo[min(kBins - 1, q >> kStepBits)], mass);
           }
         });

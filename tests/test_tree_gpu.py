@@ -322,6 +322,34 @@ def test_sample_long_rows_of_large_batches(dfl, V, dtype):
     assert dfl.dflash_last_device_error() == 0
 
 
+@pytest.mark.parametrize("V", [70000, 98304])
+@pytest.mark.parametrize("what", ["two", "equal", "whole", "hot", "narrow", "one_high"])
+def test_sample_many_tokens_of_one_weight(dfl, what, V):
+    """Rows of which one CTA holds more than 65536 tokens of nearly the same weight, with top-p: as the oracle, and
+    bit for bit as the row by itself, which eight CTAs share."""
+    rng = np.random.default_rng(V + len(what))
+    N = 90
+    x = {"two": lambda: (rng.random((N, V), np.float32) < 0.75), "equal": lambda: np.zeros((N, V)),
+         "whole": lambda: np.round(rng.standard_normal((N, V), np.float32) / 2),
+         "hot": lambda: rng.standard_normal((N, V), np.float32) * 2.5,
+         "narrow": lambda: rng.standard_normal((N, V), np.float32) * 0.002, "one_high": lambda: np.zeros((N, V))}[what]()
+    x = x.astype(np.float32)
+    if what == "one_high":
+        x[:, V // 3] = 10.0
+    x = torch.from_numpy(x).to(torch.bfloat16).cuda()
+    s = dict(temperature=np.full(N, 800.0 if what == "hot" else 1.0), top_p=np.resize([0.1, 0.5, 0.9, 0.3], N),
+             top_k=np.resize([0] * 8 + [V - 5000] * 8, N), min_p=np.resize([0.0] * 5 + [0.3], N))
+    u = rng.random(N, np.float32)
+    tok, probs = _sample(dfl, x, u, **s)
+    assert dfl.dflash_last_device_error() == 0
+    for r in range(0, N, 5):
+        one = _sample(dfl, x[r:r + 1], u[r:r + 1], **{k: v[r:r + 1] for k, v in s.items()})
+        assert one[0][0] == tok[r]
+        np.testing.assert_array_equal(one[1][0], probs[r])
+    few = [0, 1, 2, 3, 9, 89]
+    _check_sample(x[few], u[few], tok[few], probs[few], **{k: v[few] for k, v in s.items()})
+
+
 def test_sample_strides_and_alignment(dfl):
     rng = np.random.default_rng(11)
     N, V = 5, 3000
