@@ -1170,7 +1170,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       __syncthreads();
       inv = s.inv;
     }
-    const bool sparse = cut.v > -kTop;  // few are kept: zeros first, then those
+    // few are kept, or one of the lowest logit divides its equals: zeros first, then those
+    const bool sparse = cut.v > -kTop || cut.i < (int)kIndexMask;
     pass.each([&](const float (&x)[4], int at) {
       const int i = pass.first + at;
       float p[4] = {0.f, 0.f, 0.f, 0.f};

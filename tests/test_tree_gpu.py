@@ -264,6 +264,23 @@ def test_sample_masks_and_odd_values(dfl, V, dtype):
     assert dfl.dflash_last_device_error() == 0
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("V", [100, 300, 20000])
+def test_sample_lowest_logits_are_cut_by_their_numbers(dfl, V, dtype):
+    """-2^126 is the lowest logit that is a choice; of a row's tokens that have it only those in front of the cut are kept."""
+    x = torch.full((2, V), -2.0 ** 126, dtype=DT[dtype], device="cuda")
+    x[1, V // 2:] = float("-inf")
+    for s in (dict(temperature=0.0), dict(top_k=5), dict(top_k=70), dict(top_p=0.3), dict(top_k=40, top_p=0.6), dict(), dict(min_p=0.5)):
+        u = np.array([0.7, 0.2], np.float32)
+        tok, probs = _sample(dfl, x, u, **s)
+        _check_sample(x, u, tok, probs, **s)
+    x[0, 9] = 0.0  # at this temperature the others weigh 1 / e of it
+    s = dict(temperature=2.0 ** 126, top_p=0.5)
+    tok, probs = _sample(dfl, x, u, **s)
+    _check_sample(x, u, tok, probs, **s)
+    assert dfl.dflash_last_device_error() == 0
+
+
 def test_sample_rows_without_a_choice_are_recorded(dfl):
     x = torch.randn((6, 300), device="cuda")
     x[0] = float("-inf")
