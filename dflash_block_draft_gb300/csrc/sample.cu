@@ -417,8 +417,12 @@ struct Steps {
 constexpr int kStepBits = 9;  // steps of a bin of the masses
 static_assert(kBins << kStepBits == 1 << 21, "steps");
 
+// An empty list, and a cut in front of every token for the search in it.
 __device__ __forceinline__ void clear_list(Row& s) {
-  if (threadIdx.x == 0) s.listed = make_int4(0, -1, 0, 0);
+  if (threadIdx.x == 0) {
+    s.listed = make_int4(0, -1, 0, 0);
+    s.cut = (u64)key_of(INFINITY) << kIndexBits;
+  }
 }
 // Puts a token into the CTA's list, as far as there is room, and its key into the thread's range.
 __device__ __forceinline__ void enlist(Row& s, float l, int i, uint32_t& klo, uint32_t& khi) {
@@ -534,7 +538,8 @@ __device__ __forceinline__ Cut cut_at(u64 place) {
   return Cut{logit_of((uint32_t)(place >> kIndexBits)), (int)(kIndexMask - (uint32_t)(place & kIndexMask))};
 }
 
-// The listed token in which the running count or weight, `before` in front of the list, reaches the target.
+// The listed token in which the running count or weight, `before` in front of the list, reaches the target
+// (none: a cut that keeps nothing).
 template <bool WEIGHTS>
 __device__ __forceinline__ Cut cut_in_list(Row& s, int n, u64 before, u64 target) {
   const int g = group_of(n), i = threadIdx.x / g;
@@ -638,7 +643,8 @@ __device__ __forceinline__ void clear_bins(Row& s) {
 // The cut of top-k (WEIGHTS false; target: k) or top-p (true): the token, of those that
 // `prior` keeps and whose keys lie in [klo, khi], in which the running count or weight, `before` in
 // front of the range, reaches the target.  The range is divided by places, from the largest
-// key to the smallest, into 512 parts.  Returns prior where there are fewer tokens than k.
+// key to the smallest, into 512 parts.  Returns prior where there are fewer tokens than k, a cut that
+// keeps nothing where the target does not lie in the range.
 template <bool WEIGHTS, bool ONE, typename T>
 __device__ __forceinline__ Cut select(const Pass<T>& pass, Row& s, const Cut& prior, const Scale& sc, uint32_t klo,
                                       uint32_t khi, u64 before, u64 target) {
@@ -663,6 +669,7 @@ __device__ __forceinline__ Cut select(const Pass<T>& pass, Row& s, const Cut& pr
     // ---- a histogram of the range
     s.lo[tid] = 0;
     if (WEIGHTS) s.hi[tid] = 0;
+    if (tid == 0) s.found = -1;
     __syncthreads();
     pass.range(under, over, [&](float l, int at) {
       const int part = part_of(l, pass.first + at);
@@ -694,6 +701,7 @@ __device__ __forceinline__ Cut select(const Pass<T>& pass, Row& s, const Cut& pr
     }
     __syncthreads();
     const int part = s.found;
+    if (part < 0) return Cut{INFINITY, (int)kIndexMask};
     before = s.found_before;
     // ---- the part's tokens
     klo = ~0u;
@@ -824,10 +832,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   Cut cut = {-kTop, (int)kIndexMask};
   u64 total = 0;
   if (none) {
-    if (rank == 0 && tid == 0) {
-      record_error(a.err, DFLASH_ERR_INVALID);
-      token = 0;
-    }
     cut.v = INFINITY;
   } else if (temp == 0.f) {
     // ---- the first of the largest
@@ -1158,6 +1162,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           }
       }
     }
+  }
+  if (cut.v == INFINITY) {  // nothing is kept
+    total = 0;
+    token = rank == 0 && tid == 0 ? 0 : -1;
+    if (token == 0) record_error(a.err, DFLASH_ERR_INVALID);
   }
   if (token >= 0) a.tokens[r] = token;
   if (a.probs) {
