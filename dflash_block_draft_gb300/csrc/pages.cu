@@ -174,7 +174,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     load(r, had, want);
     return max(0, want - had);
   };
-  // the counts after everything that was given back; what is wanted meanwhile
+  // the counts after everything that was given back; what is wanted meanwhile (whole warps come to both halves)
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   const int wanted = plan(st, s, need);
   __syncwarp();

@@ -451,13 +451,20 @@ struct Team {
     if constexpr (ONE) __syncthreads();
     else cg::this_cluster().sync();
   }
-  // sync() in two halves; whole warps come to the second one
+  // sync() in two halves, which whole warps come to
   static __device__ __forceinline__ void arrive() {
-    if constexpr (!ONE) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    if constexpr (!ONE) {
+      __syncwarp();
+      asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    }
   }
   static __device__ __forceinline__ void wait() {
-    if constexpr (ONE) __syncthreads();
-    else asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if constexpr (ONE) {
+      __syncthreads();
+    } else {
+      __syncwarp();
+      asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    }
   }
   // what a CTA has at the place of `p`
   template <typename V>
@@ -816,7 +823,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   }
   G::arrive();
   if (tid == kThreads - 32 && min_p > 0.f) s.log_min_p = log_of(min_p);
-  __syncwarp();
   G::wait();
   float top = G::peer(s.top, tid * ranks / kThreads)[tid % (kThreads / ranks)];
   float m = logit_of(~block_least(s, ~key_of(top)));
