@@ -160,6 +160,16 @@ dflash_status_t attend(const dflash_paged_dims_t* dims, dflash_dtype_t dtype, co
   return launched(launch_attn_paged(a, dtype == DFLASH_BF16, workspace, (cudaStream_t)stream));
 }
 
+// The cache of a call that reads neither queries' heads nor max_q_len, and without `requests` nothing but the pages.
+dflash_status_t check_cache(const dflash_paged_dims_t* dims, dflash_dtype_t dtype, bool requests) {
+  if (!dims) return check_paged(dims, dtype);
+  dflash_paged_dims_t d = *dims;
+  d.H_q = d.H_kv;
+  d.max_q_len = 0;
+  if (!requests) d.R = d.total_q = d.max_pages = 0;
+  return check_paged(&d, dtype);
+}
+
 // Layers of a cache: strides in 16-byte vectors, and the cache's pointers.
 struct Layers {
   long long kps, vps, kls, vls;
@@ -468,7 +478,7 @@ dflash_status_t dflash_cache_compact(const dflash_paged_dims_t* dims, const dfla
                                      const int32_t* q_offsets, const int32_t* path, int max_path,
                                      const int32_t* num_accepted, void* k_cache, void* v_cache, int32_t* new_lens,
                                      dflash_stream_t stream) {
-  TRY(check_paged(dims, dtype));
+  TRY(check_cache(dims, dtype, true));
   Layers l;
   TRY(check_layers(dims, layers, dtype, k_cache, v_cache, &l));
   if (max_path <= 0) return DFLASH_ERR_SHAPE;
@@ -489,7 +499,7 @@ dflash_status_t dflash_cache_compact(const dflash_paged_dims_t* dims, const dfla
 dflash_status_t dflash_cache_copy(const dflash_paged_dims_t* dims, const dflash_layers_t* layers,
                                   dflash_dtype_t dtype, int n, const int32_t* src, const int32_t* dst,
                                   const int32_t* rows, void* k_cache, void* v_cache, dflash_stream_t stream) {
-  TRY(check_paged(dims, dtype));
+  TRY(check_cache(dims, dtype, false));
   Layers l;
   TRY(check_layers(dims, layers, dtype, k_cache, v_cache, &l));
   if (n < 0) return DFLASH_ERR_SHAPE;

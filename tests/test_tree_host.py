@@ -171,6 +171,18 @@ def test_cache_copy_refusals(lib, dims, over, want):
     assert _copy(lib, _paged(**dims), **over) == want
 
 
+@pytest.mark.parametrize("dims", [dict(H_q=0), dict(H_q=5), dict(H_q=65536), dict(max_q=-1), dict(max_q=2 ** 31 - 1)])
+def test_moves_read_neither_query_heads_nor_max_q_len(lib, dims):
+    """As their definitions say: whatever stands there, the call is taken (here without a request, so nothing runs)."""
+    assert _compact(lib, _paged(R=0, **dims)) == OK
+    assert _copy(lib, _paged(**dims), n=0) == OK
+
+
+@pytest.mark.parametrize("dims", [dict(R=-1), dict(R=2 ** 31 - 1), dict(total_q=-1), dict(max_pages=-1), dict(max_pages=1 << 27)])
+def test_cache_copy_reads_no_requests(lib, dims):
+    assert _copy(lib, _paged(**dims), n=0) == OK
+
+
 POOL = [
     (dict(R=-1), {}, SHAPE),
     (dict(P_=0), {}, SHAPE),
