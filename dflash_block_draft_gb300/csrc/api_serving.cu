@@ -5,6 +5,8 @@
 #include <math.h>
 #include <string.h>
 
+#include <initializer_list>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -41,6 +43,26 @@ dflash_status_t resolve_stride(int64_t given, int heads, int D, long long* out) 
 dflash_status_t check_tensor(const void* p, size_t esz) {
   if (!p) return DFLASH_ERR_INVALID;
   return aligned(p, esz) ? DFLASH_OK : DFLASH_ERR_ALIGN;
+}
+
+// Whole numbers that a call reads or writes, n of them.
+struct Ints {
+  const int32_t* p;
+  long long n;
+};
+// Whether what a call writes overlaps what it reads, or one result another: CTAs read some while others write.
+bool overlap(std::initializer_list<Ints> written, std::initializer_list<Ints> read) {
+  auto meet = [](const Ints& x, const Ints& y) {
+    const uintptr_t a = (uintptr_t)x.p, b = (uintptr_t)y.p;
+    return x.p && y.p && x.n > 0 && y.n > 0 && a < b + sizeof(int32_t) * (size_t)y.n && b < a + sizeof(int32_t) * (size_t)x.n;
+  };
+  for (auto w = written.begin(); w != written.end(); ++w) {
+    for (const Ints& r : read)
+      if (meet(*w, r)) return true;
+    for (auto v = written.begin(); v != w; ++v)
+      if (meet(*w, *v)) return true;
+  }
+  return false;
 }
 
 #define TRY(call)                                 \
@@ -468,6 +490,10 @@ dflash_status_t dflash_tree_accept(const dflash_accept_dims_t* dims, const int32
   TRY(check_tensor(path, 4));
   TRY(check_tensor(out_tokens, 4));
   TRY(check_tensor(num_accepted, 4));
+  const long long R = dims->R, T = dims->total, cells = R * dims->max_path;
+  if (overlap({{path, cells}, {out_tokens, cells}, {num_accepted, R}},
+              {{sampled, T}, {tokens, T}, {parents, T}, {q_offsets, R + 1}}))
+    return DFLASH_ERR_INVALID;
   const AcceptArgs a = {sampled, tokens, parents, q_offsets, path, out_tokens, num_accepted,
                         dims->R, dims->total, dims->max_path, device_error_word()};
   return launched(launch_tree_accept(a, (cudaStream_t)stream));
@@ -489,7 +515,10 @@ dflash_status_t dflash_cache_compact(const dflash_paged_dims_t* dims, const dfla
   TRY(check_tensor(path, 4));
   TRY(check_tensor(num_accepted, 4));
   TRY(check_tensor(new_lens, 4));
-  if (new_lens == kv_lens) return DFLASH_ERR_INVALID;
+  const long long R = dims->R;
+  if (overlap({{new_lens, R}}, {{page_table, R * dims->max_pages}, {kv_lens, R}, {q_offsets, R + 1}, {path, R * max_path},
+                                {num_accepted, R}}))
+    return DFLASH_ERR_INVALID;
   const CompactArgs a = {k_cache, v_cache, page_table, kv_lens, q_offsets, path, num_accepted, new_lens,
                          l.kps, l.vps, l.kls, l.vls, dims->R, dims->total_q, dims->page_size, dims->max_pages,
                          dims->num_pages, max_path, layers->L, l.row, device_error_word()};
@@ -527,6 +556,9 @@ dflash_status_t dflash_pages_resize(const dflash_pool_dims_t* dims, int32_t* pag
     TRY(check_tensor(old_lens, 4));
     TRY(check_tensor(new_lens, 4));
   }
+  const long long R = dims->R;
+  if (overlap({{page_table, R * dims->max_pages}, {refs, dims->num_pages}, {missing, 1}}, {{old_lens, R}, {new_lens, R}}))
+    return DFLASH_ERR_INVALID;
   return launched(launch_pages_resize(a, old_lens, new_lens, (cudaStream_t)stream));
 }
 
@@ -541,6 +573,10 @@ dflash_status_t dflash_pages_fork(const dflash_pool_dims_t* dims, int32_t* page_
   if (n > 0)
     for (const int32_t* p : {src, dst, (const int32_t*)copy_src, (const int32_t*)copy_dst, (const int32_t*)copy_rows})
       TRY(check_tensor(p, 4));
+  const long long R = dims->R;
+  if (overlap({{page_table, R * dims->max_pages}, {lens, R}, {refs, dims->num_pages}, {copy_src, n}, {copy_dst, n},
+               {copy_rows, n}, {missing, 1}}, {{src, n}, {dst, n}}))
+    return DFLASH_ERR_INVALID;
   const ForkArgs f = {src, dst, lens, copy_src, copy_dst, copy_rows, n};
   return launched(launch_pages_fork(a, f, (cudaStream_t)stream));
 }

@@ -305,7 +305,10 @@ DFLASH_API dflash_status_t dflash_attn_dense_backward(const dflash_dims_t* dims,
  * Element types, ownership, streams and errors as above.  The device that holds
  * the tensors has to be the current one.  Calls that may run at the same time
  * (on two streams, or in graphs that are replayed side by side) need a workspace
- * each.  Every call may be captured into a graph.
+ * each.  Every call may be captured into a graph.  What a call of the second list writes
+ * must not overlap what it reads, nor one result another, except where it says so; among the
+ * whole numbers of the walk, of compaction and of the pages' calls that is refused
+ * (DFLASH_ERR_INVALID).
  */
 
 /*
@@ -590,7 +593,7 @@ typedef struct {
  * The accepted nodes of a step moved together: with a = num_accepted[r] and L - n the
  * position of the request's first new token, the keys and values of position
  * L - n + path[r, j] go to position L - n + j, j < a, and new_lens[r] = L - n + a.
- * (new_lens is not kv_lens: other caches are still to be moved by the old lengths.)
+ * (new_lens does not overlap kv_lens: other caches are still to be moved by the old lengths.)
  *   path [R, max_path]: rising indexes below n, as dflash_tree_accept writes them.
  * A request whose offsets, length, count or path are out of range is recorded as
  * DFLASH_ERR_INVALID and left as it is (new_lens = kv_lens); a row whose page id is out

@@ -235,6 +235,52 @@ def test_pages_fork_refusals(lib, dims, over, want):
                                  a["cd"], a["cr"], a["missing"], a["ws"], a["nbytes"], None) == want
 
 
+def _at(i):
+    """The i-th of eight arrays in a buffer, 4096 bytes apart: far enough for the calls below."""
+    return P(4096 * (1 + i))
+
+
+@pytest.mark.parametrize("name", ["table", "lens", "off", "path", "count"])
+@pytest.mark.parametrize("shift", [0, 4])
+def test_compaction_refuses_new_lengths_in_what_it_reads(lib, name, shift):
+    """The CTAs of other layers read the counts and lengths while one writes the new lengths."""
+    a = dict(table=_at(0), lens=_at(1), off=_at(2), path=_at(3), count=_at(4))
+    assert _compact(lib, _paged(), **a, new=P(a[name].value + shift)) == INVALID
+
+
+@pytest.mark.parametrize("out", ["path", "out", "count"])
+@pytest.mark.parametrize("other", ["sampled", "tokens", "parents", "off", "path", "out", "count"])
+def test_walk_refuses_results_in_what_it_reads(lib, out, other):
+    a = {n: _at(i) for i, n in enumerate(("sampled", "tokens", "parents", "off", "path", "out", "count"))}
+    if out == other:
+        return
+    a[out] = P(a[other].value + 4)
+    assert lib.dflash_tree_accept(dfl._AcceptDims(2, 6, 4), a["sampled"], a["tokens"], a["parents"], a["off"], a["path"],
+                                  a["out"], a["count"], None) == INVALID
+
+
+@pytest.mark.parametrize("out", ["cs", "cd", "cr", "missing", "lens", "table", "refs"])
+@pytest.mark.parametrize("other", ["src", "dst", "cs", "cd", "cr", "missing", "lens", "table", "refs"])
+def test_fork_refuses_results_in_what_it_reads(lib, out, other):
+    a = {n: _at(i) for i, n in enumerate(("table", "lens", "src", "dst", "refs", "cs", "cd", "cr", "missing"))}
+    if out == other:
+        return
+    a[out] = a[other]
+    assert lib.dflash_pages_fork(_pool({}), a["table"], a["lens"], 2, a["src"], a["dst"], a["refs"], a["cs"], a["cd"],
+                                 a["cr"], a["missing"], WS, BIG, None) == INVALID
+
+
+@pytest.mark.parametrize("out", ["table", "refs", "missing"])
+@pytest.mark.parametrize("other", ["old", "new", "table", "refs", "missing"])
+def test_resize_refuses_results_in_what_it_reads(lib, out, other):
+    a = {n: _at(i) for i, n in enumerate(("table", "old", "new", "refs", "missing"))}
+    if out == other:
+        return
+    a[out] = a[other]
+    assert lib.dflash_pages_resize(_pool({}), a["table"], a["old"], a["new"], a["refs"], a["missing"], WS, BIG,
+                                   None) == INVALID
+
+
 def test_pages_workspace(lib):
     assert dfl.dflash_pages_workspace_size(1000) >= 4 * 1000
     assert lib.dflash_pages_workspace_size(_pool(dict(P_=0))) == 0
