@@ -461,7 +461,8 @@ DFLASH_API dflash_status_t dflash_attn_paged(const dflash_paged_dims_t* dims, df
  * (what is rotated, if it is, is the depth: dflash_qk_norm_rope with positions
  * L - n + depth, dflash_cache_append then without a rotation).  Node i sees the
  * context p < L - n, itself, its parent, that one's parent and so on, and no other
- * node.
+ * node.  (Keys and values of all L positions have to be finite all the same: a node that is
+ * not seen has the weight 0, and 0 times a value that is infinite or NaN is NaN.)
  *   parents [total_q] int32: index of the parent among the request's nodes, -1
  *     for a root (there may be several).  A value that is not smaller than the
  *     node's own index, or negative, ends the chain like -1.
