@@ -571,7 +571,8 @@ def dflash_attn_tree(q, k_cache, v_cache, page_table, kv_lens, q_offsets, parent
     """Attention of drafted trees: the new tokens of dflash_attn_paged are the nodes of a
     tree, each behind its parent parents [total_q] int32 (index within the request; -1: a
     root), and see the positions in front of the tree, themselves and their ancestors.
-    All keys and values have to be finite, those that a node does not see too.  Workspace as dflash_attn_paged_workspace_size says."""
+    All keys and values have to be finite, those that a node does not see too.  Workspace
+    as dflash_attn_paged_workspace_size says."""
     r = (_binding_handle or _binding()).attn_tree(q, k_cache, v_cache, page_table, kv_lens, q_offsets, parents,
                                                   max_q_len, out, lse, scale, workspace, stream)
     if r.__class__ is int:

@@ -98,6 +98,13 @@ def test_attn_tree_forms(dfl, dtype, P, form):
     _check_tree(dfl, np.random.default_rng(2), [150, 40], [60, 33], P, 8, 2, 64, dtype, form)
 
 
+@pytest.mark.parametrize("dtype,P", [("bf16", 16), ("fp32", 16), ("bf16", 7)])
+def test_attn_tree_nodes_that_see_nothing_of_whole_tiles(dfl, dtype, P):
+    """Roots far behind the first key tiles, without a context or with less than a tile of it, see the last tiles alone."""
+    _check_tree(dfl, np.random.default_rng(13), [300, 260], [300, 200], P, 8, 2, 64, dtype, "roots")
+    _check_tree(dfl, np.random.default_rng(14), [290], [300], P, 6, 2, 128, dtype, "roots")
+
+
 def test_attn_tree_scale_halves_and_loose_bound(dfl):
     rng = np.random.default_rng(3)
     _check_tree(dfl, rng, [100, 333], [16, 30], 16, 8, 2, 128, "bf16", layout="halves", scale=0.31)
@@ -316,6 +323,26 @@ def test_sample_settings_of_each_row_and_rows_by_themselves(dfl):
         assert one[0][0] == tok[r]
         np.testing.assert_array_equal(one[1][0], probs[r])
     np.testing.assert_array_equal(_sample(dfl, x, u, probs=False, **s)[0], tok)
+    assert dfl.dflash_last_device_error() == 0
+
+
+@pytest.mark.parametrize("V,dtype", [(17001, "fp32"), (20000, "bf16")])
+def test_sample_every_setting_in_one_cta_and_in_eight(dfl, V, dtype):
+    """A row of many is one CTA's and a row by itself eight CTAs': the same bits in every setting."""
+    rng = np.random.default_rng(V + 2)
+    N = 160
+    x = _rand(rng, (N, V), dtype, 3.0)
+    s = dict(temperature=rng.choice([0, 0.3, 1, 2.5, 300.0], N), top_k=rng.choice([0, -1, 1, 30, 160, 161, 512, 513, 900, V, 2 * V], N),
+             top_p=rng.choice([1.0, 0.9, 0.5, 0.99, 1.5, 0.0], N), min_p=rng.choice([0, 0.05, -1, 3.0], N))
+    u = rng.random(N, np.float32)
+    u[::9], u[4::9] = 0.0, 1 - 2.0 ** -24
+    tok, probs = _sample(dfl, x, u, **s)
+    for r in range(N):
+        one = _sample(dfl, x[r:r + 1], u[r:r + 1], **{k: v[r:r + 1] for k, v in s.items()})
+        assert one[0][0] == tok[r]
+        np.testing.assert_array_equal(one[1][0], probs[r])
+    few = list(range(0, N, 5))
+    _check_sample(x[few], u[few], tok[few], probs[few], **{k: v[few] for k, v in s.items()})
     assert dfl.dflash_last_device_error() == 0
 
 
