@@ -24,11 +24,13 @@
 //   the sums of kept weights by runs of tokens, one exchange, and the run that passes u times
 //     the whole once more, a few tokens a thread.
 //
-// Bound by instructions: a weight costs some 21, a look at a logit 2 to 15, and what a row
-// costs besides (barriers, exchanges, the list) is as much as 8000 tokens of a CTA.  Two CTAs of
-// 512 threads an SM, one row's wait under the other's work.  Measured: 64 rows of 131072 bf16
-// logits with temperature alone 20 us; 1664 rows of 32000 with top-k 40 in most of them 77;
-// 128 rows of 131072 fp32 with top-p and the distributions written 126; 4 rows of 32000 9.2.
+// Bound by instructions and as much by a row's phases, which wait for one another (46 to 62 % of
+// the issue slots, 8 to 17 % of the memory's rate): a weight costs some 21 instructions, a look at
+// a logit 2 to 15, and what a row costs besides (barriers, exchanges, the list) is as much as 8000
+// tokens of a CTA.  Two CTAs of 512 threads an SM, one row's wait under the other's work.  Measured:
+// 64 rows of 131072 bf16 logits with temperature alone 20.8 us; 1664 rows of 32000 with top-k 40 in
+// most of them 77; 128 rows of 131072 fp32 with top-p and the distributions written 126; 4 rows of
+// 32000 9.4.
 // (With a histogram of all weights for top-p and a second exact pass, 128 rows took 251 us;
 // top-k by a histogram of everything above the least of the threads' maxima, 4 rows 17.)  The
 // kernel runs once through most of its code, which was 190 KB where loops were copied and
@@ -38,9 +40,9 @@
 // depends on the order, the number of CTAs or the threads' timing.  A pair of weights takes 16
 // packed fp32 instructions in bf16 and 22 in fp32, and each some 13 others: l - m, times
 // log2(e) / T as two floats; 2^y from a table of 2^(j / 128) in two floats and a polynomial of
-// degree 3; the bits of sums with 2.5 and 1.5 2^-21 count the steps, as in verify.cu.  (The packed
-// instructions bound it: four fewer a pair took 64 rows from 24.6 us to 22.7 where eight copies of the
-// table without bank conflicts, or shuffles in its place, changed nothing.)  The
+// degree 3; the bits of sums with 2.5 and 1.5 2^-21 count the steps, as in verify.cu.  (Four packed
+// instructions fewer a pair took 64 rows from 24.6 us to 22.7 where eight copies of the table
+// without bank conflicts, or shuffles in its place, changed nothing.)  The
 // weights' errors, 2^-33.5 rms, are each other's by chance and add up to a border's as their
 // root: of a vocabulary of 131072 every 10^7th row would draw another token than the real numbers
 // (every 50th with fp32 sums of weights that are off in one direction).  Twice the instructions
@@ -175,7 +177,8 @@ __device__ __forceinline__ u64 weight(const Scale& c, const Table& tab, float l,
   return w0.joined();
 }
 
-// The weight as a float, for the distribution.
+// The weight as a float, for the distribution, whose values are fp32 anyway: off by 2^-22 where the
+// rounding of the result alone is 2^-24.  (The draw takes the weights in steps.)
 __device__ __forceinline__ float weight_f32(const Scale& c, float l) {
   const float d = l - c.m, n = rintf(d * c.ch);
   const float f = fmaf(d, c.cl, fmaf(d, c.ch, -n));
